@@ -20,6 +20,8 @@ FO_GEMM_AUTO, FO_GEMM_SINGLE, FO_GEMM_PAIRS = range(3)
 FO_ACT_NONE, FO_ACT_RELU, FO_ACT_SILU = range(3)
 FO_BAND_FORWARD, FO_BAND_SERPENTINE = range(2)
 FO_CONSUMER_SHARED, FO_CONSUMER_RESERVED = range(2)
+FO_TYPE_BF16, FO_TYPE_F32, FO_TYPE_MX4 = range(3)
+FO_MOE_FEW_TOKENS = 64   # include/fo.h
 (FO_TAB_SLOT_TILE, FO_TAB_TILE_SLOT, FO_TAB_SLOT_GROUP, FO_TAB_GROUP_TILES, FO_TAB_UNIT,
  FO_TAB_PART_START, FO_TAB_PART_LEN, FO_TAB_PART_DST, FO_TAB_DEST_UNITS,
  FO_TAB_FINAL_ROWS, FO_TAB_DEST_CAPACITY, FO_TAB_SLOT_LIVE, FO_TAB_UNIT_PLACE) = range(13)
@@ -28,6 +30,7 @@ _i32p = ctypes.POINTER(ctypes.c_int32)
 _vp = ctypes.c_void_p
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 _dp = ctypes.POINTER(ctypes.c_double)
+_i64, _i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
 
 
 class fo_plan_desc(ctypes.Structure):
@@ -43,6 +46,11 @@ class fo_plan_desc(ctypes.Structure):
         ("pad_expert_tile_rows", ctypes.c_int32),
         ("band_order", ctypes.c_int32),
     ]
+
+
+class fo_moe_few_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "tokens", "hidden", "inter", "experts", "top_k", "renormalize", "act", "weights")]
 
 
 class FoError(RuntimeError):
@@ -112,6 +120,23 @@ def lib():
             "fo_allgather_rows": (ctypes.c_int, [_vp, _vpp, _vp, _vp, ctypes.c_int, _vp]),
             "fo_plan_route": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32,
                                              _vp, _vp]),
+            "fo_mx_sizes": (ctypes.c_int, [_i64, _i64, _i64, _i64p, _i64p]),
+            "fo_mx_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64,
+                                              ctypes.c_int32, _vp, _i64, _vp, _vp, _vp]),
+            "fo_mx_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int,
+                                                _i64, _i64, _vp]),
+            "fo_mx_gemm": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_int32,
+                                          _vp, _vp, _vp, ctypes.c_int, _i64, _vp, _vp]),
+            "fo_moe_route_sizes": (ctypes.c_int, [_i64, ctypes.c_int32, ctypes.c_int32, _i64,
+                                                  _i64p, _i64p]),
+            "fo_moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int32, _i64,
+                                            ctypes.c_int32, ctypes.c_int32, _i64] + [_vp] * 10),
+            "fo_moe_route_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int32,
+                                                     _i64, ctypes.c_int32, ctypes.c_int32, _vp,
+                                                     _vp, _vp, _vp, _i64, _vp]),
+            "fo_moe_few_workspace": (ctypes.c_int, [ctypes.POINTER(fo_moe_few_desc), _i64p]),
+            "fo_moe_few": (ctypes.c_int, [ctypes.POINTER(fo_moe_few_desc), _vp, _i64, _vp, _vp,
+                                          _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
             "fo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -323,6 +348,88 @@ def fo_allgather_rows(plan, slices, out, bias, act, stream):
     _check("fo_allgather_rows",
            lib().fo_allgather_rows(plan, _ptrs(slices), int(out), int(bias) or None, act,
                                    stream or None))
+
+
+def fo_mx_sizes(batch, rows, cols):
+    """(code bytes, scale bytes) of a batch of 4-bit matrices."""
+    c, s = ctypes.c_int64(), ctypes.c_int64()
+    _check("fo_mx_sizes", lib().fo_mx_sizes(batch, rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def fo_mx_quantize(src, type, batch, batch_stride, rows, cols, row_stride, transpose, row_index,
+                   src_rows, codes, scales, stream):
+    """src, codes, scales: device addresses; row_index: device int32 or 0."""
+    _check("fo_mx_quantize",
+           lib().fo_mx_quantize(src, type, batch, batch_stride, rows, cols, row_stride,
+                                1 if transpose else 0, row_index or None, src_rows, codes,
+                                scales, stream or None))
+
+
+def fo_mx_dequantize(codes, scales, batch, rows, cols, dst, type, batch_stride, row_stride,
+                     stream):
+    _check("fo_mx_dequantize",
+           lib().fo_mx_dequantize(codes, scales, batch, rows, cols, dst, type, batch_stride,
+                                  row_stride, stream or None))
+
+
+def fo_mx_gemm(M, N, K, A_codes, A_scales, B_codes, B_scales, n_groups, group_first, group_rows,
+               D, type, row_stride, dev_status, stream):
+    """Device addresses; n_groups 0 with group_first and group_rows 0: one
+    product over all rows."""
+    _check("fo_mx_gemm",
+           lib().fo_mx_gemm(M, N, K, A_codes, A_scales, B_codes, B_scales, n_groups,
+                            group_first or None, group_rows or None, D, type, row_stride,
+                            dev_status, stream or None))
+
+
+def fo_moe_route_sizes(tokens, experts, top_k, capacity=0):
+    """(rows of the row tables, bytes of the workspace)."""
+    r, w = ctypes.c_int64(), ctypes.c_int64()
+    _check("fo_moe_route_sizes",
+           lib().fo_moe_route_sizes(tokens, experts, top_k, capacity, ctypes.byref(r),
+                                    ctypes.byref(w)))
+    return r.value, w.value
+
+
+def fo_moe_route(logits, type, tokens, experts, row_stride, top_k, renormalize, capacity, ids,
+                 weights, row_token, row_slot, token_row, expert_first, expert_rows, workspace,
+                 dev_status, stream):
+    _check("fo_moe_route",
+           lib().fo_moe_route(logits, type, tokens, experts, row_stride, top_k,
+                              1 if renormalize else 0, capacity, ids, weights, row_token,
+                              row_slot, token_row, expert_first, expert_rows, workspace,
+                              dev_status, stream or None))
+
+
+def fo_moe_route_backward(logits, type, tokens, experts, row_stride, top_k, renormalize, ids,
+                          weights, dweights, dlogits, dlogits_stride, stream):
+    _check("fo_moe_route_backward",
+           lib().fo_moe_route_backward(logits, type, tokens, experts, row_stride, top_k,
+                                       1 if renormalize else 0, ids, weights, dweights, dlogits,
+                                       dlogits_stride, stream or None))
+
+
+def make_few_desc(tokens, hidden, inter, experts, top_k, renormalize=True, act=FO_ACT_SILU,
+                  weights=FO_TYPE_BF16):
+    return fo_moe_few_desc(tokens, hidden, inter, experts, top_k, 1 if renormalize else 0, act,
+                           weights)
+
+
+def fo_moe_few_workspace(desc):
+    n = ctypes.c_int64()
+    _check("fo_moe_few_workspace", lib().fo_moe_few_workspace(ctypes.byref(desc),
+                                                              ctypes.byref(n)))
+    return n.value
+
+
+def fo_moe_few(desc, x, x_stride, router, W1, W1_scales, W2, W2_scales, y, y_stride, workspace,
+               dev_status, stream):
+    """Device addresses; W1_scales and W2_scales 0 for bf16 weights."""
+    _check("fo_moe_few",
+           lib().fo_moe_few(ctypes.byref(desc), x, x_stride, router, W1, W1_scales or None, W2,
+                            W2_scales or None, y, y_stride, workspace, dev_status,
+                            stream or None))
 
 
 def _curve(curve):

@@ -1,0 +1,282 @@
+"""The expert layer's operators on torch tensors.
+
+Plumbing only, as ``pipeline.py`` is for the signaled GEMM: torch provides
+device memory and the current stream, every step is a libfo.so call (see
+``fo.py`` and ``include/fo.h``, which states what each computes).
+
+  route, route_backward   the router: top-k experts, weights, row tables
+  quantize, dequantize    to and from the microscaled 4-bit form (MxTensor)
+  mx_gemm                 the product of two 4-bit matrices, or one per expert
+  FewTokenLayer           a whole expert layer for a generation step's tokens
+
+Calls run on the current stream of the tensors' device and do not
+synchronise.  Workspaces are kept per device and stream, so calls on
+different streams do not share one.  ``device_status`` reads (and
+synchronises) the sticky status of the calls' bounded waits.
+"""
+from dataclasses import dataclass
+
+import torch
+
+from . import fo
+
+_TYPES = {torch.bfloat16: fo.FO_TYPE_BF16, torch.float32: fo.FO_TYPE_F32}
+_ACTS = {"none": fo.FO_ACT_NONE, "relu": fo.FO_ACT_RELU, "silu": fo.FO_ACT_SILU}
+_status, _workspaces = {}, {}
+
+
+def _type(t):
+    if t.dtype not in _TYPES:
+        raise ValueError(f"bf16 or fp32 expected, not {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _on_gpu(*tensors):
+    """The common CUDA device of the tensors (None entries are skipped)."""
+    live = [t for t in tensors if t is not None]
+    dev = live[0].device
+    if dev.type != "cuda" or any(t.device != dev for t in live):
+        raise ValueError("tensors must be on one CUDA device")
+    return dev
+
+
+def _int32(t, n, what):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: contiguous int32[{n}] expected")
+
+
+def _inner(t, what):
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+
+
+def _row_stride(t, what):
+    """Row stride of a matrix (of its length where it has one row)."""
+    _inner(t, what)
+    if t.shape[-2] <= 1:
+        return max(t.shape[-1], t.stride(-2) if t.numel() else 0)
+    if t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"{what}: rows overlap")
+    return t.stride(-2)
+
+
+def _stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _status_word(dev):
+    if dev not in _status:
+        _status[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
+    return _status[dev].data_ptr()
+
+
+def _workspace(kind, dev, nbytes):
+    """A zeroed workspace of at least nbytes for this device and stream."""
+    key = (kind, dev, _stream(dev))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    return ws.data_ptr()
+
+
+def device_status(device="cuda", clear=False):
+    """The device's sticky status (FO_OK, FO_ERR_ARG for a product's group out
+    of range, FO_ERR_TIMEOUT).  Synchronises."""
+    dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if dev not in _status:
+        return fo.FO_OK
+    torch.cuda.synchronize(dev)
+    st = int(_status[dev].item())
+    if clear:
+        _status[dev].zero_()
+    return st
+
+
+# ------------------------------------------------------------------ 4-bit form
+
+@dataclass
+class MxTensor:
+    """`batch` matrices rows x cols in the 4-bit form (uint8 tensors)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    batch: int
+    rows: int
+    cols: int
+
+    def __post_init__(self):
+        want = fo.fo_mx_sizes(self.batch, self.rows, self.cols)
+        have = (self.codes.numel(), self.scales.numel())
+        if have != want or self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
+            raise ValueError(f"uint8 codes and scales of {want} bytes expected, not {have}")
+        if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+
+
+def quantize(x, transpose=False, row_index=None):
+    """x: bf16 or fp32, [rows, cols] or [batch, rows, cols] (any row stride).
+    transpose: of each matrix's transpose, blocks along its rows.  row_index:
+    int32 rows of x to take (an index outside x: a row of zeros)."""
+    if x.dim() not in (2, 3):
+        raise ValueError("a matrix or a batch of matrices expected")
+    dev, type_ = _on_gpu(x, row_index), _type(x)
+    batch = x.shape[0] if x.dim() == 3 else 1
+    src_rows, src_cols = x.shape[-2:]
+    stride = _row_stride(x, "x")
+    batch_stride = x.stride(0) if x.dim() == 3 else 0
+    rows, cols = (src_cols, src_rows) if transpose else (src_rows, src_cols)
+    if row_index is not None:
+        if transpose or batch != 1:
+            raise ValueError("row_index goes with one matrix, not transposed")
+        _int32(row_index, row_index.numel(), "row_index")
+        rows = row_index.numel()
+    nc, ns = fo.fo_mx_sizes(batch, rows, cols)
+    codes = torch.empty(nc, dtype=torch.uint8, device=dev)
+    scales = torch.empty(ns, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        fo.fo_mx_quantize(x.data_ptr(), type_, batch, batch_stride, rows, cols, stride, transpose,
+                          0 if row_index is None else row_index.data_ptr(), src_rows,
+                          codes.data_ptr(), scales.data_ptr(), _stream(dev))
+    return MxTensor(codes, scales, batch, rows, cols)
+
+
+def dequantize(q, dtype=torch.bfloat16):
+    """The values q stands for: [rows, cols], or [batch, rows, cols]."""
+    dev = _on_gpu(q.codes, q.scales)
+    out = torch.empty((q.batch, q.rows, q.cols), dtype=dtype, device=dev)
+    with torch.cuda.device(dev):
+        fo.fo_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.batch, q.rows, q.cols,
+                            out.data_ptr(), _type(out), q.rows * q.cols, q.cols, _stream(dev))
+    return out[0] if q.batch == 1 else out
+
+
+def mx_gemm(a, b, out=None, out_dtype=torch.bfloat16, group_first=None, group_rows=None):
+    """a (M x K) times the transpose of b (N x K).  With group_first and
+    group_rows (int32, one entry per matrix of b) a product per expert; rows
+    in no group keep what `out` holds."""
+    dev = _on_gpu(a.codes, b.codes, out, group_first, group_rows)
+    if a.batch != 1 or a.cols != b.cols:
+        raise ValueError("a: one matrix with as many columns as b")
+    groups = 0
+    if (group_first is None) != (group_rows is None):
+        raise ValueError("group_first and group_rows go together")
+    if group_first is not None:
+        groups = b.batch
+        _int32(group_first, groups, "group_first")
+        _int32(group_rows, groups, "group_rows")
+    elif b.batch != 1:
+        raise ValueError("a batch of b needs group_first and group_rows")
+    if out is None:
+        make = torch.zeros if groups else torch.empty
+        out = make((a.rows, b.rows), dtype=out_dtype, device=dev)
+    if tuple(out.shape) != (a.rows, b.rows):
+        raise ValueError(f"out: {(a.rows, b.rows)} expected, not {tuple(out.shape)}")
+    with torch.cuda.device(dev):
+        fo.fo_mx_gemm(a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
+                      b.codes.data_ptr(), b.scales.data_ptr(), groups,
+                      0 if group_first is None else group_first.data_ptr(),
+                      0 if group_rows is None else group_rows.data_ptr(), out.data_ptr(),
+                      _type(out), _row_stride(out, "out"), _status_word(dev), _stream(dev))
+    return out
+
+
+# ------------------------------------------------------------------ the router
+
+@dataclass
+class Routing:
+    ids: torch.Tensor           # int32 [tokens, top_k], -1: no expert
+    weights: torch.Tensor       # fp32 [tokens, top_k]
+    row_token: torch.Tensor     # int32 [table rows], -1: no token
+    row_slot: torch.Tensor      # int32 [table rows]
+    token_row: torch.Tensor     # int32 [tokens, top_k], -1: dropped
+    expert_first: torch.Tensor  # int32 [experts]
+    expert_rows: torch.Tensor   # int32 [experts]
+
+
+def route(logits, top_k, renormalize=True, capacity=0):
+    """The top-k choice of logits [tokens, experts] (bf16 or fp32)."""
+    if logits.dim() != 2:
+        raise ValueError("logits: [tokens, experts] expected")
+    dev, type_ = _on_gpu(logits), _type(logits)
+    T, E = logits.shape
+    M, nbytes = fo.fo_moe_route_sizes(T, E, top_k, capacity)
+    new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=dev)
+    r = Routing(new(T, top_k), new(T, top_k, dtype=torch.float32), new(M), new(M), new(T, top_k),
+                new(E), new(E))
+    with torch.cuda.device(dev):
+        fo.fo_moe_route(logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"), top_k,
+                        renormalize, capacity, r.ids.data_ptr(), r.weights.data_ptr(),
+                        r.row_token.data_ptr(), r.row_slot.data_ptr(), r.token_row.data_ptr(),
+                        r.expert_first.data_ptr(), r.expert_rows.data_ptr(),
+                        _workspace("route", dev, nbytes), _status_word(dev), _stream(dev))
+    return r
+
+
+def route_backward(logits, ids, weights, dweights, renormalize=True):
+    """The gradient of the logits from that of the weights (fp32)."""
+    if logits.dim() != 2:
+        raise ValueError("logits: [tokens, experts] expected")
+    dev, type_ = _on_gpu(logits, ids, weights, dweights), _type(logits)
+    T, E = logits.shape
+    k = ids.shape[-1]
+    _int32(ids, T * k, "ids")
+    for t, what in ((weights, "weights"), (dweights, "dweights")):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != T * k:
+            raise ValueError(f"{what}: contiguous fp32[{T}, {k}] expected")
+    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    with torch.cuda.device(dev):
+        fo.fo_moe_route_backward(logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"), k,
+                                 renormalize, ids.data_ptr(), weights.data_ptr(),
+                                 dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
+    return out
+
+
+# ------------------------------------------------------------------ few tokens
+
+class FewTokenLayer:
+    """An expert layer for up to fo.FO_MOE_FEW_TOKENS tokens at a time.
+
+    router: bf16 [experts, hidden].  w1: bf16 [experts, 2 * inter, hidden],
+    the gate's rows first, and w2: bf16 [experts, hidden, inter]; or both as
+    MxTensor batches of those shapes."""
+
+    def __init__(self, router, w1, w2, top_k, renormalize=True, act="silu"):
+        mx = isinstance(w1, MxTensor)
+        if mx != isinstance(w2, MxTensor):
+            raise ValueError("w1 and w2 take the same form")
+        E, H = router.shape
+        s1 = (w1.batch, w1.rows, w1.cols) if mx else tuple(w1.shape)
+        s2 = (w2.batch, w2.rows, w2.cols) if mx else tuple(w2.shape)
+        I = s2[-1]
+        if s1 != (E, 2 * I, H) or s2 != (E, H, I):
+            raise ValueError(f"w1 {s1} and w2 {s2} do not fit a router of {E} x {H}")
+        parts = (w1.codes, w1.scales, w2.codes, w2.scales) if mx else (w1, None, w2, None)
+        for t in (router,) + (() if mx else (w1, w2)):
+            if t.dtype != torch.bfloat16 or not t.is_contiguous():
+                raise ValueError("contiguous bf16 weights expected")
+        self.device = _on_gpu(router, *parts)
+        self.router, self._keep = router, parts
+        self.hidden, self.top_k = H, top_k
+        self._w = [0 if t is None else t.data_ptr() for t in parts]
+        self._desc = lambda tokens: fo.make_few_desc(
+            tokens, H, I, E, top_k, renormalize, _ACTS[act],
+            fo.FO_TYPE_MX4 if mx else fo.FO_TYPE_BF16)
+        self._bytes = fo.fo_moe_few_workspace(self._desc(fo.FO_MOE_FEW_TOKENS))
+
+    def __call__(self, x, out=None):
+        """x: bf16 [tokens, hidden] -> y of the same shape."""
+        if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype != torch.bfloat16:
+            raise ValueError(f"x: bf16 [tokens, {self.hidden}] expected")
+        dev = _on_gpu(x, self.router, out)
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if out.shape != x.shape or out.dtype != torch.bfloat16:
+            raise ValueError("out: bf16 of x's shape expected")
+        w1, s1, w2, s2 = self._w
+        with torch.cuda.device(dev):
+            fo.fo_moe_few(self._desc(x.shape[0]), x.data_ptr(), _row_stride(x, "x"),
+                          self.router.data_ptr(), w1, s1, w2, s2, out.data_ptr(),
+                          _row_stride(out, "out"), _workspace("few", dev, self._bytes),
+                          _status_word(dev), _stream(dev))
+        return out

@@ -565,6 +565,170 @@ fo_status fo_consume_reorder(const fo_plan* plan, int32_t group, fo_consumer kin
 fo_status fo_allgather_rows(const fo_plan* plan, const void* const* slices, void* out,
                             const void* bias, fo_activation act, void* cuda_stream);
 
+/* ------------------------------------------------------------------------
+ * The expert layer's operators.
+ *
+ * The All-to-All layout above assumes a routing and computes one product per
+ * expert.  These calls supply what stands around it: the router that makes
+ * the routing, the product in microscaled 4-bit floating point with the
+ * conversion to that form, and the whole layer in one call for the few
+ * tokens of a generation step.  They need no plan: shapes are arguments, and
+ * the caller owns every buffer and workspace.  Nothing is allocated and
+ * nothing synchronises, so every call can be captured into a CUDA graph.
+ *
+ * The microscaled 4-bit form of a matrix ("mx"):
+ *  - Values are E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5,
+ *    2, 3, 4, 6 and their negatives).  Each 32 consecutive values of a row
+ *    share a scale, E8M0: a byte s that stands for 2^(s - 127), 255 for NaN.
+ *  - codes: row-major, two to a byte (the even column in the low nibble);
+ *    rows padded to a multiple of 128 and columns to a multiple of 128.
+ *  - scales: blocks of 128 rows x 4 scales (128 columns), 512 bytes each,
+ *    row block by row block; the scale of row r, 32-column block j, inside
+ *    its 512 bytes is at (r % 32) * 16 + (r / 32) * 4 + j -- the order in
+ *    which the tensor cores take scales, so that a block is one copy.
+ *  - A batch of matrices is stored one after another, each padded.
+ *  The padding is part of the form: fo_mx_quantize writes it (zeros), and
+ *  the product relies on padded columns being zero with scales that are not
+ *  NaN.
+ * ---------------------------------------------------------------------- */
+typedef enum { FO_TYPE_BF16 = 0, FO_TYPE_F32 = 1, FO_TYPE_MX4 = 2 } fo_type;
+
+/* Bytes of the codes and of the scales of `batch` matrices rows x cols.
+ * FO_ERR_ARG for a negative size or one whose bytes pass 2^62. */
+fo_status fo_mx_sizes(int64_t batch, int64_t rows, int64_t cols, int64_t* code_bytes,
+                      int64_t* scale_bytes);
+
+/* Convert to the 4-bit form.  Per block of 32 values, with a the largest
+ * magnitude: the scale is 2^(floor(log2 a) - 2), at least 2^-127 (so a is
+ * between 4 and 8 scales), each value divided by it is rounded to the
+ * nearest E2M1 value, ties to the even code, magnitudes above 6 to 6.  A
+ * block that holds an infinity or a NaN gets the NaN scale.
+ *  src: device, type BF16 or F32.  Element (r, c) of matrix b is
+ *      src[b * batch_stride + r * row_stride + c], or with transpose
+ *      src[b * batch_stride + c * row_stride + r]; strides in elements, the
+ *      inner one is 1 (row_stride >= cols, with transpose >= rows).  Any
+ *      alignment of the element type.
+ *  row_index: NULL, or device int32[rows] (batch 1, no transpose): row r is
+ *      the source's row row_index[r]; an index outside [0, src_rows) marks a
+ *      row that holds no token, which becomes zeros.
+ *  codes, scales: device, 16-byte aligned, of fo_mx_sizes bytes. */
+fo_status fo_mx_quantize(const void* src, fo_type type, int64_t batch, int64_t batch_stride,
+                         int64_t rows, int64_t cols, int64_t row_stride, int32_t transpose,
+                         const int32_t* row_index, int64_t src_rows, void* codes, void* scales,
+                         void* cuda_stream);
+
+/* The values a 4-bit matrix stands for, in BF16 or F32 (both hold every
+ * such value that is below the type's largest; 6 * 2^127 and the like become
+ * infinity).  dst strides in elements, row_stride >= cols. */
+fo_status fo_mx_dequantize(const void* codes, const void* scales, int64_t batch, int64_t rows,
+                           int64_t cols, void* dst, fo_type type, int64_t batch_stride,
+                           int64_t row_stride, void* cuda_stream);
+
+/* D = A . B^T for 4-bit A (M x K) and B (N x K), both with their blocks
+ * along K; products exact, sums in fp32, one rounding to `type` (BF16 or
+ * F32).  With n_groups >= 1 a product per expert: B is a batch of n_groups
+ * matrices, and rows [group_first[g], group_first[g] + group_rows[g]) of A
+ * are multiplied by B_g; group_first[g] must be a multiple of 128 (as
+ * fo_moe_route makes it) and the ranges must be disjoint and inside [0, M).
+ * A group that breaks this is left out and sets *dev_status to FO_ERR_ARG.
+ * Rows in no group are not written.  n_groups = 0: one product over all M
+ * rows, group_first and group_rows NULL.
+ *  D: device, row_stride (elements) >= N; D and row_stride aligned to the
+ *      element only (16-byte aligned rows are stored faster).
+ *  A_codes, A_scales, B_codes, B_scales: device, 16-byte aligned.
+ *  group_first, group_rows: device int32[n_groups], n_groups <= 1024.
+ *  dev_status: device int32; a bounded wait that runs out sets it to
+ *      FO_ERR_TIMEOUT.
+ * Either operand can come from a transposed fo_mx_quantize, so the gradients
+ * dA = dD . B and dB = dD^T . A are this call on operands whose blocks lie
+ * along the summed axis.  K = 0 gives zeros. */
+fo_status fo_mx_gemm(int64_t M, int64_t N, int64_t K, const void* A_codes, const void* A_scales,
+                     const void* B_codes, const void* B_scales, int32_t n_groups,
+                     const int32_t* group_first, const int32_t* group_rows, void* D,
+                     fo_type type, int64_t row_stride, int32_t* dev_status, void* cuda_stream);
+
+/* Rows of fo_moe_route's row tables and bytes of its workspace.  capacity 0:
+ * experts' ranges packed, each starting on a multiple of 128;
+ * table_rows = the largest sum over any routing, (tokens * top_k + experts *
+ * 127) / 128 * 128.  capacity > 0: experts * capacity. */
+fo_status fo_moe_route_sizes(int64_t tokens, int32_t experts, int32_t top_k, int64_t capacity,
+                             int64_t* table_rows, int64_t* workspace_bytes);
+
+/* The router.  For each token the top_k largest of its `experts` logits, in
+ * descending order, ties to the lowest index, and their softmax weights:
+ *   p_e = exp(l_e - max l) / sum_j exp(l_j - max l),
+ *   weight = p_e, or with renormalize p_e / sum over the chosen experts.
+ * A logit of -inf bars the expert: where fewer than top_k are left, the
+ * rest of the row has id -1 and weight 0 (all barred: the whole row).  A NaN
+ * ranks above every number and makes the row's weights NaN, as does +inf.
+ * And the row tables of the products per expert (an expert's rows in the
+ * order of tokens, then slots):
+ *   expert_first[e], expert_rows[e]: expert e's range of rows (of
+ *       table_rows); with a capacity the range starts at e * capacity and
+ *       holds at most that many (the pairs past it, in token order, are
+ *       dropped), without one it starts on the next multiple of 128;
+ *   row_token, row_slot [table_rows]: the token and slot each row holds, -1
+ *       and 0 for none -- what fo_plan_route takes for a plan whose experts
+ *       have `capacity` rows, and fo_mx_quantize as row_index;
+ *   token_row [tokens * top_k]: the row of each (token, slot), -1 if it has
+ *       none.
+ * Integers only decide the tables, so they do not vary from run to run.
+ *  logits: device, BF16 or F32, row_stride (elements) >= experts.
+ *  ids int32, weights float [tokens * top_k]; experts <= 1024, top_k <= 32.
+ *  workspace: device, 16-byte aligned, fo_moe_route_sizes bytes, zeroed once
+ *      before its first use; every call leaves it ready for the next.  Calls
+ *      that overlap in time need one each.
+ *  dev_status: device int32, FO_ERR_TIMEOUT if a bounded wait ran out.  */
+fo_status fo_moe_route(const void* logits, fo_type type, int64_t tokens, int32_t experts,
+                       int64_t row_stride, int32_t top_k, int32_t renormalize, int64_t capacity,
+                       int32_t* ids, float* weights, int32_t* row_token, int32_t* row_slot,
+                       int32_t* token_row, int32_t* expert_first, int32_t* expert_rows,
+                       void* workspace, int32_t* dev_status, void* cuda_stream);
+
+/* Gradient of the logits from that of the weights, for the choice in ids:
+ *   renormalize: d_l[e_i] = w_i (g_i - sum_j w_j g_j), 0 elsewhere;
+ *   else:        d_l[e] = p_e ([e chosen] g - sum_j w_j g_j).
+ * Slots with id -1 take no part; a token with none gets zeros.  dlogits has
+ * the logits' type and is written whole (dlogits_stride >= experts). */
+fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens,
+                                int32_t experts, int64_t row_stride, int32_t top_k,
+                                int32_t renormalize, const int32_t* ids, const float* weights,
+                                const float* dweights, void* dlogits, int64_t dlogits_stride,
+                                void* cuda_stream);
+
+/* A whole expert layer for a few tokens (a generation step):
+ *   ids, w = router (as fo_moe_route) of logits = x . router^T;
+ *   y[t] = sum over slots i of w_i * W2[e_i] (act(G x_t) * (U x_t)),
+ * where W1[e] = [G; U] stacks the gate's `inter` rows on the up-projection's.
+ * A slot with id -1 adds nothing; a token with none gets zeros.
+ * Sums, logits, softmax and the activation are fp32; the hidden values
+ * act(.) * (.) are rounded once (below), y once to bf16.
+ *  weights FO_TYPE_BF16: W1 [experts][2 inter][hidden], W2
+ *      [experts][hidden][inter], row-major, scales NULL; hidden values are
+ *      rounded to bf16.
+ *  weights FO_TYPE_MX4: each expert's W1 (2 inter x hidden) and W2 (hidden x
+ *      inter) in the 4-bit form (a batch of `experts`); x and the hidden
+ *      values are taken at no less than bf16's 8 significant bits.
+ *  tokens 0 .. FO_MOE_FEW_TOKENS, experts <= 1024, top_k <= 32, hidden and
+ *  inter multiples of 8.
+ *  x: bf16, x_stride (elements) >= hidden; y: bf16, y_stride >= hidden.  x
+ *      and the weights 16-byte aligned, x_stride a multiple of 8.
+ *  router: bf16 [experts][hidden], 16-byte aligned.
+ *  workspace: as for fo_moe_route (zeroed once before its first use). */
+#define FO_MOE_FEW_TOKENS 64
+typedef struct {
+  int32_t tokens, hidden, inter, experts, top_k;
+  int32_t renormalize;
+  int32_t act;       /* fo_activation */
+  int32_t weights;   /* fo_type of W1 and W2 */
+} fo_moe_few_desc;
+
+fo_status fo_moe_few_workspace(const fo_moe_few_desc* desc, int64_t* bytes);
+fo_status fo_moe_few(const fo_moe_few_desc* desc, const void* x, int64_t x_stride,
+                     const void* router, const void* W1, const void* W1_scales, const void* W2,
+                     const void* W2_scales, void* y, int64_t y_stride, void* workspace,
+                     int32_t* dev_status, void* cuda_stream);
+
 const char* fo_status_string(fo_status status);
 
 #ifdef __cplusplus
