@@ -1,92 +1,435 @@
-// The product of two matrices in the microscaled 4-bit form:
-//   D[m][n] = sum_k a[m][k] b[n][k],  a = code value * scale, in fp32,
-// for all rows of A or for one range of rows per expert.
+// The product of two matrices in the microscaled 4-bit form, for all rows of
+// A or for one range of rows per expert:
+//   D[m][n] = sum_k a[m][k] b[n][k],  a[m][k] = value of the code x 2^(s - 127).
 //
-// The plain first form: a 64 x 64 tile per CTA, blocks of 32 columns decoded
-// to fp32 in shared memory, 4 x 4 sums per thread.
-#include <cuda_fp16.h>
+// The tensor cores take this form as it is (tcgen05.mma kind::mxf4 with block
+// scales): codes from shared memory, scales from tensor memory, sums in fp32
+// in tensor memory.  Nothing is decoded, so a value costs 4.25 bits on its
+// whole way from HBM.
+//
+// One persistent kernel, one CTA (or CTA pair) per SM (or pair of SMs):
+//  * warp 0: TMA producer.  A stage is 256 columns: 128 rows of A and this
+//    CTA's rows of B, 128 bytes each (one 128-byte swizzle atom), and the
+//    scales of both, in the blocks of 512 bytes that the form keeps them in.
+//  * warp 1: copies the stage's scales to tensor memory (tcgen05.cp, two
+//    slots in turn) and issues four MMAs of 64 columns, from one thread.
+//  * warps 2-5: epilogue.  Sums to bf16 or fp32, transposed through shared
+//    memory so that a row's stores are whole 128-byte segments.
+// The PAIR form computes 256 x BN with one cta_group::2 MMA: each CTA holds
+// 128 rows of A, half of B's rows and all of B's scales.
+//
+// Tensor memory: two sums of BN columns and two slots of scales in 512
+// columns.  BN = 256 leaves room for 464 columns of sums, so the second sum
+// starts at column 208 and shares 48 columns with the first: the epilogue
+// drains the shared columns of a tile first, and the next tile's MMAs wait for
+// those only.
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "moe_internal.h"
 #include "mx_common.cuh"
+#include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace fo {
 
 namespace {
 
-struct MxGemmArgs {
-  const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
-  int64_t M, N, K, k_blocks, n_row_blocks;
-  int32_t n_groups;
+constexpr int kThreads = 192;
+constexpr int kStageCols = 256;                  // columns of K per stage
+constexpr int kABytes = 128 * 128;
+constexpr int kBBytes = 128 * 128;               // room for this CTA's rows of B
+constexpr int kSaBytes = 1024;                   // 128 rows x 8 scales
+constexpr int kSbBytes = 3 * 1024;               // up to three blocks of rows
+constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
+constexpr int kStages = 5;
+constexpr int kStagingBytes = 4 * 32 * 128;
+constexpr int kStartOffset = kStages * kStageBytes + kStagingBytes;
+constexpr int kBarOffset = kStartOffset + 4 * (kRouteExperts + 4);
+constexpr int kSmemBytes = 1024 + kBarOffset + 256;
+constexpr int kBand = 16;                        // tile rows walked per column
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct GemmArgs {
+  CUtensorMap map_a, map_b, map_sa, map_sb;
   const int32_t* first;
   const int32_t* rows;
   void* d;
   int64_t stride;
-  int32_t bf16;
+  int32_t M, N, n_pad, n_groups, grouped;
+  int32_t k_stages, k_steps;   // stages of 256 columns, MMAs of 64 in all
+  int32_t bn, sb_blocks;       // tile columns, blocks of B's scales per stage
+  int32_t acc1, sf0, sf_cols;  // tensor memory: second sum, scales, columns per slot
+  int32_t bf16, vec;
   int32_t* status;
 };
 
-// One block of 32 columns of a row as fp32 into dst.
-__device__ void decode_block(const uint8_t* codes, const uint8_t* scales, int64_t row,
-                             int64_t k_blocks, int64_t kb, float* dst, int pitch) {
-  const uint8_t s = scales[((row / 128) * k_blocks + kb / 4) * 512 + mx_scale_row(int(row % 128)) +
-                           kb % 4];
-  const float scale = mx_scale_value(s);
-  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes + row * (k_blocks * 64) + kb * 16);
-  for (int o = 0; o < 4; ++o) {
-    uint32_t h[4];
-    mx_decode8(c[o], h);
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      dst[(o * 8 + 2 * i) * pitch] = f.x * scale;
-      dst[(o * 8 + 2 * i + 1) * pitch] = f.y * scale;
+// kind::mxf4: A and B E2M1 (1 at bits 7 and 10), scales E8M0 (bit 23), N >> 3
+// at 17, M >> 4 at 24.  The scale ids (bits 29 and 4) pick bytes 0-1 or 2-3 of
+// each 32-bit cell of scales.
+__device__ __forceinline__ uint32_t instruction(int m, int n) {
+  return (1u << 7) | (1u << 10) | (1u << 23) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+struct Tile {
+  int32_t row0, rows;   // first row of D, rows of the tile's range from there on
+  int32_t b_row, col0;  // first row of B's stack, first column of D
+};
+
+// Tile t of the launch.  Groups in order; inside a group bands of kBand tile
+// rows, column by column, so that tiles that run together share rows of A and
+// of B in L2.
+template <bool PAIR>
+__device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int32_t* start, int t, int& g) {
+  while (t >= start[g + 1]) ++g;
+  const int first = a.grouped ? __ldg(a.first + g) : 0, rows = a.grouped ? __ldg(a.rows + g) : a.M;
+  constexpr int kM = PAIR ? 256 : 128;
+  const int mt = (rows + kM - 1) / kM, nt = (a.N + a.bn - 1) / a.bn;
+  int i = t - start[g];
+  const int band = i / (kBand * nt);
+  i -= band * kBand * nt;
+  const int h = min(kBand, mt - band * kBand);
+  const int n = i / h, m = band * kBand + i % h;
+  return Tile{first + m * kM, rows - m * kM, g * a.n_pad + n * a.bn, n * a.bn};
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_constant__ GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  // 1024-byte alignment for the swizzle atoms, at the same offset in a pair
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int32_t* start = reinterpret_cast<int32_t*>(smem + kStartOffset);   // [groups + 1] tiles before
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOffset);    // PAIR: the leader's
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + 2;                                 // PAIR: the leader's
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = PAIR ? tc::cluster_rank() : 0;
+  constexpr int kM = PAIR ? 256 : 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), PAIR ? 2 : 1);
+      mbar_init(smem_u32(&empty[s]), 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), PAIR ? 8 : 4);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (a.k_stages > 0) {
+      tc::prefetch_map(&a.map_a);
+      tc::prefetch_map(&a.map_b);
+      tc::prefetch_map(&a.map_sa);
+      tc::prefetch_map(&a.map_sb);
+    }
+  }
+  if (warp == 1) tc::alloc<PAIR>(smem_u32(tmem_slot), 512);
+  // tiles before each group; a group out of order has none and is reported
+  if (warp == 2) {
+    const int nt = (a.N + a.bn - 1) / a.bn;
+    int before = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
+      const int g = g0 + lane;
+      int tiles = 0;
+      if (g < a.n_groups) {
+        const int f = a.grouped ? __ldg(a.first + g) : 0;
+        const int r = a.grouped ? __ldg(a.rows + g) : a.M;
+        if (f < 0 || r < 0 || (f & 127) || int64_t(f) + r > a.M) {
+          if (blockIdx.x == 0) atomicCAS(a.status, 0, int32_t(FO_ERR_ARG));
+        } else {
+          tiles = (r + kM - 1) / kM * nt;
+        }
+      }
+      int sum = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (g < a.n_groups) start[g] = before + sum - tiles;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) start[a.n_groups] = before;
+  }
+  tc::fence_before();
+  __syncthreads();
+  if constexpr (PAIR) tc::cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = start[a.n_groups];
+  const int worker = blockIdx.x / (PAIR ? 2 : 1), workers = gridDim.x / (PAIR ? 2 : 1);
+  const int b_rows = a.bn / (PAIR ? 2 : 1);    // rows of B this CTA stages
+  const bool shared_cols = a.acc1 < a.bn;      // the two sums overlap
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0 && a.k_stages > 0) {
+      int stage = 0, g = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int64_t issued = 0;
+      const uint64_t keep = tc::policy_evict_last();
+      const uint32_t bytes = uint32_t(kABytes + b_rows * 128 + kSaBytes + a.sb_blocks * 1024);
+      for (int t = worker; ok && t < tiles; t += workers) {
+        const Tile w = tile_at<PAIR>(a, start, t, g);
+        const int a_row = w.row0 + int(rank) * 128;
+        for (int kb = 0; kb < a.k_stages; ++kb) {
+          if (!tc::wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+          const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSaBytes;
+          if constexpr (PAIR) {
+            const uint32_t fb = tc::map_to_rank(smem_u32(&full[stage]), 0);
+            if (rank == 0)
+              mbar_expect_tx(smem_u32(&full[stage]), bytes);
+            else
+              tc::expect_tx_cluster(fb, bytes);
+            tc::load_2d_pair(sa, &a.map_a, fb, kb * 128, a_row, keep);
+            tc::load_2d_pair(sb, &a.map_b, fb, kb * 128, w.b_row + int(rank) * b_rows, keep);
+            tc::load_2d_pair(ssa, &a.map_sa, fb, kb * 256, a_row / 128, keep);
+            tc::load_2d_pair(ssb, &a.map_sb, fb, kb * 256, w.b_row / 128, keep);
+          } else {
+            const uint32_t fb = smem_u32(&full[stage]);
+            mbar_expect_tx(fb, bytes);
+            tc::load_2d(sa, &a.map_a, fb, kb * 128, a_row, keep);
+            tc::load_2d(sb, &a.map_b, fb, kb * 128, w.b_row, keep);
+            tc::load_2d(ssa, &a.map_sa, fb, kb * 256, a_row / 128, keep);
+            tc::load_2d(ssb, &a.map_sb, fb, kb * 256, w.b_row / 128, keep);
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // winding down: copies already issued land before the CTA exits
+        for (int s = 0; s < kStages; ++s) {
+          const int64_t fills = issued / kStages + (s < issued % kStages ? 1 : 0);
+          if (fills > 0) tc::wait_drain(smem_u32(&full[s]), uint32_t((fills - 1) & 1));
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0 && a.k_stages > 0) {
+      const uint32_t idesc = instruction(kM, a.bn);
+      int stage = 0, slot = 0, g = 0, i = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = worker; ok && t < tiles; t += workers, ++i) {
+        const Tile w = tile_at<PAIR>(a, start, t, g);
+        const int acc = i & 1;
+        // the sum's columns are free: all of tile i - 2's, or, where the two
+        // sums share columns, those of tile i - 1's that are shared
+        const int wait_tile = shared_cols ? i - 1 : i - 2;
+        if (wait_tile >= 0 && !tc::wait(smem_u32(&acc_empty[acc]), uint32_t(wait_tile >> 1) & 1,
+                                        abort_flag, a.status))
+          break;
+        tc::fence_after();
+        const uint32_t d = tmem + uint32_t(acc ? a.acc1 : 0);
+        const uint32_t b_shift = uint32_t(w.b_row % 128) / 32;   // columns of scales before b_row
+        int steps = a.k_steps;
+        for (int kb = 0; kb < a.k_stages; ++kb, steps -= 4) {
+          if (!tc::wait(smem_u32(&full[stage]), phase, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+          const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSaBytes;
+          const uint32_t sfa = tmem + uint32_t(a.sf0 + slot * a.sf_cols), sfb = sfa + 8;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tc::copy_scales<PAIR>(sfa + c * 4, ssa + c * 512);
+            for (int r = 0; r < a.sb_blocks; ++r)
+              tc::copy_scales<PAIR>(sfb + uint32_t(c * a.sb_blocks + r) * 4,
+                                    ssb + r * 1024 + c * 512);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < steps) {
+              const uint32_t id = (kk & 1) ? (2u << 29) | (2u << 4) : 0u;
+              tc::mma_mxf4<PAIR>(d, tc::smem_desc(sa + kk * 32, 16, 1024, 2),
+                                 tc::smem_desc(sb + kk * 32, 16, 1024, 2), idesc | id,
+                                 sfa + (kk >> 1) * 4,
+                                 sfb + uint32_t((kk >> 1) * a.sb_blocks) * 4 + b_shift,
+                                 (kb | kk) ? 1u : 0u);
+            }
+          }
+          tc::commit<PAIR>(smem_u32(&empty[stage]));
+          slot ^= 1;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        tc::commit<PAIR>(smem_u32(&acc_full[acc]));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;   // this warp's quarter of the tensor memory lanes
+    const uint32_t staging = smem_u32(smem + kStages * kStageBytes + (warp - 2) * (32 * 128));
+    const int chunks = (a.bn + 63) / 64;
+    const int es = a.bf16 ? 2 : 4;
+    int g = 0, i = 0;
+    for (int t = worker; t < tiles; t += workers, ++i) {
+      const Tile w = tile_at<PAIR>(a, start, t, g);
+      const int acc = i & 1;
+      const bool zero = a.k_stages == 0;
+      if (!zero &&
+          !tc::wait_warp(smem_u32(&acc_full[acc]), uint32_t(i >> 1) & 1, abort_flag, a.status))
+        break;
+      tc::fence_after();
+      const int r0 = int(rank) * 128 + q * 32;     // this warp's first row of the tile
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc ? a.acc1 : 0);
+      uint8_t* out = static_cast<uint8_t*>(a.d) + (int64_t(w.row0 + r0) * a.stride + w.col0) * es;
+#pragma unroll 1
+      for (int k = 0; k < chunks; ++k) {
+        // columns shared with the other sum first: the last of sum 0, the
+        // first of sum 1
+        const int c = acc ? k : chunks - 1 - k;
+        uint32_t v0[32], v1[32];
+        if (!zero) {
+          tc::tmem_ld32(taddr + c * 64, v0);
+          tc::tmem_ld32(taddr + c * 64 + 32, v1);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v0[e] = v1[e] = 0u;
+        }
+        if (!zero && k == (shared_cols ? 0 : chunks - 1)) {
+          // hand the columns to the MMA warp: the other sum's next tile, or
+          // this sum's
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&acc_empty[shared_cols ? acc ^ 1 : acc]);
+            if (PAIR && rank != 0)
+              tc::arrive_cluster(tc::map_to_rank(bar, 0));
+            else
+              mbar_arrive(bar);
+          }
+        }
+        // 32 rows x 128 bytes at a time through the staging buffer: 64
+        // columns of bf16, or twice 32 of fp32
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (a.bf16 && half == 1) break;
+          const int col = c * 64 + half * 32;      // first column of these 128 bytes
+          if (col >= a.bn || w.col0 + col >= a.N) continue;   // (uniform)
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            uint32_t x[4];
+            if (a.bf16) {
+              const uint32_t* s = p < 4 ? &v0[p * 8] : &v1[(p - 4) * 8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = pack_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = half ? v1[p * 4 + e] : v0[p * 4 + e];
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             staging + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                         "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                         : "memory");
+          }
+          __syncwarp();
+          const int piece = lane & 7, per = 16 / es;
+          const int left = min(a.N - w.col0, a.bn) - col - piece * per;   // columns from here on
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int row = it * 4 + (lane >> 3);
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(staging + row * 128 + ((piece ^ (row & 7)) << 4))
+                         : "memory");
+            if (r0 + row >= w.rows || left <= 0) continue;
+            uint8_t* to = out + (int64_t(row) * a.stride + col + piece * per) * es;
+            if (a.vec && left >= per) {
+              *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+            } else if (a.bf16) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e < left)
+                  reinterpret_cast<uint16_t*>(to)[e] = uint16_t(x[e / 2] >> (16 * (e & 1)));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (e < left) reinterpret_cast<uint32_t*>(to)[e] = x[e];
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncthreads();
+  if (warp == 1) {
+    // every MMA has completed before the tensor memory is released
+    if (lane == 0) {
+      if (rank == 0) tc::commit<PAIR>(smem_u32(drain));
+      tc::wait_drain(smem_u32(drain), 0);
+    }
+    __syncwarp();
+  }
+  tc::fence_before();
+  if constexpr (PAIR) tc::cluster_sync();   // neither CTA leaves while the pair still works
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc<PAIR>(tmem, 512);
   }
 }
 
-__global__ void __launch_bounds__(256) mx_gemm_kernel(const MxGemmArgs a) {
-  __shared__ float as[32][65], bs[32][65];
-  const int g = blockIdx.z;
-  int64_t first = 0, rows = a.M;
-  if (a.n_groups > 0) {
-    first = a.first[g];
-    rows = a.rows[g];
-    if (first < 0 || rows < 0 || first % 128 || first + rows > a.M) {
-      if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
-        atomicCAS(a.status, 0, int32_t(FO_ERR_ARG));
-      return;
-    }
+template <bool PAIR>
+fo_status launch(const GemmArgs& a, int grid, cudaStream_t st) {
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
+  const int slot = dev < 64 ? dev : 63;
+  std::call_once(once[slot], [&] {
+    err[slot] = cudaFuncSetAttribute(mx_gemm_kernel<PAIR>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<PAIR>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return FO_ERR_CUDA;
   }
-  const int64_t n0 = int64_t(blockIdx.x) * 64;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  for (int64_t m0 = int64_t(blockIdx.y) * 64; m0 < rows; m0 += int64_t(gridDim.y) * 64) {
-    float acc[4][4] = {};
-    for (int64_t kb = 0; kb < (a.K + 31) / 32; ++kb) {
-      __syncthreads();
-      if (threadIdx.x < 64) {
-        decode_block(a.a_codes, a.a_scales, first + m0 + threadIdx.x, a.k_blocks, kb,
-                     &as[0][threadIdx.x], 65);
-      } else if (threadIdx.x < 128) {
-        const int r = threadIdx.x - 64;
-        decode_block(a.b_codes, a.b_scales, g * a.n_row_blocks * 128 + n0 + r, a.k_blocks, kb,
-                     &bs[0][r], 65);
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) acc[i][j] += as[k][ty * 4 + i] * bs[k][tx * 4 + j];
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (m >= rows || n >= a.N) continue;
-        const int64_t at = (first + m) * a.stride + n;
-        if (a.bf16)
-          static_cast<__nv_bfloat16*>(a.d)[at] = __float2bfloat16_rn(acc[i][j]);
-        else
-          static_cast<float*>(a.d)[at] = acc[i][j];
-      }
-  }
+  return FO_OK;
 }
 
 }  // namespace
@@ -97,14 +440,56 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
                          const int32_t* group_rows, void* D, fo_type type, int64_t row_stride,
                          int32_t* dev_status, void* stream) {
   if (M == 0 || N == 0) return FO_OK;
-  MxGemmArgs a{static_cast<const uint8_t*>(a_codes), static_cast<const uint8_t*>(a_scales),
-               static_cast<const uint8_t*>(b_codes), static_cast<const uint8_t*>(b_scales),
-               M, N, K, mx_up(K, 128) / 128, mx_up(N, 128) / 128, n_groups, group_first,
-               group_rows, D, row_stride, type == FO_TYPE_BF16, dev_status};
-  const dim3 grid(unsigned((N + 63) / 64), unsigned(M < 64 * 1024 ? (M + 63) / 64 : 1024),
-                  n_groups > 0 ? n_groups : 1);
-  mx_gemm_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FO_ERR_CUDA;
+  const int64_t groups = n_groups > 0 ? n_groups : 1;
+  const int64_t kb = mx_up(K, 128) / 128;               // blocks of scales per row of blocks
+  const int64_t mb = mx_up(M, 128) / 128, nb = mx_up(N, 128) / 128 * groups;
+  // A pair reads half as much of B per CTA; with no more rows than one CTA
+  // takes, its second half would be empty.
+  const bool pair = M > 128;
+  GemmArgs a{};
+  a.bn = pair ? 256 : 128;
+  a.sb_blocks = 2;
+  a.acc1 = a.bn == 256 ? 208 : 224;
+  a.sf_cols = 8 + 8 * a.sb_blocks;
+  a.sf0 = 512 - 2 * a.sf_cols;
+  if (K > 0) {
+    const uint64_t pitch = uint64_t(kb) * 64;
+    const uint32_t b_rows = uint32_t(pair ? a.bn / 2 : a.bn);
+    if (!encode_tensor_map(&a.map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, pitch, mb * 128, pitch,
+                           128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&a.map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, pitch, nb * 128, pitch,
+                           128, b_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&a.map_sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kb * 128, mb,
+                           kb * 512, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_tensor_map(&a.map_sb, CU_TENSOR_MAP_DATA_TYPE_UINT32, b_scales, kb * 128, nb,
+                           kb * 512, 256, a.sb_blocks, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return FO_ERR_CUDA;
+  }
+  a.first = group_first;
+  a.rows = group_rows;
+  a.d = D;
+  a.stride = row_stride;
+  a.M = int32_t(M);
+  a.N = int32_t(N);
+  a.n_pad = int32_t(mx_up(N, 128));
+  a.n_groups = int32_t(groups);
+  a.grouped = n_groups > 0;
+  a.k_stages = int32_t((K + kStageCols - 1) / kStageCols);
+  a.k_steps = int32_t((K + 63) / 64);
+  a.bf16 = type == FO_TYPE_BF16;
+  const int es = a.bf16 ? 2 : 4;
+  a.vec = ((reinterpret_cast<uintptr_t>(D) | uintptr_t(row_stride) * es) & 15) == 0;
+  a.status = dev_status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // no more workers than tiles (with experts: than any ranges can make)
+  const int64_t most = (mb + groups) * ((N + a.bn - 1) / a.bn);
+  const int64_t workers = pair ? sms / 2 : sms;
+  const int64_t use = most < workers ? most : workers;
+  return pair ? launch<true>(a, int(2 * use), st) : launch<false>(a, int(use), st);
 }
 
 }  // namespace fo

@@ -15,4 +15,10 @@ namespace fo {
 bool encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                           uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 
+// The same for any element type, row pitch (bytes, a multiple of 16) and
+// swizzle: `inner` and `box_inner` count elements.
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                       uint64_t inner, uint64_t outer, uint64_t pitch_bytes, uint32_t box_inner,
+                       uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
 }  // namespace fo
