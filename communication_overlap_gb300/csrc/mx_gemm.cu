@@ -11,10 +11,14 @@
 //  * warp 0: TMA producer.  A stage is 256 columns: 128 rows of A and this
 //    CTA's rows of B, 128 bytes each (one 128-byte swizzle atom), and the
 //    scales of both, in the blocks of 512 bytes that the form keeps them in.
-//  * warp 1: copies the stage's scales to tensor memory (tcgen05.cp, two
-//    slots in turn) and issues four MMAs of 64 columns, from one thread.
+//  * warp 1: four MMAs of 64 columns per stage, from one thread.
 //  * warps 2-5: epilogue.  Sums to bf16 or fp32, transposed through shared
 //    memory so that a row's stores are whole 128-byte segments.
+//  * warps 6-9: the stage's scales from shared to tensor memory, through
+//    registers (tcgen05.st, a quarter of the lanes per warp), into two slots in
+//    turn.  tcgen05.cp does the same from the MMA's thread, but in line with
+//    the MMAs: the 8-expert product of 32768 x 14336 x 4096 took 1163 us with
+//    six copies per stage, against 774 us with the copies (wrongly) left out.
 // The PAIR form computes 256 x BN with one cta_group::2 MMA: each CTA holds
 // 128 rows of A, half of B's rows and all of B's scales.
 //
@@ -37,7 +41,7 @@ namespace fo {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kStageCols = 256;                  // columns of K per stage
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 128 * 128;               // room for this CTA's rows of B
@@ -45,7 +49,8 @@ constexpr int kSaBytes = 1024;                   // 128 rows x 8 scales
 constexpr int kSbBytes = 3 * 1024;               // up to three blocks of rows
 constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
 constexpr int kStages = 5;
-constexpr int kStagingBytes = 4 * 32 * 128;
+constexpr int kSlots = 4;                        // slots of scales in tensor memory
+constexpr int kStagingBytes = 4 * 2 * 32 * 128;    // two buffers per epilogue warp
 constexpr int kStartOffset = kStages * kStageBytes + kStagingBytes;
 constexpr int kBarOffset = kStartOffset + 4 * (kRouteExperts + 4);
 constexpr int kSmemBytes = 1024 + kBarOffset + 256;
@@ -53,7 +58,7 @@ constexpr int kBand = 16;                        // tile rows walked per column
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct GemmArgs {
-  CUtensorMap map_a, map_b, map_sa, map_sb;
+  CUtensorMap map_a, map_b, map_sa, map_sb, map_d;
   const int32_t* first;
   const int32_t* rows;
   void* d;
@@ -62,7 +67,8 @@ struct GemmArgs {
   int32_t k_stages, k_steps;   // stages of 256 columns, MMAs of 64 in all
   int32_t bn, sb_blocks;       // tile columns, blocks of B's scales per stage
   int32_t acc1, sf0, sf_cols;  // tensor memory: second sum, scales, columns per slot
-  int32_t bf16, vec;
+  int32_t vec;                 // map_d can address D's rows
+  int32_t n_copied;            // a 128-byte wide copy to D may reach up to this column
   int32_t* status;
 };
 
@@ -71,6 +77,12 @@ struct GemmArgs {
 // each 32-bit cell of scales.
 __device__ __forceinline__ uint32_t instruction(int m, int n) {
   return (1u << 7) | (1u << 10) | (1u << 23) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+// Wait until at most N of this thread's bulk stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 struct Tile {
@@ -95,7 +107,7 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int32_t* start,
   return Tile{first + m * kM, rows - m * kM, g * a.n_pad + n * a.bn, n * a.bn};
 }
 
-template <bool PAIR>
+template <bool PAIR, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_constant__ GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the swizzle atoms, at the same offset in a pair
@@ -106,11 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;                                 // PAIR: the leader's
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* sf_full = acc_empty + 2;       // a stage's scales are in this CTA's shared memory
+  uint64_t* sf_ready = sf_full + kStages;  // PAIR: the leader's; a slot's are in tensor memory
+  uint64_t* drain = sf_ready + kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = PAIR ? tc::cluster_rank() : 0;
   constexpr int kM = PAIR ? 256 : 128;
 
@@ -118,11 +132,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&full[s]), PAIR ? 2 : 1);
       mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&sf_full[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
       mbar_init(smem_u32(&acc_empty[b]), PAIR ? 8 : 4);
     }
+    for (int b = 0; b < kSlots; ++b) mbar_init(smem_u32(&sf_ready[b]), PAIR ? 8 : 4);
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -180,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       bool ok = true;
       int64_t issued = 0;
       const uint64_t keep = tc::policy_evict_last();
-      const uint32_t bytes = uint32_t(kABytes + b_rows * 128 + kSaBytes + a.sb_blocks * 1024);
+      const uint32_t bytes = uint32_t(kABytes + b_rows * 128);
+      const uint32_t sf_bytes = uint32_t(kSaBytes + a.sb_blocks * 1024);
       for (int t = worker; ok && t < tiles; t += workers) {
         const Tile w = tile_at<PAIR>(a, start, t, g);
         const int a_row = w.row0 + int(rank) * 128;
@@ -191,6 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           }
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
           const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSaBytes;
+          const uint32_t sfb = smem_u32(&sf_full[stage]);
+          mbar_expect_tx(sfb, sf_bytes);
+          tc::load_2d(ssa, &a.map_sa, sfb, kb * 256, a_row / 128, keep);
+          tc::load_2d(ssb, &a.map_sb, sfb, kb * 256, w.b_row / 128, keep);
           if constexpr (PAIR) {
             const uint32_t fb = tc::map_to_rank(smem_u32(&full[stage]), 0);
             if (rank == 0)
@@ -199,15 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
               tc::expect_tx_cluster(fb, bytes);
             tc::load_2d_pair(sa, &a.map_a, fb, kb * 128, a_row, keep);
             tc::load_2d_pair(sb, &a.map_b, fb, kb * 128, w.b_row + int(rank) * b_rows, keep);
-            tc::load_2d_pair(ssa, &a.map_sa, fb, kb * 256, a_row / 128, keep);
-            tc::load_2d_pair(ssb, &a.map_sb, fb, kb * 256, w.b_row / 128, keep);
           } else {
             const uint32_t fb = smem_u32(&full[stage]);
             mbar_expect_tx(fb, bytes);
             tc::load_2d(sa, &a.map_a, fb, kb * 128, a_row, keep);
             tc::load_2d(sb, &a.map_b, fb, kb * 128, w.b_row, keep);
-            tc::load_2d(ssa, &a.map_sa, fb, kb * 256, a_row / 128, keep);
-            tc::load_2d(ssb, &a.map_sb, fb, kb * 256, w.b_row / 128, keep);
           }
           ++issued;
           if (++stage == kStages) {
@@ -216,20 +233,26 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           }
         }
       }
-      if (!ok && rank == 0) {
+      if (!ok) {
         // winding down: copies already issued land before the CTA exits
         for (int s = 0; s < kStages; ++s) {
           const int64_t fills = issued / kStages + (s < issued % kStages ? 1 : 0);
-          if (fills > 0) tc::wait_drain(smem_u32(&full[s]), uint32_t((fills - 1) & 1));
+          if (fills == 0) continue;
+          tc::wait_drain(smem_u32(&sf_full[s]), uint32_t((fills - 1) & 1));
+          if (rank == 0) tc::wait_drain(smem_u32(&full[s]), uint32_t((fills - 1) & 1));
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0 && a.k_stages > 0) {
+    // The whole warp walks the loop, so that descriptors stay in uniform
+    // registers, and one elected thread issues.
+    if (rank == 0 && a.k_stages > 0) {
       const uint32_t idesc = instruction(kM, a.bn);
-      int stage = 0, slot = 0, g = 0, i = 0;
-      uint32_t phase = 0;
+      const uint64_t desc0 = tc::smem_desc(smem_u32(smem), 16, 1024, 2);
+      const bool leader = tc::elect_one();
+      int stage = 0, g = 0, i = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0;
       bool ok = true;
       for (int t = worker; ok && t < tiles; t += workers, ++i) {
         const Tile w = tile_at<PAIR>(a, start, t, g);
@@ -237,62 +260,106 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         // the sum's columns are free: all of tile i - 2's, or, where the two
         // sums share columns, those of tile i - 1's that are shared
         const int wait_tile = shared_cols ? i - 1 : i - 2;
-        if (wait_tile >= 0 && !tc::wait(smem_u32(&acc_empty[acc]), uint32_t(wait_tile >> 1) & 1,
-                                        abort_flag, a.status))
+        if (wait_tile >= 0 && !tc::wait_warp(smem_u32(&acc_empty[acc]),
+                                             uint32_t(wait_tile >> 1) & 1, abort_flag, a.status))
           break;
-        tc::fence_after();
         const uint32_t d = tmem + uint32_t(acc ? a.acc1 : 0);
         const uint32_t b_shift = uint32_t(w.b_row % 128) / 32;   // columns of scales before b_row
+        const uint32_t sf_b = 8 + b_shift, sf_half = uint32_t(a.sb_blocks) * 4;
         int steps = a.k_steps;
         for (int kb = 0; kb < a.k_stages; ++kb, steps -= 4) {
-          if (!tc::wait(smem_u32(&full[stage]), phase, abort_flag, a.status)) {
+          if (!tc::wait_warp(smem_u32(&sf_ready[slot]), slot_phase, abort_flag, a.status) ||
+              !tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status)) {
             ok = false;
             break;
           }
           tc::fence_after();
-          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-          const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSaBytes;
-          const uint32_t sfa = tmem + uint32_t(a.sf0 + slot * a.sf_cols), sfb = sfa + 8;
+          const uint64_t da = desc0 + uint64_t(stage * (kStageBytes >> 4));
+          const uint64_t db = da + (kABytes >> 4);
+          const uint32_t sfa = tmem + uint32_t(a.sf0 + slot * a.sf_cols), sfb = sfa + sf_b;
+          if (leader) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tc::copy_scales<PAIR>(sfa + c * 4, ssa + c * 512);
-            for (int r = 0; r < a.sb_blocks; ++r)
-              tc::copy_scales<PAIR>(sfb + uint32_t(c * a.sb_blocks + r) * 4,
-                                    ssb + r * 1024 + c * 512);
-          }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk < steps) {
-              const uint32_t id = (kk & 1) ? (2u << 29) | (2u << 4) : 0u;
-              tc::mma_mxf4<PAIR>(d, tc::smem_desc(sa + kk * 32, 16, 1024, 2),
-                                 tc::smem_desc(sb + kk * 32, 16, 1024, 2), idesc | id,
-                                 sfa + (kk >> 1) * 4,
-                                 sfb + uint32_t((kk >> 1) * a.sb_blocks) * 4 + b_shift,
-                                 (kb | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < steps) {
+                constexpr uint32_t kHigh = (2u << 29) | (2u << 4);
+                tc::mma_mxf4<PAIR>(d, da + kk * 2, db + kk * 2, (kk & 1) ? idesc | kHigh : idesc,
+                                   sfa + (kk >> 1) * 4, sfb + (kk >> 1) * sf_half,
+                                   (kb | kk) ? 1u : 0u);
+              }
             }
+            tc::commit<PAIR>(smem_u32(&empty[stage]));
           }
-          tc::commit<PAIR>(smem_u32(&empty[stage]));
-          slot ^= 1;
+          __syncwarp();
+          if (++slot == kSlots) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        tc::commit<PAIR>(smem_u32(&acc_full[acc]));
+        if (leader) tc::commit<PAIR>(smem_u32(&acc_full[acc]));
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------ scales
+    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = a.k_stages > 0;
+    for (int t = worker; ok && t < tiles; t += workers) {
+      for (int kb = 0; kb < a.k_stages; ++kb, ++it) {
+        ok = tc::wait_warp(smem_u32(&sf_full[stage]), phase, abort_flag, a.status);
+        // the slot's MMAs of kSlots stages ago have completed: they were the
+        // last to read that stage's shared memory, too
+        if (ok && it >= kSlots) {
+          const uint32_t j = it - kSlots;
+          ok = tc::wait_warp(smem_u32(&empty[j % kStages]), (j / kStages) & 1, abort_flag,
+                             a.status);
+        }
+        if (!ok) break;
+        tc::fence_after();
+        // a block of scales is 32 lanes x 16 bytes: a lane's four columns
+        const uint32_t from = smem_u32(smem + stage * kStageBytes) + kABytes + kBBytes + lane * 16;
+        const uint32_t to = tmem + quarter + uint32_t(a.sf0) + (it % kSlots) * uint32_t(a.sf_cols);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tc::store_scales(to + c * 4, from + c * 512);
+          for (int r = 0; r < a.sb_blocks; ++r)
+            tc::store_scales(to + 8 + uint32_t(c * a.sb_blocks + r) * 4,
+                             from + kSaBytes + r * 1024 + c * 512);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sf_ready[it % kSlots]);
+          if (PAIR && rank != 0)
+            tc::arrive_cluster_relaxed(tc::map_to_rank(bar, 0));
+          else
+            mbar_arrive(bar);
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // this warp's quarter of the tensor memory lanes
-    const uint32_t staging = smem_u32(smem + kStages * kStageBytes + (warp - 2) * (32 * 128));
-    const int chunks = (a.bn + 63) / 64;
-    const int es = a.bf16 ? 2 : 4;
+    const uint32_t staging = smem_u32(smem + kStages * kStageBytes + (warp - 2) * (2 * 32 * 128));
+    const int halves = (a.bn + 127) / 128;       // 128 columns at a time
+    constexpr int es = BF16 ? 2 : 4;
+    const bool zero = a.k_stages == 0;
     int g = 0, i = 0;
+    uint32_t turn = 0;   // staging buffers used so far
     for (int t = worker; t < tiles; t += workers, ++i) {
       const Tile w = tile_at<PAIR>(a, start, t, g);
       const int acc = i & 1;
-      const bool zero = a.k_stages == 0;
       if (!zero &&
           !tc::wait_warp(smem_u32(&acc_full[acc]), uint32_t(i >> 1) & 1, abort_flag, a.status))
         break;
@@ -301,86 +368,103 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc ? a.acc1 : 0);
       uint8_t* out = static_cast<uint8_t*>(a.d) + (int64_t(w.row0 + r0) * a.stride + w.col0) * es;
 #pragma unroll 1
-      for (int k = 0; k < chunks; ++k) {
+      for (int k = 0; k < halves; ++k) {
         // columns shared with the other sum first: the last of sum 0, the
         // first of sum 1
-        const int c = acc ? k : chunks - 1 - k;
-        uint32_t v0[32], v1[32];
+        const int c0 = (acc ? k : halves - 1 - k) * 128;
+        uint32_t v[4][32];
         if (!zero) {
-          tc::tmem_ld32(taddr + c * 64, v0);
-          tc::tmem_ld32(taddr + c * 64 + 32, v1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::tmem_ld32(taddr + c0 + j * 32, v[j]);
           tc::tmem_wait_ld();
+          if (k == (shared_cols ? 0 : halves - 1)) {
+            // hand the columns to the MMA warp: for the other sum's next
+            // tile, or for this sum's.  (The loads are complete; a release
+            // would also wait for this warp's stores to D.)
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&acc_empty[shared_cols ? acc ^ 1 : acc]);
+              if (PAIR && rank != 0)
+                tc::arrive_cluster_relaxed(tc::map_to_rank(bar, 0));
+              else
+                mbar_arrive(bar);
+            }
+          }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v0[e] = v1[e] = 0u;
-        }
-        if (!zero && k == (shared_cols ? 0 : chunks - 1)) {
-          // hand the columns to the MMA warp: the other sum's next tile, or
-          // this sum's
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&acc_empty[shared_cols ? acc ^ 1 : acc]);
-            if (PAIR && rank != 0)
-              tc::arrive_cluster(tc::map_to_rank(bar, 0));
-            else
-              mbar_arrive(bar);
-          }
-        }
-        // 32 rows x 128 bytes at a time through the staging buffer: 64
-        // columns of bf16, or twice 32 of fp32
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (a.bf16 && half == 1) break;
-          const int col = c * 64 + half * 32;      // first column of these 128 bytes
+            for (int e = 0; e < 32; ++e) v[j][e] = 0u;
+        }
+        // 32 rows x 128 bytes at a time through a staging buffer: 64 columns
+        // of bf16 or 32 of fp32, 16-byte pieces rotated by row as the 128-byte
+        // swizzle has them
+#pragma unroll
+        for (int j = 0; j < 4; j += BF16 ? 2 : 1) {
+          const int col = c0 + j * 32;             // first column of these 128 bytes
           if (col >= a.bn || w.col0 + col >= a.N) continue;   // (uniform)
+          const uint32_t buf = staging + (turn & 1) * (32 * 128);
+          ++turn;
+          if (lane == 0) bulk_wait_read<1>();      // the store that last read this buffer
+          __syncwarp();
 #pragma unroll
           for (int p = 0; p < 8; ++p) {
             uint32_t x[4];
-            if (a.bf16) {
-              const uint32_t* s = p < 4 ? &v0[p * 8] : &v1[(p - 4) * 8];
+            if constexpr (BF16) {
+              const uint32_t* s = p < 4 ? &v[j][p * 8] : &v[j + 1][(p - 4) * 8];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 x[e] = pack_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
             } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = half ? v1[p * 4 + e] : v0[p * 4 + e];
+              for (int e = 0; e < 4; ++e) x[e] = v[j][p * 4 + e];
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             staging + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                             buf + lane * 128 + ((p ^ (lane & 7)) << 4)),
                          "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                          : "memory");
           }
-          __syncwarp();
-          const int piece = lane & 7, per = 16 / es;
-          const int left = min(a.N - w.col0, a.bn) - col - piece * per;   // columns from here on
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int row = it * 4 + (lane >> 3);
-            uint32_t x[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(staging + row * 128 + ((piece ^ (row & 7)) << 4))
-                         : "memory");
-            if (r0 + row >= w.rows || left <= 0) continue;
-            uint8_t* to = out + (int64_t(row) * a.stride + col + piece * per) * es;
-            if (a.vec && left >= per) {
-              *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
-            } else if (a.bf16) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (e < left)
-                  reinterpret_cast<uint16_t*>(to)[e] = uint16_t(x[e / 2] >> (16 * (e & 1)));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (e < left) reinterpret_cast<uint32_t*>(to)[e] = x[e];
+          constexpr int kWide = BF16 ? 64 : 32;
+          if (a.vec && r0 + 32 <= w.rows && w.col0 + col + kWide <= a.n_copied) {
+            // one copy for the 32 rows
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              tensor_store_2d(&a.map_d, buf, w.col0 + col, w.row0 + r0);
+              bulk_commit();
             }
+          } else {
+            // rows that end with the range, or rows of D that no copy can
+            // address: element by element
+            __syncwarp();
+            const int left = min(a.N - w.col0, a.bn) - col;
+            for (int row = 0; row < 32 && r0 + row < w.rows; ++row) {
+#pragma unroll
+              for (int h = 0; h < kWide / 32; ++h) {
+                const int c = h * 32 + lane, byte = c * es;
+                const uint32_t from = buf + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
+                uint8_t* to = out + (int64_t(row) * a.stride + col + c) * es;
+                if (c < left) {
+                  if constexpr (BF16) {
+                    uint16_t x;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
+                    *reinterpret_cast<uint16_t*>(to) = x;
+                  } else {
+                    uint32_t x;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+                    *reinterpret_cast<uint32_t*>(to) = x;
+                  }
+                }
+              }
+            }
+            __syncwarp();
+            if (lane == 0) bulk_commit();   // an empty group: the buffers' turns count groups
           }
-          __syncwarp();
         }
       }
     }
+    if (lane == 0) bulk_wait_all();   // this warp's copies to D have been written
   }
 
   // ------------------------------------------------------------ teardown
@@ -401,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   }
 }
 
-template <bool PAIR>
+template <bool PAIR, bool BF16>
 fo_status launch(const GemmArgs& a, int grid, cudaStream_t st) {
   static std::once_flag once[64];
   static cudaError_t err[64];
@@ -409,7 +493,7 @@ fo_status launch(const GemmArgs& a, int grid, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
   const int slot = dev < 64 ? dev : 63;
   std::call_once(once[slot], [&] {
-    err[slot] = cudaFuncSetAttribute(mx_gemm_kernel<PAIR>,
+    err[slot] = cudaFuncSetAttribute(mx_gemm_kernel<PAIR, BF16>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
@@ -425,7 +509,7 @@ fo_status launch(const GemmArgs& a, int grid, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<PAIR>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<PAIR, BF16>, a) != cudaSuccess) {
     cudaGetLastError();
     return FO_ERR_CUDA;
   }
@@ -453,9 +537,9 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
   GemmArgs a{};
   a.bn = pair ? 256 : 128;
   a.sb_blocks = 2;
-  a.acc1 = a.bn == 256 ? 208 : 224;
   a.sf_cols = 8 + 8 * a.sb_blocks;
-  a.sf0 = 512 - 2 * a.sf_cols;
+  a.sf0 = 512 - kSlots * a.sf_cols;
+  a.acc1 = a.sf0 - a.bn < a.bn ? a.sf0 - a.bn : a.bn;
   if (K > 0) {
     const uint64_t pitch = uint64_t(kb) * 64;
     const uint32_t b_rows = uint32_t(pair ? a.bn / 2 : a.bn);
@@ -480,16 +564,27 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
   a.grouped = n_groups > 0;
   a.k_stages = int32_t((K + kStageCols - 1) / kStageCols);
   a.k_steps = int32_t((K + 63) / 64);
-  a.bf16 = type == FO_TYPE_BF16;
-  const int es = a.bf16 ? 2 : 4;
-  a.vec = ((reinterpret_cast<uintptr_t>(D) | uintptr_t(row_stride) * es) & 15) == 0;
+  const bool bf16 = type == FO_TYPE_BF16;
+  const int es = bf16 ? 2 : 4;
+  a.vec = ((reinterpret_cast<uintptr_t>(D) | uintptr_t(row_stride) * es) & 15) == 0 &&
+          row_stride * es < (int64_t(1) << 40);
+  // A copy leaves out whole 16-byte pieces past N, not single elements: the
+  // last columns are copied only if N ends on such a piece.
+  a.n_copied = (N * es) % 16 == 0 ? int32_t(mx_up(N, 64)) : int32_t(N);
+  if (a.vec && !encode_tensor_map(&a.map_d,
+                                  bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                  D, N, M, uint64_t(row_stride) * es, 128 / es, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_128B))
+    return FO_ERR_CUDA;
   a.status = dev_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // no more workers than tiles (with experts: than any ranges can make)
   const int64_t most = (mb + groups) * ((N + a.bn - 1) / a.bn);
   const int64_t workers = pair ? sms / 2 : sms;
   const int64_t use = most < workers ? most : workers;
-  return pair ? launch<true>(a, int(2 * use), st) : launch<false>(a, int(use), st);
+  if (pair) return bf16 ? launch<true, true>(a, int(2 * use), st) : launch<true, false>(a, int(2 * use), st);
+  return bf16 ? launch<false, true>(a, int(use), st) : launch<false, false>(a, int(use), st);
 }
 
 }  // namespace fo

@@ -20,11 +20,15 @@ constexpr uint64_t kDrainNs = 10000000ull;    // 10 ms while winding down
 // role aborted (shared flag) or after kWaitNs; then records the error.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                        int32_t* status) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
+  // the clock is read only now and then: reading it costs more than most waits
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (i % 64) continue;
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitNs) {
       *abort_flag = 1;
       atomicCAS(status, 0, int32_t(FO_ERR_TIMEOUT));
       return false;
@@ -106,6 +110,13 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
                : "memory");
 }
 
+// No release ordering: for threads whose work before it is tensor memory
+// stores they have waited for (tcgen05.wait::st).
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+
 // No release ordering: the copies are tracked by the transaction count.
 __device__ __forceinline__ void expect_tx_cluster(uint32_t addr, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
@@ -126,6 +137,17 @@ __device__ __forceinline__ void fence_before() {
 }
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
 }
 
 template <bool PAIR>
@@ -178,17 +200,21 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (uint64_t((sbo >> 4) & 0x3FFF) << 32) | (uint64_t(1) << 46) | (uint64_t(layout) << 61);
 }
 
-// 512 bytes of scales (32 rows x 16 bytes) to four columns of tensor memory,
-// repeated in the four lane quarters.
-template <bool PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
-  const uint64_t desc = smem_desc(smem, 128, 128, 0);
-  if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+// This lane's 16 bytes of a block of scales (32 lanes x 16 bytes in shared
+// memory) to four columns of its warp's lanes in tensor memory.
+__device__ __forceinline__ void store_scales(uint32_t taddr, uint32_t smem) {
+  uint32_t x[4];
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(smem)
+               : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 4-bit operands, 64 deep, scales per 32.
