@@ -14,17 +14,17 @@
 //  * warp 1: four MMAs of 64 columns per stage, from one thread.
 //  * warps 2-5: epilogue.  Sums to bf16 or fp32, transposed through shared
 //    memory so that a row's stores are whole 128-byte segments.
-//  * warps 6-9: the stage's scales from shared to tensor memory, through
-//    registers (tcgen05.st, a quarter of the lanes per warp), into two slots in
-//    turn.  tcgen05.cp does the same from the MMA's thread, but in line with
+//  * warps 6-9: the stages' scales from shared to tensor memory, through
+//    registers (tcgen05.st, a quarter of the lanes per warp), into three slots
+//    in turn.  tcgen05.cp does the same from the MMA's thread, but in line with
 //    the MMAs: the 8-expert product of 32768 x 14336 x 4096 took 1163 us with
 //    six copies per stage, against 774 us with the copies (wrongly) left out.
 // The PAIR form computes 256 x BN with one cta_group::2 MMA: each CTA holds
 // 128 rows of A, half of B's rows and all of B's scales.
 //
-// Tensor memory: two sums of BN columns and two slots of scales in 512
-// columns.  BN = 256 leaves room for 464 columns of sums, so the second sum
-// starts at column 208 and shares 48 columns with the first: the epilogue
+// Tensor memory: two sums of BN columns and three slots of scales in 512
+// columns.  BN = 256 leaves room for 440 columns of sums, so the second sum
+// starts at column 184 and shares 72 columns with the first: the epilogue
 // drains the shared columns of a tile first, and the next tile's MMAs wait for
 // those only.
 #include <cuda.h>
@@ -46,10 +46,13 @@ constexpr int kStageCols = 256;                  // columns of K per stage
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 128 * 128;               // room for this CTA's rows of B
 constexpr int kSaBytes = 1024;                   // 128 rows x 8 scales
-constexpr int kSbBytes = 3 * 1024;               // up to three blocks of rows
+constexpr int kSbBlocks = 2;                     // blocks of rows of B's scales
+constexpr int kSbBytes = kSbBlocks * 1024;
 constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
 constexpr int kStages = 5;
-constexpr int kSlots = 4;                        // slots of scales in tensor memory
+constexpr int kSlots = 3;                        // slots of scales in tensor memory
+constexpr int kSfCols = 8 + 8 * kSbBlocks;       // columns of a slot: A's, then B's
+constexpr int kSf0 = 512 - kSlots * kSfCols;
 constexpr int kStagingBytes = 4 * 2 * 32 * 128;    // two buffers per epilogue warp
 constexpr int kStartOffset = kStages * kStageBytes + kStagingBytes;
 constexpr int kBarOffset = kStartOffset + 4 * (kRouteExperts + 4);
@@ -65,8 +68,8 @@ struct GemmArgs {
   int64_t stride;
   int32_t M, N, n_pad, n_groups, grouped;
   int32_t k_stages, k_steps;   // stages of 256 columns, MMAs of 64 in all
-  int32_t bn, sb_blocks;       // tile columns, blocks of B's scales per stage
-  int32_t acc1, sf0, sf_cols;  // tensor memory: second sum, scales, columns per slot
+  int32_t bn;                  // tile columns, a multiple of 64
+  int32_t acc1;                // tensor memory column of the second sum
   int32_t vec;                 // map_d can address D's rows
   int32_t n_copied;            // a 128-byte wide copy to D may reach up to this column
   int32_t* status;
@@ -119,8 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;                                 // PAIR: the leader's
   uint64_t* sf_full = acc_empty + 2;       // a stage's scales are in this CTA's shared memory
-  uint64_t* sf_ready = sf_full + kStages;  // PAIR: the leader's; a slot's are in tensor memory
-  uint64_t* drain = sf_ready + kSlots;
+  uint64_t* drain = sf_full + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -130,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&full[s]), PAIR ? 2 : 1);
+      // a producer and four scale warps per CTA
+      mbar_init(smem_u32(&full[s]), PAIR ? 10 : 5);
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&sf_full[s]), 1);
     }
@@ -138,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       mbar_init(smem_u32(&acc_full[b]), 1);
       mbar_init(smem_u32(&acc_empty[b]), PAIR ? 8 : 4);
     }
-    for (int b = 0; b < kSlots; ++b) mbar_init(smem_u32(&sf_ready[b]), PAIR ? 8 : 4);
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       int64_t issued = 0;
       const uint64_t keep = tc::policy_evict_last();
       const uint32_t bytes = uint32_t(kABytes + b_rows * 128);
-      const uint32_t sf_bytes = uint32_t(kSaBytes + a.sb_blocks * 1024);
+      const uint32_t sf_bytes = uint32_t(kSaBytes + kSbBytes);
       for (int t = worker; ok && t < tiles; t += workers) {
         const Tile w = tile_at<PAIR>(a, start, t, g);
         const int a_row = w.row0 + int(rank) * 128;
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       const uint64_t desc0 = tc::smem_desc(smem_u32(smem), 16, 1024, 2);
       const bool leader = tc::elect_one();
       int stage = 0, g = 0, i = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int t = worker; ok && t < tiles; t += workers, ++i) {
         const Tile w = tile_at<PAIR>(a, start, t, g);
@@ -265,18 +267,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           break;
         const uint32_t d = tmem + uint32_t(acc ? a.acc1 : 0);
         const uint32_t b_shift = uint32_t(w.b_row % 128) / 32;   // columns of scales before b_row
-        const uint32_t sf_b = 8 + b_shift, sf_half = uint32_t(a.sb_blocks) * 4;
+        const uint32_t sf_b = 8 + b_shift, sf_half = uint32_t(kSbBlocks) * 4;
         int steps = a.k_steps;
         for (int kb = 0; kb < a.k_stages; ++kb, steps -= 4) {
-          if (!tc::wait_warp(smem_u32(&sf_ready[slot]), slot_phase, abort_flag, a.status) ||
-              !tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status)) {
+          if (!tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status)) {
             ok = false;
             break;
           }
           tc::fence_after();
           const uint64_t da = desc0 + uint64_t(stage * (kStageBytes >> 4));
           const uint64_t db = da + (kABytes >> 4);
-          const uint32_t sfa = tmem + uint32_t(a.sf0 + slot * a.sf_cols), sfb = sfa + sf_b;
+          const uint32_t sfa = tmem + uint32_t(kSf0 + slot * kSfCols), sfb = sfa + sf_b;
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -290,10 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
             tc::commit<PAIR>(smem_u32(&empty[stage]));
           }
           __syncwarp();
-          if (++slot == kSlots) {
-            slot = 0;
-            slot_phase ^= 1;
-          }
+          if (++slot == kSlots) slot = 0;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -307,41 +305,52 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   } else if (warp >= 6) {
     // ------------------------------------------------------------ scales
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
-    int stage = 0;
-    uint32_t phase = 0, it = 0;
+    const uint32_t base = smem_u32(smem) + kABytes + kBBytes + lane * 16;
+    uint32_t it = 0, stage = 0, phase = 0;   // stages so far, and its place in the ring
+    uint32_t slot = 0, free_stage = 0, free_phase = 0;
     bool ok = a.k_stages > 0;
     for (int t = worker; ok && t < tiles; t += workers) {
       for (int kb = 0; kb < a.k_stages; ++kb, ++it) {
         ok = tc::wait_warp(smem_u32(&sf_full[stage]), phase, abort_flag, a.status);
-        // the slot's MMAs of kSlots stages ago have completed: they were the
-        // last to read that stage's shared memory, too
+        // a block of scales is 32 lanes x 16 bytes: a lane's four columns
+        const uint32_t from = base + stage * kStageBytes;
+        uint32_t x[2][1 + kSbBlocks][4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tc::lds128(from + c * 512, x[c][0]);
+#pragma unroll
+          for (int r = 0; r < kSbBlocks; ++r)
+            tc::lds128(from + kSaBytes + r * 1024 + c * 512, x[c][1 + r]);
+        }
+        // the slot's MMAs of kSlots stages ago have completed
         if (ok && it >= kSlots) {
-          const uint32_t j = it - kSlots;
-          ok = tc::wait_warp(smem_u32(&empty[j % kStages]), (j / kStages) & 1, abort_flag,
-                             a.status);
+          ok = tc::wait_warp(smem_u32(&empty[free_stage]), free_phase, abort_flag, a.status);
+          if (++free_stage == kStages) {
+            free_stage = 0;
+            free_phase ^= 1;
+          }
         }
         if (!ok) break;
         tc::fence_after();
-        // a block of scales is 32 lanes x 16 bytes: a lane's four columns
-        const uint32_t from = smem_u32(smem + stage * kStageBytes) + kABytes + kBBytes + lane * 16;
-        const uint32_t to = tmem + quarter + uint32_t(a.sf0) + (it % kSlots) * uint32_t(a.sf_cols);
+        const uint32_t to = tmem + quarter + uint32_t(kSf0) + slot * uint32_t(kSfCols);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          tc::store_scales(to + c * 4, from + c * 512);
-          for (int r = 0; r < a.sb_blocks; ++r)
-            tc::store_scales(to + 8 + uint32_t(c * a.sb_blocks + r) * 4,
-                             from + kSaBytes + r * 1024 + c * 512);
+          tc::tmem_st4(to + c * 4, x[c][0]);
+#pragma unroll
+          for (int r = 0; r < kSbBlocks; ++r)
+            tc::tmem_st4(to + 8 + uint32_t(c * kSbBlocks + r) * 4, x[c][1 + r]);
         }
         tc::tmem_wait_st();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) {
-          const uint32_t bar = smem_u32(&sf_ready[it % kSlots]);
+          const uint32_t bar = smem_u32(&full[stage]);
           if (PAIR && rank != 0)
             tc::arrive_cluster_relaxed(tc::map_to_rank(bar, 0));
           else
             mbar_arrive(bar);
         }
+        if (++slot == kSlots) slot = 0;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -536,10 +545,7 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
   const bool pair = M > 128;
   GemmArgs a{};
   a.bn = pair ? 256 : 128;
-  a.sb_blocks = 2;
-  a.sf_cols = 8 + 8 * a.sb_blocks;
-  a.sf0 = 512 - kSlots * a.sf_cols;
-  a.acc1 = a.sf0 - a.bn < a.bn ? a.sf0 - a.bn : a.bn;
+  a.acc1 = kSf0 - a.bn < a.bn ? kSf0 - a.bn : a.bn;
   if (K > 0) {
     const uint64_t pitch = uint64_t(kb) * 64;
     const uint32_t b_rows = uint32_t(pair ? a.bn / 2 : a.bn);
@@ -550,7 +556,7 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
         !encode_tensor_map(&a.map_sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kb * 128, mb,
                            kb * 512, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !encode_tensor_map(&a.map_sb, CU_TENSOR_MAP_DATA_TYPE_UINT32, b_scales, kb * 128, nb,
-                           kb * 512, 256, a.sb_blocks, CU_TENSOR_MAP_SWIZZLE_NONE))
+                           kb * 512, 256, kSbBlocks, CU_TENSOR_MAP_SWIZZLE_NONE))
       return FO_ERR_CUDA;
   }
   a.first = group_first;

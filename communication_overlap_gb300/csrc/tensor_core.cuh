@@ -41,11 +41,13 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
 }
 
-// One lane waits, the answer is the warp's (tcgen05.ld is .aligned).
+// The same for a converged warp, whose lanes get one answer (tcgen05.ld and
+// the like are .aligned).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
                                           volatile int* abort_flag, int32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, abort_flag, status);
+  if ((threadIdx.x & 31) == 0) ok = wait_slow(bar, parity, abort_flag, status);
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -200,14 +202,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (uint64_t((sbo >> 4) & 0x3FFF) << 32) | (uint64_t(1) << 46) | (uint64_t(layout) << 61);
 }
 
-// This lane's 16 bytes of a block of scales (32 lanes x 16 bytes in shared
-// memory) to four columns of its warp's lanes in tensor memory.
-__device__ __forceinline__ void store_scales(uint32_t taddr, uint32_t smem) {
-  uint32_t x[4];
+__device__ __forceinline__ void lds128(uint32_t smem, uint32_t (&x)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                : "r"(smem)
                : "memory");
+}
+
+// Four columns of this warp's lanes in tensor memory.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&x)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
                "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                : "memory");
