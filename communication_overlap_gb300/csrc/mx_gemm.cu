@@ -8,25 +8,26 @@
 // whole way from HBM.
 //
 // One persistent kernel, one CTA (or CTA pair) per SM (or pair of SMs):
-//  * warp 0: TMA producer.  A stage is 256 columns: 128 rows of A and this
-//    CTA's rows of B, 128 bytes each (one 128-byte swizzle atom), and the
-//    scales of both, in the blocks of 512 bytes that the form keeps them in.
+//  * warps 0 and 10: TMA producers.  A stage is 256 columns: 128 rows of A and
+//    this CTA's rows of B, 128 bytes each (one 128-byte swizzle atom), from warp
+//    0, and the scales of both, in the blocks of 512 bytes that the form keeps
+//    them in, from warp 10.  (One thread for all four copies needs 600 cycles
+//    per stage, as long as the MMAs.)
 //  * warp 1: four MMAs of 64 columns per stage, from one thread.
 //  * warps 2-5: epilogue.  Sums to bf16 or fp32, transposed through shared
 //    memory so that a row's stores are whole 128-byte segments.
 //  * warps 6-9: the stages' scales from shared to tensor memory, through
-//    registers (tcgen05.st, a quarter of the lanes per warp), into three slots
-//    in turn.  tcgen05.cp does the same from the MMA's thread, but in line with
+//    registers (tcgen05.st, a quarter of the lanes per warp), a slot per stage.  tcgen05.cp does the same from the MMA's thread, but in line with
 //    the MMAs: the 8-expert product of 32768 x 14336 x 4096 took 1163 us with
 //    six copies per stage, against 774 us with the copies (wrongly) left out.
 // The PAIR form computes 256 x BN with one cta_group::2 MMA: each CTA holds
 // 128 rows of A, half of B's rows and all of B's scales.
 //
-// Tensor memory: two sums of BN columns and three slots of scales in 512
-// columns.  BN = 256 leaves room for 440 columns of sums, so the second sum
-// starts at column 184 and shares 72 columns with the first: the epilogue
-// drains the shared columns of a tile first, and the next tile's MMAs wait for
-// those only.
+// Tensor memory: two sums of BN columns and five slots of scales in 512
+// columns.  BN = 256 leaves room for 392 columns of sums, so the second sum
+// starts at column 136 and shares 120 columns with the first: the epilogue
+// drains a tile's 128 columns on that side first, and the next tile's MMAs wait
+// for those only.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -41,7 +42,7 @@ namespace fo {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kStageCols = 256;                  // columns of K per stage
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 128 * 128;               // room for this CTA's rows of B
@@ -50,9 +51,8 @@ constexpr int kSbBlocks = 2;                     // blocks of rows of B's scales
 constexpr int kSbBytes = kSbBlocks * 1024;
 constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
 constexpr int kStages = 5;
-constexpr int kSlots = 3;                        // slots of scales in tensor memory
 constexpr int kSfCols = 8 + 8 * kSbBlocks;       // columns of a slot: A's, then B's
-constexpr int kSf0 = 512 - kSlots * kSfCols;
+constexpr int kSf0 = 512 - kStages * kSfCols;     // one slot per stage
 constexpr int kStagingBytes = 4 * 2 * 32 * 128;    // two buffers per epilogue warp
 constexpr int kStartOffset = kStages * kStageBytes + kStagingBytes;
 constexpr int kBarOffset = kStartOffset + 4 * (kRouteExperts + 4);
@@ -190,59 +190,60 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   const int b_rows = a.bn / (PAIR ? 2 : 1);    // rows of B this CTA stages
   const bool shared_cols = a.acc1 < a.bn;      // the two sums overlap
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0 && a.k_stages > 0) {
-      int stage = 0, g = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      int64_t issued = 0;
-      const uint64_t keep = tc::policy_evict_last();
-      const uint32_t bytes = uint32_t(kABytes + b_rows * 128);
-      const uint32_t sf_bytes = uint32_t(kSaBytes + kSbBytes);
-      for (int t = worker; ok && t < tiles; t += workers) {
-        const Tile w = tile_at<PAIR>(a, start, t, g);
-        const int a_row = w.row0 + int(rank) * 128;
-        for (int kb = 0; kb < a.k_stages; ++kb) {
-          if (!tc::wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-          const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSaBytes;
-          const uint32_t sfb = smem_u32(&sf_full[stage]);
-          mbar_expect_tx(sfb, sf_bytes);
-          tc::load_2d(ssa, &a.map_sa, sfb, kb * 256, a_row / 128, keep);
-          tc::load_2d(ssb, &a.map_sb, sfb, kb * 256, w.b_row / 128, keep);
-          if constexpr (PAIR) {
-            const uint32_t fb = tc::map_to_rank(smem_u32(&full[stage]), 0);
+  if (warp == 0 || warp == 10) {
+    // ------------------------------------------------------------ producers
+    // warp 0 the codes, warp 10 the scales; as everywhere here the whole warp
+    // walks the loop and one elected thread issues
+    const bool codes = warp == 0;
+    const bool leader = tc::elect_one();
+    const uint64_t keep = tc::policy_evict_last();
+    const uint32_t bytes = codes ? uint32_t(kABytes + b_rows * 128) : uint32_t(kSaBytes + kSbBytes);
+    int stage = 0, g = 0;
+    uint32_t phase = 0, filled = 0;    // filled: bit s, stage s was filled at least once
+    bool ok = a.k_stages > 0;
+    for (int t = worker; ok && t < tiles; t += workers) {
+      const Tile w = tile_at<PAIR>(a, start, t, g);
+      const int a_row = w.row0 + int(rank) * 128, b_row = w.b_row + int(rank) * b_rows;
+      for (int kb = 0; kb < a.k_stages; ++kb) {
+        ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
+        if (!ok) break;
+        const uint32_t sa = smem_u32(smem) + uint32_t(stage * kStageBytes);
+        if (leader) {
+          if (!codes) {
+            const uint32_t bar = smem_u32(&sf_full[stage]);
+            mbar_expect_tx(bar, bytes);
+            tc::load_2d(sa + kABytes + kBBytes, &a.map_sa, bar, kb * 256, a_row / 128, keep);
+            tc::load_2d(sa + kABytes + kBBytes + kSaBytes, &a.map_sb, bar, kb * 256, w.b_row / 128,
+                        keep);
+          } else if constexpr (PAIR) {
+            const uint32_t bar = tc::map_to_rank(smem_u32(&full[stage]), 0);
             if (rank == 0)
               mbar_expect_tx(smem_u32(&full[stage]), bytes);
             else
-              tc::expect_tx_cluster(fb, bytes);
-            tc::load_2d_pair(sa, &a.map_a, fb, kb * 128, a_row, keep);
-            tc::load_2d_pair(sb, &a.map_b, fb, kb * 128, w.b_row + int(rank) * b_rows, keep);
+              tc::expect_tx_cluster(bar, bytes);
+            tc::load_2d_pair(sa, &a.map_a, bar, kb * 128, a_row, keep);
+            tc::load_2d_pair(sa + kABytes, &a.map_b, bar, kb * 128, b_row, keep);
           } else {
-            const uint32_t fb = smem_u32(&full[stage]);
-            mbar_expect_tx(fb, bytes);
-            tc::load_2d(sa, &a.map_a, fb, kb * 128, a_row, keep);
-            tc::load_2d(sb, &a.map_b, fb, kb * 128, w.b_row, keep);
+            const uint32_t bar = smem_u32(&full[stage]);
+            mbar_expect_tx(bar, bytes);
+            tc::load_2d(sa, &a.map_a, bar, kb * 128, a_row, keep);
+            tc::load_2d(sa + kABytes, &a.map_b, bar, kb * 128, b_row, keep);
           }
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        filled |= 1u << stage;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (!ok) {
-        // winding down: copies already issued land before the CTA exits
-        for (int s = 0; s < kStages; ++s) {
-          const int64_t fills = issued / kStages + (s < issued % kStages ? 1 : 0);
-          if (fills == 0) continue;
-          tc::wait_drain(smem_u32(&sf_full[s]), uint32_t((fills - 1) & 1));
-          if (rank == 0) tc::wait_drain(smem_u32(&full[s]), uint32_t((fills - 1) & 1));
-        }
+    }
+    if (!ok && a.k_stages > 0 && leader && (!codes || rank == 0)) {
+      // winding down: copies already issued land before the CTA exits
+      for (int s = 0; s < kStages; ++s) {
+        // the parity of stage s's last fill: this round's, or the one before
+        const uint32_t parity = s < stage ? phase : phase ^ 1;
+        if ((filled >> s) & 1u) tc::wait_drain(smem_u32(codes ? &full[s] : &sf_full[s]), parity);
       }
     }
   } else if (warp == 1) {
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       const uint32_t idesc = instruction(kM, a.bn);
       const uint64_t desc0 = tc::smem_desc(smem_u32(smem), 16, 1024, 2);
       const bool leader = tc::elect_one();
-      int stage = 0, g = 0, i = 0, slot = 0;
+      int stage = 0, g = 0, i = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int t = worker; ok && t < tiles; t += workers, ++i) {
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           tc::fence_after();
           const uint64_t da = desc0 + uint64_t(stage * (kStageBytes >> 4));
           const uint64_t db = da + (kABytes >> 4);
-          const uint32_t sfa = tmem + uint32_t(kSf0 + slot * kSfCols), sfb = sfa + sf_b;
+          const uint32_t sfa = tmem + uint32_t(kSf0 + stage * kSfCols), sfb = sfa + sf_b;
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -291,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
             tc::commit<PAIR>(smem_u32(&empty[stage]));
           }
           __syncwarp();
-          if (++slot == kSlots) slot = 0;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -302,16 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         __syncwarp();
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 6 && warp < 10) {
     // ------------------------------------------------------------ scales
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const uint32_t base = smem_u32(smem) + kABytes + kBBytes + lane * 16;
-    uint32_t it = 0, stage = 0, phase = 0;   // stages so far, and its place in the ring
-    uint32_t slot = 0, free_stage = 0, free_phase = 0;
+    uint32_t stage = 0, phase = 0;
     bool ok = a.k_stages > 0;
     for (int t = worker; ok && t < tiles; t += workers) {
-      for (int kb = 0; kb < a.k_stages; ++kb, ++it) {
+      for (int kb = 0; kb < a.k_stages; ++kb) {
+        // (the stage was refilled after its last MMAs, which were also the last
+        // to read its slot in tensor memory)
         ok = tc::wait_warp(smem_u32(&sf_full[stage]), phase, abort_flag, a.status);
+        if (!ok) break;
         // a block of scales is 32 lanes x 16 bytes: a lane's four columns
         const uint32_t from = base + stage * kStageBytes;
         uint32_t x[2][1 + kSbBlocks][4];
@@ -322,17 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           for (int r = 0; r < kSbBlocks; ++r)
             tc::lds128(from + kSaBytes + r * 1024 + c * 512, x[c][1 + r]);
         }
-        // the slot's MMAs of kSlots stages ago have completed
-        if (ok && it >= kSlots) {
-          ok = tc::wait_warp(smem_u32(&empty[free_stage]), free_phase, abort_flag, a.status);
-          if (++free_stage == kStages) {
-            free_stage = 0;
-            free_phase ^= 1;
-          }
-        }
-        if (!ok) break;
         tc::fence_after();
-        const uint32_t to = tmem + quarter + uint32_t(kSf0) + slot * uint32_t(kSfCols);
+        const uint32_t to = tmem + quarter + uint32_t(kSf0) + stage * uint32_t(kSfCols);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           tc::tmem_st4(to + c * 4, x[c][0]);
@@ -350,14 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
           else
             mbar_arrive(bar);
         }
-        if (++slot == kSlots) slot = 0;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-  } else {
+  } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // this warp's quarter of the tensor memory lanes
     const uint32_t staging = smem_u32(smem + kStages * kStageBytes + (warp - 2) * (2 * 32 * 128));
