@@ -1,159 +1,1027 @@
-// A whole expert layer for a few tokens:
-//   y[t] = sum_s w_s W2[e_s] (act(G x_t) * (U x_t)),  ids, w = top-k softmax
-// of x . router^T.
+// A whole expert layer for a few tokens, in one kernel:
+//   ids, w = top-k softmax of x . router^T,
+//   h = act(G_e x) * (U_e x),  y[t] = sum_s w_s D_e h.
 //
-// The plain first form, one warp per value: the router with a CTA per token,
-// the hidden values with a warp per (token, slot, hidden row), the outputs
-// with a warp per (token, output row).
+// A generation step reads every weight of every expert that a token reaches
+// and does almost nothing with it: HBM bounds it, and what must not happen is
+// that the reads pause.  So:
+//  * One persistent CTA per SM (a cooperative launch).  Four warps copy
+//    weights through a deep ring of stages (128 rows x 128 columns), eight warps
+//    consume them with mma.sync, a few tokens being the narrow side (16 weight
+//    rows x 8 tokens x 16 columns).  At one SM's share of HBM a bf16 stage of 32
+//    KB takes about 1400 cycles to arrive and its products take under 200 per
+//    8 tokens, so the rate of the tensor cores does not matter here.
+//  * Work is cut evenly, whatever the routing: the hidden rows of all reached
+//    experts are one line of granules and CTA c takes the c-th part of it; the
+//    output product is one line of (128 output rows, expert, 128 columns)
+//    stages, cut the same way.
+//  * A warp's 16 rows are 8 gate rows and their 8 up rows, which puts both
+//    values of a hidden row in one thread: the activation happens in registers
+//    and only the hidden values (a few rows) travel through memory, inside L2.
+//  * Between the two products stands a grid barrier.  The ring fills with the
+//    second product's weights before it; only the loads of h wait.
+//  * Output rows shared by several CTAs are joined by the last of them to
+//    finish, which adds the parts in CTA order: the same bits in every run.
+//
+// bf16 weights: bf16 products, h rounded to bf16 (x has no more).  4-bit
+// weights: codes become f16 in registers (exact), x and h are f16 with a
+// power-of-two scale per 32 values (11 significant bits), a block's sum of 32
+// products starts at zero and is added times both scales in fp32.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "moe_common.cuh"
 #include "mx_common.cuh"
+#include "pipeline.cuh"
 
 namespace fo {
 
 namespace {
 
+constexpr int kMaxCtas = 160;
+constexpr int kMaxRowBlocks = 4096;     // blocks of 128 output rows
+constexpr int kMaxStages = 16;
+constexpr int kStageK = 128;            // columns of the weights per stage
+constexpr int kSmemLimit = 232448;
+constexpr int kCopyWarps = 4, kMathWarps = 8;
+constexpr int kCopyThreads = kCopyWarps * 32, kMathThreads = kMathWarps * 32;
+constexpr int kWarps = kCopyWarps + kMathWarps;
+constexpr int kYPitch = 132;            // floats per token of the outputs' sums
+constexpr int kMxTokenPitch = 320;      // bytes per token of a 4-bit stage: 256 and a bank shift
+
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
+// Work split evenly: first item of part c of n items over g parts.
+__device__ __forceinline__ int64_t part(int64_t n, int c, int g) { return n * c / g; }
+
 struct FewArgs {
-  fo_moe_few_desc d;
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* router;
-  const void *w1, *w2;
-  const uint8_t *s1, *s2;
+  const uint8_t *w1, *w2;  // weights: bf16 or codes
+  const uint8_t *s1, *s2;  // 4-bit: scales
   uint16_t* y;
   int64_t y_stride;
-  int32_t* ids;
-  float* weights;
-  float* h;
+  int32_t T, H, I, E, K, renormalize, act;
+  int32_t w1_rows, w2_rows;   // rows of an expert's matrices as stored
+  int32_t n_x;                // tokens of a stage of the first product (a multiple of 8)
+  int32_t stages, stage_bytes;
+  int32_t off_lists, off_y, off_bar;      // shared memory offsets
+  uint32_t* barrier;          // [0], [1] counts, [2] leave
+  int32_t* done;              // [row blocks] parts finished
+  float* logits;              // [T][E]
+  uint16_t* h;                // [rows][I] bf16, or [rows][Ip] f16
+  uint16_t* xq;               // 4-bit: [T][Hp] f16
+  uint8_t *xs, *hs;           // and scales, a byte per 32: [T][Hp / 32], [rows][Ip / 32]
+  int32_t hp, ip;             // 4-bit: padded columns
+  float* parts;               // [kMaxCtas + row blocks][T][128]
+  int32_t* status;
 };
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
-  return __uint_as_float(uint32_t(p[i]) << 16);
+// The routing as every CTA keeps it in shared memory.
+struct Lists {
+  uint64_t* mask;     // [E] tokens of the a-th active expert
+  float* weight;      // [P] weight of row r (rows sorted by expert, token, slot)
+  float* pair_weight; // [P]
+  int16_t* token;     // [P] token of row r
+  int16_t* id;        // [P] expert of pair (token, slot)
+  int16_t* active;    // [E] experts that have rows
+  int16_t* first;     // [E + 1] first row of the a-th active expert
+};
+
+__device__ __forceinline__ Lists lists_at(uint8_t* p, int P, int E) {
+  Lists l;
+  l.mask = reinterpret_cast<uint64_t*>(p);
+  l.weight = reinterpret_cast<float*>(l.mask + E);
+  l.pair_weight = l.weight + P;
+  l.token = reinterpret_cast<int16_t*>(l.pair_weight + P);
+  l.id = l.token + P;
+  l.active = l.id + P;
+  l.first = l.active + E;
+  return l;
 }
 
-// Element (row, k) of a 4-bit matrix whose first row is row 0 of `codes`.
-__device__ float mx_at(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t k,
-                       int64_t k_blocks) {
-  const uint32_t byte = codes[row * k_blocks * 64 + k / 2];
-  uint32_t h[4];
-  mx_decode8((k & 1) ? byte >> 4 : byte & 15, h);
-  const float v = __half2float(__low2half(*reinterpret_cast<const __half2*>(&h[0])));
-  return v * mx_scale_value(scales[((row / 128) * k_blocks + k / 128) * 512 +
-                                   mx_scale_row(int(row % 128)) + (k % 128) / 32]);
+__host__ inline int lists_bytes(int P, int E) { return (12 * P + 12 * E + 2 + 127) / 128 * 128; }
+
+__device__ __forceinline__ float activate(float g, int act) {
+  if (act == FO_ACT_NONE) return g;
+  if (act == FO_ACT_RELU) return g > 0.0f ? g : 0.0f;
+  return g / (1.0f + __expf(-g));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// ------------------------------------------------------------------ router
+
+// Logits of a block of 4 experts x 8 tokens by one CTA: its warps share out
+// the columns, 256 at a time, and their sums meet in shared memory.
+__device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float acc[4][8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[e][t] = 0.0f;
+  for (int k = (warp * 32 + lane) * 8; k < a.H; k += kWarps * 256) {
+    uint4 r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      r[e] = e0 + e < a.E
+                 ? __ldg(reinterpret_cast<const uint4*>(a.router + int64_t(e0 + e) * a.H + k))
+                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (t0 + t >= a.T) break;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + t) * a.x_stride + k));
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t rw[4] = {r[e].x, r[e].y, r[e].z, r[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[e][t] = fmaf(bf16lo(xw[i]), bf16lo(rw[i]), acc[e][t]);
+          acc[e][t] = fmaf(bf16hi(xw[i]), bf16hi(rw[i]), acc[e][t]);
+        }
+      }
+    }
+  }
+  __syncthreads();   // red is free
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      float v = acc[e][t];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) red[(e * 8 + t) * kWarps + warp] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int e = e0 + threadIdx.x / 8, t = t0 + threadIdx.x % 8;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += red[threadIdx.x * kWarps + w];
+    if (e < a.E && t < a.T) __stcg(a.logits + int64_t(t) * a.E + e, v);
+  }
+}
+
+// ------------------------------------------------------------------ f16 with scales
+
+// The scale byte of 32 values kept as f16: with s = the exponent of the
+// largest magnitude - 14 they stay below 2^15.
+__device__ __forceinline__ uint32_t half_scale(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  if (e == 255u) return 255u;
+  return e > 15u ? e - 14u : 1u;
+}
+
+__device__ __forceinline__ uint16_t half_value(float v, uint32_t s) {
+  if (s == 255u) return 0;   // the block's scale is NaN
+  return __half_as_ushort(__float2half_rn(v * __uint_as_float((254u - s) << 23)));
+}
+
+// x as f16 with scales, a warp per 32 columns of a token (columns past H:
+// zeros), and zero scales past the last block of each row of h.
+__device__ void scale_x(const FewArgs& a) {
+  const int lane = threadIdx.x % 32, blocks = a.hp / 32;
+  const int64_t first = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
+  for (int64_t j = first; j < int64_t(a.T) * blocks; j += int64_t(gridDim.x) * kWarps) {
+    const int t = int(j / blocks), c = int(j % blocks) * 32 + lane;
+    const float v =
+        c < a.H ? __uint_as_float(uint32_t(__ldg(a.x + t * a.x_stride + c)) << 16) : 0.0f;
+    const uint32_t s =
+        half_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
+    a.xq[int64_t(t) * a.hp + c] = half_value(v, s);
+    if (lane == 0) a.xs[int64_t(t) * blocks + c / 32] = uint8_t(s);
+  }
+  const int used = (a.I + 31) / 32;
+  for (int64_t r = first * 32 + lane; r < int64_t(a.T) * a.K; r += int64_t(gridDim.x) * kWarps * 32)
+    for (int b = used; b < a.ip / 32; ++b) a.hs[r * (a.ip / 32) + b] = 0;
+}
+
+// ------------------------------------------------------------------ work items
+
+// A tile of the first product: hidden rows [i0, i0 + n) of the a-th active
+// expert.
+struct HiddenTile {
+  int32_t a, i0, n;
+};
+
+__device__ __forceinline__ bool hidden_tile(int64_t& at, int64_t end, int per_expert, int granule,
+                                            int I, HiddenTile& t) {
+  if (at >= end) return false;
+  t.a = int(at / per_expert);
+  const int g = int(at % per_expert);
+  const int n = int(min(min(end - at, int64_t(per_expert - g)), int64_t(64 / granule)));
+  t.i0 = g * granule;
+  t.n = min(n * granule, I - t.i0);
+  at += n;
+  return true;
+}
+
+// A run of the second product: output rows of block rb, the a-th active
+// expert, stages [k0, k0 + n) of its columns.
+struct OutputRun {
+  int32_t rb, a, k0, n;
+};
+
+__device__ __forceinline__ bool output_run(int64_t& at, int64_t end, int active, int k_stages,
+                                           OutputRun& r) {
+  if (at >= end) return false;
+  const int64_t unit = at / k_stages;
+  r.k0 = int(at % k_stages);
+  r.rb = int(unit / active);
+  r.a = int(unit % active);
+  r.n = int(min(end - at, int64_t(k_stages - r.k0)));
+  at += r.n;
+  return true;
+}
+
+// ------------------------------------------------------------------ instructions
+
+// 16 bytes (or 4) from global to shared memory, zeros where !valid (src is
+// then not read but must be an address).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(valid ? 16u : 0u), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 4u : 0u)
+               : "memory");
+}
+
+// Arrive on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 
-template <int V>
-__global__ void few_router_kernel(const FewArgs a) {
-  __shared__ float logits[kRouteExperts];
-  const int t = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int H = a.d.hidden, E = a.d.experts;
-  for (int e = warp; e < E; e += blockDim.x / 32) {
-    float s = 0;
-    for (int k = lane; k < H; k += 32)
-      s += bf16_at(a.x, t * a.x_stride + k) * bf16_at(a.router, int64_t(e) * H + k);
-    s = warp_sum(s);
-    if (lane == 0) logits[e] = s;
+// d += a . b for 16 rows, 8 columns, 16 deep; bf16 or f16 operands.
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (HALF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Place of 16-byte piece `p` (of a bf16 stage's 16 per row) of row `r` in a
+// tile of `rows` rows: two halves of 128 bytes per row, pieces rotated by row
+// so that eight rows' same pieces lie in different banks.
+__device__ __forceinline__ uint32_t tile_place(int r, int p, int rows) {
+  return uint32_t((p >> 3) * rows * 128 + r * 128 + (((p & 7) ^ (r & 7)) << 4));
+}
+
+// The same for 4-bit codes: 64 bytes per row, four pieces of 32 codes.
+__device__ __forceinline__ uint32_t code_place(int r, int p) {
+  return uint32_t(r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void math_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kMathThreads) : "memory");
+}
+
+// The same, and whether all say yes: the computing warps give up together, so
+// that none is left at a barrier.
+__device__ __forceinline__ bool math_all(bool yes) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(uint32_t(yes)), "n"(kMathThreads)
+      : "memory");
+  return out != 0;
+}
+
+// One warp waits (bounded) until the grid's count reaches every CTA.
+__device__ __forceinline__ bool wait_grid(const uint32_t* count, uint32_t target,
+                                          volatile int* abort_flag, int32_t* status) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; ld_acquire_gpu(count) < target; ++i) {
+      if (i % 64) continue;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag || now - t0 > kGridWaitNs) {
+        *abort_flag = 1;
+        atomicCAS(status, 0, int32_t(FO_ERR_TIMEOUT));
+        ok = 0;
+        break;
+      }
+    }
   }
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
+// ------------------------------------------------------------------ a stage's products
+
+// bf16: this warp's 16 rows of the stage times nt tiles of 8 tokens.
+template <int NT>
+__device__ __forceinline__ void stage_bf16(uint32_t stage, int warp_row, int nt, float (&acc)[NT][4]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t tokens = stage + 32768;
+  const int nb = nt * 8;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    uint32_t w[4];
+    ldsm4(stage + tile_place(warp_row + (lane & 15), ks * 2 + (lane >> 4), 128), w);
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      if (j >= nt) break;
+      const int piece = ks * 2 + ((lane >> 3) & 1);
+      if (j + 1 < NT && j + 1 < nt) {
+        uint32_t t[4];
+        ldsm4(tokens + tile_place(j * 8 + (lane >> 4) * 8 + (lane & 7), piece, nb), t);
+        mma16816<false>(acc[j], w[0], w[1], w[2], w[3], t[0], t[1]);
+        if constexpr (NT > 1)
+          mma16816<false>(acc[j + 1 < NT ? j + 1 : 0], w[0], w[1], w[2], w[3], t[2], t[3]);
+      } else {
+        uint32_t t0, t1;
+        ldsm2(tokens + tile_place(j * 8 + (lane & 7), piece, nb), t0, t1);
+        mma16816<false>(acc[j], w[0], w[1], w[2], w[3], t0, t1);
+      }
+    }
+  }
+}
+
+// 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
+// codes of a row (one word) and the same 8 columns of a token (16 bytes); which
+// of the MMA's 16 columns they stand in does not matter as long as both agree.
+template <int NT>
+__device__ __forceinline__ void stage_mx(uint32_t stage, int warp_row, int nt, float (&acc)[NT][4]) {
+  const int lane = threadIdx.x & 31;
+  const int r = warp_row + (lane >> 2), c = lane & 3;
+  const uint32_t scales = stage + 8192, tokens = scales + 512;
+  const uint32_t token_scales = tokens + uint32_t(nt * 8) * kMxTokenPitch;
+  const uint32_t sw0 = lds32(scales + r * 4), sw1 = lds32(scales + (r + 8) * 4);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    uint32_t p[4], q[4];
+    mx_decode8(lds32(stage + code_place(r, b) + c * 4), p);
+    mx_decode8(lds32(stage + code_place(r + 8, b) + c * 4), q);
+    const float s0 = mx_scale_value((sw0 >> (8 * b)) & 255u);
+    const float s1 = mx_scale_value((sw1 >> (8 * b)) & 255u);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j >= nt) break;
+      uint32_t t[4];
+      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + b * 64 + c * 16, t);
+      const float u0 = mx_scale_value((lds32(token_scales + (j * 8 + c * 2) * 4) >> (8 * b)) & 255u);
+      const float u1 =
+          mx_scale_value((lds32(token_scales + (j * 8 + c * 2 + 1) * 4) >> (8 * b)) & 255u);
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma16816<true>(d, p[0], q[0], p[1], q[1], t[0], t[1]);
+      mma16816<true>(d, p[2], q[2], p[3], q[3], t[2], t[3]);
+      acc[j][0] = fmaf(d[0] * u0, s0, acc[j][0]);
+      acc[j][1] = fmaf(d[1] * u1, s0, acc[j][1]);
+      acc[j][2] = fmaf(d[2] * u0, s1, acc[j][2]);
+      acc[j][3] = fmaf(d[3] * u1, s1, acc[j][3]);
+    }
+  }
+}
+
+template <bool MX, int NT>
+__device__ __forceinline__ void stage_product(uint32_t stage, int warp_row, int nt,
+                                              float (&acc)[NT][4]) {
+  if constexpr (MX)
+    stage_mx<NT>(stage, warp_row, nt, acc);
+  else
+    stage_bf16<NT>(stage, warp_row, nt, acc);
+}
+
+constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
+
+// NT: tiles of 8 tokens, at most.
+template <bool MX, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int P = a.T * a.K;
+  const Lists ls = lists_at(smem + a.off_lists, P, a.E);
+  float* yacc = reinterpret_cast<float*>(smem + a.off_y);   // [T][kYPitch]; first product: maxima
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.off_bar);
+  uint64_t* empty = full + kMaxStages;
+  int* abort_word = reinterpret_cast<int*>(empty + kMaxStages);
+  volatile int* abort_flag = abort_word;
+  int* n_active_s = abort_word + 1;
+  int* flag_s = abort_word + 2;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int G = int(gridDim.x), c = int(blockIdx.x);
+  constexpr int kGranule = MX ? 32 : 8;     // hidden rows that stay together
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(smem_u32(&full[s]), kCopyThreads);
+      mbar_init(smem_u32(&empty[s]), kMathWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // ---------------------------------------------------------------- router
+  {
+    const int eb = (a.E + 3) / 4, tb = (a.T + 7) / 8;
+    for (int u = c; u < eb * tb; u += G)
+      router_block(a, u % eb * 4, u / eb * 8, reinterpret_cast<float*>(smem));
+    if constexpr (MX) scale_x(a);
+  }
+  __threadfence();
   __syncthreads();
-  if (warp) return;
-  float x[V];
-  for (int i = 0; i < V; ++i)
-    x[i] = i * 32 + lane < E ? logits[i * 32 + lane] : __int_as_float(0xff800000);
-  int id;
-  float w;
-  warp_top_k<V>(x, E, a.d.top_k, a.d.renormalize != 0, id, w);
-  if (lane < a.d.top_k) {
-    a.ids[t * a.d.top_k + lane] = id;
-    a.weights[t * a.d.top_k + lane] = w;
-  }
-}
+  if (threadIdx.x == 0) *flag_s = grid_barrier(a.barrier, uint32_t(G), a.status);
+  __syncthreads();
+  const bool live = *flag_s != 0;   // every CTA of this launch came to the barrier
+  __syncthreads();
 
-__global__ void few_hidden_kernel(const FewArgs a) {
-  const int H = a.d.hidden, I = a.d.inter, K = a.d.top_k, lane = threadIdx.x % 32;
-  const int64_t job = int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-  const int64_t p = job / I, i = job % I;
-  if (p >= int64_t(a.d.tokens) * K) return;
-  const int e = a.ids[p];
-  if (e < 0) return;
-  const int64_t kb = mx_up(H, 128) / 128, rows = mx_up(2 * int64_t(I), 128);
-  float g = 0, u = 0;
-  for (int k = lane; k < H; k += 32) {
-    const float x = bf16_at(a.x, (p / K) * a.x_stride + k);
-    if (a.d.weights == FO_TYPE_BF16) {
-      const uint16_t* w = static_cast<const uint16_t*>(a.w1) + int64_t(e) * 2 * I * H;
-      g += x * bf16_at(w, i * H + k);
-      u += x * bf16_at(w, (I + i) * H + k);
-    } else {
-      const uint8_t* w = static_cast<const uint8_t*>(a.w1);
-      g += x * mx_at(w, a.s1, e * rows + i, k, kb);
-      u += x * mx_at(w, a.s1, e * rows + I + i, k, kb);
-    }
-  }
-  g = warp_sum(g);
-  u = warp_sum(u);
-  if (lane == 0) a.h[p * I + i] = (a.d.act == FO_ACT_NONE   ? g
-                                   : a.d.act == FO_ACT_RELU ? (g > 0 ? g : 0.0f)
-                                                            : g / (1.0f + expf(-g))) * u;
-}
-
-__global__ void few_output_kernel(const FewArgs a) {
-  const int H = a.d.hidden, I = a.d.inter, K = a.d.top_k, lane = threadIdx.x % 32;
-  const int64_t job = int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-  const int64_t t = job / H, r = job % H;
-  if (t >= a.d.tokens) return;
-  const int64_t kb = mx_up(I, 128) / 128, rows = mx_up(H, 128);
-  float y = 0;
-  for (int s = 0; s < K; ++s) {
-    const int e = a.ids[t * K + s];
-    if (e < 0) continue;
-    float v = 0;
-    for (int k = lane; k < I; k += 32) {
-      const float h = a.h[(t * K + s) * I + k];
-      if (a.d.weights == FO_TYPE_BF16)
-        v += h * bf16_at(static_cast<const uint16_t*>(a.w2), (int64_t(e) * H + r) * I + k);
+  if (live) {
+    // ------------------------------------------------------------- choice
+    // every CTA makes the same choice from the same logits
+    for (int t = warp; t < a.T; t += kWarps) {
+      int id;
+      float w;
+      const float* l = a.logits + int64_t(t) * a.E;
+      auto choose = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          x[i] = i * 32 + lane < a.E ? __ldcg(l + i * 32 + lane) : __int_as_float(0xff800000);
+        warp_top_k<V>(x, a.E, a.K, a.renormalize != 0, id, w);
+      };
+      if (a.E <= 32)
+        choose(Const<1>{});
+      else if (a.E <= 128)
+        choose(Const<4>{});
       else
-        v += h * mx_at(static_cast<const uint8_t*>(a.w2), a.s2, e * rows + r, k, kb);
+        choose(Const<32>{});
+      if (lane < a.K) {
+        ls.id[t * a.K + lane] = int16_t(id);
+        ls.pair_weight[t * a.K + lane] = w;
+      }
     }
-    y += a.weights[t * K + s] * warp_sum(v);
+    // rows of each expert, in the ring's memory until the ring starts
+    int32_t* count = reinterpret_cast<int32_t*>(smem);          // [E]
+    for (int e = threadIdx.x; e < a.E; e += kWarps * 32) count[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < P; p += kWarps * 32)
+      if (ls.id[p] >= 0) atomicAdd(&count[ls.id[p]], 1);
+    __syncthreads();
+    if (warp == 0) {
+      int rows = 0, active = 0;
+      for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < a.E ? count[e] : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+        const int start = rows + sum - n;
+        if (n > 0) {
+          const int at = active + __popc(has & ((1u << lane) - 1u));
+          ls.active[at] = int16_t(e);
+          ls.first[at] = int16_t(start);
+        }
+        if (e < a.E) count[e] = start;
+        rows += __shfl_sync(0xffffffffu, sum, 31);
+        active += __popc(has);
+      }
+      if (lane == 0) {
+        ls.first[active] = int16_t(rows);
+        *n_active_s = active;
+      }
+      __syncwarp();
+      for (int p0 = 0; p0 < P; p0 += 32) {   // rows in the order of pairs
+        const int p = p0 + lane;
+        const int e = p < P ? ls.id[p] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        if (e >= 0) {
+          const int row = count[e] + rank;
+          ls.token[row] = int16_t(p / a.K);
+          ls.weight[row] = ls.pair_weight[p];
+        }
+        __syncwarp();
+        if (e >= 0 && rank == 0) count[e] += __popc(same);
+        __syncwarp();
+      }
+      for (int i = lane; i < active; i += 32) {
+        uint64_t m = 0;
+        for (int r = ls.first[i]; r < ls.first[i + 1]; ++r) m |= 1ull << ls.token[r];
+        ls.mask[i] = m;
+      }
+    }
+    __syncthreads();
+
+    const int active = *n_active_s;
+    const int per_expert = (a.I + kGranule - 1) / kGranule;
+    const int64_t n1 = int64_t(active) * per_expert;
+    const int64_t at1 = part(n1, c, G), end1 = part(n1, c + 1, G);
+    const int k1 = (a.H + kStageK - 1) / kStageK;      // stages of a tile of the first product
+    const int k2 = (a.I + kStageK - 1) / kStageK;
+    const int row_blocks = (a.H + 127) / 128;
+    const int64_t n2 = int64_t(row_blocks) * active * k2;
+    const int64_t at2 = part(n2, c, G), end2 = part(n2, c + 1, G);
+    const uint32_t ring = smem_u32(smem);
+
+    if (warp < kCopyWarps) {
+      // ------------------------------------------------------------ copies
+      const int tid = threadIdx.x;
+      const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int64_t at = at1;
+      HiddenTile t;
+      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+        // hidden row p of the tile: its gate in row (p / 8) * 16 + p % 8 of the
+        // stage, its up-projection 8 rows below
+        const int64_t gate = int64_t(ls.active[t.a]) * a.w1_rows + t.i0;
+        for (int k = 0; k < k1; ++k) {
+          ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+          if constexpr (MX) {
+            const int piece = tid & 3;
+            const int64_t pitch = a.hp / 2;
+            for (int p = tid >> 2; p < t.n; p += kCopyThreads / 4) {
+              const int row = (p >> 3) * 16 + (p & 7);
+              const uint8_t* src = a.w1 + (gate + p) * pitch + k * 64 + piece * 16;
+              copy16(dst + code_place(row, piece), src, true, once);
+              copy16(dst + code_place(row + 8, piece), src + a.I * pitch, true, once);
+            }
+            {
+              const int p = (tid >> 4) * 8 + (tid & 7);
+              const int64_t row = gate + p + ((tid >> 3) & 1) * int64_t(a.I);
+              copy4(dst + 8192 + tid * 4,
+                    p < t.n ? a.s1 + ((row >> 7) * (a.hp / 128) + k) * 512 +
+                                  mx_scale_row(int(row & 127))
+                            : a.s1,
+                    p < t.n);
+            }
+            const uint32_t tok = dst + 8192 + 512, sc = tok + a.n_x * kMxTokenPitch;
+            for (int r = tid >> 4; r < a.n_x; r += kCopyThreads / 16)
+              copy16(tok + r * kMxTokenPitch + (tid & 15) * 16,
+                     a.xq + (r < a.T ? int64_t(r) * a.hp : 0) + k * 128 + (tid & 15) * 8, r < a.T,
+                     keep);
+            if (tid < a.n_x)
+              copy4(sc + tid * 4, a.xs + (tid < a.T ? int64_t(tid) * (a.hp / 32) : 0) + k * 4,
+                    tid < a.T);
+          } else {
+            const int piece = tid & 15, col = k * kStageK + piece * 8;
+            const bool in = col < a.H;
+            const int64_t c8 = in ? col : 0;
+            const uint16_t* w = reinterpret_cast<const uint16_t*>(a.w1) + gate * a.H + c8;
+            const int64_t up = int64_t(a.I) * a.H;
+            for (int p = tid >> 4; p < t.n; p += kCopyThreads / 16) {
+              const int row = (p >> 3) * 16 + (p & 7);
+              const uint16_t* src = w + int64_t(p) * a.H;
+              copy16(dst + tile_place(row, piece, 128), src, in, once);
+              copy16(dst + tile_place(row + 8, piece, 128), src + up, in, once);
+            }
+            for (int r = tid >> 4; r < a.n_x; r += kCopyThreads / 16)
+              copy16(dst + 32768 + tile_place(r, piece, a.n_x),
+                     a.x + (r < a.T ? r * a.x_stride : 0) + c8, in && r < a.T, keep);
+          }
+          copies_arrive(smem_u32(&full[stage]));
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // The second product: the weights of the first stages are on their way
+      // before the barrier, the tokens follow after it.
+      auto weights = [&](const OutputRun& r, int k, int st) {
+        const uint32_t dst = ring + uint32_t(st * a.stage_bytes);
+        const int64_t row0 = int64_t(ls.active[r.a]) * a.w2_rows + r.rb * 128;
+        if constexpr (MX) {
+          const int piece = tid & 3;
+          const int64_t pitch = a.ip / 2;
+          for (int i = tid >> 2; i < 128; i += kCopyThreads / 4)
+            copy16(dst + code_place(i, piece), a.w2 + (row0 + i) * pitch + k * 64 + piece * 16, true,
+                   once);
+          copy4(dst + 8192 + tid * 4,
+                a.s2 + ((row0 >> 7) * (a.ip / 128) + k) * 512 + mx_scale_row(tid), true);
+        } else {
+          const int piece = tid & 15, col = k * kStageK + piece * 8;
+          const bool in = col < a.I;
+          const uint16_t* src =
+              reinterpret_cast<const uint16_t*>(a.w2) + row0 * a.I + (in ? col : 0);
+          const int rows = min(128, a.H - r.rb * 128);
+          for (int i = tid >> 4; i < rows; i += kCopyThreads / 16)
+            copy16(dst + tile_place(i, piece, 128), src + int64_t(i) * a.I, in, once);
+        }
+      };
+      auto tokens = [&](const OutputRun& r, int k, int st) {
+        const uint32_t dst = ring + uint32_t(st * a.stage_bytes);
+        const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
+        const int nb = (rows + 7) / 8 * 8, piece = tid & 15, col = k * kStageK + piece * 8;
+        const int pitch = MX ? a.ip : a.I;
+        // (columns of h past the last block of 32, or past I, are not written)
+        const bool in = col < (MX ? (a.I + 31) / 32 * 32 : a.I);
+        for (int i = tid >> 4; i < nb; i += kCopyThreads / 16) {
+          const uint32_t to = MX ? dst + 8192 + 512 + i * kMxTokenPitch + piece * 16
+                                 : dst + 32768 + tile_place(i, piece, nb);
+          copy16(to, a.h + int64_t(first + (i < rows ? i : 0)) * pitch + (in ? col : 0),
+                 in && i < rows, keep);
+        }
+        if constexpr (MX) {
+          if (tid < nb)
+            copy4(dst + 8192 + 512 + nb * kMxTokenPitch + tid * 4,
+                  a.hs + int64_t(first + (tid < rows ? tid : 0)) * (a.ip / 32) + k * 4, tid < rows);
+        }
+        copies_arrive(smem_u32(&full[st]));
+      };
+      struct Place {
+        int64_t at;
+        OutputRun r;
+        int k;
+        bool more;
+      };
+      auto next = [&](Place& p) {
+        if (++p.k == p.r.k0 + p.r.n) {
+          p.more = output_run(p.at, end2, active, k2, p.r);
+          p.k = p.r.k0;
+        }
+      };
+      Place w{at2, {}, 0, false};
+      w.more = output_run(w.at, end2, active, k2, w.r);
+      w.k = w.r.k0;
+      Place v = w;                       // whose tokens come next
+      int w_stage = stage, ahead = 0;    // stages whose weights are under way
+      uint32_t w_phase = phase;
+      auto send_weights = [&]() {
+        ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
+        if (!ok) return;
+        weights(w.r, w.k, w_stage);
+        next(w);
+        ++ahead;
+        if (++w_stage == a.stages) {
+          w_stage = 0;
+          w_phase ^= 1;
+        }
+      };
+      while (ok && w.more && ahead < a.stages) send_weights();
+      if (ok && v.more) ok = wait_grid(a.barrier + 1, uint32_t(G), abort_flag, a.status);
+      while (ok && v.more) {
+        if (ahead == 0) send_weights();
+        if (!ok) break;
+        tokens(v.r, v.k, stage);
+        next(v);
+        --ahead;
+        if (++stage == a.stages) stage = 0;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
+    } else {
+      // ---------------------------------------------------------- products
+      const int mw = warp - kCopyWarps;
+      const int mtid = threadIdx.x - kCopyThreads;
+      const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
+      int stage = 0;
+      uint32_t phase = 0;
+      float acc[NT][4];
+      // `n` stages into acc; `work`: this warp's rows exist
+      auto products = [&](int n, int nt, bool work) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        bool ok = true;
+        for (int k = 0; k < n; ++k) {
+          ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
+          if (!ok) break;
+          if (work)
+            stage_product<MX, NT>(ring + uint32_t(stage * a.stage_bytes), mw * 16, nt, acc);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        return math_all(ok);
+      };
+      bool ok = true;
+      int64_t at = at1;
+      HiddenTile t;
+      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+        ok = products(k1, a.n_x / 8, mw * 8 < t.n);
+        if (!ok) break;
+        const int first = ls.first[t.a];
+        const uint64_t mask = ls.mask[t.a];
+        const int p = mw * 8 + g;                 // this thread's hidden row
+        float h[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            h[j][e] = p < t.n ? activate(acc[j][e], a.act) * acc[j][e + 2] : 0.0f;
+        if constexpr (MX) {
+          // 32 hidden rows, those of four warps, share a scale
+          uint32_t* top = reinterpret_cast<uint32_t*>(yacc);   // [8 warps][n_x]
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t m = __float_as_uint(h[j][e]) & 0x7fffffffu;
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+              if (g == 0 && j * 8 < a.n_x) top[mw * a.n_x + j * 8 + c2 + e] = m;
+            }
+          math_sync();
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int tok = j * 8 + c2 + e;
+              if (j * 8 >= a.n_x || !((mask >> tok) & 1ull)) continue;
+              const uint32_t* m = top + (mw & 4) * a.n_x + tok;
+              const uint32_t s = half_scale(
+                  max(max(m[0], m[a.n_x]), max(m[2 * a.n_x], m[3 * a.n_x])));
+              const int64_t row = first + __popcll(mask & ((1ull << tok) - 1ull));
+              if ((mw & 4) * 8 < t.n) {           // (a whole block, zeros past I)
+                a.h[row * a.ip + t.i0 + p] = half_value(h[j][e], s);
+                if ((mw & 3) == 0 && g == 0)
+                  a.hs[row * (a.ip / 32) + (t.i0 + p) / 32] = uint8_t(s);
+              }
+            }
+        } else if (p < t.n) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int tok = j * 8 + c2 + e;
+              if (j * 8 >= a.n_x || !((mask >> tok) & 1ull)) continue;
+              const int64_t row = first + __popcll(mask & ((1ull << tok) - 1ull));
+              reinterpret_cast<__nv_bfloat16*>(a.h)[row * a.I + t.i0 + p] =
+                  __float2bfloat16_rn(h[j][e]);
+            }
+        }
+      }
+      // this CTA's hidden values are written
+      __threadfence();
+      math_sync();
+      if (mtid == 0) {
+        uint32_t old;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                     : "=r"(old)
+                     : "l"(a.barrier + 1)
+                     : "memory");
+      }
+      at = at2;
+      OutputRun r;
+      int rb = -1;                         // the block being summed
+      auto flush = [&]() {
+        math_sync();
+        // the CTAs that share block rb
+        const int64_t lo = int64_t(rb) * active * k2, hi = lo + int64_t(active) * k2;
+        int c0 = int(lo * G / n2), c1 = int((hi - 1) * G / n2);
+        while (part(n2, c0 + 1, G) <= lo) ++c0;
+        while (part(n2, c0, G) > lo) --c0;
+        while (part(n2, c1 + 1, G) < hi) ++c1;
+        while (part(n2, c1, G) >= hi) --c1;
+        const bool mine = c0 == c1;
+        bool last = mine;
+        if (!mine) {
+          float* to = a.parts + int64_t(c + rb) * a.T * 128;
+          for (int i = mtid; i < a.T * 128; i += kMathThreads)
+            __stcg(to + i, yacc[(i >> 7) * kYPitch + (i & 127)]);
+          __threadfence();
+          math_sync();
+          if (mtid == 0) {
+            int32_t parts = 0;   // CTAs of [c0, c1] that have a part (others' ranges are empty)
+            for (int k = c0; k <= c1; ++k) parts += part(n2, k, G) < part(n2, k + 1, G);
+            const int32_t old = atom_add_acq_rel_gpu(a.done + rb, 1);
+            *flag_s = old + 1 == parts;
+            if (old + 1 == parts) a.done[rb] = 0;   // for the next launch
+          }
+          math_sync();
+          last = *flag_s != 0;
+          if (last) __threadfence();
+        }
+        if (last) {
+          for (int i = mtid; i < a.T * 128; i += kMathThreads) {
+            const int row = rb * 128 + (i & 127);
+            if (row >= a.H) continue;
+            float v = 0.0f;
+            if (mine) {
+              v = yacc[(i >> 7) * kYPitch + (i & 127)];
+            } else {
+              for (int k = c0; k <= c1; ++k)
+                if (part(n2, k, G) < part(n2, k + 1, G))
+                  v += __ldcg(a.parts + int64_t(k + rb) * a.T * 128 + i);
+            }
+            reinterpret_cast<__nv_bfloat16*>(a.y)[(i >> 7) * a.y_stride + row] =
+                __float2bfloat16_rn(v);
+          }
+        }
+        math_sync();   // the sums may be overwritten
+      };
+      while (ok && output_run(at, end2, active, k2, r)) {
+        if (r.rb != rb) {
+          if (rb >= 0) flush();
+          rb = r.rb;
+          for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
+        }
+        const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
+        ok = products(r.n, (rows + 7) / 8, rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = j * 8 + c2 + e;
+            if (i >= rows) continue;
+            float* to = yacc + ls.token[first + i] * kYPitch + mw * 16 + g;
+            const float w = ls.weight[first + i];
+            to[0] += w * acc[j][e];
+            to[8] += w * acc[j][e + 2];
+          }
+        __syncwarp();   // another lane may add to the same sum next
+      }
+      if (ok && rb >= 0) flush();
+      if (active == 0) {   // no token has an expert: zeros
+        for (int64_t j = int64_t(c) * kMathThreads + mtid; j < int64_t(a.T) * a.H;
+             j += int64_t(G) * kMathThreads)
+          reinterpret_cast<__nv_bfloat16*>(a.y)[j / a.H * a.y_stride + j % a.H] =
+              __float2bfloat16_rn(0.0f);
+      }
+    }
   }
-  if (lane == 0)
-    reinterpret_cast<__nv_bfloat16*>(a.y)[t * a.y_stride + r] = __float2bfloat16_rn(y);
+
+  __syncthreads();
+  if (threadIdx.x == 0) grid_barrier_leave(a.barrier + 2, a.barrier, 2, uint32_t(G));
+}
+
+struct Layout {
+  int64_t done, logits, h, xq, xs, hs, parts, bytes;
+  int hp, ip, row_blocks;
+};
+
+Layout layout_of(const fo_moe_few_desc& d) {
+  Layout l{};
+  const int64_t pairs = int64_t(d.tokens) * d.top_k;
+  l.hp = int(mx_up(d.hidden, 128));
+  l.ip = int(mx_up(d.inter, 128));
+  l.row_blocks = l.hp / 128;
+  int64_t at = 256;
+  auto take = [&](int64_t bytes) {
+    const int64_t from = at;
+    at += mx_up(bytes, 256);
+    return from;
+  };
+  // the counters' place must not depend on the shape: calls of any shape share
+  // a workspace and leave the counters at zero
+  l.done = take(4 * kMaxRowBlocks);
+  l.logits = take(4 * int64_t(d.tokens) * d.experts);
+  if (d.weights == FO_TYPE_BF16) {
+    l.h = take(2 * pairs * d.inter);
+  } else {
+    l.xq = take(2 * int64_t(d.tokens) * l.hp);
+    l.xs = take(int64_t(d.tokens) * (l.hp / 32));
+    l.h = take(2 * pairs * l.ip);
+    l.hs = take(pairs * (l.ip / 32));
+  }
+  l.parts = take(4 * int64_t(kMaxCtas + l.row_blocks) * d.tokens * 128);
+  l.bytes = at;
+  return l;
+}
+
+template <bool MX, int NT>
+fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
+  const int slot = dev < 64 ? dev : 63;
+  std::call_once(once[slot], [&] {
+    err[slot] = cudaFuncSetAttribute(few_kernel<MX, NT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  });
+  if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, few_kernel<MX, NT>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return FO_ERR_CUDA;
+  }
+  return FO_OK;
+}
+
+template <bool MX>
+fo_status launch_n(const FewArgs& a, int grid, int smem, cudaStream_t st) {
+  if (a.n_x <= 8) return launch<MX, 1>(a, grid, smem, st);
+  if (a.n_x <= 16) return launch<MX, 2>(a, grid, smem, st);
+  if (a.n_x <= 32) return launch<MX, 4>(a, grid, smem, st);
+  return launch<MX, 8>(a, grid, smem, st);
 }
 
 }  // namespace
 
-int64_t few_workspace_bytes(const fo_moe_few_desc& d) {
-  const int64_t pairs = int64_t(d.tokens) * d.top_k;
-  return 256 + mx_up(8 * pairs, 256) + 4 * pairs * d.inter;
-}
+int64_t few_workspace_bytes(const fo_moe_few_desc& d) { return layout_of(d).bytes; }
 
 fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stride,
                          const void* router, const void* W1, const void* S1, const void* W2,
                          const void* S2, void* y, int64_t y_stride, void* workspace,
-                         int32_t*, void* stream) {
-  if (d.tokens == 0) return FO_OK;
-  const int64_t pairs = int64_t(d.tokens) * d.top_k;
-  uint8_t* ws = static_cast<uint8_t*>(workspace) + 256;
-  FewArgs a{d, static_cast<const uint16_t*>(x), x_stride, static_cast<const uint16_t*>(router),
-            W1, W2, static_cast<const uint8_t*>(S1), static_cast<const uint8_t*>(S2),
-            static_cast<uint16_t*>(y), y_stride, reinterpret_cast<int32_t*>(ws),
-            reinterpret_cast<float*>(ws + 4 * pairs),
-            reinterpret_cast<float*>(ws + mx_up(8 * pairs, 256))};
+                         int32_t* dev_status, void* stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FO_ERR_CUDA;
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  const bool mx = d.weights == FO_TYPE_MX4;
+  const Layout l = layout_of(d);
+  if (l.row_blocks > kMaxRowBlocks) return FO_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  FewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = x_stride;
+  a.router = static_cast<const uint16_t*>(router);
+  a.w1 = static_cast<const uint8_t*>(W1);
+  a.w2 = static_cast<const uint8_t*>(W2);
+  a.s1 = static_cast<const uint8_t*>(S1);
+  a.s2 = static_cast<const uint8_t*>(S2);
+  a.y = static_cast<uint16_t*>(y);
+  a.y_stride = y_stride;
+  a.T = d.tokens, a.H = d.hidden, a.I = d.inter, a.E = d.experts, a.K = d.top_k;
+  a.renormalize = d.renormalize;
+  a.act = d.act;
+  a.w1_rows = mx ? int(mx_up(2 * int64_t(d.inter), 128)) : 2 * d.inter;
+  a.w2_rows = mx ? l.hp : d.hidden;
+  a.barrier = reinterpret_cast<uint32_t*>(ws);
+  a.done = reinterpret_cast<int32_t*>(ws + l.done);
+  a.logits = reinterpret_cast<float*>(ws + l.logits);
+  a.h = reinterpret_cast<uint16_t*>(ws + l.h);
+  a.xq = reinterpret_cast<uint16_t*>(ws + l.xq);
+  a.xs = ws + l.xs, a.hs = ws + l.hs;
+  a.hp = l.hp, a.ip = l.ip;
+  a.parts = reinterpret_cast<float*>(ws + l.parts);
+  a.status = dev_status;
+  a.n_x = int(mx_up(d.tokens, 8));
+  a.stage_bytes = int(mx_up(mx ? 8192 + 512 + a.n_x * (kMxTokenPitch + 4) : 32768 + a.n_x * 256, 128));
+  const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
+  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128));
+  const int tail = lists + y_bytes + kBarBytes + 128;
+  a.stages = (kSmemLimit - tail) / a.stage_bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  if (a.stages < 2) return FO_ERR_UNSUPPORTED;
+  a.off_lists = a.stages * a.stage_bytes;
+  a.off_y = a.off_lists + lists;
+  a.off_bar = a.off_y + y_bytes;
+  const int smem = a.off_bar + kBarBytes + 128;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d.experts <= 256)
-    few_router_kernel<8><<<d.tokens, 256, 0, st>>>(a);
-  else
-    few_router_kernel<32><<<d.tokens, 256, 0, st>>>(a);
-  few_hidden_kernel<<<unsigned((pairs * d.inter + 7) / 8), 256, 0, st>>>(a);
-  few_output_kernel<<<unsigned((int64_t(d.tokens) * d.hidden + 7) / 8), 256, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
+  return mx ? launch_n<true>(a, grid, smem, st) : launch_n<false>(a, grid, smem, st);
 }
 
 }  // namespace fo

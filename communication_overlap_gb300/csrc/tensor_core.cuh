@@ -6,53 +6,13 @@
 
 #include <cuda.h>
 
-#include "device_common.cuh"
+#include "pipeline.cuh"
 
 namespace fo {
 namespace tc {
 
-constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
-constexpr uint64_t kDrainNs = 10000000ull;    // 10 ms while winding down
-
-// ---------------------------------------------------------------- waits
-
-// Bounded wait for the phase with the given parity.  Gives up when another
-// role aborted (shared flag) or after kWaitNs; then records the error.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       int32_t* status) {
-  // the clock is read only now and then: reading it costs more than most waits
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (i % 64) continue;
-    if (*abort_flag) return false;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitNs) {
-      *abort_flag = 1;
-      atomicCAS(status, 0, int32_t(FO_ERR_TIMEOUT));
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                     int32_t* status) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
-}
-
-// The same for a converged warp, whose lanes get one answer (tcgen05.ld and
-// the like are .aligned).
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
-                                          volatile int* abort_flag, int32_t* status) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_slow(bar, parity, abort_flag, status);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 // Bounded wait that ignores the abort flag (while winding down).
-__device__ __noinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+static __device__ __noinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity))
     if (globaltimer_ns() - t0 > kDrainNs) return false;
@@ -63,14 +23,6 @@ __device__ __noinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-__device__ __forceinline__ uint64_t policy_evict_first() { return l2_evict_first(); }
-
-__device__ __forceinline__ uint64_t policy_evict_last() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
 }
 
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,

@@ -712,9 +712,11 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
  *  tokens 0 .. FO_MOE_FEW_TOKENS, experts <= 1024, top_k <= 32, hidden and
  *  inter multiples of 8.
  *  x: bf16, x_stride (elements) >= hidden; y: bf16, y_stride >= hidden.  x
- *      and the weights 16-byte aligned, x_stride a multiple of 8.
+ *      and the weights 16-byte aligned (4-bit codes 32), x_stride a multiple
+ *      of 8.
  *  router: bf16 [experts][hidden], 16-byte aligned.
- *  workspace: as for fo_moe_route (zeroed once before its first use). */
+ *  workspace: as for fo_moe_route (zeroed once before its first use, calls of
+ *      any shape may share one; zero it again after FO_ERR_TIMEOUT). */
 #define FO_MOE_FEW_TOKENS 64
 typedef struct {
   int32_t tokens, hidden, inter, experts, top_k;
