@@ -69,7 +69,6 @@ struct FewArgs {
   int64_t y_stride;
   int32_t T, H, I, E, K, renormalize, act;
   int32_t w1_rows, w2_rows;   // rows of an expert's matrices as stored
-  int32_t n_x;                // tokens of a stage of the first product (a multiple of 8)
   int32_t stages, stage_bytes;
   int32_t off_lists, off_y, off_bar;      // shared memory offsets
   uint32_t* barrier;          // [0], [1] counts, [2] leave
@@ -85,7 +84,6 @@ struct FewArgs {
 
 // The routing as every CTA keeps it in shared memory.
 struct Lists {
-  uint64_t* mask;     // [E] tokens of the a-th active expert
   float* weight;      // [P] weight of row r (rows sorted by expert, token, slot)
   float* pair_weight; // [P]
   int16_t* token;     // [P] token of row r
@@ -96,8 +94,7 @@ struct Lists {
 
 __device__ __forceinline__ Lists lists_at(uint8_t* p, int P, int E) {
   Lists l;
-  l.mask = reinterpret_cast<uint64_t*>(p);
-  l.weight = reinterpret_cast<float*>(l.mask + E);
+  l.weight = reinterpret_cast<float*>(p);
   l.pair_weight = l.weight + P;
   l.token = reinterpret_cast<int16_t*>(l.pair_weight + P);
   l.id = l.token + P;
@@ -106,7 +103,7 @@ __device__ __forceinline__ Lists lists_at(uint8_t* p, int P, int E) {
   return l;
 }
 
-__host__ inline int lists_bytes(int P, int E) { return (12 * P + 12 * E + 2 + 127) / 128 * 128; }
+__host__ inline int lists_bytes(int P, int E) { return (12 * P + 4 * E + 2 + 127) / 128 * 128; }
 
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == FO_ACT_NONE) return g;
@@ -385,6 +382,18 @@ __device__ __forceinline__ void stage_bf16(uint32_t stage, int warp_row, int nt,
   }
 }
 
+// Four scale bytes as floats.  Bytes 1 to 254 are the exponent field; 0
+// (2^-127) and 255 (NaN) take the long way, for the whole word.
+__device__ __forceinline__ void scale_values(uint32_t w, float (&s)[4]) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) s[b] = __uint_as_float(((w >> (8 * b)) & 255u) << 23);
+  const uint32_t n = ~w;
+  if ((((w - 0x01010101u) & n) | ((n - 0x01010101u) & w)) & 0x80808080u) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) s[b] = mx_scale_value((w >> (8 * b)) & 255u);
+  }
+}
+
 // 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
 // codes of a row (one word) and the same 8 columns of a token (16 bytes); which
 // of the MMA's 16 columns they stand in does not matter as long as both agree.
@@ -395,28 +404,37 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, int warp_row, int nt, f
   const uint32_t scales = stage + 8192, tokens = scales + 512;
   const uint32_t token_scales = tokens + uint32_t(nt * 8) * kMxTokenPitch;
   const uint32_t sw0 = lds32(scales + r * 4), sw1 = lds32(scales + (r + 8) * 4);
+  uint32_t w0[4], w1[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    uint32_t p[4], q[4];
-    mx_decode8(lds32(stage + code_place(r, b) + c * 4), p);
-    mx_decode8(lds32(stage + code_place(r + 8, b) + c * 4), q);
-    const float s0 = mx_scale_value((sw0 >> (8 * b)) & 255u);
-    const float s1 = mx_scale_value((sw1 >> (8 * b)) & 255u);
+    w0[b] = lds32(stage + code_place(r, b) + c * 4);
+    w1[b] = lds32(stage + code_place(r + 8, b) + c * 4);
+  }
+  float s0[4], s1[4];
+  scale_values(sw0, s0);
+  scale_values(sw1, s1);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j >= nt) break;
-      uint32_t t[4];
-      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + b * 64 + c * 16, t);
-      const float u0 = mx_scale_value((lds32(token_scales + (j * 8 + c * 2) * 4) >> (8 * b)) & 255u);
-      const float u1 =
-          mx_scale_value((lds32(token_scales + (j * 8 + c * 2 + 1) * 4) >> (8 * b)) & 255u);
+  for (int j = 0; j < NT; ++j) {
+    if (j >= nt) break;
+    uint32_t t[4][4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + b * 64 + c * 16, t[b]);
+    float u0[4], u1[4];
+    scale_values(lds32(token_scales + (j * 8 + c * 2) * 4), u0);
+    scale_values(lds32(token_scales + (j * 8 + c * 2 + 1) * 4), u1);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t p[4], q[4];
+      mx_decode8(w0[b], p);
+      mx_decode8(w1[b], q);
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma16816<true>(d, p[0], q[0], p[1], q[1], t[0], t[1]);
-      mma16816<true>(d, p[2], q[2], p[3], q[3], t[2], t[3]);
-      acc[j][0] = fmaf(d[0] * u0, s0, acc[j][0]);
-      acc[j][1] = fmaf(d[1] * u1, s0, acc[j][1]);
-      acc[j][2] = fmaf(d[2] * u0, s1, acc[j][2]);
-      acc[j][3] = fmaf(d[3] * u1, s1, acc[j][3]);
+      mma16816<true>(d, p[0], q[0], p[1], q[1], t[b][0], t[b][1]);
+      mma16816<true>(d, p[2], q[2], p[3], q[3], t[b][2], t[b][3]);
+      acc[j][0] = fmaf(d[0] * u0[b], s0[b], acc[j][0]);
+      acc[j][1] = fmaf(d[1] * u1[b], s0[b], acc[j][1]);
+      acc[j][2] = fmaf(d[2] * u0[b], s1[b], acc[j][2]);
+      acc[j][3] = fmaf(d[3] * u1[b], s1[b], acc[j][3]);
     }
   }
 }
@@ -547,11 +565,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
         if (e >= 0 && rank == 0) count[e] += __popc(same);
         __syncwarp();
       }
-      for (int i = lane; i < active; i += 32) {
-        uint64_t m = 0;
-        for (int r = ls.first[i]; r < ls.first[i + 1]; ++r) m |= 1ull << ls.token[r];
-        ls.mask[i] = m;
-      }
     }
     __syncthreads();
 
@@ -579,6 +592,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
         // hidden row p of the tile: its gate in row (p / 8) * 16 + p % 8 of the
         // stage, its up-projection 8 rows below
         const int64_t gate = int64_t(ls.active[t.a]) * a.w1_rows + t.i0;
+        const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
+        const int nb = (rows + 7) / 8 * 8;
         for (int k = 0; k < k1; ++k) {
           ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
           if (!ok) break;
@@ -601,14 +616,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
                             : a.s1,
                     p < t.n);
             }
-            const uint32_t tok = dst + 8192 + 512, sc = tok + a.n_x * kMxTokenPitch;
-            for (int r = tid >> 4; r < a.n_x; r += kCopyThreads / 16)
-              copy16(tok + r * kMxTokenPitch + (tid & 15) * 16,
-                     a.xq + (r < a.T ? int64_t(r) * a.hp : 0) + k * 128 + (tid & 15) * 8, r < a.T,
-                     keep);
-            if (tid < a.n_x)
-              copy4(sc + tid * 4, a.xs + (tid < a.T ? int64_t(tid) * (a.hp / 32) : 0) + k * 4,
-                    tid < a.T);
+            const uint32_t tok = dst + 8192 + 512, sc = tok + nb * kMxTokenPitch;
+            for (int i = tid >> 4; i < nb; i += kCopyThreads / 16)
+              copy16(tok + i * kMxTokenPitch + (tid & 15) * 16,
+                     a.xq + int64_t(ls.token[first + (i < rows ? i : 0)]) * a.hp + k * 128 +
+                         (tid & 15) * 8,
+                     i < rows, keep);
+            if (tid < nb)
+              copy4(sc + tid * 4,
+                    a.xs + int64_t(ls.token[first + (tid < rows ? tid : 0)]) * (a.hp / 32) + k * 4,
+                    tid < rows);
           } else {
             const int piece = tid & 15, col = k * kStageK + piece * 8;
             const bool in = col < a.H;
@@ -621,9 +638,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
               copy16(dst + tile_place(row, piece, 128), src, in, once);
               copy16(dst + tile_place(row + 8, piece, 128), src + up, in, once);
             }
-            for (int r = tid >> 4; r < a.n_x; r += kCopyThreads / 16)
-              copy16(dst + 32768 + tile_place(r, piece, a.n_x),
-                     a.x + (r < a.T ? r * a.x_stride : 0) + c8, in && r < a.T, keep);
+            for (int i = tid >> 4; i < nb; i += kCopyThreads / 16)
+              copy16(dst + 32768 + tile_place(i, piece, nb),
+                     a.x + ls.token[first + (i < rows ? i : 0)] * a.x_stride + c8, in && i < rows,
+                     keep);
           }
           copies_arrive(smem_u32(&full[stage]));
           if (++stage == a.stages) {
@@ -748,10 +766,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       int64_t at = at1;
       HiddenTile t;
       while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
-        ok = products(k1, a.n_x / 8, mw * 8 < t.n);
+        const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
+        const int nb = (rows + 7) / 8 * 8;
+        ok = products(k1, nb / 8, mw * 8 < t.n);
         if (!ok) break;
-        const int first = ls.first[t.a];
-        const uint64_t mask = ls.mask[t.a];
         const int p = mw * 8 + g;                 // this thread's hidden row
         float h[NT][2];
 #pragma unroll
@@ -761,7 +779,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
             h[j][e] = p < t.n ? activate(acc[j][e], a.act) * acc[j][e + 2] : 0.0f;
         if constexpr (MX) {
           // 32 hidden rows, those of four warps, share a scale
-          uint32_t* top = reinterpret_cast<uint32_t*>(yacc);   // [8 warps][n_x]
+          uint32_t* top = reinterpret_cast<uint32_t*>(yacc);   // [8 warps][nb]
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -769,19 +787,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
               uint32_t m = __float_as_uint(h[j][e]) & 0x7fffffffu;
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-              if (g == 0 && j * 8 < a.n_x) top[mw * a.n_x + j * 8 + c2 + e] = m;
+              if (g == 0 && j * 8 < nb) top[mw * nb + j * 8 + c2 + e] = m;
             }
           math_sync();
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int tok = j * 8 + c2 + e;
-              if (j * 8 >= a.n_x || !((mask >> tok) & 1ull)) continue;
-              const uint32_t* m = top + (mw & 4) * a.n_x + tok;
-              const uint32_t s = half_scale(
-                  max(max(m[0], m[a.n_x]), max(m[2 * a.n_x], m[3 * a.n_x])));
-              const int64_t row = first + __popcll(mask & ((1ull << tok) - 1ull));
+              const int i = j * 8 + c2 + e;
+              if (i >= rows) continue;
+              const uint32_t* m = top + (mw & 4) * nb + i;
+              const uint32_t s = half_scale(max(max(m[0], m[nb]), max(m[2 * nb], m[3 * nb])));
+              const int64_t row = first + i;
               if ((mw & 4) * 8 < t.n) {           // (a whole block, zeros past I)
                 a.h[row * a.ip + t.i0 + p] = half_value(h[j][e], s);
                 if ((mw & 3) == 0 && g == 0)
@@ -793,11 +810,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int tok = j * 8 + c2 + e;
-              if (j * 8 >= a.n_x || !((mask >> tok) & 1ull)) continue;
-              const int64_t row = first + __popcll(mask & ((1ull << tok) - 1ull));
-              reinterpret_cast<__nv_bfloat16*>(a.h)[row * a.I + t.i0 + p] =
-                  __float2bfloat16_rn(h[j][e]);
+              const int i = j * 8 + c2 + e;
+              if (i < rows)
+                reinterpret_cast<__nv_bfloat16*>(a.h)[int64_t(first + i) * a.I + t.i0 + p] =
+                    __float2bfloat16_rn(h[j][e]);
             }
         }
       }
@@ -961,9 +977,9 @@ fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
 
 template <bool MX>
 fo_status launch_n(const FewArgs& a, int grid, int smem, cudaStream_t st) {
-  if (a.n_x <= 8) return launch<MX, 1>(a, grid, smem, st);
-  if (a.n_x <= 16) return launch<MX, 2>(a, grid, smem, st);
-  if (a.n_x <= 32) return launch<MX, 4>(a, grid, smem, st);
+  if (a.T <= 8) return launch<MX, 1>(a, grid, smem, st);
+  if (a.T <= 16) return launch<MX, 2>(a, grid, smem, st);
+  if (a.T <= 32) return launch<MX, 4>(a, grid, smem, st);
   return launch<MX, 8>(a, grid, smem, st);
 }
 
@@ -1008,8 +1024,9 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.hp = l.hp, a.ip = l.ip;
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
-  a.n_x = int(mx_up(d.tokens, 8));
-  a.stage_bytes = int(mx_up(mx ? 8192 + 512 + a.n_x * (kMxTokenPitch + 4) : 32768 + a.n_x * 256, 128));
+  // an expert's tokens: all of them at most
+  const int nb = int(mx_up(d.tokens, 8));
+  a.stage_bytes = int(mx_up(mx ? 8192 + 512 + nb * (kMxTokenPitch + 4) : 32768 + nb * 256, 128));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
   const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128));
   const int tail = lists + y_bytes + kBarBytes + 128;
