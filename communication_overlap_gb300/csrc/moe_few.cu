@@ -16,7 +16,7 @@
 //    output product is one line of (128 output rows, expert, 128 columns)
 //    stages, cut the same way.
 //  * A warp's 16 rows are 8 gate rows and their 8 up rows, which puts both
-//    values of a hidden row in one thread: the activation happens in registers
+//    sums of a hidden row in one thread: the activation happens in registers
 //    and only the hidden values (a few rows) travel through memory, inside L2.
 //  * Between the two products stands a grid barrier.  The ring fills with the
 //    second product's weights before it; only the loads of h wait.
@@ -45,9 +45,7 @@ constexpr int kMaxRowBlocks = 4096;     // blocks of 128 output rows
 constexpr int kMaxStages = 16;
 constexpr int kStageK = 128;            // columns of the weights per stage
 constexpr int kSmemLimit = 232448;
-constexpr int kCopyWarps = 4, kMathWarps = 8;
-constexpr int kCopyThreads = kCopyWarps * 32, kMathThreads = kMathWarps * 32;
-constexpr int kWarps = kCopyWarps + kMathWarps;
+constexpr int kCopyWarps = 4, kCopyThreads = kCopyWarps * 32;
 constexpr int kYPitch = 132;            // floats per token of the outputs' sums
 constexpr int kMxTokenPitch = 320;      // bytes per token of a 4-bit stage: 256 and a bank shift
 
@@ -116,13 +114,13 @@ __device__ __forceinline__ float activate(float g, int act) {
 // Logits of a block of 4 experts x 8 tokens by one CTA: its warps share out
 // the columns, 256 at a time, and their sums meet in shared memory.
 __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float acc[4][8];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[e][t] = 0.0f;
-  for (int k = (warp * 32 + lane) * 8; k < a.H; k += kWarps * 256) {
+  for (int k = (warp * 32 + lane) * 8; k < a.H; k += warps * 256) {
     uint4 r[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -153,14 +151,13 @@ __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
       float v = acc[e][t];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) red[(e * 8 + t) * kWarps + warp] = v;
+      if (lane == 0) red[(e * 8 + t) * warps + warp] = v;
     }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int e = e0 + threadIdx.x / 8, t = t0 + threadIdx.x % 8;
     float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[threadIdx.x * kWarps + w];
+    for (int w = 0; w < warps; ++w) v += red[threadIdx.x * warps + w];
     if (e < a.E && t < a.T) __stcg(a.logits + int64_t(t) * a.E + e, v);
   }
 }
@@ -183,9 +180,9 @@ __device__ __forceinline__ uint16_t half_value(float v, uint32_t s) {
 // x as f16 with scales, a warp per 32 columns of a token (columns past H:
 // zeros), and zero scales past the last block of each row of h.
 __device__ void scale_x(const FewArgs& a) {
-  const int lane = threadIdx.x % 32, blocks = a.hp / 32;
-  const int64_t first = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
-  for (int64_t j = first; j < int64_t(a.T) * blocks; j += int64_t(gridDim.x) * kWarps) {
+  const int lane = threadIdx.x % 32, blocks = a.hp / 32, warps = blockDim.x / 32;
+  const int64_t first = int64_t(blockIdx.x) * warps + threadIdx.x / 32;
+  for (int64_t j = first; j < int64_t(a.T) * blocks; j += int64_t(gridDim.x) * warps) {
     const int t = int(j / blocks), c = int(j % blocks) * 32 + lane;
     const float v =
         c < a.H ? __uint_as_float(uint32_t(__ldg(a.x + t * a.x_stride + c)) << 16) : 0.0f;
@@ -195,7 +192,7 @@ __device__ void scale_x(const FewArgs& a) {
     if (lane == 0) a.xs[int64_t(t) * blocks + c / 32] = uint8_t(s);
   }
   const int used = (a.I + 31) / 32;
-  for (int64_t r = first * 32 + lane; r < int64_t(a.T) * a.K; r += int64_t(gridDim.x) * kWarps * 32)
+  for (int64_t r = first * 32 + lane; r < int64_t(a.T) * a.K; r += int64_t(gridDim.x) * warps * 32)
     for (int b = used; b < a.ip / 32; ++b) a.hs[r * (a.ip / 32) + b] = 0;
 }
 
@@ -240,9 +237,11 @@ __device__ __forceinline__ bool output_run(int64_t& at, int64_t end, int active,
 // ------------------------------------------------------------------ instructions
 
 // 16 bytes (or 4) from global to shared memory, zeros where !valid (src is
-// then not read but must be an address).
+// then not read but must be an address).  The 256 bytes around them come to L2
+// together: a 4-bit stage takes 64 bytes of a row, and pieces that small, one
+// row apart, reach a quarter of HBM's rate.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(dst),
                "l"(src), "r"(valid ? 16u : 0u), "l"(policy)
                : "memory");
 }
@@ -309,12 +308,14 @@ __device__ __forceinline__ uint32_t code_place(int r, int p) {
   return uint32_t(r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
 }
 
+template <int THREADS>
 __device__ __forceinline__ void math_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kMathThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // The same, and whether all say yes: the computing warps give up together, so
 // that none is left at a barrier.
+template <int THREADS>
 __device__ __forceinline__ bool math_all(bool yes) {
   uint32_t out;
   asm volatile(
@@ -323,7 +324,7 @@ __device__ __forceinline__ bool math_all(bool yes) {
       "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(out)
-      : "r"(uint32_t(yes)), "n"(kMathThreads)
+      : "r"(uint32_t(yes)), "n"(THREADS)
       : "memory");
   return out != 0;
 }
@@ -353,16 +354,20 @@ __device__ __forceinline__ bool wait_grid(const uint32_t* count, uint32_t target
 
 // ------------------------------------------------------------------ a stage's products
 
-// bf16: this warp's 16 rows of the stage times nt tiles of 8 tokens.
-template <int NT>
-__device__ __forceinline__ void stage_bf16(uint32_t stage, int warp_row, int nt, float (&acc)[NT][4]) {
+// bf16: this warp's 16 rows of the stage (8 from lo, 8 from hi on) times nt
+// tiles of 8 tokens.
+template <int NT, int KS>
+__device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int kh, int nt,
+                                           float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31;
+  const int row = ((lane & 8) ? hi : lo) + (lane & 7);
   const uint32_t tokens = stage + 32768;
   const int nb = nt * 8;
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
+  for (int i = 0; i < 8 / KS; ++i) {
+    const int ks = kh * (8 / KS) + i;
     uint32_t w[4];
-    ldsm4(stage + tile_place(warp_row + (lane & 15), ks * 2 + (lane >> 4), 128), w);
+    ldsm4(stage + tile_place(row, ks * 2 + (lane >> 4), 128), w);
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
       if (j >= nt) break;
@@ -382,49 +387,52 @@ __device__ __forceinline__ void stage_bf16(uint32_t stage, int warp_row, int nt,
   }
 }
 
-// Four scale bytes as floats.  Bytes 1 to 254 are the exponent field; 0
+// The word's first N scale bytes as floats.  Bytes 1 to 254 are the exponent field; 0
 // (2^-127) and 255 (NaN) take the long way, for the whole word.
-__device__ __forceinline__ void scale_values(uint32_t w, float (&s)[4]) {
+template <int N>
+__device__ __forceinline__ void scale_values(uint32_t w, float (&s)[N]) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) s[b] = __uint_as_float(((w >> (8 * b)) & 255u) << 23);
-  const uint32_t n = ~w;
-  if ((((w - 0x01010101u) & n) | ((n - 0x01010101u) & w)) & 0x80808080u) {
+  for (int b = 0; b < N; ++b) s[b] = __uint_as_float(((w >> (8 * b)) & 255u) << 23);
+  const uint32_t v = N == 4 ? w : (w & 0xffffu) | 0x7f7f0000u, n = ~v;   // (N is 2 or 4)
+  if ((((v - 0x01010101u) & n) | ((n - 0x01010101u) & v)) & 0x80808080u) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) s[b] = mx_scale_value((w >> (8 * b)) & 255u);
+    for (int b = 0; b < N; ++b) s[b] = mx_scale_value((w >> (8 * b)) & 255u);
   }
 }
 
 // 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
 // codes of a row (one word) and the same 8 columns of a token (16 bytes); which
 // of the MMA's 16 columns they stand in does not matter as long as both agree.
-template <int NT>
-__device__ __forceinline__ void stage_mx(uint32_t stage, int warp_row, int nt, float (&acc)[NT][4]) {
+template <int NT, int KS>
+__device__ __forceinline__ void stage_mx(uint32_t stage, int lo, int hi, int kh, int nt,
+                                         float (&acc)[NT][4]) {
+  constexpr int kBlocks = 4 / KS;
   const int lane = threadIdx.x & 31;
-  const int r = warp_row + (lane >> 2), c = lane & 3;
+  const int r = lo + (lane >> 2), r8 = hi + (lane >> 2), c = lane & 3;
   const uint32_t scales = stage + 8192, tokens = scales + 512;
   const uint32_t token_scales = tokens + uint32_t(nt * 8) * kMxTokenPitch;
-  const uint32_t sw0 = lds32(scales + r * 4), sw1 = lds32(scales + (r + 8) * 4);
-  uint32_t w0[4], w1[4];
+  const int b0 = kh * kBlocks;
+  uint32_t w0[kBlocks], w1[kBlocks];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    w0[b] = lds32(stage + code_place(r, b) + c * 4);
-    w1[b] = lds32(stage + code_place(r + 8, b) + c * 4);
+  for (int b = 0; b < kBlocks; ++b) {
+    w0[b] = lds32(stage + code_place(r, b0 + b) + c * 4);
+    w1[b] = lds32(stage + code_place(r8, b0 + b) + c * 4);
   }
-  float s0[4], s1[4];
-  scale_values(sw0, s0);
-  scale_values(sw1, s1);
+  float s0[kBlocks], s1[kBlocks];
+  scale_values(lds32(scales + r * 4) >> (8 * b0), s0);
+  scale_values(lds32(scales + r8 * 4) >> (8 * b0), s1);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     if (j >= nt) break;
-    uint32_t t[4][4];
+    uint32_t t[kBlocks][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + b * 64 + c * 16, t[b]);
-    float u0[4], u1[4];
-    scale_values(lds32(token_scales + (j * 8 + c * 2) * 4), u0);
-    scale_values(lds32(token_scales + (j * 8 + c * 2 + 1) * 4), u1);
+    for (int b = 0; b < kBlocks; ++b)
+      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + (b0 + b) * 64 + c * 16, t[b]);
+    float u0[kBlocks], u1[kBlocks];
+    scale_values(lds32(token_scales + (j * 8 + c * 2) * 4) >> (8 * b0), u0);
+    scale_values(lds32(token_scales + (j * 8 + c * 2 + 1) * 4) >> (8 * b0), u1);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < kBlocks; ++b) {
       uint32_t p[4], q[4];
       mx_decode8(w0[b], p);
       mx_decode8(w1[b], q);
@@ -439,20 +447,21 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, int warp_row, int nt, f
   }
 }
 
-template <bool MX, int NT>
-__device__ __forceinline__ void stage_product(uint32_t stage, int warp_row, int nt,
-                                              float (&acc)[NT][4]) {
-  if constexpr (MX)
-    stage_mx<NT>(stage, warp_row, nt, acc);
-  else
-    stage_bf16<NT>(stage, warp_row, nt, acc);
-}
-
 constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
+
+// Computing warps: 8 of 16 rows each, or twice that, each pair sharing 16 rows
+// and halving the columns of a stage.  Decoding 4-bit weights is a chain of
+// dependent steps (8 warps took 1470 cycles for a stage that HBM delivers in
+// 400), so it wants the second set; with many tokens its registers do not fit.
+template <bool MX, int NT>
+constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
+template <bool MX, int NT>
+constexpr int kThreads = kCopyThreads + 256 * kSplit<MX, NT>;
 
 // NT: tiles of 8 tokens, at most.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs a) {
+  constexpr int KS = kSplit<MX, NT>, kMathThreads = 256 * KS, kWarps = kThreads<MX, NT> / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   const int P = a.T * a.K;
   const Lists ls = lists_at(smem + a.off_lists, P, a.E);
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(&full[s]), kCopyThreads);
-      mbar_init(smem_u32(&empty[s]), kMathWarps);
+      mbar_init(smem_u32(&empty[s]), 8 * KS);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -581,69 +590,93 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
 
     if (warp < kCopyWarps) {
       // ------------------------------------------------------------ copies
+      // Rows r0, r0 + 8 or 32, ... of a stage, one piece of 16 bytes of each:
+      // 16 pieces to a row of bf16, 4 to a row of codes.
       const int tid = threadIdx.x;
+      const int piece = MX ? tid & 3 : tid & 15, r0 = MX ? tid >> 2 : tid >> 4;
+      const uint32_t place = MX ? code_place(r0, piece) : tile_place(r0, piece, 128);
       const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // The tokens of stage k: nb rows of 256 bytes, 8 at a time, `rows` of them
+      // from memory (`src`: this thread's piece of its first row; the others by
+      // their token or in order from `base`), columns below `cols`.
+      auto send_tokens = [&](uint32_t dst, int nb, int rows, int first, int k, int64_t row_pitch,
+                             int cols, const uint16_t* src, const uint8_t* scale,
+                             const uint16_t* base, bool by_token) {
+        const int q = tid & 15;
+        const bool in = k * 128 + q * 8 < cols;
+        for (int i = tid >> 4; i < nb; i += 8) {
+          if (i >= 8) {
+            const int row = first + min(i, rows - 1);
+            src = base + (by_token ? int64_t(ls.token[row]) : int64_t(row)) * row_pitch + k * 128 + q * 8;
+          }
+          copy16(MX ? dst + 8192 + 512 + i * kMxTokenPitch + q * 16
+                    : dst + 32768 + tile_place(i, q, nb),
+                 in ? src : base, in && i < rows, keep);
+        }
+        if constexpr (MX)
+          if (tid < nb)
+            copy4(dst + 8192 + 512 + nb * kMxTokenPitch + tid * 4, scale, tid < rows);
+      };
       int64_t at = at1;
       HiddenTile t;
       while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
-        // hidden row p of the tile: its gate in row (p / 8) * 16 + p % 8 of the
-        // stage, its up-projection 8 rows below
+        // a stage's rows: the gate's from 0, the up-projection's from 64 on.
+        // A thread's addresses advance by a constant from stage to stage.
         const int64_t gate = int64_t(ls.active[t.a]) * a.w1_rows + t.i0;
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         const int nb = (rows + 7) / 8 * 8;
+        const int64_t pitch = MX ? a.hp / 2 : int64_t(a.H) * 2, up = a.I * pitch;   // bytes
+        const uint8_t* src = a.w1 + (gate + r0) * pitch + piece * 16;
+        const int left = t.n - r0;             // rows from this thread's first on
+        const uint8_t* scale = a.s1;
+        bool scaled = false;
+        if constexpr (MX) {
+          const int64_t row = gate + (tid & 63) + (tid >> 6) * int64_t(a.I);
+          scale += (row >> 7) * (a.hp / 128) * int64_t(512) + mx_scale_row(int(row & 127));
+          scaled = (tid & 63) < t.n;
+        }
+        const int64_t token = ls.token[first + min(tid >> 4, rows - 1)];
+        const uint16_t* tok = (MX ? a.xq + token * a.hp : a.x + token * a.x_stride) + (tid & 15) * 8;
+        const uint8_t* tok_scale =
+            a.xs + (MX ? int64_t(ls.token[first + min(tid, rows - 1)]) * (a.hp / 32) : 0);
         for (int k = 0; k < k1; ++k) {
           ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
           if (!ok) break;
           const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+          const uint32_t to = dst + place;
           if constexpr (MX) {
-            const int piece = tid & 3;
-            const int64_t pitch = a.hp / 2;
-            for (int p = tid >> 2; p < t.n; p += kCopyThreads / 4) {
-              const int row = (p >> 3) * 16 + (p & 7);
-              const uint8_t* src = a.w1 + (gate + p) * pitch + k * 64 + piece * 16;
-              copy16(dst + code_place(row, piece), src, true, once);
-              copy16(dst + code_place(row + 8, piece), src + a.I * pitch, true, once);
+            if (left > 0) {
+              copy16(to, src, true, once);
+              copy16(to + 4096, src + up, true, once);
             }
-            {
-              const int p = (tid >> 4) * 8 + (tid & 7);
-              const int64_t row = gate + p + ((tid >> 3) & 1) * int64_t(a.I);
-              copy4(dst + 8192 + tid * 4,
-                    p < t.n ? a.s1 + ((row >> 7) * (a.hp / 128) + k) * 512 +
-                                  mx_scale_row(int(row & 127))
-                            : a.s1,
-                    p < t.n);
+            if (left > 32) {
+              copy16(to + 2048, src + 32 * pitch, true, once);
+              copy16(to + 6144, src + 32 * pitch + up, true, once);
             }
-            const uint32_t tok = dst + 8192 + 512, sc = tok + nb * kMxTokenPitch;
-            for (int i = tid >> 4; i < nb; i += kCopyThreads / 16)
-              copy16(tok + i * kMxTokenPitch + (tid & 15) * 16,
-                     a.xq + int64_t(ls.token[first + (i < rows ? i : 0)]) * a.hp + k * 128 +
-                         (tid & 15) * 8,
-                     i < rows, keep);
-            if (tid < nb)
-              copy4(sc + tid * 4,
-                    a.xs + int64_t(ls.token[first + (tid < rows ? tid : 0)]) * (a.hp / 32) + k * 4,
-                    tid < rows);
+            if (scaled) copy4(dst + 8192 + tid * 4, scale, true);
           } else {
-            const int piece = tid & 15, col = k * kStageK + piece * 8;
-            const bool in = col < a.H;
-            const int64_t c8 = in ? col : 0;
-            const uint16_t* w = reinterpret_cast<const uint16_t*>(a.w1) + gate * a.H + c8;
-            const int64_t up = int64_t(a.I) * a.H;
-            for (int p = tid >> 4; p < t.n; p += kCopyThreads / 16) {
-              const int row = (p >> 3) * 16 + (p & 7);
-              const uint16_t* src = w + int64_t(p) * a.H;
-              copy16(dst + tile_place(row, piece, 128), src, in, once);
-              copy16(dst + tile_place(row + 8, piece, 128), src + up, in, once);
+            const bool in = k * kStageK + piece * 8 < a.H;
+            const uint8_t* from = in ? src : a.w1;
+            const int64_t step = in ? 8 * pitch : 0, half = in ? up : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i * 8 < left) {
+                copy16(to + i * 1024, from, in, once);
+                copy16(to + 8192 + i * 1024, from + half, in, once);
+                from += step;
+              }
             }
-            for (int i = tid >> 4; i < nb; i += kCopyThreads / 16)
-              copy16(dst + 32768 + tile_place(i, piece, nb),
-                     a.x + ls.token[first + (i < rows ? i : 0)] * a.x_stride + c8, in && i < rows,
-                     keep);
           }
+          send_tokens(dst, nb, rows, first, k, MX ? a.hp : int64_t(a.x_stride),
+                      MX ? a.hp : a.H, tok, tok_scale, MX ? a.xq : a.x, true);
           copies_arrive(smem_u32(&full[stage]));
+          src += MX ? 64 : 256;
+          scale += 512;
+          tok += 128;
+          tok_scale += 4;
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1;
@@ -652,70 +685,61 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       }
       // The second product: the weights of the first stages are on their way
       // before the barrier, the tokens follow after it.
-      auto weights = [&](const OutputRun& r, int k, int st) {
-        const uint32_t dst = ring + uint32_t(st * a.stage_bytes);
-        const int64_t row0 = int64_t(ls.active[r.a]) * a.w2_rows + r.rb * 128;
-        if constexpr (MX) {
-          const int piece = tid & 3;
-          const int64_t pitch = a.ip / 2;
-          for (int i = tid >> 2; i < 128; i += kCopyThreads / 4)
-            copy16(dst + code_place(i, piece), a.w2 + (row0 + i) * pitch + k * 64 + piece * 16, true,
-                   once);
-          copy4(dst + 8192 + tid * 4,
-                a.s2 + ((row0 >> 7) * (a.ip / 128) + k) * 512 + mx_scale_row(tid), true);
-        } else {
-          const int piece = tid & 15, col = k * kStageK + piece * 8;
-          const bool in = col < a.I;
-          const uint16_t* src =
-              reinterpret_cast<const uint16_t*>(a.w2) + row0 * a.I + (in ? col : 0);
-          const int rows = min(128, a.H - r.rb * 128);
-          for (int i = tid >> 4; i < rows; i += kCopyThreads / 16)
-            copy16(dst + tile_place(i, piece, 128), src + int64_t(i) * a.I, in, once);
-        }
-      };
-      auto tokens = [&](const OutputRun& r, int k, int st) {
-        const uint32_t dst = ring + uint32_t(st * a.stage_bytes);
-        const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
-        const int nb = (rows + 7) / 8 * 8, piece = tid & 15, col = k * kStageK + piece * 8;
-        const int pitch = MX ? a.ip : a.I;
-        // (columns of h past the last block of 32, or past I, are not written)
-        const bool in = col < (MX ? (a.I + 31) / 32 * 32 : a.I);
-        for (int i = tid >> 4; i < nb; i += kCopyThreads / 16) {
-          const uint32_t to = MX ? dst + 8192 + 512 + i * kMxTokenPitch + piece * 16
-                                 : dst + 32768 + tile_place(i, piece, nb);
-          copy16(to, a.h + int64_t(first + (i < rows ? i : 0)) * pitch + (in ? col : 0),
-                 in && i < rows, keep);
-        }
-        if constexpr (MX) {
-          if (tid < nb)
-            copy4(dst + 8192 + 512 + nb * kMxTokenPitch + tid * 4,
-                  a.hs + int64_t(first + (tid < rows ? tid : 0)) * (a.ip / 32) + k * 4, tid < rows);
-        }
-        copies_arrive(smem_u32(&full[st]));
-      };
       struct Place {
         int64_t at;
         OutputRun r;
         int k;
         bool more;
+        const uint8_t *src, *scale;      // weights, or a token's h and scales
       };
-      auto next = [&](Place& p) {
-        if (++p.k == p.r.k0 + p.r.n) {
-          p.more = output_run(p.at, end2, active, k2, p.r);
-          p.k = p.r.k0;
+      const int64_t pitch = MX ? a.ip / 2 : int64_t(a.I) * 2;
+      auto open = [&](Place& p, bool weights) {
+        p.more = output_run(p.at, end2, active, k2, p.r);
+        p.k = p.r.k0;
+        if (!p.more) return;
+        if (weights) {
+          const int64_t row = int64_t(ls.active[p.r.a]) * a.w2_rows + p.r.rb * 128;
+          p.src = a.w2 + (row + r0) * pitch + piece * 16 + int64_t(p.k) * (MX ? 64 : 256);
+          if constexpr (MX)
+            p.scale = a.s2 + ((row >> 7) * (a.ip / 128) + p.k) * int64_t(512) + mx_scale_row(tid);
+        } else {
+          const int first = ls.first[p.r.a], rows = ls.first[p.r.a + 1] - first;
+          p.src = reinterpret_cast<const uint8_t*>(
+              a.h + int64_t(first + min(tid >> 4, rows - 1)) * (MX ? a.ip : a.I) + (tid & 15) * 8 +
+              p.k * 128);
+          if constexpr (MX)
+            p.scale = a.hs + int64_t(first + min(tid, rows - 1)) * (a.ip / 32) + p.k * 4;
         }
       };
-      Place w{at2, {}, 0, false};
-      w.more = output_run(w.at, end2, active, k2, w.r);
-      w.k = w.r.k0;
-      Place v = w;                       // whose tokens come next
+      Place w{at2, {}, 0, false, nullptr, nullptr}, v{at2, {}, 0, false, nullptr, nullptr};
+      open(w, true);
+      open(v, false);
       int w_stage = stage, ahead = 0;    // stages whose weights are under way
       uint32_t w_phase = phase;
       auto send_weights = [&]() {
         ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
         if (!ok) return;
-        weights(w.r, w.k, w_stage);
-        next(w);
+        const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes), to = dst + place;
+        if constexpr (MX) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) copy16(to + i * 2048, w.src + i * 32 * pitch, true, once);
+          copy4(dst + 8192 + tid * 4, w.scale, true);
+          w.scale += 512;
+        } else {
+          const bool in = w.k * kStageK + piece * 8 < a.I;
+          const uint8_t* from = in ? w.src : a.w2;
+          const int64_t step = in ? 8 * pitch : 0;
+          const int left = a.H - w.r.rb * 128 - r0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i * 8 < left) {
+              copy16(to + i * 1024, from, in, once);
+              from += step;
+            }
+          }
+        }
+        w.src += MX ? 64 : 256;
+        if (++w.k == w.r.k0 + w.r.n) open(w, true);
         ++ahead;
         if (++w_stage == a.stages) {
           w_stage = 0;
@@ -727,22 +751,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       while (ok && v.more) {
         if (ahead == 0) send_weights();
         if (!ok) break;
-        tokens(v.r, v.k, stage);
-        next(v);
+        const int first = ls.first[v.r.a], rows = ls.first[v.r.a + 1] - first;
+        // (columns of h past I, or past its last block of 32, are not written)
+        send_tokens(ring + uint32_t(stage * a.stage_bytes), (rows + 7) / 8 * 8, rows, first, v.k,
+                    MX ? a.ip : a.I, MX ? (a.I + 31) / 32 * 32 : a.I,
+                    reinterpret_cast<const uint16_t*>(v.src), v.scale, a.h, false);
+        copies_arrive(smem_u32(&full[stage]));
+        v.src += 256;
+        if constexpr (MX) v.scale += 4;
+        if (++v.k == v.r.k0 + v.r.n) open(v, false);
         --ahead;
         if (++stage == a.stages) stage = 0;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
     } else {
       // ---------------------------------------------------------- products
-      const int mw = warp - kCopyWarps;
+      const int mw = (warp - kCopyWarps) & 7, kh = (warp - kCopyWarps) >> 3;
       const int mtid = threadIdx.x - kCopyThreads;
       const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
       int stage = 0;
       uint32_t phase = 0;
       float acc[NT][4];
+      float* half_sums = yacc + a.T * kYPitch;   // [NT][8 warps][32 lanes][4]
       // `n` stages into acc; `work`: this warp's rows exist
-      auto products = [&](int n, int nt, bool work) {
+      auto products = [&](int n, int nt, int lo, int hi, bool work) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -751,8 +783,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
         for (int k = 0; k < n; ++k) {
           ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
           if (!ok) break;
-          if (work)
-            stage_product<MX, NT>(ring + uint32_t(stage * a.stage_bytes), mw * 16, nt, acc);
+          if (work) {
+            const uint32_t at = ring + uint32_t(stage * a.stage_bytes);
+            if constexpr (MX)
+              stage_mx<NT, KS>(at, lo, hi, kh, nt, acc);
+            else
+              stage_bf16<NT, KS>(at, lo, hi, kh, nt, acc);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
           if (++stage == a.stages) {
@@ -760,7 +797,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
             phase ^= 1;
           }
         }
-        return math_all(ok);
+        if constexpr (KS == 1) {
+          return math_all<kMathThreads>(ok);
+        } else {
+          // the halves of K meet in the first set of warps
+          float* to = half_sums + (mw * 32 + lane) * 4;
+          if (kh == 1)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              *reinterpret_cast<float4*>(to + j * 1024) =
+                  make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+          ok = math_all<kMathThreads>(ok);
+          if (kh == 0)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float4 v = *reinterpret_cast<const float4*>(to + j * 1024);
+              acc[j][0] += v.x, acc[j][1] += v.y, acc[j][2] += v.z, acc[j][3] += v.w;
+            }
+          math_sync<kMathThreads>();
+          return ok;
+        }
       };
       bool ok = true;
       int64_t at = at1;
@@ -768,7 +824,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         const int nb = (rows + 7) / 8 * 8;
-        ok = products(k1, nb / 8, mw * 8 < t.n);
+        ok = products(k1, nb / 8, mw * 8, 64 + mw * 8, mw * 8 < t.n);
         if (!ok) break;
         const int p = mw * 8 + g;                 // this thread's hidden row
         float h[NT][2];
@@ -787,15 +843,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
               uint32_t m = __float_as_uint(h[j][e]) & 0x7fffffffu;
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-              if (g == 0 && j * 8 < nb) top[mw * nb + j * 8 + c2 + e] = m;
+              if (kh == 0 && g == 0 && j * 8 < nb) top[mw * nb + j * 8 + c2 + e] = m;
             }
-          math_sync();
+          math_sync<kMathThreads>();
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = j * 8 + c2 + e;
-              if (i >= rows) continue;
+              if (i >= rows || kh != 0) continue;
               const uint32_t* m = top + (mw & 4) * nb + i;
               const uint32_t s = half_scale(max(max(m[0], m[nb]), max(m[2 * nb], m[3 * nb])));
               const int64_t row = first + i;
@@ -811,7 +867,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = j * 8 + c2 + e;
-              if (i < rows)
+              if (i < rows && kh == 0)
                 reinterpret_cast<__nv_bfloat16*>(a.h)[int64_t(first + i) * a.I + t.i0 + p] =
                     __float2bfloat16_rn(h[j][e]);
             }
@@ -819,7 +875,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       }
       // this CTA's hidden values are written
       __threadfence();
-      math_sync();
+      math_sync<kMathThreads>();
       if (mtid == 0) {
         uint32_t old;
         asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
@@ -831,7 +887,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
       OutputRun r;
       int rb = -1;                         // the block being summed
       auto flush = [&]() {
-        math_sync();
+        math_sync<kMathThreads>();
         // the CTAs that share block rb
         const int64_t lo = int64_t(rb) * active * k2, hi = lo + int64_t(active) * k2;
         int c0 = int(lo * G / n2), c1 = int((hi - 1) * G / n2);
@@ -846,15 +902,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
           for (int i = mtid; i < a.T * 128; i += kMathThreads)
             __stcg(to + i, yacc[(i >> 7) * kYPitch + (i & 127)]);
           __threadfence();
-          math_sync();
+          math_sync<kMathThreads>();
           if (mtid == 0) {
             int32_t parts = 0;   // CTAs of [c0, c1] that have a part (others' ranges are empty)
-            for (int k = c0; k <= c1; ++k) parts += part(n2, k, G) < part(n2, k + 1, G);
+            for (int k = c0; k <= c1; ++k)
+              parts += n2 >= G || part(n2, k, G) < part(n2, k + 1, G);
             const int32_t old = atom_add_acq_rel_gpu(a.done + rb, 1);
             *flag_s = old + 1 == parts;
             if (old + 1 == parts) a.done[rb] = 0;   // for the next launch
           }
-          math_sync();
+          math_sync<kMathThreads>();
           last = *flag_s != 0;
           if (last) __threadfence();
         }
@@ -866,15 +923,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
             if (mine) {
               v = yacc[(i >> 7) * kYPitch + (i & 127)];
             } else {
+              const float* from = a.parts + int64_t(rb) * a.T * 128 + i;
+#pragma unroll 8
               for (int k = c0; k <= c1; ++k)
-                if (part(n2, k, G) < part(n2, k + 1, G))
-                  v += __ldcg(a.parts + int64_t(k + rb) * a.T * 128 + i);
+                if (n2 >= G || part(n2, k, G) < part(n2, k + 1, G))
+                  v += __ldcg(from + int64_t(k) * a.T * 128);
             }
             reinterpret_cast<__nv_bfloat16*>(a.y)[(i >> 7) * a.y_stride + row] =
                 __float2bfloat16_rn(v);
           }
         }
-        math_sync();   // the sums may be overwritten
+        math_sync<kMathThreads>();   // the sums may be overwritten
       };
       while (ok && output_run(at, end2, active, k2, r)) {
         if (r.rb != rb) {
@@ -883,14 +942,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_kernel(const FewArgs a) {
           for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
         }
         const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
-        ok = products(r.n, (rows + 7) / 8, rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
+        ok = products(r.n, (rows + 7) / 8, mw * 16, mw * 16 + 8, rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int i = j * 8 + c2 + e;
-            if (i >= rows) continue;
+            if (i >= rows || kh != 0) continue;
             float* to = yacc + ls.token[first + i] * kYPitch + mw * 16 + g;
             const float w = ls.weight[first + i];
             to[0] += w * acc[j][e];
@@ -960,7 +1019,7 @@ fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
   if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kThreads<MX, NT>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1028,7 +1087,8 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   const int nb = int(mx_up(d.tokens, 8));
   a.stage_bytes = int(mx_up(mx ? 8192 + 512 + nb * (kMxTokenPitch + 4) : 32768 + nb * 256, 128));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
-  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128));
+  // the outputs' sums, then the halves of K on their way (where split)
+  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 8192 : 0);
   const int tail = lists + y_bytes + kBarBytes + 128;
   a.stages = (kSmemLimit - tail) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
