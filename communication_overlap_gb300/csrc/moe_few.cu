@@ -27,6 +27,7 @@
 // weights: codes become f16 in registers (exact), x and h are f16 with a
 // power-of-two scale per 32 values (11 significant bits), a block's sum of 32
 // products starts at zero and is added times both scales in fp32.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +35,8 @@
 
 #include "moe_common.cuh"
 #include "mx_common.cuh"
-#include "pipeline.cuh"
+#include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace fo {
 
@@ -43,11 +45,15 @@ namespace {
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRowBlocks = 4096;     // blocks of 128 output rows
 constexpr int kMaxStages = 16;
-constexpr int kStageK = 128;            // columns of the weights per stage
 constexpr int kSmemLimit = 232448;
-constexpr int kCopyWarps = 4, kCopyThreads = kCopyWarps * 32;
 constexpr int kYPitch = 132;            // floats per token of the outputs' sums
-constexpr int kMxTokenPitch = 320;      // bytes per token of a 4-bit stage: 256 and a bank shift
+// Columns of the weights per stage: 256 bytes of a bf16 row, 128 of a 4-bit one.
+template <bool MX>
+constexpr int kStageK = MX ? 256 : 128;
+// A token's share of a 4-bit stage, in memory and in shared memory: 256 f16
+// values, their eight scale bytes, and what shifts the next token by 16 banks.
+constexpr int kMxToken = 576;
+constexpr int kMxScales = 16384, kMxTokens = kMxScales + 4096;   // offsets in a stage
 
 template <int N>
 struct Const {
@@ -58,6 +64,7 @@ struct Const {
 __device__ __forceinline__ int64_t part(int64_t n, int c, int g) { return n * c / g; }
 
 struct FewArgs {
+  CUtensorMap map_w1, map_w2;   // 4-bit: boxes of 128 bytes x 32 and 128 rows
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* router;
@@ -72,10 +79,12 @@ struct FewArgs {
   uint32_t* barrier;          // [0], [1] counts, [2] leave
   int32_t* done;              // [row blocks] parts finished
   float* logits;              // [T][E]
-  uint16_t* h;                // [rows][I] bf16, or [rows][Ip] f16
-  uint16_t* xq;               // 4-bit: [T][Hp] f16
-  uint8_t *xs, *hs;           // and scales, a byte per 32: [T][Hp / 32], [rows][Ip / 32]
-  int32_t hp, ip;             // 4-bit: padded columns
+  uint16_t* h;                // bf16: [rows][I]
+  uint8_t *xq, *hq;           // 4-bit: [stage of columns][token or row] of kMxToken bytes
+  float* x_scale;             // 4-bit: [T]
+  int32_t h_rows;             // rows of hq per stage
+  int32_t hp, ip;             // 4-bit: columns of xq and hq, whole stages
+  int32_t hb, ib;             // and blocks of 128 columns of the weights
   float* parts;               // [kMaxCtas + row blocks][T][128]
   int32_t* status;
 };
@@ -177,23 +186,44 @@ __device__ __forceinline__ uint16_t half_value(float v, uint32_t s) {
   return __half_as_ushort(__float2half_rn(v * __uint_as_float((254u - s) << 23)));
 }
 
-// x as f16 with scales, a warp per 32 columns of a token (columns past H:
-// zeros), and zero scales past the last block of each row of h.
+// x as f16 with one scale per token, a warp per token (the last CTAs': the
+// first have the router), zeros past H; and zeros for h past its last block of
+// 32 columns.
 __device__ void scale_x(const FewArgs& a) {
-  const int lane = threadIdx.x % 32, blocks = a.hp / 32, warps = blockDim.x / 32;
-  const int64_t first = int64_t(blockIdx.x) * warps + threadIdx.x / 32;
-  for (int64_t j = first; j < int64_t(a.T) * blocks; j += int64_t(gridDim.x) * warps) {
-    const int t = int(j / blocks), c = int(j % blocks) * 32 + lane;
-    const float v =
-        c < a.H ? __uint_as_float(uint32_t(__ldg(a.x + t * a.x_stride + c)) << 16) : 0.0f;
-    const uint32_t s =
-        half_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
-    a.xq[int64_t(t) * a.hp + c] = half_value(v, s);
-    if (lane == 0) a.xs[int64_t(t) * blocks + c / 32] = uint8_t(s);
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int64_t slot = int64_t(threadIdx.x / 32) * gridDim.x + (gridDim.x - 1 - blockIdx.x);
+  const int64_t slots = int64_t(warps) * gridDim.x;
+  for (int64_t t = slot; t < a.T; t += slots) {
+    const uint16_t* x = a.x + t * a.x_stride;
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.H; c += 256) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    }
+    const uint32_t s = half_scale(__reduce_max_sync(0xffffffffu, m) << 16);
+#pragma unroll 2
+    for (int c = lane * 8; c < a.hp; c += 256) {
+      const uint4 v = c < a.H ? __ldg(reinterpret_cast<const uint4*>(x + c)) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = half_value(bf16lo(w[i]), s) | uint32_t(half_value(bf16hi(w[i]), s)) << 16;
+      *reinterpret_cast<uint4*>(a.xq + (int64_t(c >> 8) * a.T + t) * kMxToken + (c & 255) * 2) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (lane == 0) a.x_scale[t] = s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
   }
-  const int used = (a.I + 31) / 32;
-  for (int64_t r = first * 32 + lane; r < int64_t(a.T) * a.K; r += int64_t(gridDim.x) * warps * 32)
-    for (int b = used; b < a.ip / 32; ++b) a.hs[r * (a.ip / 32) + b] = 0;
+  const int used = (a.I + 31) / 32 * 32;
+  for (int64_t r = slot; r < int64_t(a.T) * a.K; r += slots)
+    for (int c = used + lane; c < a.ip; c += 32) {
+      uint8_t* to = a.hq + (int64_t(c >> 8) * a.h_rows + r) * kMxToken;
+      reinterpret_cast<uint16_t*>(to)[c & 255] = 0;
+      if (lane == 0) to[512 + ((c & 255) >> 5)] = 1;
+    }
 }
 
 // ------------------------------------------------------------------ work items
@@ -236,21 +266,13 @@ __device__ __forceinline__ bool output_run(int64_t& at, int64_t end, int active,
 
 // ------------------------------------------------------------------ instructions
 
-// 16 bytes (or 4) from global to shared memory, zeros where !valid (src is
-// then not read but must be an address).  The 256 bytes around them come to L2
-// together: a 4-bit stage takes 64 bytes of a row, and pieces that small, one
-// row apart, reach a quarter of HBM's rate.
+// 16 bytes from global to shared memory, zeros where !valid (src is then not
+// read but must be an address).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(dst),
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
                "l"(src), "r"(valid ? 16u : 0u), "l"(policy)
                : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 4u : 0u)
-               : "memory");
-}
-
 // Arrive on `bar` when this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
@@ -303,9 +325,30 @@ __device__ __forceinline__ uint32_t tile_place(int r, int p, int rows) {
   return uint32_t((p >> 3) * rows * 128 + r * 128 + (((p & 7) ^ (r & 7)) << 4));
 }
 
-// The same for 4-bit codes: 64 bytes per row, four pieces of 32 codes.
+// The same for 4-bit codes: 128 bytes per row, eight pieces of 32 codes, in
+// the order of the TMA's 128-byte swizzle.
 __device__ __forceinline__ uint32_t code_place(int r, int p) {
-  return uint32_t(r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+  return uint32_t(r * 128 + ((p ^ (r & 7)) << 4));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 template <int THREADS>
@@ -387,62 +430,83 @@ __device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int k
   }
 }
 
-// The word's first N scale bytes as floats.  Bytes 1 to 254 are the exponent field; 0
-// (2^-127) and 255 (NaN) take the long way, for the whole word.
-template <int N>
-__device__ __forceinline__ void scale_values(uint32_t w, float (&s)[N]) {
-#pragma unroll
-  for (int b = 0; b < N; ++b) s[b] = __uint_as_float(((w >> (8 * b)) & 255u) << 23);
-  const uint32_t v = N == 4 ? w : (w & 0xffffu) | 0x7f7f0000u, n = ~v;   // (N is 2 or 4)
-  if ((((v - 0x01010101u) & n) | ((n - 0x01010101u) & v)) & 0x80808080u) {
-#pragma unroll
-    for (int b = 0; b < N; ++b) s[b] = mx_scale_value((w >> (8 * b)) & 255u);
-  }
+// Byte b of a word of scales as a float: its exponent field.  (Byte 0, 2^-127,
+// becomes zero: such a block adds less than 1e-36.)
+__device__ __forceinline__ float scale_of(uint32_t w, int b) {
+  return __uint_as_float((b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1) &
+                         0x7f800000u);
 }
 
 // 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
 // codes of a row (one word) and the same 8 columns of a token (16 bytes); which
 // of the MMA's 16 columns they stand in does not matter as long as both agree.
-template <int NT, int KS>
-__device__ __forceinline__ void stage_mx(uint32_t stage, int lo, int hi, int kh, int nt,
+// row0, row1: the thread's rows; scale0, scale1: where their scales are;
+// blocks: of the stage's eight, those that exist.  TOKEN_SCALES: the tokens'
+// values have a scale per block, too.
+template <int NT, int KS, bool TOKEN_SCALES>
+__device__ __forceinline__ void stage_mx(uint32_t stage, int row0, int row1, uint32_t scale0,
+                                         uint32_t scale1, int kh, int nt, int blocks,
                                          float (&acc)[NT][4]) {
-  constexpr int kBlocks = 4 / KS;
-  const int lane = threadIdx.x & 31;
-  const int r = lo + (lane >> 2), r8 = hi + (lane >> 2), c = lane & 3;
-  const uint32_t scales = stage + 8192, tokens = scales + 512;
-  const uint32_t token_scales = tokens + uint32_t(nt * 8) * kMxTokenPitch;
-  const int b0 = kh * kBlocks;
-  uint32_t w0[kBlocks], w1[kBlocks];
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const uint32_t tokens = stage + kMxTokens + uint32_t(lane >> 2) * kMxToken + c * 16;
+  const uint32_t token_scales = stage + kMxTokens + uint32_t(c * 2) * kMxToken + 512;
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
-    w0[b] = lds32(stage + code_place(r, b0 + b) + c * 4);
-    w1[b] = lds32(stage + code_place(r8, b0 + b) + c * 4);
-  }
-  float s0[kBlocks], s1[kBlocks];
-  scale_values(lds32(scales + r * 4) >> (8 * b0), s0);
-  scale_values(lds32(scales + r8 * 4) >> (8 * b0), s1);
+  for (int q4 = 0; q4 < 2 / KS; ++q4) {
+    const int q = kh + q4;                     // four blocks, a word of scales
+    if (q * 4 >= blocks) break;
+    uint32_t w0[4], w1[4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    if (j >= nt) break;
-    uint32_t t[kBlocks][4];
+    for (int b = 0; b < 4; ++b) {
+      w0[b] = lds32(stage + code_place(row0, q * 4 + b) + c * 4);
+      w1[b] = lds32(stage + code_place(row1, q * 4 + b) + c * 4);
+    }
+    const uint32_t sw0 = lds32(stage + scale0 + q * 512), sw1 = lds32(stage + scale1 + q * 512);
+    float s0[4], s1[4];
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-      lds128(tokens + uint32_t(j * 8 + (lane >> 2)) * kMxTokenPitch + (b0 + b) * 64 + c * 16, t[b]);
-    float u0[kBlocks], u1[kBlocks];
-    scale_values(lds32(token_scales + (j * 8 + c * 2) * 4) >> (8 * b0), u0);
-    scale_values(lds32(token_scales + (j * 8 + c * 2 + 1) * 4) >> (8 * b0), u1);
+    for (int b = 0; b < 4; ++b) s0[b] = scale_of(sw0, b), s1[b] = scale_of(sw1, b);
+    // 255 is NaN, not the infinity that its exponent field makes
+    if (((((sw0 & 0x7f7f7f7fu) + 0x01010101u) & sw0) | (((sw1 & 0x7f7f7f7fu) + 0x01010101u) & sw1)) &
+        0x80808080u) {
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      uint32_t p[4], q[4];
-      mx_decode8(w0[b], p);
-      mx_decode8(w1[b], q);
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma16816<true>(d, p[0], q[0], p[1], q[1], t[b][0], t[b][1]);
-      mma16816<true>(d, p[2], q[2], p[3], q[3], t[b][2], t[b][3]);
-      acc[j][0] = fmaf(d[0] * u0[b], s0[b], acc[j][0]);
-      acc[j][1] = fmaf(d[1] * u1[b], s0[b], acc[j][1]);
-      acc[j][2] = fmaf(d[2] * u0[b], s1[b], acc[j][2]);
-      acc[j][3] = fmaf(d[3] * u1[b], s1[b], acc[j][3]);
+      for (int b = 0; b < 4; ++b) {
+        s0[b] = mx_scale_value((sw0 >> (8 * b)) & 255u);
+        s1[b] = mx_scale_value((sw1 >> (8 * b)) & 255u);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j >= nt) break;
+      uint32_t t[4][4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        lds128(tokens + uint32_t(j * 8) * kMxToken + (q * 4 + b) * 64, t[b]);
+      uint32_t v0 = 0, v1 = 0;
+      if constexpr (TOKEN_SCALES) {
+        v0 = lds32(token_scales + uint32_t(j * 8) * kMxToken + q * 4);
+        v1 = lds32(token_scales + uint32_t(j * 8 + 1) * kMxToken + q * 4);
+      }
+      uint64_t lo = pack2(acc[j][0], acc[j][1]), hi = pack2(acc[j][2], acc[j][3]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t p[4], r[4];
+        mx_decode8(w0[b], p);
+        mx_decode8(w1[b], r);
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma16816<true>(d, p[0], r[0], p[1], r[1], t[b][0], t[b][1]);
+        mma16816<true>(d, p[2], r[2], p[3], r[3], t[b][2], t[b][3]);
+        uint64_t d0 = pack2(d[0], d[1]), d1 = pack2(d[2], d[3]);
+        if constexpr (TOKEN_SCALES) {
+          // (a token's scale byte is never 0, and 255 comes with zeros, which
+          // infinity makes NaN)
+          const uint64_t u = pack2(scale_of(v0, b), scale_of(v1, b));
+          d0 = mul2(d0, u);
+          d1 = mul2(d1, u);
+        }
+        lo = fma2(d0, pack2(s0[b], s0[b]), lo);
+        hi = fma2(d1, pack2(s1[b], s1[b]), hi);
+      }
+      unpack2(lo, acc[j][0], acc[j][1]);
+      unpack2(hi, acc[j][2], acc[j][3]);
     }
   }
 }
@@ -455,14 +519,22 @@ constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
 // 400), so it wants the second set; with many tokens its registers do not fit.
 template <bool MX, int NT>
 constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
+// Copying warps: one that issues bulk copies, or four that copy 16 bytes a
+// thread.
+template <bool MX>
+constexpr int kCopyWarps = MX ? 1 : 4;
 template <bool MX, int NT>
-constexpr int kThreads = kCopyThreads + 256 * kSplit<MX, NT>;
+constexpr int kThreads = 32 * kCopyWarps<MX> + 256 * kSplit<MX, NT>;
 
 // NT: tiles of 8 tokens, at most.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int kCopyThreads = 32 * kCopyWarps<MX>;
   constexpr int KS = kSplit<MX, NT>, kMathThreads = 256 * KS, kWarps = kThreads<MX, NT> / 32;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  // 1024-byte alignment, for the copies' swizzle
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int P = a.T * a.K;
   const Lists ls = lists_at(smem + a.off_lists, P, a.E);
   float* yacc = reinterpret_cast<float*>(smem + a.off_y);   // [T][kYPitch]; first product: maxima
@@ -479,7 +551,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&full[s]), kCopyThreads);
+      mbar_init(smem_u32(&full[s]), MX ? 2 : kCopyThreads);   // 4-bit: weights, tokens
       mbar_init(smem_u32(&empty[s]), 8 * KS);
     }
     *abort_flag = 0;
@@ -494,6 +566,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
     if constexpr (MX) scale_x(a);
   }
   __threadfence();
+  if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) *flag_s = grid_barrier(a.barrier, uint32_t(G), a.status);
   __syncthreads();
@@ -575,26 +648,28 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
         __syncwarp();
       }
     }
+    // (threads wrote to the ring's memory and to x's copy, bulk copies follow)
+    if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
     __syncthreads();
 
     const int active = *n_active_s;
     const int per_expert = (a.I + kGranule - 1) / kGranule;
     const int64_t n1 = int64_t(active) * per_expert;
     const int64_t at1 = part(n1, c, G), end1 = part(n1, c + 1, G);
-    const int k1 = (a.H + kStageK - 1) / kStageK;      // stages of a tile of the first product
-    const int k2 = (a.I + kStageK - 1) / kStageK;
+    const int k1 = (a.H + kStageK<MX> - 1) / kStageK<MX>;      // stages of a tile of the first product
+    const int k2 = (a.I + kStageK<MX> - 1) / kStageK<MX>;
     const int row_blocks = (a.H + 127) / 128;
     const int64_t n2 = int64_t(row_blocks) * active * k2;
     const int64_t at2 = part(n2, c, G), end2 = part(n2, c + 1, G);
     const uint32_t ring = smem_u32(smem);
 
-    if (warp < kCopyWarps) {
-      // ------------------------------------------------------------ copies
-      // Rows r0, r0 + 8 or 32, ... of a stage, one piece of 16 bytes of each:
-      // 16 pieces to a row of bf16, 4 to a row of codes.
+    if (!MX && warp < kCopyWarps<MX>) {
+      // ------------------------------------------------------ copies, bf16
+      // A thread has rows r0, r0 + 8, ... of a stage, one of the 16 pieces of 16
+      // bytes of each.
       const int tid = threadIdx.x;
-      const int piece = MX ? tid & 3 : tid & 15, r0 = MX ? tid >> 2 : tid >> 4;
-      const uint32_t place = MX ? code_place(r0, piece) : tile_place(r0, piece, 128);
+      const int piece = tid & 15, r0 = tid >> 4;
+      const uint32_t place = tile_place(r0, piece, 128);
       const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
@@ -603,22 +678,16 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
       // from memory (`src`: this thread's piece of its first row; the others by
       // their token or in order from `base`), columns below `cols`.
       auto send_tokens = [&](uint32_t dst, int nb, int rows, int first, int k, int64_t row_pitch,
-                             int cols, const uint16_t* src, const uint8_t* scale,
-                             const uint16_t* base, bool by_token) {
-        const int q = tid & 15;
-        const bool in = k * 128 + q * 8 < cols;
-        for (int i = tid >> 4; i < nb; i += 8) {
+                             int cols, const uint16_t* src, const uint16_t* base, bool by_token) {
+        const bool in = k * kStageK<MX> + piece * 8 < cols;
+        for (int i = r0; i < nb; i += 8) {
           if (i >= 8) {
             const int row = first + min(i, rows - 1);
-            src = base + (by_token ? int64_t(ls.token[row]) : int64_t(row)) * row_pitch + k * 128 + q * 8;
+            src = base + (by_token ? int64_t(ls.token[row]) : int64_t(row)) * row_pitch +
+                  k * kStageK<MX> + piece * 8;
           }
-          copy16(MX ? dst + 8192 + 512 + i * kMxTokenPitch + q * 16
-                    : dst + 32768 + tile_place(i, q, nb),
-                 in ? src : base, in && i < rows, keep);
+          copy16(dst + 32768 + tile_place(i, piece, nb), in ? src : base, in && i < rows, keep);
         }
-        if constexpr (MX)
-          if (tid < nb)
-            copy4(dst + 8192 + 512 + nb * kMxTokenPitch + tid * 4, scale, tid < rows);
       };
       int64_t at = at1;
       HiddenTile t;
@@ -628,37 +697,18 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
         const int64_t gate = int64_t(ls.active[t.a]) * a.w1_rows + t.i0;
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         const int nb = (rows + 7) / 8 * 8;
-        const int64_t pitch = MX ? a.hp / 2 : int64_t(a.H) * 2, up = a.I * pitch;   // bytes
+        const int64_t pitch = int64_t(a.H) * 2, up = a.I * pitch;   // bytes
         const uint8_t* src = a.w1 + (gate + r0) * pitch + piece * 16;
         const int left = t.n - r0;             // rows from this thread's first on
-        const uint8_t* scale = a.s1;
-        bool scaled = false;
-        if constexpr (MX) {
-          const int64_t row = gate + (tid & 63) + (tid >> 6) * int64_t(a.I);
-          scale += (row >> 7) * (a.hp / 128) * int64_t(512) + mx_scale_row(int(row & 127));
-          scaled = (tid & 63) < t.n;
-        }
-        const int64_t token = ls.token[first + min(tid >> 4, rows - 1)];
-        const uint16_t* tok = (MX ? a.xq + token * a.hp : a.x + token * a.x_stride) + (tid & 15) * 8;
-        const uint8_t* tok_scale =
-            a.xs + (MX ? int64_t(ls.token[first + min(tid, rows - 1)]) * (a.hp / 32) : 0);
+        const uint16_t* tok =
+            a.x + ls.token[first + min(r0, rows - 1)] * a.x_stride + piece * 8;
         for (int k = 0; k < k1; ++k) {
           ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
           if (!ok) break;
           const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
-          const uint32_t to = dst + place;
-          if constexpr (MX) {
-            if (left > 0) {
-              copy16(to, src, true, once);
-              copy16(to + 4096, src + up, true, once);
-            }
-            if (left > 32) {
-              copy16(to + 2048, src + 32 * pitch, true, once);
-              copy16(to + 6144, src + 32 * pitch + up, true, once);
-            }
-            if (scaled) copy4(dst + 8192 + tid * 4, scale, true);
-          } else {
-            const bool in = k * kStageK + piece * 8 < a.H;
+          {
+            const uint32_t to = dst + place;
+            const bool in = k * kStageK<MX> + piece * 8 < a.H;
             const uint8_t* from = in ? src : a.w1;
             const int64_t step = in ? 8 * pitch : 0, half = in ? up : 0;
 #pragma unroll
@@ -670,13 +720,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
               }
             }
           }
-          send_tokens(dst, nb, rows, first, k, MX ? a.hp : int64_t(a.x_stride),
-                      MX ? a.hp : a.H, tok, tok_scale, MX ? a.xq : a.x, true);
+          send_tokens(dst, nb, rows, first, k, a.x_stride, a.H, tok, a.x, true);
           copies_arrive(smem_u32(&full[stage]));
-          src += MX ? 64 : 256;
-          scale += 512;
-          tok += 128;
-          tok_scale += 4;
+          src += 256;
+          tok += kStageK<MX>;
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1;
@@ -690,28 +737,23 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
         OutputRun r;
         int k;
         bool more;
-        const uint8_t *src, *scale;      // weights, or a token's h and scales
+        const uint8_t* src;      // weights, or a row of h
       };
-      const int64_t pitch = MX ? a.ip / 2 : int64_t(a.I) * 2;
+      const int64_t pitch = int64_t(a.I) * 2;
       auto open = [&](Place& p, bool weights) {
         p.more = output_run(p.at, end2, active, k2, p.r);
         p.k = p.r.k0;
         if (!p.more) return;
         if (weights) {
           const int64_t row = int64_t(ls.active[p.r.a]) * a.w2_rows + p.r.rb * 128;
-          p.src = a.w2 + (row + r0) * pitch + piece * 16 + int64_t(p.k) * (MX ? 64 : 256);
-          if constexpr (MX)
-            p.scale = a.s2 + ((row >> 7) * (a.ip / 128) + p.k) * int64_t(512) + mx_scale_row(tid);
+          p.src = a.w2 + (row + r0) * pitch + piece * 16 + int64_t(p.k) * 256;
         } else {
           const int first = ls.first[p.r.a], rows = ls.first[p.r.a + 1] - first;
           p.src = reinterpret_cast<const uint8_t*>(
-              a.h + int64_t(first + min(tid >> 4, rows - 1)) * (MX ? a.ip : a.I) + (tid & 15) * 8 +
-              p.k * 128);
-          if constexpr (MX)
-            p.scale = a.hs + int64_t(first + min(tid, rows - 1)) * (a.ip / 32) + p.k * 4;
+              a.h + int64_t(first + min(r0, rows - 1)) * a.I + piece * 8 + p.k * kStageK<MX>);
         }
       };
-      Place w{at2, {}, 0, false, nullptr, nullptr}, v{at2, {}, 0, false, nullptr, nullptr};
+      Place w{at2, {}, 0, false, nullptr}, v{at2, {}, 0, false, nullptr};
       open(w, true);
       open(v, false);
       int w_stage = stage, ahead = 0;    // stages whose weights are under way
@@ -719,14 +761,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
       auto send_weights = [&]() {
         ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
         if (!ok) return;
-        const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes), to = dst + place;
-        if constexpr (MX) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) copy16(to + i * 2048, w.src + i * 32 * pitch, true, once);
-          copy4(dst + 8192 + tid * 4, w.scale, true);
-          w.scale += 512;
-        } else {
-          const bool in = w.k * kStageK + piece * 8 < a.I;
+        const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes);
+        {
+          const bool in = w.k * kStageK<MX> + piece * 8 < a.I;
+          const uint32_t to = dst + place;
           const uint8_t* from = in ? w.src : a.w2;
           const int64_t step = in ? 8 * pitch : 0;
           const int left = a.H - w.r.rb * 128 - r0;
@@ -738,7 +776,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
             }
           }
         }
-        w.src += MX ? 64 : 256;
+        w.src += 256;
         if (++w.k == w.r.k0 + w.r.n) open(w, true);
         ++ahead;
         if (++w_stage == a.stages) {
@@ -752,21 +790,137 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
         if (ahead == 0) send_weights();
         if (!ok) break;
         const int first = ls.first[v.r.a], rows = ls.first[v.r.a + 1] - first;
-        // (columns of h past I, or past its last block of 32, are not written)
         send_tokens(ring + uint32_t(stage * a.stage_bytes), (rows + 7) / 8 * 8, rows, first, v.k,
-                    MX ? a.ip : a.I, MX ? (a.I + 31) / 32 * 32 : a.I,
-                    reinterpret_cast<const uint16_t*>(v.src), v.scale, a.h, false);
+                    a.I, a.I, reinterpret_cast<const uint16_t*>(v.src), a.h, false);
         copies_arrive(smem_u32(&full[stage]));
         v.src += 256;
-        if constexpr (MX) v.scale += 4;
         if (++v.k == v.r.k0 + v.r.n) open(v, false);
         --ahead;
         if (++stage == a.stages) stage = 0;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
+    } else if (MX && warp == 0) {
+      // ----------------------------------------------------- copies, 4-bit
+      // All of a stage comes by bulk copies that one warp issues: the codes as
+      // boxes of 128 bytes x 32 or 128 rows, the scales as the blocks of 512 bytes
+      // they are kept in (two of a row of blocks, the last may be alone), a token
+      // (values and scales) as one piece.
+      const bool leader = lane == 0;
+      const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
+      const int64_t kb1 = a.hb, kb2 = a.ib;     // blocks of scales in a row of blocks
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int64_t at = at1;
+      HiddenTile t;
+      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+        const int gate = int(ls.active[t.a]) * a.w1_rows + t.i0, up = gate + a.I;
+        const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
+        // (rows past the tile's come along in whole boxes; nobody reads them)
+        const int boxes = (t.n + 31) / 32;
+        const int gb = ((gate & 127) + t.n + 127) >> 7, ub = ((up & 127) + t.n + 127) >> 7;
+        const uint8_t* gs = a.s1 + int64_t(gate >> 7) * kb1 * 512;
+        const uint8_t* us = a.s1 + int64_t(up >> 7) * kb1 * 512;
+        const uint8_t* tok0 = a.xq + int64_t(ls.token[first + min(lane, rows - 1)]) * kMxToken;
+        const uint8_t* tok1 = a.xq + int64_t(ls.token[first + min(lane + 32, rows - 1)]) * kMxToken;
+        for (int k = 0; k < k1; ++k) {
+          ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+          const uint32_t bar = smem_u32(&full[stage]);
+          if (leader) {
+            const uint32_t sb = kb1 - 2 * k > 1 ? 1024 : 512;
+            mbar_expect_tx(bar, uint32_t(boxes * 8192) + uint32_t(gb + ub) * sb);
+            mbar_expect_tx(bar, uint32_t(rows * kMxToken));
+            for (int i = 0; i < boxes; ++i) {
+              tc::load_2d(dst + i * 4096, &a.map_w1, bar, k * 128, gate + i * 32, once);
+              tc::load_2d(dst + 8192 + i * 4096, &a.map_w1, bar, k * 128, up + i * 32, once);
+            }
+            for (int i = 0; i < gb; ++i)
+              bulk_load_hint(dst + kMxScales + i * 1024, gs + (i * kb1 + 2 * k) * 512, sb, bar, once);
+            for (int i = 0; i < ub; ++i)
+              bulk_load_hint(dst + kMxScales + 2048 + i * 1024, us + (i * kb1 + 2 * k) * 512, sb,
+                             bar, once);
+          }
+          __syncwarp();   // (the expected bytes stand before the first that land)
+          const int64_t off = int64_t(k) * a.T * kMxToken;
+          if (lane < rows)
+            bulk_load_hint(dst + kMxTokens + lane * kMxToken, tok0 + off, kMxToken, bar, keep);
+          if (lane + 32 < rows)
+            bulk_load_hint(dst + kMxTokens + (lane + 32) * kMxToken, tok1 + off, kMxToken, bar, keep);
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // The second product: the weights of the first stages are on their way
+      // before the barrier, the tokens follow after it.
+      struct Place {
+        int64_t at;
+        OutputRun r;
+        int k;
+        bool more;
+      };
+      auto open = [&](Place& p) {
+        p.more = output_run(p.at, end2, active, k2, p.r);
+        p.k = p.r.k0;
+      };
+      Place w{at2, {}, 0, false}, v{at2, {}, 0, false};
+      open(w);
+      open(v);
+      int w_stage = stage, ahead = 0;    // stages whose weights are under way
+      uint32_t w_phase = phase;
+      auto send_weights = [&]() {
+        ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
+        if (!ok) return;
+        if (leader) {
+          const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes);
+          const uint32_t bar = smem_u32(&full[w_stage]);
+          const int row = int(ls.active[w.r.a]) * a.w2_rows + w.r.rb * 128;
+          const uint32_t sb = kb2 - 2 * w.k > 1 ? 1024 : 512;
+          mbar_expect_tx(bar, 16384 + sb);
+          tc::load_2d(dst, &a.map_w2, bar, w.k * 128, row, once);
+          bulk_load_hint(dst + kMxScales, a.s2 + (int64_t(row >> 7) * kb2 + 2 * w.k) * 512, sb, bar,
+                         once);
+        }
+        __syncwarp();
+        if (++w.k == w.r.k0 + w.r.n) open(w);
+        ++ahead;
+        if (++w_stage == a.stages) {
+          w_stage = 0;
+          w_phase ^= 1;
+        }
+      };
+      while (ok && w.more && ahead < a.stages) send_weights();
+      if (ok && v.more) {
+        ok = wait_grid(a.barrier + 1, uint32_t(G), abort_flag, a.status);
+        asm volatile("fence.proxy.async;" ::: "memory");   // h was written by threads
+      }
+      while (ok && v.more) {
+        if (ahead == 0) send_weights();
+        if (!ok) break;
+        const int first = ls.first[v.r.a], rows = ls.first[v.r.a + 1] - first;
+        if (leader) {
+          const uint32_t bar = smem_u32(&full[stage]);
+          mbar_expect_tx(bar, uint32_t(rows * kMxToken));
+          bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxTokens,
+                         a.hq + (int64_t(v.k) * a.h_rows + first) * kMxToken,
+                         uint32_t(rows * kMxToken), bar, keep);
+        }
+        __syncwarp();
+        if (++v.k == v.r.k0 + v.r.n) open(v);
+        --ahead;
+        if (++stage == a.stages) stage = 0;
+      }
+      if (!ok) {
+        // winding down: copies already issued land before the CTA exits
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < tc::kDrainNs) __nanosleep(1000);
+      }
     } else {
       // ---------------------------------------------------------- products
-      const int mw = (warp - kCopyWarps) & 7, kh = (warp - kCopyWarps) >> 3;
+      const int mw = (warp - kCopyWarps<MX>) & 7, kh = (warp - kCopyWarps<MX>) >> 3;
       const int mtid = threadIdx.x - kCopyThreads;
       const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
       int stage = 0;
@@ -774,7 +928,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
       float acc[NT][4];
       float* half_sums = yacc + a.T * kYPitch;   // [NT][8 warps][32 lanes][4]
       // `n` stages into acc; `work`: this warp's rows exist
-      auto products = [&](int n, int nt, int lo, int hi, bool work) {
+      auto products = [&](auto second, int n, int nt, int lo, int hi, uint32_t scale0,
+                          uint32_t scale1, int blocks, bool work) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -786,7 +941,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
           if (work) {
             const uint32_t at = ring + uint32_t(stage * a.stage_bytes);
             if constexpr (MX)
-              stage_mx<NT, KS>(at, lo, hi, kh, nt, acc);
+              stage_mx<NT, KS, decltype(second)::value != 0>(at, lo + g, hi + g, scale0, scale1,
+                                                             kh, nt, blocks - 8 * k, acc);
             else
               stage_bf16<NT, KS>(at, lo, hi, kh, nt, acc);
           }
@@ -824,15 +980,28 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
       while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         const int nb = (rows + 7) / 8 * 8;
-        ok = products(k1, nb / 8, mw * 8, 64 + mw * 8, mw * 8 < t.n);
-        if (!ok) break;
+        // a 4-bit row's scales: in the blocks of the tile's gate or up rows
         const int p = mw * 8 + g;                 // this thread's hidden row
+        const int gr = (t.i0 & 127) + p, ur = ((t.i0 + a.I) & 127) + p;
+        ok = products(Const<0>{}, k1, nb / 8, mw * 8, 64 + mw * 8,
+                      kMxScales + (gr >> 7) * 1024 + mx_scale_row(gr & 127),
+                      kMxScales + 2048 + (ur >> 7) * 1024 + mx_scale_row(ur & 127),
+                      (a.H + 31) / 32, mw * 8 < t.n);
+        if (!ok) break;
         float h[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
+          {
+            if constexpr (MX) {   // the token's scale
+              const int i = min(j * 8 + c2 + e, rows - 1);
+              const float u = __ldcg(a.x_scale + ls.token[first + i]);
+              acc[j][e] *= u;
+              acc[j][e + 2] *= u;
+            }
             h[j][e] = p < t.n ? activate(acc[j][e], a.act) * acc[j][e + 2] : 0.0f;
+          }
         if constexpr (MX) {
           // 32 hidden rows, those of four warps, share a scale
           uint32_t* top = reinterpret_cast<uint32_t*>(yacc);   // [8 warps][nb]
@@ -856,9 +1025,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
               const uint32_t s = half_scale(max(max(m[0], m[nb]), max(m[2 * nb], m[3 * nb])));
               const int64_t row = first + i;
               if ((mw & 4) * 8 < t.n) {           // (a whole block, zeros past I)
-                a.h[row * a.ip + t.i0 + p] = half_value(h[j][e], s);
-                if ((mw & 3) == 0 && g == 0)
-                  a.hs[row * (a.ip / 32) + (t.i0 + p) / 32] = uint8_t(s);
+                const int col = t.i0 + p;
+                uint8_t* to = a.hq + (int64_t(col >> 8) * a.h_rows + row) * kMxToken;
+                reinterpret_cast<uint16_t*>(to)[col & 255] = half_value(h[j][e], s);
+                if ((mw & 3) == 0 && g == 0) to[512 + ((col & 255) >> 5)] = uint8_t(s);
               }
             }
         } else if (p < t.n) {
@@ -875,6 +1045,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
       }
       // this CTA's hidden values are written
       __threadfence();
+      if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
       math_sync<kMathThreads>();
       if (mtid == 0) {
         uint32_t old;
@@ -942,7 +1113,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
           for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
         }
         const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
-        ok = products(r.n, (rows + 7) / 8, mw * 16, mw * 16 + 8, rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
+        ok = products(Const<1>{}, r.n, (rows + 7) / 8, mw * 16, mw * 16 + 8,
+                      kMxScales + mx_scale_row(mw * 16 + g),
+                      kMxScales + mx_scale_row(mw * 16 + 8 + g), (a.I + 31) / 32 - 8 * r.k0,
+                      rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -972,16 +1146,16 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const FewArgs 
 }
 
 struct Layout {
-  int64_t done, logits, h, xq, xs, hs, parts, bytes;
+  int64_t done, logits, h, x_scale, xq, hq, parts, bytes;
   int hp, ip, row_blocks;
 };
 
 Layout layout_of(const fo_moe_few_desc& d) {
   Layout l{};
   const int64_t pairs = int64_t(d.tokens) * d.top_k;
-  l.hp = int(mx_up(d.hidden, 128));
-  l.ip = int(mx_up(d.inter, 128));
-  l.row_blocks = l.hp / 128;
+  l.hp = int(mx_up(d.hidden, kStageK<true>));
+  l.ip = int(mx_up(d.inter, kStageK<true>));
+  l.row_blocks = int(mx_up(d.hidden, 128) / 128);
   int64_t at = 256;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -995,10 +1169,9 @@ Layout layout_of(const fo_moe_few_desc& d) {
   if (d.weights == FO_TYPE_BF16) {
     l.h = take(2 * pairs * d.inter);
   } else {
-    l.xq = take(2 * int64_t(d.tokens) * l.hp);
-    l.xs = take(int64_t(d.tokens) * (l.hp / 32));
-    l.h = take(2 * pairs * l.ip);
-    l.hs = take(pairs * (l.ip / 32));
+    l.x_scale = take(4 * int64_t(d.tokens));
+    l.xq = take(int64_t(d.tokens) * (l.hp / kStageK<true>) * kMxToken);
+    l.hq = take(pairs * (l.ip / kStageK<true>) * kMxToken);
   }
   l.parts = take(4 * int64_t(kMaxCtas + l.row_blocks) * d.tokens * 128);
   l.bytes = at;
@@ -1073,30 +1246,39 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.renormalize = d.renormalize;
   a.act = d.act;
   a.w1_rows = mx ? int(mx_up(2 * int64_t(d.inter), 128)) : 2 * d.inter;
-  a.w2_rows = mx ? l.hp : d.hidden;
+  a.w2_rows = mx ? l.row_blocks * 128 : d.hidden;
   a.barrier = reinterpret_cast<uint32_t*>(ws);
   a.done = reinterpret_cast<int32_t*>(ws + l.done);
   a.logits = reinterpret_cast<float*>(ws + l.logits);
   a.h = reinterpret_cast<uint16_t*>(ws + l.h);
-  a.xq = reinterpret_cast<uint16_t*>(ws + l.xq);
-  a.xs = ws + l.xs, a.hs = ws + l.hs;
+  a.x_scale = reinterpret_cast<float*>(ws + l.x_scale);
+  a.xq = ws + l.xq, a.hq = ws + l.hq;
+  a.h_rows = d.tokens * d.top_k;
   a.hp = l.hp, a.ip = l.ip;
+  a.hb = int(mx_up(d.hidden, 128) / 128), a.ib = int(mx_up(d.inter, 128) / 128);
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
   // an expert's tokens: all of them at most
   const int nb = int(mx_up(d.tokens, 8));
-  a.stage_bytes = int(mx_up(mx ? 8192 + 512 + nb * (kMxTokenPitch + 4) : 32768 + nb * 256, 128));
+  a.stage_bytes = int(mx_up(mx ? kMxTokens + nb * kMxToken : 32768 + nb * 256, 1024));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
   // the outputs' sums, then the halves of K on their way (where split)
   const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 8192 : 0);
-  const int tail = lists + y_bytes + kBarBytes + 128;
+  const int tail = lists + y_bytes + kBarBytes + 1024;
   a.stages = (kSmemLimit - tail) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   if (a.stages < 2) return FO_ERR_UNSUPPORTED;
   a.off_lists = a.stages * a.stage_bytes;
   a.off_y = a.off_lists + lists;
   a.off_bar = a.off_y + y_bytes;
-  const int smem = a.off_bar + kBarBytes + 128;
+  const int smem = a.off_bar + kBarBytes + 1024;
+  if (mx && (!encode_tensor_map(&a.map_w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, W1, uint64_t(a.hb) * 64,
+                                uint64_t(a.w1_rows) * d.experts, uint64_t(a.hb) * 64, 128, 32,
+                                CU_TENSOR_MAP_SWIZZLE_128B) ||
+             !encode_tensor_map(&a.map_w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, W2, uint64_t(a.ib) * 64,
+                                uint64_t(a.w2_rows) * d.experts, uint64_t(a.ib) * 64, 128, 128,
+                                CU_TENSOR_MAP_SWIZZLE_128B)))
+    return FO_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return mx ? launch_n<true>(a, grid, smem, st) : launch_n<false>(a, grid, smem, st);
 }
