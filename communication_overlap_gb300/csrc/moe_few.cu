@@ -46,12 +46,13 @@ constexpr int kMaxCtas = 160;
 constexpr int kMaxRowBlocks = 4096;     // blocks of 128 output rows
 constexpr int kMaxStages = 16;
 constexpr int kSmemLimit = 232448;
+constexpr int kCopyWarps = 4;
 constexpr int kYPitch = 132;            // floats per token of the outputs' sums
 // Columns of the weights per stage: 256 bytes of a bf16 row, 128 of a 4-bit one.
 template <bool MX>
 constexpr int kStageK = MX ? 256 : 128;
 // A token's share of a 4-bit stage, in memory and in shared memory: 256 f16
-// values, their eight scale bytes, and what shifts the next token by 16 banks.
+// values, their eight scales (fp32), and what shifts the next token by 16 banks.
 constexpr int kMxToken = 576;
 constexpr int kMxScales = 16384, kMxTokens = kMxScales + 4096;   // offsets in a stage
 
@@ -64,7 +65,7 @@ struct Const {
 __device__ __forceinline__ int64_t part(int64_t n, int c, int g) { return n * c / g; }
 
 struct FewArgs {
-  CUtensorMap map_w1, map_w2;   // 4-bit: boxes of 128 bytes x 32 and 128 rows
+  CUtensorMap map_w1[2], map_w2;   // 4-bit: boxes of 128 bytes x 32, 64 and 64 rows
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* router;
@@ -93,6 +94,7 @@ struct FewArgs {
 struct Lists {
   float* weight;      // [P] weight of row r (rows sorted by expert, token, slot)
   float* pair_weight; // [P]
+  float* x_scale;     // [P] 4-bit: scale of row r's token
   int16_t* token;     // [P] token of row r
   int16_t* id;        // [P] expert of pair (token, slot)
   int16_t* active;    // [E] experts that have rows
@@ -103,14 +105,15 @@ __device__ __forceinline__ Lists lists_at(uint8_t* p, int P, int E) {
   Lists l;
   l.weight = reinterpret_cast<float*>(p);
   l.pair_weight = l.weight + P;
-  l.token = reinterpret_cast<int16_t*>(l.pair_weight + P);
+  l.x_scale = l.pair_weight + P;
+  l.token = reinterpret_cast<int16_t*>(l.x_scale + P);
   l.id = l.token + P;
   l.active = l.id + P;
   l.first = l.active + E;
   return l;
 }
 
-__host__ inline int lists_bytes(int P, int E) { return (12 * P + 4 * E + 2 + 127) / 128 * 128; }
+__host__ inline int lists_bytes(int P, int E) { return (16 * P + 4 * E + 2 + 127) / 128 * 128; }
 
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == FO_ACT_NONE) return g;
@@ -186,26 +189,28 @@ __device__ __forceinline__ uint16_t half_value(float v, uint32_t s) {
   return __half_as_ushort(__float2half_rn(v * __uint_as_float((254u - s) << 23)));
 }
 
-// x as f16 with one scale per token, a warp per token (the last CTAs': the
-// first have the router), zeros past H; and zeros for h past its last block of
-// 32 columns.
-__device__ void scale_x(const FewArgs& a) {
-  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  const int64_t slot = int64_t(threadIdx.x / 32) * gridDim.x + (gridDim.x - 1 - blockIdx.x);
-  const int64_t slots = int64_t(warps) * gridDim.x;
-  for (int64_t t = slot; t < a.T; t += slots) {
+// x as f16 with one scale per token, a CTA per token (from the last CTA on: the
+// first have the router), zeros past H; and zeros (of scale 1) for h past its
+// last block of 32 columns.  `red`: a word per warp.
+__device__ void scale_x(const FewArgs& a, uint32_t* red) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const int from_last = int(gridDim.x) - 1 - int(blockIdx.x);
+  for (int t = from_last; t < a.T; t += int(gridDim.x)) {
     const uint16_t* x = a.x + t * a.x_stride;
     uint32_t m = 0;
-#pragma unroll 4
-    for (int c = lane * 8; c < a.H; c += 256) {
+    for (int c = threadIdx.x * 8; c < a.H; c += blockDim.x * 8) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
     }
-    const uint32_t s = half_scale(__reduce_max_sync(0xffffffffu, m) << 16);
-#pragma unroll 2
-    for (int c = lane * 8; c < a.hp; c += 256) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    __syncthreads();
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, lane < warps ? red[lane] : 0u);
+    const uint32_t s = half_scale(m << 16);
+    for (int c = threadIdx.x * 8; c < a.hp; c += blockDim.x * 8) {
       const uint4 v = c < a.H ? __ldg(reinterpret_cast<const uint4*>(x + c)) : make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t o[4];
@@ -215,15 +220,17 @@ __device__ void scale_x(const FewArgs& a) {
       *reinterpret_cast<uint4*>(a.xq + (int64_t(c >> 8) * a.T + t) * kMxToken + (c & 255) * 2) =
           make_uint4(o[0], o[1], o[2], o[3]);
     }
-    if (lane == 0) a.x_scale[t] = s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
+    if (threadIdx.x == 0)
+      a.x_scale[t] = s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
   }
   const int used = (a.I + 31) / 32 * 32;
-  for (int64_t r = slot; r < int64_t(a.T) * a.K; r += slots)
-    for (int c = used + lane; c < a.ip; c += 32) {
-      uint8_t* to = a.hq + (int64_t(c >> 8) * a.h_rows + r) * kMxToken;
-      reinterpret_cast<uint16_t*>(to)[c & 255] = 0;
-      if (lane == 0) to[512 + ((c & 255) >> 5)] = 1;
-    }
+  if (used < a.ip)
+    for (int r = from_last * warps + warp; r < a.T * a.K; r += int(gridDim.x) * warps)
+      for (int c = used + lane; c < a.ip; c += 32) {
+        uint8_t* to = a.hq + (int64_t(c >> 8) * a.h_rows + r) * kMxToken;
+        reinterpret_cast<uint16_t*>(to)[c & 255] = 0;
+        if (lane == 0) reinterpret_cast<float*>(to + 512)[(c & 255) >> 5] = 1.0f;
+      }
 }
 
 // ------------------------------------------------------------------ work items
@@ -345,12 +352,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 template <int THREADS>
 __device__ __forceinline__ void math_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -440,13 +441,14 @@ __device__ __forceinline__ float scale_of(uint32_t w, int b) {
 // 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
 // codes of a row (one word) and the same 8 columns of a token (16 bytes); which
 // of the MMA's 16 columns they stand in does not matter as long as both agree.
-// row0, row1: the thread's rows; scale0, scale1: where their scales are;
-// blocks: of the stage's eight, those that exist.  TOKEN_SCALES: the tokens'
-// values have a scale per block, too.
+// code: the thread's word of each block in its first row; row1: from there to
+// its second; scale0, scale1: where their scales are; blocks: of the stage's
+// eight, those that exist.  TOKEN_SCALES: the tokens' values have a scale per
+// block, too.
 template <int NT, int KS, bool TOKEN_SCALES>
-__device__ __forceinline__ void stage_mx(uint32_t stage, int row0, int row1, uint32_t scale0,
-                                         uint32_t scale1, int kh, int nt, int blocks,
-                                         float (&acc)[NT][4]) {
+__device__ __forceinline__ void stage_mx(uint32_t stage, const uint32_t (&code)[8 / KS],
+                                         uint32_t row1, uint32_t scale0, uint32_t scale1, int kh,
+                                         int nt, int blocks, float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, c = lane & 3;
   const uint32_t tokens = stage + kMxTokens + uint32_t(lane >> 2) * kMxToken + c * 16;
   const uint32_t token_scales = stage + kMxTokens + uint32_t(c * 2) * kMxToken + 512;
@@ -457,8 +459,8 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, int row0, int row1, uin
     uint32_t w0[4], w1[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      w0[b] = lds32(stage + code_place(row0, q * 4 + b) + c * 4);
-      w1[b] = lds32(stage + code_place(row1, q * 4 + b) + c * 4);
+      w0[b] = lds32(stage + code[q4 * 4 + b]);
+      w1[b] = lds32(stage + code[q4 * 4 + b] + row1);
     }
     const uint32_t sw0 = lds32(stage + scale0 + q * 512), sw1 = lds32(stage + scale1 + q * 512);
     float s0[4], s1[4];
@@ -476,16 +478,14 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, int row0, int row1, uin
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
-      uint32_t t[4][4];
+      uint32_t t[4][4], u0[4], u1[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         lds128(tokens + uint32_t(j * 8) * kMxToken + (q * 4 + b) * 64, t[b]);
-      uint32_t v0 = 0, v1 = 0;
       if constexpr (TOKEN_SCALES) {
-        v0 = lds32(token_scales + uint32_t(j * 8) * kMxToken + q * 4);
-        v1 = lds32(token_scales + uint32_t(j * 8 + 1) * kMxToken + q * 4);
+        lds128(token_scales + uint32_t(j * 8) * kMxToken + q * 16, u0);
+        lds128(token_scales + uint32_t(j * 8 + 1) * kMxToken + q * 16, u1);
       }
-      uint64_t lo = pack2(acc[j][0], acc[j][1]), hi = pack2(acc[j][2], acc[j][3]);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         uint32_t p[4], r[4];
@@ -494,19 +494,17 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, int row0, int row1, uin
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         mma16816<true>(d, p[0], r[0], p[1], r[1], t[b][0], t[b][1]);
         mma16816<true>(d, p[2], r[2], p[3], r[3], t[b][2], t[b][3]);
-        uint64_t d0 = pack2(d[0], d[1]), d1 = pack2(d[2], d[3]);
         if constexpr (TOKEN_SCALES) {
-          // (a token's scale byte is never 0, and 255 comes with zeros, which
-          // infinity makes NaN)
-          const uint64_t u = pack2(scale_of(v0, b), scale_of(v1, b));
-          d0 = mul2(d0, u);
-          d1 = mul2(d1, u);
+          uint64_t lo = pack2(d[0], d[1]), hi = pack2(d[2], d[3]);
+          const uint64_t u = pack2(__uint_as_float(u0[b]), __uint_as_float(u1[b]));
+          unpack2(mul2(lo, u), d[0], d[1]);
+          unpack2(mul2(hi, u), d[2], d[3]);
         }
-        lo = fma2(d0, pack2(s0[b], s0[b]), lo);
-        hi = fma2(d1, pack2(s1[b], s1[b]), hi);
+        acc[j][0] = fmaf(d[0], s0[b], acc[j][0]);
+        acc[j][1] = fmaf(d[1], s0[b], acc[j][1]);
+        acc[j][2] = fmaf(d[2], s1[b], acc[j][2]);
+        acc[j][3] = fmaf(d[3], s1[b], acc[j][3]);
       }
-      unpack2(lo, acc[j][0], acc[j][1]);
-      unpack2(hi, acc[j][2], acc[j][3]);
     }
   }
 }
@@ -519,17 +517,13 @@ constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
 // 400), so it wants the second set; with many tokens its registers do not fit.
 template <bool MX, int NT>
 constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
-// Copying warps: one that issues bulk copies, or four that copy 16 bytes a
-// thread.
-template <bool MX>
-constexpr int kCopyWarps = MX ? 1 : 4;
 template <bool MX, int NT>
-constexpr int kThreads = 32 * kCopyWarps<MX> + 256 * kSplit<MX, NT>;
+constexpr int kThreads = 32 * kCopyWarps + 256 * kSplit<MX, NT>;
 
 // NT: tiles of 8 tokens, at most.
 template <bool MX, int NT>
 __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int kCopyThreads = 32 * kCopyWarps<MX>;
+  constexpr int kCopyThreads = 32 * kCopyWarps;
   constexpr int KS = kSplit<MX, NT>, kMathThreads = 256 * KS, kWarps = kThreads<MX, NT> / 32;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment, for the copies' swizzle
@@ -551,7 +545,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&full[s]), MX ? 2 : kCopyThreads);   // 4-bit: weights, tokens
+      mbar_init(smem_u32(&full[s]), MX ? kCopyWarps : kCopyThreads);
       mbar_init(smem_u32(&empty[s]), 8 * KS);
     }
     *abort_flag = 0;
@@ -563,7 +557,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     const int eb = (a.E + 3) / 4, tb = (a.T + 7) / 8;
     for (int u = c; u < eb * tb; u += G)
       router_block(a, u % eb * 4, u / eb * 8, reinterpret_cast<float*>(smem));
-    if constexpr (MX) scale_x(a);
+    if constexpr (MX) scale_x(a, reinterpret_cast<uint32_t*>(smem) + 1024);
   }
   __threadfence();
   if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
@@ -642,6 +636,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           const int row = count[e] + rank;
           ls.token[row] = int16_t(p / a.K);
           ls.weight[row] = ls.pair_weight[p];
+          if constexpr (MX) ls.x_scale[row] = __ldcg(a.x_scale + p / a.K);
         }
         __syncwarp();
         if (e >= 0 && rank == 0) count[e] += __popc(same);
@@ -663,7 +658,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     const int64_t at2 = part(n2, c, G), end2 = part(n2, c + 1, G);
     const uint32_t ring = smem_u32(smem);
 
-    if (!MX && warp < kCopyWarps<MX>) {
+    if (!MX && warp < kCopyWarps) {
       // ------------------------------------------------------ copies, bf16
       // A thread has rows r0, r0 + 8, ... of a stage, one of the 16 pieces of 16
       // bytes of each.
@@ -799,119 +794,120 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         if (++stage == a.stages) stage = 0;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
-    } else if (MX && warp == 0) {
+    } else if (MX && warp < kCopyWarps) {
       // ----------------------------------------------------- copies, 4-bit
-      // All of a stage comes by bulk copies that one warp issues: the codes as
-      // boxes of 128 bytes x 32 or 128 rows, the scales as the blocks of 512 bytes
-      // they are kept in (two of a row of blocks, the last may be alone), a token
-      // (values and scales) as one piece.
+      // All of a stage comes by bulk copies, from four warps: codes of the first
+      // and of the second 64 rows (boxes of 128 bytes x 64 rows), scales (blocks
+      // of 512 bytes as they are kept, two of a row of blocks, the last may be
+      // alone), tokens (values and scales in one piece).  Each walks the stages
+      // by itself; one warp for all needs 1800 cycles for a stage.
       const bool leader = lane == 0;
       const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
       const int64_t kb1 = a.hb, kb2 = a.ib;     // blocks of scales in a row of blocks
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      auto begin = [&]() {
+        ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
+        return ok;
+      };
+      auto end = [&]() {
+        __syncwarp();
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
       int64_t at = at1;
       HiddenTile t;
       while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
         const int gate = int(ls.active[t.a]) * a.w1_rows + t.i0, up = gate + a.I;
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
-        // (rows past the tile's come along in whole boxes; nobody reads them)
-        const int boxes = (t.n + 31) / 32;
-        const int gb = ((gate & 127) + t.n + 127) >> 7, ub = ((up & 127) + t.n + 127) >> 7;
-        const uint8_t* gs = a.s1 + int64_t(gate >> 7) * kb1 * 512;
-        const uint8_t* us = a.s1 + int64_t(up >> 7) * kb1 * 512;
-        const uint8_t* tok0 = a.xq + int64_t(ls.token[first + min(lane, rows - 1)]) * kMxToken;
-        const uint8_t* tok1 = a.xq + int64_t(ls.token[first + min(lane + 32, rows - 1)]) * kMxToken;
-        for (int k = 0; k < k1; ++k) {
-          ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
-          if (!ok) break;
-          const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
-          const uint32_t bar = smem_u32(&full[stage]);
-          if (leader) {
-            const uint32_t sb = kb1 - 2 * k > 1 ? 1024 : 512;
-            mbar_expect_tx(bar, uint32_t(boxes * 8192) + uint32_t(gb + ub) * sb);
-            mbar_expect_tx(bar, uint32_t(rows * kMxToken));
-            for (int i = 0; i < boxes; ++i) {
-              tc::load_2d(dst + i * 4096, &a.map_w1, bar, k * 128, gate + i * 32, once);
-              tc::load_2d(dst + 8192 + i * 4096, &a.map_w1, bar, k * 128, up + i * 32, once);
+        if (warp < 2) {
+          // (rows past the tile's come along in whole boxes; nobody reads them)
+          const CUtensorMap* map = t.n > 32 ? &a.map_w1[1] : &a.map_w1[0];
+          const int row = warp ? up : gate;
+          const uint32_t bytes = t.n > 32 ? 8192 : 4096;
+          for (int k = 0; k < k1 && begin(); ++k, end())
+            if (leader) {
+              mbar_expect_tx(smem_u32(&full[stage]), bytes);
+              tc::load_2d(ring + uint32_t(stage * a.stage_bytes + warp * 8192), map,
+                          smem_u32(&full[stage]), k * 128, row, once);
             }
-            for (int i = 0; i < gb; ++i)
-              bulk_load_hint(dst + kMxScales + i * 1024, gs + (i * kb1 + 2 * k) * 512, sb, bar, once);
-            for (int i = 0; i < ub; ++i)
-              bulk_load_hint(dst + kMxScales + 2048 + i * 1024, us + (i * kb1 + 2 * k) * 512, sb,
-                             bar, once);
+        } else if (warp == 2) {
+          const int gb = ((gate & 127) + t.n + 127) >> 7, ub = ((up & 127) + t.n + 127) >> 7;
+          const uint8_t* gs = a.s1 + int64_t(gate >> 7) * kb1 * 512;
+          const uint8_t* us = a.s1 + int64_t(up >> 7) * kb1 * 512;
+          for (int k = 0; k < k1 && begin(); ++k, end()) {
+            if (leader) {
+              const uint32_t sb = kb1 - 2 * k > 1 ? 1024 : 512, bar = smem_u32(&full[stage]);
+              const uint32_t dst = ring + uint32_t(stage * a.stage_bytes) + kMxScales;
+              mbar_expect_tx(bar, uint32_t(gb + ub) * sb);
+              bulk_load_hint(dst, gs, sb, bar, once);
+              if (gb > 1) bulk_load_hint(dst + 1024, gs + kb1 * 512, sb, bar, once);
+              bulk_load_hint(dst + 2048, us, sb, bar, once);
+              if (ub > 1) bulk_load_hint(dst + 3072, us + kb1 * 512, sb, bar, once);
+            }
+            gs += 1024;
+            us += 1024;
           }
-          __syncwarp();   // (the expected bytes stand before the first that land)
-          const int64_t off = int64_t(k) * a.T * kMxToken;
-          if (lane < rows)
-            bulk_load_hint(dst + kMxTokens + lane * kMxToken, tok0 + off, kMxToken, bar, keep);
-          if (lane + 32 < rows)
-            bulk_load_hint(dst + kMxTokens + (lane + 32) * kMxToken, tok1 + off, kMxToken, bar, keep);
-          if (++stage == a.stages) {
-            stage = 0;
-            phase ^= 1;
+        } else {
+          const uint8_t* tok0 = a.xq + int64_t(ls.token[first + min(lane, rows - 1)]) * kMxToken;
+          const uint8_t* tok1 = a.xq + int64_t(ls.token[first + min(lane + 32, rows - 1)]) * kMxToken;
+          const int64_t step = int64_t(a.T) * kMxToken;
+          for (int k = 0; k < k1 && begin(); ++k, end()) {
+            const uint32_t bar = smem_u32(&full[stage]);
+            const uint32_t dst = ring + uint32_t(stage * a.stage_bytes) + kMxTokens + lane * kMxToken;
+            if (leader) mbar_expect_tx(bar, uint32_t(rows * kMxToken));
+            __syncwarp();   // (the expected bytes stand before the first that land)
+            if (lane < rows) bulk_load_hint(dst, tok0, kMxToken, bar, keep);
+            if (lane + 32 < rows) bulk_load_hint(dst + 32 * kMxToken, tok1, kMxToken, bar, keep);
+            tok0 += step;
+            tok1 += step;
           }
         }
       }
       // The second product: the weights of the first stages are on their way
       // before the barrier, the tokens follow after it.
-      struct Place {
-        int64_t at;
-        OutputRun r;
-        int k;
-        bool more;
-      };
-      auto open = [&](Place& p) {
-        p.more = output_run(p.at, end2, active, k2, p.r);
-        p.k = p.r.k0;
-      };
-      Place w{at2, {}, 0, false}, v{at2, {}, 0, false};
-      open(w);
-      open(v);
-      int w_stage = stage, ahead = 0;    // stages whose weights are under way
-      uint32_t w_phase = phase;
-      auto send_weights = [&]() {
-        ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
-        if (!ok) return;
-        if (leader) {
-          const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes);
-          const uint32_t bar = smem_u32(&full[w_stage]);
-          const int row = int(ls.active[w.r.a]) * a.w2_rows + w.r.rb * 128;
-          const uint32_t sb = kb2 - 2 * w.k > 1 ? 1024 : 512;
-          mbar_expect_tx(bar, 16384 + sb);
-          tc::load_2d(dst, &a.map_w2, bar, w.k * 128, row, once);
-          bulk_load_hint(dst + kMxScales, a.s2 + (int64_t(row >> 7) * kb2 + 2 * w.k) * 512, sb, bar,
-                         once);
-        }
-        __syncwarp();
-        if (++w.k == w.r.k0 + w.r.n) open(w);
-        ++ahead;
-        if (++w_stage == a.stages) {
-          w_stage = 0;
-          w_phase ^= 1;
-        }
-      };
-      while (ok && w.more && ahead < a.stages) send_weights();
-      if (ok && v.more) {
+      if (ok && warp == 3 && at2 < end2) {
         ok = wait_grid(a.barrier + 1, uint32_t(G), abort_flag, a.status);
         asm volatile("fence.proxy.async;" ::: "memory");   // h was written by threads
       }
-      while (ok && v.more) {
-        if (ahead == 0) send_weights();
-        if (!ok) break;
-        const int first = ls.first[v.r.a], rows = ls.first[v.r.a + 1] - first;
-        if (leader) {
-          const uint32_t bar = smem_u32(&full[stage]);
-          mbar_expect_tx(bar, uint32_t(rows * kMxToken));
-          bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxTokens,
-                         a.hq + (int64_t(v.k) * a.h_rows + first) * kMxToken,
-                         uint32_t(rows * kMxToken), bar, keep);
+      at = at2;
+      OutputRun r;
+      while (ok && output_run(at, end2, active, k2, r)) {
+        const int row = int(ls.active[r.a]) * a.w2_rows + r.rb * 128;
+        const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
+        if (warp < 2) {
+          for (int k = r.k0; k < r.k0 + r.n && begin(); ++k, end())
+            if (leader) {
+              mbar_expect_tx(smem_u32(&full[stage]), 8192);
+              tc::load_2d(ring + uint32_t(stage * a.stage_bytes + warp * 8192), &a.map_w2,
+                          smem_u32(&full[stage]), k * 128, row + warp * 64, once);
+            }
+        } else if (warp == 2) {
+          const uint8_t* src = a.s2 + (int64_t(row >> 7) * kb2 + 2 * r.k0) * 512;
+          for (int k = r.k0; k < r.k0 + r.n && begin(); ++k, end()) {
+            if (leader) {
+              const uint32_t sb = kb2 - 2 * k > 1 ? 1024 : 512, bar = smem_u32(&full[stage]);
+              mbar_expect_tx(bar, sb);
+              bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxScales, src, sb, bar, once);
+            }
+            src += 1024;
+          }
+        } else {
+          const uint8_t* src = a.hq + (int64_t(r.k0) * a.h_rows + first) * kMxToken;
+          const uint32_t bytes = uint32_t(rows * kMxToken);
+          for (int k = r.k0; k < r.k0 + r.n && begin(); ++k, end()) {
+            if (leader) {
+              const uint32_t bar = smem_u32(&full[stage]);
+              mbar_expect_tx(bar, bytes);
+              bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxTokens, src, bytes, bar,
+                             keep);
+            }
+            src += int64_t(a.h_rows) * kMxToken;
+          }
         }
-        __syncwarp();
-        if (++v.k == v.r.k0 + v.r.n) open(v);
-        --ahead;
-        if (++stage == a.stages) stage = 0;
       }
       if (!ok) {
         // winding down: copies already issued land before the CTA exits
@@ -920,7 +916,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       }
     } else {
       // ---------------------------------------------------------- products
-      const int mw = (warp - kCopyWarps<MX>) & 7, kh = (warp - kCopyWarps<MX>) >> 3;
+      const int mw = (warp - kCopyWarps) & 7, kh = (warp - kCopyWarps) >> 3;
       const int mtid = threadIdx.x - kCopyThreads;
       const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
       int stage = 0;
@@ -934,6 +930,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        uint32_t code[8 / KS];               // 4-bit: places of a thread's words
+#pragma unroll
+        for (int b = 0; b < 8 / KS; ++b)
+          code[b] = code_place(lo + g, kh * (8 / KS) + b) + (lane & 3) * 4;
         bool ok = true;
         for (int k = 0; k < n; ++k) {
           ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
@@ -941,8 +941,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           if (work) {
             const uint32_t at = ring + uint32_t(stage * a.stage_bytes);
             if constexpr (MX)
-              stage_mx<NT, KS, decltype(second)::value != 0>(at, lo + g, hi + g, scale0, scale1,
-                                                             kh, nt, blocks - 8 * k, acc);
+              stage_mx<NT, KS, decltype(second)::value != 0>(at, code, uint32_t(hi - lo) * 128,
+                                                             scale0, scale1, kh, nt,
+                                                             blocks - 8 * k, acc);
             else
               stage_bf16<NT, KS>(at, lo, hi, kh, nt, acc);
           }
@@ -996,7 +997,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           {
             if constexpr (MX) {   // the token's scale
               const int i = min(j * 8 + c2 + e, rows - 1);
-              const float u = __ldcg(a.x_scale + ls.token[first + i]);
+              const float u = ls.x_scale[first + i];
               acc[j][e] *= u;
               acc[j][e + 2] *= u;
             }
@@ -1028,7 +1029,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                 const int col = t.i0 + p;
                 uint8_t* to = a.hq + (int64_t(col >> 8) * a.h_rows + row) * kMxToken;
                 reinterpret_cast<uint16_t*>(to)[col & 255] = half_value(h[j][e], s);
-                if ((mw & 3) == 0 && g == 0) to[512 + ((col & 255) >> 5)] = uint8_t(s);
+                if ((mw & 3) == 0 && g == 0)
+                  reinterpret_cast<float*>(to + 512)[(col & 255) >> 5] =
+                      s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
               }
             }
         } else if (p < t.n) {
@@ -1272,12 +1275,14 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.off_y = a.off_lists + lists;
   a.off_bar = a.off_y + y_bytes;
   const int smem = a.off_bar + kBarBytes + 1024;
-  if (mx && (!encode_tensor_map(&a.map_w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, W1, uint64_t(a.hb) * 64,
-                                uint64_t(a.w1_rows) * d.experts, uint64_t(a.hb) * 64, 128, 32,
-                                CU_TENSOR_MAP_SWIZZLE_128B) ||
-             !encode_tensor_map(&a.map_w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, W2, uint64_t(a.ib) * 64,
-                                uint64_t(a.w2_rows) * d.experts, uint64_t(a.ib) * 64, 128, 128,
-                                CU_TENSOR_MAP_SWIZZLE_128B)))
+  const auto box = [&](CUtensorMap* map, const void* base, int rows, int blocks, uint32_t height) {
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, uint64_t(blocks) * 64,
+                             uint64_t(rows) * d.experts, uint64_t(blocks) * 64, 128, height,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (mx && (!box(&a.map_w1[0], W1, a.w1_rows, a.hb, 32) ||
+             !box(&a.map_w1[1], W1, a.w1_rows, a.hb, 64) ||
+             !box(&a.map_w2, W2, a.w2_rows, a.ib, 64)))
     return FO_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return mx ? launch_n<true>(a, grid, smem, st) : launch_n<false>(a, grid, smem, st);
