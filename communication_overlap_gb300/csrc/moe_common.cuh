@@ -85,9 +85,12 @@ __device__ __forceinline__ bool grid_barrier(uint32_t* count, uint32_t target, i
   uint32_t old;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
   if (old + 1 == target) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (ld_acquire_gpu(count) < target) {
-    if (globaltimer_ns() - t0 > kGridWaitNs) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; ld_acquire_gpu(count) < target; ++i) {
+    if (i % 64) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kGridWaitNs) {
       atomicCAS(status, 0, int32_t(FO_ERR_TIMEOUT));
       return false;
     }

@@ -61,8 +61,21 @@ struct Const {
   static constexpr int value = N;
 };
 
-// Work split evenly: first item of part c of n items over g parts.
-__device__ __forceinline__ int64_t part(int64_t n, int c, int g) { return n * c / g; }
+// n items cut into g even parts: first(c) = n * c / g.  (Every item is 128 bytes
+// of weights or more, so their number fits 32 bits; a 64-bit division is 400
+// cycles.)
+struct Cut {
+  int32_t n, g, base, rem;
+  __device__ __forceinline__ Cut(int n_, int g_) : n(n_), g(g_), base(n_ / g_), rem(n_ % g_) {}
+  __device__ __forceinline__ int first(int c) const { return base * c + rem * c / g; }
+  // the part that item x lies in
+  __device__ __forceinline__ int owner(int x) const {
+    int c = min(int(float(x) * float(g) / float(n)), g - 1);
+    while (first(c + 1) <= x) ++c;
+    while (first(c) > x) --c;
+    return c;
+  }
+};
 
 struct FewArgs {
   CUtensorMap map_w1[2], map_w2;   // 4-bit: boxes of 128 bytes x 32, 64 and 64 rows
@@ -160,6 +173,7 @@ __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
+      if (t0 + t >= a.T) break;
       float v = acc[e][t];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -169,7 +183,8 @@ __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
   if (threadIdx.x < 32) {
     const int e = e0 + threadIdx.x / 8, t = t0 + threadIdx.x % 8;
     float v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += red[threadIdx.x * warps + w];
+    if (e < a.E && t < a.T)
+      for (int w = 0; w < warps; ++w) v += red[threadIdx.x * warps + w];
     if (e < a.E && t < a.T) __stcg(a.logits + int64_t(t) * a.E + e, v);
   }
 }
@@ -236,40 +251,58 @@ __device__ void scale_x(const FewArgs& a, uint32_t* red) {
 // ------------------------------------------------------------------ work items
 
 // A tile of the first product: hidden rows [i0, i0 + n) of the a-th active
-// expert.
+// expert; and the walk over a CTA's granules, tile by tile.
 struct HiddenTile {
   int32_t a, i0, n;
 };
 
-__device__ __forceinline__ bool hidden_tile(int64_t& at, int64_t end, int per_expert, int granule,
-                                            int I, HiddenTile& t) {
-  if (at >= end) return false;
-  t.a = int(at / per_expert);
-  const int g = int(at % per_expert);
-  const int n = int(min(min(end - at, int64_t(per_expert - g)), int64_t(64 / granule)));
-  t.i0 = g * granule;
-  t.n = min(n * granule, I - t.i0);
-  at += n;
-  return true;
-}
+struct HiddenWalk {
+  int32_t left, a, g;
+  __device__ __forceinline__ HiddenWalk(int from, int to, int per_expert)
+      : left(to - from), a(from / per_expert), g(from % per_expert) {}
+  __device__ __forceinline__ bool next(int per_expert, int granule, int I, HiddenTile& t) {
+    if (left <= 0) return false;
+    const int n = min(min(left, per_expert - g), 64 / granule);
+    t.a = a;
+    t.i0 = g * granule;
+    t.n = min(n * granule, I - t.i0);
+    left -= n;
+    g += n;
+    if (g == per_expert) g = 0, ++a;
+    return true;
+  }
+};
 
 // A run of the second product: output rows of block rb, the a-th active
-// expert, stages [k0, k0 + n) of its columns.
+// expert, stages [k0, k0 + n) of its columns; and the walk over them.
 struct OutputRun {
   int32_t rb, a, k0, n;
 };
 
-__device__ __forceinline__ bool output_run(int64_t& at, int64_t end, int active, int k_stages,
-                                           OutputRun& r) {
-  if (at >= end) return false;
-  const int64_t unit = at / k_stages;
-  r.k0 = int(at % k_stages);
-  r.rb = int(unit / active);
-  r.a = int(unit % active);
-  r.n = int(min(end - at, int64_t(k_stages - r.k0)));
-  at += r.n;
-  return true;
-}
+struct OutputWalk {
+  int32_t left, rb, a, k;
+  __device__ __forceinline__ OutputWalk(int from, int to, int active, int k_stages)
+      : left(to - from) {
+    const int unit = from / k_stages;
+    k = from % k_stages;
+    rb = unit / max(active, 1);
+    a = unit % max(active, 1);
+  }
+  __device__ __forceinline__ bool next(int active, int k_stages, OutputRun& r) {
+    if (left <= 0) return false;
+    r.rb = rb;
+    r.a = a;
+    r.k0 = k;
+    r.n = min(left, k_stages - k);
+    left -= r.n;
+    k += r.n;
+    if (k == k_stages) {
+      k = 0;
+      if (++a == active) a = 0, ++rb;
+    }
+    return true;
+  }
+};
 
 // ------------------------------------------------------------------ instructions
 
@@ -323,6 +356,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero, f16 operands.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Place of 16-byte piece `p` (of a bf16 stage's 16 per row) of row `r` in a
@@ -400,16 +442,15 @@ __device__ __forceinline__ bool wait_grid(const uint32_t* count, uint32_t target
 
 // bf16: this warp's 16 rows of the stage (8 from lo, 8 from hi on) times nt
 // tiles of 8 tokens.
-template <int NT, int KS>
-__device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int kh, int nt,
+template <int NT>
+__device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int nt,
                                            float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31;
   const int row = ((lane & 8) ? hi : lo) + (lane & 7);
   const uint32_t tokens = stage + 32768;
   const int nb = nt * 8;
 #pragma unroll
-  for (int i = 0; i < 8 / KS; ++i) {
-    const int ks = kh * (8 / KS) + i;
+  for (int ks = 0; ks < 8; ++ks) {
     uint32_t w[4];
     ldsm4(stage + tile_place(row, ks * 2 + (lane >> 4), 128), w);
 #pragma unroll
@@ -431,50 +472,51 @@ __device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int k
   }
 }
 
-// Byte b of a word of scales as a float: its exponent field.  (Byte 0, 2^-127,
-// becomes zero: such a block adds less than 1e-36.)
-__device__ __forceinline__ float scale_of(uint32_t w, int b) {
-  return __uint_as_float((b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1) &
-                         0x7f800000u);
+// Four scale bytes as floats.
+__device__ __forceinline__ void scales_of(uint32_t w, float (&s)[4]) {
+  uint32_t p[2];
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "mov.b32 {h0, h1}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, h0;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %1, h1;\n\t}"
+      : "=r"(p[0]), "=r"(p[1])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s[2 * i] = bf16lo(p[i]), s[2 * i + 1] = bf16hi(p[i]);
 }
 
 // 4-bit: a block of 32 columns is two MMAs.  A thread takes 8 consecutive
 // codes of a row (one word) and the same 8 columns of a token (16 bytes); which
 // of the MMA's 16 columns they stand in does not matter as long as both agree.
-// code: the thread's word of each block in its first row; row1: from there to
-// its second; scale0, scale1: where their scales are; blocks: of the stage's
-// eight, those that exist.  TOKEN_SCALES: the tokens' values have a scale per
-// block, too.
-template <int NT, int KS, bool TOKEN_SCALES>
-__device__ __forceinline__ void stage_mx(uint32_t stage, const uint32_t (&code)[8 / KS],
-                                         uint32_t row1, uint32_t scale0, uint32_t scale1, int kh,
-                                         int nt, int blocks, float (&acc)[NT][4]) {
+// code: the thread's word of the first block in its first row (those of the
+// other blocks differ in the swizzled bits only); its second row is 64 rows
+// further in the first product, 8 in the second (SECOND, where the tokens'
+// values have a scale per block, too).  scale0, scale1: where the rows' scales
+// are; blocks: of the stage's eight, those that exist.
+template <int NT, bool SECOND>
+__device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t scale0,
+                                         uint32_t scale1, int nt, int blocks,
+                                         float (&acc)[NT][4]) {
+  constexpr uint32_t kRow1 = SECOND ? 8 * 128 : 64 * 128;
   const int lane = threadIdx.x & 31, c = lane & 3;
   const uint32_t tokens = stage + kMxTokens + uint32_t(lane >> 2) * kMxToken + c * 16;
   const uint32_t token_scales = stage + kMxTokens + uint32_t(c * 2) * kMxToken + 512;
+  code += stage;
+  scale0 += stage;
+  scale1 += stage;
 #pragma unroll
-  for (int q4 = 0; q4 < 2 / KS; ++q4) {
-    const int q = kh + q4;                     // four blocks, a word of scales
+  for (int q = 0; q < 2; ++q) {                // four blocks, a word of scales
     if (q * 4 >= blocks) break;
     uint32_t w0[4], w1[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      w0[b] = lds32(stage + code[q4 * 4 + b]);
-      w1[b] = lds32(stage + code[q4 * 4 + b] + row1);
+      const uint32_t at = code ^ uint32_t((q * 4 + b) << 4);
+      w0[b] = lds32(at);
+      w1[b] = lds32(at + kRow1);
     }
-    const uint32_t sw0 = lds32(stage + scale0 + q * 512), sw1 = lds32(stage + scale1 + q * 512);
     float s0[4], s1[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) s0[b] = scale_of(sw0, b), s1[b] = scale_of(sw1, b);
-    // 255 is NaN, not the infinity that its exponent field makes
-    if (((((sw0 & 0x7f7f7f7fu) + 0x01010101u) & sw0) | (((sw1 & 0x7f7f7f7fu) + 0x01010101u) & sw1)) &
-        0x80808080u) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        s0[b] = mx_scale_value((sw0 >> (8 * b)) & 255u);
-        s1[b] = mx_scale_value((sw1 >> (8 * b)) & 255u);
-      }
-    }
+    scales_of(lds32(scale0 + q * 512), s0);
+    scales_of(lds32(scale1 + q * 512), s1);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
@@ -482,7 +524,7 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, const uint32_t (&code)[
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         lds128(tokens + uint32_t(j * 8) * kMxToken + (q * 4 + b) * 64, t[b]);
-      if constexpr (TOKEN_SCALES) {
+      if constexpr (SECOND) {
         lds128(token_scales + uint32_t(j * 8) * kMxToken + q * 16, u0);
         lds128(token_scales + uint32_t(j * 8 + 1) * kMxToken + q * 16, u1);
       }
@@ -491,10 +533,10 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, const uint32_t (&code)[
         uint32_t p[4], r[4];
         mx_decode8(w0[b], p);
         mx_decode8(w1[b], r);
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma16816<true>(d, p[0], r[0], p[1], r[1], t[b][0], t[b][1]);
+        float d[4];
+        mma16816_zero(d, p[0], r[0], p[1], r[1], t[b][0], t[b][1]);
         mma16816<true>(d, p[2], r[2], p[3], r[3], t[b][2], t[b][3]);
-        if constexpr (TOKEN_SCALES) {
+        if constexpr (SECOND) {
           uint64_t lo = pack2(d[0], d[1]), hi = pack2(d[2], d[3]);
           const uint64_t u = pack2(__uint_as_float(u0[b]), __uint_as_float(u1[b]));
           unpack2(mul2(lo, u), d[0], d[1]);
@@ -511,10 +553,10 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, const uint32_t (&code)[
 
 constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
 
-// Computing warps: 8 of 16 rows each, or twice that, each pair sharing 16 rows
-// and halving the columns of a stage.  Decoding 4-bit weights is a chain of
-// dependent steps (8 warps took 1470 cycles for a stage that HBM delivers in
-// 400), so it wants the second set; with many tokens its registers do not fit.
+// Computing warps: 8 of 16 rows each, or two such sets that take turns at the
+// stages.  Decoding 4-bit weights is a chain of dependent steps (8 warps took
+// 1470 cycles for a stage that HBM delivers in 900), so it wants the second set;
+// with many tokens its registers do not fit.
 template <bool MX, int NT>
 constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
 template <bool MX, int NT>
@@ -546,7 +588,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(&full[s]), MX ? kCopyWarps : kCopyThreads);
-      mbar_init(smem_u32(&empty[s]), 8 * KS);
+      mbar_init(smem_u32(&empty[s]), 8);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -649,13 +691,13 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
 
     const int active = *n_active_s;
     const int per_expert = (a.I + kGranule - 1) / kGranule;
-    const int64_t n1 = int64_t(active) * per_expert;
-    const int64_t at1 = part(n1, c, G), end1 = part(n1, c + 1, G);
+    const Cut cut1(active * per_expert, G);
     const int k1 = (a.H + kStageK<MX> - 1) / kStageK<MX>;      // stages of a tile of the first product
     const int k2 = (a.I + kStageK<MX> - 1) / kStageK<MX>;
     const int row_blocks = (a.H + 127) / 128;
-    const int64_t n2 = int64_t(row_blocks) * active * k2;
-    const int64_t at2 = part(n2, c, G), end2 = part(n2, c + 1, G);
+    const Cut cut2(row_blocks * active * k2, G);
+    const HiddenWalk walk1(cut1.first(c), cut1.first(c + 1), per_expert);
+    const OutputWalk walk2(cut2.first(c), cut2.first(c + 1), active, k2);
     const uint32_t ring = smem_u32(smem);
 
     if (!MX && warp < kCopyWarps) {
@@ -684,9 +726,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           copy16(dst + 32768 + tile_place(i, piece, nb), in ? src : base, in && i < rows, keep);
         }
       };
-      int64_t at = at1;
+      HiddenWalk hidden = walk1;
       HiddenTile t;
-      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+      while (ok && hidden.next(per_expert, kGranule, a.I, t)) {
         // a stage's rows: the gate's from 0, the up-projection's from 64 on.
         // A thread's addresses advance by a constant from stage to stage.
         const int64_t gate = int64_t(ls.active[t.a]) * a.w1_rows + t.i0;
@@ -728,7 +770,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       // The second product: the weights of the first stages are on their way
       // before the barrier, the tokens follow after it.
       struct Place {
-        int64_t at;
+        OutputWalk walk;
         OutputRun r;
         int k;
         bool more;
@@ -736,7 +778,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       };
       const int64_t pitch = int64_t(a.I) * 2;
       auto open = [&](Place& p, bool weights) {
-        p.more = output_run(p.at, end2, active, k2, p.r);
+        p.more = p.walk.next(active, k2, p.r);
         p.k = p.r.k0;
         if (!p.more) return;
         if (weights) {
@@ -748,7 +790,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
               a.h + int64_t(first + min(r0, rows - 1)) * a.I + piece * 8 + p.k * kStageK<MX>);
         }
       };
-      Place w{at2, {}, 0, false, nullptr}, v{at2, {}, 0, false, nullptr};
+      Place w{walk2, {}, 0, false, nullptr}, v{walk2, {}, 0, false, nullptr};
       open(w, true);
       open(v, false);
       int w_stage = stage, ahead = 0;    // stages whose weights are under way
@@ -818,9 +860,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           phase ^= 1;
         }
       };
-      int64_t at = at1;
+      HiddenWalk hidden = walk1;
       HiddenTile t;
-      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+      while (ok && hidden.next(per_expert, kGranule, a.I, t)) {
         const int gate = int(ls.active[t.a]) * a.w1_rows + t.i0, up = gate + a.I;
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         if (warp < 2) {
@@ -869,13 +911,13 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       }
       // The second product: the weights of the first stages are on their way
       // before the barrier, the tokens follow after it.
-      if (ok && warp == 3 && at2 < end2) {
+      if (ok && warp == 3 && walk2.left > 0) {
         ok = wait_grid(a.barrier + 1, uint32_t(G), abort_flag, a.status);
         asm volatile("fence.proxy.async;" ::: "memory");   // h was written by threads
       }
-      at = at2;
+      OutputWalk out = walk2;
       OutputRun r;
-      while (ok && output_run(at, end2, active, k2, r)) {
+      while (ok && out.next(active, k2, r)) {
         const int row = int(ls.active[r.a]) * a.w2_rows + r.rb * 128;
         const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
         if (warp < 2) {
@@ -919,8 +961,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       const int mw = (warp - kCopyWarps) & 7, kh = (warp - kCopyWarps) >> 3;
       const int mtid = threadIdx.x - kCopyThreads;
       const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
-      int stage = 0;
+      int stage = kh;                      // this set's next stage
       uint32_t phase = 0;
+      int turn = 0;                        // the set whose turn is next
       float acc[NT][4];
       float* half_sums = yacc + a.T * kYPitch;   // [NT][8 warps][32 lanes][4]
       // `n` stages into acc; `work`: this warp's rows exist
@@ -930,34 +973,32 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-        uint32_t code[8 / KS];               // 4-bit: places of a thread's words
-#pragma unroll
-        for (int b = 0; b < 8 / KS; ++b)
-          code[b] = code_place(lo + g, kh * (8 / KS) + b) + (lane & 3) * 4;
+        const uint32_t code = code_place(lo + g, 0) + (lane & 3) * 4;   // 4-bit
         bool ok = true;
-        for (int k = 0; k < n; ++k) {
+        for (int k = KS == 1 ? 0 : turn ^ kh; k < n; k += KS) {
           ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
           if (!ok) break;
           if (work) {
             const uint32_t at = ring + uint32_t(stage * a.stage_bytes);
             if constexpr (MX)
-              stage_mx<NT, KS, decltype(second)::value != 0>(at, code, uint32_t(hi - lo) * 128,
-                                                             scale0, scale1, kh, nt,
-                                                             blocks - 8 * k, acc);
+              stage_mx<NT, decltype(second)::value != 0>(at, code, scale0, scale1, nt,
+                                                         blocks - 8 * k, acc);
             else
-              stage_bf16<NT, KS>(at, lo, hi, kh, nt, acc);
+              stage_bf16<NT>(at, lo, hi, nt, acc);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
-          if (++stage == a.stages) {
-            stage = 0;
+          stage += KS;
+          if (stage >= a.stages) {
+            stage -= a.stages;
             phase ^= 1;
           }
         }
+        turn ^= n & 1;
         if constexpr (KS == 1) {
           return math_all<kMathThreads>(ok);
         } else {
-          // the halves of K meet in the first set of warps
+          // the two sets' sums meet in the first
           float* to = half_sums + (mw * 32 + lane) * 4;
           if (kh == 1)
 #pragma unroll
@@ -976,9 +1017,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         }
       };
       bool ok = true;
-      int64_t at = at1;
+      HiddenWalk hidden = walk1;
       HiddenTile t;
-      while (ok && hidden_tile(at, end1, per_expert, kGranule, a.I, t)) {
+      while (ok && hidden.next(per_expert, kGranule, a.I, t)) {
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
         const int nb = (rows + 7) / 8 * 8;
         // a 4-bit row's scales: in the blocks of the tile's gate or up rows
@@ -1057,18 +1098,14 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                      : "l"(a.barrier + 1)
                      : "memory");
       }
-      at = at2;
+      OutputWalk out = walk2;
       OutputRun r;
       int rb = -1;                         // the block being summed
       auto flush = [&]() {
         math_sync<kMathThreads>();
         // the CTAs that share block rb
-        const int64_t lo = int64_t(rb) * active * k2, hi = lo + int64_t(active) * k2;
-        int c0 = int(lo * G / n2), c1 = int((hi - 1) * G / n2);
-        while (part(n2, c0 + 1, G) <= lo) ++c0;
-        while (part(n2, c0, G) > lo) --c0;
-        while (part(n2, c1 + 1, G) < hi) ++c1;
-        while (part(n2, c1, G) >= hi) --c1;
+        const int lo = rb * active * k2, hi = lo + active * k2;
+        const int c0 = cut2.owner(lo), c1 = cut2.owner(hi - 1);
         const bool mine = c0 == c1;
         bool last = mine;
         if (!mine) {
@@ -1080,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           if (mtid == 0) {
             int32_t parts = 0;   // CTAs of [c0, c1] that have a part (others' ranges are empty)
             for (int k = c0; k <= c1; ++k)
-              parts += n2 >= G || part(n2, k, G) < part(n2, k + 1, G);
+              parts += cut2.first(k) < cut2.first(k + 1);
             const int32_t old = atom_add_acq_rel_gpu(a.done + rb, 1);
             *flag_s = old + 1 == parts;
             if (old + 1 == parts) a.done[rb] = 0;   // for the next launch
@@ -1100,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
               const float* from = a.parts + int64_t(rb) * a.T * 128 + i;
 #pragma unroll 8
               for (int k = c0; k <= c1; ++k)
-                if (n2 >= G || part(n2, k, G) < part(n2, k + 1, G))
+                if (cut2.first(k) < cut2.first(k + 1))
                   v += __ldcg(from + int64_t(k) * a.T * 128);
             }
             reinterpret_cast<__nv_bfloat16*>(a.y)[(i >> 7) * a.y_stride + row] =
@@ -1109,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         }
         math_sync<kMathThreads>();   // the sums may be overwritten
       };
-      while (ok && output_run(at, end2, active, k2, r)) {
+      while (ok && out.next(active, k2, r)) {
         if (r.rb != rb) {
           if (rb >= 0) flush();
           rb = r.rb;
@@ -1234,6 +1271,11 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   const bool mx = d.weights == FO_TYPE_MX4;
   const Layout l = layout_of(d);
   if (l.row_blocks > kMaxRowBlocks) return FO_ERR_UNSUPPORTED;
+  // (weights of more than 2^31 items do not fit any memory; see Cut)
+  const int64_t most = int64_t(d.tokens) * d.top_k < d.experts ? d.tokens * d.top_k : d.experts;
+  if (most * (int64_t(d.inter) / 8 + 1) > 0x7fffffff ||
+      most * l.row_blocks * (int64_t(d.inter) / 128 + 1) > 0x7fffffff)
+    return FO_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   FewArgs a{};
   a.x = static_cast<const uint16_t*>(x);
@@ -1265,7 +1307,7 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   const int nb = int(mx_up(d.tokens, 8));
   a.stage_bytes = int(mx_up(mx ? kMxTokens + nb * kMxToken : 32768 + nb * 256, 1024));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
-  // the outputs' sums, then the halves of K on their way (where split)
+  // the outputs' sums, then those of the second set on their way
   const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 8192 : 0);
   const int tail = lists + y_bytes + kBarBytes + 1024;
   a.stages = (kSmemLimit - tail) / a.stage_bytes;
