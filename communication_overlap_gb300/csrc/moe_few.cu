@@ -136,29 +136,34 @@ __device__ __forceinline__ float activate(float g, int act) {
 
 // ------------------------------------------------------------------ router
 
-// Logits of a block of 4 experts x 8 tokens by one CTA: its warps share out
+// Logits of a block of EB experts x 8 tokens by one CTA: its warps share out
 // the columns, 256 at a time, and their sums meet in shared memory.
+template <int EB>
 __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float acc[4][8];
+  const int nt = min(a.T - t0, 8);
+  float acc[EB][8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+  for (int e = 0; e < EB; ++e)
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[e][t] = 0.0f;
   for (int k = (warp * 32 + lane) * 8; k < a.H; k += warps * 256) {
-    uint4 r[4];
+    uint4 r[EB], x[8];     // (all loads, then all products)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < EB; ++e)
       r[e] = e0 + e < a.E
                  ? __ldg(reinterpret_cast<const uint4*>(a.router + int64_t(e0 + e) * a.H + k))
                  : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t0 + t >= a.T) break;
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + t) * a.x_stride + k));
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+    for (int t = 0; t < 8; ++t)
+      x[t] = t < nt ? __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + t) * a.x_stride + k))
+                    : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+    for (int t = 0; t < 8; ++t) {
+      if (t >= nt) break;
+      const uint32_t xw[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+      for (int e = 0; e < EB; ++e) {
         const uint32_t rw[4] = {r[e].x, r[e].y, r[e].z, r[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -170,22 +175,24 @@ __device__ void router_block(const FewArgs& a, int e0, int t0, float* red) {
   }
   __syncthreads();   // red is free
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+  for (int t = 0; t < 8; ++t) {
+    if (t >= nt) break;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t0 + t >= a.T) break;
+    for (int e = 0; e < EB; ++e) {
       float v = acc[e][t];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) red[(e * 8 + t) * warps + warp] = v;
     }
+  }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int e = e0 + threadIdx.x / 8, t = t0 + threadIdx.x % 8;
-    float v = 0.0f;
-    if (e < a.E && t < a.T)
+  if (threadIdx.x < EB * 8) {
+    const int e = e0 + threadIdx.x / 8, t = threadIdx.x % 8;
+    if (e < a.E && t < nt) {
+      float v = 0.0f;
       for (int w = 0; w < warps; ++w) v += red[threadIdx.x * warps + w];
-    if (e < a.E && t < a.T) __stcg(a.logits + int64_t(t) * a.E + e, v);
+      __stcg(a.logits + int64_t(t0 + t) * a.E + e, v);
+    }
   }
 }
 
@@ -596,9 +603,14 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
 
   // ---------------------------------------------------------------- router
   {
-    const int eb = (a.E + 3) / 4, tb = (a.T + 7) / 8;
-    for (int u = c; u < eb * tb; u += G)
-      router_block(a, u % eb * 4, u / eb * 8, reinterpret_cast<float*>(smem));
+    // an expert per CTA while that is one round, else four
+    float* red = reinterpret_cast<float*>(smem);
+    const int tb = (a.T + 7) / 8, eb = (a.E + 3) / 4;
+    if (a.E * tb <= G) {
+      if (c < a.E * tb) router_block<1>(a, c % a.E, c / a.E * 8, red);
+    } else {
+      for (int u = c; u < eb * tb; u += G) router_block<4>(a, u % eb * 4, u / eb * 8, red);
+    }
     if constexpr (MX) scale_x(a, reinterpret_cast<uint32_t*>(smem) + 1024);
   }
   __threadfence();
@@ -1088,10 +1100,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         }
       }
       // this CTA's hidden values are written
-      __threadfence();
       if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
       math_sync<kMathThreads>();
-      if (mtid == 0) {
+      if (mtid == 0) {     // (a release: what stood before the barrier above is in it)
         uint32_t old;
         asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
                      : "=r"(old)
@@ -1112,19 +1123,17 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           float* to = a.parts + int64_t(c + rb) * a.T * 128;
           for (int i = mtid; i < a.T * 128; i += kMathThreads)
             __stcg(to + i, yacc[(i >> 7) * kYPitch + (i & 127)]);
-          __threadfence();
           math_sync<kMathThreads>();
           if (mtid == 0) {
-            int32_t parts = 0;   // CTAs of [c0, c1] that have a part (others' ranges are empty)
-            for (int k = c0; k <= c1; ++k)
-              parts += cut2.first(k) < cut2.first(k + 1);
+            int32_t parts = c1 - c0 + 1;   // less those whose range is empty
+            if (cut2.base == 0)
+              for (int k = c0; k <= c1; ++k) parts -= cut2.first(k) == cut2.first(k + 1);
             const int32_t old = atom_add_acq_rel_gpu(a.done + rb, 1);
             *flag_s = old + 1 == parts;
             if (old + 1 == parts) a.done[rb] = 0;   // for the next launch
           }
           math_sync<kMathThreads>();
           last = *flag_s != 0;
-          if (last) __threadfence();
         }
         if (last) {
           for (int i = mtid; i < a.T * 128; i += kMathThreads) {
@@ -1136,9 +1145,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
             } else {
               const float* from = a.parts + int64_t(rb) * a.T * 128 + i;
 #pragma unroll 8
-              for (int k = c0; k <= c1; ++k)
-                if (cut2.first(k) < cut2.first(k + 1))
-                  v += __ldcg(from + int64_t(k) * a.T * 128);
+              for (int k = c0; k <= c1; ++k) {
+                const bool has = cut2.base > 0 || cut2.first(k) < cut2.first(k + 1);
+                v += has ? __ldcg(from + int64_t(k) * a.T * 128) : 0.0f;
+              }
             }
             reinterpret_cast<__nv_bfloat16*>(a.y)[(i >> 7) * a.y_stride + row] =
                 __float2bfloat16_rn(v);
