@@ -66,8 +66,12 @@ struct Const {
 // cycles.)
 struct Cut {
   int32_t n, g, base, rem;
-  __device__ __forceinline__ Cut(int n_, int g_) : n(n_), g(g_), base(n_ / g_), rem(n_ % g_) {}
-  __device__ __forceinline__ int first(int c) const { return base * c + rem * c / g; }
+  uint32_t inverse;   // ceil(2^24 / g): x / g = x * inverse >> 24 for x < g * g, g <= 160
+  __device__ __forceinline__ Cut(int n_, int g_, uint32_t inverse_)
+      : n(n_), g(g_), base(n_ / g_), rem(n_ - base * g_), inverse(inverse_) {}
+  __device__ __forceinline__ int first(int c) const {
+    return base * c + int(uint32_t(rem * c) * inverse >> 24);
+  }
   // the part that item x lies in
   __device__ __forceinline__ int owner(int x) const {
     int c = min(int(float(x) * float(g) / float(n)), g - 1);
@@ -89,6 +93,7 @@ struct FewArgs {
   int32_t T, H, I, E, K, renormalize, act;
   int32_t w1_rows, w2_rows;   // rows of an expert's matrices as stored
   int32_t stages, stage_bytes;
+  uint32_t inverse_g;
   int32_t off_lists, off_y, off_bar;      // shared memory offsets
   uint32_t* barrier;          // [0], [1] counts, [2] leave
   int32_t* done;              // [row blocks] parts finished
@@ -401,14 +406,14 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-template <int THREADS>
+// Among the threads of the first set of computing warps.
+constexpr int kMathThreads = 256;
 __device__ __forceinline__ void math_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kMathThreads) : "memory");
 }
 
-// The same, and whether all say yes: the computing warps give up together, so
-// that none is left at a barrier.
-template <int THREADS>
+// The same, and whether all say yes: these warps give up together, so that none
+// is left at a barrier.
 __device__ __forceinline__ bool math_all(bool yes) {
   uint32_t out;
   asm volatile(
@@ -417,7 +422,7 @@ __device__ __forceinline__ bool math_all(bool yes) {
       "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(out)
-      : "r"(uint32_t(yes)), "n"(THREADS)
+      : "r"(uint32_t(yes)), "n"(kMathThreads)
       : "memory");
   return out != 0;
 }
@@ -558,12 +563,13 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
   }
 }
 
-constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
+constexpr int kBarBytes = 8 * (2 * kMaxStages + 2) + 16;
 
 // Computing warps: 8 of 16 rows each, or two such sets that take turns at the
 // stages.  Decoding 4-bit weights is a chain of dependent steps (8 warps took
 // 1470 cycles for a stage that HBM delivers in 900), so it wants the second set;
-// with many tokens its registers do not fit.
+// with many tokens its registers do not fit.  The second set leaves its sums in
+// shared memory and goes on; what follows a tile is the first's work.
 template <bool MX, int NT>
 constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
 template <bool MX, int NT>
@@ -573,7 +579,7 @@ constexpr int kThreads = 32 * kCopyWarps + 256 * kSplit<MX, NT>;
 template <bool MX, int NT>
 __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kCopyThreads = 32 * kCopyWarps;
-  constexpr int KS = kSplit<MX, NT>, kMathThreads = 256 * KS, kWarps = kThreads<MX, NT> / 32;
+  constexpr int KS = kSplit<MX, NT>, kWarps = kThreads<MX, NT> / 32;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment, for the copies' swizzle
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -583,7 +589,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
   float* yacc = reinterpret_cast<float*>(smem + a.off_y);   // [T][kYPitch]; first product: maxima
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.off_bar);
   uint64_t* empty = full + kMaxStages;
-  int* abort_word = reinterpret_cast<int*>(empty + kMaxStages);
+  uint64_t* sums = empty + kMaxStages;   // the second set's sums: there, taken
+  int* abort_word = reinterpret_cast<int*>(sums + 2);
   volatile int* abort_flag = abort_word;
   int* n_active_s = abort_word + 1;
   int* flag_s = abort_word + 2;
@@ -597,6 +604,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       mbar_init(smem_u32(&full[s]), MX ? kCopyWarps : kCopyThreads);
       mbar_init(smem_u32(&empty[s]), 8);
     }
+    mbar_init(smem_u32(&sums[0]), 8);
+    mbar_init(smem_u32(&sums[1]), 8);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -703,11 +712,11 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
 
     const int active = *n_active_s;
     const int per_expert = (a.I + kGranule - 1) / kGranule;
-    const Cut cut1(active * per_expert, G);
+    const Cut cut1(active * per_expert, G, a.inverse_g);
     const int k1 = (a.H + kStageK<MX> - 1) / kStageK<MX>;      // stages of a tile of the first product
     const int k2 = (a.I + kStageK<MX> - 1) / kStageK<MX>;
     const int row_blocks = (a.H + 127) / 128;
-    const Cut cut2(row_blocks * active * k2, G);
+    const Cut cut2(row_blocks * active * k2, G, a.inverse_g);
     const HiddenWalk walk1(cut1.first(c), cut1.first(c + 1), per_expert);
     const OutputWalk walk2(cut2.first(c), cut2.first(c + 1), active, k2);
     const uint32_t ring = smem_u32(smem);
@@ -850,11 +859,12 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
     } else if (MX && warp < kCopyWarps) {
       // ----------------------------------------------------- copies, 4-bit
-      // All of a stage comes by bulk copies, from four warps: codes of the first
-      // and of the second 64 rows (boxes of 128 bytes x 64 rows), scales (blocks
-      // of 512 bytes as they are kept, two of a row of blocks, the last may be
-      // alone), tokens (values and scales in one piece).  Each walks the stages
-      // by itself; one warp for all needs 1800 cycles for a stage.
+      // All of a stage comes by bulk copies: codes (boxes of 128 bytes x 64 rows),
+      // scales (blocks of 512 bytes as they are kept, two of a row of blocks, the
+      // last may be alone), tokens (values and scales in one piece).  To issue one
+      // takes a warp 200 to 400 cycles, a stage's seven 1800 (and the four of
+      // scales 1100), so four warps share them, two at most in each, and walk the
+      // stages by themselves.
       const bool leader = lane == 0;
       const uint64_t once = tc::policy_evict_first(), keep = tc::policy_evict_last();
       const int64_t kb1 = a.hb, kb2 = a.ib;     // blocks of scales in a row of blocks
@@ -877,30 +887,37 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       while (ok && hidden.next(per_expert, kGranule, a.I, t)) {
         const int gate = int(ls.active[t.a]) * a.w1_rows + t.i0, up = gate + a.I;
         const int first = ls.first[t.a], rows = ls.first[t.a + 1] - first;
+        const int gb = ((gate & 127) + t.n + 127) >> 7, ub = ((up & 127) + t.n + 127) >> 7;
         if (warp < 2) {
-          // (rows past the tile's come along in whole boxes; nobody reads them)
+          // codes of the gate's or of the up-projection's rows, and where those lie
+          // in two rows of blocks, the second's scales.  (Rows past the tile's come
+          // along in whole boxes; nobody reads them.)
           const CUtensorMap* map = t.n > 32 ? &a.map_w1[1] : &a.map_w1[0];
           const int row = warp ? up : gate;
+          const bool two = (warp ? ub : gb) > 1;
           const uint32_t bytes = t.n > 32 ? 8192 : 4096;
-          for (int k = 0; k < k1 && begin(); ++k, end())
+          const uint8_t* scales = a.s1 + (int64_t(row >> 7) + 1) * kb1 * 512;
+          for (int k = 0; k < k1 && begin(); ++k, end()) {
             if (leader) {
-              mbar_expect_tx(smem_u32(&full[stage]), bytes);
-              tc::load_2d(ring + uint32_t(stage * a.stage_bytes + warp * 8192), map,
-                          smem_u32(&full[stage]), k * 128, row, once);
+              const uint32_t sb = !two ? 0 : kb1 - 2 * k > 1 ? 1024 : 512;
+              const uint32_t bar = smem_u32(&full[stage]);
+              const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+              mbar_expect_tx(bar, bytes + sb);
+              tc::load_2d(dst + warp * 8192, map, bar, k * 128, row, once);
+              if (two) bulk_load_hint(dst + kMxScales + warp * 2048 + 1024, scales, sb, bar, once);
             }
+            scales += 1024;
+          }
         } else if (warp == 2) {
-          const int gb = ((gate & 127) + t.n + 127) >> 7, ub = ((up & 127) + t.n + 127) >> 7;
           const uint8_t* gs = a.s1 + int64_t(gate >> 7) * kb1 * 512;
           const uint8_t* us = a.s1 + int64_t(up >> 7) * kb1 * 512;
           for (int k = 0; k < k1 && begin(); ++k, end()) {
             if (leader) {
               const uint32_t sb = kb1 - 2 * k > 1 ? 1024 : 512, bar = smem_u32(&full[stage]);
               const uint32_t dst = ring + uint32_t(stage * a.stage_bytes) + kMxScales;
-              mbar_expect_tx(bar, uint32_t(gb + ub) * sb);
+              mbar_expect_tx(bar, 2 * sb);
               bulk_load_hint(dst, gs, sb, bar, once);
-              if (gb > 1) bulk_load_hint(dst + 1024, gs + kb1 * 512, sb, bar, once);
               bulk_load_hint(dst + 2048, us, sb, bar, once);
-              if (ub > 1) bulk_load_hint(dst + 3072, us + kb1 * 512, sb, bar, once);
             }
             gs += 1024;
             us += 1024;
@@ -976,6 +993,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       int stage = kh;                      // this set's next stage
       uint32_t phase = 0;
       int turn = 0;                        // the set whose turn is next
+      uint32_t sums_phase = 0;
       float acc[NT][4];
       float* half_sums = yacc + a.T * kYPitch;   // [NT][8 warps][32 lanes][4]
       // `n` stages into acc; `work`: this warp's rows exist
@@ -1007,26 +1025,30 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           }
         }
         turn ^= n & 1;
-        if constexpr (KS == 1) {
-          return math_all<kMathThreads>(ok);
-        } else {
-          // the two sets' sums meet in the first
+        if constexpr (KS == 2) {
           float* to = half_sums + (mw * 32 + lane) * 4;
-          if (kh == 1)
+          if (kh == 1) {
+            ok = ok && tc::wait_warp(smem_u32(&sums[1]), sums_phase ^ 1, abort_flag, a.status);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
               *reinterpret_cast<float4*>(to + j * 1024) =
                   make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-          ok = math_all<kMathThreads>(ok);
-          if (kh == 0)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sums[0]));
+            sums_phase ^= 1;
+            return ok;
+          }
+          ok = ok && tc::wait_warp(smem_u32(&sums[0]), sums_phase, abort_flag, a.status);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float4 v = *reinterpret_cast<const float4*>(to + j * 1024);
-              acc[j][0] += v.x, acc[j][1] += v.y, acc[j][2] += v.z, acc[j][3] += v.w;
-            }
-          math_sync<kMathThreads>();
-          return ok;
+          for (int j = 0; j < NT; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(to + j * 1024);
+            acc[j][0] += v.x, acc[j][1] += v.y, acc[j][2] += v.z, acc[j][3] += v.w;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sums[1]));
+          sums_phase ^= 1;
         }
+        return math_all(ok);
       };
       bool ok = true;
       HiddenWalk hidden = walk1;
@@ -1042,6 +1064,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                       kMxScales + 2048 + (ur >> 7) * 1024 + mx_scale_row(ur & 127),
                       (a.H + 31) / 32, mw * 8 < t.n);
         if (!ok) break;
+        if (KS == 2 && kh == 1) continue;
         float h[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1066,15 +1089,15 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
               uint32_t m = __float_as_uint(h[j][e]) & 0x7fffffffu;
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-              if (kh == 0 && g == 0 && j * 8 < nb) top[mw * nb + j * 8 + c2 + e] = m;
+              if (g == 0 && j * 8 < nb) top[mw * nb + j * 8 + c2 + e] = m;
             }
-          math_sync<kMathThreads>();
+          math_sync();
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = j * 8 + c2 + e;
-              if (i >= rows || kh != 0) continue;
+              if (i >= rows) continue;
               const uint32_t* m = top + (mw & 4) * nb + i;
               const uint32_t s = half_scale(max(max(m[0], m[nb]), max(m[2 * nb], m[3 * nb])));
               const int64_t row = first + i;
@@ -1093,15 +1116,17 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = j * 8 + c2 + e;
-              if (i < rows && kh == 0)
+              if (i < rows)
                 reinterpret_cast<__nv_bfloat16*>(a.h)[int64_t(first + i) * a.I + t.i0 + p] =
                     __float2bfloat16_rn(h[j][e]);
             }
         }
       }
       // this CTA's hidden values are written
-      if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
-      math_sync<kMathThreads>();
+      if (kh == 0) {
+        if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
+        math_sync();
+      }
       if (mtid == 0) {     // (a release: what stood before the barrier above is in it)
         uint32_t old;
         asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
@@ -1113,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       OutputRun r;
       int rb = -1;                         // the block being summed
       auto flush = [&]() {
-        math_sync<kMathThreads>();
+        math_sync();
         // the CTAs that share block rb
         const int lo = rb * active * k2, hi = lo + active * k2;
         const int c0 = cut2.owner(lo), c1 = cut2.owner(hi - 1);
@@ -1123,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           float* to = a.parts + int64_t(c + rb) * a.T * 128;
           for (int i = mtid; i < a.T * 128; i += kMathThreads)
             __stcg(to + i, yacc[(i >> 7) * kYPitch + (i & 127)]);
-          math_sync<kMathThreads>();
+          math_sync();
           if (mtid == 0) {
             int32_t parts = c1 - c0 + 1;   // less those whose range is empty
             if (cut2.base == 0)
@@ -1132,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
             *flag_s = old + 1 == parts;
             if (old + 1 == parts) a.done[rb] = 0;   // for the next launch
           }
-          math_sync<kMathThreads>();
+          math_sync();
           last = *flag_s != 0;
         }
         if (last) {
@@ -1154,10 +1179,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                 __float2bfloat16_rn(v);
           }
         }
-        math_sync<kMathThreads>();   // the sums may be overwritten
+        math_sync();   // the sums may be overwritten
       };
       while (ok && out.next(active, k2, r)) {
-        if (r.rb != rb) {
+        if (kh == 0 && r.rb != rb) {
           if (rb >= 0) flush();
           rb = r.rb;
           for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
@@ -1166,14 +1191,15 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         ok = products(Const<1>{}, r.n, (rows + 7) / 8, mw * 16, mw * 16 + 8,
                       kMxScales + mx_scale_row(mw * 16 + g),
                       kMxScales + mx_scale_row(mw * 16 + 8 + g), (a.I + 31) / 32 - 8 * r.k0,
-                      rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
+                      r.rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
         if (!ok) break;
+        if (KS == 2 && kh == 1) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int i = j * 8 + c2 + e;
-            if (i >= rows || kh != 0) continue;
+            if (i >= rows) continue;
             float* to = yacc + ls.token[first + i] * kYPitch + mw * 16 + g;
             const float w = ls.weight[first + i];
             to[0] += w * acc[j][e];
@@ -1182,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         __syncwarp();   // another lane may add to the same sum next
       }
       if (ok && rb >= 0) flush();
-      if (active == 0) {   // no token has an expert: zeros
+      if (active == 0 && kh == 0) {   // no token has an expert: zeros
         for (int64_t j = int64_t(c) * kMathThreads + mtid; j < int64_t(a.T) * a.H;
              j += int64_t(G) * kMathThreads)
           reinterpret_cast<__nv_bfloat16*>(a.y)[j / a.H * a.y_stride + j % a.H] =
@@ -1323,6 +1349,7 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.stages = (kSmemLimit - tail) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   if (a.stages < 2) return FO_ERR_UNSUPPORTED;
+  a.inverse_g = uint32_t(((1 << 24) + grid - 1) / grid);
   a.off_lists = a.stages * a.stage_bytes;
   a.off_y = a.off_lists + lists;
   a.off_bar = a.off_y + y_bytes;
