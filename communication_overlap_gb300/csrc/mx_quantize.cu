@@ -24,40 +24,56 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight consecutive elements as they are kept.
 template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float<uint16_t>(uint16_t v) {
-  return __uint_as_float(uint32_t(v) << 16);
-}
-template <>
-__device__ __forceinline__ float to_float<float>(float v) {
-  return v;
-}
+struct Eight {
+  static constexpr int kWords = 2 * int(sizeof(T));
+  uint32_t w[kWords];
 
-// Eight consecutive elements as floats; `valid` of them exist.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int valid, bool vec, float (&v)[8]) {
-  if (vec && valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(u[i]);
-        v[2 * i + 1] = bf16hi(u[i]);
-      }
-    } else {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < valid ? to_float<T>(p[i]) : 0.0f;
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-}
+  __device__ __forceinline__ void load(const T* p) {   // 16-byte aligned
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void load_some(const T* p, int valid) {   // the first of them
+    zero();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) {
+        if constexpr (sizeof(T) == 2)
+          w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
+        else
+          w[i] = __float_as_uint(p[i]);
+      }
+  }
+  // The largest magnitude's fp32 bits.
+  __device__ __forceinline__ uint32_t amax() const {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+      for (int i = 1; i < 4; ++i)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+      return max(m << 16, m & 0xffff0000u);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 2)
+      return i & 1 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
 
 struct QuantArgs {
   const void* src;
@@ -89,33 +105,43 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
                      uintptr_t(a.row_stride) * sizeof(T)) & kAlign) == 0;
   const int r0 = threadIdx.x >> 4;                 // 16 rows per pass
   uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * (int64_t(a.col_blocks) * 64);
-  float v[8][8];
+  // which rows, then all loads, then the rest: no load waits for another
+  const T* from[8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t r = int64_t(rb) * kMxRows + p * 16 + r0;
-    int64_t from = r;
-    bool live = r < a.rows;
-    if (a.row_index != nullptr && live) {
-      from = a.row_index[r];
-      live = from >= 0 && from < a.src_rows;
+    int64_t row = r < a.rows ? r : -1;
+    if (a.row_index != nullptr && r < a.rows) {
+      row = a.row_index[r];
+      if (row >= a.src_rows) row = -1;
     }
-    load8<T>(src + (live ? from * a.row_stride + c0 : 0), live ? valid : 0, vec, v[p]);
+    from[p] = row < 0 ? nullptr : src + row * a.row_stride + c0;
+  }
+  Eight<T> v[8];
+  if (vec && valid == 8) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      v[p].zero();
+      if (from[p] != nullptr) v[p].load(from[p]);
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p].load_some(from[p], from[p] != nullptr ? valid : 0);
   }
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int r = p * 16 + r0;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[p][i]) & 0x7fffffffu);
+    uint32_t m = v[p].amax();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t s = mx_scale_byte(m);
     const float inv = mx_inverse_scale(s);
+    float u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[p][i] = s == 255u ? 0.0f : v[p][i] * inv;
+    for (int i = 0; i < 8; ++i) u[i] = s == 255u ? 0.0f : v[p].value(i) * inv;
     __stcs(reinterpret_cast<uint32_t*>(codes + int64_t(r) * (int64_t(a.col_blocks) * 64) +
                                        int64_t(cb) * 64 + col / 2),
-           mx_encode8(v[p]));
+           mx_encode8(u));
     if ((threadIdx.x & 3) == 0)
       reinterpret_cast<uint8_t*>(scale_block)[mx_scale_row(r) + (col >> 5)] = uint8_t(s);
   }

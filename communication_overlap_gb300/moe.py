@@ -11,9 +11,14 @@ device memory and the current stream, every step is a libfo.so call (see
 
 Calls run on the current stream of the tensors' device and do not
 synchronise.  Workspaces are kept per device and stream, so calls on
-different streams do not share one.  ``device_status`` reads (and
+different streams do not share one; a call that is captured into a CUDA graph
+takes its workspace from the graph's memory.  ``device_status`` reads (and
 synchronises) the sticky status of the calls' bounded waits.
+
+A generation step makes small calls, so the time here counts: the device is
+switched only where another is current, sizes are computed once per shape.
 """
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -31,13 +36,15 @@ def _type(t):
     return _TYPES[t.dtype]
 
 
-def _on_gpu(*tensors):
+def _on_gpu(first, *others):
     """The common CUDA device of the tensors (None entries are skipped)."""
-    live = [t for t in tensors if t is not None]
-    dev = live[0].device
-    if dev.type != "cuda" or any(t.device != dev for t in live):
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be on one CUDA device")
+    if index < 0 or not first.is_cuda:
         raise ValueError("tensors must be on one CUDA device")
-    return dev
+    return first.device
 
 
 def _int32(t, n, what):
@@ -61,13 +68,25 @@ def _row_stride(t, what):
 
 
 def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _run(dev, call, *args):
+    """call(*args) with dev current."""
+    if torch._C._cuda_getDevice() == dev.index:
+        call(*args)
+    else:
+        with torch.cuda.device(dev):
+            call(*args)
 
 
 def _status_word(dev):
-    if dev not in _status:
-        _status[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
-    return _status[dev].data_ptr()
+    st = _status.get(dev)
+    if st is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call once on this device before capturing into a CUDA graph")
+        st = _status[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
+    return st.data_ptr()
 
 
 def _workspace(kind, dev, nbytes):
@@ -75,8 +94,12 @@ def _workspace(kind, dev, nbytes):
     key = (kind, dev, _stream(dev))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    return ws.data_ptr()
+        # (under capture this is the graph's memory, zeroed again by each replay,
+        # and goes back to it in stream order)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        if not torch.cuda.is_current_stream_capturing():
+            _workspaces[key] = ws
+    return ws
 
 
 def device_status(device="cuda", clear=False):
@@ -96,6 +119,10 @@ def device_status(device="cuda", clear=False):
 
 # ------------------------------------------------------------------ 4-bit form
 
+_mx_sizes = functools.lru_cache(256)(fo.fo_mx_sizes)
+_route_sizes = functools.lru_cache(256)(fo.fo_moe_route_sizes)
+
+
 @dataclass
 class MxTensor:
     """`batch` matrices rows x cols in the 4-bit form (uint8 tensors)."""
@@ -106,7 +133,7 @@ class MxTensor:
     cols: int
 
     def __post_init__(self):
-        want = fo.fo_mx_sizes(self.batch, self.rows, self.cols)
+        want = _mx_sizes(self.batch, self.rows, self.cols)
         have = (self.codes.numel(), self.scales.numel())
         if have != want or self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
             raise ValueError(f"uint8 codes and scales of {want} bytes expected, not {have}")
@@ -131,13 +158,12 @@ def quantize(x, transpose=False, row_index=None):
             raise ValueError("row_index goes with one matrix, not transposed")
         _int32(row_index, row_index.numel(), "row_index")
         rows = row_index.numel()
-    nc, ns = fo.fo_mx_sizes(batch, rows, cols)
+    nc, ns = _mx_sizes(batch, rows, cols)
     codes = torch.empty(nc, dtype=torch.uint8, device=dev)
     scales = torch.empty(ns, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        fo.fo_mx_quantize(x.data_ptr(), type_, batch, batch_stride, rows, cols, stride, transpose,
-                          0 if row_index is None else row_index.data_ptr(), src_rows,
-                          codes.data_ptr(), scales.data_ptr(), _stream(dev))
+    _run(dev, fo.fo_mx_quantize, x.data_ptr(), type_, batch, batch_stride, rows, cols, stride,
+         transpose, 0 if row_index is None else row_index.data_ptr(), src_rows, codes.data_ptr(),
+         scales.data_ptr(), _stream(dev))
     return MxTensor(codes, scales, batch, rows, cols)
 
 
@@ -145,9 +171,8 @@ def dequantize(q, dtype=torch.bfloat16):
     """The values q stands for: [rows, cols], or [batch, rows, cols]."""
     dev = _on_gpu(q.codes, q.scales)
     out = torch.empty((q.batch, q.rows, q.cols), dtype=dtype, device=dev)
-    with torch.cuda.device(dev):
-        fo.fo_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.batch, q.rows, q.cols,
-                            out.data_ptr(), _type(out), q.rows * q.cols, q.cols, _stream(dev))
+    _run(dev, fo.fo_mx_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), q.batch, q.rows,
+         q.cols, out.data_ptr(), _type(out), q.rows * q.cols, q.cols, _stream(dev))
     return out[0] if q.batch == 1 else out
 
 
@@ -172,12 +197,11 @@ def mx_gemm(a, b, out=None, out_dtype=torch.bfloat16, group_first=None, group_ro
         out = make((a.rows, b.rows), dtype=out_dtype, device=dev)
     if tuple(out.shape) != (a.rows, b.rows):
         raise ValueError(f"out: {(a.rows, b.rows)} expected, not {tuple(out.shape)}")
-    with torch.cuda.device(dev):
-        fo.fo_mx_gemm(a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
-                      b.codes.data_ptr(), b.scales.data_ptr(), groups,
-                      0 if group_first is None else group_first.data_ptr(),
-                      0 if group_rows is None else group_rows.data_ptr(), out.data_ptr(),
-                      _type(out), _row_stride(out, "out"), _status_word(dev), _stream(dev))
+    _run(dev, fo.fo_mx_gemm, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
+         b.codes.data_ptr(), b.scales.data_ptr(), groups,
+         0 if group_first is None else group_first.data_ptr(),
+         0 if group_rows is None else group_rows.data_ptr(), out.data_ptr(), _type(out),
+         _row_stride(out, "out"), _status_word(dev), _stream(dev))
     return out
 
 
@@ -200,16 +224,18 @@ def route(logits, top_k, renormalize=True, capacity=0):
         raise ValueError("logits: [tokens, experts] expected")
     dev, type_ = _on_gpu(logits), _type(logits)
     T, E = logits.shape
-    M, nbytes = fo.fo_moe_route_sizes(T, E, top_k, capacity)
-    new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=dev)
-    r = Routing(new(T, top_k), new(T, top_k, dtype=torch.float32), new(M), new(M), new(T, top_k),
-                new(E), new(E))
-    with torch.cuda.device(dev):
-        fo.fo_moe_route(logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"), top_k,
-                        renormalize, capacity, r.ids.data_ptr(), r.weights.data_ptr(),
-                        r.row_token.data_ptr(), r.row_slot.data_ptr(), r.token_row.data_ptr(),
-                        r.expert_first.data_ptr(), r.expert_rows.data_ptr(),
-                        _workspace("route", dev, nbytes), _status_word(dev), _stream(dev))
+    M, nbytes = _route_sizes(T, E, top_k, capacity)
+    # one allocation, cut up
+    P = T * top_k
+    ids, weights, token_row, row_token, row_slot, first, rows = torch.empty(
+        3 * P + 2 * M + 2 * E, dtype=torch.int32, device=dev).split((P, P, P, M, M, E, E))
+    r = Routing(ids.view(T, top_k), weights.view(torch.float32).view(T, top_k), row_token, row_slot,
+                token_row.view(T, top_k), first, rows)
+    ws = _workspace("route", dev, nbytes)
+    _run(dev, fo.fo_moe_route, logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"),
+         top_k, renormalize, capacity, ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(),
+         row_slot.data_ptr(), token_row.data_ptr(), first.data_ptr(), rows.data_ptr(),
+         ws.data_ptr(), _status_word(dev), _stream(dev))
     return r
 
 
@@ -225,10 +251,9 @@ def route_backward(logits, ids, weights, dweights, renormalize=True):
         if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != T * k:
             raise ValueError(f"{what}: contiguous fp32[{T}, {k}] expected")
     out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    with torch.cuda.device(dev):
-        fo.fo_moe_route_backward(logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"), k,
-                                 renormalize, ids.data_ptr(), weights.data_ptr(),
-                                 dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
+    _run(dev, fo.fo_moe_route_backward, logits.data_ptr(), type_, T, E,
+         _row_stride(logits, "logits"), k, renormalize, ids.data_ptr(), weights.data_ptr(),
+         dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
     return out
 
 
@@ -259,9 +284,9 @@ class FewTokenLayer:
         self.router, self._keep = router, parts
         self.hidden, self.top_k = H, top_k
         self._w = [0 if t is None else t.data_ptr() for t in parts]
-        self._desc = lambda tokens: fo.make_few_desc(
+        self._desc = functools.lru_cache(fo.FO_MOE_FEW_TOKENS)(lambda tokens: fo.make_few_desc(
             tokens, H, I, E, top_k, renormalize, _ACTS[act],
-            fo.FO_TYPE_MX4 if mx else fo.FO_TYPE_BF16)
+            fo.FO_TYPE_MX4 if mx else fo.FO_TYPE_BF16))
         self._bytes = fo.fo_moe_few_workspace(self._desc(fo.FO_MOE_FEW_TOKENS))
 
     def __call__(self, x, out=None):
@@ -274,9 +299,8 @@ class FewTokenLayer:
         if out.shape != x.shape or out.dtype != torch.bfloat16:
             raise ValueError("out: bf16 of x's shape expected")
         w1, s1, w2, s2 = self._w
-        with torch.cuda.device(dev):
-            fo.fo_moe_few(self._desc(x.shape[0]), x.data_ptr(), _row_stride(x, "x"),
-                          self.router.data_ptr(), w1, s1, w2, s2, out.data_ptr(),
-                          _row_stride(out, "out"), _workspace("few", dev, self._bytes),
-                          _status_word(dev), _stream(dev))
+        ws = _workspace("few", dev, self._bytes)
+        _run(dev, fo.fo_moe_few, self._desc(x.shape[0]), x.data_ptr(), _row_stride(x, "x"),
+             self.router.data_ptr(), w1, s1, w2, s2, out.data_ptr(), _row_stride(out, "out"),
+             ws.data_ptr(), _status_word(dev), _stream(dev))
         return out
