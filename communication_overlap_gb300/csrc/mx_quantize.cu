@@ -34,11 +34,37 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  __device__ __forceinline__ void load(const T* p) {   // 16-byte aligned
+  // ALIGN: bytes that p is a multiple of, 16, or down to an element
+  template <int ALIGN>
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (ALIGN == 16) {
 #pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (ALIGN == 8) {
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
+        w[2 * i] = v.x, w[2 * i + 1] = v.y;
+      }
+    } else if constexpr (ALIGN == 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {      // p + 1 is a multiple of 4 bytes, or p is
+      uint32_t h[2] = {p[0], p[7]}, m[3];
+      if (reinterpret_cast<uintptr_t>(p) & 2) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) m[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 1) + i);
+        w[0] = h[0] | m[0] << 16;
+        w[1] = __funnelshift_r(m[0], m[1], 16);
+        w[2] = __funnelshift_r(m[1], m[2], 16);
+        w[3] = m[2] >> 16 | h[1] << 16;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+      }
     }
   }
   __device__ __forceinline__ void load_some(const T* p, int valid) {   // the first of them
@@ -86,9 +112,18 @@ struct QuantArgs {
   int32_t row_blocks, col_blocks;
 };
 
+// What all rows of all matrices start at a multiple of: 16 bytes, 8, 4 or 2.
+int rows_align(const void* p, int64_t batch, int64_t batch_stride, int64_t row_stride,
+               int64_t size) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | uintptr_t(row_stride * size) |
+                         uintptr_t(batch > 1 ? batch_stride * size : 0) | 16;
+  return int(bits & (~bits + 1));
+}
+
 // Rows of the source (or gathered rows of it) become rows of the result.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
+// ALIGN: what the rows' addresses are a multiple of, in bytes.
+template <typename T, int ALIGN>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) quantize_rows_kernel(const QuantArgs a) {
   __shared__ __align__(16) uint32_t scale_block[kMxScaleBytes / 4];
   int64_t id = blockIdx.x;
   const int cb = int(id % a.col_blocks);
@@ -100,13 +135,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
   const int64_t c0 = int64_t(cb) * kMxCols + col;
   const int64_t left = a.cols - c0;
   const int valid = left < 0 ? 0 : (left < 8 ? int(left) : 8);
-  constexpr uintptr_t kAlign = 15;
-  const bool vec = ((reinterpret_cast<uintptr_t>(src) |
-                     uintptr_t(a.row_stride) * sizeof(T)) & kAlign) == 0;
   const int r0 = threadIdx.x >> 4;                 // 16 rows per pass
-  uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * (int64_t(a.col_blocks) * 64);
+  const int64_t pitch = int64_t(a.col_blocks) * 64;
+  uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * pitch + c0 / 2;
   // which rows, then all loads, then the rest: no load waits for another
-  const T* from[8];
+  const T* from[8];                                // null: a row of zeros
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t r = int64_t(rb) * kMxRows + p * 16 + r0;
@@ -118,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
     from[p] = row < 0 ? nullptr : src + row * a.row_stride + c0;
   }
   Eight<T> v[8];
-  if (vec && valid == 8) {
+  if (valid == 8) {
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       v[p].zero();
-      if (from[p] != nullptr) v[p].load(from[p]);
+      if (from[p] != nullptr) v[p].template load<ALIGN>(from[p]);
     }
   } else {
 #pragma unroll
@@ -138,10 +171,9 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
     const float inv = mx_inverse_scale(s);
     float u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = s == 255u ? 0.0f : v[p].value(i) * inv;
-    __stcs(reinterpret_cast<uint32_t*>(codes + int64_t(r) * (int64_t(a.col_blocks) * 64) +
-                                       int64_t(cb) * 64 + col / 2),
-           mx_encode8(u));
+    for (int i = 0; i < 8; ++i) u[i] = v[p].value(i) * inv;
+    const uint32_t q = mx_encode8(u);
+    __stcs(reinterpret_cast<uint32_t*>(codes + int64_t(r) * pitch), s == 255u ? 0u : q);
     if ((threadIdx.x & 3) == 0)
       reinterpret_cast<uint8_t*>(scale_block)[mx_scale_row(r) + (col >> 5)] = uint8_t(s);
   }
@@ -151,6 +183,42 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
                                 ((b * a.row_blocks + rb) * a.col_blocks + cb) *
                                     int64_t(kMxScaleBytes))[threadIdx.x] = scale_block[threadIdx.x];
 }
+
+// Rows that do not start at 16 bytes are written through shared memory, half a
+// block at a time: a warp stores a row in whole words, whatever the row's
+// address, and the elements at its ends alone.  (Element by element from
+// registers 8190 x 4100 bf16 took 98 us, this way 27.  For reading, where L1
+// holds what neighbours share, the same detour took 60 us instead of 23.)
+template <typename T>
+struct Staged {
+  static constexpr int kRows = 64;
+  static constexpr int kPitch = kMxCols + 16 / int(sizeof(T));   // elements
+  T tile[kRows * kPitch];
+
+  __device__ __forceinline__ T* row(int i) { return tile + i * kPitch; }
+  // Row i's first n elements to p; by a warp.
+  __device__ __forceinline__ void store(int i, T* p, int n) {
+    const int lane = threadIdx.x & 31;
+    const T* from = row(i);
+    if constexpr (sizeof(T) == 2) {
+      const int odd = n > 0 ? int(reinterpret_cast<uintptr_t>(p) >> 1) & 1 : 0;
+      const int words = (n - odd) / 2;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = j * 32 + lane;
+        if (k < words)
+          __stcs(reinterpret_cast<uint32_t*>(p + odd) + k,
+                 uint32_t(from[odd + 2 * k]) | uint32_t(from[odd + 2 * k + 1]) << 16);
+      }
+      if (lane == 0 && odd) p[0] = from[0];
+      if (lane == 1 && ((n - odd) & 1)) p[n - 1] = from[n - 1];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j * 32 + lane < n) __stcs(p + j * 32 + lane, from[j * 32 + lane]);
+    }
+  }
+};
 
 // Columns of the source become rows of the result: the tile goes through
 // shared memory as [column of the result][row], two rows to a thread, four
@@ -217,19 +285,31 @@ __global__ void __launch_bounds__(kThreads) quantize_cols_kernel(const QuantArgs
   __syncthreads();
   const int blk = threadIdx.x & 3, r = (threadIdx.x >> 2) * 2;   // rows r and r + 1
   const uint8_t* from = tile + blk * (32 * C::kPitch + C::kShift) + r * int(sizeof(T));
-  uint32_t m0 = 0, m1 = 0;
-#pragma unroll 8
+  // both rows' 32 values: a word of two bf16 each, or two words
+  constexpr int kW = int(sizeof(T)) / 2;
+  uint32_t w[32 * kW];
+#pragma unroll
   for (int i = 0; i < 32; ++i) {
-    uint32_t x0, x1;
     if constexpr (sizeof(T) == 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(from + i * C::kPitch);
-      x0 = w << 16, x1 = w & 0xffff0000u;
+      w[i] = *reinterpret_cast<const uint32_t*>(from + i * C::kPitch);
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(from + i * C::kPitch);
-      x0 = w.x, x1 = w.y;
+      const uint2 v = *reinterpret_cast<const uint2*>(from + i * C::kPitch);
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
     }
-    m0 = max(m0, x0 & 0x7fffffffu);
-    m1 = max(m1, x1 & 0x7fffffffu);
+  }
+  uint32_t m0 = 0, m1 = 0;
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 32; ++i)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+    m0 = m << 16, m1 = m & 0xffff0000u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      m0 = max(m0, w[2 * i] & 0x7fffffffu);
+      m1 = max(m1, w[2 * i + 1] & 0x7fffffffu);
+    }
   }
   const uint32_t s0 = mx_scale_byte(m0), s1 = mx_scale_byte(m1);
   const float i0 = mx_inverse_scale(s0), i1 = mx_inverse_scale(s1);
@@ -239,19 +319,15 @@ __global__ void __launch_bounds__(kThreads) quantize_cols_kernel(const QuantArgs
     float u0[8], u1[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float x0, x1;
+      const int at = o * 8 + i;
       if constexpr (sizeof(T) == 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(from + (o * 8 + i) * C::kPitch);
-        x0 = bf16lo(w), x1 = bf16hi(w);
+        u0[i] = bf16lo(w[at]) * i0, u1[i] = bf16hi(w[at]) * i1;
       } else {
-        const float2 w = *reinterpret_cast<const float2*>(from + (o * 8 + i) * C::kPitch);
-        x0 = w.x, x1 = w.y;
+        u0[i] = __uint_as_float(w[2 * at]) * i0, u1[i] = __uint_as_float(w[2 * at + 1]) * i1;
       }
-      u0[i] = s0 == 255u ? 0.0f : x0 * i0;
-      u1[i] = s1 == 255u ? 0.0f : x1 * i1;
     }
-    q0[o] = mx_encode8(u0);
-    q1[o] = mx_encode8(u1);
+    q0[o] = s0 == 255u ? 0u : mx_encode8(u0);
+    q1[o] = s1 == 255u ? 0u : mx_encode8(u1);
   }
   const int64_t pitch = int64_t(a.col_blocks) * 64;
   uint8_t* dst = a.codes + ((b * a.row_blocks + rb) * int64_t(kMxRows) + r) * pitch +
@@ -277,7 +353,7 @@ struct DequantArgs {
   int32_t row_blocks, col_blocks;
 };
 
-template <typename T>
+template <typename T, bool STAGED>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
   int64_t id = blockIdx.x;
   const int cb = int(id % a.col_blocks);
@@ -289,12 +365,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
   const int64_t c0 = int64_t(cb) * kMxCols + col;
   const int64_t left = a.cols - c0;
   const int valid = left < 0 ? 0 : (left < 8 ? int(left) : 8);
-  const bool vec = valid == 8 && ((reinterpret_cast<uintptr_t>(dst) |
-                                   uintptr_t(a.row_stride) * sizeof(T)) & 15) == 0;
   const int r0 = threadIdx.x >> 4;
   const int64_t pitch = int64_t(a.col_blocks) * 64;
-  const uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * pitch +
-                         int64_t(cb) * 64 + col / 2;
+  const uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * pitch + c0 / 2;
   const uint8_t* scales = a.scales + ((b * a.row_blocks + rb) * a.col_blocks + cb) *
                                          int64_t(kMxScaleBytes) + (col >> 5);
   uint32_t q[8];
@@ -305,10 +378,11 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
     q[p] = __ldcs(reinterpret_cast<const uint32_t*>(codes + r * pitch));
     s[p] = scales[mx_scale_row(r)];
   }
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = int64_t(rb) * kMxRows + p * 16 + r0;
-    if (r >= a.rows) continue;
+  // whether all of the warp's columns exist
+  const bool pair = !STAGED && __all_sync(0xffffffffu, valid == 8);
+  // eight values of pass p to `to` (of shared memory where STAGED), if live;
+  // by whole warps
+  const auto put = [&](int p, T* to, bool live) {
     uint32_t h[4];
     mx_decode8(q[p], h);
     const float scale = mx_scale_value(s[p]);
@@ -319,27 +393,68 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
       v[2 * i] = f.x * scale;
       v[2 * i + 1] = f.y * scale;
     }
-    T* to = dst + r * a.row_stride + c0;
     if constexpr (sizeof(T) == 2) {
       const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      if (vec) {
+      if (STAGED) {
+        *reinterpret_cast<uint4*>(to) = w;
+      } else if (live && valid == 8) {
         __stcs(reinterpret_cast<uint4*>(to), w);
-      } else {
+      } else if (live) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i < valid) to[i] = uint16_t(u[i / 2] >> (16 * (i & 1)));
       }
     } else {
-      if (vec) {
-        __stcs(reinterpret_cast<float4*>(to), make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(reinterpret_cast<float4*>(to) + 1, make_float4(v[4], v[5], v[6], v[7]));
-      } else {
+      float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+      if (STAGED) {
+        reinterpret_cast<float4*>(to)[0] = lo;
+        reinterpret_cast<float4*>(to)[1] = hi;
+      } else if (pair) {
+        // two neighbouring lanes trade halves, so that each store of theirs is 32
+        // bytes in one piece (127 -> 100 us at 32768 x 4096)
+        const bool odd = threadIdx.x & 1;
+        const float4 give = odd ? lo : hi;
+        float4 got;
+        got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+        got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+        got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+        got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+        T* at = odd ? to - 4 : to;
+        if (live) {
+          __stcs(reinterpret_cast<float4*>(at), odd ? got : lo);
+          __stcs(reinterpret_cast<float4*>(at + 8), odd ? hi : got);
+        }
+      } else if (live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i < valid) to[i] = v[i];
       }
+    }
+  };
+  if constexpr (STAGED) {
+    __shared__ __align__(16) Staged<T> staged;
+    const int warp = threadIdx.x >> 5;
+    const int n = int(min(a.cols - int64_t(cb) * kMxCols, int64_t(kMxCols)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) put(h * 4 + p, staged.row(p * 16 + r0) + col, true);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t r = int64_t(rb) * kMxRows + h * 64 + i * 8 + warp;
+        if (r < a.rows)
+          staged.store(i * 8 + warp, dst + r * a.row_stride + int64_t(cb) * kMxCols, n);
+      }
+      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int64_t r = int64_t(rb) * kMxRows + p * 16 + r0;
+      put(p, dst + r * a.row_stride + c0, r < a.rows);
     }
   }
 }
@@ -371,10 +486,17 @@ fo_status launch_mx_quantize(const void* src, fo_type type, int64_t batch, int64
   if (transpose)
     return type == FO_TYPE_BF16 ? launch_cols<uint16_t>(a, unsigned(blocks), st)
                                 : launch_cols<float>(a, unsigned(blocks), st);
+  const unsigned grid = unsigned(blocks);
+  const int align = rows_align(src, batch, batch_stride, row_stride, type == FO_TYPE_BF16 ? 2 : 4);
   if (type == FO_TYPE_BF16)
-    quantize_rows_kernel<uint16_t><<<unsigned(blocks), kThreads, 0, st>>>(a);
+    (align == 16  ? quantize_rows_kernel<uint16_t, 16>
+     : align == 8 ? quantize_rows_kernel<uint16_t, 8>
+     : align == 4 ? quantize_rows_kernel<uint16_t, 4>
+                  : quantize_rows_kernel<uint16_t, 2>)<<<grid, kThreads, 0, st>>>(a);
   else
-    quantize_rows_kernel<float><<<unsigned(blocks), kThreads, 0, st>>>(a);
+    (align == 16  ? quantize_rows_kernel<float, 16>
+     : align == 8 ? quantize_rows_kernel<float, 8>
+                  : quantize_rows_kernel<float, 4>)<<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
@@ -388,10 +510,15 @@ fo_status launch_mx_dequantize(const void* codes, const void* scales, int64_t ba
   DequantArgs a{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), dst,
                 batch_stride, row_stride, rows, cols, int32_t(rb), int32_t(cb)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = unsigned(blocks);
+  const bool staged =
+      rows_align(dst, batch, batch_stride, row_stride, type == FO_TYPE_BF16 ? 2 : 4) != 16;
   if (type == FO_TYPE_BF16)
-    dequantize_kernel<uint16_t><<<unsigned(blocks), kThreads, 0, st>>>(a);
+    (staged ? dequantize_kernel<uint16_t, true>
+            : dequantize_kernel<uint16_t, false>)<<<grid, kThreads, 0, st>>>(a);
   else
-    dequantize_kernel<float><<<unsigned(blocks), kThreads, 0, st>>>(a);
+    (staged ? dequantize_kernel<float, true>
+            : dequantize_kernel<float, false>)<<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 

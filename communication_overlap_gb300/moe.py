@@ -225,18 +225,17 @@ def route(logits, top_k, renormalize=True, capacity=0):
     dev, type_ = _on_gpu(logits), _type(logits)
     T, E = logits.shape
     M, nbytes = _route_sizes(T, E, top_k, capacity)
-    # one allocation, cut up
-    P = T * top_k
-    ids, weights, token_row, row_token, row_slot, first, rows = torch.empty(
-        3 * P + 2 * M + 2 * E, dtype=torch.int32, device=dev).split((P, P, P, M, M, E, E))
-    r = Routing(ids.view(T, top_k), weights.view(torch.float32).view(T, top_k), row_token, row_slot,
-                token_row.view(T, top_k), first, rows)
+    # (seven allocations are cheaper than one and seven views of it)
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+    ids, token_row, row_token, row_slot = new(T, top_k), new(T, top_k), new(M), new(M)
+    first, rows = new(E), new(E)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     ws = _workspace("route", dev, nbytes)
     _run(dev, fo.fo_moe_route, logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"),
          top_k, renormalize, capacity, ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(),
          row_slot.data_ptr(), token_row.data_ptr(), first.data_ptr(), rows.data_ptr(),
          ws.data_ptr(), _status_word(dev), _stream(dev))
-    return r
+    return Routing(ids, weights, row_token, row_slot, token_row, first, rows)
 
 
 def route_backward(logits, ids, weights, dweights, renormalize=True):
