@@ -112,7 +112,7 @@ struct FewArgs {
 struct Lists {
   float* weight;      // [P] weight of row r (rows sorted by expert, token, slot)
   float* pair_weight; // [P]
-  float* x_scale;     // [P] 4-bit: scale of row r's token
+  float* x_scale;     // [T] 4-bit: scale of a token
   int16_t* token;     // [P] token of row r
   int16_t* id;        // [P] expert of pair (token, slot)
   int16_t* active;    // [E] experts that have rows
@@ -136,7 +136,7 @@ __host__ inline int lists_bytes(int P, int E) { return (16 * P + 4 * E + 2 + 127
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == FO_ACT_NONE) return g;
   if (act == FO_ACT_RELU) return g > 0.0f ? g : 0.0f;
-  return g / (1.0f + __expf(-g));
+  return __fdividef(g, 1.0f + __expf(-g));   // (a few units of the last place of fp32)
 }
 
 // ------------------------------------------------------------------ router
@@ -633,6 +633,9 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     }
     if constexpr (MX) scale_x(a, reinterpret_cast<uint32_t*>(smem) + 1024);
   }
+  // rows of each expert, in the ring's memory until the ring starts
+  int32_t* count = reinterpret_cast<int32_t*>(smem + 16384);          // [E]
+  for (int e = threadIdx.x; e < a.E; e += kWarps * 32) count[e] = 0;
   __threadfence();
   if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
   __syncthreads();
@@ -646,7 +649,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     // every CTA makes the same choice from the same logits
     for (int t = warp; t < a.T; t += kWarps) {
       int id;
-      float w;
+      float w, x_scale = 0.0f;
+      if constexpr (MX) x_scale = __ldcg(a.x_scale + t);
       const float* l = a.logits + int64_t(t) * a.E;
       auto choose = [&](auto v) {
         constexpr int V = decltype(v)::value;
@@ -665,14 +669,11 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       if (lane < a.K) {
         ls.id[t * a.K + lane] = int16_t(id);
         ls.pair_weight[t * a.K + lane] = w;
+        if (id >= 0) atomicAdd(&count[id], 1);
       }
+      if constexpr (MX)
+        if (lane == 0) ls.x_scale[t] = x_scale;
     }
-    // rows of each expert, in the ring's memory until the ring starts
-    int32_t* count = reinterpret_cast<int32_t*>(smem);          // [E]
-    for (int e = threadIdx.x; e < a.E; e += kWarps * 32) count[e] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < P; p += kWarps * 32)
-      if (ls.id[p] >= 0) atomicAdd(&count[ls.id[p]], 1);
     __syncthreads();
     if (warp == 0) {
       int rows = 0, active = 0;
@@ -710,7 +711,6 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           const int row = count[e] + rank;
           ls.token[row] = int16_t(p / a.K);
           ls.weight[row] = ls.pair_weight[p];
-          if constexpr (MX) ls.x_scale[row] = __ldcg(a.x_scale + p / a.K);
         }
         __syncwarp();
         if (e >= 0 && rank == 0) count[e] += __popc(same);
@@ -1084,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           for (int e = 0; e < 2; ++e) {
             if constexpr (MX) {   // the token's scale
               const int i = min(j * 8 + c2 + e, rows - 1);
-              const float u = ls.x_scale[first + i];
+              const float u = ls.x_scale[ls.token[first + i]];
               acc[j][e] *= u;
               acc[j][e + 2] *= u;
             }
@@ -1368,8 +1368,10 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
   // an expert's tokens: all of them at most
+  // (4-bit: rows up to a multiple of 8 are read and not used; they may lie in the
+  // next stage, the last stage's in what follows the ring)
   const int nb = int(mx_up(d.tokens, 8));
-  a.stage_bytes = int(mx_up(mx ? kMxTokens + nb * kMxToken : 32768 + nb * 256, 1024));
+  a.stage_bytes = int(mx_up(mx ? kMxTokens + d.tokens * kMxToken : 32768 + nb * 256, 1024));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
   // the outputs' sums, then those of the second set on their way
   const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 8192 : 0);
