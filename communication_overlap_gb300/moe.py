@@ -30,10 +30,11 @@ _ACTS = {"none": fo.FO_ACT_NONE, "relu": fo.FO_ACT_RELU, "silu": fo.FO_ACT_SILU}
 _status, _workspaces = {}, {}
 
 
-def _type(t):
-    if t.dtype not in _TYPES:
-        raise ValueError(f"bf16 or fp32 expected, not {t.dtype}")
-    return _TYPES[t.dtype]
+def _type(dtype):
+    type_ = _TYPES.get(dtype)
+    if type_ is None:
+        raise ValueError(f"bf16 or fp32 expected, not {dtype}")
+    return type_
 
 
 def _on_gpu(first, *others):
@@ -59,12 +60,16 @@ def _inner(t, what):
 
 def _row_stride(t, what):
     """Row stride of a matrix (of its length where it has one row)."""
+    rows, cols = t.shape[-2:]
+    if t.is_contiguous():
+        return cols
     _inner(t, what)
-    if t.shape[-2] <= 1:
-        return max(t.shape[-1], t.stride(-2) if t.numel() else 0)
-    if t.stride(-2) < t.shape[-1]:
+    stride = t.stride(-2)
+    if rows <= 1:
+        return max(cols, stride if t.numel() else 0)
+    if stride < cols:
         raise ValueError(f"{what}: rows overlap")
-    return t.stride(-2)
+    return stride
 
 
 def _stream(dev):
@@ -139,6 +144,8 @@ class MxTensor:
             raise ValueError(f"uint8 codes and scales of {want} bytes expected, not {have}")
         if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
+        if self.codes.get_device() != self.scales.get_device():
+            raise ValueError("codes and scales must be on one device")
 
 
 def quantize(x, transpose=False, row_index=None):
@@ -147,11 +154,10 @@ def quantize(x, transpose=False, row_index=None):
     int32 rows of x to take (an index outside x: a row of zeros)."""
     if x.dim() not in (2, 3):
         raise ValueError("a matrix or a batch of matrices expected")
-    dev, type_ = _on_gpu(x, row_index), _type(x)
-    batch = x.shape[0] if x.dim() == 3 else 1
-    src_rows, src_cols = x.shape[-2:]
+    dev, type_ = _on_gpu(x, row_index), _type(x.dtype)
+    *batch, src_rows, src_cols = x.shape
+    batch, batch_stride = (batch[0], x.stride(0)) if batch else (1, 0)
     stride = _row_stride(x, "x")
-    batch_stride = x.stride(0) if x.dim() == 3 else 0
     rows, cols = (src_cols, src_rows) if transpose else (src_rows, src_cols)
     if row_index is not None:
         if transpose or batch != 1:
@@ -169,11 +175,12 @@ def quantize(x, transpose=False, row_index=None):
 
 def dequantize(q, dtype=torch.bfloat16):
     """The values q stands for: [rows, cols], or [batch, rows, cols]."""
-    dev = _on_gpu(q.codes, q.scales)
-    out = torch.empty((q.batch, q.rows, q.cols), dtype=dtype, device=dev)
-    _run(dev, fo.fo_mx_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), q.batch, q.rows,
-         q.cols, out.data_ptr(), _type(out), q.rows * q.cols, q.cols, _stream(dev))
-    return out[0] if q.batch == 1 else out
+    dev, type_ = _on_gpu(q.codes, q.scales), _type(dtype)
+    batch, rows, cols = q.batch, q.rows, q.cols
+    out = torch.empty((rows, cols) if batch == 1 else (batch, rows, cols), dtype=dtype, device=dev)
+    _run(dev, fo.fo_mx_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), batch, rows, cols,
+         out.data_ptr(), type_, rows * cols, cols, _stream(dev))
+    return out
 
 
 def mx_gemm(a, b, out=None, out_dtype=torch.bfloat16, group_first=None, group_rows=None):
@@ -200,7 +207,7 @@ def mx_gemm(a, b, out=None, out_dtype=torch.bfloat16, group_first=None, group_ro
     _run(dev, fo.fo_mx_gemm, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
          b.codes.data_ptr(), b.scales.data_ptr(), groups,
          0 if group_first is None else group_first.data_ptr(),
-         0 if group_rows is None else group_rows.data_ptr(), out.data_ptr(), _type(out),
+         0 if group_rows is None else group_rows.data_ptr(), out.data_ptr(), _type(out.dtype),
          _row_stride(out, "out"), _status_word(dev), _stream(dev))
     return out
 
@@ -222,7 +229,7 @@ def route(logits, top_k, renormalize=True, capacity=0):
     """The top-k choice of logits [tokens, experts] (bf16 or fp32)."""
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
-    dev, type_ = _on_gpu(logits), _type(logits)
+    dev, type_ = _on_gpu(logits), _type(logits.dtype)
     T, E = logits.shape
     M, nbytes = _route_sizes(T, E, top_k, capacity)
     # (seven allocations are cheaper than one and seven views of it)
@@ -242,7 +249,7 @@ def route_backward(logits, ids, weights, dweights, renormalize=True):
     """The gradient of the logits from that of the weights (fp32)."""
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
-    dev, type_ = _on_gpu(logits, ids, weights, dweights), _type(logits)
+    dev, type_ = _on_gpu(logits, ids, weights, dweights), _type(logits.dtype)
     T, E = logits.shape
     k = ids.shape[-1]
     _int32(ids, T * k, "ids")
