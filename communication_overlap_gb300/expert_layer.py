@@ -60,14 +60,15 @@ class ExpertLayer:
     def forward(self, x):
         logits = x @ self.router.t()
         r = moe.route(logits, self.top_k, self.renormalize)
-        up = moe.mx_gemm(moe.quantize(x, row_index=r.row_token), self.w1,
-                         group_first=r.expert_first, group_rows=r.expert_rows)
-        gate, up = up.float().chunk(2, dim=1)
-        h = torch.nn.functional.silu(gate) * up
-        out = moe.mx_gemm(moe.quantize(h), self.w2, out_dtype=torch.float32,
-                          group_first=r.expert_first, group_rows=r.expert_rows)
-        rows = out[r.token_row.clamp(min=0).long()]              # [tokens, top_k, hidden]
-        y = (rows * r.weights.unsqueeze(-1) * (r.token_row >= 0).unsqueeze(-1)).sum(1)
+        groups = dict(group_first=r.expert_first, group_rows=r.expert_rows)
+        # (rows of no expert are left as they are, and nothing reads them)
+        up = torch.empty((r.row_token.numel(), self.w1.rows), dtype=torch.bfloat16,
+                         device=x.device)
+        moe.mx_gemm(moe.quantize(x, row_index=r.row_token), self.w1, out=up, **groups)
+        gate, up = up.chunk(2, dim=1)
+        h = torch.nn.functional.silu(gate).mul_(up)
+        out = moe.mx_gemm(moe.quantize(h), self.w2, out_dtype=torch.float32, **groups)
+        y = torch.bmm(r.weights.unsqueeze(1), out[r.token_row.clamp(min=0).long()]).squeeze(1)
         return y.to(x.dtype), Step(logits, r)
 
     def backward(self, step, dweights, dup):
@@ -80,8 +81,7 @@ class ExpertLayer:
         dlogits = moe.route_backward(step.logits, r.ids, r.weights, dweights, self.renormalize)
         drows = moe.mx_gemm(moe.quantize(dup), self.w1_t, out_dtype=torch.float32,
                             group_first=r.expert_first, group_rows=r.expert_rows)
-        rows = drows[r.token_row.clamp(min=0).long()]
-        dx = (rows * (r.token_row >= 0).unsqueeze(-1)).sum(1)
+        dx = (drows[r.token_row.clamp(min=0).long()] * (r.token_row >= 0).unsqueeze(-1)).sum(1)
         return dlogits, dx
 
 
