@@ -92,7 +92,7 @@ struct FewArgs {
   int64_t y_stride;
   int32_t T, H, I, E, K, renormalize, act;
   int32_t w1_rows, w2_rows;   // rows of an expert's matrices as stored
-  int32_t stages, stage_bytes;
+  int32_t ring_bytes;
   uint32_t inverse_g;
   int32_t off_lists, off_y, off_bar;      // shared memory offsets
   uint32_t* barrier;          // [0], [1] counts, [2] leave
@@ -540,6 +540,15 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
     float s0[4], s1[4];
     scales_of(lds32(scale0 + q * 512), s0);
     scales_of(lds32(scale1 + q * 512), s1);
+    // (with more than two tiles of tokens the codes are decoded once for all)
+    uint32_t p[NT > 2 ? 4 : 1][4], r[NT > 2 ? 4 : 1][4];
+    if constexpr (NT > 2) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        mx_decode8(w0[b], p[b]);
+        mx_decode8(w1[b], r[b]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
@@ -553,12 +562,15 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t p[4], r[4];
-        mx_decode8(w0[b], p);
-        mx_decode8(w1[b], r);
+        constexpr bool kOnce = NT > 2;
+        const int at = kOnce ? b : 0;
+        if constexpr (!kOnce) {
+          mx_decode8(w0[b], p[0]);
+          mx_decode8(w1[b], r[0]);
+        }
         float d[4];
-        mma16816_zero(d, p[0], r[0], p[1], r[1], t[b][0], t[b][1]);
-        mma16816<true>(d, p[2], r[2], p[3], r[3], t[b][2], t[b][3]);
+        mma16816_zero(d, p[at][0], r[at][0], p[at][1], r[at][1], t[b][0], t[b][1]);
+        mma16816<true>(d, p[at][2], r[at][2], p[at][3], r[at][3], t[b][2], t[b][3]);
         if constexpr (SECOND) {
           uint64_t lo = pack2(d[0], d[1]), hi = pack2(d[2], d[3]);
           const uint64_t u = pack2(__uint_as_float(u0[b]), __uint_as_float(u1[b]));
@@ -579,7 +591,8 @@ constexpr int kBarBytes = 8 * (2 * kMaxStages + 2) + 16;
 // Computing warps: 8 of 16 rows each, or two such sets that take turns at the
 // stages.  Decoding 4-bit weights is a chain of dependent steps (8 warps took
 // 1470 cycles for a stage that HBM delivers in 900), so it wants the second set;
-// with many tokens its registers do not fit.  The second set leaves its sums in
+// with many tokens its registers do not fit (48 tokens, 8 experts of 14336 x
+// 4096: 333 us without it, 434 with).  The second set leaves its sums in
 // shared memory and goes on; what follows a tile is the first's work.
 template <bool MX, int NT>
 constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
@@ -605,13 +618,14 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
   volatile int* abort_flag = abort_word;
   int* n_active_s = abort_word + 1;
   int* flag_s = abort_word + 2;
+  int* most_s = abort_word + 3;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int G = int(gridDim.x), c = int(blockIdx.x);
   constexpr int kGranule = MX ? 32 : 8;     // hidden rows that stay together
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&full[s]), MX ? kCopyWarps : kCopyThreads);
       mbar_init(smem_u32(&empty[s]), 8);
     }
@@ -676,7 +690,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     }
     __syncthreads();
     if (warp == 0) {
-      int rows = 0, active = 0;
+      int rows = 0, active = 0, most = 1;
       for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
         const int n = e < a.E ? count[e] : 0;
@@ -694,10 +708,13 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           ls.first[at] = int16_t(start);
         }
         if (e < a.E) count[e] = start;
+        most = max(most, n);
         rows += __shfl_sync(0xffffffffu, sum, 31);
         active += __popc(has);
       }
+      most = __reduce_max_sync(0xffffffffu, most);
       if (lane == 0) {
+        *most_s = most;
         ls.first[active] = int16_t(rows);
         *n_active_s = active;
       }
@@ -722,6 +739,13 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
     __syncthreads();
 
     const int active = *n_active_s;
+    // A stage has room for the most tokens that an expert got.
+    // (4-bit: rows up to a multiple of 8 are read and not used; they may lie in the
+    // next stage, the last stage's in what follows the ring)
+    const int most = *most_s;
+    const int stage_bytes =
+        ((MX ? kMxTokens + most * kMxToken : 32768 + (most + 7) / 8 * 8 * 256) + 1023) / 1024 * 1024;
+    const int stages = min(a.ring_bytes / stage_bytes, kMaxStages);
     const int per_expert = (a.I + kGranule - 1) / kGranule;
     const Cut cut1(active * per_expert, G, a.inverse_g);
     const int k1 = (a.H + kStageK<MX> - 1) / kStageK<MX>;      // stages of a tile of the first product
@@ -774,7 +798,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         for (int k = 0; k < k1; ++k) {
           ok = tc::wait_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, a.status);
           if (!ok) break;
-          const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+          const uint32_t dst = ring + uint32_t(stage * stage_bytes);
           {
             const uint32_t to = dst + place;
             const bool in = k * kStageK<MX> + piece * 8 < a.H;
@@ -793,7 +817,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           copies_arrive(smem_u32(&full[stage]));
           src += 256;
           tok += kStageK<MX>;
-          if (++stage == a.stages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1;
           }
@@ -830,7 +854,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       auto send_weights = [&]() {
         ok = tc::wait_warp(smem_u32(&empty[w_stage]), w_phase ^ 1, abort_flag, a.status);
         if (!ok) return;
-        const uint32_t dst = ring + uint32_t(w_stage * a.stage_bytes);
+        const uint32_t dst = ring + uint32_t(w_stage * stage_bytes);
         {
           const bool in = w.k * kStageK<MX> + piece * 8 < a.I;
           const uint32_t to = dst + place;
@@ -848,24 +872,24 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         w.src += 256;
         if (++w.k == w.r.k0 + w.r.n) open(w, true);
         ++ahead;
-        if (++w_stage == a.stages) {
+        if (++w_stage == stages) {
           w_stage = 0;
           w_phase ^= 1;
         }
       };
-      while (ok && w.more && ahead < a.stages) send_weights();
+      while (ok && w.more && ahead < stages) send_weights();
       if (ok && v.more) ok = wait_grid(a.barrier + 1, uint32_t(G), abort_flag, a.status);
       while (ok && v.more) {
         if (ahead == 0) send_weights();
         if (!ok) break;
         const int first = ls.first[v.r.a], rows = ls.first[v.r.a + 1] - first;
-        send_tokens(ring + uint32_t(stage * a.stage_bytes), (rows + 7) / 8 * 8, rows, first, v.k,
+        send_tokens(ring + uint32_t(stage * stage_bytes), (rows + 7) / 8 * 8, rows, first, v.k,
                     a.I, a.I, reinterpret_cast<const uint16_t*>(v.src), a.h, false);
         copies_arrive(smem_u32(&full[stage]));
         v.src += 256;
         if (++v.k == v.r.k0 + v.r.n) open(v, false);
         --ahead;
-        if (++stage == a.stages) stage = 0;
+        if (++stage == stages) stage = 0;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is left when the CTA exits
     } else if (MX && warp < kCopyWarps) {
@@ -888,7 +912,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       };
       auto end = [&]() {
         __syncwarp();
-        if (++stage == a.stages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -912,7 +936,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
             if (leader) {
               const uint32_t sb = !two ? 0 : kb1 - 2 * k > 1 ? 1024 : 512;
               const uint32_t bar = smem_u32(&full[stage]);
-              const uint32_t dst = ring + uint32_t(stage * a.stage_bytes);
+              const uint32_t dst = ring + uint32_t(stage * stage_bytes);
               mbar_expect_tx(bar, bytes + sb);
               tc::load_2d(dst + warp * 8192, map, bar, k * 128, row, once);
               if (two) bulk_load_hint(dst + kMxScales + warp * 2048 + 1024, scales, sb, bar, once);
@@ -925,7 +949,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           for (int k = 0; k < k1 && begin(); ++k, end()) {
             if (leader) {
               const uint32_t sb = kb1 - 2 * k > 1 ? 1024 : 512, bar = smem_u32(&full[stage]);
-              const uint32_t dst = ring + uint32_t(stage * a.stage_bytes) + kMxScales;
+              const uint32_t dst = ring + uint32_t(stage * stage_bytes) + kMxScales;
               mbar_expect_tx(bar, 2 * sb);
               bulk_load_hint(dst, gs, sb, bar, once);
               bulk_load_hint(dst + 2048, us, sb, bar, once);
@@ -939,7 +963,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           const int64_t step = int64_t(a.T) * kMxToken;
           for (int k = 0; k < k1 && begin(); ++k, end()) {
             const uint32_t bar = smem_u32(&full[stage]);
-            const uint32_t dst = ring + uint32_t(stage * a.stage_bytes) + kMxTokens + lane * kMxToken;
+            const uint32_t dst = ring + uint32_t(stage * stage_bytes) + kMxTokens + lane * kMxToken;
             if (leader) mbar_expect_tx(bar, uint32_t(rows * kMxToken));
             __syncwarp();   // (the expected bytes stand before the first that land)
             if (lane < rows) bulk_load_hint(dst, tok0, kMxToken, bar, keep);
@@ -964,7 +988,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           for (int k = r.k0; k < r.k0 + r.n && begin(); ++k, end())
             if (leader) {
               mbar_expect_tx(smem_u32(&full[stage]), 8192);
-              tc::load_2d(ring + uint32_t(stage * a.stage_bytes + warp * 8192), &a.map_w2,
+              tc::load_2d(ring + uint32_t(stage * stage_bytes + warp * 8192), &a.map_w2,
                           smem_u32(&full[stage]), k * 128, row + warp * 64, once);
             }
         } else if (warp == 2) {
@@ -973,7 +997,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
             if (leader) {
               const uint32_t sb = kb2 - 2 * k > 1 ? 1024 : 512, bar = smem_u32(&full[stage]);
               mbar_expect_tx(bar, sb);
-              bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxScales, src, sb, bar, once);
+              bulk_load_hint(ring + uint32_t(stage * stage_bytes) + kMxScales, src, sb, bar, once);
             }
             src += 1024;
           }
@@ -984,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
             if (leader) {
               const uint32_t bar = smem_u32(&full[stage]);
               mbar_expect_tx(bar, bytes);
-              bulk_load_hint(ring + uint32_t(stage * a.stage_bytes) + kMxTokens, src, bytes, bar,
+              bulk_load_hint(ring + uint32_t(stage * stage_bytes) + kMxTokens, src, bytes, bar,
                              keep);
             }
             src += int64_t(a.h_rows) * kMxToken;
@@ -1020,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
           if (!ok) break;
           if (work) {
-            const uint32_t at = ring + uint32_t(stage * a.stage_bytes);
+            const uint32_t at = ring + uint32_t(stage * stage_bytes);
             if constexpr (MX)
               stage_mx<NT, decltype(second)::value != 0>(at, code, scale0, scale1, nt,
                                                          blocks - 8 * k, acc);
@@ -1030,8 +1054,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
           stage += KS;
-          if (stage >= a.stages) {
-            stage -= a.stages;
+          if (stage >= stages) {
+            stage -= stages;
             phase ^= 1;
           }
         }
@@ -1311,12 +1335,17 @@ fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
   return FO_OK;
 }
 
+// NT of the kernel that a number of tokens takes.
+int tiles_of(int tokens) { return tokens <= 8 ? 1 : tokens <= 16 ? 2 : tokens <= 32 ? 4 : 8; }
+
 template <bool MX>
 fo_status launch_n(const FewArgs& a, int grid, int smem, cudaStream_t st) {
-  if (a.T <= 8) return launch<MX, 1>(a, grid, smem, st);
-  if (a.T <= 16) return launch<MX, 2>(a, grid, smem, st);
-  if (a.T <= 32) return launch<MX, 4>(a, grid, smem, st);
-  return launch<MX, 8>(a, grid, smem, st);
+  switch (tiles_of(a.T)) {
+    case 1: return launch<MX, 1>(a, grid, smem, st);
+    case 2: return launch<MX, 2>(a, grid, smem, st);
+    case 4: return launch<MX, 4>(a, grid, smem, st);
+    default: return launch<MX, 8>(a, grid, smem, st);
+  }
 }
 
 }  // namespace
@@ -1367,20 +1396,17 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.hb = int(mx_up(d.hidden, 128) / 128), a.ib = int(mx_up(d.inter, 128) / 128);
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
-  // an expert's tokens: all of them at most
-  // (4-bit: rows up to a multiple of 8 are read and not used; they may lie in the
-  // next stage, the last stage's in what follows the ring)
-  const int nb = int(mx_up(d.tokens, 8));
-  a.stage_bytes = int(mx_up(mx ? kMxTokens + d.tokens * kMxToken : 32768 + nb * 256, 1024));
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
   // the outputs' sums, then those of the second set on their way
-  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 8192 : 0);
+  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 4096 * tiles_of(d.tokens) : 0);
   const int tail = lists + y_bytes + kBarBytes + 1024;
-  a.stages = (kSmemLimit - tail) / a.stage_bytes;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  if (a.stages < 2) return FO_ERR_UNSUPPORTED;
+  a.ring_bytes = (kSmemLimit - tail) / 1024 * 1024;
+  // two stages at least, if one expert gets all tokens
+  const int64_t largest = mx_up(mx ? kMxTokens + d.tokens * kMxToken
+                                   : 32768 + mx_up(d.tokens, 8) * 256, 1024);
+  if (a.ring_bytes < 2 * largest) return FO_ERR_UNSUPPORTED;
   a.inverse_g = uint32_t(((1 << 24) + grid - 1) / grid);
-  a.off_lists = a.stages * a.stage_bytes;
+  a.off_lists = a.ring_bytes;
   a.off_y = a.off_lists + lists;
   a.off_bar = a.off_y + y_bytes;
   const int smem = a.off_bar + kBarBytes + 1024;
