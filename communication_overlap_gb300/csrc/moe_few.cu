@@ -406,7 +406,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Among the threads of the first set of computing warps.
+// Among the computing warps.
 constexpr int kMathThreads = 256;
 __device__ __forceinline__ void math_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kMathThreads) : "memory");
@@ -521,30 +521,37 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
                                          uint32_t scale1, int nt, int blocks,
                                          float (&acc)[NT][4]) {
   constexpr uint32_t kRow1 = SECOND ? 8 * 128 : 64 * 128;
+  // blocks whose operands are taken before the first product; with one tile of
+  // tokens there are registers for all
+  constexpr int kTake = NT == 1 ? 8 : 4;
   const int lane = threadIdx.x & 31, c = lane & 3;
   const uint32_t tokens = stage + kMxTokens + uint32_t(lane >> 2) * kMxToken + c * 16;
   const uint32_t token_scales = stage + kMxTokens + uint32_t(c * 2) * kMxToken + 512;
   code += stage;
   scale0 += stage;
   scale1 += stage;
+  // (past the matrix codes and tokens are zeros, scales whatever was there)
+  const bool two = blocks > 4;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {                // four blocks, a word of scales
-    if (q * 4 >= blocks) break;
-    uint32_t w0[4], w1[4];
+  for (int b0 = 0; b0 < 8; b0 += kTake) {
+    uint32_t w0[kTake], w1[kTake], sw0[kTake / 4], sw1[kTake / 4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t at = code ^ uint32_t((q * 4 + b) << 4);
+    for (int b = 0; b < kTake; ++b) {
+      const uint32_t at = code ^ uint32_t((b0 + b) << 4);
       w0[b] = lds32(at);
       w1[b] = lds32(at + kRow1);
     }
-    float s0[4], s1[4];
-    scales_of(lds32(scale0 + q * 512), s0);
-    scales_of(lds32(scale1 + q * 512), s1);
-    // (with more than two tiles of tokens the codes are decoded once for all)
-    uint32_t p[NT > 2 ? 4 : 1][4], r[NT > 2 ? 4 : 1][4];
-    if constexpr (NT > 2) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+    for (int q = 0; q < kTake / 4; ++q) {
+      sw0[q] = lds32(scale0 + (b0 / 4 + q) * 512);
+      sw1[q] = lds32(scale1 + (b0 / 4 + q) * 512);
+      if (b0 / 4 + q == 1 && !two) sw0[q] = sw1[q] = 0;
+    }
+    // (with more than one tile of tokens the codes are decoded once for all)
+    uint32_t p[NT > 1 ? kTake : 1][4], r[NT > 1 ? kTake : 1][4];
+    if constexpr (NT > 1) {
+#pragma unroll
+      for (int b = 0; b < kTake; ++b) {
         mx_decode8(w0[b], p[b]);
         mx_decode8(w1[b], r[b]);
       }
@@ -552,58 +559,57 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
-      uint32_t t[4][4], u0[4], u1[4];
+      uint32_t t[kTake][4], u0[kTake / 4][4], u1[kTake / 4][4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        lds128(tokens + uint32_t(j * 8) * kMxToken + (q * 4 + b) * 64, t[b]);
+      for (int b = 0; b < kTake; ++b)
+        lds128(tokens + uint32_t(j * 8) * kMxToken + (b0 + b) * 64, t[b]);
       if constexpr (SECOND) {
-        lds128(token_scales + uint32_t(j * 8) * kMxToken + q * 16, u0);
-        lds128(token_scales + uint32_t(j * 8 + 1) * kMxToken + q * 16, u1);
+#pragma unroll
+        for (int q = 0; q < kTake / 4; ++q) {
+          lds128(token_scales + uint32_t(j * 8) * kMxToken + (b0 / 4 + q) * 16, u0[q]);
+          lds128(token_scales + uint32_t(j * 8 + 1) * kMxToken + (b0 / 4 + q) * 16, u1[q]);
+        }
       }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        constexpr bool kOnce = NT > 2;
-        const int at = kOnce ? b : 0;
-        if constexpr (!kOnce) {
+      for (int b = 0; b < kTake; ++b) {
+        const int at = NT > 1 ? b : 0;
+        if constexpr (NT == 1) {
           mx_decode8(w0[b], p[0]);
           mx_decode8(w1[b], r[0]);
         }
-        float d[4];
+        float d[4], s0[4], s1[4];
         mma16816_zero(d, p[at][0], r[at][0], p[at][1], r[at][1], t[b][0], t[b][1]);
         mma16816<true>(d, p[at][2], r[at][2], p[at][3], r[at][3], t[b][2], t[b][3]);
+        scales_of(sw0[b / 4], s0);
+        scales_of(sw1[b / 4], s1);
         if constexpr (SECOND) {
           uint64_t lo = pack2(d[0], d[1]), hi = pack2(d[2], d[3]);
-          const uint64_t u = pack2(__uint_as_float(u0[b]), __uint_as_float(u1[b]));
+          const uint64_t u =
+              pack2(__uint_as_float(u0[b / 4][b % 4]), __uint_as_float(u1[b / 4][b % 4]));
           unpack2(mul2(lo, u), d[0], d[1]);
           unpack2(mul2(hi, u), d[2], d[3]);
         }
-        acc[j][0] = fmaf(d[0], s0[b], acc[j][0]);
-        acc[j][1] = fmaf(d[1], s0[b], acc[j][1]);
-        acc[j][2] = fmaf(d[2], s1[b], acc[j][2]);
-        acc[j][3] = fmaf(d[3], s1[b], acc[j][3]);
+        acc[j][0] = fmaf(d[0], s0[b % 4], acc[j][0]);
+        acc[j][1] = fmaf(d[1], s0[b % 4], acc[j][1]);
+        acc[j][2] = fmaf(d[2], s1[b % 4], acc[j][2]);
+        acc[j][3] = fmaf(d[3], s1[b % 4], acc[j][3]);
       }
     }
   }
 }
 
-constexpr int kBarBytes = 8 * (2 * kMaxStages + 2) + 16;
+constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
 
-// Computing warps: 8 of 16 rows each, or two such sets that take turns at the
-// stages.  Decoding 4-bit weights is a chain of dependent steps (8 warps took
-// 1470 cycles for a stage that HBM delivers in 900), so it wants the second set;
-// with many tokens its registers do not fit (48 tokens, 8 experts of 14336 x
-// 4096: 333 us without it, 434 with).  The second set leaves its sums in
-// shared memory and goes on; what follows a tile is the first's work.
-template <bool MX, int NT>
-constexpr int kSplit = MX && NT <= 2 ? 2 : 1;
-template <bool MX, int NT>
-constexpr int kThreads = 32 * kCopyWarps + 256 * kSplit<MX, NT>;
+// Copying warps and 8 computing warps of 16 rows each.  (With 4-bit weights a
+// second set of eight, taking turns at the stages, is no faster: 58 us instead of
+// 57 at 1 token, 154 instead of 150 at 8, and its registers do not suffice.)
+constexpr int kThreads = 32 * kCopyWarps + kMathThreads;
 
 // NT: tiles of 8 tokens, at most.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kCopyThreads = 32 * kCopyWarps;
-  constexpr int KS = kSplit<MX, NT>, kWarps = kThreads<MX, NT> / 32;
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment, for the copies' swizzle
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -613,8 +619,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
   float* yacc = reinterpret_cast<float*>(smem + a.off_y);   // [T][kYPitch]; first product: maxima
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.off_bar);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* sums = empty + kMaxStages;   // the second set's sums: there, taken
-  int* abort_word = reinterpret_cast<int*>(sums + 2);
+  int* abort_word = reinterpret_cast<int*>(empty + kMaxStages);
   volatile int* abort_flag = abort_word;
   int* n_active_s = abort_word + 1;
   int* flag_s = abort_word + 2;
@@ -629,8 +634,6 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       mbar_init(smem_u32(&full[s]), MX ? kCopyWarps : kCopyThreads);
       mbar_init(smem_u32(&empty[s]), 8);
     }
-    mbar_init(smem_u32(&sums[0]), 8);
-    mbar_init(smem_u32(&sums[1]), 8);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1022,15 +1025,12 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
       }
     } else {
       // ---------------------------------------------------------- products
-      const int mw = (warp - kCopyWarps) & 7, kh = (warp - kCopyWarps) >> 3;
+      const int mw = warp - kCopyWarps;
       const int mtid = threadIdx.x - kCopyThreads;
       const int g = lane >> 2, c2 = (lane & 3) * 2;   // row and first column of a thread's sums
-      int stage = kh;                      // this set's next stage
+      int stage = 0;
       uint32_t phase = 0;
-      int turn = 0;                        // the set whose turn is next
-      uint32_t sums_phase = 0;
       float acc[NT][4];
-      float* half_sums = yacc + a.T * kYPitch;   // [NT][8 warps][32 lanes][4]
       // `n` stages into acc; `work`: this warp's rows exist
       auto products = [&](auto second, int n, int nt, int lo, int hi, uint32_t scale0,
                           uint32_t scale1, int blocks, bool work) {
@@ -1040,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
         const uint32_t code = code_place(lo + g, 0) + (lane & 3) * 4;   // 4-bit
         bool ok = true;
-        for (int k = KS == 1 ? 0 : turn ^ kh; k < n; k += KS) {
+        for (int k = 0; k < n; ++k) {
           ok = tc::wait_warp(smem_u32(&full[stage]), phase, abort_flag, a.status);
           if (!ok) break;
           if (work) {
@@ -1053,35 +1053,10 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
-          stage += KS;
-          if (stage >= stages) {
-            stage -= stages;
+          if (++stage == stages) {
+            stage = 0;
             phase ^= 1;
           }
-        }
-        turn ^= n & 1;
-        if constexpr (KS == 2) {
-          float* to = half_sums + (mw * 32 + lane) * 4;
-          if (kh == 1) {
-            ok = ok && tc::wait_warp(smem_u32(&sums[1]), sums_phase ^ 1, abort_flag, a.status);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              *reinterpret_cast<float4*>(to + j * 1024) =
-                  make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sums[0]));
-            sums_phase ^= 1;
-            return ok;
-          }
-          ok = ok && tc::wait_warp(smem_u32(&sums[0]), sums_phase, abort_flag, a.status);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(to + j * 1024);
-            acc[j][0] += v.x, acc[j][1] += v.y, acc[j][2] += v.z, acc[j][3] += v.w;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sums[1]));
-          sums_phase ^= 1;
         }
         return math_all(ok);
       };
@@ -1099,7 +1074,6 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                       kMxScales + 2048 + (ur >> 7) * 1024 + mx_scale_row(ur & 127),
                       (a.H + 31) / 32, mw * 8 < t.n);
         if (!ok) break;
-        if (KS == 2 && kh == 1) continue;
         float h[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -1165,10 +1139,8 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         }
       }
       // this CTA's hidden values are written
-      if (kh == 0) {
-        if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
-        math_sync();
-      }
+      if constexpr (MX) asm volatile("fence.proxy.async;" ::: "memory");
+      math_sync();
       if (mtid == 0) {     // (a release: what stood before the barrier above is in it)
         uint32_t old;
         asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
@@ -1232,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         math_sync();   // the sums may be overwritten
       };
       while (ok && out.next(active, k2, r)) {
-        if (kh == 0 && r.rb != rb) {
+        if (r.rb != rb) {
           if (rb >= 0) flush();
           rb = r.rb;
           for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
@@ -1243,7 +1215,6 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
                       kMxScales + mx_scale_row(mw * 16 + 8 + g), (a.I + 31) / 32 - 8 * r.k0,
                       r.rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
         if (!ok) break;
-        if (KS == 2 && kh == 1) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if (j * 8 >= rows) break;
@@ -1260,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads<MX, NT>, 1) few_kernel(const __grid_c
         __syncwarp();   // another lane may add to the same sum next
       }
       if (ok && rb >= 0) flush();
-      if (active == 0 && kh == 0) {   // no token has an expert: zeros
+      if (active == 0) {   // no token has an expert: zeros
         for (int64_t j = int64_t(c) * kMathThreads + mtid; j < int64_t(a.T) * a.H;
              j += int64_t(G) * kMathThreads)
           reinterpret_cast<__nv_bfloat16*>(a.y)[j / a.H * a.y_stride + j % a.H] =
@@ -1320,7 +1291,7 @@ fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
   if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads<MX, NT>);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1335,17 +1306,12 @@ fo_status launch(const FewArgs& a, int grid, int smem, cudaStream_t st) {
   return FO_OK;
 }
 
-// NT of the kernel that a number of tokens takes.
-int tiles_of(int tokens) { return tokens <= 8 ? 1 : tokens <= 16 ? 2 : tokens <= 32 ? 4 : 8; }
-
 template <bool MX>
 fo_status launch_n(const FewArgs& a, int grid, int smem, cudaStream_t st) {
-  switch (tiles_of(a.T)) {
-    case 1: return launch<MX, 1>(a, grid, smem, st);
-    case 2: return launch<MX, 2>(a, grid, smem, st);
-    case 4: return launch<MX, 4>(a, grid, smem, st);
-    default: return launch<MX, 8>(a, grid, smem, st);
-  }
+  if (a.T <= 8) return launch<MX, 1>(a, grid, smem, st);
+  if (a.T <= 16) return launch<MX, 2>(a, grid, smem, st);
+  if (a.T <= 32) return launch<MX, 4>(a, grid, smem, st);
+  return launch<MX, 8>(a, grid, smem, st);
 }
 
 }  // namespace
@@ -1397,8 +1363,8 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
-  // the outputs' sums, then those of the second set on their way
-  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx && d.tokens <= 16 ? 4096 * tiles_of(d.tokens) : 0);
+  // the outputs' sums; past the ring's end 4-bit tokens that nobody uses are read
+  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx ? 8 * kMxToken : 0);
   const int tail = lists + y_bytes + kBarBytes + 1024;
   a.ring_bytes = (kSmemLimit - tail) / 1024 * 1024;
   // two stages at least, if one expert gets all tokens
