@@ -17,9 +17,9 @@
 //  * warps 2-5: epilogue.  Sums to bf16 or fp32, transposed through shared
 //    memory so that a row's stores are whole 128-byte segments.
 //  * warps 6-9: the stages' scales from shared to tensor memory, through
-//    registers (tcgen05.st, a quarter of the lanes per warp), a slot per stage.  tcgen05.cp does the same from the MMA's thread, but in line with
-//    the MMAs: the 8-expert product of 32768 x 14336 x 4096 took 1163 us with
-//    six copies per stage, against 774 us with the copies (wrongly) left out.
+//    registers (tcgen05.st, a quarter of the lanes per warp), a slot per stage.
+//    tcgen05.cp does the same from the MMA's thread, but in line with the MMAs:
+//    the 8-expert product of 32768 x 14336 x 4096 took 1163 us with it.
 // The PAIR form computes 256 x BN with one cta_group::2 MMA: each CTA holds
 // 128 rows of A, half of B's rows and all of B's scales.
 //
@@ -27,7 +27,15 @@
 // columns.  BN = 256 leaves room for 392 columns of sums, so the second sum
 // starts at column 136 and shares 120 columns with the first: the epilogue
 // drains a tile's 128 columns on that side first, and the next tile's MMAs wait
-// for those only.
+// for those only.  (BN = 192 needs no sharing but moves more per MMA: 635 us
+// instead of 565 for the 8-expert product.)
+//
+// Measured: 565 us for 32768 rows over 8 experts, N = 14336, K = 4096 (6.8
+// PFLOP/s at the 1.67 GHz that the power limit leaves), 41 us for 8192 x 4096 x
+// 2752 with fp32 output (writing that alone takes 21), 10.4 us for 512 x 4096 x
+// 4096.  Of a tile's 10100 cycles at K = 4096 the MMAs take 8500; the rest is
+// the wait for the shared columns.  A second set of epilogue warps changes
+// nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -532,9 +540,11 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
   const int64_t groups = n_groups > 0 ? n_groups : 1;
   const int64_t kb = mx_up(K, 128) / 128;               // blocks of scales per row of blocks
   const int64_t mb = mx_up(M, 128) / 128, nb = mx_up(N, 128) / 128 * groups;
-  // A pair reads half as much of B per CTA; with no more rows than one CTA
-  // takes, its second half would be empty.
-  const bool pair = M > 128;
+  // A pair reads half as much of B per CTA, and its tiles are four times as
+  // large: while those of one CTA all run at once, they are faster (512 x 4096 x
+  // 4096: 10.4 us, pairs 12.4; 1024 x 4096 x 4096: 14.5 and 12.4), and with no
+  // more rows than one CTA takes a pair's second half would be empty.
+  const bool pair = M > 128 && mb * (nb / groups) > sms;
   GemmArgs a{};
   a.bn = pair ? 256 : 128;
   a.acc1 = kSf0 - a.bn < a.bn ? kSf0 - a.bn : a.bn;

@@ -235,6 +235,39 @@ def test_product_per_expert(rows, out):
     assert moe.device_status() == fo.FO_OK
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows", [[300, 0, 257, 1, 1200, 128], [2000], [513] * 4])
+def test_product_per_expert_of_many_tiles(rows, out):
+    """More tiles than the GPU has SMs, with ragged ends in both directions."""
+    first = [sum(-(-r // 128) * 128 for r in rows[:g]) for g in range(len(rows))]
+    M, N, K = first[-1] + -(-rows[-1] // 128) * 128, 1301, 333
+    qa, qb, av, bv = product_case(M, N, K, out, sum(rows) + 1, rows)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    d = torch.full((M, N), 7.0, dtype=out, device="cuda")
+    if len(rows) == 1:
+        qb = moe.MxTensor(qb.codes, qb.scales, 1, N, K)
+    moe.mx_gemm(qa, qb, out=d, group_first=dev(first), group_rows=dev(rows))
+    used = np.zeros(M, dtype=bool)
+    for g, (f, r) in enumerate(zip(first, rows)):
+        used[f:f + r] = True
+        if r:
+            product_close(d[f:f + r], av[f:f + r], bv[g], out)
+    assert (host(d)[~used] == 7.0).all()
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("pad, offset", [(0, 0), (3, 1), (8, 4)])
+def test_product_of_many_ragged_tiles(pad, offset, out):
+    M, N, K = 1930, 1301, 333
+    qa, qb, av, bv = product_case(M, N, K, out, 12)
+    buf = torch.full((M * (N + pad) + offset + 64,), 7.0, dtype=out, device="cuda")
+    view = buf[offset:offset + M * (N + pad)].view(M, N + pad)[:, :N]
+    moe.mx_gemm(qa, qb, out=view)
+    product_close(view, av, bv[0], out)
+    view.fill_(7.0)
+    assert bool((buf == 7.0).all())
+
+
 @pytest.mark.parametrize("first, rows", [
     ([0, 64], [64, 64]), ([0, -128], [64, 64]), ([0, 128], [64, -1]), ([0, 256], [64, 1]),
     ([0, 128], [64, 2 ** 31 - 1])])
