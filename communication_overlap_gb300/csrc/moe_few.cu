@@ -518,15 +518,18 @@ __device__ __forceinline__ void scales_of(uint32_t w, float (&s)[4]) {
 // are; blocks: of the stage's eight, those that exist.
 template <int NT, bool SECOND>
 __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t scale0,
-                                         uint32_t scale1, int nt, int blocks,
+                                         uint32_t scale1, int rows, int blocks,
                                          float (&acc)[NT][4]) {
   constexpr uint32_t kRow1 = SECOND ? 8 * 128 : 64 * 128;
   // blocks whose operands are taken before the first product; with one tile of
   // tokens there are registers for all
   constexpr int kTake = NT == 1 ? 8 : 4;
   const int lane = threadIdx.x & 31, c = lane & 3;
-  const uint32_t tokens = stage + kMxTokens + uint32_t(lane >> 2) * kMxToken + c * 16;
-  const uint32_t token_scales = stage + kMxTokens + uint32_t(c * 2) * kMxToken + 512;
+  // rows past the last token's read that one again, which costs nothing (a row of
+  // its own for each of the eight: 416 cycles of shared memory per stage)
+  const auto token = [&](int i) {
+    return stage + kMxTokens + uint32_t(min(i, rows - 1)) * kMxToken;
+  };
   code += stage;
   scale0 += stage;
   scale1 += stage;
@@ -534,7 +537,8 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
   const bool two = blocks > 4;
 #pragma unroll
   for (int b0 = 0; b0 < 8; b0 += kTake) {
-    uint32_t w0[kTake], w1[kTake], sw0[kTake / 4], sw1[kTake / 4];
+    uint32_t w0[kTake], w1[kTake];
+    float s0[kTake / 4][4], s1[kTake / 4][4];
 #pragma unroll
     for (int b = 0; b < kTake; ++b) {
       const uint32_t at = code ^ uint32_t((b0 + b) << 4);
@@ -543,9 +547,9 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
     }
 #pragma unroll
     for (int q = 0; q < kTake / 4; ++q) {
-      sw0[q] = lds32(scale0 + (b0 / 4 + q) * 512);
-      sw1[q] = lds32(scale1 + (b0 / 4 + q) * 512);
-      if (b0 / 4 + q == 1 && !two) sw0[q] = sw1[q] = 0;
+      const bool in = b0 / 4 + q == 0 || two;
+      scales_of(in ? lds32(scale0 + (b0 / 4 + q) * 512) : 0u, s0[q]);
+      scales_of(in ? lds32(scale1 + (b0 / 4 + q) * 512) : 0u, s1[q]);
     }
     // (with more than one tile of tokens the codes are decoded once for all)
     uint32_t p[NT > 1 ? kTake : 1][4], r[NT > 1 ? kTake : 1][4];
@@ -558,16 +562,16 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if (j >= nt) break;
+      if (j * 8 >= rows) break;
       uint32_t t[kTake][4], u0[kTake / 4][4], u1[kTake / 4][4];
 #pragma unroll
       for (int b = 0; b < kTake; ++b)
-        lds128(tokens + uint32_t(j * 8) * kMxToken + (b0 + b) * 64, t[b]);
+        lds128(token(j * 8 + (lane >> 2)) + c * 16 + (b0 + b) * 64, t[b]);
       if constexpr (SECOND) {
 #pragma unroll
         for (int q = 0; q < kTake / 4; ++q) {
-          lds128(token_scales + uint32_t(j * 8) * kMxToken + (b0 / 4 + q) * 16, u0[q]);
-          lds128(token_scales + uint32_t(j * 8 + 1) * kMxToken + (b0 / 4 + q) * 16, u1[q]);
+          lds128(token(j * 8 + c * 2) + 512 + (b0 / 4 + q) * 16, u0[q]);
+          lds128(token(j * 8 + c * 2 + 1) + 512 + (b0 / 4 + q) * 16, u1[q]);
         }
       }
 #pragma unroll
@@ -577,11 +581,9 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
           mx_decode8(w0[b], p[0]);
           mx_decode8(w1[b], r[0]);
         }
-        float d[4], s0[4], s1[4];
+        float d[4];
         mma16816_zero(d, p[at][0], r[at][0], p[at][1], r[at][1], t[b][0], t[b][1]);
         mma16816<true>(d, p[at][2], r[at][2], p[at][3], r[at][3], t[b][2], t[b][3]);
-        scales_of(sw0[b / 4], s0);
-        scales_of(sw1[b / 4], s1);
         if constexpr (SECOND) {
           uint64_t lo = pack2(d[0], d[1]), hi = pack2(d[2], d[3]);
           const uint64_t u =
@@ -589,10 +591,10 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
           unpack2(mul2(lo, u), d[0], d[1]);
           unpack2(mul2(hi, u), d[2], d[3]);
         }
-        acc[j][0] = fmaf(d[0], s0[b % 4], acc[j][0]);
-        acc[j][1] = fmaf(d[1], s0[b % 4], acc[j][1]);
-        acc[j][2] = fmaf(d[2], s1[b % 4], acc[j][2]);
-        acc[j][3] = fmaf(d[3], s1[b % 4], acc[j][3]);
+        acc[j][0] = fmaf(d[0], s0[b / 4][b % 4], acc[j][0]);
+        acc[j][1] = fmaf(d[1], s0[b / 4][b % 4], acc[j][1]);
+        acc[j][2] = fmaf(d[2], s1[b / 4][b % 4], acc[j][2]);
+        acc[j][3] = fmaf(d[3], s1[b / 4][b % 4], acc[j][3]);
       }
     }
   }
@@ -743,8 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
     const int active = *n_active_s;
     // A stage has room for the most tokens that an expert got.
-    // (4-bit: rows up to a multiple of 8 are read and not used; they may lie in the
-    // next stage, the last stage's in what follows the ring)
     const int most = *most_s;
     const int stage_bytes =
         ((MX ? kMxTokens + most * kMxToken : 32768 + (most + 7) / 8 * 8 * 256) + 1023) / 1024 * 1024;
@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       uint32_t phase = 0;
       float acc[NT][4];
       // `n` stages into acc; `work`: this warp's rows exist
-      auto products = [&](auto second, int n, int nt, int lo, int hi, uint32_t scale0,
+      auto products = [&](auto second, int n, int rows, int lo, int hi, uint32_t scale0,
                           uint32_t scale1, int blocks, bool work) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1046,10 +1046,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           if (work) {
             const uint32_t at = ring + uint32_t(stage * stage_bytes);
             if constexpr (MX)
-              stage_mx<NT, decltype(second)::value != 0>(at, code, scale0, scale1, nt,
+              stage_mx<NT, decltype(second)::value != 0>(at, code, scale0, scale1, rows,
                                                          blocks - 8 * k, acc);
             else
-              stage_bf16<NT>(at, lo, hi, nt, acc);
+              stage_bf16<NT>(at, lo, hi, (rows + 7) / 8, acc);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // a 4-bit row's scales: in the blocks of the tile's gate or up rows
         const int p = mw * 8 + g;                 // this thread's hidden row
         const int gr = (t.i0 & 127) + p, ur = ((t.i0 + a.I) & 127) + p;
-        ok = products(Const<0>{}, k1, nb / 8, mw * 8, 64 + mw * 8,
+        ok = products(Const<0>{}, k1, rows, mw * 8, 64 + mw * 8,
                       kMxScales + (gr >> 7) * 1024 + mx_scale_row(gr & 127),
                       kMxScales + 2048 + (ur >> 7) * 1024 + mx_scale_row(ur & 127),
                       (a.H + 31) / 32, mw * 8 < t.n);
@@ -1210,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           for (int i = mtid; i < a.T * kYPitch; i += kMathThreads) yacc[i] = 0.0f;
         }
         const int first = ls.first[r.a], rows = ls.first[r.a + 1] - first;
-        ok = products(Const<1>{}, r.n, (rows + 7) / 8, mw * 16, mw * 16 + 8,
+        ok = products(Const<1>{}, r.n, rows, mw * 16, mw * 16 + 8,
                       kMxScales + mx_scale_row(mw * 16 + g),
                       kMxScales + mx_scale_row(mw * 16 + 8 + g), (a.I + 31) / 32 - 8 * r.k0,
                       r.rb * 128 + mw * 16 < a.H);   // (and the zeros are set)
@@ -1363,8 +1363,7 @@ fo_status launch_moe_few(const fo_moe_few_desc& d, const void* x, int64_t x_stri
   a.parts = reinterpret_cast<float*>(ws + l.parts);
   a.status = dev_status;
   const int lists = lists_bytes(d.tokens * d.top_k, d.experts);
-  // the outputs' sums; past the ring's end 4-bit tokens that nobody uses are read
-  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128)) + (mx ? 8 * kMxToken : 0);
+  const int y_bytes = int(mx_up(d.tokens * kYPitch * 4, 128));   // the outputs' sums
   const int tail = lists + y_bytes + kBarBytes + 1024;
   a.ring_bytes = (kSmemLimit - tail) / 1024 * 1024;
   // two stages at least, if one expert gets all tokens
