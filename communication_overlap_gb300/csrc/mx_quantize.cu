@@ -122,7 +122,7 @@ int rows_align(const void* p, int64_t batch, int64_t batch_stride, int64_t row_s
 
 // Rows of the source (or gathered rows of it) become rows of the result.
 // ALIGN: what the rows' addresses are a multiple of, in bytes.
-template <typename T, int ALIGN>
+template <typename T, int ALIGN, bool GATHER>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) quantize_rows_kernel(const QuantArgs a) {
   __shared__ __align__(16) uint32_t scale_block[kMxScaleBytes / 4];
   int64_t id = blockIdx.x;
@@ -139,28 +139,35 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) quantize_row
   const int64_t pitch = int64_t(a.col_blocks) * 64;
   uint8_t* codes = a.codes + (b * a.row_blocks + rb) * int64_t(kMxRows) * pitch + c0 / 2;
   // which rows, then all loads, then the rest: no load waits for another
-  const T* from[8];                                // null: a row of zeros
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = int64_t(rb) * kMxRows + p * 16 + r0;
-    int64_t row = r < a.rows ? r : -1;
-    if (a.row_index != nullptr && r < a.rows) {
-      row = a.row_index[r];
-      if (row >= a.src_rows) row = -1;
-    }
-    from[p] = row < 0 ? nullptr : src + row * a.row_stride + c0;
-  }
+  const int64_t first = int64_t(rb) * kMxRows + r0;
   Eight<T> v[8];
-  if (valid == 8) {
+  const auto load = [&](int p, const T* from, bool live) {
+    if (valid == 8) {
+      v[p].zero();
+      if (live) v[p].template load<ALIGN>(from);
+    } else {
+      v[p].load_some(from, live ? valid : 0);
+    }
+  };
+  if constexpr (GATHER) {
+    int32_t row[8];                                // -1: a row of zeros
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      v[p].zero();
-      if (from[p] != nullptr) v[p].template load<ALIGN>(from[p]);
+      row[p] = first + p * 16 < a.rows ? __ldg(a.row_index + first + p * 16) : -1;
+      if (row[p] >= a.src_rows) row[p] = -1;
     }
-  } else {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) v[p].load_some(from[p], from[p] != nullptr ? valid : 0);
+    for (int p = 0; p < 8; ++p) load(p, src + int64_t(row[p]) * a.row_stride + c0, row[p] >= 0);
+  } else {
+    const int left = int(min(a.rows - first, int64_t(kMxRows)));
+    const T* from = src + first * a.row_stride + c0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      load(p, from, p * 16 < left);
+      from += 16 * a.row_stride;
+    }
   }
+  uint8_t* to = codes + int64_t(r0) * pitch;
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int r = p * 16 + r0;
@@ -173,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) quantize_row
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = v[p].value(i) * inv;
     const uint32_t q = mx_encode8(u);
-    __stcs(reinterpret_cast<uint32_t*>(codes + int64_t(r) * pitch), s == 255u ? 0u : q);
+    __stcs(reinterpret_cast<uint32_t*>(to), s == 255u ? 0u : q);
+    to += 16 * pitch;
     if ((threadIdx.x & 3) == 0)
       reinterpret_cast<uint8_t*>(scale_block)[mx_scale_row(r) + (col >> 5)] = uint8_t(s);
   }
@@ -459,6 +467,26 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
   }
 }
 
+template <typename T, int ALIGN>
+void launch_rows_by(const QuantArgs& a, unsigned grid, cudaStream_t st) {
+  if (a.row_index != nullptr)
+    quantize_rows_kernel<T, ALIGN, true><<<grid, kThreads, 0, st>>>(a);
+  else
+    quantize_rows_kernel<T, ALIGN, false><<<grid, kThreads, 0, st>>>(a);
+}
+
+template <typename T>
+void launch_rows(const QuantArgs& a, int align, unsigned grid, cudaStream_t st) {
+  if (align == 16)
+    launch_rows_by<T, 16>(a, grid, st);
+  else if (align == 8)
+    launch_rows_by<T, 8>(a, grid, st);
+  else if (align == 4)
+    launch_rows_by<T, 4>(a, grid, st);
+  else
+    launch_rows_by<T, sizeof(T)>(a, grid, st);
+}
+
 template <typename T>
 fo_status launch_cols(const QuantArgs& a, unsigned grid, cudaStream_t st) {
   constexpr int bytes = TileOf<T>::kBytes;
@@ -489,14 +517,9 @@ fo_status launch_mx_quantize(const void* src, fo_type type, int64_t batch, int64
   const unsigned grid = unsigned(blocks);
   const int align = rows_align(src, batch, batch_stride, row_stride, type == FO_TYPE_BF16 ? 2 : 4);
   if (type == FO_TYPE_BF16)
-    (align == 16  ? quantize_rows_kernel<uint16_t, 16>
-     : align == 8 ? quantize_rows_kernel<uint16_t, 8>
-     : align == 4 ? quantize_rows_kernel<uint16_t, 4>
-                  : quantize_rows_kernel<uint16_t, 2>)<<<grid, kThreads, 0, st>>>(a);
+    launch_rows<uint16_t>(a, align, grid, st);
   else
-    (align == 16  ? quantize_rows_kernel<float, 16>
-     : align == 8 ? quantize_rows_kernel<float, 8>
-                  : quantize_rows_kernel<float, 4>)<<<grid, kThreads, 0, st>>>(a);
+    launch_rows<float>(a, align, grid, st);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
