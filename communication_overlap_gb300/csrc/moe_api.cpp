@@ -208,9 +208,6 @@ fo_status fo_moe_few(const fo_moe_few_desc* d, const void* x, int64_t x_stride,
       !fo::aligned16(W1_scales) || !fo::aligned16(W2_scales) || !fo::aligned16(workspace) ||
       !fo::aligned4(dev_status) || !aligned_type(y, FO_TYPE_BF16))
     return FO_ERR_ARG;
-  // the copies that expand 4-bit codes start on 32 bytes
-  if (mx && ((reinterpret_cast<uintptr_t>(W1) | reinterpret_cast<uintptr_t>(W2)) & 31))
-    return FO_ERR_ARG;
   // rows of all experts are indexed with 32 bits
   if (!fits_int32(int64_t(d->experts) * ((2 * int64_t(d->inter) + 127) / 128 * 128)) ||
       !fits_int32(int64_t(d->experts) * ((int64_t(d->hidden) + 127) / 128 * 128)))

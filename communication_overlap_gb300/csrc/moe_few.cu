@@ -6,15 +6,13 @@
 // and does almost nothing with it: HBM bounds it, and what must not happen is
 // that the reads pause.  So:
 //  * One persistent CTA per SM (a cooperative launch).  Four warps copy
-//    weights through a deep ring of stages (128 rows x 128 columns), eight warps
-//    consume them with mma.sync, a few tokens being the narrow side (16 weight
-//    rows x 8 tokens x 16 columns).  At one SM's share of HBM a bf16 stage of 32
-//    KB takes about 1400 cycles to arrive and its products take under 200 per
-//    8 tokens, so the rate of the tensor cores does not matter here.
+//    weights through a deep ring of stages (128 rows x 128 columns of bf16, or x
+//    256 of 4 bits), eight warps consume them with mma.sync, a few tokens being
+//    the narrow side (16 weight rows x 8 tokens x 16 columns).
 //  * Work is cut evenly, whatever the routing: the hidden rows of all reached
 //    experts are one line of granules and CTA c takes the c-th part of it; the
-//    output product is one line of (128 output rows, expert, 128 columns)
-//    stages, cut the same way.
+//    output product is one line of (128 output rows, expert, stage of columns),
+//    cut the same way.
 //  * A warp's 16 rows are 8 gate rows and their 8 up rows, which puts both
 //    sums of a hidden row in one thread: the activation happens in registers
 //    and only the hidden values (a few rows) travel through memory, inside L2.
@@ -23,10 +21,24 @@
 //  * Output rows shared by several CTAs are joined by the last of them to
 //    finish, which adds the parts in CTA order: the same bits in every run.
 //
-// bf16 weights: bf16 products, h rounded to bf16 (x has no more).  4-bit
-// weights: codes become f16 in registers (exact), x and h are f16 with a
-// power-of-two scale per 32 values (11 significant bits), a block's sum of 32
-// products starts at zero and is added times both scales in fp32.
+// bf16 weights: copied 16 bytes per thread (cp.async: rows of any multiple of
+// 16 bytes); bf16 products, h rounded to bf16 as an operand of such (x has no
+// more bits).  4-bit weights: bulk copies of codes and scales as they are kept;
+// codes become f16 in registers (exact), x and h are f16 (11 bits) with a
+// power-of-two scale per token and per 32 values; a block's sum of 32 products
+// starts at zero and is added times the scales in fp32.
+//
+// Measured (8 experts, hidden 4096, inter 14336, top 2; bytes are those of the
+// reached experts' weights):
+//   bf16   1 token 117 us (6.0 TB/s), 8 tokens 366 (6.7), 48 tokens 419 (6.7):
+//          the reads, and 20 us around them (launch, router and choice 6, the two
+//          barriers, the join)
+//   4-bit  1 token 56 us (3.4 TB/s), 8 tokens 147 (4.5), 48 tokens 280 (2.7): the
+//          computing warps.  A stage of 20 KB takes them 800 to 900 cycles (HBM
+//          750 to 880) for one tile of tokens, nearly twice that for two: each
+//          word of codes passes through registers, and 8 warps start on a stage
+//          together.  Tried: 16 warps that halve a stage's columns or take turns
+//          at stages (no faster), operands taken half a stage ahead (15% slower).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -456,7 +468,7 @@ __device__ __forceinline__ bool wait_grid(const uint32_t* count, uint32_t target
 // tiles of 8 tokens.  The weights' 16 rows x 128 columns are taken first, then
 // two tiles of tokens at a time: eight independent steps' loads, and two chains
 // of products (with the columns outermost a step waited for its own loads: 1330
-// cycles per stage instead of 500 at 12 tokens).
+// cycles per stage instead of 740 at 12 tokens).
 template <int NT>
 __device__ __forceinline__ void stage_bf16(uint32_t stage, int lo, int hi, int nt,
                                            float (&acc)[NT][4]) {

@@ -6,10 +6,16 @@
 // are exact and the only rounding is the one to E2M1.
 //
 // Both directions move each byte once and compute almost nothing: HBM bounds
-// them.  A CTA takes one block of scales (128 rows x 128 columns): 256
-// threads, each 8 rows apart x 8 columns, all loads issued before the first
-// use (16 bytes x 8 per thread of bf16), four neighbouring lanes to a block of
-// 32.
+// them, and the instructions per value come close (12 to quantize, 9 back: the
+// issue slots are 70% busy).  A CTA takes one block of scales (128 rows x 128
+// columns): 256 threads, each 8 rows 16 apart x 8 columns, all loads issued
+// before the first use (16 bytes x 8 per thread of bf16), four neighbouring lanes
+// to a block of 32.  (512 threads over two blocks of columns, for longer pieces
+// of a row: 78 us instead of 53.)
+//
+// Measured at 32768 x 4096 (bf16, fp32): quantize 53 us (6.4 TB/s) and 89 (6.9),
+// gathered rows 56 and 93, transposed 60 (5.7) and 122 (5.0), back 53 (6.4) and
+// 91 (6.7).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -59,11 +59,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return out;
 }
 
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
-}
-
 // No release ordering: for threads whose work before it is tensor memory
 // stores they have waited for (tcgen05.wait::st).
 __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t addr) {

@@ -708,12 +708,13 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
  *      rounded to bf16.
  *  weights FO_TYPE_MX4: each expert's W1 (2 inter x hidden) and W2 (hidden x
  *      inter) in the 4-bit form (a batch of `experts`); x and the hidden
- *      values are taken at no less than bf16's 8 significant bits.
+ *      values are taken as f16 (11 significant bits) with a power-of-two scale
+ *      per token and per 32 hidden values: values below 2^-28 of the largest
+ *      under their scale keep fewer, and an infinity makes the scale a NaN.
  *  tokens 0 .. FO_MOE_FEW_TOKENS, experts <= 1024, top_k <= 32, hidden and
  *  inter multiples of 8.
  *  x: bf16, x_stride (elements) >= hidden; y: bf16, y_stride >= hidden.  x
- *      and the weights 16-byte aligned (4-bit codes 32), x_stride a multiple
- *      of 8.
+ *      and the weights 16-byte aligned, x_stride a multiple of 8.
  *  router: bf16 [experts][hidden], 16-byte aligned.
  *  workspace: as for fo_moe_route (zeroed once before its first use, calls of
  *      any shape may share one; zero it again after FO_ERR_TIMEOUT). */
