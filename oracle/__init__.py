@@ -21,6 +21,7 @@ Modules:
   gemm    -- fp64-accumulated GEMM rounded once to bf16
   comm    -- pre-comm reorder, the four communication stand-ins, post-comm reorder
   pipeline-- one whole pass of the path (used by tests and the CPU baseline)
+  moe     -- the expert layer's operators (router, 4-bit form, product, few tokens) in 64 bits
 
 Where the pages leave a step open, the function that takes the step states
 the reading it uses in its own docstring.
