@@ -27,15 +27,20 @@
 // columns.  BN = 256 leaves room for 392 columns of sums, so the second sum
 // starts at column 136 and shares 120 columns with the first: the epilogue
 // drains a tile's 128 columns on that side first, and the next tile's MMAs wait
-// for those only.  (BN = 192 needs no sharing but moves more per MMA: 635 us
-// instead of 565 for the 8-expert product.)
+// for those only.
+//
+// What bounds it: a stage of the PAIR form brings 35 KB into an SM, 550 cycles at
+// the 64 bytes per cycle that L2 delivers to one, and its MMAs take 512; of a
+// tile's 10100 cycles at K = 4096 about 1150 are the wait for the shared columns.
+// Narrower tiles need no sharing but more bytes per product: the 8-expert product
+// below takes 609 us with 192 columns and 806 with 128, and a sixth stage changes
+// neither.  Nor do scales in a ring of their own, ahead of the codes, or a second
+// set of epilogue warps.
 //
 // Measured: 565 us for 32768 rows over 8 experts, N = 14336, K = 4096 (6.8
-// PFLOP/s at the 1.67 GHz that the power limit leaves), 41 us for 8192 x 4096 x
-// 2752 with fp32 output (writing that alone takes 21), 10.4 us for 512 x 4096 x
-// 4096.  Of a tile's 10100 cycles at K = 4096 the MMAs take 8500; the rest is
-// the wait for the shared columns.  A second set of epilogue warps changes
-// nothing.
+// PFLOP/s at the 1.67 GHz that the power limit leaves; 630 us in a long run), 41
+// us for 8192 x 4096 x 2752 with fp32 output (writing that alone takes 21), 10.4
+// us for 512 x 4096 x 4096.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
