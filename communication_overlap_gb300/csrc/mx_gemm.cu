@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
     if (!ok && a.k_stages > 0 && leader && (!codes || rank == 0)) {
       // winding down: copies already issued land before the CTA exits
       for (int s = 0; s < kStages; ++s) {
-        // the parity of stage s's last fill: this round's, or the one before
+        // the parity of stage s's last fill: this pass's, or that of the one before
         const uint32_t parity = s < stage ? phase : phase ^ 1;
         if ((filled >> s) & 1u) tc::wait_drain(smem_u32(codes ? &full[s] : &sf_full[s]), parity);
       }
