@@ -37,7 +37,7 @@
 // neither.  Nor do scales in a ring of their own, ahead of the codes, or a second
 // set of epilogue warps.
 //
-// Measured: 565 us for 32768 rows over 8 experts, N = 14336, K = 4096 (6.8
+// Measured: 552 us for 32768 rows over 8 experts, N = 14336, K = 4096 (7.0
 // PFLOP/s at the 1.67 GHz that the power limit leaves; 630 us in a long run), 41
 // us for 8192 x 4096 x 2752 with fp32 output (writing that alone takes 21), 10.4
 // us for 512 x 4096 x 4096.
@@ -99,6 +99,54 @@ __device__ __forceinline__ uint32_t instruction(int m, int n) {
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// The first `rows` rows and n columns of a staging buffer to D, by a warp: by
+// words, a lane each, where D's rows start on words, else by elements; eight rows
+// at a time.  (Row by row, 16602 x 645 x 275 with fp32 output took 48 us and 4234
+// x 3092 x 202 with bf16 41, this way 26 and 19.  Out of line: inlined, it makes
+// the copies' path slower, 4234 x 3096 x 202 14.4 us instead of 12.5.)
+template <bool BF16>
+static __device__ __noinline__ void store_rows(uint32_t buf, uint8_t* to, int64_t pitch, int rows,
+                                               int n) {
+  const int lane = threadIdx.x & 31;
+  const auto staged = [&](int row, int byte) {
+    return buf + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
+  };
+  const bool words = ((reinterpret_cast<uintptr_t>(to) | uintptr_t(pitch)) & 3) == 0;
+#pragma unroll 1
+  for (int r = 0; r < rows; r += 8) {
+    if (!BF16 || words) {
+      constexpr int kPer = BF16 ? 2 : 1;       // columns of a word
+      uint32_t x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[i]) : "r"(staged(r + i, lane * 4)) : "memory");
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r + i < rows && lane * kPer + kPer <= n)
+          *reinterpret_cast<uint32_t*>(to + int64_t(r + i) * pitch + lane * 4) = x[i];
+      if (BF16 && (n & 1) && lane < 8 && r + lane < rows) {   // the last column
+        uint16_t e;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(e) : "r"(staged(r + lane, (n - 1) * 2)) : "memory");
+        *reinterpret_cast<uint16_t*>(to + int64_t(r + lane) * pitch + (n - 1) * 2) = e;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 64; h += 32) {
+        uint16_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("ld.shared.u16 %0, [%1];"
+                       : "=h"(x[i]) : "r"(staged(r + i, (h + lane) * 2)) : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r + i < rows && h + lane < n)
+            *reinterpret_cast<uint16_t*>(to + int64_t(r + i) * pitch + (h + lane) * 2) = x[i];
+      }
+    }
+  }
 }
 
 struct Tile {
@@ -449,29 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
               bulk_commit();
             }
           } else {
-            // rows that end with the range, or rows of D that no copy can
-            // address: element by element
+            // rows that end with the range, or rows of D that no copy can address
             __syncwarp();
-            const int left = min(a.N - w.col0, a.bn) - col;
-            for (int row = 0; row < 32 && r0 + row < w.rows; ++row) {
-#pragma unroll
-              for (int h = 0; h < kWide / 32; ++h) {
-                const int c = h * 32 + lane, byte = c * es;
-                const uint32_t from = buf + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
-                uint8_t* to = out + (int64_t(row) * a.stride + col + c) * es;
-                if (c < left) {
-                  if constexpr (BF16) {
-                    uint16_t x;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
-                    *reinterpret_cast<uint16_t*>(to) = x;
-                  } else {
-                    uint32_t x;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
-                    *reinterpret_cast<uint32_t*>(to) = x;
-                  }
-                }
-              }
-            }
+            store_rows<BF16>(buf, out + int64_t(col) * es, a.stride * es, min(32, w.rows - r0),
+                             min(min(a.N - w.col0, a.bn) - col, kWide));
             __syncwarp();
             if (lane == 0) bulk_commit();   // an empty group: the buffers' turns count groups
           }
