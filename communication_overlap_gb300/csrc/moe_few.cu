@@ -678,33 +678,43 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   if (live) {
     // ------------------------------------------------------------- choice
     // every CTA makes the same choice from the same logits
-    for (int t = warp; t < a.T; t += kWarps) {
-      int id;
-      float w, x_scale = 0.0f;
-      if constexpr (MX) x_scale = __ldcg(a.x_scale + t);
-      const float* l = a.logits + int64_t(t) * a.E;
-      auto choose = [&](auto v) {
-        constexpr int V = decltype(v)::value;
-        float x[V];
+    auto choose = [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      constexpr bool kAhead = V <= 4;     // the next token's logits are under way
+      auto load = [&](int t, float (&x)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          x[i] = i * 32 + lane < a.E ? __ldcg(l + i * 32 + lane) : __int_as_float(0xff800000);
-        warp_top_k<V>(x, a.E, a.K, a.renormalize != 0, id, w);
+          x[i] = t < a.T && i * 32 + lane < a.E ? __ldcg(a.logits + int64_t(t) * a.E + i * 32 + lane)
+                                                : __int_as_float(0xff800000);
       };
-      if (a.E <= 32)
-        choose(Const<1>{});
-      else if (a.E <= 128)
-        choose(Const<4>{});
-      else
-        choose(Const<32>{});
-      if (lane < a.K) {
-        ls.id[t * a.K + lane] = int16_t(id);
-        ls.pair_weight[t * a.K + lane] = w;
-        if (id >= 0) atomicAdd(&count[id], 1);
+      float x[V], next[V];
+      if (kAhead) load(warp, next);
+      for (int t = warp; t < a.T; t += kWarps) {
+        if (kAhead) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] = next[i];
+          load(t + kWarps, next);
+        } else {
+          load(t, x);
+        }
+        const float x_scale = MX ? __ldcg(a.x_scale + t) : 0.0f;
+        int id;
+        float w;
+        warp_top_k<V>(x, a.E, a.K, a.renormalize != 0, id, w);
+        if (lane < a.K) {
+          ls.id[t * a.K + lane] = int16_t(id);
+          ls.pair_weight[t * a.K + lane] = w;
+          if (id >= 0) atomicAdd(&count[id], 1);
+        }
+        if (MX && lane == 0) ls.x_scale[t] = x_scale;
       }
-      if constexpr (MX)
-        if (lane == 0) ls.x_scale[t] = x_scale;
-    }
+    };
+    if (a.E <= 32)
+      choose(Const<1>{});
+    else if (a.E <= 128)
+      choose(Const<4>{});
+    else
+      choose(Const<32>{});
     __syncthreads();
     if (warp == 0) {
       int rows = 0, active = 0, most = 1;
@@ -1191,25 +1201,38 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           last = *flag_s != 0;
         }
         if (last) {
+          // four vectors per thread at once: with many tokens and CTAs the parts'
+          // latency is what the join takes
           const float4* from = reinterpret_cast<const float4*>(a.parts + int64_t(rb) * a.T * 128);
-          for (int i = mtid; i < a.T * 32; i += kMathThreads) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (mine) {
-              v = *sums_at(i);
-            } else {
-#pragma unroll 8
+          constexpr int kAtOnce = 4;
+          for (int i0 = mtid; i0 < a.T * 32; i0 += kMathThreads * kAtOnce) {
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int i = i0 + u * kMathThreads;
+              v[u] = mine && i < a.T * 32 ? *sums_at(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            if (!mine) {
+#pragma unroll 4
               for (int k = c0; k <= c1; ++k) {
                 const bool has = cut2.base > 0 || cut2.first(k) < cut2.first(k + 1);
-                const float4 u = has ? __ldcg(from + int64_t(k) * a.T * 32 + i)
-                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                  const int i = i0 + u * kMathThreads;
+                  const float4 x = has && i < a.T * 32 ? __ldcg(from + int64_t(k) * a.T * 32 + i)
+                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  v[u].x += x.x, v[u].y += x.y, v[u].z += x.z, v[u].w += x.w;
+                }
               }
             }
-            const int row = rb * 128 + (i & 31) * 4;
-            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + (i >> 5) * a.y_stride + row;
-            if (row < a.H) {   // (H is a multiple of 8)
-              y[0] = __float2bfloat16_rn(v.x), y[1] = __float2bfloat16_rn(v.y);
-              y[2] = __float2bfloat16_rn(v.z), y[3] = __float2bfloat16_rn(v.w);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int i = i0 + u * kMathThreads, row = rb * 128 + (i & 31) * 4;
+              if (i >= a.T * 32 || row >= a.H) continue;   // (H is a multiple of 8)
+              __nv_bfloat16* y =
+                  reinterpret_cast<__nv_bfloat16*>(a.y) + (i >> 5) * a.y_stride + row;
+              y[0] = __float2bfloat16_rn(v[u].x), y[1] = __float2bfloat16_rn(v[u].y);
+              y[2] = __float2bfloat16_rn(v[u].z), y[3] = __float2bfloat16_rn(v[u].w);
             }
           }
         }
