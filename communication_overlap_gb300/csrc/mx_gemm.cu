@@ -578,7 +578,9 @@ fo_status launch_mx_gemm(int64_t M, int64_t N, int64_t K, const void* a_codes,
   // large: while those of one CTA all run at once, they are faster (512 x 4096 x
   // 4096: 10.4 us, pairs 12.4; 1024 x 4096 x 4096: 14.5 and 12.4), and with no
   // more rows than one CTA takes a pair's second half would be empty.
-  const bool pair = M > 128 && mb * (nb / groups) > sms;
+  // So it is with experts of 128 rows or less on average, whose rounded rows A has
+  // (16 experts of 2 rows, N = 9123, K = 877: 25 us, pairs 37).
+  const bool pair = M > 128 && mb >= 2 * groups && mb * (nb / groups) > sms;
   GemmArgs a{};
   a.bn = pair ? 256 : 128;
   a.acc1 = kSf0 - a.bn < a.bn ? kSf0 - a.bn : a.bn;
