@@ -615,8 +615,9 @@ __device__ __forceinline__ void stage_mx(uint32_t stage, uint32_t code, uint32_t
 constexpr int kBarBytes = 8 * (2 * kMaxStages) + 16;
 
 // Copying warps and 8 computing warps of 16 rows each.  (With 4-bit weights a
-// second set of eight, taking turns at the stages, is no faster: 58 us instead of
-// 57 at 1 token, 154 instead of 150 at 8, and its registers do not suffice.)
+// second set of eight, taking turns at the stages, gives next to nothing: 55 us
+// with and without it at 1 token, 144 instead of 147 at 8, 434 instead of 333 at
+// 48, where its registers do not suffice.)
 constexpr int kThreads = 32 * kCopyWarps + kMathThreads;
 
 // NT: tiles of 8 tokens, at most.
