@@ -12,7 +12,7 @@ device memory and the current stream, every step is a libfo.so call (see
 Calls run on the current stream of the tensors' device and do not
 synchronise.  Workspaces are kept per device and stream, so calls on
 different streams do not share one; a call that is captured into a CUDA graph
-takes its workspace from the graph's memory.  ``device_status`` reads (and
+takes one of its own from the graph's memory.  ``device_status`` reads (and
 synchronises) the sticky status of the calls' bounded waits.
 
 A generation step makes small calls, so the time here counts: the device is
@@ -85,25 +85,35 @@ def _run(dev, call, *args):
             call(*args)
 
 
+def _capturing(dev):
+    """Whether dev's current stream is being captured into a CUDA graph."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _status_word(dev):
     st = _status.get(dev)
     if st is None:
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing(dev):
             raise RuntimeError("call once on this device before capturing into a CUDA graph")
         st = _status[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
     return st.data_ptr()
 
 
-def _workspace(kind, dev, nbytes):
-    """A zeroed workspace of at least nbytes for this device and stream."""
+def _workspace(kind, dev, nbytes, captured=None):
+    """A zeroed workspace of at least nbytes for this device and stream.  A call
+    under capture gets one of its own (of captured() bytes, where that is less),
+    also on a stream that has one: the graph keeps the address, the stream's goes
+    back to the allocator when a larger call comes, and a replay may run on
+    another stream beside it.  Its memory is the graph's, zeroed by each replay."""
+    if _capturing(dev):
+        return torch.zeros(captured() if captured else nbytes, dtype=torch.uint8, device=dev)
     key = (kind, dev, _stream(dev))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        # (under capture this is the graph's memory, zeroed again by each replay,
-        # and goes back to it in stream order)
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        if not torch.cuda.is_current_stream_capturing():
-            _workspaces[key] = ws
+        ws = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -293,7 +303,7 @@ class FewTokenLayer:
         self._desc = functools.lru_cache(fo.FO_MOE_FEW_TOKENS)(lambda tokens: fo.make_few_desc(
             tokens, H, I, E, top_k, renormalize, _ACTS[act],
             fo.FO_TYPE_MX4 if mx else fo.FO_TYPE_BF16))
-        self._bytes = fo.fo_moe_few_workspace(self._desc(fo.FO_MOE_FEW_TOKENS))
+        self._bytes = fo.fo_moe_few_workspace(self._desc(fo.FO_MOE_FEW_TOKENS))   # any call's
 
     def __call__(self, x, out=None):
         """x: bf16 [tokens, hidden] -> y of the same shape."""
@@ -305,8 +315,9 @@ class FewTokenLayer:
         if out.shape != x.shape or out.dtype != torch.bfloat16:
             raise ValueError("out: bf16 of x's shape expected")
         w1, s1, w2, s2 = self._w
-        ws = _workspace("few", dev, self._bytes)
-        _run(dev, fo.fo_moe_few, self._desc(x.shape[0]), x.data_ptr(), _row_stride(x, "x"),
+        desc = self._desc(x.shape[0])
+        ws = _workspace("few", dev, self._bytes, lambda: fo.fo_moe_few_workspace(desc))
+        _run(dev, fo.fo_moe_few, desc, x.data_ptr(), _row_stride(x, "x"),
              self.router.data_ptr(), w1, s1, w2, s2, out.data_ptr(), _row_stride(out, "out"),
              ws.data_ptr(), _status_word(dev), _stream(dev))
         return out
