@@ -119,7 +119,8 @@ def _workspace(kind, dev, nbytes, captured=None):
 
 def device_status(device="cuda", clear=False):
     """The device's sticky status (FO_OK, FO_ERR_ARG for a product's group out
-    of range, FO_ERR_TIMEOUT).  Synchronises."""
+    of range, FO_ERR_TIMEOUT).  Synchronises.  Clearing an error also gives up the
+    device's workspaces: a call whose wait ran out leaves its counters anywhere."""
     dev = torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
@@ -127,8 +128,10 @@ def device_status(device="cuda", clear=False):
         return fo.FO_OK
     torch.cuda.synchronize(dev)
     st = int(_status[dev].item())
-    if clear:
+    if clear and st != fo.FO_OK:
         _status[dev].zero_()
+        for key in [k for k in _workspaces if k[1] == dev]:
+            del _workspaces[key]
     return st
 
 

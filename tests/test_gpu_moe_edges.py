@@ -91,3 +91,17 @@ def test_a_replay_beside_eager_calls():
     torch.cuda.synchronize()
     assert wrong.tolist() == [0, 0]
     assert moe.device_status() == fo.FO_OK
+
+
+def test_a_workspace_is_fresh_after_an_error_is_cleared():
+    """Counters of joined output rows as a wait that ran out may leave them, and
+    its status, set from here: the next call has a workspace without them."""
+    layer, x = few_layer(9, 512, 640, 8, 2, 36)
+    y = layer(x)
+    dev = x.device
+    key = ("few", dev, torch.cuda.current_stream().cuda_stream)
+    moe._workspaces[key][256:512] = 1
+    moe._status[dev].fill_(fo.FO_ERR_TIMEOUT)
+    assert moe.device_status(clear=True) == fo.FO_ERR_TIMEOUT
+    assert torch.equal(layer(x), y)
+    assert moe.device_status() == fo.FO_OK

@@ -31,3 +31,21 @@ def test_a_captured_call_has_a_workspace_of_its_own(device):
     assert moe._workspace("few", dev, 100) is eager
     larger = moe._workspace("few", dev, 200)
     assert larger.numel() >= 200 and moe._workspace("few", dev, 100) is larger
+
+
+@pytest.mark.parametrize("status", [fo.FO_ERR_TIMEOUT, fo.FO_ERR_ARG])
+def test_clearing_an_error_gives_the_workspaces_up(device, monkeypatch, status):
+    """A wait that ran out leaves a workspace's counters anywhere; the status
+    keeps the first error only, so one of another kind may stand before it."""
+    dev = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda d=None: None)
+    other = torch.device("cuda", 1)
+    ws = torch.ones(100, dtype=torch.uint8)
+    moe._status[dev] = torch.tensor([status], dtype=torch.int32)
+    moe._workspaces[("few", dev, 7)] = moe._workspaces[("few", other, 7)] = ws
+    assert moe.device_status(dev) == status and ("few", dev, 7) in moe._workspaces
+    assert moe.device_status(dev, clear=True) == status
+    assert ("few", dev, 7) not in moe._workspaces and ("few", other, 7) in moe._workspaces
+    moe._workspaces[("few", dev, 7)] = ws
+    assert moe.device_status(dev, clear=True) == fo.FO_OK
+    assert moe._workspaces[("few", dev, 7)] is ws
