@@ -26,6 +26,8 @@
 // faster.  The gradient: 10 us for 16384 of 128.
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "moe_common.cuh"
 
 namespace fo {
@@ -34,6 +36,7 @@ namespace {
 
 constexpr int kRouteWarps = 16;
 constexpr int kRouteThreads = kRouteWarps * 32;
+constexpr int kRouteSmemLimit = 200 * 1024;   // that a launch asks for (8 KB more are static)
 
 __device__ __forceinline__ float load_logit(const void* p, int64_t i, bool bf16) {
   return bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16)
@@ -324,10 +327,18 @@ fo_status sm_count(int* sms) {
 
 template <int V>
 fo_status launch_v(const RouteKernelArgs& a, int grid, int smem, cudaStream_t st) {
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(route_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-          cudaSuccess)
-    return FO_ERR_CUDA;
+  // the limit once, not each launch's size: that would be lowered between another
+  // thread's setting and its launch, and 48 KB bound the static part's sum with it
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
+  const int slot = dev < 64 ? dev : 63;
+  std::call_once(once[slot], [&] {
+    err[slot] = cudaFuncSetAttribute(route_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kRouteSmemLimit);
+  });
+  if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kRouteThreads);
@@ -385,7 +396,7 @@ fo_status launch_moe_route(const void* logits, fo_type type, int64_t tokens, int
   a.status = dev_status;
   const int64_t chunk = route_chunk(tokens, sms);
   const int64_t smem = route_smem(chunk, top_k, experts);
-  if (smem > 200 * 1024) return FO_ERR_UNSUPPORTED;
+  if (smem > kRouteSmemLimit) return FO_ERR_UNSUPPORTED;
   a.chunk = int32_t(chunk);
   const int grid = tokens == 0 ? 1 : int((tokens + chunk - 1) / chunk);
   const int v = (experts + 31) / 32;

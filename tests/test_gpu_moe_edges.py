@@ -1,7 +1,15 @@
 """The expert layer's operators at the edges of what include/fo.h promises:
 sizes between the tested ones, calls that share a device's memory, tokens and
 experts that are missing, values at the ends of their types.
+
+Tolerances, derived before the first run:
+ - softmax weights: as for the router's other tests, 64 * 2^-24 of the weight.
 """
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -14,6 +22,7 @@ if torch.cuda.is_available():
     from communication_overlap_gb300 import moe
 
 BF16, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def host(t):
@@ -105,3 +114,83 @@ def test_a_workspace_is_fresh_after_an_error_is_cleared():
     assert moe.device_status(clear=True) == fo.FO_ERR_TIMEOUT
     assert torch.equal(layer(x), y)
     assert moe.device_status() == fo.FO_OK
+
+
+# ------------------------------------------------------------------ the router's sizes
+
+def routed(logits, k):
+    """The router's outputs for finite logits (float64), all tokens at once."""
+    T, E = logits.shape
+    ids = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k]
+    w = torch.softmax(logits, 1).gather(1, ids)
+    flat = ids.reshape(-1)
+    i = torch.arange(T * k, device=flat.device)
+    order = torch.sort(flat, stable=True).indices
+    rows = torch.bincount(flat, minlength=E)
+    span = (rows + 127) // 128 * 128
+    first = span.cumsum(0) - span
+    at = torch.empty_like(i)
+    at[order] = first[flat[order]] + i - (rows.cumsum(0) - rows)[flat[order]]
+    M = (T * k + E * 127) // 128 * 128
+    row_token, row_slot = at.new_full((M,), -1), at.new_zeros(M)
+    row_token[at], row_slot[at] = i // k, i % k
+    return dict(ids=ids, weights=w / w.sum(1, keepdim=True), row_token=row_token,
+                row_slot=row_slot, token_row=at.view(T, k), expert_first=first,
+                expert_rows=rows)
+
+
+def check_routed(T, E, k, dtype=F32):
+    x = normal(np.random.default_rng(T + E + k), (T, E), dtype, 2.0)
+    r, want = moe.route(x, k), routed(x.double(), k)
+    for n in ("ids", "row_token", "row_slot", "token_row", "expert_first", "expert_rows"):
+        assert torch.equal(getattr(r, n).long(), want[n]), n
+    off = (r.weights.double() - want["weights"]).abs()
+    assert bool((off <= 64 * 2.0 ** -24 * want["weights"] + 1e-38).all())
+    assert moe.device_status() == fo.FO_OK
+
+
+# per expert and token of a block the kernel takes shared memory: sizes whose
+# part that the launch asks for is below 48 KB, and the sum above
+BETWEEN = [(5, 600, 8), (3, 715, 8), (24000, 512, 10), (90000, 384, 8), (120000, 256, 8)]
+
+
+@pytest.mark.parametrize("T, E, k", BETWEEN)
+def test_route_as_a_process_first_call(T, E, k):
+    """(An earlier, larger call would leave the kernel with more shared memory.)"""
+    code = f"import test_gpu_moe_edges as t; t.check_routed({T}, {E}, {k})"
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_route_from_two_threads():
+    """Calls of different sizes of one kernel, each from a thread and on a stream
+    of its own."""
+    failed = []
+
+    def calls(T, E, k):
+        try:
+            x = normal(np.random.default_rng(E), (T, E), F32)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                torch.cuda.synchronize()
+                for _ in range(300):
+                    moe.route(x, k)
+                torch.cuda.synchronize()
+        except Exception as e:      # noqa: BLE001 (reported by the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=calls, args=a) for a in ((20, 1024, 32), (20, 730, 8))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert moe.device_status() == fo.FO_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T, E, k", [(200, 300, 10), (33, 600, 8), (500, 512, 10), (100, 1000, 32),
+                                     (300, 40, 32), (1, 1024, 1)])
+def test_route_of_many_experts(T, E, k, dtype):
+    check_routed(T, E, k, dtype)
