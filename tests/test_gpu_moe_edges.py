@@ -194,3 +194,8 @@ def test_route_from_two_threads():
                                      (300, 40, 32), (1, 1024, 1)])
 def test_route_of_many_experts(T, E, k, dtype):
     check_routed(T, E, k, dtype)
+
+
+@pytest.mark.parametrize("T, E, k", [(250000, 32, 32), (170000, 1024, 32)])
+def test_route_of_more_tokens_than_shared_memory_holds(T, E, k):
+    check_routed(T, E, k)
