@@ -58,7 +58,9 @@ class ExpertLayer:
         return self.few(x) if x.shape[0] <= fo.FO_MOE_FEW_TOKENS else self.forward(x)[0]
 
     def forward(self, x):
-        logits = x @ self.router.t()
+        # fp32, as the one-kernel layer has them: in bf16 close logits would tie, and
+        # a token might choose other experts in a prompt than in a generation step
+        logits = torch.mm(x, self.router.t(), out_dtype=torch.float32)
         r = moe.route(logits, self.top_k, self.renormalize)
         groups = dict(group_first=r.expert_first, group_rows=r.expert_rows)
         # (rows of no expert are left as they are, and nothing reads them)
@@ -72,7 +74,7 @@ class ExpertLayer:
         return y.to(x.dtype), Step(logits, r)
 
     def backward(self, step, dweights, dup):
-        """The logits' gradient from that of the routing weights (fp32 [tokens,
+        """The logits' (fp32) gradient from that of the routing weights (fp32 [tokens,
         top_k]), and the first projection's input's from that of its output
         (`dup`, a row per row of the routing's tables)."""
         if self.w1_t is None:

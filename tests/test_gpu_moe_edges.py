@@ -3,7 +3,9 @@ sizes between the tested ones, calls that share a device's memory, tokens and
 experts that are missing, values at the ends of their types.
 
 Tolerances, derived before the first run:
- - softmax weights: as for the router's other tests, 64 * 2^-24 of the weight.
+ - softmax weights: as for the router's other tests, 64 * 2^-24 of the weight;
+ - logits of a bf16 product with fp32 sums: H roundings of 2^-24 of the sum of
+   magnitudes, doubled.
 """
 import os
 import subprocess
@@ -15,11 +17,12 @@ import pytest
 import torch
 
 from communication_overlap_gb300 import fo
+from oracle import moe as oracle
 
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
-    from communication_overlap_gb300 import moe
+    from communication_overlap_gb300 import expert_layer, moe
 
 BF16, F32 = torch.bfloat16, torch.float32
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -199,3 +202,35 @@ def test_route_of_many_experts(T, E, k, dtype):
 @pytest.mark.parametrize("T, E, k", [(250000, 32, 32), (170000, 1024, 32)])
 def test_route_of_more_tokens_than_shared_memory_holds(T, E, k):
     check_routed(T, E, k)
+
+
+# ------------------------------------------------------------------ the layer
+
+def layer_of(router, H, I, E, k, rng):
+    w1, w2 = normal(rng, (E, 2 * I, H), BF16, H ** -0.5), normal(rng, (E, H, I), BF16, I ** -0.5)
+    return expert_layer.ExpertLayer(router, moe.quantize(w1), moe.quantize(w2), k,
+                                    w1_t=moe.quantize(w1, transpose=True))
+
+
+def test_prompt_and_generation_choose_the_same_experts():
+    """Experts 2j and 2j + 1 have logits 2^-8 apart, less than a bf16 step of
+    most: all tokens choose the odd one, in a prompt and one at a time."""
+    rng = np.random.default_rng(21)
+    T, H, I, E = 70, 256, 64, 8
+    x = normal(rng, (T, H), BF16)
+    x[:, 0] = 1.0
+    router = normal(rng, (E, H), BF16, 4 / np.sqrt(H))
+    router[1::2] = router[::2]
+    router[::2, 0], router[1::2, 0] = 0.0, 2.0 ** -8
+    layer = layer_of(router, H, I, E, 1, rng)
+    y, step = layer.forward(x)
+    logits = host(x) @ host(router).T
+    size = np.abs(host(x)) @ np.abs(host(router)).T
+    assert (np.abs(host(step.logits) - logits) <= 2 * H * 2.0 ** -24 * size).all()
+    want = oracle.route(logits, 1, True)["ids"]
+    assert (want % 2 == 1).all() and np.array_equal(host(step.routing.ids), want)
+    # two experts' outputs are as far apart as they are large; one's in 4 bits
+    # (a prompt's activations) and in 16 about a fifth of that
+    few = host(torch.cat([layer(x[t:t + 1]) for t in range(T)]))
+    off = np.linalg.norm(host(y) - few, axis=1)
+    assert (off <= np.linalg.norm(few, axis=1) / 2).all()
