@@ -5,7 +5,8 @@ experts that are missing, values at the ends of their types.
 Tolerances, derived before the first run:
  - softmax weights: as for the router's other tests, 64 * 2^-24 of the weight;
  - logits of a bf16 product with fp32 sums: H roundings of 2^-24 of the sum of
-   magnitudes, doubled.
+   magnitudes, doubled;
+ - a token of the prompt path: see test_prompt_token_by_token.
 """
 import os
 import subprocess
@@ -234,3 +235,27 @@ def test_prompt_and_generation_choose_the_same_experts():
     few = host(torch.cat([layer(x[t:t + 1]) for t in range(T)]))
     off = np.linalg.norm(host(y) - few, axis=1)
     assert (off <= np.linalg.norm(few, axis=1) / 2).all()
+
+
+@pytest.mark.parametrize("T, H, I, E, k", [(70, 256, 192, 4, 2), (130, 136, 264, 6, 3)])
+def test_prompt_token_by_token(T, H, I, E, k):
+    """A prompt against the definition with its 4-bit roundings, each token by
+    itself, the experts chosen from 64-bit logits.  A hidden value carries bf16
+    roundings (2^-7 of it in all) that the oracle's does not, so one in twenty
+    takes the neighbouring code and moves by half its size at most.  Of a token's
+    I >= 192 values under each expert that is up to 1/20 + 5 sqrt(1/20 / I) = 0.13
+    of them: sqrt(0.13) / 2 = 0.18 of the norm; 1/4 covers it with the sum over
+    experts.  (A wrong weight or row moves a token by its own norm.)"""
+    layer = expert_layer.ExpertLayer.random(H, I, E, k, seed=T)
+    x = normal(np.random.default_rng(T), (T, H), BF16)
+    y = host(layer.forward(x)[0])
+    values = lambda q: host(moe.dequantize(q, F32)).reshape(q.batch, q.rows, q.cols)
+    rounded = lambda v: oracle.mx_values(*oracle.mx_quantize(v))[:, :v.shape[1]]
+    w1, w2, xq = values(layer.w1), values(layer.w2), rounded(host(x))
+    r = oracle.route(host(x) @ host(layer.router).T, k, True)
+    for t in range(T):
+        exact = np.zeros(H)
+        for e, w in zip(r["ids"][t], r["weights"][t]):
+            g, u = np.split(w1[e] @ xq[t], 2)
+            exact += w * (w2[e] @ rounded((g / (1 + np.exp(-g)) * u)[None])[0])
+        assert np.linalg.norm(y[t] - exact) <= np.linalg.norm(exact) / 4, t
