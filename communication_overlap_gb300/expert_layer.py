@@ -69,9 +69,18 @@ class ExpertLayer:
         moe.mx_gemm(moe.quantize(x, row_index=r.row_token), self.w1, out=up, **groups)
         gate, up = up.chunk(2, dim=1)
         h = torch.nn.functional.silu(gate).mul_(up)
-        out = moe.mx_gemm(moe.quantize(h), self.w2, out_dtype=torch.float32, **groups)
-        y = torch.bmm(r.weights.unsqueeze(1), out[r.token_row.clamp(min=0).long()]).squeeze(1)
+        rows = self._rows(moe.quantize(h), self.w2, groups)
+        y = torch.bmm(r.weights.unsqueeze(1), rows[r.token_row.long()]).squeeze(1)
         return y.to(x.dtype), Step(logits, r)
+
+    @staticmethod
+    def _rows(a, w, groups):
+        """The product per expert in fp32, and after it a row of zeros: the row of
+        index -1, which slots without one read."""
+        rows = torch.empty((a.rows + 1, w.rows), device=a.codes.device)
+        rows[-1] = 0
+        moe.mx_gemm(a, w, out=rows[:-1], **groups)
+        return rows
 
     def backward(self, step, dweights, dup):
         """The logits' (fp32) gradient from that of the routing weights (fp32 [tokens,
@@ -81,9 +90,9 @@ class ExpertLayer:
             raise ValueError("backward needs w1_t")
         r = step.routing
         dlogits = moe.route_backward(step.logits, r.ids, r.weights, dweights, self.renormalize)
-        drows = moe.mx_gemm(moe.quantize(dup), self.w1_t, out_dtype=torch.float32,
-                            group_first=r.expert_first, group_rows=r.expert_rows)
-        dx = (drows[r.token_row.clamp(min=0).long()] * (r.token_row >= 0).unsqueeze(-1)).sum(1)
+        drows = self._rows(moe.quantize(dup), self.w1_t,
+                           dict(group_first=r.expert_first, group_rows=r.expert_rows))
+        dx = drows[r.token_row.long()].sum(1)
         return dlogits, dx
 
 

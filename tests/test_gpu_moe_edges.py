@@ -259,3 +259,38 @@ def test_prompt_token_by_token(T, H, I, E, k):
             g, u = np.split(w1[e] @ xq[t], 2)
             exact += w * (w2[e] @ rounded((g / (1 + np.exp(-g)) * u)[None])[0])
         assert np.linalg.norm(y[t] - exact) <= np.linalg.norm(exact) / 4, t
+
+
+def test_slots_without_a_row_read_none():
+    """One expert is barred, and a NaN stands in the first row of the tables:
+    nothing of it reaches the slots that have no row."""
+    rng = np.random.default_rng(22)
+    T, H, I, E = 70, 64, 64, 3
+    x = normal(rng, (T, H), BF16).abs()
+    router = normal(rng, (E, H), BF16, H ** -0.5)
+    router[1] = float("-inf")
+    layer = layer_of(router, H, I, E, 3, rng)
+    clean, step = layer.forward(x)
+    assert bool((step.routing.token_row == -1).any(1).all())
+    rows = step.routing.row_token.numel()
+    dup = normal(rng, (rows, 2 * I), BF16)
+    g = normal(rng, (T, 3), F32)
+    _, dx = layer.backward(step, g, dup)
+    first = int(step.routing.row_token[0])
+    others = [t for t in range(T) if t != first]
+    bad = x.clone()
+    bad[first] = float("nan")
+    y, _ = layer.forward(bad)
+    assert bool(y[others].isfinite().all()) and torch.equal(y[others], clean[others])
+    dup[0] = float("nan")
+    _, dx_bad = layer.backward(step, g, dup)
+    assert torch.equal(dx_bad[others], dx[others])
+    assert bool(torch.isnan(dx_bad[first]).all())
+
+
+def test_prompt_of_barred_tokens_is_zero():
+    rng = np.random.default_rng(23)
+    router = torch.full((3, 64), float("-inf"), dtype=BF16, device="cuda")
+    layer = layer_of(router, 64, 64, 3, 2, rng)
+    y, _ = layer.forward(normal(rng, (70, 64), BF16).abs())
+    assert not y.any()
