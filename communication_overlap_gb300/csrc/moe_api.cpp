@@ -77,7 +77,9 @@ fo_status fo_mx_quantize(const void* src, fo_type type, int64_t batch, int64_t b
   int64_t n = 0;
   if (!type_ok(type) || !mx_elements(batch, rows, cols, &n)) return FO_ERR_ARG;
   if (n == 0) return FO_OK;
-  if (!src || !codes || !scales || !fo::aligned16(codes) || !fo::aligned16(scales))
+  // (a matrix without rows has no address to gather from)
+  if ((!src && !(row_index && src_rows == 0)) || !codes || !scales || !fo::aligned16(codes) ||
+      !fo::aligned16(scales))
     return FO_ERR_ARG;
   if (!aligned_type(src, type) || !fo::aligned4(row_index)) return FO_ERR_ARG;
   if (row_stride < (transpose ? rows : cols) || batch_stride < 0) return FO_ERR_ARG;

@@ -610,7 +610,8 @@ fo_status fo_mx_sizes(int64_t batch, int64_t rows, int64_t cols, int64_t* code_b
  *      alignment of the element type.
  *  row_index: NULL, or device int32[rows] (batch 1, no transpose): row r is
  *      the source's row row_index[r]; an index outside [0, src_rows) marks a
- *      row that holds no token, which becomes zeros.
+ *      row that holds no token, which becomes zeros (src may be NULL where
+ *      src_rows is 0).
  *  codes, scales: device, 16-byte aligned, of fo_mx_sizes bytes. */
 fo_status fo_mx_quantize(const void* src, fo_type type, int64_t batch, int64_t batch_stride,
                          int64_t rows, int64_t cols, int64_t row_stride, int32_t transpose,

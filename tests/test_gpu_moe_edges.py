@@ -294,3 +294,21 @@ def test_prompt_of_barred_tokens_is_zero():
     layer = layer_of(router, 64, 64, 3, 2, rng)
     y, _ = layer.forward(normal(rng, (70, 64), BF16).abs())
     assert not y.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gathered_rows_of_a_matrix_without_rows(dtype):
+    idx = torch.tensor([-1, 0, 5], dtype=torch.int32, device="cuda")
+    q = moe.quantize(torch.empty((0, 96), dtype=dtype, device="cuda"), row_index=idx)
+    assert (q.rows, q.cols) == (3, 96) and not moe.dequantize(q).any()
+
+
+@pytest.mark.parametrize("E", [1, 4])
+def test_prompt_without_tokens(E):
+    layer = expert_layer.ExpertLayer.random(64, 64, E, 1)
+    y, step = layer.forward(torch.empty((0, 64), dtype=BF16, device="cuda"))
+    assert y.shape == (0, 64)
+    rows = step.routing.row_token.numel()
+    dlogits, dx = layer.backward(step, torch.empty((0, 1), device="cuda"),
+                                 torch.empty((rows, 128), dtype=BF16, device="cuda"))
+    assert dlogits.shape == (0, E) and dx.shape == (0, 64)

@@ -49,3 +49,17 @@ def test_clearing_an_error_gives_the_workspaces_up(device, monkeypatch, status):
     moe._workspaces[("few", dev, 7)] = ws
     assert moe.device_status(dev, clear=True) == fo.FO_OK
     assert moe._workspaces[("few", dev, 7)] is ws
+
+
+def test_gathering_from_a_matrix_without_rows_is_no_bad_argument():
+    """(Without a GPU the call gets as far as asking for the device.)"""
+    args = dict(src=0, type=0, batch=1, batch_stride=0, rows=8, cols=64, row_stride=64,
+                transpose=0, row_index=64, src_rows=0, codes=64, scales=64, stream=0)
+    if torch.cuda.is_available():
+        pytest.skip("these addresses are not to be launched on")
+    with pytest.raises(fo.FoError) as e:
+        fo.fo_mx_quantize(*args.values())
+    assert e.value.status != fo.FO_ERR_ARG
+    with pytest.raises(fo.FoError) as e:
+        fo.fo_mx_quantize(*{**args, "src_rows": 1}.values())
+    assert e.value.status == fo.FO_ERR_ARG
