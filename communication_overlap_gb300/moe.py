@@ -217,6 +217,8 @@ def mx_gemm(a, b, out=None, out_dtype=torch.bfloat16, group_first=None, group_ro
         out = make((a.rows, b.rows), dtype=out_dtype, device=dev)
     if tuple(out.shape) != (a.rows, b.rows):
         raise ValueError(f"out: {(a.rows, b.rows)} expected, not {tuple(out.shape)}")
+    if group_first is not None and groups == 0:
+        return out          # no row is in a group (to the library, 0: one product of all rows)
     _run(dev, fo.fo_mx_gemm, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
          b.codes.data_ptr(), b.scales.data_ptr(), groups,
          0 if group_first is None else group_first.data_ptr(),

@@ -312,3 +312,15 @@ def test_prompt_without_tokens(E):
     dlogits, dx = layer.backward(step, torch.empty((0, 1), device="cuda"),
                                  torch.empty((rows, 128), dtype=BF16, device="cuda"))
     assert dlogits.shape == (0, E) and dx.shape == (0, 64)
+
+
+@pytest.mark.parametrize("K", [0, 64])
+def test_product_over_no_experts(K):
+    """A product per expert with no expert at all: every row keeps what it holds."""
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    bytes_ = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")
+    a = moe.MxTensor(*map(bytes_, fo.fo_mx_sizes(1, 5, K)), 1, 5, K)
+    b = moe.MxTensor(bytes_(0), bytes_(0), 0, 9, K)
+    d = torch.full((5, 9), 7.0, dtype=F32, device="cuda")
+    assert moe.mx_gemm(a, b, out=d, group_first=none, group_rows=none) is d
+    assert bool((d == 7.0).all())
