@@ -89,6 +89,8 @@ class ExpertLayer:
         if self.w1_t is None:
             raise ValueError("backward needs w1_t")
         r = step.routing
+        if dup.dim() != 2 or dup.shape[0] != r.row_token.numel():
+            raise ValueError(f"dup: {r.row_token.numel()} rows expected, not {tuple(dup.shape)}")
         dlogits = moe.route_backward(step.logits, r.ids, r.weights, dweights, self.renormalize)
         drows = self._rows(moe.quantize(dup), self.w1_t,
                            dict(group_first=r.expert_first, group_rows=r.expert_rows))

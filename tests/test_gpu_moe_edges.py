@@ -324,3 +324,14 @@ def test_product_over_no_experts(K):
     d = torch.full((5, 9), 7.0, dtype=F32, device="cuda")
     assert moe.mx_gemm(a, b, out=d, group_first=none, group_rows=none) is d
     assert bool((d == 7.0).all())
+
+
+def test_backward_refuses_gradients_of_other_tables():
+    """(The routing's rows index the product of `dup`.)"""
+    layer = expert_layer.ExpertLayer.random(64, 64, 3, 2)
+    _, step = layer.forward(normal(np.random.default_rng(24), (70, 64), BF16))
+    rows, g = step.routing.row_token.numel(), torch.zeros((70, 2), device="cuda")
+    for n in (0, rows - 128, rows + 128):
+        with pytest.raises(ValueError):
+            layer.backward(step, g, torch.zeros((n, 128), dtype=BF16, device="cuda"))
+    layer.backward(step, g, torch.zeros((rows, 128), dtype=BF16, device="cuda"))
