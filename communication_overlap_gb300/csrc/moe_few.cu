@@ -148,7 +148,10 @@ __host__ inline int lists_bytes(int P, int E) { return (16 * P + 4 * E + 2 + 127
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == FO_ACT_NONE) return g;
   if (act == FO_ACT_RELU) return g > 0.0f ? g : 0.0f;
-  return __fdividef(g, 1.0f + __expf(-g));   // (a few units of the last place of fp32)
+  // (Not the fast forms: their division gives 0 where 1 + e^-g passes 2^126, though
+  // silu is 1e-36 there, and their exponential loses a bit per doubling of g.  They
+  // save 0.8% at 48 tokens of 4-bit weights, 346 us of 349, and nothing at 1 or 8.)
+  return g / (1.0f + expf(-g));
 }
 
 // ------------------------------------------------------------------ router

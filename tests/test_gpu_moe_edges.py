@@ -4,6 +4,8 @@ experts that are missing, values at the ends of their types.
 
 Tolerances, derived before the first run:
  - softmax weights: as for the router's other tests, 64 * 2^-24 of the weight;
+ - the layer of few tokens: 2^-8 of the value and of the terms' magnitudes (a
+   rounding of each hidden value and one of the output, 2^-9 each, doubled);
  - logits of a bf16 product with fp32 sums: H roundings of 2^-24 of the sum of
    magnitudes, doubled;
  - a token of the prompt path: see test_prompt_token_by_token.
@@ -335,3 +337,24 @@ def test_backward_refuses_gradients_of_other_tables():
         with pytest.raises(ValueError):
             layer.backward(step, g, torch.zeros((n, 128), dtype=BF16, device="cuda"))
     layer.backward(step, g, torch.zeros((rows, 128), dtype=BF16, device="cuda"))
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx"])
+@pytest.mark.parametrize("gate", [-88.0, -87.5, -60.0, -0.0078125, 30.0])
+def test_silu_far_from_zero(gate, form):
+    """silu(g) = g e^g is small but not zero at -88, where 1 + e^-g nears the
+    largest fp32 value; a large second factor brings it back."""
+    H, E = 64, 1
+    x = torch.zeros((1, H), dtype=BF16, device="cuda")
+    x[0, 0] = abs(gate) / 64
+    w1 = torch.zeros((E, 2 * H, H), dtype=BF16, device="cuda")
+    w1[:, :H, 0] = 64.0 * np.sign(gate)
+    w1[:, H:, 0] = 2.0 ** 100
+    w2 = torch.eye(H, dtype=BF16, device="cuda")[None]
+    router = torch.zeros((E, H), dtype=BF16, device="cuda")
+    args = (host(x), host(router), host(w1), host(w2))
+    if form == "mx":
+        w1, w2 = moe.quantize(w1), moe.quantize(w2)
+    y = host(moe.FewTokenLayer(router, w1, w2, 1)(x))
+    want, spread = oracle.few(*args, 1, True)
+    assert (np.abs(y - want) <= (np.abs(want) + spread) * 2.0 ** -8).all() and want.all()
