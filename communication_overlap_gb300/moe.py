@@ -13,7 +13,9 @@ Calls run on the current stream of the tensors' device and do not
 synchronise.  Workspaces are kept per device and stream, so calls on
 different streams do not share one; a call that is captured into a CUDA graph
 takes one of its own from the graph's memory.  ``device_status`` reads (and
-synchronises) the sticky status of the calls' bounded waits.
+synchronises) the sticky status of the calls' bounded waits.  No call is part of
+autograd: where it would lose a gradient (not where its result is in 4 bits, which
+carry none) it refuses tensors that require one.
 
 A generation step makes small calls, so the time here counts: the device is
 switched only where another is current, sizes are computed once per shape.
@@ -46,6 +48,14 @@ def _on_gpu(first, *others):
     if index < 0 or not first.is_cuda:
         raise ValueError("tensors must be on one CUDA device")
     return first.device
+
+
+def _untracked(*tensors):
+    """Refuses tensors whose gradient a call would lose without a word."""
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("no gradient flows through this call: detach its tensors, or call it "
+                             "under torch.no_grad() (route_backward is the router's gradient)")
 
 
 def _int32(t, n, what):
@@ -242,6 +252,7 @@ class Routing:
 
 def route(logits, top_k, renormalize=True, capacity=0):
     """The top-k choice of logits [tokens, experts] (bf16 or fp32)."""
+    _untracked(logits)
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
     dev, type_ = _on_gpu(logits), _type(logits.dtype)
@@ -262,6 +273,7 @@ def route(logits, top_k, renormalize=True, capacity=0):
 
 def route_backward(logits, ids, weights, dweights, renormalize=True):
     """The gradient of the logits from that of the weights (fp32)."""
+    _untracked(logits, weights, dweights)
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
     dev, type_ = _on_gpu(logits, ids, weights, dweights), _type(logits.dtype)
@@ -303,6 +315,7 @@ class FewTokenLayer:
                 raise ValueError("contiguous bf16 weights expected")
         self.device = _on_gpu(router, *parts)
         self.router, self._keep = router, parts
+        self._float = (router,) if mx else (router, w1, w2)
         self.hidden, self.top_k = H, top_k
         self._w = [0 if t is None else t.data_ptr() for t in parts]
         self._desc = functools.lru_cache(fo.FO_MOE_FEW_TOKENS)(lambda tokens: fo.make_few_desc(
@@ -312,6 +325,7 @@ class FewTokenLayer:
 
     def __call__(self, x, out=None):
         """x: bf16 [tokens, hidden] -> y of the same shape."""
+        _untracked(x, *self._float)
         if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype != torch.bfloat16:
             raise ValueError(f"x: bf16 [tokens, {self.hidden}] expected")
         dev = _on_gpu(x, self.router, out)

@@ -358,3 +358,28 @@ def test_silu_far_from_zero(gate, form):
     y = host(moe.FewTokenLayer(router, w1, w2, 1)(x))
     want, spread = oracle.few(*args, 1, True)
     assert (np.abs(y - want) <= (np.abs(want) + spread) * 2.0 ** -8).all() and want.all()
+
+
+@pytest.mark.parametrize("which", ["x", "router", "w1", "w2"])
+def test_few_refuses_tensors_that_require_a_gradient(which):
+    rng = np.random.default_rng(37)
+    t = dict(x=normal(rng, (3, 64), BF16), router=normal(rng, (4, 64), BF16, 0.1),
+             w1=normal(rng, (4, 64, 64), BF16, 0.1), w2=normal(rng, (4, 64, 32), BF16, 0.1))
+    y = moe.FewTokenLayer(t["router"], t["w1"], t["w2"], 2)(t["x"])
+    t[which].requires_grad_()
+    layer = moe.FewTokenLayer(t["router"], t["w1"], t["w2"], 2)
+    with pytest.raises(ValueError, match="gradient"):
+        layer(t["x"])
+    with torch.no_grad():
+        assert torch.equal(layer(t["x"]), y)
+
+
+def test_prompt_refuses_tensors_that_require_a_gradient():
+    layer = expert_layer.ExpertLayer.random(64, 64, 3, 2)
+    x = normal(np.random.default_rng(38), (70, 64), BF16)
+    y = layer(x)
+    layer.router.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        layer(x)
+    with torch.no_grad():
+        assert torch.equal(layer(x), y)

@@ -63,3 +63,17 @@ def test_gathering_from_a_matrix_without_rows_is_no_bad_argument():
     with pytest.raises(fo.FoError) as e:
         fo.fo_mx_quantize(*{**args, "src_rows": 1}.values())
     assert e.value.status == fo.FO_ERR_ARG
+
+
+def test_calls_that_would_lose_a_gradient_are_refused():
+    x, w = torch.zeros((4, 8)), torch.zeros((4, 2))
+    ids = torch.zeros((4, 2), dtype=torch.int32)
+    tracked = lambda t: t.clone().requires_grad_()
+    for call in (lambda: moe.route(tracked(x), 2),
+                 lambda: moe.route_backward(tracked(x), ids, w, w),
+                 lambda: moe.route_backward(x, ids, tracked(w), w),
+                 lambda: moe.route_backward(x, ids, w, tracked(w))):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+            call()
