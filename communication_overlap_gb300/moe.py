@@ -9,13 +9,13 @@ device memory and the current stream, every step is a libfo.so call (see
   mx_gemm                 the product of two 4-bit matrices, or one per expert
   FewTokenLayer           a whole expert layer for a generation step's tokens
 
-Calls run on the current stream of the tensors' device and do not
-synchronise.  Workspaces are kept per device and stream, so calls on
-different streams do not share one; a call that is captured into a CUDA graph
+Calls run on the current stream of the tensors' device and, but for a device's
+first, do not synchronise.  Workspaces are kept per device and stream, so calls
+on different streams do not share one; a call that is captured into a CUDA graph
 takes one of its own from the graph's memory.  ``device_status`` reads (and
 synchronises) the sticky status of the calls' bounded waits.  No call is part of
-autograd: where it would lose a gradient (not where its result is in 4 bits, which
-carry none) it refuses tensors that require one.
+autograd: where it would lose a gradient (not where its result is in 4 bits,
+which carry none) it refuses tensors that require one.
 
 A generation step makes small calls, so the time here counts: the device is
 switched only where another is current, sizes are computed once per shape.
@@ -108,7 +108,9 @@ def _status_word(dev):
     if st is None:
         if _capturing(dev):
             raise RuntimeError("call once on this device before capturing into a CUDA graph")
-        st = _status[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        torch.cuda.current_stream(dev).synchronize()    # (other streams' calls write it, too)
+        _status[dev] = st
     return st.data_ptr()
 
 
@@ -140,6 +142,7 @@ def device_status(device="cuda", clear=False):
     st = int(_status[dev].item())
     if clear and st != fo.FO_OK:
         _status[dev].zero_()
+        torch.cuda.synchronize(dev)     # (before another stream's next error)
         for key in [k for k in _workspaces if k[1] == dev]:
             del _workspaces[key]
     return st

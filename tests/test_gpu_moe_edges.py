@@ -383,3 +383,21 @@ def test_prompt_refuses_tensors_that_require_a_gradient():
         layer(x)
     with torch.no_grad():
         assert torch.equal(layer(x), y)
+
+
+def test_an_error_on_another_stream_is_kept(monkeypatch):
+    """The device's first call runs behind other work on its stream, an erring call
+    at once on a second: the first's zeroing of the status does not undo it."""
+    monkeypatch.setattr(moe, "_status", {})
+    q = moe.quantize(torch.ones((128, 64), dtype=BF16, device="cuda"))
+    first, rows = (torch.tensor([v], dtype=torch.int32, device="cuda") for v in (64, 1))
+    d = torch.zeros((128, 128), dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+        moe.mx_gemm(q, q)
+    with torch.cuda.stream(r):
+        moe.mx_gemm(q, q, out=d, group_first=first, group_rows=rows)
+    assert moe.device_status(clear=True) == fo.FO_ERR_ARG
+    assert moe.device_status() == fo.FO_OK

@@ -77,3 +77,21 @@ def test_calls_that_would_lose_a_gradient_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_the_status_word_is_set_before_any_other_stream_can_use_it(device, monkeypatch):
+    """It is zeroed on one stream and used on all: once when it is made, and when
+    an error is cleared, its zero is waited for."""
+    dev, _ = device
+    waits = []
+    stream = lambda d: type("Stream", (), {"synchronize": lambda self: waits.append(d)})()
+    monkeypatch.setattr(torch.cuda, "current_stream", stream)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda d=None: waits.append(d))
+    moe._status_word(dev)
+    assert waits == [dev]
+    moe._status_word(dev)
+    assert waits == [dev]
+    gpu = torch.device("cuda", 0)
+    moe._status[gpu] = torch.tensor([fo.FO_ERR_ARG], dtype=torch.int32)
+    assert moe.device_status(gpu, clear=True) == fo.FO_ERR_ARG
+    assert waits == [dev, gpu, gpu]
