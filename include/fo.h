@@ -630,9 +630,10 @@ fo_status fo_mx_dequantize(const void* codes, const void* scales, int64_t batch,
  * F32).  With n_groups >= 1 a product per expert: B is a batch of n_groups
  * matrices, and rows [group_first[g], group_first[g] + group_rows[g]) of A
  * are multiplied by B_g; group_first[g] must be a multiple of 128 (as
- * fo_moe_route makes it) and the ranges must be disjoint and inside [0, M).
- * A group that breaks this is left out and sets *dev_status to FO_ERR_ARG.
- * Rows in no group are not written.  n_groups = 0: one product over all M
+ * fo_moe_route makes it) and the range inside [0, M).  A group that breaks
+ * this is left out and sets *dev_status to FO_ERR_ARG.  That the ranges are
+ * disjoint is not checked: a row in two of them holds elements of either
+ * product.  Rows in no group are not written.  n_groups = 0: one product over all M
  * rows, group_first and group_rows NULL.
  *  D: device, row_stride (elements) >= N; D and row_stride aligned to the
  *      element only (16-byte aligned rows are stored faster).
@@ -678,7 +679,7 @@ fo_status fo_moe_route_sizes(int64_t tokens, int32_t experts, int32_t top_k, int
  *  ids int32, weights float [tokens * top_k]; experts <= 1024, top_k <= 32.
  *  workspace: device, 16-byte aligned, fo_moe_route_sizes bytes, zeroed once
  *      before its first use; every call leaves it ready for the next.  Calls
- *      that overlap in time need one each.
+ *      that overlap in time need one each; a graph's replays are such calls too.
  *  dev_status: device int32, FO_ERR_TIMEOUT if a bounded wait ran out.  */
 fo_status fo_moe_route(const void* logits, fo_type type, int64_t tokens, int32_t experts,
                        int64_t row_stride, int32_t top_k, int32_t renormalize, int64_t capacity,
@@ -717,8 +718,10 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
  *  x: bf16, x_stride (elements) >= hidden; y: bf16, y_stride >= hidden.  x
  *      and the weights 16-byte aligned, x_stride a multiple of 8.
  *  router: bf16 [experts][hidden], 16-byte aligned.
- *  workspace: as for fo_moe_route (zeroed once before its first use, calls of
- *      any shape may share one; zero it again after FO_ERR_TIMEOUT). */
+ *  workspace: device, 16-byte aligned, fo_moe_few_workspace bytes, zeroed once
+ *      before its first use and again after FO_ERR_TIMEOUT.  Calls of any shape
+ *      may share one (of the largest's bytes), but not with fo_moe_route, nor
+ *      calls that overlap in time; a graph's replays are such calls too. */
 #define FO_MOE_FEW_TOKENS 64
 typedef struct {
   int32_t tokens, hidden, inter, experts, top_k;
