@@ -33,12 +33,18 @@
 //   bf16   1 token 117 us (6.0 TB/s), 8 tokens 366 (6.7), 48 tokens 419 (6.7):
 //          the reads, and 20 us around them (launch, router and choice 6, the two
 //          barriers, the join)
-//   4-bit  1 token 56 us (3.4 TB/s), 8 tokens 147 (4.5), 48 tokens 280 (2.7): the
-//          computing warps.  A stage of 20 KB takes them 800 to 900 cycles (HBM
-//          750 to 880) for one tile of tokens, nearly twice that for two: each
-//          word of codes passes through registers, and 8 warps start on a stage
-//          together.  Tried: 16 warps that halve a stage's columns or take turns
-//          at stages (no faster), operands taken half a stage ahead (15% slower).
+//   4-bit  1 token 56 us (3.4 TB/s), 8 tokens 148 (4.5), 48 tokens 287 (2.6) while no
+//          expert has more than 16, 350 with one of 17, 576 with one of all 48: the
+//          cut is even in weights, and an expert's stages take longer by its tiles of
+//          8 tokens.  No unit is near its limit (1 token: issue slots 28% busy, tensor
+//          cores 10%).  With the products taken out 1 token still takes 47 us: copies,
+//          barriers and the ends of tiles (2000 to 3000 cycles each), 16 us of it
+//          outside the two products.  A stage's products, 800 to 900 cycles per 20 KB
+//          (HBM 750 to 880) for one tile of tokens and nearly twice that for two, are
+//          a chain of shared memory, decoding, two MMAs and scaling in 8 warps that
+//          start together; they count with more tokens.  Tried: 16 warps that halve a
+//          stage's columns or take turns at stages (no faster), operands taken half a
+//          stage ahead (15% slower).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -37,10 +37,10 @@
 // neither.  Nor do scales in a ring of their own, ahead of the codes, or a second
 // set of epilogue warps.
 //
-// Measured: 552 us for 32768 rows over 8 experts, N = 14336, K = 4096 (7.0
-// PFLOP/s at the 1.67 GHz that the power limit leaves; 630 us in a long run), 41
-// us for 8192 x 4096 x 2752 with fp32 output (writing that alone takes 21), 10.4
-// us for 512 x 4096 x 4096.
+// Measured: 552 us in a short run and up to 630 in a long one for 32768 rows over 8
+// experts, N = 14336, K = 4096 (7.0 to 6.1 PFLOP/s, at the 1.67 GHz and below that
+// the power limit leaves), 44 us for 8192 x 4096 x 2752 with fp32 output (writing
+// that alone takes 21), 10.4 us for 512 x 4096 x 4096.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

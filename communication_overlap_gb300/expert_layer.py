@@ -8,8 +8,10 @@
 Weights are kept once, in the 4-bit form.  Up to fo.FO_MOE_FEW_TOKENS tokens
 go through the one-kernel layer, which reads only the experts that are chosen.
 More go through the router, the gathering quantizer and one product per
-projection over all experts; the activation between the projections and the
-weighted sum of a token's rows are plain torch operations.
+projection over all experts; the router's logits, the activation between the
+projections and the weighted sum of a token's rows are plain torch operations.
+Neither way is part of autograd: backward is called with gradients, and tensors
+that require one are refused.
 
 ``python -m communication_overlap_gb300.expert_layer`` runs a prompt, a
 gradient and some generation steps (the last ones replayed from a CUDA graph)
@@ -68,6 +70,8 @@ class ExpertLayer:
                          device=x.device)
         moe.mx_gemm(moe.quantize(x, row_index=r.row_token), self.w1, out=up, **groups)
         gate, up = up.chunk(2, dim=1)
+        # (the gate, up and silu rounded to bf16, 2^-9 each: the conversion that
+        # follows rounds to two significant bits)
         h = torch.nn.functional.silu(gate).mul_(up)
         rows = self._rows(moe.quantize(h), self.w2, groups)
         y = torch.bmm(r.weights.unsqueeze(1), rows[r.token_row.long()]).squeeze(1)

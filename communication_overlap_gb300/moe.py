@@ -300,7 +300,8 @@ class FewTokenLayer:
 
     router: bf16 [experts, hidden].  w1: bf16 [experts, 2 * inter, hidden],
     the gate's rows first, and w2: bf16 [experts, hidden, inter]; or both as
-    MxTensor batches of those shapes."""
+    MxTensor batches of those shapes.  x's rows and all of these start on 16
+    bytes."""
 
     def __init__(self, router, w1, w2, top_k, renormalize=True, act="silu"):
         mx = isinstance(w1, MxTensor)
