@@ -105,7 +105,9 @@ def draw(rng):
         return dict(op=op, tokens=tokens, experts=experts, top_k=top_k, groups=groups,
                     top_groups=top_groups, group_top=rng.choice([1, 2]), scoring=scoring,
                     bias=rng.random() < 0.6, scale=rng.choice([1.0, 2.5, 16.0]),
-                    dtype=rng.choice(["bf16", "f32"]), renormalize=rng.random() < 0.5,
+                    dtype=rng.choice(["bf16", "f32"]),
+                    # (of one weight, renormalised, the gradient is zero)
+                    renormalize=top_k > 1 and rng.random() < 0.5,
                     capacity=capacity, backward=rng.random() < 0.5)
     if op == "norm":
         hidden = _log_int(rng, 64, 8192)
