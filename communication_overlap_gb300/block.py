@@ -1,0 +1,268 @@
+"""What stands around the expert layer's products in a model's block, on torch
+tensors.
+
+Plumbing only, as ``moe.py``: torch provides device memory and the current
+stream, every step is a libfo.so call (``include/fo.h`` states what each
+computes).
+
+  norm, norm_backward           RMS norm of a block's output, its gate and scale
+                                into the residual stream, RMS norm of the stream
+                                for the next block, in one pass
+  activate, activate_backward   the gated activation between the projections,
+                                with a checkpoint of 8 bits for the backward pass
+  combine, combine_backward     the weighted sum of a token's rows of the experts'
+                                outputs
+
+Calls run on the current stream of the tensors' device and do not synchronise.
+None is part of autograd: tensors that require a gradient are refused (detach
+them, or call under ``torch.no_grad()``).  ``moe.device_status`` tells of a row
+index that was out of range.
+"""
+import functools
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import fo
+from .moe import (_ACTS, _int32, _on_gpu, _row_stride, _run, _status_word, _stream, _type,
+                  _untracked)
+
+_checkpoint_sizes = functools.lru_cache(256)(fo.fo_checkpoint_sizes)
+
+
+def _detached(*tensors):
+    _untracked(*(t for t in tensors if t is not None))
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _matrix(t, shape, dtype, what):
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} {shape} expected, not {t.dtype} {tuple(t.shape)}")
+
+
+# ------------------------------------------------------------------ the norms
+
+@dataclass
+class Normed:
+    stream: torch.Tensor                # the residual stream after the block
+    y: Optional[torch.Tensor]           # the next block's input, where pre_gain was given
+    post_rstd: Optional[torch.Tensor]   # fp32 [tokens], for norm_backward
+    pre_rstd: Optional[torch.Tensor]
+
+
+@dataclass
+class NormGrads:
+    x: torch.Tensor
+    residual: Optional[torch.Tensor]
+    post_gain: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+    pre_gain: Optional[torch.Tensor]
+
+
+def _norm_desc(x, residual, post_gain, gate, pre_gain, scale, eps):
+    """(device, tokens, hidden, description, the gate's row stride)"""
+    if x.dim() != 2:
+        raise ValueError("x: [tokens, hidden] expected")
+    dev = _on_gpu(x, residual, post_gain, gate, pre_gain)
+    T, H = x.shape
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual: {tuple(x.shape)} expected, not {tuple(residual.shape)}")
+    stream_type = x.dtype if residual is None else residual.dtype
+    if x.dtype == torch.float32 and stream_type != torch.float32:
+        raise ValueError("a bf16 residual stream takes bf16 blocks")
+    params = [p for p in (post_gain, gate, pre_gain) if p is not None]
+    param_type = params[0].dtype if params else torch.float32
+    for p, what in ((post_gain, "post_gain"), (pre_gain, "pre_gain")):
+        if p is not None and (tuple(p.shape) != (H,) or not p.is_contiguous()):
+            raise ValueError(f"{what}: contiguous [{H}] expected, not {tuple(p.shape)}")
+    if any(p.dtype != param_type for p in params):
+        raise ValueError("the gains and the gate have one type")
+    gates, gate_stride = 1, 0
+    if gate is not None:
+        if gate.dim() == 2 and gate.shape[1] == H:
+            gates, gate_stride = gate.shape[0], _row_stride(gate, "gate")
+        elif tuple(gate.shape) == (H,) and gate.is_contiguous():
+            gate_stride = H
+        else:
+            raise ValueError(f"gate: [{H}] or [rows, {H}] expected, not {tuple(gate.shape)}")
+        if gates < 1 or T % gates:
+            raise ValueError(f"gate: {gates} rows do not divide {T} tokens")
+    desc = fo.make_norm_desc(T, H, _type(x.dtype), _type(stream_type), _type(param_type), gates,
+                             scale, eps)
+    return dev, T, H, desc, gate_stride
+
+
+def norm(x, residual=None, post_gain=None, gate=None, scale=1.0, pre_gain=None, eps=1e-6):
+    """stream = residual + scale * gate * (RMS norm of x times post_gain), y = RMS
+    norm of the stream times pre_gain; without post_gain x as it is, without
+    residual or gate as if they were zeros or ones.
+
+    x: [tokens, hidden], bf16 or fp32 (any row stride); y has its type.
+    residual and stream: bf16 or fp32, fp32 for fp32 x.  gains: [hidden]; gate:
+    [hidden], or [rows, hidden] where rows divides tokens (a row for each run of
+    tokens / rows tokens); all of one type.  Where nothing but pre_gain is
+    given, the stream is x itself."""
+    _detached(x, residual, post_gain, gate, pre_gain)
+    dev, T, H, desc, gate_stride = _norm_desc(x, residual, post_gain, gate, pre_gain, scale, eps)
+    summed = residual is not None or post_gain is not None or gate is not None or scale != 1.0
+    empty = torch.empty
+    stream = empty((T, H), dtype=x.dtype if residual is None else residual.dtype,
+                   device=dev) if summed else x
+    y = None if pre_gain is None else empty((T, H), dtype=x.dtype, device=dev)
+    post_rstd = None if post_gain is None else empty(T, dtype=torch.float32, device=dev)
+    pre_rstd = None if pre_gain is None else empty(T, dtype=torch.float32, device=dev)
+    _run(dev, fo.fo_block_norm, desc, x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
+         0 if residual is None else _row_stride(residual, "residual"), _ptr(post_gain),
+         _ptr(gate), gate_stride, _ptr(pre_gain), stream.data_ptr() if summed else 0, H, _ptr(y),
+         H, _ptr(post_rstd), _ptr(pre_rstd), _stream(dev))
+    return Normed(stream, y, post_rstd, pre_rstd)
+
+
+def norm_backward(x, residual, normed, dstream=None, dy=None, post_gain=None, gate=None,
+                  scale=1.0, pre_gain=None):
+    """The gradients of norm's inputs and parameters, from those of its stream
+    (None: zeros) and of its y (None where there was none).  x, residual and the
+    parameters: the forward call's; normed: what it returned."""
+    _detached(x, residual, post_gain, gate, pre_gain, dstream, dy)
+    dev, T, H, desc, gate_stride = _norm_desc(x, residual, post_gain, gate, pre_gain, scale, 0.0)
+    _on_gpu(x, dstream, dy, normed.post_rstd, normed.pre_rstd)
+    if (dy is None) != (pre_gain is None):
+        raise ValueError("dy and pre_gain go together")
+    if dy is not None:
+        _matrix(dy, (T, H), x.dtype, "dy")
+    if dstream is not None:
+        _matrix(dstream, (T, H), x.dtype if residual is None else residual.dtype, "dstream")
+    for gain, rstd, what in ((post_gain, normed.post_rstd, "post"),
+                             (pre_gain, normed.pre_rstd, "pre")):
+        if gain is not None and (rstd is None or tuple(rstd.shape) != (T,)):
+            raise ValueError(f"normed holds no {what}_rstd of {T} tokens")
+    empty, like = torch.empty, torch.empty_like
+    dx = empty((T, H), dtype=x.dtype, device=dev)
+    dresidual = None if residual is None else empty((T, H), dtype=residual.dtype, device=dev)
+    dpost = None if post_gain is None else like(post_gain)
+    dpre = None if pre_gain is None else like(pre_gain)
+    dgate = None if gate is None else empty(gate.shape, dtype=gate.dtype, device=dev)
+    ws = empty(fo.fo_block_norm_workspace(desc), dtype=torch.uint8, device=dev)
+    _run(dev, fo.fo_block_norm_backward, desc, x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
+         0 if residual is None else _row_stride(residual, "residual"), _ptr(post_gain),
+         _ptr(gate), gate_stride, _ptr(pre_gain), _ptr(normed.post_rstd), _ptr(normed.pre_rstd),
+         _ptr(dstream), 0 if dstream is None else _row_stride(dstream, "dstream"), _ptr(dy),
+         0 if dy is None else _row_stride(dy, "dy"), dx.data_ptr(), H, _ptr(dresidual), H,
+         _ptr(dpost), _ptr(dgate), _ptr(dpre), ws.data_ptr(), _stream(dev))
+    return NormGrads(dx, dresidual, dpost, dgate, dpre)
+
+
+# ------------------------------------------------------------------ the activation
+
+@dataclass
+class Checkpoint:
+    """[gate | up] rows in 8 bits: int8 codes [rows, 2, padded], a scale byte per
+    32 values (include/fo.h states the form)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    inter: int
+    act: str
+
+    def values(self, dtype=torch.float32):
+        """The values it stands for, [rows, 2 * inter]."""
+        s = self.scales.view(self.rows, 2, -1, 1).to(torch.int32)
+        step = torch.where(s == 0, torch.full_like(s, 1 << 22), s << 23).view(torch.float32)
+        step = torch.where(s == 255, torch.full_like(step, float("nan")), step)
+        v = self.codes.view(self.rows, 2, s.shape[2], 32).to(torch.float32) * step
+        return v.view(self.rows, 2, -1)[..., :self.inter].reshape(self.rows, -1).to(dtype)
+
+
+def activate(u, act="silu", checkpoint=False):
+    """h = act(gate) * up for rows u = [gate | up] (bf16 or fp32, any row stride),
+    and with checkpoint what activate_backward needs of u, in 8 bits: (h, kept),
+    kept None without."""
+    _detached(u)
+    if u.dim() != 2 or u.shape[1] % 2:
+        raise ValueError("u: [rows, 2 * inter] expected")
+    dev, type_ = _on_gpu(u), _type(u.dtype)
+    if act not in _ACTS:
+        raise ValueError(f"act: one of {sorted(_ACTS)} expected, not {act!r}")
+    R, I = u.shape[0], u.shape[1] // 2
+    h = torch.empty((R, I), dtype=u.dtype, device=dev)
+    kept = None
+    if checkpoint:
+        nc, ns = _checkpoint_sizes(R, I)
+        kept = Checkpoint(torch.empty(nc, dtype=torch.int8, device=dev),
+                          torch.empty(ns, dtype=torch.uint8, device=dev), R, I, act)
+    _run(dev, fo.fo_gated_act, u.data_ptr(), type_, R, I, _row_stride(u, "u"), _ACTS[act],
+         h.data_ptr(), I, kept.codes.data_ptr() if kept else 0,
+         kept.scales.data_ptr() if kept else 0, _stream(dev))
+    return h, kept
+
+
+def activate_backward(dh, kept):
+    """The gradient of u (in dh's type) from that of h, with the values that the
+    checkpoint stands for."""
+    _detached(dh)
+    if tuple(dh.shape) != (kept.rows, kept.inter):
+        raise ValueError(f"dh: {(kept.rows, kept.inter)} expected, not {tuple(dh.shape)}")
+    dev, type_ = _on_gpu(dh, kept.codes, kept.scales), _type(dh.dtype)
+    du = torch.empty((kept.rows, 2 * kept.inter), dtype=dh.dtype, device=dev)
+    _run(dev, fo.fo_gated_act_backward, dh.data_ptr(), type_, kept.rows, kept.inter,
+         _row_stride(dh, "dh"), _ACTS[kept.act], kept.codes.data_ptr(), kept.scales.data_ptr(),
+         du.data_ptr(), 2 * kept.inter, _stream(dev))
+    return du
+
+
+# ------------------------------------------------------------------ the weighted sum
+
+def _slots(token_row, weights):
+    if token_row.dim() != 2:
+        raise ValueError("token_row: int32 [tokens, top_k] expected")
+    _int32(token_row, token_row.numel(), "token_row")
+    if weights is not None and (weights.dtype != torch.float32 or not weights.is_contiguous()
+                                or weights.shape != token_row.shape):
+        raise ValueError(f"weights: contiguous fp32 {tuple(token_row.shape)} expected")
+    return token_row.shape
+
+
+def combine(rows, token_row, weights=None, out=None, out_dtype=None):
+    """y[t] = sum over slots s of weights[t, s] * rows[token_row[t, s]] (-1: no
+    row; no weights: ones).  rows: [table rows, hidden], bf16 or fp32, any row
+    stride; token_row and weights as a Routing holds them."""
+    _detached(rows, weights)
+    if rows.dim() != 2:
+        raise ValueError("rows: [table rows, hidden] expected")
+    T, k = _slots(token_row, weights)
+    dev, type_ = _on_gpu(rows, token_row, weights, out), _type(rows.dtype)
+    M, H = rows.shape
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=dev)
+    if tuple(out.shape) != (T, H):
+        raise ValueError(f"out: {(T, H)} expected, not {tuple(out.shape)}")
+    _run(dev, fo.fo_moe_combine, _ptr(rows), type_, M, H, _row_stride(rows, "rows"),
+         token_row.data_ptr(), _ptr(weights), T, k, out.data_ptr(), _type(out.dtype),
+         _row_stride(out, "out"), _status_word(dev), _stream(dev))
+    return out
+
+
+def combine_backward(dy, rows, token_row, row_token, weights=None):
+    """(drows, dweights): drows has rows' type, with zeros where a row holds no
+    token; dweights (fp32) is None without weights.  token_row and row_token: of
+    one Routing."""
+    _detached(dy, rows, weights)
+    if rows.dim() != 2:
+        raise ValueError("rows: [table rows, hidden] expected")
+    T, k = _slots(token_row, weights)
+    M, H = rows.shape
+    if tuple(dy.shape) != (T, H):
+        raise ValueError(f"dy: {(T, H)} expected, not {tuple(dy.shape)}")
+    _int32(row_token, M, "row_token")
+    dev = _on_gpu(dy, rows, token_row, row_token, weights)
+    drows = torch.empty((M, H), dtype=rows.dtype, device=dev)
+    dweights = None if weights is None else torch.empty_like(weights)
+    _run(dev, fo.fo_moe_combine_backward, dy.data_ptr(), _type(dy.dtype), _row_stride(dy, "dy"),
+         rows.data_ptr(), _type(rows.dtype), M, H, _row_stride(rows, "rows"),
+         token_row.data_ptr(), row_token.data_ptr(), _ptr(weights), T, k, drows.data_ptr(), H,
+         _ptr(dweights), _status_word(dev), _stream(dev))
+    return drows, dweights

@@ -2,14 +2,20 @@
 // include/fo.h): argument checks and dispatch to the kernel launchers.
 #include <cuda_runtime.h>
 
+#include <cmath>
+
+#include "api_checks.h"
 #include "fo_internal.h"
 #include "moe_internal.h"
+
+using fo::aligned_type;
+using fo::device_ok;
+using fo::fits_int32;
+using fo::type_ok;
 
 namespace {
 
 constexpr int64_t kMaxBytes = int64_t(1) << 62;
-
-bool type_ok(fo_type t) { return t == FO_TYPE_BF16 || t == FO_TYPE_F32; }
 
 // Padded rows x columns of a batch: false when the bytes pass 2^62.
 bool mx_elements(int64_t batch, int64_t rows, int64_t cols, int64_t* n) {
@@ -21,25 +27,6 @@ bool mx_elements(int64_t batch, int64_t rows, int64_t cols, int64_t* n) {
   if (b >= kMaxBytes) return false;
   *n = b;
   return true;
-}
-
-// Sizes that the kernels index with 32-bit rows and columns.
-bool fits_int32(int64_t n) { return n >= 0 && n <= (int64_t(1) << 31) - 256; }
-
-bool device_ok(fo_status* st) {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-    *st = FO_ERR_CUDA;
-    return false;
-  }
-  *st = FO_ERR_UNSUPPORTED;
-  return major == 10 && minor == 3;
-}
-
-bool aligned_type(const void* p, fo_type t) {
-  return (reinterpret_cast<uintptr_t>(p) & (t == FO_TYPE_BF16 ? 1u : 3u)) == 0;
 }
 
 bool few_desc_ok(const fo_moe_few_desc* d) {
@@ -55,6 +42,16 @@ bool few_desc_ok(const fo_moe_few_desc* d) {
 bool route_shape_ok(int64_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= 0 && experts >= 1 && experts <= fo::kRouteExperts && top_k >= 1 &&
          top_k <= fo::kRouteTopK && top_k <= experts;
+}
+
+bool route_desc_ok(const fo_route_desc* d) {
+  if (!d || !route_shape_ok(0, d->experts, d->top_k) || d->capacity < 0) return false;
+  if (d->score != FO_SCORE_SOFTMAX && d->score != FO_SCORE_SIGMOID) return false;
+  if (d->groups < 1 || d->groups > fo::kRouteGroups || d->experts % d->groups) return false;
+  if (d->top_groups < 1 || d->top_groups > d->groups) return false;
+  if (d->top_k > int64_t(d->top_groups) * (d->experts / d->groups)) return false;
+  if (d->group_top != 1 && d->group_top != 2) return false;
+  return std::isfinite(d->scale) && d->scale > 0.0f;
 }
 
 }  // namespace
@@ -188,6 +185,50 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
   return fo::launch_moe_route_backward(logits, type, tokens, experts, row_stride, top_k,
                                        renormalize != 0, ids, weights, dweights, dlogits,
                                        dlogits_stride, stream);
+}
+
+fo_status fo_moe_route_scored(const fo_route_desc* d, const void* logits, fo_type type,
+                              int64_t tokens, int64_t row_stride, const float* bias,
+                              int32_t* ids, float* weights, int32_t* row_token,
+                              int32_t* row_slot, int32_t* token_row, int32_t* expert_first,
+                              int32_t* expert_rows, void* workspace, int32_t* dev_status,
+                              void* stream) {
+  if (!route_desc_ok(d)) return FO_ERR_ARG;
+  int64_t table_rows = 0;
+  fo_status st = fo_moe_route_sizes(tokens, d->experts, d->top_k, d->capacity, &table_rows,
+                                    nullptr);
+  if (st != FO_OK) return st;
+  if (!type_ok(type) || row_stride < d->experts) return FO_ERR_ARG;
+  if (!expert_first || !expert_rows || !workspace || !dev_status) return FO_ERR_ARG;
+  if (tokens > 0 && (!logits || !ids || !weights || !token_row)) return FO_ERR_ARG;
+  if (table_rows > 0 && (!row_token || !row_slot)) return FO_ERR_ARG;
+  if (!aligned_type(logits, type) || !fo::aligned4(bias) || !fo::aligned4(ids) ||
+      !fo::aligned4(weights) || !fo::aligned4(row_token) || !fo::aligned4(row_slot) ||
+      !fo::aligned4(token_row) || !fo::aligned4(expert_first) || !fo::aligned4(expert_rows) ||
+      !fo::aligned4(dev_status) || !fo::aligned16(workspace))
+    return FO_ERR_ARG;
+  if (!device_ok(&st)) return st;
+  return fo::launch_moe_route_scored(*d, logits, type, tokens, row_stride, bias, table_rows, ids,
+                                     weights, row_token, row_slot, token_row, expert_first,
+                                     expert_rows, workspace, dev_status, stream);
+}
+
+fo_status fo_moe_route_scored_backward(const fo_route_desc* d, const void* logits, fo_type type,
+                                       int64_t tokens, int64_t row_stride, const int32_t* ids,
+                                       const float* weights, const float* dweights,
+                                       void* dlogits, int64_t dlogits_stride, void* stream) {
+  if (!route_desc_ok(d) || !type_ok(type) || tokens < 0) return FO_ERR_ARG;
+  if (row_stride < d->experts || dlogits_stride < d->experts) return FO_ERR_ARG;
+  if (tokens == 0) return FO_OK;
+  if (!logits || !ids || !weights || !dweights || !dlogits) return FO_ERR_ARG;
+  if (!aligned_type(logits, type) || !aligned_type(dlogits, type) || !fo::aligned4(ids) ||
+      !fo::aligned4(weights) || !fo::aligned4(dweights))
+    return FO_ERR_ARG;
+  if (!fits_int32(tokens)) return FO_ERR_UNSUPPORTED;
+  fo_status st;
+  if (!device_ok(&st)) return st;
+  return fo::launch_moe_route_scored_backward(*d, logits, type, tokens, row_stride, ids, weights,
+                                              dweights, dlogits, dlogits_stride, stream);
 }
 
 fo_status fo_moe_few_workspace(const fo_moe_few_desc* d, int64_t* bytes) {

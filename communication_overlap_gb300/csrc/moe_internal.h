@@ -10,6 +10,7 @@ namespace fo {
 
 constexpr int kRouteExperts = 1024;   // experts a router may choose from
 constexpr int kRouteTopK = 32;        // slots of a token
+constexpr int kRouteGroups = 32;      // groups of experts
 
 // mx_quantize.cu
 fo_status launch_mx_quantize(const void* src, fo_type type, int64_t batch, int64_t batch_stride,
@@ -40,6 +41,20 @@ fo_status launch_moe_route_backward(const void* logits, fo_type type, int64_t to
                                     bool renormalize, const int32_t* ids, const float* weights,
                                     const float* dweights, void* dlogits,
                                     int64_t dlogits_stride, void* stream);
+
+fo_status launch_moe_route_scored(const fo_route_desc& d, const void* logits, fo_type type,
+                                  int64_t tokens, int64_t row_stride, const float* bias,
+                                  int64_t table_rows, int32_t* ids, float* weights,
+                                  int32_t* row_token, int32_t* row_slot, int32_t* token_row,
+                                  int32_t* expert_first, int32_t* expert_rows, void* workspace,
+                                  int32_t* dev_status, void* stream);
+
+// moe_route_scored_backward.cu
+fo_status launch_moe_route_scored_backward(const fo_route_desc& d, const void* logits,
+                                           fo_type type, int64_t tokens, int64_t row_stride,
+                                           const int32_t* ids, const float* weights,
+                                           const float* dweights, void* dlogits,
+                                           int64_t dlogits_stride, void* stream);
 
 // moe_few.cu
 int64_t few_workspace_bytes(const fo_moe_few_desc& d);

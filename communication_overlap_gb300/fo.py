@@ -21,6 +21,7 @@ FO_ACT_NONE, FO_ACT_RELU, FO_ACT_SILU = range(3)
 FO_BAND_FORWARD, FO_BAND_SERPENTINE = range(2)
 FO_CONSUMER_SHARED, FO_CONSUMER_RESERVED = range(2)
 FO_TYPE_BF16, FO_TYPE_F32, FO_TYPE_MX4 = range(3)
+FO_SCORE_SOFTMAX, FO_SCORE_SIGMOID = range(2)
 FO_MOE_FEW_TOKENS = 64   # include/fo.h
 (FO_TAB_SLOT_TILE, FO_TAB_TILE_SLOT, FO_TAB_SLOT_GROUP, FO_TAB_GROUP_TILES, FO_TAB_UNIT,
  FO_TAB_PART_START, FO_TAB_PART_LEN, FO_TAB_PART_DST, FO_TAB_DEST_UNITS,
@@ -51,6 +52,19 @@ class fo_plan_desc(ctypes.Structure):
 class fo_moe_few_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "tokens", "hidden", "inter", "experts", "top_k", "renormalize", "act", "weights")]
+
+
+class fo_route_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "experts", "top_k", "renormalize", "score", "groups", "top_groups", "group_top")] + [
+        ("scale", ctypes.c_float), ("capacity", ctypes.c_int64)]
+
+
+class fo_norm_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("param_type", ctypes.c_int32), ("gates", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class FoError(RuntimeError):
@@ -134,6 +148,27 @@ def lib():
             "fo_moe_route_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int32,
                                                      _i64, ctypes.c_int32, ctypes.c_int32, _vp,
                                                      _vp, _vp, _vp, _i64, _vp]),
+            "fo_moe_route_scored": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64] + [_vp] * 11),
+            "fo_moe_route_scored_backward": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64,
+                                                            _vp, _vp, _vp, _vp, _i64, _vp]),
+            "fo_moe_combine": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _i64,
+                                              ctypes.c_int32, _vp, ctypes.c_int, _i64, _vp,
+                                              _vp]),
+            "fo_moe_combine_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _vp, ctypes.c_int,
+                                                       _i64, _i64, _i64, _vp, _vp, _vp, _i64,
+                                                       ctypes.c_int32, _vp, _i64, _vp, _vp,
+                                                       _vp]),
+            "fo_checkpoint_sizes": (ctypes.c_int, [_i64, _i64, _i64p, _i64p]),
+            "fo_gated_act": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int,
+                                            _vp, _i64, _vp, _vp, _vp]),
+            "fo_gated_act_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64,
+                                                     ctypes.c_int, _vp, _vp, _vp, _i64, _vp]),
+            "fo_block_norm": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                             _i64, _vp, _i64, _vp, _vp, _vp]),
+            "fo_block_norm_workspace": (ctypes.c_int, [_vp, _i64p]),
+            "fo_block_norm_backward": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                                                      _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp,
+                                                      _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
             "fo_moe_few_workspace": (ctypes.c_int, [ctypes.POINTER(fo_moe_few_desc), _i64p]),
             "fo_moe_few": (ctypes.c_int, [ctypes.POINTER(fo_moe_few_desc), _vp, _i64, _vp, _vp,
                                           _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
@@ -408,6 +443,109 @@ def fo_moe_route_backward(logits, type, tokens, experts, row_stride, top_k, reno
            lib().fo_moe_route_backward(logits, type, tokens, experts, row_stride, top_k,
                                        1 if renormalize else 0, ids, weights, dweights, dlogits,
                                        dlogits_stride, stream or None))
+
+
+def make_route_desc(experts, top_k, renormalize=True, capacity=0, score=FO_SCORE_SOFTMAX,
+                    groups=1, top_groups=1, group_top=1, scale=1.0):
+    return fo_route_desc(experts, top_k, 1 if renormalize else 0, score, groups, top_groups,
+                         group_top, scale, capacity)
+
+
+def fo_moe_route_scored(desc, logits, type, tokens, row_stride, bias, ids, weights, row_token,
+                        row_slot, token_row, expert_first, expert_rows, workspace, dev_status,
+                        stream):
+    """desc: make_route_desc's; device addresses; bias 0 for none."""
+    _check("fo_moe_route_scored",
+           lib().fo_moe_route_scored(ctypes.byref(desc), logits, type, tokens, row_stride,
+                                     bias or None, ids, weights, row_token, row_slot, token_row,
+                                     expert_first, expert_rows, workspace, dev_status,
+                                     stream or None))
+
+
+def fo_moe_route_scored_backward(desc, logits, type, tokens, row_stride, ids, weights, dweights,
+                                 dlogits, dlogits_stride, stream):
+    _check("fo_moe_route_scored_backward",
+           lib().fo_moe_route_scored_backward(ctypes.byref(desc), logits, type, tokens,
+                                              row_stride, ids, weights, dweights, dlogits,
+                                              dlogits_stride, stream or None))
+
+
+def fo_moe_combine(rows, type, table_rows, hidden, row_stride, token_row, weights, tokens, top_k,
+                   y, y_type, y_stride, dev_status, stream):
+    """Device addresses; weights 0 for ones."""
+    _check("fo_moe_combine",
+           lib().fo_moe_combine(rows or None, type, table_rows, hidden, row_stride, token_row,
+                                weights or None, tokens, top_k, y, y_type, y_stride, dev_status,
+                                stream or None))
+
+
+def fo_moe_combine_backward(dy, dy_type, dy_stride, rows, type, table_rows, hidden, row_stride,
+                            token_row, row_token, weights, tokens, top_k, drows, drows_stride,
+                            dweights, dev_status, stream):
+    """Device addresses; dweights (and then rows) 0 to leave them out."""
+    _check("fo_moe_combine_backward",
+           lib().fo_moe_combine_backward(dy, dy_type, dy_stride, rows or None, type, table_rows,
+                                         hidden, row_stride, token_row, row_token,
+                                         weights or None, tokens, top_k, drows, drows_stride,
+                                         dweights or None, dev_status, stream or None))
+
+
+def fo_checkpoint_sizes(rows, inter):
+    """(code bytes, scale bytes) of the checkpoint of `rows` rows of 2 * inter values."""
+    c, s = ctypes.c_int64(), ctypes.c_int64()
+    _check("fo_checkpoint_sizes",
+           lib().fo_checkpoint_sizes(rows, inter, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def fo_gated_act(u, type, rows, inter, u_stride, act, h, h_stride, codes, scales, stream):
+    """Device addresses; codes and scales 0 for no checkpoint."""
+    _check("fo_gated_act",
+           lib().fo_gated_act(u, type, rows, inter, u_stride, act, h, h_stride, codes or None,
+                              scales or None, stream or None))
+
+
+def fo_gated_act_backward(dh, type, rows, inter, dh_stride, act, codes, scales, du, du_stride,
+                          stream):
+    _check("fo_gated_act_backward",
+           lib().fo_gated_act_backward(dh, type, rows, inter, dh_stride, act, codes, scales, du,
+                                       du_stride, stream or None))
+
+
+def make_norm_desc(tokens, hidden, type, stream_type, param_type, gates=1, scale=1.0, eps=0.0):
+    return fo_norm_desc(tokens, hidden, type, stream_type, param_type, gates, scale, eps)
+
+
+def fo_block_norm(desc, x, x_stride, residual, residual_stride, post_gain, gate, gate_stride,
+                  pre_gain, sum, sum_stride, y, y_stride, post_rstd, pre_rstd, stream):
+    """desc: make_norm_desc's; device addresses, 0 where the header allows NULL."""
+    _check("fo_block_norm",
+           lib().fo_block_norm(ctypes.byref(desc), x, x_stride, residual or None,
+                               residual_stride, post_gain or None, gate or None, gate_stride,
+                               pre_gain or None, sum or None, sum_stride, y or None, y_stride,
+                               post_rstd or None, pre_rstd or None, stream or None))
+
+
+def fo_block_norm_workspace(desc):
+    n = ctypes.c_int64()
+    _check("fo_block_norm_workspace",
+           lib().fo_block_norm_workspace(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def fo_block_norm_backward(desc, x, x_stride, residual, residual_stride, post_gain, gate,
+                           gate_stride, pre_gain, post_rstd, pre_rstd, dsum, dsum_stride, dy,
+                           dy_stride, dx, dx_stride, dresidual, dresidual_stride, dpost, dgate,
+                           dpre, workspace, stream):
+    """desc: make_norm_desc's; device addresses, 0 where the header allows NULL."""
+    _check("fo_block_norm_backward",
+           lib().fo_block_norm_backward(ctypes.byref(desc), x, x_stride, residual or None,
+                                        residual_stride, post_gain or None, gate or None,
+                                        gate_stride, pre_gain or None, post_rstd or None,
+                                        pre_rstd or None, dsum or None, dsum_stride, dy or None,
+                                        dy_stride, dx, dx_stride, dresidual or None,
+                                        dresidual_stride, dpost or None, dgate or None,
+                                        dpre or None, workspace, stream or None))
 
 
 def make_few_desc(tokens, hidden, inter, experts, top_k, renormalize=True, act=FO_ACT_SILU,

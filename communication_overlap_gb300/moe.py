@@ -253,29 +253,70 @@ class Routing:
     expert_rows: torch.Tensor   # int32 [experts]
 
 
-def route(logits, top_k, renormalize=True, capacity=0):
-    """The top-k choice of logits [tokens, experts] (bf16 or fp32)."""
+_SCORES = {"softmax": fo.FO_SCORE_SOFTMAX, "sigmoid": fo.FO_SCORE_SIGMOID}
+
+
+@functools.lru_cache(256)
+def _route_desc(experts, top_k, renormalize, capacity, scoring, groups, top_groups, group_top,
+                scale):
+    """The balanced router's description, None where the call is the plain router's."""
+    if scoring not in _SCORES:
+        raise ValueError(f"scoring: one of {sorted(_SCORES)} expected, not {scoring!r}")
+    if scoring == "softmax" and groups == 1 and scale == 1.0:
+        return None
+    return fo.make_route_desc(experts, top_k, renormalize, capacity, _SCORES[scoring], groups,
+                              top_groups, group_top, scale)
+
+
+def route(logits, top_k, renormalize=True, capacity=0, scoring="softmax", bias=None, groups=1,
+          top_groups=1, group_top=1, scale=1.0):
+    """The top-k choice of logits [tokens, experts] (bf16 or fp32).
+
+    The balanced router's options: scoring "softmax" or "sigmoid"; bias (fp32
+    [experts]) is added to the scores for the choice, not for the weights;
+    with groups, only the experts of the top_groups groups whose group_top (1
+    or 2) largest sum to the most may be chosen; scale multiplies the weights."""
     _untracked(logits)
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
-    dev, type_ = _on_gpu(logits), _type(logits.dtype)
+    dev, type_ = _on_gpu(logits, bias), _type(logits.dtype)
     T, E = logits.shape
     M, nbytes = _route_sizes(T, E, top_k, capacity)
+    desc = _route_desc(E, top_k, bool(renormalize), capacity, scoring, groups, top_groups,
+                       group_top, float(scale))
+    if bias is not None:
+        if bias.dtype != torch.float32 or not bias.is_contiguous() or tuple(bias.shape) != (E,):
+            raise ValueError(f"bias: contiguous fp32[{E}] expected")
+        if desc is None:
+            desc = fo.make_route_desc(E, top_k, renormalize, capacity)
+    elif desc is None and (top_groups, group_top) != (1, 1):
+        # (of one group there is one to choose: as the balanced router refuses others)
+        desc = fo.make_route_desc(E, top_k, renormalize, capacity, top_groups=top_groups,
+                                  group_top=group_top)
     # (seven allocations are cheaper than one and seven views of it)
     new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
     ids, token_row, row_token, row_slot = new(T, top_k), new(T, top_k), new(M), new(M)
     first, rows = new(E), new(E)
     weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     ws = _workspace("route", dev, nbytes)
-    _run(dev, fo.fo_moe_route, logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"),
-         top_k, renormalize, capacity, ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(),
-         row_slot.data_ptr(), token_row.data_ptr(), first.data_ptr(), rows.data_ptr(),
-         ws.data_ptr(), _status_word(dev), _stream(dev))
+    if desc is None:
+        _run(dev, fo.fo_moe_route, logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"),
+             top_k, renormalize, capacity, ids.data_ptr(), weights.data_ptr(),
+             row_token.data_ptr(), row_slot.data_ptr(), token_row.data_ptr(), first.data_ptr(),
+             rows.data_ptr(), ws.data_ptr(), _status_word(dev), _stream(dev))
+    else:
+        _run(dev, fo.fo_moe_route_scored, desc, logits.data_ptr(), type_, T,
+             _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(),
+             ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(), row_slot.data_ptr(),
+             token_row.data_ptr(), first.data_ptr(), rows.data_ptr(), ws.data_ptr(),
+             _status_word(dev), _stream(dev))
     return Routing(ids, weights, row_token, row_slot, token_row, first, rows)
 
 
-def route_backward(logits, ids, weights, dweights, renormalize=True):
-    """The gradient of the logits from that of the weights (fp32)."""
+def route_backward(logits, ids, weights, dweights, renormalize=True, scoring="softmax",
+                   scale=1.0):
+    """The gradient of the logits from that of the weights (fp32).  The bias and
+    the groups have had their say in ids and enter no further."""
     _untracked(logits, weights, dweights)
     if logits.dim() != 2:
         raise ValueError("logits: [tokens, experts] expected")
@@ -286,10 +327,16 @@ def route_backward(logits, ids, weights, dweights, renormalize=True):
     for t, what in ((weights, "weights"), (dweights, "dweights")):
         if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != T * k:
             raise ValueError(f"{what}: contiguous fp32[{T}, {k}] expected")
+    desc = _route_desc(E, k, bool(renormalize), 0, scoring, 1, 1, 1, float(scale))
     out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _run(dev, fo.fo_moe_route_backward, logits.data_ptr(), type_, T, E,
-         _row_stride(logits, "logits"), k, renormalize, ids.data_ptr(), weights.data_ptr(),
-         dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
+    if desc is None:
+        _run(dev, fo.fo_moe_route_backward, logits.data_ptr(), type_, T, E,
+             _row_stride(logits, "logits"), k, renormalize, ids.data_ptr(), weights.data_ptr(),
+             dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
+    else:
+        _run(dev, fo.fo_moe_route_scored_backward, desc, logits.data_ptr(), type_, T,
+             _row_stride(logits, "logits"), ids.data_ptr(), weights.data_ptr(),
+             dweights.data_ptr(), out.data_ptr(), E, _stream(dev))
     return out
 
 

@@ -698,6 +698,53 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
                                 const float* dweights, void* dlogits, int64_t dlogits_stride,
                                 void* cuda_stream);
 
+/* The balanced router.  Per token, with s_e = sigmoid(l_e) or softmax(l)_e:
+ *   choice values c_e = s_e + bias_e (bias decides the choice, not the weights);
+ *   with groups > 1, experts [g * experts / groups, (g + 1) * experts / groups)
+ *       are group g, its score is the sum of its group_top (1 or 2) largest c
+ *       (of fewer where fewer are left), and only the top_groups groups with the
+ *       largest scores may be chosen from, ties to the lowest group;
+ *   the top_k largest c, in descending order, ties to the lowest index;
+ *   weight = scale * s_e, or with renormalize scale * s_e / sum over the chosen.
+ * The choice is the one that 64-bit arithmetic on these formulas makes: where
+ * fp32 values are too near to each other to tell, they are computed again.
+ * Weights are computed in fp32.  A logit or a choice value of -inf bars the
+ * expert; slots without one, the row tables, -1 entries, workspace, status and
+ * alignment are fo_moe_route's.  A NaN choice value ranks above every number
+ * (several: by index), and a weight that a NaN enters is NaN. */
+typedef enum { FO_SCORE_SOFTMAX = 0, FO_SCORE_SIGMOID = 1 } fo_score;
+typedef struct {
+  int32_t experts, top_k;      /* as fo_moe_route's */
+  int32_t renormalize;
+  int32_t score;               /* fo_score */
+  int32_t groups;              /* 1 .. 32, divides experts */
+  int32_t top_groups;          /* 1 .. groups; top_k <= top_groups * experts / groups */
+  int32_t group_top;           /* 1 or 2 */
+  float scale;                 /* finite, > 0 */
+  int64_t capacity;            /* as fo_moe_route's */
+} fo_route_desc;
+
+/*  bias: device float[experts], or NULL. */
+fo_status fo_moe_route_scored(const fo_route_desc* desc, const void* logits, fo_type type,
+                              int64_t tokens, int64_t row_stride, const float* bias,
+                              int32_t* ids, float* weights, int32_t* row_token,
+                              int32_t* row_slot, int32_t* token_row, int32_t* expert_first,
+                              int32_t* expert_rows, void* workspace, int32_t* dev_status,
+                              void* cuda_stream);
+
+/* Gradient of the logits from that of the weights, for the choice in ids (which
+ * the bias and the groups made: they enter no further).  With dot = sum of w g
+ * over a token's slots, at a chosen expert
+ *   sigmoid: w (1 - s) (g - dot / scale) renormalized, else w (1 - s) g;
+ *   softmax: w (g - dot / scale) renormalized, else w g - s dot;
+ * elsewhere 0, or -s dot for softmax not renormalized.  Slots with id -1 take no
+ * part.  dlogits has the logits' type and is written whole. */
+fo_status fo_moe_route_scored_backward(const fo_route_desc* desc, const void* logits,
+                                       fo_type type, int64_t tokens, int64_t row_stride,
+                                       const int32_t* ids, const float* weights,
+                                       const float* dweights, void* dlogits,
+                                       int64_t dlogits_stride, void* cuda_stream);
+
 /* A whole expert layer for a few tokens (a generation step):
  *   ids, w = router (as fo_moe_route) of logits = x . router^T;
  *   y[t] = sum over slots i of w_i * W2[e_i] (act(G x_t) * (U x_t)),
@@ -735,6 +782,121 @@ fo_status fo_moe_few(const fo_moe_few_desc* desc, const void* x, int64_t x_strid
                      const void* router, const void* W1, const void* W1_scales, const void* W2,
                      const void* W2_scales, void* y, int64_t y_stride, void* workspace,
                      int32_t* dev_status, void* cuda_stream);
+
+/* ------------------------------------------------------------------------
+ * What stands around the expert layer's products in a model's block: the
+ * norms with the residual stream, the activation between the projections and
+ * its checkpoint, the weighted sum of a token's rows; each with its gradient.
+ * As above: no plan, nothing allocated, nothing synchronised, no workspace
+ * that keeps anything from one call for the next.
+ *
+ * Types are BF16 or F32.  Strides are in elements, of rows, at least the
+ * row's length; tensors are aligned to their element (rows that all lie on 16
+ * bytes, of a multiple of 8 columns, go fastest).  Outputs do not overlap
+ * inputs.  Sums, means and everything between loads and stores are fp32, each
+ * output is rounded once.  No result depends on the order in which CTAs run.
+ * ---------------------------------------------------------------------- */
+
+/* The weighted sum of a token's rows of the experts' outputs:
+ *   y[t] = sum over slots s of weights[t][s] * rows[token_row[t][s]],
+ * slots in order; a slot of -1 adds nothing, whatever its weight, and a token
+ * with none gets zeros.  Rows that no slot names are not read.
+ *  rows: device, type, [table_rows][hidden]; token_row: device
+ *      int32[tokens * top_k], as fo_moe_route makes it (an entry >= table_rows
+ *      adds nothing and sets *dev_status to FO_ERR_ARG); weights: device
+ *      float[tokens * top_k], or NULL for ones.  top_k 1 .. 32.
+ *  y: device, y_type, [tokens][hidden]. */
+fo_status fo_moe_combine(const void* rows, fo_type type, int64_t table_rows, int64_t hidden,
+                         int64_t row_stride, const int32_t* token_row, const float* weights,
+                         int64_t tokens, int32_t top_k, void* y, fo_type y_type,
+                         int64_t y_stride, int32_t* dev_status, void* cuda_stream);
+
+/* Its gradients: drows[r] = weights[t][s] * dy[t] for the row of (t, s), zeros
+ * for rows that hold no token; dweights[t][s] = <dy[t], rows[r]>, 0 for a slot
+ * without a row.
+ *  row_token: device int32[table_rows], as the routing made it with token_row
+ *      (negative: no token).  A slot whose row does not name its token there is
+ *      left out and sets *dev_status to FO_ERR_ARG; a row that names a token
+ *      none of whose slots names it back keeps what drows holds.  Two slots of
+ *      one token with the same row: that row gets the last one's.
+ *  dweights: NULL to leave them out (rows may then be NULL). */
+fo_status fo_moe_combine_backward(const void* dy, fo_type dy_type, int64_t dy_stride,
+                                  const void* rows, fo_type type, int64_t table_rows,
+                                  int64_t hidden, int64_t row_stride, const int32_t* token_row,
+                                  const int32_t* row_token, const float* weights,
+                                  int64_t tokens, int32_t top_k, void* drows,
+                                  int64_t drows_stride, float* dweights, int32_t* dev_status,
+                                  void* cuda_stream);
+
+/* Bytes of the 8-bit checkpoint of `rows` rows of 2 * inter values.  With
+ * padded = inter rounded up to 32, codes are int8 [rows][2][padded] (gate
+ * half, then the other) and scales bytes [rows][2][padded / 32].  A block of
+ * 32 values has the step 2^(scale - 127) (255: NaN, it held an infinity or a
+ * NaN): 2^(floor(log2 a) - 6) for its largest magnitude a, at least 2^-127;
+ * codes are the nearest integers to value / step, ties to even, at most 127
+ * in magnitude.  Codes past inter are 0. */
+fo_status fo_checkpoint_sizes(int64_t rows, int64_t inter, int64_t* code_bytes,
+                              int64_t* scale_bytes);
+
+/* h = act(g) * v for rows [g | v] of u (2 * inter columns); RELU keeps g when
+ * g > 0 (else 0), SILU is g / (1 + exp(-g)).  With codes and scales (both or
+ * neither NULL) u is also kept in 8 bits for the backward pass.
+ *  codes, scales: device, codes 16-byte aligned, of fo_checkpoint_sizes bytes. */
+fo_status fo_gated_act(const void* u, fo_type type, int64_t rows, int64_t inter,
+                       int64_t u_stride, fo_activation act, void* h, int64_t h_stride,
+                       void* codes, void* scales, void* cuda_stream);
+
+/* du = [dh * v * act'(g) | dh * act(g)] with g and v the values that the
+ * checkpoint stands for.  dh and du have one type.  RELU's derivative at 0 is 0. */
+fo_status fo_gated_act_backward(const void* dh, fo_type type, int64_t rows, int64_t inter,
+                                int64_t dh_stride, fo_activation act, const void* codes,
+                                const void* scales, void* du, int64_t du_stride,
+                                void* cuda_stream);
+
+/* RMS norm of a block's output, its gate and scale into the residual stream,
+ * and RMS norm of the stream for the next block.  Per token:
+ *   u = x * post_rstd * post_gain,  post_rstd = 1 / sqrt(mean x^2 + eps)
+ *       (u = x where post_gain is NULL);
+ *   sum = residual + scale * gate * u;
+ *   y = sum * pre_rstd * pre_gain,  pre_rstd = 1 / sqrt(mean sum^2 + eps)
+ *       (not written where pre_gain is NULL; of the unrounded sum).
+ * residual NULL: zeros; gate NULL: ones; sum NULL: not written.
+ *  x, y: type.  residual, sum: stream_type (F32 where type is F32).  gains
+ *      [hidden] and gate [gates][hidden]: param_type.  gates divides tokens,
+ *      and tokens / gates consecutive tokens share a row of the gate (1: one
+ *      row for all; tokens: a row each); ignored where gate is NULL.
+ *  post_rstd, pre_rstd: device float[tokens], written where their gain is
+ *      given (the backward pass reads them). */
+typedef struct {
+  int64_t tokens, hidden;
+  int32_t type, stream_type, param_type;    /* fo_type */
+  int64_t gates;
+  float scale;
+  float eps;                                /* >= 0 */
+} fo_norm_desc;
+
+fo_status fo_block_norm(const fo_norm_desc* desc, const void* x, int64_t x_stride,
+                        const void* residual, int64_t residual_stride, const void* post_gain,
+                        const void* gate, int64_t gate_stride, const void* pre_gain, void* sum,
+                        int64_t sum_stride, void* y, int64_t y_stride, float* post_rstd,
+                        float* pre_rstd, void* cuda_stream);
+
+/* Its gradients, from those of sum (dsum, NULL: zeros) and of y (dy, NULL
+ * where pre_gain is): dx (type), dresidual (stream_type; NULL: not written),
+ * and for each parameter that is given its own in param_type, dpost and dpre
+ * [hidden], dgate [gates][hidden], summed over the tokens that share it.
+ *  post_rstd, pre_rstd: as the forward call wrote them.
+ *  workspace: device, 16-byte aligned, fo_block_norm_workspace bytes, of any
+ *      content; calls that overlap in time need one each. */
+fo_status fo_block_norm_workspace(const fo_norm_desc* desc, int64_t* bytes);
+fo_status fo_block_norm_backward(const fo_norm_desc* desc, const void* x, int64_t x_stride,
+                                 const void* residual, int64_t residual_stride,
+                                 const void* post_gain, const void* gate, int64_t gate_stride,
+                                 const void* pre_gain, const float* post_rstd,
+                                 const float* pre_rstd, const void* dsum, int64_t dsum_stride,
+                                 const void* dy, int64_t dy_stride, void* dx, int64_t dx_stride,
+                                 void* dresidual, int64_t dresidual_stride, void* dpost,
+                                 void* dgate, void* dpre, void* workspace, void* cuda_stream);
 
 const char* fo_status_string(fo_status status);
 

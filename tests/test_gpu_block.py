@@ -1,0 +1,496 @@
+"""The block's operators on the GPU against the 64-bit oracle.
+
+Tolerances, all derived before the first run (e = 2^-24; an output's own rounding
+is at most half a step, eps / 2 of its type relative to the value):
+ - the weighted sum: a rounding per slot, top_k e of the sum of magnitudes; its
+   weights' gradients: a lane adds at most H / 32 + 1 products in a row, then 5 +
+   8 sums, so (H / 32 + 16) e of the sum of magnitudes;
+ - the activation: expf is within 2 ulp (4 e) and s = 1 / (1 + x) has two
+   roundings more; h another two: 8 e relative.  1 + g (1 - s) may cancel, so
+   its gradient is off by 16 e of dh v s (1 + |g|).  Products whose value lies
+   below the normal numbers may be zeros: 2^-120 absolute;
+ - checkpoint codes and scales are exact;
+ - norms: a thread's squares are at most H / 256 + 8, then 5 + 32 sums: below 64 e
+   for H below 4096 and 96 e here throughout; halved by the root, and with the
+   products 64 e of the magnitudes each value is made of;
+ - gradients of the norms: 256 e of the magnitudes (three sums, each as above, of
+   magnitudes, and products of them); the parameters' (tokens + 256) e of theirs.
+"""
+import numpy as np
+import pytest
+import torch
+
+from communication_overlap_gb300 import fo
+from oracle import block as oracle
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from communication_overlap_gb300 import block, moe
+
+BF16, F32 = torch.bfloat16, torch.float32
+E = 2.0 ** -24
+
+
+def host(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def normal(rng, shape, dtype, scale=1.0):
+    return torch.from_numpy(rng.standard_normal(shape) * scale).to(dtype).cuda()
+
+
+def strided(t, pad, offset=0):
+    """The same matrix with `pad` extra elements per row, starting `offset`
+    elements into its memory."""
+    R, C = t.shape
+    buf = torch.full((R * (C + pad) + offset,), float("nan"), dtype=t.dtype, device=t.device)
+    v = buf[offset:].view(R, C + pad)[:, :C]
+    v.copy_(t)
+    return v
+
+
+def near(got, want, bound, dtype):
+    """|got - want| within bound and the rounding of a value that far off."""
+    got = host(got)
+    bound = bound + half_step(dtype) * (np.abs(want) + bound) + 2.0 ** -120
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
+
+
+# ------------------------------------------------------------------ the weighted sum
+
+def routing(rng, T, n, k, empty=0.1):
+    """token_row and row_token: every row at most once, some slots without one."""
+    rows = rng.permutation(n)[:T * k]
+    rows = np.concatenate([rows, np.full(T * k - len(rows), -1)])
+    token_row = np.where(rng.random((T, k)) < empty, -1, rng.permutation(rows).reshape(T, k))
+    row_token = np.full(n, -1)
+    for t, s in np.argwhere(token_row >= 0):
+        row_token[token_row[t, s]] = t
+    dev = lambda a: torch.from_numpy(a).int().cuda()
+    return token_row, dev(token_row), dev(row_token)
+
+
+COMBINE = [(1, 1, 1, 1), (3, 8, 8, 2), (5, 33, 40, 3), (7, 256, 7, 1), (40, 2048, 90, 2),
+           (9, 2056, 80, 9), (6, 4101, 20, 3), (130, 64, 1100, 8), (4, 136, 200, 32), (3, 520, 0, 2)]
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("T, H, n, k", COMBINE)
+def test_combine(T, H, n, k, types):
+    rng = np.random.default_rng(T * H + k)
+    t, o = types
+    index, token_row, row_token = routing(rng, T, n, k)
+    rows, w = normal(rng, (n, H), t), normal(rng, (T, k), F32)
+    dy = normal(rng, (T, H), o)
+    r64 = host(rows).reshape(n, H)
+    rows[row_token < 0] = float("nan")          # nothing reads the rows without a token
+    for weights in (w, None):
+        w64 = host(weights)
+        y = block.combine(rows, token_row, weights, out_dtype=o)
+        mag = oracle.combine(np.abs(r64), index, None if w64 is None else np.abs(w64))
+        near(y, oracle.combine(r64, index, w64), k * E * mag, o)
+        drows, dw = block.combine_backward(dy, rows, token_row, row_token, weights)
+        want, want_w = oracle.combine_backward(host(dy), r64, index, w64)
+        near(drows, want, E * np.abs(want), t)
+        if weights is None:
+            assert dw is None
+        else:
+            _, mag = oracle.combine_backward(np.abs(host(dy)), np.abs(r64), index, w64)
+            near(dw, want_w, (H / 32 + 16) * E * mag, F32)
+    assert moe.device_status() == fo.FO_OK
+
+
+@pytest.mark.parametrize("pad, offset", [(8, 8), (1, 0), (3, 1), (2, 2), (4, 4)])
+def test_combine_strides(pad, offset):
+    rng = np.random.default_rng(pad)
+    T, H, n, k = 9, 72, 30, 2
+    index, token_row, row_token = routing(rng, T, n, k)
+    rows, w, dy = normal(rng, (n, H), BF16), normal(rng, (T, k), F32), normal(rng, (T, H), BF16)
+    y = block.combine(rows, token_row, w)
+    drows, dw = block.combine_backward(dy, rows, token_row, row_token, w)
+    out = torch.full((T, H + pad), 7.0, dtype=BF16, device="cuda")
+    block.combine(strided(rows, pad, offset), token_row, w, out=out[:, :H])
+    assert torch.equal(out[:, :H], y) and (out[:, H:] == 7).all()
+    drows2, dw2 = block.combine_backward(strided(dy, pad, offset), strided(rows, pad, offset),
+                                         token_row, row_token, w)
+    assert torch.equal(drows2, drows)
+    # (other threads, another order of the sum)
+    near(dw2, host(dw), 2 * (H / 32 + 16) * E * (np.abs(host(dy)).max() * np.abs(host(rows)).max() * H),
+         F32)
+
+
+def test_combine_rows_out_of_range():
+    """Their slots add nothing, and the status says so."""
+    rows = torch.ones((4, 8), device="cuda")
+    index = torch.tensor([[0, 4], [1 << 30, 2]], dtype=torch.int32, device="cuda")
+    assert moe.device_status(clear=True) == fo.FO_OK
+    y = block.combine(rows, index)
+    assert torch.equal(y, torch.ones((2, 8), device="cuda"))
+    assert moe.device_status(clear=True) == fo.FO_ERR_ARG
+    # a row that holds another token is not written through this one's slot
+    row_token = torch.tensor([0, 0, 1, -1], dtype=torch.int32, device="cuda")
+    index = torch.tensor([[0, 1], [1, 2]], dtype=torch.int32, device="cuda")
+    w = torch.ones((2, 2), device="cuda")
+    drows, dw = block.combine_backward(torch.full((2, 8), 3.0, device="cuda"), rows, index,
+                                       row_token, w)
+    assert torch.equal(drows[:3], torch.full((3, 8), 3.0, device="cuda"))
+    assert not drows[3].any() and dw.tolist() == [[24, 24], [0, 24]]
+    assert moe.device_status(clear=True) == fo.FO_ERR_ARG
+
+
+def test_combine_infinite_weights_of_empty_slots():
+    index = torch.tensor([[-1, 0]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[float("inf"), 2.0]], device="cuda")
+    y = block.combine(torch.ones((1, 3), device="cuda"), index, w)
+    assert y.tolist() == [[2, 2, 2]]
+
+
+# ------------------------------------------------------------------ the activation
+
+def check_act(u, dh, kind):
+    I = u.shape[1] // 2
+    g, v = np.split(host(u), 2, axis=1)
+    h, kept = block.activate(u, kind, checkpoint=True)
+    want = oracle.act(g, kind) * v
+    near(h, want, 8 * E * np.abs(want), u.dtype)
+    assert torch.equal(block.activate(u, kind)[0], h)
+    halves = [oracle.checkpoint(x) for x in (g, v)]
+    codes = np.stack([c for c, _, _ in halves], 1)
+    scales = np.stack([s for _, s, _ in halves], 1)
+    assert np.array_equal(kept.scales.cpu().numpy(), scales.reshape(-1))
+    assert np.array_equal(kept.codes.cpu().numpy(), codes.reshape(-1))
+    values = np.concatenate([x for _, _, x in halves], 1)
+    assert np.array_equal(host(kept.values()), values)
+    g, v = np.split(values, 2, axis=1)
+    du = block.activate_backward(dh, kept)
+    d = host(dh)
+    s = 1 / (1 + np.exp(-g)) if kind == "silu" else 1
+    want = np.concatenate([d * v * oracle.act_slope(g, kind), d * oracle.act(g, kind)], 1)
+    bound = np.concatenate([np.abs(d * v) * s * (1 + np.abs(g)), np.abs(want[:, I:])], 1) * 16 * E
+    near(du, want, bound, dh.dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows, inter", [(1, 1), (2, 8), (3, 31), (5, 32), (4, 33), (7, 72),
+                                         (3, 256), (2, 257), (33, 96), (3, 2056), (2, 4100), (300, 40)])
+def test_act(rows, inter, dtype):
+    rng = np.random.default_rng(rows * 1000 + inter)
+    scale = 10.0 ** rng.uniform(-3, 1.5, (rows, 1))
+    u = normal(rng, (rows, 2 * inter), dtype) * torch.from_numpy(scale).to(dtype).cuda()
+    for kind in ("silu", "relu", "none"):
+        check_act(u, normal(rng, (rows, inter), dtype), kind)
+
+
+@pytest.mark.parametrize("pad, offset", [(8, 8), (1, 0), (3, 1), (2, 2)])
+def test_act_strides(pad, offset):
+    rng = np.random.default_rng(pad)
+    u, dh = normal(rng, (5, 144), BF16), normal(rng, (5, 72), BF16)
+    h, kept = block.activate(u, checkpoint=True)
+    h2, kept2 = block.activate(strided(u, pad, offset), checkpoint=True)
+    assert torch.equal(h, h2) and torch.equal(kept.codes, kept2.codes)
+    assert torch.equal(kept.scales, kept2.scales)
+    assert torch.equal(block.activate_backward(dh, kept),
+                       block.activate_backward(strided(dh, pad, offset), kept2))
+
+
+@pytest.mark.parametrize("inter", [64, 33])
+def test_act_extremes(inter):
+    """Zeros, the smallest and largest numbers, ties between codes, and blocks
+    with an infinity or a NaN, which stand for NaNs and leave the others alone."""
+    u = torch.zeros((8, 2 * inter), device="cuda")
+    u[1, :3] = torch.tensor([1e-45, -3e-45, 2e-44], device="cuda")
+    u[2, :4] = torch.tensor([3e38, -3.4e38, 1e38, 1.0], device="cuda")
+    u[3, :4] = torch.tensor([64.0, 0.5, 1.5, -2.5], device="cuda")      # a step of 1
+    u[4, :2] = torch.tensor([127.6, -127.9], device="cuda")
+    u[5, inter:inter + 2] = torch.tensor([2.0 ** -126, 2.0 ** -121], device="cuda")
+    u[6, 0] = float("inf")
+    u[7, inter + 1] = float("nan")
+    u[7, inter - 1] = 3.0
+    _, kept = block.activate(u, checkpoint=True)
+    halves = [oracle.checkpoint(x) for x in np.split(host(u), 2, axis=1)]
+    assert np.array_equal(kept.scales.cpu().numpy(),
+                          np.stack([s for _, s, _ in halves], 1).reshape(-1))
+    assert np.array_equal(kept.codes.cpu().numpy(),
+                          np.stack([c for c, _, _ in halves], 1).reshape(-1))
+    values = np.concatenate([v for _, _, v in halves], 1)
+    got = host(kept.values())
+    assert np.array_equal(got, values, equal_nan=True)
+    du = host(block.activate_backward(torch.ones((8, inter), device="cuda"), kept))
+    bad = np.isnan(values)
+    assert bad[6, :32].all() and bad[7, inter:inter + 32].all() and bad.sum() == 64
+    assert np.isnan(du[6, :32]).all() and np.isnan(du[7, :32]).all()
+    assert np.isfinite(du[:6]).all()
+
+
+def test_act_far_gates():
+    """silu of gates beyond expf's range: zeros and the gate itself."""
+    g = torch.tensor([[-1e4, -200.0, -100.0, 100.0, 200.0, 1e4]], device="cuda")
+    h, _ = block.activate(torch.cat((g, torch.full_like(g, 2.0)), 1))
+    assert h.tolist() == [[0, 0, 0, 200, 400, 2e4]]
+    for x in g[0].tolist():
+        u = torch.tensor([[x, 2.0]], device="cuda")
+        _, kept = block.activate(u, checkpoint=True)
+        du = block.activate_backward(torch.ones((1, 1), device="cuda"), kept)
+        v = host(kept.values())[0]
+        assert du.tolist() == [[v[1], v[0]] if x > 0 else [0, 0]]
+
+
+# ------------------------------------------------------------------ the norms
+
+def check_norm(x, residual, post, gate, scale, pre, eps, dstream, dy):
+    p = [host(t) for t in (x, residual, post, gate, pre)]
+    x64, r64, post64, gate64, pre64 = p
+    how = dict(post_gain=post, gate=gate, scale=scale, pre_gain=pre)
+    scale = float(np.float32(scale))
+    n = block.norm(x, residual, eps=eps, **how)
+    f = oracle.norm(x64, r64, post64, gate64, scale, pre64, float(np.float32(eps)))
+    T, H = x64.shape
+    mag = np.abs(f["q"] * f["u"]) + (0 if r64 is None else np.abs(r64))
+    if n.stream is x:
+        assert residual is None and post is None and gate is None and scale == 1
+    else:
+        near(n.stream, f["sum"], 64 * E * mag, n.stream.dtype)
+    # the second norm's inputs are off by 64 e of mag each
+    sn_mag = mag * f["r2"]
+    sn_mag = sn_mag + np.abs(f["sum"]) * f["r2"] * (sn_mag * np.abs(f["sum"]) * f["r2"]).mean(1, keepdims=True)
+    if pre is None:
+        assert n.y is None
+    else:
+        near(n.y, f["sum"] * f["r2"] * pre64, 128 * E * sn_mag * np.abs(pre64), x.dtype)
+    d = block.norm_backward(x, residual, n, dstream=dstream, dy=dy, **how)
+    d64 = np.zeros((T, H)) if dstream is None else host(dstream)
+    want = oracle.norm_backward(x64, r64, post64, gate64, scale, pre64, float(np.float32(eps)),
+                                None if dstream is None else d64, host(dy))
+    big = np.abs(d64)
+    if pre is not None:
+        e = np.abs(host(dy) * pre64)
+        big = big + f["r2"] * (e + sn_mag * (e * sn_mag).mean(1, keepdims=True))
+    if residual is None:
+        assert d.residual is None
+    else:
+        near(d.residual, want["residual"], 256 * E * big, residual.dtype)
+    w = np.abs(f["q"]) * big
+    if post is not None:
+        xn = np.abs(f["xn"])
+        near(d.post_gain, want["post_gain"], (T + 256) * E * (w * xn).sum(0), post.dtype)
+        w = w * np.abs(post64)
+        w = f["r1"] * (w + xn * (w * xn).mean(1, keepdims=True))
+    else:
+        assert d.post_gain is None
+    near(d.x, want["x"], 256 * E * w, x.dtype)
+    if gate is not None:
+        mag = (scale * np.abs(f["u"]) * big).reshape(gate64.size // H, -1, H).sum(1)
+        near(d.gate, want["gate"], (T + 256) * E * mag.reshape(gate64.shape), gate.dtype)
+    else:
+        assert d.gate is None
+    if pre is not None:
+        near(d.pre_gain, want["pre_gain"], (T + 256) * E * (np.abs(host(dy)) * sn_mag).sum(0),
+             pre.dtype)
+    return n, d
+
+
+def norm_case(rng, T, H, x_type, s_type, p_type, post, gates, pre, residual):
+    make = lambda there, shape, t: normal(rng, shape, t) if there else None
+    x = normal(rng, (T, H), x_type, 2.0)
+    s_type = s_type if residual else x_type
+    gate = None if gates is None else normal(rng, (H,) if gates == 0 else (gates, H), p_type)
+    return [x, make(residual, (T, H), s_type), make(post, (H,), p_type), gate, 0.75,
+            make(pre, (H,), p_type), 1e-5, make(True, (T, H), s_type), make(pre, (T, H), x_type)]
+
+
+NORM_SIZES = [(1, 1), (1, 8), (2, 33), (3, 64), (5, 264), (24, 72), (4, 1024), (6, 1032), (3, 1416),
+              (12, 2752), (2, 4096), (3, 4104), (2, 8192), (1, 8200), (3, 1001), (2, 9001)]
+TYPES = [(BF16, BF16, BF16), (BF16, F32, F32), (F32, F32, F32), (BF16, BF16, F32),
+         (F32, F32, BF16)]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("T, H", NORM_SIZES)
+def test_norm(T, H, types):
+    rng = np.random.default_rng(T * 10000 + H)
+    gates = [None, 0, 1, T] + [g for g in (2, 3, 4) if g < T and T % g == 0]
+    for i, (post, pre, residual) in enumerate(((True, True, True), (False, True, True),
+                                               (True, False, True), (True, True, False))):
+        check_norm(*norm_case(rng, T, H, *types, post, gates[(i + H) % len(gates)], pre, residual))
+
+
+@pytest.mark.parametrize("H", [64, 2752, 8192, 333])
+@pytest.mark.parametrize("T, gates", [(2500, 0), (2500, 4), (2500, 1250), (3000, 3000), (777, 7),
+                                      (1217, 1), (5000, 100)])
+def test_norm_many_tokens(T, gates, H):
+    """More tokens than workers, gates' rows that end inside a worker's range."""
+    if H > 3000 and T > 2500:
+        T, gates = 1500, 1500 if gates == 3000 else 30
+    rng = np.random.default_rng(T + gates)
+    check_norm(*norm_case(rng, T, H, BF16, F32, F32, True, gates, True, True))
+
+
+def test_norm_alone():
+    """The norm before a block: the stream is x itself."""
+    rng = np.random.default_rng(0)
+    x, pre = normal(rng, (3, 64), BF16), normal(rng, (64,), BF16)
+    n = block.norm(x, pre_gain=pre)
+    assert n.stream is x and n.post_rstd is None
+    check_norm(x, None, None, None, 1.0, pre, 1e-6, None, normal(rng, (3, 64), BF16))
+    # and its gradient with one of the stream besides
+    check_norm(x, None, None, None, 1.0, pre, 1e-6, normal(rng, (3, 64), BF16),
+               normal(rng, (3, 64), BF16))
+
+
+@pytest.mark.parametrize("H", [72, 9000])
+def test_norm_without_a_gradient_of_the_stream(H):
+    rng = np.random.default_rng(1)
+    case = norm_case(rng, 5, H, BF16, BF16, F32, True, 0, True, True)
+    case[7] = None
+    check_norm(*case)
+    # and of the stream alone
+    case = norm_case(rng, 5, H, BF16, BF16, F32, False, 5, False, True)
+    check_norm(*case)
+
+
+@pytest.mark.parametrize("pad, offset", [(8, 8), (1, 0), (3, 1), (2, 2)])
+def test_norm_strides(pad, offset):
+    rng = np.random.default_rng(pad)
+    x, res, post, gate, scale, pre, eps, ds, dy = norm_case(rng, 6, 72, BF16, BF16, BF16, True, 3,
+                                                            True, True)
+    wide = lambda t: strided(t, pad, offset)
+    check_norm(wide(x), wide(res), post, wide(gate), scale, pre, eps, wide(ds), wide(dy))
+
+
+def test_norm_rows_are_alone():
+    """Zeros, infinities and NaN stay in their rows; a row of zeros without eps is
+    0 / 0."""
+    rng = np.random.default_rng(2)
+    x, res, post, gate, scale, pre, _, ds, dy = norm_case(rng, 8, 136, F32, F32, F32, True, 0, True,
+                                                          True)
+    x[2], res[2] = 0, 0
+    clean = block.norm(x, res, post, gate, scale, pre, eps=1e-6)
+    assert not clean.y[2].any() and not clean.stream[2].any()
+    assert torch.isfinite(clean.y).all()
+    x[4, 3], x[5, 7], res[6, 1] = float("inf"), float("nan"), float("-inf")
+    n = block.norm(x, res, post, gate, scale, pre, eps=1e-6)
+    ok = [0, 1, 2, 3, 7]
+    assert torch.equal(n.y[ok], clean.y[ok]) and torch.equal(n.stream[ok], clean.stream[ok])
+    assert torch.isnan(n.y[5]).all() and torch.isnan(n.y[4]).any() and torch.isnan(n.y[6]).any()
+    d0 = block.norm_backward(x, res, clean, ds, dy, post, gate, scale, pre)
+    d = block.norm_backward(x, res, n, ds, dy, post, gate, scale, pre)
+    assert torch.equal(d.x[ok], d0.x[ok]) and torch.equal(d.residual[ok], d0.residual[ok])
+    assert torch.isnan(block.norm(torch.zeros((1, 8), device="cuda"), eps=0.0,
+                                  pre_gain=torch.ones(8, device="cuda")).y).all()
+
+
+def test_nothing():
+    """No tokens, no columns, no rows."""
+    z = lambda *s: torch.zeros(s, device="cuda")
+    n = block.norm(z(0, 16), z(0, 16), post_gain=z(16), gate=z(16), pre_gain=z(16))
+    assert n.y.shape == (0, 16)
+    d = block.norm_backward(z(0, 16), z(0, 16), n, z(0, 16), z(0, 16), z(16), z(16), 1.0, z(16))
+    assert not d.post_gain.any() and not d.gate.any() and not d.pre_gain.any()
+    assert block.norm(z(3, 0), z(3, 0), pre_gain=z(0)).y.shape == (3, 0)
+    h, kept = block.activate(z(0, 64), checkpoint=True)
+    assert block.activate_backward(h, kept).shape == (0, 64)
+    h, kept = block.activate(z(4, 0), checkpoint=True)
+    assert block.activate_backward(h, kept).shape == (4, 0)
+    none = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+    assert block.combine(z(0, 8), none).tolist() == [[0] * 8] * 2
+    drows, dw = block.combine_backward(z(2, 8), z(0, 8), none, none[:0, 0], z(2, 2))
+    assert drows.shape == (0, 8) and not dw.any()
+    empty = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    drows, dw = block.combine_backward(z(0, 8), z(3, 8) + 1, empty, none.view(-1)[:3].contiguous(),
+                                       z(0, 2))
+    assert not drows.any() and dw.shape == (0, 2)
+
+
+# ------------------------------------------------------------------ how they are called
+
+def all_calls(s):
+    """One pass of each operator over s, a dict of tensors."""
+    n = block.norm(s["x"], s["res"], s["post"], s["gate"], 0.5, s["pre"])
+    d = block.norm_backward(s["x"], s["res"], n, s["ds"], s["dy"], s["post"], s["gate"], 0.5,
+                            s["pre"])
+    h, kept = block.activate(s["u"], checkpoint=True)
+    du = block.activate_backward(s["dh"], kept)
+    y = block.combine(s["rows"], s["token_row"], s["w"])
+    drows, dw = block.combine_backward(s["dy2"], s["rows"], s["token_row"], s["row_token"], s["w"])
+    return [n.stream, n.y, d.x, d.residual, d.post_gain, d.gate, d.pre_gain, h, du, y, drows, dw]
+
+
+def some_inputs(seed, H=264, T=300):
+    rng = np.random.default_rng(seed)
+    x, res, post, gate, _, pre, _, ds, dy = norm_case(rng, T, H, BF16, BF16, BF16, True, 3, True, True)
+    _, token_row, row_token = routing(rng, 50, 120, 2)
+    return dict(x=x, res=res, post=post, gate=gate, pre=pre, ds=ds, dy=dy,
+                u=normal(rng, (70, 2 * H), BF16), dh=normal(rng, (70, H), BF16),
+                rows=normal(rng, (120, H), BF16), token_row=token_row, row_token=row_token,
+                w=normal(rng, (50, 2), F32), dy2=normal(rng, (50, H), BF16))
+
+
+@pytest.mark.parametrize("H", [264, 333, 4200])
+def test_repeated_and_captured(H):
+    """The same results in every run, from a graph, and on another stream beside
+    the first; a graph's replay reads what its inputs hold by then."""
+    a, b = some_inputs(0, H), some_inputs(1, H)
+    want_a, want_b = all_calls(a), all_calls(b)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(all_calls(a), want_a))
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(one):
+        got_a = all_calls(a)
+    with torch.cuda.stream(two):
+        got_b = all_calls(b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got_a, want_a))
+    assert all(torch.equal(p, q) for p, q in zip(got_b, want_b))
+    live = {k: v.clone() for k, v in a.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = all_calls(live)
+    for src, want in ((a, want_a), (b, want_b), (a, want_a)):
+        for k in live:
+            live[k].copy_(src[k])
+        graph.replay()
+        beside = all_calls(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+        assert all(torch.equal(p, q) for p, q in zip(beside, want_b))
+
+
+def test_refusals():
+    z = lambda *s, t=F32: torch.zeros(s, dtype=t, device="cuda")
+    bad = [
+        lambda: block.norm(z(2, 8), z(2, 8, t=BF16)),                   # fp32 into a bf16 stream
+        lambda: block.norm(z(2, 8), z(3, 8)),
+        lambda: block.norm(z(2, 8), post_gain=z(7)),
+        lambda: block.norm(z(2, 8), post_gain=z(8), pre_gain=z(8, t=BF16)),
+        lambda: block.norm(z(2, 8), gate=z(3, 8)),
+        lambda: block.norm(z(2, 8), gate=z(0, 8)),
+        lambda: block.norm(z(2, 8).half(), pre_gain=z(8)),
+        lambda: block.norm(z(2, 8).t().contiguous().t(), pre_gain=z(8)),
+        lambda: block.norm(z(1, 8).expand(2, 8), pre_gain=z(8)),
+        lambda: block.norm(z(2, 8).requires_grad_(), pre_gain=z(8)),
+        lambda: block.norm(z(2, 8), pre_gain=z(8).cpu()),
+        lambda: block.norm(z(2, 8), pre_gain=z(8), scale=float("nan")),
+        lambda: block.norm_backward(z(2, 8), None, block.norm(z(2, 8), pre_gain=z(8)), pre_gain=z(8)),
+        lambda: block.norm_backward(z(2, 8), None, block.norm(z(2, 8)), dy=z(2, 8), pre_gain=z(8)),
+        lambda: block.norm_backward(z(2, 8), None, block.norm(z(3, 8), pre_gain=z(8)), dy=z(2, 8),
+                                    pre_gain=z(8)),
+        lambda: block.activate(z(2, 7)),
+        lambda: block.activate(z(2, 8), act="tanh"),
+        lambda: block.activate(z(2, 8).double()),
+        lambda: block.activate_backward(z(2, 5), block.activate(z(2, 8), checkpoint=True)[1]),
+        lambda: block.combine(z(4, 8), z(2, 2)),
+        lambda: block.combine(z(4, 8), z(2, 2).int(), z(2, 3)),
+        lambda: block.combine(z(4, 8), z(2, 2).int(), out=z(2, 7)),
+        lambda: block.combine_backward(z(2, 7), z(4, 8), z(2, 2).int(), z(4).int()),
+        lambda: block.combine_backward(z(2, 8), z(4, 8), z(2, 2).int(), z(5).int()),
+    ]
+    for call in bad:
+        with pytest.raises((ValueError, fo.FoError)):
+            call()
