@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 
 #include "block_common.cuh"
 
@@ -53,16 +54,16 @@ __device__ __forceinline__ void load_param(const void* p, int64_t i, bool f32, f
   }
 }
 
-// Sums over the row's warps of N values per thread, the same on every thread:
-// by shuffles, then through shared memory in warp order.  Every thread of the
-// CTA calls it; buf: [2][N][32], the halves taken in turn, so that one barrier
-// per sum is enough.
+// Sums over the warps of a CTA of N values per thread, the same on every thread:
+// by shuffles, then through shared memory in warp order.  Every thread of the CTA
+// calls it; buf: [2][N][32], the halves taken in turn, so that one barrier per sum
+// is enough.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], int first_warp, int warps, float* buf,
-                                         int& turn) {
+__device__ __forceinline__ void cta_sums(float (&v)[N], float* buf, int& turn) {
+  const int warps = int(blockDim.x) >> 5;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;      // (the same for all of the CTA)
+  if (warps == 1) return;
   float* at = buf + turn * N * 32;
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) {
@@ -73,8 +74,105 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int first_warp, int warp
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float sum = 0.0f;
-    for (int w = 0; w < warps; ++w) sum += at[i * 32 + first_warp + w];
+    for (int w = 0; w < warps; ++w) sum += at[i * 32 + w];
     v[i] = sum;
+  }
+}
+
+// The threads of a row, one of several of a CTA: they meet at a barrier of their
+// own, so that a CTA's rows need not keep step.
+struct RowGroup {
+  int warps;      // of the row
+  int index;      // of the row in the CTA
+  int tid;        // of the row's threads
+
+  __device__ __forceinline__ static RowGroup of(int warps) {
+    const int index = int(threadIdx.x >> 5) / warps;
+    return {warps, index, int(threadIdx.x) - index * warps * 32};
+  }
+  // cta_sums over the row.  buf: [2][N][32] floats of zeros: a row's warps take
+  // slots from a multiple of four on, and are read by four.
+  template <int N>
+  __device__ __forceinline__ void sums(float (&v)[N], float* buf, int& turn) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (warps == 1) return;
+    float* at = buf + turn * N * 32 + index * ((warps + 3) & ~3);
+    turn ^= 1;
+    if ((tid & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[i * 32 + (tid >> 5)] = v[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float sum = 0.0f;
+      for (int w = 0; w < warps; w += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(at + i * 32 + w);
+        sum += (f.x + f.y) + (f.z + f.w);
+      }
+      v[i] = sum;
+    }
+  }
+};
+
+// Rows of a CTA where a row has `warps` warps and the CTA at most `most`.
+inline int rows_of_cta(int warps, int most) { return warps <= most ? most / warps : 1; }
+
+// A ring in shared memory that a thread fills for itself, rows ahead of their use:
+// no other thread reads its pieces, so no barrier guards them.  Piece i of stage s
+// lies at (s * pieces + i) * threads + thread, 16 bytes each.
+struct OwnRing {
+  uint32_t base;        // of this thread's first piece
+  uint32_t step;        // bytes from one piece to the next
+
+  __device__ __forceinline__ OwnRing(const void* smem)
+      : base(smem_u32(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
+  __device__ __forceinline__ uint32_t at(int piece) const { return base + uint32_t(piece) * step; }
+  // eight elements into the ring from piece `piece` on
+  template <typename T>
+  __device__ __forceinline__ void fetch(int piece, const T* src) const {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(piece + i)),
+                   "l"(reinterpret_cast<const uint4*>(src) + i)
+                   : "memory");
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(int piece, float (&v)[8]) const {
+    Pack8<T> p;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(p.w[i].x), "=r"(p.w[i].y), "=r"(p.w[i].z), "=r"(p.w[i].w)
+                   : "r"(at(piece + i))
+                   : "memory");
+    p.get(v);
+  }
+  __device__ __forceinline__ static void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  template <int N>      // all but the last N groups have arrived
+  __device__ __forceinline__ static void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  }
+};
+
+// scale gate post of eight columns (factors that are not given left out).
+__device__ __forceinline__ void load_factor(const NormArgs& a, int col, int64_t gate_row,
+                                            float (&w)[8]) {
+  float p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = a.scale;
+  if (a.gate != nullptr) {
+    load_param<8>(a.gate, gate_row + col, a.params_f32, p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= p[i];
+  }
+  if (a.post != nullptr) {
+    load_param<8>(a.post, col, a.params_f32, p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= p[i];
   }
 }
 
@@ -90,6 +188,31 @@ inline bool norm_rows_on_16(const NormArgs& a, fo_type type, fo_type stream_type
          norm_on_16(a.residual, a.residual_stride, s) && norm_on_16(a.gate, a.gate_stride, p) &&
          norm_on_16(a.post, 0, p) && norm_on_16(a.pre, 0, p) &&
          norm_on_16(a.sum, a.sum_stride, s) && norm_on_16(a.y, a.y_stride, x);
+}
+
+// The current device's SMs.
+inline fo_status sm_count(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FO_ERR_CUDA;
+  return FO_OK;
+}
+
+// Lets a kernel take up to kNormSmem bytes of dynamic shared memory, once per
+// kernel and device (not a launch's own size: another thread's launch may follow).
+constexpr int kNormSmem = 220 * 1024;
+template <auto K>
+fo_status allow_smem() {
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
+  const int slot = dev < 64 ? dev : 63;
+  std::call_once(once[slot], [&] {
+    err[slot] = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+  });
+  return err[slot] == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
 }  // namespace fo

@@ -25,7 +25,7 @@ namespace fo {
 
 namespace {
 
-constexpr int64_t kWorkers = 2048;      // the most
+constexpr int kMaxSms = 192;      // that take part
 
 struct BackShape {
   int32_t workers, per_worker;
@@ -132,22 +132,17 @@ __device__ __forceinline__ void means_of(const float (&sum)[3], float r2, int hi
   m1 = (sum[1] - r2 * m2 * sum[2]) / float(hidden);
 }
 
-// The gate's sums of W columns, where a token is the last of its gate's row or of
-// the worker's.
+// A worker's sums for W columns of a gate's row, which token t is the last of here.
 template <int W>
-__device__ __forceinline__ void flush_gate(const NormBackArgs& a, const BackShape& n, int64_t t,
-                                           int64_t t1, int64_t worker, int col,
-                                           float (&dgate)[W]) {
+__device__ __forceinline__ void store_gate(const NormBackArgs& a, const BackShape& n, int64_t t,
+                                           int64_t worker, int col, const float (&dgate)[W]) {
   const NormArgs& f = a.f;
-  if (f.gate == nullptr || (t + 1 != t1 && (t + 1) % f.gate_rows != 0)) return;
   if (f.gate_rows > 1)
     store_piece<W>(n.gate_part + (worker + t / f.gate_rows) * f.hidden + col, dgate);
   else if (f.params_f32)
     store_piece<W>(static_cast<float*>(a.dgate) + t * f.hidden + col, dgate);
   else
     store_piece<W>(static_cast<uint16_t*>(a.dgate) + t * f.hidden + col, dgate);
-#pragma unroll
-  for (int i = 0; i < W; ++i) dgate[i] = 0.0f;
 }
 
 template <int W>
@@ -159,43 +154,129 @@ __device__ __forceinline__ void store_parts(const NormBackArgs& a, const BackSha
   if (f.post != nullptr) store_piece<W>(n.post_part + worker * f.hidden + col, dpost);
 }
 
-// A worker per row of threads, eight columns per thread; several to a CTA where a
-// row has up to four warps.
-template <typename A, typename S>
+// Rows of up to 4096 columns, eight per thread; a worker per row of threads, several
+// to a CTA where a row has few warps.  The parameters' product w = scale gate post
+// and pre stay in registers and DEPTH rows are under way in the ring.  Of the
+// parameters' sums two are kept: of dy sn, and G of xn D over tokens with the
+// same gate, since dgate = scale post G and dpost = scale gate G.
+template <typename A, typename S, int DEPTH>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a,
                                                             const BackShape n, int warps) {
-  __shared__ float buf[2 * 3 * 32];
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float buf[2 * 3 * 32];
+  constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of a row's eight columns
+  constexpr int kPieces = 2 * (kA + kS);                    // x, dy, residual, dsum
+  for (int i = threadIdx.x; i < 192; i += blockDim.x) buf[i] = 0.0f;
+  __syncthreads();
   int turn = 0;
   const NormArgs& f = a.f;
-  const int row = int(threadIdx.x >> 5) / warps;
-  const int col = (int(threadIdx.x) - row * warps * 32) * 8;
-  const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + row;
-  const int64_t t0 = worker * n.per_worker;
-  const int64_t t1 = min(t0 + n.per_worker, int64_t(f.tokens));
-  float dpre[8], dpost[8], dgate[8];
+  const RowGroup g = RowGroup::of(warps);
+  const OwnRing ring(smem);
+  const int col = g.tid * 8;
+  const bool has = col < f.hidden;
+  const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + g.index;
+  const int t0 = int(min(worker * n.per_worker, int64_t(f.tokens)));
+  const int t1 = min(t0 + n.per_worker, f.tokens);
+  const float inv = 1.0f / float(f.hidden);
+  const auto fetch = [&](int t, int stage) {
+    if (has && t < t1) {
+      const int at = stage * kPieces;
+      ring.fetch(at, static_cast<const A*>(f.x) + t * f.x_stride + col);
+      if (f.pre != nullptr)
+        ring.fetch(at + kA, static_cast<const A*>(a.dy) + t * a.dy_stride + col);
+      if (f.residual != nullptr)
+        ring.fetch(at + 2 * kA, static_cast<const S*>(f.residual) + t * f.residual_stride + col);
+      if (a.dsum != nullptr)
+        ring.fetch(at + 2 * kA + kS, static_cast<const S*>(a.dsum) + t * a.dsum_stride + col);
+    }
+    OwnRing::commit();
+  };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dpre[i] = dpost[i] = dgate[i] = 0.0f;
-  Columns<A, S, 8> next;
-  next.load(a, t0, col, t0 < t1 && col < f.hidden);
-  // (the same number of rounds for all of the CTA: they meet at the sums)
-  for (int k = 0; k < n.per_worker; ++k) {
-    const int64_t t = t0 + k;
-    const bool live = t < t1 && col < f.hidden;
-    const Columns<A, S, 8> c = next;
-    next.load(a, t + 1, col, t + 1 < t1 && col < f.hidden);
-    const float r1 = live && f.post ? f.post_rstd[t] : 1.0f;
-    const float r2 = live && f.pre ? f.pre_rstd[t] : 0.0f;
-    const int64_t gate_row = live && f.gate ? t / f.gate_rows * f.gate_stride : 0;
+  for (int i = 0; i < DEPTH; ++i) fetch(t0 + i, i);
+  float w[8], pre[8], dpre[8], dpost[8], sum_g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pre[i] = dpre[i] = dpost[i] = sum_g[i] = 0.0f;
+  if (has && f.pre != nullptr) load_param<8>(f.pre, col, f.params_f32, pre);
+  // the tokens from which on another row of the gate holds
+  int gate_row = -1, gate_end = t0;
+  int stage = 0;
+  float r1 = f.post && t0 < t1 ? f.post_rstd[t0] : 1.0f;
+  float r2 = f.pre && t0 < t1 ? f.pre_rstd[t0] : 0.0f;
+  for (int t = t0; t < t1; ++t) {
+    if (t >= gate_end) {
+      gate_row = f.gate ? int(uint32_t(t) / uint32_t(f.gate_rows)) : 0;
+      gate_end = f.gate ? int(min(int64_t(gate_row + 1) * f.gate_rows, int64_t(t1))) : t1;
+      if (has) load_factor(f, col, gate_row * f.gate_stride, w);
+    }
+    OwnRing::wait<DEPTH - 1>();
+    float xn[8], sn[8], dy[8], d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xn[i] = sn[i] = dy[i] = d[i] = 0.0f;
+    if (has) {
+      const int at = stage * kPieces;
+      ring.get<A>(at, xn);
+      if (f.pre != nullptr) ring.get<A>(at + kA, dy);
+      if (f.residual != nullptr) ring.get<S>(at + 2 * kA, sn);
+      if (a.dsum != nullptr) ring.get<S>(at + 2 * kA + kS, d);
+    }
+    fetch(t + DEPTH, stage);
+    if (++stage == DEPTH) stage = 0;
+    const int next = t + 1 < t1 ? t + 1 : t;
+    const float next_r1 = f.post ? f.post_rstd[next] : 1.0f;
+    const float next_r2 = f.pre ? f.pre_rstd[next] : 0.0f;
     float sum[3] = {0.0f, 0.0f, 0.0f};
-    if (live) c.sums(a, col, gate_row, r1, r2, sum);
-    row_sums<3>(sum, row * warps, warps, buf, turn);
-    if (!live) continue;
-    float m1, m2;
-    means_of(sum, r2, f.hidden, m1, m2);
-    c.gradients(a, t, col, gate_row, r1, r2, m1, m2, dpre, dpost, dgate);
-    flush_gate<8>(a, n, t, t1, worker, col, dgate);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      xn[i] *= r1;
+      const float z = w[i] * xn[i], e = dy[i] * pre[i];
+      sn[i] = (sn[i] + z) * r2;
+      d[i] = fmaf(r2, e, d[i]);
+      sum[0] = fmaf(e, sn[i], sum[0]);
+      sum[1] = fmaf(z, d[i], sum[1]);
+      sum[2] = fmaf(z, sn[i], sum[2]);
+    }
+    g.sums<3>(sum, buf, turn);
+    const float k = r2 * (sum[0] * inv);
+    const float m1 = (sum[1] - k * sum[2]) * inv;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d[i] = fmaf(-k, sn[i], d[i]);
+      dpre[i] = fmaf(dy[i], sn[i], dpre[i]);
+      sum_g[i] = fmaf(xn[i], d[i], sum_g[i]);
+      o[i] = w[i] * d[i];
+      if (f.post != nullptr) o[i] = r1 * fmaf(-m1, xn[i], o[i]);
+    }
+    r1 = next_r1, r2 = next_r2;
+    if (!has) continue;
+    if (a.dresidual != nullptr)
+      store_piece<8>(static_cast<S*>(a.dresidual) + t * a.dresidual_stride + col, d);
+    store_piece<8>(static_cast<A*>(a.dx) + t * a.dx_stride + col, o);
+    if (t + 1 < gate_end) continue;
+    // the last token with this gate here
+    float p[8], q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = q[i] = f.scale;
+    if (f.post != nullptr) {
+      load_param<8>(f.post, col, f.params_f32, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] *= f.scale;
+    }
+    if (f.gate != nullptr) {
+      load_param<8>(f.gate, gate_row * f.gate_stride + col, f.params_f32, q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] *= f.scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] *= sum_g[i];
+      dpost[i] = fmaf(q[i], sum_g[i], dpost[i]);
+      sum_g[i] = 0.0f;
+    }
+    if (f.gate != nullptr) store_gate<8>(a, n, t, worker, col, p);
   }
-  if (t0 < t1 && col < f.hidden) store_parts<8>(a, n, worker, col, dpre, dpost);
+  OwnRing::wait<0>();
+  if (t0 < t1 && has) store_parts<8>(a, n, worker, col, dpre, dpost);
 }
 
 // Any rows, first: the two means of each token, by a CTA.
@@ -214,7 +295,7 @@ __global__ void __launch_bounds__(512) norm_means_kernel(const NormBackArgs a, c
     c.load(a, t, col, true);
     c.sums(a, col, gate_row, r1, r2, sum);
   }
-  row_sums<3>(sum, 0, int(blockDim.x) >> 5, buf, turn);
+  cta_sums<3>(sum, buf, turn);
   float m1, m2;
   means_of(sum, r2, f.hidden, m1, m2);
   if (threadIdx.x == 0) n.means[t] = make_float2(m1, m2);
@@ -242,7 +323,11 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackArgs a,
     c.gradients(a, t, col, f.gate ? t / f.gate_rows * f.gate_stride : 0,
                 f.post ? f.post_rstd[t] : 1.0f, f.pre ? f.pre_rstd[t] : 0.0f, m.x, m.y, dpre,
                 dpost, dgate);
-    flush_gate<W>(a, n, t, t1, worker, col, dgate);
+    if (f.gate && (t + 1 == t1 || (t + 1) % f.gate_rows == 0)) {
+      store_gate<W>(a, n, t, worker, col, dgate);
+#pragma unroll
+      for (int i = 0; i < W; ++i) dgate[i] = 0.0f;
+    }
   }
   store_parts<W>(a, n, worker, col, dpre, dpost);
 }
@@ -289,24 +374,39 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormBackArgs a, co
 
 // Workers of at least as many as are asked for, where there are the tokens.
 void share_out(BackShape* n, int64_t tokens, int64_t most) {
-  if (most > kWorkers) most = kWorkers;
   n->per_worker = int32_t((tokens + most - 1) / most);
   n->workers = int32_t((tokens + n->per_worker - 1) / n->per_worker);
 }
 
+// The most workers: a row of threads each, or the CTAs along the tokens.
+int64_t whole_workers(int64_t hidden, int sms) {
+  return int64_t(sms) * rows_of_cta(int((hidden + 255) / 256), 16);
+}
+int64_t column_workers(int64_t hidden, int width, int sms) {
+  const int64_t pieces = (hidden + 256 * width - 1) / (256 * width);
+  return (int64_t(sms) * 4 + pieces - 1) / pieces;
+}
+
+template <typename A, typename S, int DEPTH>
+fo_status launch_ring(const NormBackArgs& a, const BackShape& n, int warps, int rows,
+                      int row_bytes, cudaStream_t st) {
+  const fo_status q = allow_smem<norm_backward_kernel<A, S, DEPTH>>();
+  if (q != FO_OK) return q;
+  norm_backward_kernel<A, S, DEPTH><<<unsigned((n.workers + rows - 1) / rows), rows * warps * 32,
+                                      DEPTH * row_bytes, st>>>(a, n, warps);
+  return FO_OK;
+}
+
 template <typename A, typename S>
-void launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec, int sms,
-            cudaStream_t st) {
+fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec, int sms,
+                 cudaStream_t st) {
   const NormArgs& f = a.f;
   const int64_t H = f.hidden;
   const bool whole = vec && H <= 4096;
-  const int warps = int((H + 255) / 256), rows = warps <= 4 ? 8 / warps : 1;
-  const int width = vec ? 8 : 1;
-  const int64_t pieces = (H + 256 * width - 1) / (256 * width);
   if (whole) {
-    share_out(n, f.tokens, int64_t(sms) * rows);
+    share_out(n, f.tokens, whole_workers(H, sms));
   } else {
-    share_out(n, f.tokens, (int64_t(sms) * 4 + pieces - 1) / pieces);
+    share_out(n, f.tokens, column_workers(H, vec ? 8 : 1, sms));
     n->means = reinterpret_cast<float2*>(workspace);
     workspace += (2 * int64_t(f.tokens) + 3) / 4 * 4;
   }
@@ -314,27 +414,31 @@ void launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec, int
   n->post_part = n->pre_part + n->workers * H;
   n->gate_part = n->post_part + n->workers * H;
   if (whole) {
-    norm_backward_kernel<A, S><<<unsigned((n->workers + rows - 1) / rows), rows * warps * 32, 0, st>>>(
-        a, *n, warps);
-    return;
+    const int warps = int((H + 255) / 256), rows = rows_of_cta(warps, 16);
+    const int row = rows * warps * 32 * 16 * int(sizeof(A) + sizeof(S));
+    return 4 * row <= kNormSmem ? launch_ring<A, S, 4>(a, *n, warps, rows, row, st)
+                                : launch_ring<A, S, 2>(a, *n, warps, rows, row, st);
   }
-  const unsigned grid = unsigned(n->workers * pieces);
   if (vec) {
+    const int pieces = int((H + 2047) / 2048);
     norm_means_kernel<A, S, 8><<<unsigned(f.tokens), 512, 0, st>>>(a, *n);
-    norm_columns_kernel<A, S, 8><<<grid, 256, 0, st>>>(a, *n, int(pieces));
+    norm_columns_kernel<A, S, 8><<<unsigned(n->workers * pieces), 256, 0, st>>>(a, *n, pieces);
   } else {
-    const int w = int((H + 31) / 32);
+    const int pieces = int((H + 255) / 256), w = int((H + 31) / 32);
     norm_means_kernel<A, S, 1><<<unsigned(f.tokens), (w < 16 ? w : 16) * 32, 0, st>>>(a, *n);
-    norm_columns_kernel<A, S, 1><<<grid, 256, 0, st>>>(a, *n, int(pieces));
+    norm_columns_kernel<A, S, 1><<<unsigned(n->workers * pieces), 256, 0, st>>>(a, *n, pieces);
   }
+  return FO_OK;
 }
 
 }  // namespace
 
-// Both means of every token, and the workers' parts (a multiple of 16 bytes each
-// where the rows are).
+// Both means of every token, and the workers' parts.
 int64_t block_norm_workspace_bytes(int64_t tokens, int64_t hidden, int64_t gates) {
-  const int64_t workers = tokens < kWorkers ? tokens : kWorkers;
+  int64_t workers = column_workers(hidden, 8, kMaxSms);
+  if (hidden <= 4096 && workers < whole_workers(hidden, kMaxSms))
+    workers = whole_workers(hidden, kMaxSms);
+  if (workers > tokens) workers = tokens;
   const int64_t gate_parts = gates > 0 && gates < tokens ? workers + gates : 0;
   return 8 * tokens + 16 + 4 * hidden * (2 * workers + gate_parts);
 }
@@ -347,10 +451,10 @@ fo_status launch_block_norm_backward(const NormBackArgs& a, fo_type type, fo_typ
                    norm_on_16(a.dy, a.dy_stride, sa) && norm_on_16(a.dx, a.dx_stride, sa) &&
                    norm_on_16(a.dresidual, a.dresidual_stride, ss) &&
                    norm_on_16(a.dgate, f.hidden, sp);
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FO_ERR_CUDA;
+  int sms = 0;
+  fo_status q = sm_count(&sms);
+  if (q != FO_OK) return q;
+  if (sms > kMaxSms) sms = kMaxSms;
   // (a gate's row for every token is written by the kernel itself)
   const int64_t joined = f.gate && f.gate_rows != 1 ? gates : 0;
   const int64_t results = (f.pre != nullptr) + (f.post != nullptr) + joined;
@@ -361,12 +465,13 @@ fo_status launch_block_norm_backward(const NormBackArgs& a, fo_type type, fo_typ
   // (without tokens there are no parts, and the sums are zeros)
   if (f.tokens > 0) {
     if (type == FO_TYPE_F32)
-      launch<float, float>(a, &n, a.workspace, vec, sms, st);
+      q = launch<float, float>(a, &n, a.workspace, vec, sms, st);
     else if (stream_type == FO_TYPE_F32)
-      launch<uint16_t, float>(a, &n, a.workspace, vec, sms, st);
+      q = launch<uint16_t, float>(a, &n, a.workspace, vec, sms, st);
     else
-      launch<uint16_t, uint16_t>(a, &n, a.workspace, vec, sms, st);
+      q = launch<uint16_t, uint16_t>(a, &n, a.workspace, vec, sms, st);
   }
+  if (q != FO_OK) return q;
   if (cudaGetLastError() != cudaSuccess) return FO_ERR_CUDA;
   if (results > 0)
     norm_join_kernel<<<unsigned(results * columns), 256, 0, st>>>(a, n, int(columns));
