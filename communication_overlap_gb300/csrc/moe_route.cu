@@ -29,7 +29,6 @@
 #include <mutex>
 
 #include "moe_common.cuh"
-#include "moe_scores.cuh"
 
 namespace fo {
 
@@ -60,21 +59,19 @@ struct RouteKernelArgs {
   int32_t* counts;     // [grid][experts] pairs of each chunk per expert
   int32_t* status;
   int32_t chunk;       // tokens per CTA
-  ScoreArgs score;     // of the router with scores
 };
 
 // Shared memory: ids of the chunk where they fit (1056 tokens of top 32 over 1024
 // experts do, 160512 on 152 SMs; a larger chunk reads them back from the output),
 // per-warp counts (then starts) per expert, the chunk's start per expert.  (Ids last:
 // 28.8 us instead of 26.7 for 16384 tokens of 128 experts.)
-// With groups of experts, each warp's keys per expert.
-__host__ __device__ inline int64_t route_smem(int64_t kept, int experts, bool grouped) {
-  return 4 * (kept + int64_t(kRouteWarps + 1 + (grouped ? kRouteWarps : 0)) * experts);
+__host__ __device__ inline int64_t route_smem(int64_t kept, int experts) {
+  return 4 * (kept + int64_t(kRouteWarps + 1) * experts);
 }
 
 // KEPT: the chunk's ids stay in shared memory.  (Decided at run time, 100000 tokens
 // of 128 experts take 104 us, not 100.)
-template <int V, bool KEPT, bool SCORED>
+template <int V, bool KEPT>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKernelArgs a) {
   extern __shared__ int32_t sm[];
   const int E = a.experts, K = a.top_k;
@@ -123,13 +120,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKernelA
     }
     int id;
     float w;
-    if constexpr (SCORED) {
-      // (the groups' scratch lies behind the starts per expert)
-      warp_choose<V>(x, a.score, E, K, a.renormalize != 0,
-                     reinterpret_cast<uint32_t*>(start + E) + warp * E, id, w);
-    } else {
-      warp_top_k<V>(x, E, K, a.renormalize != 0, id, w);
-    }
+    warp_top_k<V>(x, E, K, a.renormalize != 0, id, w);
     if (lane < K) {
       ids[t * K + lane] = id;
       a.ids[(t0 + t) * K + lane] = id;
@@ -338,7 +329,7 @@ fo_status sm_count(int* sms) {
   return FO_OK;
 }
 
-template <int V, bool KEPT, bool SCORED>
+template <int V, bool KEPT>
 fo_status launch_as(const RouteKernelArgs& a, int grid, int smem, cudaStream_t st) {
   // the limit once, not each launch's size: that would be lowered between another
   // thread's setting and its launch, and 48 KB bound the static part's sum with it
@@ -349,7 +340,7 @@ fo_status launch_as(const RouteKernelArgs& a, int grid, int smem, cudaStream_t s
   const int slot = dev < 64 ? dev : 63;
   std::call_once(once[slot], [&] {
     err[slot] =
-        cudaFuncSetAttribute(route_kernel<V, KEPT, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(route_kernel<V, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kRouteSmemLimit);
   });
   if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
@@ -363,30 +354,18 @@ fo_status launch_as(const RouteKernelArgs& a, int grid, int smem, cudaStream_t s
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = grid > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, route_kernel<V, KEPT, SCORED>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, route_kernel<V, KEPT>, a) != cudaSuccess) {
     cudaGetLastError();
     return FO_ERR_CUDA;
   }
   return FO_OK;
 }
 
-template <int V, bool SCORED>
+template <int V>
 fo_status launch_v(const RouteKernelArgs& a, int grid, cudaStream_t st) {
-  const bool grouped = a.score.groups > 1;
-  const int64_t kept = route_smem(int64_t(a.chunk) * a.top_k, a.experts, grouped);
-  if (kept <= kRouteSmemLimit) return launch_as<V, true, SCORED>(a, grid, int(kept), st);
-  return launch_as<V, false, SCORED>(a, grid, int(route_smem(0, a.experts, grouped)), st);
-}
-
-template <bool SCORED>
-fo_status launch_by_experts(const RouteKernelArgs& a, int grid, cudaStream_t st) {
-  const int v = (a.experts + 31) / 32;
-  if (v <= 1) return launch_v<1, SCORED>(a, grid, st);
-  if (v <= 2) return launch_v<2, SCORED>(a, grid, st);
-  if (v <= 4) return launch_v<4, SCORED>(a, grid, st);
-  if (v <= 8) return launch_v<8, SCORED>(a, grid, st);
-  if (v <= 16) return launch_v<16, SCORED>(a, grid, st);
-  return launch_v<32, SCORED>(a, grid, st);
+  const int64_t kept = route_smem(int64_t(a.chunk) * a.top_k, a.experts);
+  if (kept <= kRouteSmemLimit) return launch_as<V, true>(a, grid, int(kept), st);
+  return launch_as<V, false>(a, grid, int(route_smem(0, a.experts)), st);
 }
 
 }  // namespace
@@ -396,31 +375,17 @@ fo_status launch_by_experts(const RouteKernelArgs& a, int grid, cudaStream_t st)
 constexpr int64_t kRouteMaxCtas = 1024;
 int64_t route_workspace_bytes(int experts) { return 256 + kRouteMaxCtas * 4 * int64_t(experts); }
 
-namespace {
-
-// The launch of either router; a.score says which scores.
-template <bool SCORED>
-fo_status launch_route(RouteKernelArgs& a, void* workspace, void* stream) {
-  int sms = 0;
-  const fo_status q = sm_count(&sms);
-  if (q != FO_OK) return q;
-  if (sms > kRouteMaxCtas) sms = int(kRouteMaxCtas);
-  a.barrier = static_cast<uint32_t*>(workspace);
-  a.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
-  const int64_t chunk = route_chunk(a.tokens, sms);
-  a.chunk = int32_t(chunk);
-  const int grid = a.tokens == 0 ? 1 : int((a.tokens + chunk - 1) / chunk);
-  return launch_by_experts<SCORED>(a, grid, static_cast<cudaStream_t>(stream));
-}
-
-}  // namespace
-
 fo_status launch_moe_route(const void* logits, fo_type type, int64_t tokens, int32_t experts,
                            int64_t row_stride, int32_t top_k, bool renormalize,
                            int64_t capacity, int64_t table_rows, int32_t* ids, float* weights,
                            int32_t* row_token, int32_t* row_slot, int32_t* token_row,
                            int32_t* expert_first, int32_t* expert_rows, void* workspace,
                            int32_t* dev_status, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  const fo_status q = sm_count(&sms);
+  if (q != FO_OK) return q;
+  if (sms > kRouteMaxCtas) sms = int(kRouteMaxCtas);
   RouteKernelArgs a{};
   a.logits = logits;
   a.stride = row_stride;
@@ -438,41 +403,19 @@ fo_status launch_moe_route(const void* logits, fo_type type, int64_t tokens, int
   a.token_row = token_row;
   a.expert_first = expert_first;
   a.expert_rows = expert_rows;
+  a.barrier = static_cast<uint32_t*>(workspace);
+  a.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
   a.status = dev_status;
-  return launch_route<false>(a, workspace, stream);
-}
-
-fo_status launch_moe_route_scored(const fo_route_desc& d, const void* logits, fo_type type,
-                                  int64_t tokens, int64_t row_stride, const float* bias,
-                                  int64_t table_rows, int32_t* ids, float* weights,
-                                  int32_t* row_token, int32_t* row_slot, int32_t* token_row,
-                                  int32_t* expert_first, int32_t* expert_rows, void* workspace,
-                                  int32_t* dev_status, void* stream) {
-  RouteKernelArgs a{};
-  a.logits = logits;
-  a.stride = row_stride;
-  a.bf16 = type == FO_TYPE_BF16;
-  a.tokens = int32_t(tokens);
-  a.experts = d.experts;
-  a.top_k = d.top_k;
-  a.renormalize = d.renormalize != 0;
-  a.capacity = d.capacity;
-  a.table_rows = table_rows;
-  a.ids = ids;
-  a.weights = weights;
-  a.row_token = row_token;
-  a.row_slot = row_slot;
-  a.token_row = token_row;
-  a.expert_first = expert_first;
-  a.expert_rows = expert_rows;
-  a.status = dev_status;
-  a.score.bias = bias;
-  a.score.sigmoid = d.score == FO_SCORE_SIGMOID;
-  a.score.groups = d.groups;
-  a.score.top_groups = d.top_groups;
-  a.score.group_top = d.group_top;
-  a.score.scale = d.scale;
-  return launch_route<true>(a, workspace, stream);
+  const int64_t chunk = route_chunk(tokens, sms);
+  a.chunk = int32_t(chunk);
+  const int grid = tokens == 0 ? 1 : int((tokens + chunk - 1) / chunk);
+  const int v = (experts + 31) / 32;
+  if (v <= 1) return launch_v<1>(a, grid, st);
+  if (v <= 2) return launch_v<2>(a, grid, st);
+  if (v <= 4) return launch_v<4>(a, grid, st);
+  if (v <= 8) return launch_v<8>(a, grid, st);
+  if (v <= 16) return launch_v<16>(a, grid, st);
+  return launch_v<32>(a, grid, st);
 }
 
 fo_status launch_moe_route_backward(const void* logits, fo_type type, int64_t tokens,
