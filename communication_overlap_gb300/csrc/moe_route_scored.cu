@@ -23,7 +23,7 @@ namespace fo {
 namespace {
 
 constexpr int kScoredSmemLimit = 200 * 1024;   // that a launch asks for
-constexpr int kScoredMaxCtas = 1024;           // whose counts the workspace has room for
+constexpr int kScoredMaxCtas = 256;            // whose counts the workspace has room for
 constexpr int kShareRows = 4096;               // of the tables, per CTA without a barrier
 
 struct ScoredArgs {
@@ -38,15 +38,16 @@ struct ScoredArgs {
   int32_t* expert_first;
   int32_t* expert_rows;
   uint32_t* barrier;   // [0] count, [1] leave
-  int32_t* counts;     // [grid][experts] pairs of each chunk per expert
+  void* counts;        // [grid][pitch] pairs of each chunk per expert, 16 bits each
+                       //   where a chunk has fewer tokens than that holds, else 32
   int32_t* status;
   int32_t chunk;       // tokens per CTA
   int32_t segments;    // of a chunk's pairs
+  int32_t pitch;       // experts, to a multiple of 8
   int32_t alone;       // every CTA has all tokens, and there is no barrier
 };
 
-// Threads of a CTA: as many as hold V logits, keys and biases each in registers.
-constexpr int scored_threads(int v) { return v <= 4 ? 1024 : 512; }
+constexpr int kScoredThreads = 512;            // 128 registers each
 
 __device__ __forceinline__ void clear_rows(int32_t* p, int64_t lo, int64_t hi, int32_t v) {
   if (((reinterpret_cast<uintptr_t>(p + lo)) & 15) == 0) {
@@ -60,7 +61,7 @@ __device__ __forceinline__ void clear_rows(int32_t* p, int64_t lo, int64_t hi, i
 
 // KEPT: the chunk's ids stay in shared memory, where they fit.
 template <int V, bool KEPT>
-__global__ void __launch_bounds__(scored_threads(V), 1) scored_kernel(const ScoredArgs a) {
+__global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredArgs a) {
   extern __shared__ int32_t sm[];
   const int E = a.score.experts, K = a.score.top_k;
   int32_t* cnt = KEPT ? sm + int64_t(a.chunk) * K : sm;   // [segments][E]
@@ -76,36 +77,46 @@ __global__ void __launch_bounds__(scored_threads(V), 1) scored_kernel(const Scor
   int32_t* ids = KEPT ? sm : a.ids + t0 * K;              // [chunk * K]
   // a segment's pairs, whole groups of 32
   const int per = (pairs + a.segments * 32 - 1) / (a.segments * 32) * 32;
-  // a token's logits are on their way while the one before it is chosen for, where a
-  // warp has registers for both
+  // a warp takes kTokens tokens at a time, and the next ones' logits are on their way
+  // meanwhile, where it has registers for that
   const LaneExperts<V> own(a.score);
+  constexpr int kTokens = V <= 8 ? 2 : 1;
   constexpr bool kAhead = V <= 8;
-  float ahead[kAhead ? V : 1];
-  if constexpr (kAhead) own.load(a.score, (t0 + warp) * a.score.stride, warp < n, ahead);
+  float ahead[kTokens][V];
+  const auto load = [&](int t) {
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j)
+      own.load(a.score, (t0 + t + j * warps) * a.score.stride, t + j * warps < n, ahead[j]);
+  };
+  if constexpr (kAhead) load(warp);
   for (int i = threadIdx.x; i < (a.segments + 2) * E; i += blockDim.x) cnt[i] = 0;
   // this CTA's share of the row tables starts empty
   const int64_t share = ((a.table_rows + gridDim.x - 1) / gridDim.x + 3) / 4 * 4;
   const int64_t lo = min(share * blockIdx.x, a.table_rows), hi = min(lo + share, a.table_rows);
   clear_rows(a.row_token, lo, hi, -1);
   clear_rows(a.row_slot, lo, hi, 0);
-  for (int t = warp; t < n; t += warps) {
-    const int64_t at = (t0 + t) * a.score.stride;
-    float x[V];
-    if constexpr (kAhead) {
+  for (int t = warp; t < n; t += kTokens * warps) {
+    int64_t at[kTokens];
+    float x[kTokens][V], w[kTokens];
+    int id[kTokens];
+    if constexpr (!kAhead) load(t);
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = ahead[i];
-      own.load(a.score, at + warps * a.score.stride, t + warps < n, ahead);
-    } else {
-      own.load(a.score, at, true, x);
+    for (int j = 0; j < kTokens; ++j) {
+      // (of a token past the last, the first is looked at once more where it must be)
+      at[j] = (t0 + (t + j * warps < n ? t + j * warps : t)) * a.score.stride;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = ahead[j][i];
     }
-    int id;
-    float w;
-    warp_choose<V>(a.score, own, at, x, id, w);
-    if (lane < K) {
-      ids[t * K + lane] = id;
+    if constexpr (kAhead) load(t + kTokens * warps);
+    warp_choose<V, kTokens>(a.score, own, at, x, id, w);
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      const int u = t + j * warps;
+      if (u >= n || lane >= K) continue;
+      ids[u * K + lane] = id[j];
       if (lead) {
-        a.ids[(t0 + t) * K + lane] = id;
-        a.weights[(t0 + t) * K + lane] = w;
+        a.ids[(t0 + u) * K + lane] = id[j];
+        a.weights[(t0 + u) * K + lane] = w[j];
       }
     }
   }
@@ -125,8 +136,10 @@ __global__ void __launch_bounds__(scored_threads(V), 1) scored_kernel(const Scor
     }
     if (a.alone)
       total[e] = sum;
+    else if (a.chunk <= 65535)
+      __stcg(static_cast<uint16_t*>(a.counts) + blockIdx.x * a.pitch + e, uint16_t(sum));
     else
-      __stcg(a.counts + int64_t(blockIdx.x) * E + e, sum);
+      __stcg(static_cast<int32_t*>(a.counts) + blockIdx.x * E + e, sum);
   }
   if (!a.alone) {
     __threadfence();
@@ -135,20 +148,52 @@ __global__ void __launch_bounds__(scored_threads(V), 1) scored_kernel(const Scor
     __syncthreads();
     if (threadIdx.x == 0) grid_barrier_leave(a.barrier + 1, a.barrier, 1, gridDim.x);
     if (!ok_s) return;
-    // earlier chunks' pairs per expert and the total; several threads per expert share
-    // out the chunks
-    const int parts = max(int(blockDim.x) / E, 1);
-    for (int i = threadIdx.x; i < E * parts; i += blockDim.x) {
-      const int e = i % E;
-      int before = 0, all = 0;
+    // earlier chunks' pairs per expert and the total.  152 CTAs read 152 rows of counts
+    // each: in 16 bits, eight experts per load, the threads of a column sharing out
+    // the rows (one 32-bit count per load: 16384 x 256 took 5 us longer).
+    if (a.chunk <= 65535) {
+      const int columns = a.pitch / 8, parts = max(int(blockDim.x) / columns, 1);
+      for (int i = threadIdx.x; i < columns * parts; i += blockDim.x) {
+        const int col = i % columns;
+        uint32_t before[4] = {0, 0, 0, 0}, all[4] = {0, 0, 0, 0};     // two experts each:
+        int hi_before[4] = {0, 0, 0, 0}, hi_all[4] = {0, 0, 0, 0};    // low halves, high halves
+        const uint4* row = static_cast<const uint4*>(a.counts) + col;
 #pragma unroll 8
-      for (int c = i / E; c < int(gridDim.x); c += parts) {
-        const int v = __ldcg(a.counts + int64_t(c) * E + e);
-        before += c < int(blockIdx.x) ? v : 0;
-        all += v;
+        for (int c = i / columns; c < int(gridDim.x); c += parts) {
+          const uint4 v = __ldcg(row + c * columns);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            all[j] += u[j] & 0xffffu;
+            hi_all[j] += int(u[j] >> 16);
+            if (c < int(blockIdx.x)) {
+              before[j] += u[j] & 0xffffu;
+              hi_before[j] += int(u[j] >> 16);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = col * 8 + 2 * j;
+          // (integers: in any order)
+          if (e < E && all[j]) atomicAdd(&total[e], int(all[j]));
+          if (e < E && before[j]) atomicAdd(&start[e], int(before[j]));
+          if (e + 1 < E && hi_all[j]) atomicAdd(&total[e + 1], hi_all[j]);
+          if (e + 1 < E && hi_before[j]) atomicAdd(&start[e + 1], hi_before[j]);
+        }
       }
-      if (all) atomicAdd(&total[e], all);        // (integers: in any order)
-      if (before) atomicAdd(&start[e], before);
+    } else {
+      for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const int32_t* row = static_cast<const int32_t*>(a.counts) + e;
+        int before = 0, all = 0;
+        for (int c = 0; c < int(gridDim.x); ++c) {
+          const int v = __ldcg(row + c * E);
+          before += c < int(blockIdx.x) ? v : 0;
+          all += v;
+        }
+        total[e] = all;
+        start[e] = before;
+      }
     }
   }
   __syncthreads();
@@ -223,7 +268,7 @@ fo_status launch_as(const ScoredArgs& a, int grid, int smem, cudaStream_t st) {
   if (err[slot] != cudaSuccess) return FO_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(scored_threads(V));
+  cfg.blockDim = dim3(kScoredThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -240,7 +285,7 @@ fo_status launch_as(const ScoredArgs& a, int grid, int smem, cudaStream_t st) {
 
 template <int V>
 fo_status launch_v(ScoredArgs a, int sms, cudaStream_t st) {
-  constexpr int warps = scored_threads(V) / 32;
+  constexpr int warps = kScoredThreads / 32;
   const int E = a.score.experts, K = a.score.top_k;
   a.score.vec = a.score.vec && a.score.per % V == 0 && V * (a.score.bf16 ? 2 : 4) % 16 == 0;
   int64_t grid;
@@ -308,7 +353,8 @@ fo_status launch_moe_route_scored(const fo_route_desc& d, const void* logits, fo
   a.expert_first = expert_first;
   a.expert_rows = expert_rows;
   a.barrier = static_cast<uint32_t*>(workspace);
-  a.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
+  a.counts = static_cast<uint8_t*>(workspace) + 256;
+  a.pitch = (d.experts + 7) / 8 * 8;
   a.status = dev_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // a lane's experts: of a group, and up to 64 (a group of 60 to a lane)

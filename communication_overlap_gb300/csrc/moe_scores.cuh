@@ -67,16 +67,41 @@ __device__ __forceinline__ double shfl_xor_64(double x, int o) {
   return __shfl_xor_sync(0xffffffffu, x, o);
 }
 
-// What two fp32 choices may be off together.  sigmoid by __expf (2 + 1.173 |l|
-// ulp, where s (1 - s) |l| is at most 0.28) and a division of 2 ulp: each below
-// 2^-21.  softmax: l - max rounded, __expf, a sum of up to 64 + 5 roundings: below
-// 2^-17 of the value.  The addition's rounding.  `ulps`: what a key leaves out.
-__device__ __forceinline__ float choice_margin(bool sigmoid, float c, float ulps) {
-  return (sigmoid ? 0x1p-20f : 0x1p-16f) + fabsf(c) * (0x1p-22f + ulps * 0x1p-23f);
+// What two fp32 choices may be off together: `score`, for their scores, and what the
+// choice's own magnitude adds, the addition's rounding and the `ulps` that a key
+// leaves out.
+//  sigmoid: the power of two's argument is rounded twice (|l| 2^-23 of the
+//      exponential, where s (1 - s) |l| is at most 0.28), ex2.approx is off by 2^-22,
+//      the addition by 2^-24, rcp.approx by 2^-23: each below 2^-21.
+//  softmax: of a score p, which is at most the largest, 1 / sum: p |l - max| 2^-23 (at
+//      most 0.37 2^-23), ex2.approx, rcp.approx, the product, and the sum of expf
+//      (2 ulp) with V + 5 roundings: each below (V + 16) 2^-24.
+__device__ __forceinline__ float score_margin(bool sigmoid, float inv, int v) {
+  return sigmoid ? 0x1p-20f : inv * float(v + 16) * 0x1p-23f;
+}
+__device__ __forceinline__ float choice_margin(float score, float c, float ulps) {
+  return score + fabsf(c) * (0x1p-22f + ulps * 0x1p-23f);
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid_32(float l) {
+  return inverse_fast(1.0f + exp2_fast(l * -kLog2e));
+}
+__device__ __forceinline__ float softmax_32(float l, float top, float inv) {
+  return exp2_fast((l - top) * kLog2e) * inv;
+}
 __device__ __forceinline__ float score_32(const ScoreArgs& a, float l, float top, float inv) {
-  return a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - top) * inv;
+  return a.sigmoid ? sigmoid_32(l) : softmax_32(l, top, inv);
 }
 
 // A choice in fp64: top and sum are softmax's, of the token.
@@ -105,71 +130,73 @@ __device__ __noinline__ bool all_alike(const ScoreArgs& a, int64_t at) {
   return __all_sync(0xffffffffu, alike);
 }
 
-// The groups that stay, in fp64: bit g of the result.  Of each group only the
-// experts that may be among its two largest are computed: those within a margin of
-// its second (or only) fp32 choice, `low`, on the lanes of its group.
+// Of the groups whose lanes say `unsure` the `open_groups` best, in fp64: bit g of the
+// result.  Only experts that may be among a group's two largest are computed, those
+// from `low` on (at most its second, or only, fp32 choice, less a margin), and all of
+// them at once, a lane each: an exponential and a division in fp64 take a
+// microsecond.
 __device__ __noinline__ uint32_t groups_64(const ScoreArgs& a, int64_t at, int width, float top,
-                                           float inv, float low) {
-  const int lane = threadIdx.x & 31, lanes = 1 << a.lane_bits;
-  const int g = lane >> a.lane_bits, sub = lane & (lanes - 1);
-  const bool alike = all_alike(a, at);
-  const double sum = a.sigmoid ? 1.0 : softmax_sum_64(a, at, top);
-  const float from = low - choice_margin(a.sigmoid, low, 0.0f);
-  double m1 = 0.0, m2 = 0.0;
-  int n = 0;              // of the two, how many there are
-  bool nan = false;       // ranks the group above every number
+                                           float inv, float low, bool unsure, int open_groups) {
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> a.lane_bits, sub = lane & ((1 << a.lane_bits) - 1);
+  const float ninf = __int_as_float(0xff800000);
+  // (without a bias the largest choice is the largest logit's)
+  const bool by_logit = a.bias == nullptr && a.group_top == 1;
+  const double sum = a.sigmoid || by_logit ? 1.0 : softmax_sum_64(a, at, top);
+  double m1 = 0.0, m2 = 0.0;    // of group `lane`, the two largest so far
+  int n = 0;                    // and how many of them there are
+  bool nan = false;             // ranks the group above every number
+  int mine = -1, held = 0;      // the lane's candidate, and how many lanes have one
+  const auto take = [&]() {
+    float l = 0.0f, b = 0.0f;
+    if (mine >= 0) l = logit_at(a, at + mine), b = a.bias ? __ldg(a.bias + mine) : 0.0f;
+    const double v = mine < 0 ? 0.0 : by_logit ? double(l) : choice_64(a, l, b, top, sum);
+    for (int j = 0; j < held; ++j) {
+      const double w = __shfl_sync(0xffffffffu, v, j);
+      const int e = __shfl_sync(0xffffffffu, mine, j);
+      if (e / a.per != lane) continue;
+      if (w != w) {
+        nan = true;
+      } else if (n == 0 || w > m1) {
+        m2 = m1;
+        m1 = w;
+        n = n ? 2 : 1;
+      } else if (n == 1 || w > m2) {
+        m2 = w;
+        n = 2;
+      }
+    }
+    mine = -1, held = 0;
+  };
   for (int i = 0; i < width; ++i) {
-    const int k = sub * width + i;
-    if (g >= a.groups || k >= a.per) continue;
-    const float l = logit_at(a, at + g * a.per + k);
-    const float b = a.bias ? __ldg(a.bias + g * a.per + k) : 0.0f;
-    const float c = score_32(a, l, top, inv) + b;
-    if (l == __int_as_float(0xff800000) || c == __int_as_float(0xff800000) || c < from) continue;
-    const double v = alike ? 0.0 : choice_64(a, l, b, top, sum);
-    if (v != v) {
-      nan = true;
-    } else if (n == 0 || v > m1) {
-      m2 = m1;
-      m1 = v;
-      n = n ? 2 : 1;
-    } else if (n == 1 || v > m2) {
-      m2 = v;
-      n = 2;
+    const int k = sub * width + i, e = g * a.per + k;
+    bool in = unsure && g < a.groups && k < a.per;
+    if (in) {
+      const float l = logit_at(a, at + e);
+      const float c = by_logit ? l : score_32(a, l, top, inv) + (a.bias ? __ldg(a.bias + e) : 0.0f);
+      in = l != ninf && c != ninf && !(c < low);
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, in);
+    if (held + __popc(todo) > 32) take();
+    for (; todo; todo &= todo - 1) {
+      const int c = __shfl_sync(0xffffffffu, e, __ffs(todo) - 1);
+      if (lane == held) mine = c;
+      ++held;
     }
   }
-  for (int o = 1; o < lanes; o <<= 1) {
-    const double v1 = shfl_xor_64(m1, o), v2 = shfl_xor_64(m2, o);
-    const int k = __shfl_xor_sync(0xffffffffu, n, o);
-    nan |= __shfl_xor_sync(0xffffffffu, int(nan), o) != 0;
-    if (k == 0) continue;
-    if (n == 0) {
-      m1 = v1, m2 = v2, n = k;
-      continue;
-    }
-    // the two largest of m1 >= m2 and v1 >= v2
-    double next = fmin(m1, v1);
-    if (v1 > m1) {
-      if (k == 2 && v2 > next) next = v2;
-    } else if (n == 2 && m2 > next) {
-      next = m2;
-    }
-    m1 = fmax(m1, v1), m2 = next, n = 2;
-  }
-  const bool any = g < a.groups && (n > 0 || nan);
+  take();
+  const bool any = n > 0 || nan;
   const double score = a.group_top == 2 && n == 2 ? m1 + m2 : m1;
   int rank = 0;
-  uint32_t kept = 0;
   for (int h = 0; h < a.groups; ++h) {
-    const int from_lane = h << a.lane_bits;
-    const double v = __shfl_sync(0xffffffffu, score, from_lane);
-    const bool has = __shfl_sync(0xffffffffu, int(any), from_lane) != 0;
-    const bool its = __shfl_sync(0xffffffffu, int(nan), from_lane) != 0;
-    const bool above = its || nan ? its && (!nan || h < g) : v > score || (v == score && h < g);
-    if (has && (!any || above)) ++rank;
+    const double v = __shfl_sync(0xffffffffu, score, h);
+    const bool has = __shfl_sync(0xffffffffu, int(any), h) != 0;
+    const bool its = __shfl_sync(0xffffffffu, int(nan), h) != 0;
+    const bool above = its || nan ? its && (!nan || h < lane)
+                                  : v > score || (v == score && h < lane);
+    rank += has && above;
   }
-  const uint32_t ballot = __ballot_sync(0xffffffffu, any && rank < a.top_groups && sub == 0);
-  for (int h = 0; h < a.groups; ++h) kept |= (ballot >> (h << a.lane_bits) & 1u) << h;
-  return kept;
+  return __ballot_sync(0xffffffffu, any && rank < open_groups);
 }
 
 // A choice among any number of near ties: each round takes the largest fp32 value
@@ -200,7 +227,8 @@ __device__ __noinline__ int choose_among_all(const ScoreArgs& a, int64_t at, int
     const float c = order_value(best);
     // (without a bias the values are the logits, and exact; so are infinities and NaN)
     const bool finite = a.bias != nullptr && c < pinf;
-    const uint32_t from = finite ? order_key(c - choice_margin(a.sigmoid, c, 0.0f)) : best;
+    const uint32_t from =
+        finite ? order_key(c - choice_margin(score_margin(a.sigmoid, inv, width), c, 0.0f)) : best;
     uint32_t low = 0xffffffffu;       // the lowest candidate
     for (int i = width - 1; i >= 0; --i) {
       const uint32_t k = order_key(value(i, l, b));
@@ -308,7 +336,7 @@ struct LaneExperts {
     if constexpr (V <= 8)
       return bias[i];
     else
-      return a.bias && i < count ? __ldg(a.bias + first + i) : 0.0f;
+      return i < count ? __ldg(a.bias + first + i) : 0.0f;
   }
   // The logits of the token that starts at `at`; -inf past the lane's experts.
   __device__ __forceinline__ void load(const ScoreArgs& a, int64_t at, bool live,
@@ -346,180 +374,246 @@ struct LaneExperts {
   }
 };
 
-// The choice for the token whose logits start at `at` and are x: lane j < top_k
-// returns slot j in id (-1: none) and weight.
+// One token's choice on its way through warp_choose.
 template <int V>
-__device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExperts<V>& own,
-                                            int64_t at, const float (&x)[V], int& id,
-                                            float& weight) {
-  const int lane = threadIdx.x & 31;
+struct Choice {
+  uint32_t key[V];
+  float top, sum, inv;      // softmax's
+  bool open;                // this lane's experts may be chosen
+  int win;                  // slot `lane`: the lane that had it, and its key
+  uint32_t full;
+};
+
+// The keys, sorted.
+template <int V>
+__device__ __forceinline__ void make_keys(const ScoreArgs& a, const LaneExperts<V>& own,
+                                          const float (&x)[V], Choice<V>& c) {
   const float ninf = __int_as_float(0xff800000);
   constexpr uint32_t kMask = V - 1;
-  // softmax's statistics in fp32
-  float top = 0.0f, sum = 1.0f;
+  c.top = 0.0f, c.sum = c.inv = 1.0f;
   if (!a.sigmoid) {
-    top = ninf;
+    c.top = x[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
-    top = warp_most(top);
-    sum = 0.0f;
+    for (int i = 1; i < V; ++i) c.top = fmaxf(c.top, x[i]);
+    c.top = warp_most(c.top);
+    c.sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += x[i] != ninf ? expf(x[i] - top) : 0.0f;
-    sum = warp_add(sum);
+    for (int i = 0; i < V; ++i) c.sum += x[i] != ninf ? expf(x[i] - c.top) : 0.0f;
+    c.sum = warp_add(c.sum);
+    c.inv = inverse_fast(c.sum);
   }
-  const float inv = 1.0f / sum;
-  // keys of the choice; the group's two largest values' keys
-  const bool by_logit = a.bias == nullptr;
-  const bool exact_groups = by_logit && a.group_top == 1;
-  uint32_t key[V], k1 = 0, k2 = 0;
+  float v[V];
+  if (a.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = x[i] + 0.0f;       // (-0 becomes +0)
+  } else if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = sigmoid_32(x[i]) + own.bias_of(a, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = softmax_32(x[i], c.top, c.inv) + own.bias_of(a, i);
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float c = x[i];
-    uint32_t k;
-    if (!by_logit) {
-      c = score_32(a, x[i], top, inv) + own.bias_of(a, i);
-      if (x[i] == ninf) c = ninf;
-    }
-    k = order_key(c);
-    key[i] = k >= kLeastKey ? (k & ~kMask) | (kMask - uint32_t(i)) : 0u;
-    if (a.groups > 1) {
-      if (by_logit && !exact_groups && k >= kLeastKey) k = order_key(score_32(a, x[i], top, inv));
-      if (k < kLeastKey) k = 0u;
-      k2 = max(k2, min(k1, k));
-      k1 = max(k1, k);
-    }
+    const int32_t b = __float_as_int(v[i]);
+    const uint32_t k = uint32_t(b) ^ (uint32_t(b >> 31) | 0x80000000u);
+    // (a NaN is no -inf; fminf takes the number of the two)
+    c.key[i] = fminf(x[i], v[i]) == ninf ? 0u : (k & ~kMask) | (kMask - uint32_t(i));
   }
-  bool open = own.count > 0;
-  if (a.groups > 1) {
-    const int lanes = 1 << a.lane_bits, g = lane >> a.lane_bits;
-    for (int o = 1; o < lanes; o <<= 1) {
-      const uint32_t v1 = __shfl_xor_sync(0xffffffffu, k1, o);
-      const uint32_t v2 = __shfl_xor_sync(0xffffffffu, k2, o);
-      k2 = max(max(k2, v2), min(k1, v1));
-      k1 = max(k1, v1);
-    }
-    uint32_t score = k1;
-    if (a.group_top == 2 && k2 != 0u) score = order_key(order_value(k1) + order_value(k2));
-    int rank = 0;
+  sort_keys<V>(c.key);
+  c.open = own.count > 0;
+}
+
+// Bars the experts of the groups that do not stay.
+template <int V>
+__device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choice<V>& c) {
+  constexpr uint32_t kMask = V - 1;
+  const int lane = threadIdx.x & 31, lanes = 1 << a.lane_bits, g = lane >> a.lane_bits;
+  const bool by_logit = a.bias == nullptr;
+  // the two largest of the lane, then of the group
+  uint32_t k1 = c.key[0] & ~kMask, k2 = V > 1 ? c.key[V > 1 ? 1 : 0] & ~kMask : 0u;
+  if (by_logit && a.group_top == 2) {     // (scores grow with the logits)
+    if (k1 != 0u) k1 = order_key(score_32(a, order_value(k1), c.top, c.inv));
+    if (k2 != 0u) k2 = order_key(score_32(a, order_value(k2), c.top, c.inv));
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    const uint32_t v1 = __shfl_xor_sync(0xffffffffu, k1, o);
+    const uint32_t v2 = __shfl_xor_sync(0xffffffffu, k2, o);
+    k2 = max(max(k2, v2), min(k1, v1));
+    k1 = max(k1, v1);
+  }
+  uint32_t score = k1;
+  if (a.group_top == 2 && k2 != 0u) score = order_key(order_value(k1) + order_value(k2));
+  int rank = 0;
 #pragma unroll 8
-    for (int h = 0; h < a.groups; ++h) {
-      const uint32_t v = __shfl_sync(0xffffffffu, score, h << a.lane_bits);
-      rank += v > score || (v == score && h < g);
-    }
-    bool stays = g < a.groups && score != 0u && rank < a.top_groups;
-    if (!exact_groups) {
-      const uint32_t in = __reduce_min_sync(0xffffffffu, stays ? score : 0xffffffffu);
-      const uint32_t out = __reduce_max_sync(0xffffffffu, g < a.groups && !stays ? score : 0u);
-      const float vi = order_value(in), vo = order_value(out);
-      // (a sum of two is off by twice as much)
-      if (out != 0u && (in == out || vi - vo < 2.0f * choice_margin(a.sigmoid, vi, 0.0f))) {
-        const float low = a.group_top == 2 && k2 != 0u ? order_value(k2) : order_value(k1);
-        const uint32_t kept = groups_64(a, at, V, top, inv, k1 != 0u ? low : ninf);
-        stays = g < a.groups && (kept >> g & 1u);
-      }
-    }
-    open = open && stays;
-    if (!stays) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = 0u;
+  for (int h = 0; h < a.groups; ++h) {
+    const uint32_t v = __shfl_sync(0xffffffffu, score, h << a.lane_bits);
+    rank += v > score || (v == score && h < g);
+  }
+  bool stays = g < a.groups && score != 0u && rank < a.top_groups;
+  const uint32_t in = __reduce_min_sync(0xffffffffu, stays ? score : 0xffffffffu);
+  const uint32_t out = __reduce_max_sync(0xffffffffu, g < a.groups && !stays ? score : 0u);
+  if (out != 0u) {
+    // (bf16 logits are exact; of fp32 ones the keys leave bits out; sums of two are off
+    // by twice as much)
+    const bool logits = by_logit && a.group_top == 1;
+    const float s0 = score_margin(a.sigmoid, c.inv, V), vi = order_value(in);
+    const float margin = logits ? 0.0f : 2.0f * choice_margin(s0, vi, float(4 * V));
+    const bool near = in == out ? !(logits && a.bf16) : vi - order_value(out) < margin;
+    if (near && !all_alike(a, at)) {
+      // groups further than a margin from the last that stays are sure
+      const bool unsure = g < a.groups && score != 0u &&
+                          (score == in || fabsf(order_value(score) - vi) <= margin);
+      const bool sure = stays && !unsure;
+      const int n_sure =
+          __popc(__ballot_sync(0xffffffffu, sure && (lane & (lanes - 1)) == 0));
+      const float least = order_value(a.group_top == 2 && k2 != 0u ? k2 : k1);
+      const float low =
+          least - (logits ? fabsf(least) * (float(V) * 0x1p-22f)
+                          : choice_margin(s0, least, float(4 * V)));
+      const uint32_t best =
+          groups_64(a, at, V, c.top, c.inv, low, unsure, a.top_groups - n_sure);
+      stays = sure || (unsure && (best >> g & 1u));
     }
   }
-  sort_keys<V>(key);
-  // the slots and the expert that comes next, for its margin; and on while ranks
-  // are too near to tell
-  const int K = a.top_k;
-  id = -1;
-  uint32_t mine = 0u, last = 0u;
-  int s = 0;
-  const auto round = [&]() {
-    const uint32_t head = key[0] & ~kMask;
-    const uint32_t best = __reduce_max_sync(0xffffffffu, head);
-    if (best == 0u) return false;
-    const int win = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
-    const uint32_t full = __shfl_sync(0xffffffffu, key[0], win);
-    if (lane == s) {
-      id = (win >> a.lane_bits) * a.per + (win & ((1 << a.lane_bits) - 1)) * V +
-           int(kMask - (full & kMask));
-      mine = best;
-    }
-    if (lane == win) {
+  c.open = c.open && stays;
+  if (!stays) {
 #pragma unroll
-      for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-      key[V - 1] = 0u;
-    }
-    last = best;
-    ++s;
-    return true;
+    for (int i = 0; i < V; ++i) c.key[i] = 0u;
+  }
+}
+
+// The next rank: the largest head of the lanes' lists, on the lowest lane that has
+// it.  Its key without the lane's bits, 0 where none is left.
+template <int V>
+__device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int s) {
+  constexpr uint32_t kMask = V - 1;
+  const int lane = threadIdx.x & 31;
+  const uint32_t head = c.key[0] & ~kMask;
+  const uint32_t best = __reduce_max_sync(0xffffffffu, head);
+  const int win = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+  const uint32_t full = __shfl_sync(0xffffffffu, c.key[0], win);
+  if (lane == s) c.win = win, c.full = full;
+  const bool mine = lane == win;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t after = i + 1 < V ? c.key[i + 1 < V ? i + 1 : i] : 0u;
+    c.key[i] = mine ? after : c.key[i];
+  }
+  return best;
+}
+
+// The choice for N tokens at once, whose logits start at `at` and are x: lane j <
+// top_k returns slot j in id (-1: none) and weight.  (Their steps are independent,
+// so one's wait for a reduction is filled by the other's.)
+template <int V, int N>
+__device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExperts<V>& own,
+                                            const int64_t (&at)[N], const float (&x)[N][V],
+                                            int (&id)[N], float (&weight)[N]) {
+  constexpr uint32_t kMask = V - 1;
+  const int lane = threadIdx.x & 31, K = a.top_k;
+  const float ninf = __int_as_float(0xff800000);
+  const bool by_logit = a.bias == nullptr;
+  Choice<V> c[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) make_keys<V>(a, own, x[n], c[n]);
+  if (a.groups > 1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) keep_groups<V>(a, at[n], c[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n].win = 0, c[n].full = 0u;
+  // the slots, and the expert that comes next for its margin (bf16 logits alone keep
+  // all their bits in a key and need none)
+  const bool exact = by_logit && a.bf16;
+  const int rounds = exact || K == 32 ? K : K + 1;
+  uint32_t last[N];
+  for (int s = 0; s < rounds; ++s) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) last[n] = next_rank<V>(c[n], s);
+  }
+  float l[N], b[N];
+  const auto expert = [&](const Choice<V>& q) {
+    return q.full == 0u ? -1
+                        : (q.win >> a.lane_bits) * a.per +
+                              (q.win & ((1 << a.lane_bits) - 1)) * V + int(kMask - (q.full & kMask));
   };
-  const int rounds = K < 32 ? K + 1 : 32;
-  bool more = true;
-  while (s < rounds && more) more = round();
-  float l = id >= 0 ? logit_at(a, at + id) : 0.0f;
-  // (bf16 logits keep all their bits in a key: without a bias they are exact)
-  if (!(by_logit && a.bf16)) {
-    float b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
-    const auto near = [&](uint32_t hi, uint32_t lo) {
-      if (hi == 0u || lo == 0u) return false;
-      if (by_logit || hi == lo) return hi == lo;
-      const float c = order_value(hi);
-      return c - order_value(lo) < choice_margin(a.sigmoid, c, float(kMask));
-    };
-    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
-    const float next_l = __shfl_down_sync(0xffffffffu, l, 1);
-    const float next_b = __shfl_down_sync(0xffffffffu, b, 1);
-    // (alike neighbours lie in order; but at the last slot another expert may be as
-    // near behind them)
-    const bool alike = lane + 1 < K && l == next_l && b == next_b;
-    const bool unsure = lane < K && lane < 31 && !alike && near(mine, next);
-    // (no lane holds the expert after slot 31)
-    bool all = false;
-    if (K == 32)
-      all = near(__shfl_sync(0xffffffffu, mine, 31),
-                 __reduce_max_sync(0xffffffffu, key[0] & ~kMask));
-    if (__any_sync(0xffffffffu, unsure) || all) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    id[n] = expert(c[n]);
+    l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
+    b[n] = id[n] >= 0 && !by_logit ? __ldg(a.bias + id[n]) : 0.0f;
+  }
+  if (!exact) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const auto near = [&](uint32_t hi, uint32_t lo) {
+        if (hi == 0u || lo == 0u) return false;
+        if (by_logit || hi == lo) return hi == lo;
+        const float v = order_value(hi);
+        return v - order_value(lo) < choice_margin(score_margin(a.sigmoid, c[n].inv, V), v, float(V));
+      };
+      const uint32_t mine = c[n].full & ~kMask;
+      const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+      const float next_l = __shfl_down_sync(0xffffffffu, l[n], 1);
+      const float next_b = __shfl_down_sync(0xffffffffu, b[n], 1);
+      // (alike neighbours lie in order; but at the last slot another expert may be as
+      // near behind them)
+      const bool alike = lane + 1 < K && l[n] == next_l && b[n] == next_b;
+      const bool unsure = lane < K && lane < 31 && !alike && near(mine, next);
+      bool all = false;       // (no lane holds the expert after slot 31)
+      if (K == 32)
+        all = near(__shfl_sync(0xffffffffu, mine, 31),
+                   __reduce_max_sync(0xffffffffu, c[n].key[0] & ~kMask));
+      if ((!__any_sync(0xffffffffu, unsure) && !all) || all_alike(a, at[n])) continue;
       // the ranks that follow, as far as they are near to the one before
-      bool chain = near(__shfl_sync(0xffffffffu, mine, K - 1), last) && s == K + 1;
+      int s = rounds;
+      bool chain = K < 32 && near(__shfl_sync(0xffffffffu, mine, K - 1), last[n]);
       while (chain && s < 32) {
-        const uint32_t before = last;
-        if (!round()) break;
-        chain = near(before, last);
+        const uint32_t before = last[n];
+        last[n] = next_rank<V>(c[n], s++);
+        chain = near(before, last[n]);
       }
-      all |= chain && s == 32;
-      if (all) {
-        if (!all_alike(a, at)) id = choose_among_all(a, at, V, top, inv, open);
+      if (all || chain) {
+        id[n] = choose_among_all(a, at[n], V, c[n].top, c[n].inv, c[n].open);
       } else {
-        l = id >= 0 ? logit_at(a, at + id) : 0.0f;
-        b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, id >= 0);
-        id = rank_again(a, at, top, id, l, b, __popc(lanes));
+        id[n] = expert(c[n]);
+        l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
+        b[n] = id[n] >= 0 && !by_logit ? __ldg(a.bias + id[n]) : 0.0f;
+        const uint32_t lanes = __ballot_sync(0xffffffffu, id[n] >= 0);
+        id[n] = rank_again(a, at[n], c[n].top, id[n], l[n], b[n], __popc(lanes));
       }
-      if (lane >= K) id = -1;
-      l = id >= 0 ? logit_at(a, at + id) : 0.0f;
+      if (lane >= K) id[n] = -1;
+      l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
     }
   }
-  if (lane >= K) id = -1;
-  // the weights, in fp32.  Chosen scores may all be far below 1: those to be
-  // renormalised share a factor that makes the largest about 1.
-  float w = 0.0f;
-  if (a.renormalize) {
-    const float most = warp_most(id >= 0 ? l : ninf);
-    if (id >= 0) {
-      if (a.sigmoid) {
-        // e^(l - m) / (1 + e^l) with m the largest chosen logit, where that is negative
-        const float m = fminf(most, 0.0f);
-        w = l < 0.0f ? expf(l - m) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
-      } else {
-        // softmax over the chosen, whatever share of the whole they have (a NaN or
-        // +inf anywhere enters every score)
-        w = sum == sum ? expf(l - most) : sum;
-      }
+  // the weights, in fp32, by expf and a division of 2 ulp.  Chosen scores may all be
+  // far below 1: those to be renormalised share a factor that makes the largest
+  // about 1.
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (lane >= K) id[n] = -1;
+    float w = 0.0f;
+    if (a.renormalize) {
+      // e^(l - m) / (1 + e^l), m the largest chosen logit where that is negative; softmax
+      // over the chosen, whatever share of the whole they have (a NaN or +inf anywhere
+      // enters every score)
+      const float most =
+          order_value(__reduce_max_sync(0xffffffffu, id[n] >= 0 ? order_key(l[n]) : 0u));
+      if (a.sigmoid)
+        w = __fdividef(expf(fminf(l[n], 0.0f) - fminf(most, 0.0f)), 1.0f + expf(-fabsf(l[n])));
+      else
+        w = c[n].sum == c[n].sum ? expf(l[n] - most) : c[n].sum;
+      if (l[n] != l[n]) w = l[n];       // (fminf would drop a NaN)
+      w = id[n] >= 0 ? w : 0.0f;
+      w = __fdividef(w, warp_add(w));
+    } else if (a.sigmoid) {
+      w = __fdividef(1.0f, 1.0f + expf(-l[n]));
+    } else {
+      w = __fdividef(expf(l[n] - c[n].top), c[n].sum);
     }
-    const float total = warp_add(w);
-    w = id >= 0 ? w / total : 0.0f;
-  } else if (id >= 0) {
-    w = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / sum;
+    weight[n] = id[n] >= 0 ? a.scale * w : 0.0f;
   }
-  weight = id >= 0 ? a.scale * w : 0.0f;
 }
 
 }  // namespace fo

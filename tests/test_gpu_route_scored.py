@@ -273,3 +273,25 @@ def test_refusals():
         moe.route_backward(l, torch.zeros((2, 2), dtype=torch.int32, device="cuda"),
                            torch.zeros((2, 2), device="cuda"), torch.zeros((2, 2), device="cuda"),
                            scoring="tanh")
+
+
+def test_more_tokens_than_16_bits_count():
+    """So many that a chunk's pairs per expert pass 16 bits (most go to one)."""
+    T = 256 * 65536 + 77
+    g = torch.Generator(device="cuda").manual_seed(9)
+    l = torch.randn((T, 3), generator=g, device="cuda").to(BF16)
+    l[:, 1] += 4
+    r = moe.route(l, 1, True, 0, "sigmoid")
+    ids = r.ids[:, 0].long()
+    assert torch.equal(ids, l.float().argmax(1)) or (l.gather(1, ids[:, None]) == l.amax(1, True)).all()
+    count = torch.bincount(ids, minlength=3)
+    assert torch.equal(r.expert_rows.long(), count)
+    span = (count + 127) // 128 * 128
+    first = span.cumsum(0) - span
+    assert torch.equal(r.expert_first.long(), first)
+    for e in range(3):
+        tokens = torch.nonzero(ids == e)[:, 0]
+        rows = torch.arange(len(tokens), device="cuda") + first[e]
+        assert torch.equal(r.token_row[tokens, 0].long(), rows)
+        assert torch.equal(r.row_token[rows].long(), tokens)
+    assert int((r.row_token >= 0).sum()) == T
