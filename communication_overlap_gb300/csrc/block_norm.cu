@@ -39,85 +39,133 @@ __device__ __forceinline__ void stream_of(const NormArgs& a, int col, int64_t ga
   for (int i = 0; i < W; ++i) s[i] = fmaf(a.scale, v[i], r[i]);
 }
 
-// A row of up to 8192 columns, eight per thread; several rows to a CTA where a row
-// has few warps.  CTAs walk over the tokens with the parameters' product in
-// registers and DEPTH rows under way in the ring: with a CTA per row, which loads
-// its parameters and waits for its own row, 16384 x 4096 took 168 us.
-template <typename A, typename S, int DEPTH>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps) {
+// Rows of up to 8192 columns; several to a CTA where they have few warps.  CTAs walk
+// over the tokens with the parameters' product in registers and DEPTH rows under way
+// in the ring, two values per instruction.  16384 x 4096: a CTA per row, which loads
+// its parameters and waits for its own row, took 168 us; this with eight columns per
+// thread and one value per instruction 116.
+template <typename A, typename S, int NV, int DEPTH>
+__global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warps) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float buf[2 * 32];
-  constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of a row's eight columns
-  constexpr int kPieces = kA + kS;
+  constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of eight columns
+  constexpr int kPieces = NV * (kA + kS);
   if (threadIdx.x < 64) buf[threadIdx.x] = 0.0f;
   __syncthreads();
   int turn = 0;
   const RowGroup g = RowGroup::of(warps);
   const OwnRing ring(smem);
-  const int col = g.tid * 8;
-  const bool has = col < a.hidden;
   const int rows = int(blockDim.x) / (warps * 32);
-  const int64_t step = int64_t(gridDim.x) * rows;
-  const int64_t t0 = int64_t(blockIdx.x) * rows + g.index;
+  const int step = int(gridDim.x) * rows;
+  const int t0 = int(blockIdx.x) * rows + g.index;
   const float inv = 1.0f / float(a.hidden);
-  const auto fetch = [&](int64_t t, int stage) {
-    if (has && t < a.tokens) {
-      ring.fetch(stage * kPieces, static_cast<const A*>(a.x) + t * a.x_stride + col);
-      if (a.residual != nullptr)
-        ring.fetch(stage * kPieces + kA,
-                   static_cast<const S*>(a.residual) + t * a.residual_stride + col);
+  int col[NV];
+  bool has[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    col[v] = (v * warps * 32 + g.tid) * 8;
+    has[v] = col[v] < a.hidden;
+  }
+  const A* x_at = static_cast<const A*>(a.x) + int64_t(t0) * a.x_stride;
+  const S* r_at = static_cast<const S*>(a.residual) + int64_t(t0) * a.residual_stride;
+  const int64_t x_step = step * a.x_stride, r_step = step * a.residual_stride;
+  int fetched = t0;
+  const auto fetch = [&](int stage) {
+    if (fetched < a.tokens) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (has[v]) {
+          const int at = stage * kPieces + v * (kA + kS);
+          ring.fetch(at, x_at + col[v]);
+          if (a.residual != nullptr) ring.fetch(at + kA, r_at + col[v]);
+        }
     }
     OwnRing::commit();
+    fetched += step;
+    x_at += x_step;
+    r_at += r_step;
   };
 #pragma unroll
-  for (int i = 0; i < DEPTH; ++i) fetch(t0 + i * step, i);
-  float w[8], pre[8];
+  for (int i = 0; i < DEPTH; ++i) fetch(i);
+  Pair w[NV][4], pre[NV][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pre[i] = 0.0f;
-  if (has && a.pre != nullptr) load_param<8>(a.pre, col, a.params_f32, pre);
-  int64_t gate_row = -1;
-  int stage = 0;
-  for (int64_t t = t0; t < a.tokens; t += step) {
-    if (has) {
-      const int64_t row = a.gate_stride ? int64_t(uint32_t(t) / uint32_t(a.gate_rows)) : 0;
-      if (row != gate_row) load_factor(a, col, row * a.gate_stride, w);
+  for (int v = 0; v < NV; ++v) {
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = 0.0f;
+    if (has[v] && a.pre != nullptr) load_param<8>(a.pre, col[v], a.params_f32, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pre[v][i] = Pair::of(p[2 * i], p[2 * i + 1]), w[v][i] = Pair::of(0.0f);
+  }
+  int gate_row = -1, stage = 0;
+  S* sum_at = static_cast<S*>(a.sum) + int64_t(t0) * a.sum_stride;
+  A* y_at = static_cast<A*>(a.y) + int64_t(t0) * a.y_stride;
+  const int64_t sum_step = step * a.sum_stride, y_step = step * a.y_stride;
+  for (int t = t0; t < a.tokens; t += step) {
+    const int row = a.gate_stride ? int(uint32_t(t) / uint32_t(a.gate_rows)) : 0;
+    if (row != gate_row) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float p[8];
+        if (!has[v]) continue;
+        load_factor(a, col[v], row * a.gate_stride, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[v][i] = Pair::of(p[2 * i], p[2 * i + 1]);
+      }
       gate_row = row;
     }
     OwnRing::wait<DEPTH - 1>();
-    float x[8], s[8];
+    Pair x[NV][4], s[NV][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = s[i] = 0.0f;
-    if (has) {
-      ring.get<A>(stage * kPieces, x);
-      if (a.residual != nullptr) ring.get<S>(stage * kPieces + kA, s);
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[v][i] = s[v][i] = Pair::of(0.0f);
+      if (has[v]) {
+        const int at = stage * kPieces + v * (kA + kS);
+        ring.get<A>(at, x[v]);
+        if (a.residual != nullptr) ring.get<S>(at + kA, s[v]);
+      }
     }
-    fetch(t + DEPTH * step, stage);
-    if (++stage == DEPTH) stage = 0;
-    float r1 = 1.0f;
+    fetch(stage);
+    stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    Pair r1 = Pair::of(1.0f);
     if (a.post != nullptr) {
-      float sum[1] = {0.0f};
+      Pair sum = Pair::of(0.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] = fmaf(x[i], x[i], sum[0]);
-      g.sums<1>(sum, buf, turn);
-      r1 = rsqrtf(fmaf(sum[0], inv, a.eps));
-      if (g.tid == 0) a.post_rstd[t] = r1;
-    }
-    float sum[1] = {0.0f};
+      for (int v = 0; v < NV; ++v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[i] = fmaf(w[i], x[i] * r1, s[i]);
-      sum[0] = fmaf(s[i], s[i], sum[0]);
+        for (int i = 0; i < 4; ++i) sum = fma2(x[v][i], x[v][i], sum);
+      }
+      float total[1] = {sum.sum()};
+      g.sums<1>(total, buf, turn);
+      const float r = rsqrtf(fmaf(total[0], inv, a.eps));
+      if (g.tid == 0) a.post_rstd[t] = r;
+      r1 = Pair::of(r);
     }
-    if (has && a.sum != nullptr)
-      store_piece<8>(static_cast<S*>(a.sum) + t * a.sum_stride + col, s);
+    Pair sum = Pair::of(0.0f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[v][i] = fma2(w[v][i], x[v][i] * r1, s[v][i]);
+        sum = fma2(s[v][i], s[v][i], sum);
+      }
+      if (has[v] && a.sum != nullptr) store8(sum_at + col[v], s[v]);
+    }
+    sum_at += sum_step;
     if (a.pre == nullptr) continue;
-    g.sums<1>(sum, buf, turn);
-    const float r2 = rsqrtf(fmaf(sum[0], inv, a.eps));
+    float total[1] = {sum.sum()};
+    g.sums<1>(total, buf, turn);
+    const float r2 = rsqrtf(fmaf(total[0], inv, a.eps));
     if (g.tid == 0) a.pre_rstd[t] = r2;
-    if (!has) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= r2 * pre[i];
-    store_piece<8>(static_cast<A*>(a.y) + t * a.y_stride + col, s);
+    for (int v = 0; v < NV; ++v) {
+      if (!has[v]) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[v][i] = s[v][i] * Pair::of(r2) * pre[v][i];
+      store8(y_at + col[v], s[v]);
+    }
+    y_at += y_step;
   }
   OwnRing::wait<0>();
 }
@@ -184,30 +232,28 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a) {
   }
 }
 
-template <typename A, typename S, int DEPTH>
-fo_status launch_ring(const NormArgs& a, int warps, int rows, int row_bytes, cudaStream_t st) {
+template <typename A, typename S, int NV, int DEPTH>
+fo_status launch_ring(const NormArgs& a, const RowShape& s, int row_bytes, cudaStream_t st) {
   int sms = 0;
   fo_status q = sm_count(&sms);
-  if (q == FO_OK) q = allow_smem<norm_kernel<A, S, DEPTH>>();
+  if (q == FO_OK) q = allow_smem<norm_kernel<A, S, NV, DEPTH>>();
   if (q != FO_OK) return q;
-  const int threads = rows * warps * 32;
-  const int64_t most = (int64_t(a.tokens) + rows - 1) / rows;
-  const int64_t ctas = int64_t(sms) * (threads <= 512 ? 2 : 1);
-  norm_kernel<A, S, DEPTH><<<unsigned(most < ctas ? most : ctas), threads, DEPTH * row_bytes, st>>>(
-      a, warps);
+  const int64_t most = (int64_t(a.tokens) + s.rows - 1) / s.rows;
+  const int64_t ctas = int64_t(sms) * (s.threads <= 256 ? 2 : 1);
+  norm_kernel<A, S, NV, DEPTH>
+      <<<unsigned(most < ctas ? most : ctas), s.threads, DEPTH * row_bytes, st>>>(a, s.warps);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
 template <typename A, typename S>
 fo_status launch(const NormArgs& a, bool vec, cudaStream_t st) {
   if (vec && a.hidden <= 8192) {
-    const int warps = (a.hidden + 255) / 256, rows = rows_of_cta(warps, 16);
-    const int threads = rows * warps * 32;
-    // four rows under way where two CTAs of up to 512 threads fit on an SM so, else two
-    const int row = threads * 16 * int(sizeof(A) + sizeof(S)) / 2;
-    const bool deep = 4 * row <= (threads <= 512 ? kNormSmem / 2 : kNormSmem);
-    return deep ? launch_ring<A, S, 4>(a, warps, rows, row, st)
-                : launch_ring<A, S, 2>(a, warps, rows, row, st);
+    const RowShape s = row_shape(a.hidden);
+    // four rows under way where two CTAs of 256 threads, or one of more, fit so, else two
+    const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S)) / 2;
+    const bool deep = 4 * row <= (s.threads <= 256 ? kNormSmem / 2 : kNormSmem);
+    if (s.nv == 1) return launch_ring<A, S, 1, 4>(a, s, row, st);
+    return deep ? launch_ring<A, S, 2, 4>(a, s, row, st) : launch_ring<A, S, 2, 2>(a, s, row, st);
   } else if (vec) {
     norm_any_kernel<A, S, 8><<<unsigned(a.tokens), 512, 0, st>>>(a);
   } else {

@@ -9,6 +9,57 @@
 
 namespace fo {
 
+// Two fp32 values that one instruction takes at once.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ static Pair of(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+  }
+  __device__ __forceinline__ static Pair of(float x) { return of(x, x); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  }
+  __device__ __forceinline__ float sum() const {
+    float lo, hi;
+    get(lo, hi);
+    return lo + hi;
+  }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Pack8<T>& p, Pair (&x)[4]) {
+  float v[8];
+  p.get(v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
+}
+
+// Eight elements as four pairs, to 16 bytes of memory.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i].get(v[2 * i], v[2 * i + 1]);
+  store8(p, v);
+}
+
 // W consecutive elements of a row: eight, on 16 bytes, or one.
 template <typename T, int W>
 struct Piece {
@@ -116,8 +167,20 @@ struct RowGroup {
   }
 };
 
-// Rows of a CTA where a row has `warps` warps and the CTA at most `most`.
-inline int rows_of_cta(int warps, int most) { return warps <= most ? most / warps : 1; }
+// How rows of up to 8192 columns lie over threads: NV times eight columns per thread
+// (two where a row has more than 256: half the threads to meet at its sums, and half
+// the addresses), and CTAs of 256 threads where a row needs no more.
+struct RowShape {
+  int nv, warps, rows, threads;
+};
+inline RowShape row_shape(int hidden) {
+  RowShape s;
+  s.nv = hidden <= 256 ? 1 : 2;
+  s.warps = hidden > 0 ? (hidden + 256 * s.nv - 1) / (256 * s.nv) : 1;
+  s.rows = s.warps <= 8 ? 8 / s.warps : 1;
+  s.threads = s.rows * s.warps * 32;
+  return s;
+}
 
 // A ring in shared memory that a thread fills for itself, rows ahead of their use:
 // no other thread reads its pieces, so no barrier guards them.  Piece i of stage s
@@ -139,15 +202,27 @@ struct OwnRing {
                    : "memory");
   }
   template <typename T>
-  __device__ __forceinline__ void get(int piece, float (&v)[8]) const {
-    Pack8<T> p;
+  __device__ __forceinline__ void get(int piece, Pack8<T>& p) const {
 #pragma unroll
     for (int i = 0; i < int(sizeof(T)) / 2; ++i)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(p.w[i].x), "=r"(p.w[i].y), "=r"(p.w[i].z), "=r"(p.w[i].w)
                    : "r"(at(piece + i))
                    : "memory");
-    p.get(v);
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(int piece, Pair (&x)[4]) const {
+    Pack8<T> p;
+    get(piece, p);
+    pairs_of(p, x);
+  }
+  // eight fp32 values of the thread's own
+  __device__ __forceinline__ void put(int piece, const float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(piece + i)), "f"(v[4 * i]),
+                   "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                   : "memory");
   }
   __device__ __forceinline__ static void commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");

@@ -14,9 +14,9 @@
 //
 // A worker takes a contiguous range of tokens and keeps the parameters' sums of
 // its columns in registers; a last kernel adds the workers' in their order, so
-// results do not vary from run to run.  Rows of up to 4096 columns on 16 bytes go
-// through one kernel, which holds a row in registers between the two passes;
-// others through two, one for the means and one for the columns.
+// results do not vary from run to run.  Rows of up to 8192 columns on 16 bytes (4096
+// in fp32) go through one kernel, which holds a row in registers between the two
+// passes; others through two, one for the means and one for the columns.
 #include <cuda_runtime.h>
 
 #include "block_norm.cuh"
@@ -145,6 +145,16 @@ __device__ __forceinline__ void store_gate(const NormBackArgs& a, const BackShap
     store_piece<W>(static_cast<uint16_t*>(a.dgate) + t * f.hidden + col, dgate);
 }
 
+// scale times eight values of a parameter from `i` on, or scale alone.
+__device__ __forceinline__ void factor_of(const NormArgs& f, const void* p, int64_t i,
+                                          float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = 1.0f;
+  if (p != nullptr) load_param<8>(p, i, f.params_f32, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] *= f.scale;
+}
+
 template <int W>
 __device__ __forceinline__ void store_parts(const NormBackArgs& a, const BackShape& n,
                                             int64_t worker, int col, const float (&dpre)[W],
@@ -154,51 +164,75 @@ __device__ __forceinline__ void store_parts(const NormBackArgs& a, const BackSha
   if (f.post != nullptr) store_piece<W>(n.post_part + worker * f.hidden + col, dpost);
 }
 
-// Rows of up to 4096 columns, eight per thread; a worker per row of threads, several
-// to a CTA where a row has few warps.  The parameters' product w = scale gate post
-// and pre stay in registers and DEPTH rows are under way in the ring.  Of the
-// parameters' sums two are kept: of dy sn, and G of xn D over tokens with the
-// same gate, since dgate = scale post G and dpost = scale gate G.
-template <typename A, typename S, int DEPTH>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a,
-                                                            const BackShape n, int warps) {
+// Rows of up to 8192 columns; a worker per row of threads, several to a CTA where a
+// row has few warps.  DEPTH rows are under way in the ring, the parameters' product w =
+// scale gate post and pre lie behind it, and one instruction takes two values.  Of the
+// parameters' sums two are kept: of dy sn, and G of xn D over tokens with the same
+// gate, since dgate = scale post G and dpost = scale gate G (summed over the gates,
+// where a worker meets several: GATES).  16384 x 4096: eight columns per thread and one
+// value per instruction took 174 us.
+template <typename A, typename S, int NV, int DEPTH, bool GATES>
+__global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArgs a,
+                                                               const BackShape n, int warps) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float buf[2 * 3 * 32];
-  constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of a row's eight columns
-  constexpr int kPieces = 2 * (kA + kS);                    // x, dy, residual, dsum
+  constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of eight columns
+  constexpr int kOf = 2 * (kA + kS);                        // x, dy, residual, dsum
+  constexpr int kPieces = NV * kOf;
+  constexpr int kW = DEPTH * kPieces, kPre = kW + 2 * NV;   // the parameters' pieces
   for (int i = threadIdx.x; i < 192; i += blockDim.x) buf[i] = 0.0f;
   __syncthreads();
   int turn = 0;
   const NormArgs& f = a.f;
   const RowGroup g = RowGroup::of(warps);
   const OwnRing ring(smem);
-  const int col = g.tid * 8;
-  const bool has = col < f.hidden;
+  int col[NV];
+  bool has[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    col[v] = (v * warps * 32 + g.tid) * 8;
+    has[v] = col[v] < f.hidden;
+  }
   const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + g.index;
   const int t0 = int(min(worker * n.per_worker, int64_t(f.tokens)));
   const int t1 = min(t0 + n.per_worker, f.tokens);
   const float inv = 1.0f / float(f.hidden);
   const auto fetch = [&](int t, int stage) {
-    if (has && t < t1) {
-      const int at = stage * kPieces;
-      ring.fetch(at, static_cast<const A*>(f.x) + t * f.x_stride + col);
-      if (f.pre != nullptr)
-        ring.fetch(at + kA, static_cast<const A*>(a.dy) + t * a.dy_stride + col);
-      if (f.residual != nullptr)
-        ring.fetch(at + 2 * kA, static_cast<const S*>(f.residual) + t * f.residual_stride + col);
-      if (a.dsum != nullptr)
-        ring.fetch(at + 2 * kA + kS, static_cast<const S*>(a.dsum) + t * a.dsum_stride + col);
+    if (t < t1) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (has[v]) {
+          const int at = stage * kPieces + v * kOf;
+          ring.fetch(at, static_cast<const A*>(f.x) + (t * f.x_stride + col[v]));
+          if (f.pre != nullptr)
+            ring.fetch(at + kA, static_cast<const A*>(a.dy) + (t * a.dy_stride + col[v]));
+          if (f.residual != nullptr)
+            ring.fetch(at + 2 * kA,
+                       static_cast<const S*>(f.residual) + (t * f.residual_stride + col[v]));
+          if (a.dsum != nullptr)
+            ring.fetch(at + 2 * kA + kS,
+                       static_cast<const S*>(a.dsum) + (t * a.dsum_stride + col[v]));
+        }
     }
     OwnRing::commit();
   };
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) fetch(t0 + i, i);
-  float w[8], pre[8], dpre[8], dpost[8], sum_g[8];
+  const Pair zero = Pair::of(0.0f);
+  Pair dpre[NV][4], sum_g[NV][4], dpost[GATES ? NV : 1][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pre[i] = dpre[i] = dpost[i] = sum_g[i] = 0.0f;
-  if (has && f.pre != nullptr) load_param<8>(f.pre, col, f.params_f32, pre);
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dpre[v][i] = sum_g[v][i] = dpost[GATES ? v : 0][i] = zero;
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = 0.0f;
+    ring.put(kW + 2 * v, p);
+    if (has[v] && f.pre != nullptr) load_param<8>(f.pre, col[v], f.params_f32, p);
+    ring.put(kPre + 2 * v, p);
+  }
   // the tokens from which on another row of the gate holds
-  int gate_row = -1, gate_end = t0;
+  int gate_row = 0, gate_end = t0;
   int stage = 0;
   float r1 = f.post && t0 < t1 ? f.post_rstd[t0] : 1.0f;
   float r2 = f.pre && t0 < t1 ? f.pre_rstd[t0] : 0.0f;
@@ -206,77 +240,117 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
     if (t >= gate_end) {
       gate_row = f.gate ? int(uint32_t(t) / uint32_t(f.gate_rows)) : 0;
       gate_end = f.gate ? int(min(int64_t(gate_row + 1) * f.gate_rows, int64_t(t1))) : t1;
-      if (has) load_factor(f, col, gate_row * f.gate_stride, w);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (has[v]) {
+          float p[8];
+          load_factor(f, col[v], gate_row * f.gate_stride, p);
+          ring.put(kW + 2 * v, p);
+        }
     }
     OwnRing::wait<DEPTH - 1>();
-    float xn[8], sn[8], dy[8], d[8];
+    // (x and dy are kept as they lie in memory: a bf16 pair in one register, not two)
+    Pack8<A> px[NV], py[NV];
+    Pair sn[NV][4], d[NV][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xn[i] = sn[i] = dy[i] = d[i] = 0.0f;
-    if (has) {
-      const int at = stage * kPieces;
-      ring.get<A>(at, xn);
-      if (f.pre != nullptr) ring.get<A>(at + kA, dy);
-      if (f.residual != nullptr) ring.get<S>(at + 2 * kA, sn);
-      if (a.dsum != nullptr) ring.get<S>(at + 2 * kA + kS, d);
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sn[v][i] = d[v][i] = zero;
+      px[v].zero();
+      py[v].zero();
+      if (has[v]) {
+        const int at = stage * kPieces + v * kOf;
+        ring.get(at, px[v]);
+        if (f.pre != nullptr) ring.get(at + kA, py[v]);
+        if (f.residual != nullptr) ring.get<S>(at + 2 * kA, sn[v]);
+        if (a.dsum != nullptr) ring.get<S>(at + 2 * kA + kS, d[v]);
+      }
     }
     fetch(t + DEPTH, stage);
-    if (++stage == DEPTH) stage = 0;
+    stage = stage + 1 == DEPTH ? 0 : stage + 1;
     const int next = t + 1 < t1 ? t + 1 : t;
     const float next_r1 = f.post ? f.post_rstd[next] : 1.0f;
     const float next_r2 = f.pre ? f.pre_rstd[next] : 0.0f;
-    float sum[3] = {0.0f, 0.0f, 0.0f};
+    Pair sa = zero, sb = zero, sc = zero;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      xn[i] *= r1;
-      const float z = w[i] * xn[i], e = dy[i] * pre[i];
-      sn[i] = (sn[i] + z) * r2;
-      d[i] = fmaf(r2, e, d[i]);
-      sum[0] = fmaf(e, sn[i], sum[0]);
-      sum[1] = fmaf(z, d[i], sum[1]);
-      sum[2] = fmaf(z, sn[i], sum[2]);
+    for (int v = 0; v < NV; ++v) {
+      Pair w[4], pre[4], x[4], dy[4];
+      pairs_of(px[v], x);
+      pairs_of(py[v], dy);
+      ring.get<float>(kW + 2 * v, w);
+      ring.get<float>(kPre + 2 * v, pre);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Pair z = w[i] * (x[i] * Pair::of(r1)), e = dy[i] * pre[i];
+        sn[v][i] = (sn[v][i] + z) * Pair::of(r2);
+        d[v][i] = fma2(Pair::of(r2), e, d[v][i]);
+        sa = fma2(e, sn[v][i], sa);
+        sb = fma2(z, d[v][i], sb);
+        sc = fma2(z, sn[v][i], sc);
+      }
     }
+    float sum[3] = {sa.sum(), sb.sum(), sc.sum()};
     g.sums<3>(sum, buf, turn);
     const float k = r2 * (sum[0] * inv);
     const float m1 = (sum[1] - k * sum[2]) * inv;
-    float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d[i] = fmaf(-k, sn[i], d[i]);
-      dpre[i] = fmaf(dy[i], sn[i], dpre[i]);
-      sum_g[i] = fmaf(xn[i], d[i], sum_g[i]);
-      o[i] = w[i] * d[i];
-      if (f.post != nullptr) o[i] = r1 * fmaf(-m1, xn[i], o[i]);
+    for (int v = 0; v < NV; ++v) {
+      Pair w[4], o[4], x[4], dy[4];
+      pairs_of(px[v], x);
+      pairs_of(py[v], dy);
+      ring.get<float>(kW + 2 * v, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Pair xn = x[i] * Pair::of(r1);
+        d[v][i] = fma2(Pair::of(-k), sn[v][i], d[v][i]);
+        dpre[v][i] = fma2(dy[i], sn[v][i], dpre[v][i]);
+        sum_g[v][i] = fma2(xn, d[v][i], sum_g[v][i]);
+        o[i] = w[i] * d[v][i];
+        if (f.post != nullptr) o[i] = Pair::of(r1) * fma2(Pair::of(-m1), xn, o[i]);
+      }
+      if (!has[v]) continue;
+      if (a.dresidual != nullptr)
+        store8(static_cast<S*>(a.dresidual) + (t * a.dresidual_stride + col[v]), d[v]);
+      store8(static_cast<A*>(a.dx) + (t * a.dx_stride + col[v]), o);
     }
     r1 = next_r1, r2 = next_r2;
-    if (!has) continue;
-    if (a.dresidual != nullptr)
-      store_piece<8>(static_cast<S*>(a.dresidual) + t * a.dresidual_stride + col, d);
-    store_piece<8>(static_cast<A*>(a.dx) + t * a.dx_stride + col, o);
     if (t + 1 < gate_end) continue;
     // the last token with this gate here
-    float p[8], q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = q[i] = f.scale;
-    if (f.post != nullptr) {
-      load_param<8>(f.post, col, f.params_f32, p);
+    for (int v = 0; v < NV; ++v) {
+      if (!has[v]) continue;
+      float p[8], q[8], s[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] *= f.scale;
+      for (int i = 0; i < 4; ++i) sum_g[v][i].get(s[2 * i], s[2 * i + 1]), sum_g[v][i] = zero;
+      if (f.gate != nullptr) {
+        factor_of(f, f.post, col[v], p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] *= s[i];
+        store_gate<8>(a, n, t, worker, col[v], p);
+      }
+      if (f.post == nullptr) continue;
+      factor_of(f, f.gate, gate_row * f.gate_stride + col[v], q);
+      if constexpr (GATES) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dpost[v][i] = fma2(Pair::of(q[2 * i], q[2 * i + 1]), Pair::of(s[2 * i], s[2 * i + 1]),
+                             dpost[v][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] *= s[i];
+        store_piece<8>(n.post_part + worker * f.hidden + col[v], q);
+      }
     }
-    if (f.gate != nullptr) {
-      load_param<8>(f.gate, gate_row * f.gate_stride + col, f.params_f32, q);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] *= f.scale;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] *= sum_g[i];
-      dpost[i] = fmaf(q[i], sum_g[i], dpost[i]);
-      sum_g[i] = 0.0f;
-    }
-    if (f.gate != nullptr) store_gate<8>(a, n, t, worker, col, p);
   }
   OwnRing::wait<0>();
-  if (t0 < t1 && has) store_parts<8>(a, n, worker, col, dpre, dpost);
+  if (t0 >= t1) return;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (!has[v]) continue;
+    if (f.pre != nullptr) store8(n.pre_part + worker * f.hidden + col[v], dpre[v]);
+    if (GATES && f.post != nullptr)
+      store8(n.post_part + worker * f.hidden + col[v], dpost[GATES ? v : 0]);
+  }
 }
 
 // Any rows, first: the two means of each token, by a CTA.
@@ -372,28 +446,31 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormBackArgs a, co
     static_cast<uint16_t*>(to)[at + col] = narrow<uint16_t>(sum);
 }
 
-// Workers of at least as many as are asked for, where there are the tokens.
+// Workers of at most as many as are asked for, where there are the tokens.
 void share_out(BackShape* n, int64_t tokens, int64_t most) {
   n->per_worker = int32_t((tokens + most - 1) / most);
   n->workers = int32_t((tokens + n->per_worker - 1) / n->per_worker);
 }
 
-// The most workers: a row of threads each, or the CTAs along the tokens.
+// The most workers: a row of threads each, of two CTAs per SM, or the CTAs along the
+// tokens.
 int64_t whole_workers(int64_t hidden, int sms) {
-  return int64_t(sms) * rows_of_cta(int((hidden + 255) / 256), 16);
+  const RowShape s = row_shape(int(hidden));
+  return int64_t(sms) * s.rows * (s.threads <= 256 ? 2 : 1);
 }
 int64_t column_workers(int64_t hidden, int width, int sms) {
   const int64_t pieces = (hidden + 256 * width - 1) / (256 * width);
   return (int64_t(sms) * 4 + pieces - 1) / pieces;
 }
 
-template <typename A, typename S, int DEPTH>
-fo_status launch_ring(const NormBackArgs& a, const BackShape& n, int warps, int rows,
-                      int row_bytes, cudaStream_t st) {
-  const fo_status q = allow_smem<norm_backward_kernel<A, S, DEPTH>>();
+template <typename A, typename S, int NV, int DEPTH, bool GATES>
+fo_status launch_ring(const NormBackArgs& a, const BackShape& n, const RowShape& s, int row_bytes,
+                      cudaStream_t st) {
+  constexpr auto kernel = norm_backward_kernel<A, S, NV, DEPTH, GATES>;
+  const fo_status q = allow_smem<kernel>();
   if (q != FO_OK) return q;
-  norm_backward_kernel<A, S, DEPTH><<<unsigned((n.workers + rows - 1) / rows), rows * warps * 32,
-                                      DEPTH * row_bytes, st>>>(a, n, warps);
+  const int smem = DEPTH * row_bytes + s.threads * NV * 64;
+  kernel<<<unsigned((n.workers + s.rows - 1) / s.rows), s.threads, smem, st>>>(a, n, s.warps);
   return FO_OK;
 }
 
@@ -402,7 +479,10 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
                  cudaStream_t st) {
   const NormArgs& f = a.f;
   const int64_t H = f.hidden;
-  const bool whole = vec && H <= 4096;
+  const RowShape s = row_shape(H <= 8192 ? int(H) : 0);
+  const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S));
+  const int params = s.threads * s.nv * 64;
+  const bool whole = vec && H <= 8192 && 2 * row + params <= kNormSmem;
   if (whole) {
     share_out(n, f.tokens, whole_workers(H, sms));
   } else {
@@ -414,10 +494,17 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   n->post_part = n->pre_part + n->workers * H;
   n->gate_part = n->post_part + n->workers * H;
   if (whole) {
-    const int warps = int((H + 255) / 256), rows = rows_of_cta(warps, 16);
-    const int row = rows * warps * 32 * 16 * int(sizeof(A) + sizeof(S));
-    return 4 * row <= kNormSmem ? launch_ring<A, S, 4>(a, *n, warps, rows, row, st)
-                                : launch_ring<A, S, 2>(a, *n, warps, rows, row, st);
+    const bool gates = f.gate != nullptr && f.gate_rows < f.tokens;
+    // three rows under way where two CTAs of 256 threads, or one of more, fit so, else two
+    const bool deep = 3 * row + params <= (s.threads <= 256 ? kNormSmem / 2 : kNormSmem);
+    if (s.nv == 1)
+      return gates ? launch_ring<A, S, 1, 3, true>(a, *n, s, row, st)
+                   : launch_ring<A, S, 1, 3, false>(a, *n, s, row, st);
+    if (deep)
+      return gates ? launch_ring<A, S, 2, 3, true>(a, *n, s, row, st)
+                   : launch_ring<A, S, 2, 3, false>(a, *n, s, row, st);
+    return gates ? launch_ring<A, S, 2, 2, true>(a, *n, s, row, st)
+                 : launch_ring<A, S, 2, 2, false>(a, *n, s, row, st);
   }
   if (vec) {
     const int pieces = int((H + 2047) / 2048);
@@ -436,7 +523,7 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
 // Both means of every token, and the workers' parts.
 int64_t block_norm_workspace_bytes(int64_t tokens, int64_t hidden, int64_t gates) {
   int64_t workers = column_workers(hidden, 8, kMaxSms);
-  if (hidden <= 4096 && workers < whole_workers(hidden, kMaxSms))
+  if (hidden <= 8192 && workers < whole_workers(hidden, kMaxSms))
     workers = whole_workers(hidden, kMaxSms);
   if (workers > tokens) workers = tokens;
   const int64_t gate_parts = gates > 0 && gates < tokens ? workers + gates : 0;

@@ -194,3 +194,8 @@ def test_norm_of_nothing_and_of_too_much():
     desc = fo.make_norm_desc(**NORM_DESC)
     assert fo.fo_block_norm_workspace(desc) > 0
     refused(ARG, fo.fo_block_norm_workspace, fo.make_norm_desc(**{**NORM_DESC, "gates": 3}))
+    # any size, none among them: the parts of as many workers as there may be
+    for hidden in (0, 1, 255, 256, 257, 2752, 8192, 8193, 100000):
+        desc = fo.make_norm_desc(**{**NORM_DESC, "tokens": 1 << 20, "hidden": hidden})
+        assert fo.fo_block_norm_workspace(desc) >= 8 << 20
+    fo.fo_block_norm_backward(*norm_args(NORM_BACK, dict(hidden=0)))
