@@ -248,7 +248,9 @@ fo_status launch_ring(const NormArgs& a, const RowShape& s, int row_bytes, cudaS
 template <typename A, typename S>
 fo_status launch(const NormArgs& a, bool vec, cudaStream_t st) {
   if (vec && a.hidden <= 8192) {
-    const RowShape s = row_shape(a.hidden);
+    // two times eight columns per thread where a row has more than 256 (half the threads
+    // to meet at its sums, half the addresses), and CTAs of 256 threads where that does
+    const RowShape s = row_shape(a.hidden, a.hidden <= 256 ? 1 : 2, 8);
     // four rows under way where two CTAs of 256 threads, or one of more, fit so, else two
     const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S)) / 2;
     const bool deep = 4 * row <= (s.threads <= 256 ? kNormSmem / 2 : kNormSmem);

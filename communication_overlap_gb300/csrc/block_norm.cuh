@@ -51,6 +51,11 @@ __device__ __forceinline__ void pairs_of(const Pack8<T>& p, Pair (&x)[4]) {
   for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
 }
 
+__device__ __forceinline__ void pairs_of(const float (&v)[8], Pair (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
+}
+
 // Eight elements as four pairs, to 16 bytes of memory.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
@@ -141,43 +146,72 @@ struct RowGroup {
     const int index = int(threadIdx.x >> 5) / warps;
     return {warps, index, int(threadIdx.x) - index * warps * 32};
   }
-  // cta_sums over the row.  buf: [2][N][32] floats of zeros: a row's warps take
-  // slots from a multiple of four on, and are read by four.
+  // cta_sums over the row, of up to 16 warps.  buf, zeros at first: of one value [2][32]
+  // (a row's warps take slots from a multiple of four on), of three [2][8 rows][3][16].
   template <int N>
   __device__ __forceinline__ void sums(float (&v)[N], float* buf, int& turn) const {
+    const int lane = tid & 31;
+    if constexpr (N == 3) {
+      // the lanes share the values out on the first two steps: the four quarters of the
+      // warp, by their lanes' bits 4 and 3, then add up v0, v1, v2 and nothing
+      const bool hi = lane & 16, odd = lane & 8;
+      const float give = hi ? v[0] : v[2], keep = hi ? v[2] : v[0];
+      const float a = keep + __shfl_xor_sync(0xffffffffu, give, 16);          // v0 or v2
+      const float give1 = hi ? v[1] : 0.0f, keep1 = hi ? 0.0f : v[1];
+      const float b = keep1 + __shfl_xor_sync(0xffffffffu, give1, 16);        // v1 or 0
+      float s = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (warps == 1) return;
-    float* at = buf + turn * N * 32 + index * ((warps + 3) & ~3);
-    turn ^= 1;
-    if ((tid & 31) == 0) {
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (warps == 1) {
+        v[0] = __shfl_sync(0xffffffffu, s, 0);
+        v[1] = __shfl_sync(0xffffffffu, s, 8);
+        v[2] = __shfl_sync(0xffffffffu, s, 16);
+        return;
+      }
+      // value i of warp w at i * 16 + w
+      float* at = buf + (turn * 8 + index) * 3 * 16;
+      turn ^= 1;
+      if ((lane & 7) == 0 && lane < 24) at[(lane >> 3) * 16 + (tid >> 5)] = s;
+      meet();
+      // a quarter of the warp adds a value's sums, two warps' to a lane
+      const float2 p = *reinterpret_cast<const float2*>(at + min(lane >> 3, 2) * 16 + (lane & 7) * 2);
+      s = p.x + p.y;
 #pragma unroll
-      for (int i = 0; i < N; ++i) at[i * 32 + (tid >> 5)] = v[i];
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      v[0] = __shfl_sync(0xffffffffu, s, 0);
+      v[1] = __shfl_sync(0xffffffffu, s, 8);
+      v[2] = __shfl_sync(0xffffffffu, s, 16);
+    } else {
+      static_assert(N == 1, "one value or three");
+      v[0] = warp_sum(v[0]);
+      if (warps == 1) return;
+      float* at = buf + turn * 32 + index * ((warps + 3) & ~3);
+      turn ^= 1;
+      if (lane == 0) at[tid >> 5] = v[0];
+      meet();
       float sum = 0.0f;
       for (int w = 0; w < warps; w += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(at + i * 32 + w);
+        const float4 f = *reinterpret_cast<const float4*>(at + w);
         sum += (f.x + f.y) + (f.z + f.w);
       }
-      v[i] = sum;
+      v[0] = sum;
     }
+  }
+  __device__ __forceinline__ void meet() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
   }
 };
 
-// How rows of up to 8192 columns lie over threads: NV times eight columns per thread
-// (two where a row has more than 256: half the threads to meet at its sums, and half
-// the addresses), and CTAs of 256 threads where a row needs no more.
+// How rows lie over threads: NV times eight columns per thread, and several rows to a
+// CTA where one has few warps.
 struct RowShape {
   int nv, warps, rows, threads;
 };
-inline RowShape row_shape(int hidden) {
+inline RowShape row_shape(int64_t hidden, int nv, int cta_warps) {
   RowShape s;
-  s.nv = hidden <= 256 ? 1 : 2;
-  s.warps = hidden > 0 ? (hidden + 256 * s.nv - 1) / (256 * s.nv) : 1;
-  s.rows = s.warps <= 8 ? 8 / s.warps : 1;
+  s.nv = nv;
+  s.warps = hidden > 0 ? int((hidden + 256 * nv - 1) / (256 * nv)) : 1;
+  s.rows = s.warps <= cta_warps ? cta_warps / s.warps : 1;
   s.threads = s.rows * s.warps * 32;
   return s;
 }

@@ -175,12 +175,14 @@ template <typename A, typename S, int NV, int DEPTH, bool GATES>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArgs a,
                                                                const BackShape n, int warps) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float buf[2 * 3 * 32];
+  __shared__ __align__(16) float buf[2 * 8 * 48];           // of up to eight rows
   constexpr int kA = sizeof(A) / 2, kS = sizeof(S) / 2;     // pieces of eight columns
   constexpr int kOf = 2 * (kA + kS);                        // x, dy, residual, dsum
   constexpr int kPieces = NV * kOf;
-  constexpr int kW = DEPTH * kPieces, kPre = kW + 2 * NV;   // the parameters' pieces
-  for (int i = threadIdx.x; i < 192; i += blockDim.x) buf[i] = 0.0f;
+  // the parameters: in registers, or of two times eight columns in pieces of their own
+  constexpr bool kKeep = NV == 1;
+  constexpr int kW = DEPTH * kPieces, kPre = kW + 2 * NV;
+  for (int i = threadIdx.x; i < 2 * 8 * 48; i += blockDim.x) buf[i] = 0.0f;
   __syncthreads();
   int turn = 0;
   const NormArgs& f = a.f;
@@ -190,35 +192,64 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
   bool has[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
+    // (threads without columns work on the row's first ones with parameters of zero,
+    // and store nothing)
     col[v] = (v * warps * 32 + g.tid) * 8;
     has[v] = col[v] < f.hidden;
+    if (!has[v]) col[v] = 0;
   }
   const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + g.index;
   const int t0 = int(min(worker * n.per_worker, int64_t(f.tokens)));
   const int t1 = min(t0 + n.per_worker, f.tokens);
   const float inv = 1.0f / float(f.hidden);
-  const auto fetch = [&](int t, int stage) {
-    if (t < t1) {
+  const A* x_at = static_cast<const A*>(f.x) + t0 * f.x_stride;
+  const A* dy_at = static_cast<const A*>(a.dy) + t0 * a.dy_stride;
+  const S* r_at = static_cast<const S*>(f.residual) + t0 * f.residual_stride;
+  const S* d_at = static_cast<const S*>(a.dsum) + t0 * a.dsum_stride;
+  int fetched = t0;
+  // (what is not given stays the zeros that the ring starts with)
+  const auto fetch = [&](int stage) {
+    if (fetched < t1) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (has[v]) {
-          const int at = stage * kPieces + v * kOf;
-          ring.fetch(at, static_cast<const A*>(f.x) + (t * f.x_stride + col[v]));
-          if (f.pre != nullptr)
-            ring.fetch(at + kA, static_cast<const A*>(a.dy) + (t * a.dy_stride + col[v]));
-          if (f.residual != nullptr)
-            ring.fetch(at + 2 * kA,
-                       static_cast<const S*>(f.residual) + (t * f.residual_stride + col[v]));
-          if (a.dsum != nullptr)
-            ring.fetch(at + 2 * kA + kS,
-                       static_cast<const S*>(a.dsum) + (t * a.dsum_stride + col[v]));
-        }
+      for (int v = 0; v < NV; ++v) {
+        const int at = stage * kPieces + v * kOf;
+        ring.fetch(at, x_at + col[v]);
+        if (f.pre != nullptr) ring.fetch(at + kA, dy_at + col[v]);
+        if (f.residual != nullptr) ring.fetch(at + 2 * kA, r_at + col[v]);
+        if (a.dsum != nullptr) ring.fetch(at + 2 * kA + kS, d_at + col[v]);
+      }
     }
     OwnRing::commit();
+    ++fetched;
+    x_at += f.x_stride;
+    dy_at += a.dy_stride;
+    r_at += f.residual_stride;
+    d_at += a.dsum_stride;
   };
+  {
+    const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < DEPTH; ++i) fetch(t0 + i, i);
+    for (int i = 0; i < DEPTH * kPieces; i += 2) ring.put(i, none);
+  }
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) fetch(i);
   const Pair zero = Pair::of(0.0f);
+  Pair kept_w[4], kept_pre[4];
+  const auto set_w = [&](int v, const float (&p)[8]) {
+    if constexpr (kKeep)
+      pairs_of(p, kept_w);
+    else
+      ring.put(kW + 2 * v, p);
+  };
+  const auto get_params = [&](int v, Pair (&w)[4], Pair (&pre)[4]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = kept_w[i], pre[i] = kept_pre[i];
+    } else {
+      ring.get<float>(kW + 2 * v, w);
+      ring.get<float>(kPre + 2 * v, pre);
+    }
+  };
   Pair dpre[NV][4], sum_g[NV][4], dpost[GATES ? NV : 1][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -227,9 +258,12 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = 0.0f;
-    ring.put(kW + 2 * v, p);
+    set_w(v, p);
     if (has[v] && f.pre != nullptr) load_param<8>(f.pre, col[v], f.params_f32, p);
-    ring.put(kPre + 2 * v, p);
+    if constexpr (kKeep)
+      pairs_of(p, kept_pre);
+    else
+      ring.put(kPre + 2 * v, p);
   }
   // the tokens from which on another row of the gate holds
   int gate_row = 0, gate_end = t0;
@@ -245,7 +279,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
         if (has[v]) {
           float p[8];
           load_factor(f, col[v], gate_row * f.gate_stride, p);
-          ring.put(kW + 2 * v, p);
+          set_w(v, p);
         }
     }
     OwnRing::wait<DEPTH - 1>();
@@ -254,19 +288,13 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     Pair sn[NV][4], d[NV][4];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sn[v][i] = d[v][i] = zero;
-      px[v].zero();
-      py[v].zero();
-      if (has[v]) {
-        const int at = stage * kPieces + v * kOf;
-        ring.get(at, px[v]);
-        if (f.pre != nullptr) ring.get(at + kA, py[v]);
-        if (f.residual != nullptr) ring.get<S>(at + 2 * kA, sn[v]);
-        if (a.dsum != nullptr) ring.get<S>(at + 2 * kA + kS, d[v]);
-      }
+      const int at = stage * kPieces + v * kOf;
+      ring.get(at, px[v]);
+      ring.get(at + kA, py[v]);
+      ring.get<S>(at + 2 * kA, sn[v]);
+      ring.get<S>(at + 2 * kA + kS, d[v]);
     }
-    fetch(t + DEPTH, stage);
+    fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     const int next = t + 1 < t1 ? t + 1 : t;
     const float next_r1 = f.post ? f.post_rstd[next] : 1.0f;
@@ -277,8 +305,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
       Pair w[4], pre[4], x[4], dy[4];
       pairs_of(px[v], x);
       pairs_of(py[v], dy);
-      ring.get<float>(kW + 2 * v, w);
-      ring.get<float>(kPre + 2 * v, pre);
+      get_params(v, w, pre);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Pair z = w[i] * (x[i] * Pair::of(r1)), e = dy[i] * pre[i];
@@ -295,10 +322,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     const float m1 = (sum[1] - k * sum[2]) * inv;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      Pair w[4], o[4], x[4], dy[4];
+      Pair w[4], pre[4], o[4], x[4], dy[4];
       pairs_of(px[v], x);
       pairs_of(py[v], dy);
-      ring.get<float>(kW + 2 * v, w);
+      get_params(v, w, pre);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Pair xn = x[i] * Pair::of(r1);
@@ -452,12 +479,13 @@ void share_out(BackShape* n, int64_t tokens, int64_t most) {
   n->workers = int32_t((tokens + n->per_worker - 1) / n->per_worker);
 }
 
-// The most workers: a row of threads each, of two CTAs per SM, or the CTAs along the
-// tokens.
-int64_t whole_workers(int64_t hidden, int sms) {
-  const RowShape s = row_shape(int(hidden));
-  return int64_t(sms) * s.rows * (s.threads <= 256 ? 2 : 1);
-}
+// Rows of one kernel: eight columns per thread up to 4096, and CTAs of 512 threads
+// (with twice as many per thread the accumulators spill, and fewer rows are under way:
+// 181 us).
+RowShape whole_shape(int64_t hidden) { return row_shape(hidden, hidden <= 4096 ? 1 : 2, 16); }
+
+// The most workers: a row of threads each, or the CTAs along the tokens.
+int64_t whole_workers(int64_t hidden, int sms) { return int64_t(sms) * whole_shape(hidden).rows; }
 int64_t column_workers(int64_t hidden, int width, int sms) {
   const int64_t pieces = (hidden + 256 * width - 1) / (256 * width);
   return (int64_t(sms) * 4 + pieces - 1) / pieces;
@@ -469,7 +497,7 @@ fo_status launch_ring(const NormBackArgs& a, const BackShape& n, const RowShape&
   constexpr auto kernel = norm_backward_kernel<A, S, NV, DEPTH, GATES>;
   const fo_status q = allow_smem<kernel>();
   if (q != FO_OK) return q;
-  const int smem = DEPTH * row_bytes + s.threads * NV * 64;
+  const int smem = DEPTH * row_bytes + (NV == 1 ? 0 : s.threads * NV * 64);
   kernel<<<unsigned((n.workers + s.rows - 1) / s.rows), s.threads, smem, st>>>(a, n, s.warps);
   return FO_OK;
 }
@@ -479,9 +507,9 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
                  cudaStream_t st) {
   const NormArgs& f = a.f;
   const int64_t H = f.hidden;
-  const RowShape s = row_shape(H <= 8192 ? int(H) : 0);
+  const RowShape s = whole_shape(H <= 8192 ? H : 0);
   const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S));
-  const int params = s.threads * s.nv * 64;
+  const int params = s.nv == 1 ? 0 : s.threads * s.nv * 64;
   const bool whole = vec && H <= 8192 && 2 * row + params <= kNormSmem;
   if (whole) {
     share_out(n, f.tokens, whole_workers(H, sms));
@@ -495,14 +523,13 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   n->gate_part = n->post_part + n->workers * H;
   if (whole) {
     const bool gates = f.gate != nullptr && f.gate_rows < f.tokens;
-    // three rows under way where two CTAs of 256 threads, or one of more, fit so, else two
-    const bool deep = 3 * row + params <= (s.threads <= 256 ? kNormSmem / 2 : kNormSmem);
+    // four rows under way where they fit
+    if (s.nv == 1 && 4 * row <= kNormSmem)
+      return gates ? launch_ring<A, S, 1, 4, true>(a, *n, s, row, st)
+                   : launch_ring<A, S, 1, 4, false>(a, *n, s, row, st);
     if (s.nv == 1)
-      return gates ? launch_ring<A, S, 1, 3, true>(a, *n, s, row, st)
-                   : launch_ring<A, S, 1, 3, false>(a, *n, s, row, st);
-    if (deep)
-      return gates ? launch_ring<A, S, 2, 3, true>(a, *n, s, row, st)
-                   : launch_ring<A, S, 2, 3, false>(a, *n, s, row, st);
+      return gates ? launch_ring<A, S, 1, 2, true>(a, *n, s, row, st)
+                   : launch_ring<A, S, 1, 2, false>(a, *n, s, row, st);
     return gates ? launch_ring<A, S, 2, 2, true>(a, *n, s, row, st)
                  : launch_ring<A, S, 2, 2, false>(a, *n, s, row, st);
   }
