@@ -7,8 +7,6 @@
 // outputs are rounded once.
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "block_common.cuh"
 
 namespace fo {
@@ -150,140 +148,228 @@ struct CombineBackArgs {
   int32_t warps;            // of a token: 1, 2, 4 or 8
 };
 
-// A token per group of warps, SLOTS of its slots at a time: dy, the rows, their
-// products and the rows' gradients, CHUNKS times W columns per thread under way; then
-// the products' sums over the group.  CTAs walk over the tokens; the rows of the next
-// token are looked up, and checked against row_token, two tokens and one ahead.
-template <typename T, typename O, int W, int SLOTS, int CHUNKS>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const CombineBackArgs a) {
-  __shared__ float part[2][kThreads / 32][SLOTS];
-  const CombineArgs& f = a.f;
+// The rows that hold no token become zeros: 32 of them looked at by a warp.
+template <typename T, int W>
+__device__ __forceinline__ void zero_empty_rows(const CombineBackArgs& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int group = warp / a.warps, in_group = warp % a.warps;
-  const int per = (kThreads / 32) / a.warps;           // tokens of a CTA
-  const int64_t step = int64_t(gridDim.x) * per;
-  const T* rows = static_cast<const T*>(f.rows);
-  T* drows = static_cast<T*>(a.drows);
-  int turn = 0;
-  // the first slots of a token: its rows, and the tokens that those name
-  const auto look_up = [&](int64_t t, int s0, int32_t (&r)[SLOTS], float (&w)[SLOTS]) {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-      const bool has = t < f.tokens && s0 + j < f.top_k;
-      r[j] = has ? __ldg(f.token_row + t * f.top_k + s0 + j) : -1;
-      w[j] = has && f.weights ? __ldg(f.weights + t * f.top_k + s0 + j) : 1.0f;
-    }
-  };
-  const auto named = [&](const int32_t (&r)[SLOTS], int32_t (&by)[SLOTS]) {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j)
-      by[j] = r[j] >= 0 && r[j] < f.table_rows ? __ldg(a.row_token + r[j]) : -1;
-  };
-  const int64_t first = int64_t(blockIdx.x) * per + group;
-  int32_t r[SLOTS], by[SLOTS], next_r[SLOTS];
-  float w[SLOTS], next_w[SLOTS];
-  look_up(first, 0, r, w);
-  named(r, by);
-  look_up(first + step, 0, next_r, next_w);
-  // (as many rounds for all of the CTA's groups: they meet at the sums)
-  for (int64_t base = int64_t(blockIdx.x) * per; base < f.tokens; base += step) {
-    const int64_t t = base + group;
-    const bool live = t < f.tokens;
-    const O* dy = static_cast<const O*>(a.dy) + t * a.dy_stride;
-    int32_t next_by[SLOTS], then_r[SLOTS];
-    float then_w[SLOTS];
-    named(next_r, next_by);
-    look_up(t + 2 * step, 0, then_r, then_w);
-    for (int s0 = 0; s0 < f.top_k; s0 += SLOTS) {
-      if (s0 > 0) {
-        look_up(t, s0, r, w);
-        named(r, by);
-      }
-      float dot[SLOTS];
-#pragma unroll
-      for (int j = 0; j < SLOTS; ++j) {
-        dot[j] = 0.0f;
-        // (a row outside the table, or one that holds another token, is not this one's)
-        if (live && r[j] >= 0 && by[j] != int32_t(t)) {
-          atomicCAS(f.status, 0, int32_t(FO_ERR_ARG));
-          r[j] = -1;
-        }
-      }
-      const int stride = a.warps * 32 * W;
-      if (live)
-        for (int c0 = (in_group * 32 + lane) * W; c0 < f.hidden; c0 += CHUNKS * stride) {
-          Columns<O, W> g[CHUNKS];
-          Columns<T, W> v[CHUNKS][SLOTS];
-#pragma unroll
-          for (int k = 0; k < CHUNKS; ++k) {
-            const int c = c0 + k * stride;
-            if (c >= f.hidden) continue;
-            if (f.top_k > SLOTS)
-              g[k].load(dy + c);
-            else
-              g[k].load_once(dy + c);
-            if (a.dweights) {
-#pragma unroll
-              for (int j = 0; j < SLOTS; ++j)
-                if (r[j] >= 0) v[k][j].load_once(rows + r[j] * f.row_stride + c);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < CHUNKS; ++k) {
-            const int c = c0 + k * stride;
-            if (c >= f.hidden) continue;
-            float x[W];
-            g[k].get(x);
-#pragma unroll
-            for (int j = 0; j < SLOTS; ++j)
-              if (r[j] >= 0) {
-                float y[W];
-                if (a.dweights) {
-                  v[k][j].get(y);
-#pragma unroll
-                  for (int i = 0; i < W; ++i) dot[j] = fmaf(x[i], y[i], dot[j]);
-                }
-#pragma unroll
-                for (int i = 0; i < W; ++i) y[i] = w[j] * x[i];
-                Columns<T, W>::store(drows + r[j] * a.drows_stride + c, y);
-              }
-          }
-        }
-      if (!a.dweights) continue;
-#pragma unroll
-      for (int j = 0; j < SLOTS; ++j) dot[j] = warp_sum(dot[j]);
-      if (lane == 0) {
-#pragma unroll
-        for (int j = 0; j < SLOTS; ++j) part[turn][warp][j] = dot[j];
-      }
-      __syncthreads();
-      if (in_group == 0 && lane < SLOTS && live && s0 + lane < f.top_k) {
-        float sum = 0.0f;
-        for (int i = 0; i < a.warps; ++i) sum += part[turn][warp + i][lane];
-        a.dweights[t * f.top_k + s0 + lane] = sum;
-      }
-      turn ^= 1;
-    }
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-      r[j] = next_r[j], w[j] = next_w[j], by[j] = next_by[j];
-      next_r[j] = then_r[j], next_w[j] = then_w[j];
-    }
-  }
-  // the rows that hold no token become zeros: 32 of them looked at by a warp
-  const int64_t looks = (f.table_rows + 31) / 32;
+  const int64_t looks = (a.f.table_rows + 31) / 32;
   for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + warp; i < looks;
        i += int64_t(gridDim.x) * (kThreads / 32)) {
     const int64_t row = i * 32 + lane;
-    uint32_t todo = __ballot_sync(0xffffffffu, row < f.table_rows && __ldg(a.row_token + row) < 0);
+    uint32_t todo =
+        __ballot_sync(0xffffffffu, row < a.f.table_rows && __ldg(a.row_token + row) < 0);
     for (; todo; todo &= todo - 1) {
-      T* at = drows + (i * 32 + __ffs(todo) - 1) * a.drows_stride;
+      T* at = static_cast<T*>(a.drows) + (i * 32 + __ffs(todo) - 1) * a.drows_stride;
       float zero[W];
 #pragma unroll
       for (int k = 0; k < W; ++k) zero[k] = 0.0f;
-      for (int c = lane * W; c < f.hidden; c += 32 * W) Columns<T, W>::store(at + c, zero);
+      for (int c = lane * W; c < a.f.hidden; c += 32 * W) Columns<T, W>::store(at + c, zero);
     }
   }
+}
+
+// Some of a token's slots on their way: their rows, then the tokens that those name.
+template <int SLOTS>
+struct Slots {
+  int64_t t;
+  int s0;
+  int32_t r[SLOTS], by[SLOTS];
+  float w[SLOTS];
+
+  // Slots number `i` of a group of warps: `of` of them to a token.
+  __device__ __forceinline__ void look_up(const CombineBackArgs& a, int64_t first, int64_t step,
+                                          int64_t i, int of) {
+    t = first + i / of * step;
+    s0 = int(i % of) * SLOTS;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      const bool has = t < a.f.tokens && s0 + j < a.f.top_k;
+      r[j] = has ? __ldg(a.f.token_row + t * a.f.top_k + s0 + j) : -1;
+      w[j] = has && a.f.weights ? __ldg(a.f.weights + t * a.f.top_k + s0 + j) : 1.0f;
+    }
+  }
+  __device__ __forceinline__ void name(const CombineBackArgs& a) {
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+      by[j] = r[j] >= 0 && r[j] < a.f.table_rows ? __ldg(a.row_token + r[j]) : -1;
+  }
+  // A row outside the table, or one that holds another token, is not this one's.
+  __device__ __forceinline__ void check(const CombineBackArgs& a) {
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+      if (r[j] >= 0 && by[j] != int32_t(t)) {
+        atomicCAS(a.f.status, 0, int32_t(FO_ERR_ARG));
+        r[j] = -1;
+      }
+  }
+};
+
+// The sums of SLOTS products over a token's warps.  part: [2][warps][SLOTS].
+template <int SLOTS>
+__device__ __forceinline__ void store_dots(const CombineBackArgs& a, float (&dot)[SLOTS],
+                                           float (*part)[kThreads / 32][SLOTS], int& turn,
+                                           int64_t t, int s0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < SLOTS; ++j) dot[j] = warp_sum(dot[j]);
+  if (lane == 0) {
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) part[turn][warp][j] = dot[j];
+  }
+  __syncthreads();
+  if (warp % a.warps == 0 && lane < SLOTS && t < a.f.tokens && s0 + lane < a.f.top_k) {
+    float sum = 0.0f;
+    for (int i = 0; i < a.warps; ++i) sum += part[turn][warp + i][lane];
+    a.dweights[t * a.f.top_k + s0 + lane] = sum;
+  }
+  turn ^= 1;
+}
+
+// Rows on 16 bytes.  A token belongs to a group of warps, SLOTS of its slots are taken
+// at a time, and CHUNKS times eight columns per thread: a round of dy, the rows, their
+// products and the rows' gradients.  CTAs walk over the tokens.  While a round is
+// worked on, the next one's data are on their way into the ring, its rows have been
+// checked against row_token, and those of the slots behind it are being looked up:
+// three waits in a row otherwise (161 us for 16384 x 4096, top 2; with look-ups alone
+// ahead 136).
+template <typename T, typename O, int SLOTS, int CHUNKS>
+__global__ void __launch_bounds__(kThreads, 3) combine_backward_kernel(const CombineBackArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][kThreads / 32][SLOTS];
+  constexpr int kT = sizeof(T) / 2, kO = sizeof(O) / 2;     // pieces of eight columns
+  constexpr int kOf = kO + SLOTS * kT, kPieces = CHUNKS * kOf;
+  const CombineArgs& f = a.f;
+  const OwnRing ring(smem);
+  const int warp = threadIdx.x >> 5;
+  const int per = (kThreads / 32) / a.warps;           // tokens of a CTA
+  const int64_t step = int64_t(gridDim.x) * per;
+  const int64_t first = int64_t(blockIdx.x) * per + warp / a.warps;
+  const int col0 = ((warp % a.warps) * 32 + int(threadIdx.x & 31)) * 8;
+  const int stride = a.warps * 32 * 8;                 // from one of a thread's columns to the next
+  const int of = (f.top_k + SLOTS - 1) / SLOTS;
+  const auto fetch = [&](const Slots<SLOTS>& q, int c0, int stage) {
+    if (q.t < f.tokens) {
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k) {
+        const int c = c0 + k * stride, at = stage * kPieces + k * kOf;
+        if (c >= f.hidden) continue;
+        ring.fetch(at, static_cast<const O*>(a.dy) + (q.t * a.dy_stride + c));
+        if (a.dweights == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+          if (q.r[j] >= 0)
+            ring.fetch(at + kO + j * kT,
+                       static_cast<const T*>(f.rows) + (q.r[j] * f.row_stride + c));
+      }
+    }
+    OwnRing::commit();
+  };
+  int turn = 0, stage = 0;
+  Slots<SLOTS> now, next;
+  now.look_up(a, first, step, 0, of);
+  now.name(a);
+  now.check(a);
+  fetch(now, col0, 0);
+  next.look_up(a, first, step, 1, of);
+  next.name(a);
+  // (as many rounds for all of the CTA's groups: they meet at the sums)
+  const int64_t steps = (f.tokens - int64_t(blockIdx.x) * per + step - 1) / step;
+  for (int64_t i = 0; i < steps * of; ++i) {
+    Slots<SLOTS> then;
+    then.look_up(a, first, step, i + 2, of);
+    next.check(a);
+    float dot[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) dot[j] = 0.0f;
+    for (int c0 = 0; c0 < f.hidden; c0 += CHUNKS * stride) {
+      if (c0 + CHUNKS * stride < f.hidden)
+        fetch(now, col0 + c0 + CHUNKS * stride, stage ^ 1);
+      else
+        fetch(next, col0, stage ^ 1);
+      OwnRing::wait<1>();
+      if (now.t < f.tokens) {
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+          const int c = col0 + c0 + k * stride, at = stage * kPieces + k * kOf;
+          if (c >= f.hidden) continue;
+          Pack8<O> g;
+          float x[8];
+          ring.get(at, g);
+          g.get(x);
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j)
+            if (now.r[j] >= 0) {
+              float y[8];
+              if (a.dweights) {
+                Pack8<T> v;
+                ring.get(at + kO + j * kT, v);
+                v.get(y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dot[j] = fmaf(x[e], y[e], dot[j]);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = now.w[j] * x[e];
+              store8(static_cast<T*>(a.drows) + (now.r[j] * a.drows_stride + c), y);
+            }
+        }
+      }
+      stage ^= 1;
+    }
+    if (a.dweights) store_dots<SLOTS>(a, dot, part, turn, now.t, now.s0);
+    now = next;
+    next = then;
+    next.name(a);
+  }
+  OwnRing::wait<0>();
+  zero_empty_rows<T, 8>(a);
+}
+
+// Any rows: a column per thread at a time, without the ring.
+template <typename T, typename O, int SLOTS>
+__global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const CombineBackArgs a) {
+  __shared__ float part[2][kThreads / 32][SLOTS];
+  const CombineArgs& f = a.f;
+  const int warp = threadIdx.x >> 5;
+  const int per = (kThreads / 32) / a.warps;
+  const int64_t step = int64_t(gridDim.x) * per;
+  const int64_t first = int64_t(blockIdx.x) * per + warp / a.warps;
+  const int of = (f.top_k + SLOTS - 1) / SLOTS;
+  int turn = 0;
+  Slots<SLOTS> now, next;
+  now.look_up(a, first, step, 0, of);
+  now.name(a);
+  next.look_up(a, first, step, 1, of);
+  const int64_t steps = (f.tokens - int64_t(blockIdx.x) * per + step - 1) / step;
+  for (int64_t i = 0; i < steps * of; ++i) {
+    next.name(a);
+    Slots<SLOTS> then;
+    then.look_up(a, first, step, i + 2, of);
+    now.check(a);
+    float dot[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) dot[j] = 0.0f;
+    if (now.t < f.tokens) {
+      const O* dy = static_cast<const O*>(a.dy) + now.t * a.dy_stride;
+#pragma unroll 4
+      for (int c = (warp % a.warps) * 32 + int(threadIdx.x & 31); c < f.hidden; c += a.warps * 32) {
+        const float x = widen(__ldg(dy + c));
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+          if (now.r[j] >= 0) {
+            if (a.dweights)
+              dot[j] = fmaf(
+                  x, widen(__ldcs(static_cast<const T*>(f.rows) + now.r[j] * f.row_stride + c)),
+                  dot[j]);
+            __stcs(static_cast<T*>(a.drows) + now.r[j] * a.drows_stride + c,
+                   narrow<T>(now.w[j] * x));
+          }
+      }
+    }
+    if (a.dweights) store_dots<SLOTS>(a, dot, part, turn, now.t, now.s0);
+    now = next;
+    next = then;
+  }
+  zero_empty_rows<T, 1>(a);
 }
 
 // 16-byte rows of 8-element pieces.
@@ -292,17 +378,20 @@ bool vec_rows(const void* p, int64_t stride, fo_type type) {
   return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) & 15) == 0;
 }
 
-// How many CTAs of a kernel the device holds at once, asked for once per device.
+// How many CTAs of a kernel, with so much shared memory always, the device holds at
+// once; asked for once per device.
 template <auto K>
-fo_status resident(int* ctas) {
+fo_status resident(int smem, int* ctas) {
   static std::once_flag once[64];
   static int count[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
+  const fo_status q = smem > 0 ? allow_smem<K>() : FO_OK;
+  if (q != FO_OK) return q;
   const int slot = dev < 64 ? dev : 63;
   std::call_once(once[slot], [&] {
     int per_sm = 0, sms = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K, kThreads, 0) == cudaSuccess &&
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K, kThreads, smem) == cudaSuccess &&
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
       count[slot] = per_sm * sms;
   });
@@ -321,7 +410,7 @@ fo_status forward_as(CombineArgs a, cudaStream_t st) {
   a.items = int32_t(items);
   constexpr auto kernel = combine_kernel<T, O, W, SLOTS, TOKENS>;
   int ctas = 0;
-  const fo_status q = resident<kernel>(&ctas);
+  const fo_status q = resident<kernel>(0, &ctas);
   if (q != FO_OK) return q;
   kernel<<<unsigned(items < ctas ? items : ctas), kThreads, 0, st>>>(a);
   return FO_OK;
@@ -334,25 +423,30 @@ fo_status forward(const CombineArgs& a, bool vec, cudaStream_t st) {
   return forward_as<T, O, 8, 4, 1>(a, st);
 }
 
-template <typename T, typename O, int W, int SLOTS, int CHUNKS>
-fo_status backward_as(const CombineBackArgs& a, cudaStream_t st) {
+template <auto K>
+fo_status backward_as(const CombineBackArgs& a, int smem, cudaStream_t st) {
   const int64_t per = (kThreads / 32) / a.warps;
   int64_t grid = (int64_t(a.f.tokens) + per - 1) / per;
   const int64_t looks = (a.f.table_rows + kThreads - 1) / kThreads;
   if (grid < looks) grid = looks;
-  constexpr auto kernel = combine_backward_kernel<T, O, W, SLOTS, CHUNKS>;
   int ctas = 0;
-  const fo_status q = resident<kernel>(&ctas);
+  const fo_status q = resident<K>(smem, &ctas);
   if (q != FO_OK) return q;
-  kernel<<<unsigned(grid < ctas ? grid : ctas), kThreads, 0, st>>>(a);
+  K<<<unsigned(grid < ctas ? grid : ctas), kThreads, smem, st>>>(a);
   return FO_OK;
 }
 
 template <typename T, typename O>
 fo_status backward(const CombineBackArgs& a, bool vec, cudaStream_t st) {
-  if (!vec) return backward_as<T, O, 1, 4, 2>(a, st);
-  if (a.f.top_k <= 2) return backward_as<T, O, 8, 2, 2>(a, st);
-  return backward_as<T, O, 8, 4, 1>(a, st);
+  constexpr int kT = sizeof(T) / 2, kO = sizeof(O) / 2;
+  // two rounds of the ring
+  constexpr auto bytes = [](int slots, int chunks) {
+    return 2 * chunks * (kO + slots * kT) * 16 * kThreads;
+  };
+  if (!vec) return backward_as<combine_backward_any_kernel<T, O, 4>>(a, 0, st);
+  if (a.f.top_k <= 2)
+    return backward_as<combine_backward_kernel<T, O, 2, 2>>(a, bytes(2, 2), st);
+  return backward_as<combine_backward_kernel<T, O, 4, 1>>(a, bytes(4, 1), st);
 }
 
 fo_status launched() { return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA; }

@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
       for (int i = 0; i < 4; ++i) x[v][i] = s[v][i] = Pair::of(0.0f);
       if (has[v]) {
         const int at = stage * kPieces + v * (kA + kS);
-        ring.get<A>(at, x[v]);
-        if (a.residual != nullptr) ring.get<S>(at + kA, s[v]);
+        get_pairs<A>(ring, at, x[v]);
+        if (a.residual != nullptr) get_pairs<S>(ring, at + kA, s[v]);
       }
     }
     fetch(stage);
@@ -253,7 +253,7 @@ fo_status launch(const NormArgs& a, bool vec, cudaStream_t st) {
     const RowShape s = row_shape(a.hidden, a.hidden <= 256 ? 1 : 2, 8);
     // four rows under way where two CTAs of 256 threads, or one of more, fit so, else two
     const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S)) / 2;
-    const bool deep = 4 * row <= (s.threads <= 256 ? kNormSmem / 2 : kNormSmem);
+    const bool deep = 4 * row <= (s.threads <= 256 ? kBlockSmem / 2 : kBlockSmem);
     if (s.nv == 1) return launch_ring<A, S, 1, 4>(a, s, row, st);
     return deep ? launch_ring<A, S, 2, 4>(a, s, row, st) : launch_ring<A, S, 2, 2>(a, s, row, st);
   } else if (vec) {

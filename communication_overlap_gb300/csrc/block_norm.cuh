@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cstdint>
-#include <mutex>
 
 #include "block_common.cuh"
 
@@ -216,56 +215,13 @@ inline RowShape row_shape(int64_t hidden, int nv, int cta_warps) {
   return s;
 }
 
-// A ring in shared memory that a thread fills for itself, rows ahead of their use:
-// no other thread reads its pieces, so no barrier guards them.  Piece i of stage s
-// lies at (s * pieces + i) * threads + thread, 16 bytes each.
-struct OwnRing {
-  uint32_t base;        // of this thread's first piece
-  uint32_t step;        // bytes from one piece to the next
-
-  __device__ __forceinline__ OwnRing(const void* smem)
-      : base(smem_u32(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
-  __device__ __forceinline__ uint32_t at(int piece) const { return base + uint32_t(piece) * step; }
-  // eight elements into the ring from piece `piece` on
-  template <typename T>
-  __device__ __forceinline__ void fetch(int piece, const T* src) const {
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(piece + i)),
-                   "l"(reinterpret_cast<const uint4*>(src) + i)
-                   : "memory");
-  }
-  template <typename T>
-  __device__ __forceinline__ void get(int piece, Pack8<T>& p) const {
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(p.w[i].x), "=r"(p.w[i].y), "=r"(p.w[i].z), "=r"(p.w[i].w)
-                   : "r"(at(piece + i))
-                   : "memory");
-  }
-  template <typename T>
-  __device__ __forceinline__ void get(int piece, Pair (&x)[4]) const {
-    Pack8<T> p;
-    get(piece, p);
-    pairs_of(p, x);
-  }
-  // eight fp32 values of the thread's own
-  __device__ __forceinline__ void put(int piece, const float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(piece + i)), "f"(v[4 * i]),
-                   "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
-                   : "memory");
-  }
-  __device__ __forceinline__ static void commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  template <int N>      // all but the last N groups have arrived
-  __device__ __forceinline__ static void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-  }
-};
+// Eight elements of a ring's pieces as pairs.
+template <typename T>
+__device__ __forceinline__ void get_pairs(const OwnRing& ring, int piece, Pair (&x)[4]) {
+  Pack8<T> p;
+  ring.get(piece, p);
+  pairs_of(p, x);
+}
 
 // scale gate post of eight columns (factors that are not given left out).
 __device__ __forceinline__ void load_factor(const NormArgs& a, int col, int64_t gate_row,
@@ -297,31 +253,6 @@ inline bool norm_rows_on_16(const NormArgs& a, fo_type type, fo_type stream_type
          norm_on_16(a.residual, a.residual_stride, s) && norm_on_16(a.gate, a.gate_stride, p) &&
          norm_on_16(a.post, 0, p) && norm_on_16(a.pre, 0, p) &&
          norm_on_16(a.sum, a.sum_stride, s) && norm_on_16(a.y, a.y_stride, x);
-}
-
-// The current device's SMs.
-inline fo_status sm_count(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FO_ERR_CUDA;
-  return FO_OK;
-}
-
-// Lets a kernel take up to kNormSmem bytes of dynamic shared memory, once per
-// kernel and device (not a launch's own size: another thread's launch may follow).
-constexpr int kNormSmem = 220 * 1024;
-template <auto K>
-fo_status allow_smem() {
-  static std::once_flag once[64];
-  static cudaError_t err[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FO_ERR_CUDA;
-  const int slot = dev < 64 ? dev : 63;
-  std::call_once(once[slot], [&] {
-    err[slot] = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
-  });
-  return err[slot] == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
 }  // namespace fo

@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = kept_w[i], pre[i] = kept_pre[i];
     } else {
-      ring.get<float>(kW + 2 * v, w);
-      ring.get<float>(kPre + 2 * v, pre);
+      get_pairs<float>(ring, kW + 2 * v, w);
+      get_pairs<float>(ring, kPre + 2 * v, pre);
     }
   };
   Pair dpre[NV][4], sum_g[NV][4], dpost[GATES ? NV : 1][4];
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
       const int at = stage * kPieces + v * kOf;
       ring.get(at, px[v]);
       ring.get(at + kA, py[v]);
-      ring.get<S>(at + 2 * kA, sn[v]);
-      ring.get<S>(at + 2 * kA + kS, d[v]);
+      get_pairs<S>(ring, at + 2 * kA, sn[v]);
+      get_pairs<S>(ring, at + 2 * kA + kS, d[v]);
     }
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
@@ -510,7 +510,7 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   const RowShape s = whole_shape(H <= 8192 ? H : 0);
   const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S));
   const int params = s.nv == 1 ? 0 : s.threads * s.nv * 64;
-  const bool whole = vec && H <= 8192 && 2 * row + params <= kNormSmem;
+  const bool whole = vec && H <= 8192 && 2 * row + params <= kBlockSmem;
   if (whole) {
     share_out(n, f.tokens, whole_workers(H, sms));
   } else {
@@ -524,7 +524,7 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   if (whole) {
     const bool gates = f.gate != nullptr && f.gate_rows < f.tokens;
     // four rows under way where they fit
-    if (s.nv == 1 && 4 * row <= kNormSmem)
+    if (s.nv == 1 && 4 * row <= kBlockSmem)
       return gates ? launch_ring<A, S, 1, 4, true>(a, *n, s, row, st)
                    : launch_ring<A, S, 1, 4, false>(a, *n, s, row, st);
     if (s.nv == 1)
