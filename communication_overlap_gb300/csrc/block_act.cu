@@ -205,11 +205,9 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const ActArgs a) {
     float g[8], u[8], h[8];
     pg[r].get(g);
     pu[r].get(u);
-    if (live && in) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = gated<T>(g[i], u[i], a.act);
-      store8(static_cast<T*>(a.h) + row * a.h_stride + p.col, h);
-    }
+    for (int i = 0; i < 8; ++i) h[i] = gated<T>(g[i], u[i], a.act);
+    store8_warp(static_cast<T*>(a.h) + row * a.h_stride + p.col, live && in, h);
     if (a.codes == nullptr) continue;
     const uint32_t mg = block_max<true>(amax_of(pg[r])), mu = block_max<true>(amax_of(pu[r]));
     if (!live) continue;
@@ -248,7 +246,7 @@ template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a, const void* dh,
                                                                void* du) {
   const Place p = place(a, 8, ROWS);
-  if (!p.live || p.col >= a.inter) return;
+  const bool in = p.live && p.col < a.inter;
   const int blocks = a.padded / kCheckpointBlock;
   Pack8<T> pd[ROWS];
   uint2 qg[ROWS], qu[ROWS];
@@ -256,7 +254,12 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a,
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const int64_t row = p.row + r * a.per_cta;
-    if (row >= a.rows) continue;
+    if (!in || row >= a.rows) {
+      pd[r].zero();
+      qg[r] = qu[r] = make_uint2(0, 0);
+      sg[r] = su[r] = 0;
+      continue;
+    }
     const int8_t* from = a.codes + row * 2 * a.padded + p.col;
     const uint8_t* s = a.scales + row * 2 * blocks + p.col / kCheckpointBlock;
     pd[r].load_once(static_cast<const T*>(dh) + row * a.h_stride + p.col);
@@ -268,7 +271,6 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a,
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const int64_t row = p.row + r * a.per_cta;
-    if (row >= a.rows) continue;
     float d[8], g[8], u[8], og[8], ou[8];
     pd[r].get(d);
     values_of(qg[r], step_value(sg[r]), g);
@@ -276,8 +278,8 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a,
 #pragma unroll
     for (int i = 0; i < 8; ++i) gated_backward<T>(d[i], g[i], u[i], a.act, og[i], ou[i]);
     T* dst = static_cast<T*>(du) + row * a.u_stride + p.col;
-    store8(dst, og);
-    store8(dst + a.inter, ou);
+    store8_warp(dst, in && row < a.rows, og);
+    store8_warp(dst + a.inter, in && row < a.rows, ou);
   }
 }
 

@@ -45,7 +45,10 @@ struct Columns {
   __device__ __forceinline__ void load_once(const T* at) { p.load_once(at); }
   __device__ __forceinline__ void load(const T* at) { p.load(at); }
   __device__ __forceinline__ void get(float (&v)[8]) const { p.get(v); }
-  __device__ __forceinline__ static void store(T* at, const float (&v)[8]) { store8(at, v); }
+  // by whole warps; `in`: of this lane
+  __device__ __forceinline__ static void store(T* at, bool in, const float (&v)[8]) {
+    store8_warp(at, in, v);
+  }
 };
 template <typename T>
 struct Columns<T, 1> {
@@ -53,8 +56,8 @@ struct Columns<T, 1> {
   __device__ __forceinline__ void load_once(const T* at) { e = __ldcs(at); }
   __device__ __forceinline__ void load(const T* at) { e = __ldg(at); }
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = widen(e); }
-  __device__ __forceinline__ static void store(T* at, const float (&v)[1]) {
-    __stcs(at, narrow<T>(v[0]));
+  __device__ __forceinline__ static void store(T* at, bool in, const float (&v)[1]) {
+    if (in) __stcs(at, narrow<T>(v[0]));
   }
 };
 
@@ -131,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
       const int64_t t = token(item, i);
-      if (in && local < per && t < a.tokens)
-        Columns<O, W>::store(static_cast<O*>(a.y) + t * a.y_stride + col, acc[i]);
+      Columns<O, W>::store(static_cast<O*>(a.y) + t * a.y_stride + col,
+                           in && local < per && t < a.tokens, acc[i]);
     }
   }
 }
@@ -148,177 +151,203 @@ struct CombineBackArgs {
   int32_t warps;            // of a token: 1, 2, 4 or 8
 };
 
-// The rows that hold no token become zeros: 32 of them looked at by a warp.
+// The rows that hold no token become zeros: a warp looks at 32 of them, far apart, as
+// they come in runs.
 template <typename T, int W>
 __device__ __forceinline__ void zero_empty_rows(const CombineBackArgs& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t looks = (a.f.table_rows + 31) / 32;
   for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + warp; i < looks;
        i += int64_t(gridDim.x) * (kThreads / 32)) {
-    const int64_t row = i * 32 + lane;
+    const int64_t row = i + lane * looks;
     uint32_t todo =
         __ballot_sync(0xffffffffu, row < a.f.table_rows && __ldg(a.row_token + row) < 0);
     for (; todo; todo &= todo - 1) {
-      T* at = static_cast<T*>(a.drows) + (i * 32 + __ffs(todo) - 1) * a.drows_stride;
+      T* at = static_cast<T*>(a.drows) + (i + (__ffs(todo) - 1) * looks) * a.drows_stride;
       float zero[W];
 #pragma unroll
       for (int k = 0; k < W; ++k) zero[k] = 0.0f;
-      for (int c = lane * W; c < a.f.hidden; c += 32 * W) Columns<T, W>::store(at + c, zero);
+      for (int c = lane * W; c - lane * W < a.f.hidden; c += 32 * W)
+        Columns<T, W>::store(at + c, c < a.f.hidden, zero);
     }
   }
 }
 
-// Some of a token's slots on their way: their rows, then the tokens that those name.
+// The rounds of a group of warps: SLOTS slots of a token at a time.
 template <int SLOTS>
-struct Slots {
+struct Round {
   int64_t t;
   int s0;
-  int32_t r[SLOTS], by[SLOTS];
-  float w[SLOTS];
-
-  // Slots number `i` of a group of warps: `of` of them to a token.
-  __device__ __forceinline__ void look_up(const CombineBackArgs& a, int64_t first, int64_t step,
-                                          int64_t i, int of) {
-    t = first + i / of * step;
-    s0 = int(i % of) * SLOTS;
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-      const bool has = t < a.f.tokens && s0 + j < a.f.top_k;
-      r[j] = has ? __ldg(a.f.token_row + t * a.f.top_k + s0 + j) : -1;
-      w[j] = has && a.f.weights ? __ldg(a.f.weights + t * a.f.top_k + s0 + j) : 1.0f;
-    }
-  }
-  __device__ __forceinline__ void name(const CombineBackArgs& a) {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j)
-      by[j] = r[j] >= 0 && r[j] < a.f.table_rows ? __ldg(a.row_token + r[j]) : -1;
-  }
-  // A row outside the table, or one that holds another token, is not this one's.
-  __device__ __forceinline__ void check(const CombineBackArgs& a) {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j)
-      if (r[j] >= 0 && by[j] != int32_t(t)) {
-        atomicCAS(a.f.status, 0, int32_t(FO_ERR_ARG));
-        r[j] = -1;
-      }
+  __device__ __forceinline__ void advance(const CombineArgs& f, int64_t step) {
+    s0 += SLOTS;
+    if (s0 >= f.top_k) s0 = 0, t += step;
   }
 };
 
-// The sums of SLOTS products over a token's warps.  part: [2][warps][SLOTS].
+// A lane's slot of a round: its row and weight.
 template <int SLOTS>
-__device__ __forceinline__ void store_dots(const CombineBackArgs& a, float (&dot)[SLOTS],
-                                           float (*part)[kThreads / 32][SLOTS], int& turn,
-                                           int64_t t, int s0) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int j = 0; j < SLOTS; ++j) dot[j] = warp_sum(dot[j]);
-  if (lane == 0) {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) part[turn][warp][j] = dot[j];
-  }
-  __syncthreads();
-  if (warp % a.warps == 0 && lane < SLOTS && t < a.f.tokens && s0 + lane < a.f.top_k) {
-    float sum = 0.0f;
-    for (int i = 0; i < a.warps; ++i) sum += part[turn][warp + i][lane];
-    a.dweights[t * a.f.top_k + s0 + lane] = sum;
-  }
-  turn ^= 1;
+__device__ __forceinline__ void look_up(const CombineArgs& f, const Round<SLOTS>& q, bool mine,
+                                        int slot, int32_t& r, float& w) {
+  const bool has = mine && q.t < f.tokens && q.s0 + slot < f.top_k;
+  const int64_t at = q.t * f.top_k + q.s0 + slot;
+  r = has ? __ldg(f.token_row + at) : -1;
+  w = has && f.weights ? __ldg(f.weights + at) : 1.0f;
 }
 
-// Rows on 16 bytes.  A token belongs to a group of warps, SLOTS of its slots are taken
-// at a time, and CHUNKS times eight columns per thread: a round of dy, the rows, their
-// products and the rows' gradients.  CTAs walk over the tokens.  While a round is
-// worked on, the next one's data are on their way into the ring, its rows have been
-// checked against row_token, and those of the slots behind it are being looked up:
-// three waits in a row otherwise (161 us for 16384 x 4096, top 2; with look-ups alone
-// ahead 136).
-template <typename T, typename O, int SLOTS, int CHUNKS>
+// The threads of a token meet.
+__device__ __forceinline__ void meet(int group, int warps) {
+  if (warps == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+}
+
+// Rows on 16 bytes.  A token belongs to a group of warps; a round is SLOTS of its
+// slots, in pieces of CHUNKS times eight columns per thread: dy, the rows, their
+// products and the rows' gradients.  Groups walk over the tokens, each at its own
+// pace.  STAGES - 1 pieces ahead of the one that is worked on are on their way into the
+// ring, and the group's first warp looks the rows up and checks them three rounds
+// ahead, for all: look-up, check and rows are three waits in a row otherwise (161 us
+// for 16384 x 4096, top 2; with look-ups ahead alone 136; with the ring, but eight
+// warps to each token, which meet at its sums, 125).
+template <typename T, typename O, int SLOTS, int CHUNKS, int STAGES>
 __global__ void __launch_bounds__(kThreads, 3) combine_backward_kernel(const CombineBackArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[2][kThreads / 32][SLOTS];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float part[2][kWarps][SLOTS];
+  __shared__ int32_t row_s[4][kWarps][SLOTS];          // of the round (by 4) and the group
+  __shared__ float weight_s[4][kWarps][SLOTS];
   constexpr int kT = sizeof(T) / 2, kO = sizeof(O) / 2;     // pieces of eight columns
   constexpr int kOf = kO + SLOTS * kT, kPieces = CHUNKS * kOf;
   const CombineArgs& f = a.f;
   const OwnRing ring(smem);
-  const int warp = threadIdx.x >> 5;
-  const int per = (kThreads / 32) / a.warps;           // tokens of a CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / a.warps;
+  const bool leads = warp % a.warps == 0 && lane < SLOTS;
+  const int per = kWarps / a.warps;                    // tokens of a CTA
   const int64_t step = int64_t(gridDim.x) * per;
-  const int64_t first = int64_t(blockIdx.x) * per + warp / a.warps;
-  const int col0 = ((warp % a.warps) * 32 + int(threadIdx.x & 31)) * 8;
+  const int64_t first = int64_t(blockIdx.x) * per + group;
+  const int col0 = ((warp % a.warps) * 32 + lane) * 8;
   const int stride = a.warps * 32 * 8;                 // from one of a thread's columns to the next
-  const int of = (f.top_k + SLOTS - 1) / SLOTS;
-  const auto fetch = [&](const Slots<SLOTS>& q, int c0, int stage) {
-    if (q.t < f.tokens) {
+  const auto name = [&](int32_t r) {
+    return r >= 0 && r < f.table_rows ? __ldg(a.row_token + r) : -1;
+  };
+  const auto publish = [&](int i, int64_t t, int32_t r, int32_t by, float w) {
+    if (!leads) return;
+    // (a row outside the table, or one that holds another token, is not this one's)
+    if (r >= 0 && by != int32_t(t)) {
+      atomicCAS(f.status, 0, int32_t(FO_ERR_ARG));
+      r = -1;
+    }
+    row_s[i & 3][group][lane] = r;
+    weight_s[i & 3][group][lane] = w;
+  };
+  // the rounds that are worked on, fetched next, published next and looked up next
+  Round<SLOTS> now{first, 0}, ahead{first, 0}, named{first, 0}, looked{first, 0};
+  int32_t r3, by3, r4;
+  float w3, w4;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    look_up(f, looked, leads, lane, r3, w3);
+    publish(i, looked.t, r3, name(r3), w3);
+    looked.advance(f, step);
+    named.advance(f, step);
+  }
+  look_up(f, looked, leads, lane, r3, w3);
+  by3 = name(r3);
+  looked.advance(f, step);
+  look_up(f, looked, leads, lane, r4, w4);
+  looked.advance(f, step);
+  meet(group, a.warps);
+  int ahead_i = 0, ahead_c = 0;
+  const auto fetch = [&](int stage) {
+    if (ahead.t < f.tokens) {
+      int32_t r[SLOTS];
+#pragma unroll
+      for (int j = 0; j < SLOTS; ++j) r[j] = row_s[ahead_i & 3][group][j];
 #pragma unroll
       for (int k = 0; k < CHUNKS; ++k) {
-        const int c = c0 + k * stride, at = stage * kPieces + k * kOf;
-        if (c >= f.hidden) continue;
-        ring.fetch(at, static_cast<const O*>(a.dy) + (q.t * a.dy_stride + c));
+        const int c = col0 + ahead_c + k * stride, at = stage * kPieces + k * kOf;
+        if (c - lane * 8 >= f.hidden) continue;
+        ring.fetch(at, static_cast<const O*>(a.dy) + ahead.t * a.dy_stride, c, f.hidden);
         if (a.dweights == nullptr) continue;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-          if (q.r[j] >= 0)
-            ring.fetch(at + kO + j * kT,
-                       static_cast<const T*>(f.rows) + (q.r[j] * f.row_stride + c));
+          if (r[j] >= 0)
+            ring.fetch(at + kO + j * kT, static_cast<const T*>(f.rows) + r[j] * f.row_stride, c,
+                       f.hidden);
       }
     }
     OwnRing::commit();
-  };
-  int turn = 0, stage = 0;
-  Slots<SLOTS> now, next;
-  now.look_up(a, first, step, 0, of);
-  now.name(a);
-  now.check(a);
-  fetch(now, col0, 0);
-  next.look_up(a, first, step, 1, of);
-  next.name(a);
-  // (as many rounds for all of the CTA's groups: they meet at the sums)
-  const int64_t steps = (f.tokens - int64_t(blockIdx.x) * per + step - 1) / step;
-  for (int64_t i = 0; i < steps * of; ++i) {
-    Slots<SLOTS> then;
-    then.look_up(a, first, step, i + 2, of);
-    next.check(a);
-    float dot[SLOTS];
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) dot[j] = 0.0f;
-    for (int c0 = 0; c0 < f.hidden; c0 += CHUNKS * stride) {
-      if (c0 + CHUNKS * stride < f.hidden)
-        fetch(now, col0 + c0 + CHUNKS * stride, stage ^ 1);
-      else
-        fetch(next, col0, stage ^ 1);
-      OwnRing::wait<1>();
-      if (now.t < f.tokens) {
-#pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-          const int c = col0 + c0 + k * stride, at = stage * kPieces + k * kOf;
-          if (c >= f.hidden) continue;
-          Pack8<O> g;
-          float x[8];
-          ring.get(at, g);
-          g.get(x);
-#pragma unroll
-          for (int j = 0; j < SLOTS; ++j)
-            if (now.r[j] >= 0) {
-              float y[8];
-              if (a.dweights) {
-                Pack8<T> v;
-                ring.get(at + kO + j * kT, v);
-                v.get(y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dot[j] = fmaf(x[e], y[e], dot[j]);
-              }
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = now.w[j] * x[e];
-              store8(static_cast<T*>(a.drows) + (now.r[j] * a.drows_stride + c), y);
-            }
-        }
-      }
-      stage ^= 1;
+    ahead_c += CHUNKS * stride;
+    if (ahead_c >= f.hidden) {
+      ahead_c = 0;
+      ++ahead_i;
+      ahead.advance(f, step);
     }
-    if (a.dweights) store_dots<SLOTS>(a, dot, part, turn, now.t, now.s0);
-    now = next;
-    next = then;
-    next.name(a);
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  int turn = 0, stage = 0;
+  for (int i = 0; now.t < f.tokens; ++i) {
+    int32_t r[SLOTS];
+    float w[SLOTS];
+    Pair dot[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      r[j] = row_s[i & 3][group][j];
+      w[j] = weight_s[i & 3][group][j];
+      dot[j] = Pair::of(0.0f);
+    }
+    for (int c0 = 0; c0 < f.hidden; c0 += CHUNKS * stride) {
+      OwnRing::settle<T, O>();
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);
+      OwnRing::wait<STAGES - 1>();
+      OwnRing::settle<T, O>();
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k) {
+        const int c = col0 + c0 + k * stride, at = stage * kPieces + k * kOf;
+        if (c - lane * 8 >= f.hidden) continue;
+        const bool in = c < f.hidden;
+        Pair x[4], y[4];
+        get_pairs<O>(ring, at, x);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+          if (r[j] >= 0) {
+            if (a.dweights && in) {
+              get_pairs<T>(ring, at + kO + j * kT, y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dot[j] = fma2(x[e], y[e], dot[j]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = Pair::of(w[j]) * x[e];
+            store8_warp(static_cast<T*>(a.drows) + (r[j] * a.drows_stride + c), in, y);
+          }
+      }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    publish(i + 3, named.t, r3, by3, w3);
+    named.advance(f, step);
+    r3 = r4, w3 = w4;
+    by3 = name(r3);
+    look_up(f, looked, leads, lane, r4, w4);
+    looked.advance(f, step);
+    if (a.dweights) {
+      float sum[SLOTS];
+#pragma unroll
+      for (int j = 0; j < SLOTS; ++j) {
+        sum[j] = warp_sum(dot[j].sum());
+        if (lane == 0) part[turn][warp][j] = sum[j];
+      }
+    }
+    meet(group, a.warps);
+    if (a.dweights && leads && now.s0 + lane < f.top_k) {
+      float sum = 0.0f;
+      for (int k = 0; k < a.warps; ++k) sum += part[turn][warp + k][lane];
+      a.dweights[now.t * f.top_k + now.s0 + lane] = sum;
+    }
+    turn ^= 1;
+    now.advance(f, step);
   }
   OwnRing::wait<0>();
   zero_empty_rows<T, 8>(a);
@@ -329,45 +358,72 @@ template <typename T, typename O, int SLOTS>
 __global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const CombineBackArgs a) {
   __shared__ float part[2][kThreads / 32][SLOTS];
   const CombineArgs& f = a.f;
-  const int warp = threadIdx.x >> 5;
-  const int per = (kThreads / 32) / a.warps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / a.warps, per = (kThreads / 32) / a.warps;
   const int64_t step = int64_t(gridDim.x) * per;
-  const int64_t first = int64_t(blockIdx.x) * per + warp / a.warps;
-  const int of = (f.top_k + SLOTS - 1) / SLOTS;
   int turn = 0;
-  Slots<SLOTS> now, next;
-  now.look_up(a, first, step, 0, of);
-  now.name(a);
-  next.look_up(a, first, step, 1, of);
-  const int64_t steps = (f.tokens - int64_t(blockIdx.x) * per + step - 1) / step;
-  for (int64_t i = 0; i < steps * of; ++i) {
-    next.name(a);
-    Slots<SLOTS> then;
-    then.look_up(a, first, step, i + 2, of);
-    now.check(a);
-    float dot[SLOTS];
+  Round<SLOTS> now{int64_t(blockIdx.x) * per + group, 0};
+  for (; now.t < f.tokens; now.advance(f, step)) {
+    int32_t mine, by;
+    float weight;
+    look_up(f, now, lane < SLOTS, lane, mine, weight);
+    by = mine >= 0 && mine < f.table_rows ? __ldg(a.row_token + mine) : -1;
+    if (mine >= 0 && by != int32_t(now.t)) {
+      atomicCAS(f.status, 0, int32_t(FO_ERR_ARG));
+      mine = -1;
+    }
+    int32_t r[SLOTS];
+    float w[SLOTS], dot[SLOTS];
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j) dot[j] = 0.0f;
-    if (now.t < f.tokens) {
-      const O* dy = static_cast<const O*>(a.dy) + now.t * a.dy_stride;
-#pragma unroll 4
-      for (int c = (warp % a.warps) * 32 + int(threadIdx.x & 31); c < f.hidden; c += a.warps * 32) {
-        const float x = widen(__ldg(dy + c));
+    for (int j = 0; j < SLOTS; ++j) {
+      r[j] = __shfl_sync(0xffffffffu, mine, j);
+      w[j] = __shfl_sync(0xffffffffu, weight, j);
+      dot[j] = 0.0f;
+    }
+    const O* dy = static_cast<const O*>(a.dy) + now.t * a.dy_stride;
+    // CHUNKS columns' loads before their stores
+    constexpr int kChunks = 4;
+    const int stride = a.warps * 32;
+    for (int c0 = (warp % a.warps) * 32 + lane; c0 < f.hidden; c0 += kChunks * stride) {
+      O g[kChunks];
+      T v[kChunks][SLOTS];
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = c0 + k * stride;
+        if (c >= f.hidden) continue;
+        g[k] = __ldg(dy + c);
+        if (a.dweights == nullptr) continue;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-          if (now.r[j] >= 0) {
-            if (a.dweights)
-              dot[j] = fmaf(
-                  x, widen(__ldcs(static_cast<const T*>(f.rows) + now.r[j] * f.row_stride + c)),
-                  dot[j]);
-            __stcs(static_cast<T*>(a.drows) + now.r[j] * a.drows_stride + c,
-                   narrow<T>(now.w[j] * x));
+          if (r[j] >= 0)
+            v[k][j] = __ldcs(static_cast<const T*>(f.rows) + (r[j] * f.row_stride + c));
+      }
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = c0 + k * stride;
+        if (c >= f.hidden) continue;
+        const float x = widen(g[k]);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+          if (r[j] >= 0) {
+            if (a.dweights) dot[j] = fmaf(x, widen(v[k][j]), dot[j]);
+            __stcs(static_cast<T*>(a.drows) + (r[j] * a.drows_stride + c), narrow<T>(w[j] * x));
           }
       }
     }
-    if (a.dweights) store_dots<SLOTS>(a, dot, part, turn, now.t, now.s0);
-    now = next;
-    next = then;
+    if (a.dweights == nullptr) continue;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      dot[j] = warp_sum(dot[j]);
+      if (lane == 0) part[turn][warp][j] = dot[j];
+    }
+    meet(group, a.warps);
+    if (warp % a.warps == 0 && lane < SLOTS && now.s0 + lane < f.top_k) {
+      float sum = 0.0f;
+      for (int k = 0; k < a.warps; ++k) sum += part[turn][warp + k][lane];
+      a.dweights[now.t * f.top_k + now.s0 + lane] = sum;
+    }
+    turn ^= 1;
   }
   zero_empty_rows<T, 1>(a);
 }
@@ -423,15 +479,33 @@ fo_status forward(const CombineArgs& a, bool vec, cudaStream_t st) {
   return forward_as<T, O, 8, 4, 1>(a, st);
 }
 
+// The warps of a token: the fewest (they meet at each of its sums) with which the
+// groups of all CTAs come out even over the tokens to within a twentieth, or the most
+// even number, up to a warp per `width` columns.
+int token_warps(int64_t tokens, int64_t hidden, int width, int ctas) {
+  int best = 1;
+  double most = 0.0;
+  for (int w = 1; w <= 8; w *= 2) {
+    if (w > 1 && int64_t(w / 2) * width >= hidden) break;
+    const int64_t groups = int64_t(ctas) * (kThreads / 32) / w;
+    const int64_t rounds = (tokens + groups - 1) / groups;
+    const double even = rounds > 0 ? double(tokens) / double(groups * rounds) : 1.0;
+    if (even > most) best = w, most = even;
+    if (even > 0.95) break;
+  }
+  return best;
+}
+
 template <auto K>
-fo_status backward_as(const CombineBackArgs& a, int smem, cudaStream_t st) {
+fo_status backward_as(CombineBackArgs a, int smem, int width, cudaStream_t st) {
+  int ctas = 0;
+  const fo_status q = resident<K>(smem, &ctas);
+  if (q != FO_OK) return q;
+  a.warps = token_warps(a.f.tokens, a.f.hidden, width, ctas);
   const int64_t per = (kThreads / 32) / a.warps;
   int64_t grid = (int64_t(a.f.tokens) + per - 1) / per;
   const int64_t looks = (a.f.table_rows + kThreads - 1) / kThreads;
   if (grid < looks) grid = looks;
-  int ctas = 0;
-  const fo_status q = resident<K>(smem, &ctas);
-  if (q != FO_OK) return q;
   K<<<unsigned(grid < ctas ? grid : ctas), kThreads, smem, st>>>(a);
   return FO_OK;
 }
@@ -439,14 +513,18 @@ fo_status backward_as(const CombineBackArgs& a, int smem, cudaStream_t st) {
 template <typename T, typename O>
 fo_status backward(const CombineBackArgs& a, bool vec, cudaStream_t st) {
   constexpr int kT = sizeof(T) / 2, kO = sizeof(O) / 2;
-  // two rounds of the ring
-  constexpr auto bytes = [](int slots, int chunks) {
-    return 2 * chunks * (kO + slots * kT) * 16 * kThreads;
+  // of three CTAs' rings on an SM: three stages, or two of four fp32 rows
+  constexpr int kStages = kT == 1 ? 3 : 2;
+  constexpr auto bytes = [](int slots, int chunks, int stages) {
+    return stages * chunks * (kO + slots * kT) * 16 * kThreads;
   };
-  if (!vec) return backward_as<combine_backward_any_kernel<T, O, 4>>(a, 0, st);
+  if (!vec) return backward_as<combine_backward_any_kernel<T, O, 4>>(a, 0, 32, st);
+  if (a.f.top_k <= 2 && kT == 1)
+    return backward_as<combine_backward_kernel<T, O, 2, 2, 3>>(a, bytes(2, 2, 3), 256, st);
   if (a.f.top_k <= 2)
-    return backward_as<combine_backward_kernel<T, O, 2, 2>>(a, bytes(2, 2), st);
-  return backward_as<combine_backward_kernel<T, O, 4, 1>>(a, bytes(4, 1), st);
+    return backward_as<combine_backward_kernel<T, O, 2, 1, 3>>(a, bytes(2, 1, 3), 256, st);
+  return backward_as<combine_backward_kernel<T, O, 4, 1, kStages>>(a, bytes(4, 1, kStages), 256,
+                                                                   st);
 }
 
 fo_status launched() { return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA; }
@@ -490,8 +568,6 @@ fo_status launch_combine_backward(const void* dy, fo_type dy_type, int64_t dy_st
   a.drows = drows, a.drows_stride = drows_stride, a.dweights = dweights;
   const bool vec = hidden % 8 == 0 && (!dweights || vec_rows(rows, row_stride, type)) &&
                    vec_rows(dy, dy_stride, dy_type) && vec_rows(drows, drows_stride, type);
-  const int64_t warps = ((vec ? hidden / 8 : hidden) + 31) / 32;
-  a.warps = warps <= 1 ? 1 : warps <= 2 ? 2 : warps <= 4 ? 4 : 8;
   if (tokens == 0 && table_rows == 0) return FO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = type == FO_TYPE_BF16, ybf = dy_type == FO_TYPE_BF16;

@@ -66,15 +66,93 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
+// Two fp32 values that one instruction takes at once.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ static Pair of(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+  }
+  __device__ __forceinline__ static Pair of(float x) { return of(x, x); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  }
+  __device__ __forceinline__ float sum() const {
+    float lo, hi;
+    get(lo, hi);
+    return lo + hi;
+  }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Pack8<T>& p, Pair (&x)[4]) {
+  float v[8];
+  p.get(v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
+}
+
+__device__ __forceinline__ void pairs_of(const float (&v)[8], Pair (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
+}
+
+// store8 by a whole warp whose lanes have neighbouring eights; `in`: this lane's are to
+// be stored.  Of fp32 two lanes trade halves, so that a store of theirs is 32 bytes in
+// one piece: half a sector each costs twice the traffic to L2.
+template <typename T>
+__device__ __forceinline__ void store8_warp(T* p, bool in, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    if (in) store8(p, v);
+  } else {
+    const bool odd = threadIdx.x & 1;
+    const bool other = __shfl_xor_sync(0xffffffffu, int(in), 1) != 0;
+    float4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[4], 1);
+    got.y = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[5], 1);
+    got.z = __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[6], 1);
+    got.w = __shfl_xor_sync(0xffffffffu, odd ? v[3] : v[7], 1);
+    const float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+    // the even lane's eight, then the odd one's
+    if (odd ? other : in) __stcs(reinterpret_cast<float4*>(odd ? p - 4 : p), odd ? got : lo);
+    if (odd ? in : other) __stcs(reinterpret_cast<float4*>(odd ? p + 4 : p + 8), odd ? hi : got);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8_warp(T* p, bool in, const Pair (&x)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i].get(v[2 * i], v[2 * i + 1]);
+  store8_warp(p, in, v);
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// A ring in shared memory that a thread fills for itself, rows ahead of their use:
-// no other thread reads its pieces, so no barrier guards them.  Piece i of stage s
-// lies at (s * pieces + i) * threads + thread, 16 bytes each.
+// A ring in shared memory that a thread fills for itself, rows ahead of their use, so
+// that no barrier guards it: piece i of stage s lies at (s * pieces + i) * threads +
+// thread, 16 bytes each.  Of fp32 rows two neighbouring lanes fetch 32 bytes together
+// (half a sector each would be read from L2 twice), into each other's pieces: these
+// need a __syncwarp after a wait, and one between their reads and the next fetch.
 struct OwnRing {
   uint32_t base;        // of this thread's first piece
   uint32_t step;        // bytes from one piece to the next
@@ -82,14 +160,28 @@ struct OwnRing {
   __device__ __forceinline__ OwnRing(const void* smem)
       : base(smem_u32(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
   __device__ __forceinline__ uint32_t at(int piece) const { return base + uint32_t(piece) * step; }
-  // eight elements into the ring from piece `piece` on
+  __device__ __forceinline__ static void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
+  // The row's eight elements from `col` on into the ring from piece `piece` on, where they
+  // exist (col < limit).  By whole warps; col is a multiple of 8 and goes with the lane.
   template <typename T>
-  __device__ __forceinline__ void fetch(int piece, const T* src) const {
+  __device__ __forceinline__ void fetch(int piece, const T* row, int col, int limit) const {
+    if constexpr (sizeof(T) == 2) {
+      if (col < limit) copy16(at(piece), row + col);
+    } else {
+      const int odd = (col >> 3) & 1;
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(piece + i)),
-                   "l"(reinterpret_cast<const uint4*>(src) + i)
-                   : "memory");
+      for (int h = 0; h < 2; ++h) {
+        const int c = (col & ~8) | (h << 3);       // of the even lane, then of the odd one
+        if (c < limit) copy16(at(piece + odd) + (h - odd) * 16, row + c + odd * 4);
+      }
+    }
+  }
+  // After a wait, and before the next fetch, of rows of these types.
+  template <typename A, typename B>
+  __device__ __forceinline__ static void settle() {
+    if constexpr (sizeof(A) == 4 || sizeof(B) == 4) __syncwarp();
   }
   template <typename T>
   __device__ __forceinline__ void get(int piece, Pack8<T>& p) const {
@@ -116,6 +208,14 @@ struct OwnRing {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
   }
 };
+
+// Eight elements of a ring's pieces as pairs.
+template <typename T>
+__device__ __forceinline__ void get_pairs(const OwnRing& ring, int piece, Pair (&x)[4]) {
+  Pack8<T> p;
+  ring.get(piece, p);
+  pairs_of(p, x);
+}
 
 // The current device's SMs.
 inline fo_status sm_count(int* sms) {

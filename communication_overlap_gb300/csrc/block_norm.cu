@@ -73,12 +73,11 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
   const auto fetch = [&](int stage) {
     if (fetched < a.tokens) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (has[v]) {
-          const int at = stage * kPieces + v * (kA + kS);
-          ring.fetch(at, x_at + col[v]);
-          if (a.residual != nullptr) ring.fetch(at + kA, r_at + col[v]);
-        }
+      for (int v = 0; v < NV; ++v) {
+        const int at = stage * kPieces + v * (kA + kS);
+        ring.fetch(at, x_at, col[v], a.hidden);
+        if (a.residual != nullptr) ring.fetch(at + kA, r_at, col[v], a.hidden);
+      }
     }
     OwnRing::commit();
     fetched += step;
@@ -115,6 +114,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
       gate_row = row;
     }
     OwnRing::wait<DEPTH - 1>();
+    OwnRing::settle<A, S>();
     Pair x[NV][4], s[NV][4];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
         if (a.residual != nullptr) get_pairs<S>(ring, at + kA, s[v]);
       }
     }
+    OwnRing::settle<A, S>();
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     Pair r1 = Pair::of(1.0f);
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
         s[v][i] = fma2(w[v][i], x[v][i] * r1, s[v][i]);
         sum = fma2(s[v][i], s[v][i], sum);
       }
-      if (has[v] && a.sum != nullptr) store8(sum_at + col[v], s[v]);
+      if (a.sum != nullptr) store8_warp(sum_at + col[v], has[v], s[v]);
     }
     sum_at += sum_step;
     if (a.pre == nullptr) continue;
@@ -160,10 +161,9 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
     if (g.tid == 0) a.pre_rstd[t] = r2;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!has[v]) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[v][i] = s[v][i] * Pair::of(r2) * pre[v][i];
-      store8(y_at + col[v], s[v]);
+      store8_warp(y_at + col[v], has[v], s[v]);
     }
     y_at += y_step;
   }

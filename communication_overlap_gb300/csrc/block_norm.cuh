@@ -8,62 +8,6 @@
 
 namespace fo {
 
-// Two fp32 values that one instruction takes at once.
-struct Pair {
-  uint64_t v;
-  __device__ __forceinline__ static Pair of(float lo, float hi) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
-    return p;
-  }
-  __device__ __forceinline__ static Pair of(float x) { return of(x, x); }
-  __device__ __forceinline__ void get(float& lo, float& hi) const {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-  }
-  __device__ __forceinline__ float sum() const {
-    float lo, hi;
-    get(lo, hi);
-    return lo + hi;
-  }
-};
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-  Pair d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return d;
-}
-
-template <typename T>
-__device__ __forceinline__ void pairs_of(const Pack8<T>& p, Pair (&x)[4]) {
-  float v[8];
-  p.get(v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
-}
-
-__device__ __forceinline__ void pairs_of(const float (&v)[8], Pair (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
-}
-
-// Eight elements as four pairs, to 16 bytes of memory.
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i].get(v[2 * i], v[2 * i + 1]);
-  store8(p, v);
-}
-
 // W consecutive elements of a row: eight, on 16 bytes, or one.
 template <typename T, int W>
 struct Piece {
@@ -213,14 +157,6 @@ inline RowShape row_shape(int64_t hidden, int nv, int cta_warps) {
   s.rows = s.warps <= cta_warps ? cta_warps / s.warps : 1;
   s.threads = s.rows * s.warps * 32;
   return s;
-}
-
-// Eight elements of a ring's pieces as pairs.
-template <typename T>
-__device__ __forceinline__ void get_pairs(const OwnRing& ring, int piece, Pair (&x)[4]) {
-  Pack8<T> p;
-  ring.get(piece, p);
-  pairs_of(p, x);
 }
 
 // scale gate post of eight columns (factors that are not given left out).

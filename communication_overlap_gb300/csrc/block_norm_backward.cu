@@ -155,6 +155,13 @@ __device__ __forceinline__ void factor_of(const NormArgs& f, const void* p, int6
   for (int k = 0; k < 8; ++k) v[k] *= f.scale;
 }
 
+__device__ __forceinline__ void store_pairs(float* p, const Pair (&x)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i].get(v[2 * i], v[2 * i + 1]);
+  store8(p, v);
+}
+
 template <int W>
 __device__ __forceinline__ void store_parts(const NormBackArgs& a, const BackShape& n,
                                             int64_t worker, int col, const float (&dpre)[W],
@@ -192,11 +199,9 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
   bool has[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    // (threads without columns work on the row's first ones with parameters of zero,
-    // and store nothing)
+    // (threads without columns work on the zeros that the ring starts with)
     col[v] = (v * warps * 32 + g.tid) * 8;
     has[v] = col[v] < f.hidden;
-    if (!has[v]) col[v] = 0;
   }
   const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + g.index;
   const int t0 = int(min(worker * n.per_worker, int64_t(f.tokens)));
@@ -213,10 +218,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int at = stage * kPieces + v * kOf;
-        ring.fetch(at, x_at + col[v]);
-        if (f.pre != nullptr) ring.fetch(at + kA, dy_at + col[v]);
-        if (f.residual != nullptr) ring.fetch(at + 2 * kA, r_at + col[v]);
-        if (a.dsum != nullptr) ring.fetch(at + 2 * kA + kS, d_at + col[v]);
+        ring.fetch(at, x_at, col[v], f.hidden);
+        if (f.pre != nullptr) ring.fetch(at + kA, dy_at, col[v], f.hidden);
+        if (f.residual != nullptr) ring.fetch(at + 2 * kA, r_at, col[v], f.hidden);
+        if (a.dsum != nullptr) ring.fetch(at + 2 * kA + kS, d_at, col[v], f.hidden);
       }
     }
     OwnRing::commit();
@@ -230,6 +235,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < DEPTH * kPieces; i += 2) ring.put(i, none);
+    OwnRing::settle<A, S>();
   }
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) fetch(i);
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
         }
     }
     OwnRing::wait<DEPTH - 1>();
+    OwnRing::settle<A, S>();
     // (x and dy are kept as they lie in memory: a bf16 pair in one register, not two)
     Pack8<A> px[NV], py[NV];
     Pair sn[NV][4], d[NV][4];
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
       get_pairs<S>(ring, at + 2 * kA, sn[v]);
       get_pairs<S>(ring, at + 2 * kA + kS, d[v]);
     }
+    OwnRing::settle<A, S>();
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     const int next = t + 1 < t1 ? t + 1 : t;
@@ -335,10 +343,9 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
         o[i] = w[i] * d[v][i];
         if (f.post != nullptr) o[i] = Pair::of(r1) * fma2(Pair::of(-m1), xn, o[i]);
       }
-      if (!has[v]) continue;
       if (a.dresidual != nullptr)
-        store8(static_cast<S*>(a.dresidual) + (t * a.dresidual_stride + col[v]), d[v]);
-      store8(static_cast<A*>(a.dx) + (t * a.dx_stride + col[v]), o);
+        store8_warp(static_cast<S*>(a.dresidual) + (t * a.dresidual_stride + col[v]), has[v], d[v]);
+      store8_warp(static_cast<A*>(a.dx) + (t * a.dx_stride + col[v]), has[v], o);
     }
     r1 = next_r1, r2 = next_r2;
     if (t + 1 < gate_end) continue;
@@ -374,9 +381,9 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     if (!has[v]) continue;
-    if (f.pre != nullptr) store8(n.pre_part + worker * f.hidden + col[v], dpre[v]);
+    if (f.pre != nullptr) store_pairs(n.pre_part + worker * f.hidden + col[v], dpre[v]);
     if (GATES && f.post != nullptr)
-      store8(n.post_part + worker * f.hidden + col[v], dpost[GATES ? v : 0]);
+      store_pairs(n.post_part + worker * f.hidden + col[v], dpost[GATES ? v : 0]);
   }
 }
 
