@@ -300,10 +300,8 @@ __global__ void __launch_bounds__(kThreads, 3) combine_backward_kernel(const Com
       dot[j] = Pair::of(0.0f);
     }
     for (int c0 = 0; c0 < f.hidden; c0 += CHUNKS * stride) {
-      OwnRing::settle<T, O>();
       fetch(stage == 0 ? STAGES - 1 : stage - 1);
       OwnRing::wait<STAGES - 1>();
-      OwnRing::settle<T, O>();
 #pragma unroll
       for (int k = 0; k < CHUNKS; ++k) {
         const int c = col0 + c0 + k * stride, at = stage * kPieces + k * kOf;

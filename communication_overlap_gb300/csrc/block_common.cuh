@@ -148,11 +148,9 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// A ring in shared memory that a thread fills for itself, rows ahead of their use, so
-// that no barrier guards it: piece i of stage s lies at (s * pieces + i) * threads +
-// thread, 16 bytes each.  Of fp32 rows two neighbouring lanes fetch 32 bytes together
-// (half a sector each would be read from L2 twice), into each other's pieces: these
-// need a __syncwarp after a wait, and one between their reads and the next fetch.
+// A ring in shared memory that a thread fills for itself, rows ahead of their use: no
+// other thread reads its pieces, so no barrier guards them.  Piece i of stage s lies
+// at (s * pieces + i) * threads + thread, 16 bytes each.
 struct OwnRing {
   uint32_t base;        // of this thread's first piece
   uint32_t step;        // bytes from one piece to the next
@@ -160,28 +158,23 @@ struct OwnRing {
   __device__ __forceinline__ OwnRing(const void* smem)
       : base(smem_u32(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
   __device__ __forceinline__ uint32_t at(int piece) const { return base + uint32_t(piece) * step; }
-  __device__ __forceinline__ static void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  }
   // The row's eight elements from `col` on into the ring from piece `piece` on, where they
-  // exist (col < limit).  By whole warps; col is a multiple of 8 and goes with the lane.
+  // exist (col < limit).  A lane's eight fp32 values are two copies, each of half a
+  // sector per lane: through L1, where the second finds what the first brought.  (Past
+  // L1 both go to L2, whose tags then bind: 16384 x 4096 in fp32 at 4.7 TB/s.)
   template <typename T>
   __device__ __forceinline__ void fetch(int piece, const T* row, int col, int limit) const {
+    if (col >= limit) return;
     if constexpr (sizeof(T) == 2) {
-      if (col < limit) copy16(at(piece), row + col);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(piece)), "l"(row + col)
+                   : "memory");
     } else {
-      const int odd = (col >> 3) & 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = (col & ~8) | (h << 3);       // of the even lane, then of the odd one
-        if (c < limit) copy16(at(piece + odd) + (h - odd) * 16, row + c + odd * 4);
-      }
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at(piece)), "l"(row + col)
+                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at(piece + 1)),
+                   "l"(row + col + 4)
+                   : "memory");
     }
-  }
-  // After a wait, and before the next fetch, of rows of these types.
-  template <typename A, typename B>
-  __device__ __forceinline__ static void settle() {
-    if constexpr (sizeof(A) == 4 || sizeof(B) == 4) __syncwarp();
   }
   template <typename T>
   __device__ __forceinline__ void get(int piece, Pack8<T>& p) const {

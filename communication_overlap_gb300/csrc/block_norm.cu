@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
       gate_row = row;
     }
     OwnRing::wait<DEPTH - 1>();
-    OwnRing::settle<A, S>();
     Pair x[NV][4], s[NV][4];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -126,7 +125,6 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
         if (a.residual != nullptr) get_pairs<S>(ring, at + kA, s[v]);
       }
     }
-    OwnRing::settle<A, S>();
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     Pair r1 = Pair::of(1.0f);

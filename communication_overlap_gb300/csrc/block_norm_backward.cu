@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < DEPTH * kPieces; i += 2) ring.put(i, none);
-    OwnRing::settle<A, S>();
   }
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) fetch(i);
@@ -289,7 +288,6 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
         }
     }
     OwnRing::wait<DEPTH - 1>();
-    OwnRing::settle<A, S>();
     // (x and dy are kept as they lie in memory: a bf16 pair in one register, not two)
     Pack8<A> px[NV], py[NV];
     Pair sn[NV][4], d[NV][4];
@@ -301,7 +299,6 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
       get_pairs<S>(ring, at + 2 * kA, sn[v]);
       get_pairs<S>(ring, at + 2 * kA + kS, d[v]);
     }
-    OwnRing::settle<A, S>();
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     const int next = t + 1 < t1 ? t + 1 : t;
