@@ -31,12 +31,13 @@ from .moe import (_ACTS, _int32, _on_gpu, _row_stride, _run, _status_word, _stre
 _checkpoint_sizes = functools.lru_cache(256)(fo.fo_checkpoint_sizes)
 
 
-def _detached(*tensors):
-    _untracked(*(t for t in tensors if t is not None))
-
-
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
+
+
+def _stride(t, what):
+    """Row stride of a matrix, 0 of none."""
+    return 0 if t is None else _row_stride(t, what)
 
 
 def _matrix(t, shape, dtype, what):
@@ -50,8 +51,16 @@ def _matrix(t, shape, dtype, what):
 class Normed:
     stream: torch.Tensor                # the residual stream after the block
     y: Optional[torch.Tensor]           # the next block's input, where pre_gain was given
-    post_rstd: Optional[torch.Tensor]   # fp32 [tokens], for norm_backward
-    pre_rstd: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]        # fp32 [2, tokens], of the two norms: norm_backward
+                                        #   reads the rows whose gains were given
+
+    @property
+    def post_rstd(self):
+        return self.rstd[0]
+
+    @property
+    def pre_rstd(self):
+        return self.rstd[1]
 
 
 @dataclass
@@ -63,37 +72,50 @@ class NormGrads:
     pre_gain: Optional[torch.Tensor]
 
 
-def _norm_desc(x, residual, post_gain, gate, pre_gain, scale, eps):
-    """(device, tokens, hidden, description, the gate's row stride)"""
-    if x.dim() != 2:
-        raise ValueError("x: [tokens, hidden] expected")
-    dev = _on_gpu(x, residual, post_gain, gate, pre_gain)
-    T, H = x.shape
-    if residual is not None and residual.shape != x.shape:
-        raise ValueError(f"residual: {tuple(x.shape)} expected, not {tuple(residual.shape)}")
-    stream_type = x.dtype if residual is None else residual.dtype
-    if x.dtype == torch.float32 and stream_type != torch.float32:
+@functools.lru_cache(256)
+def _norm_desc(T, H, dtype, stream_dtype, param_dtype, gates, scale, eps):
+    if dtype == torch.float32 and stream_dtype != torch.float32:
         raise ValueError("a bf16 residual stream takes bf16 blocks")
-    params = [p for p in (post_gain, gate, pre_gain) if p is not None]
-    param_type = params[0].dtype if params else torch.float32
+    if gates < 1 or T % gates:
+        raise ValueError(f"gate: {gates} rows do not divide {T} tokens")
+    desc = fo.make_norm_desc(T, H, _type(dtype), _type(stream_dtype), _type(param_dtype), gates,
+                             scale, eps)
+    return desc, fo.fo_block_norm_workspace(desc)
+
+
+def _norm_args(x, residual, post_gain, gate, pre_gain, scale, eps):
+    """(device, tokens, hidden, (description, workspace bytes), the gate's row stride)"""
+    dev = _on_gpu(x, residual, post_gain, gate, pre_gain)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x: [tokens, hidden] expected")
+    T, H = shape
+    stream_dtype = x.dtype
+    if residual is not None:
+        stream_dtype = residual.dtype
+        if residual.shape != shape:
+            raise ValueError(f"residual: {tuple(shape)} expected, not {tuple(residual.shape)}")
+    param_dtype, gates, gate_stride = None, 1, 0
     for p, what in ((post_gain, "post_gain"), (pre_gain, "pre_gain")):
-        if p is not None and (tuple(p.shape) != (H,) or not p.is_contiguous()):
+        if p is None:
+            continue
+        if p.shape != (H,) or not p.is_contiguous():
             raise ValueError(f"{what}: contiguous [{H}] expected, not {tuple(p.shape)}")
-    if any(p.dtype != param_type for p in params):
-        raise ValueError("the gains and the gate have one type")
-    gates, gate_stride = 1, 0
+        if param_dtype is not None and p.dtype != param_dtype:
+            raise ValueError("the gains and the gate have one type")
+        param_dtype = p.dtype
     if gate is not None:
         if gate.dim() == 2 and gate.shape[1] == H:
             gates, gate_stride = gate.shape[0], _row_stride(gate, "gate")
-        elif tuple(gate.shape) == (H,) and gate.is_contiguous():
+        elif gate.shape == (H,) and gate.is_contiguous():
             gate_stride = H
         else:
             raise ValueError(f"gate: [{H}] or [rows, {H}] expected, not {tuple(gate.shape)}")
-        if gates < 1 or T % gates:
-            raise ValueError(f"gate: {gates} rows do not divide {T} tokens")
-    desc = fo.make_norm_desc(T, H, _type(x.dtype), _type(stream_type), _type(param_type), gates,
-                             scale, eps)
-    return dev, T, H, desc, gate_stride
+        if param_dtype is not None and gate.dtype != param_dtype:
+            raise ValueError("the gains and the gate have one type")
+        param_dtype = gate.dtype
+    return dev, T, H, _norm_desc(T, H, x.dtype, stream_dtype, param_dtype or torch.float32, gates,
+                                 scale, eps), gate_stride
 
 
 def norm(x, residual=None, post_gain=None, gate=None, scale=1.0, pre_gain=None, eps=1e-6):
@@ -106,20 +128,24 @@ def norm(x, residual=None, post_gain=None, gate=None, scale=1.0, pre_gain=None, 
     [hidden], or [rows, hidden] where rows divides tokens (a row for each run of
     tokens / rows tokens); all of one type.  Where nothing but pre_gain is
     given, the stream is x itself."""
-    _detached(x, residual, post_gain, gate, pre_gain)
-    dev, T, H, desc, gate_stride = _norm_desc(x, residual, post_gain, gate, pre_gain, scale, eps)
+    _untracked(x, residual, post_gain, gate, pre_gain)
+    dev, T, H, (desc, _), gate_stride = _norm_args(x, residual, post_gain, gate, pre_gain, scale,
+                                                   eps)
+    stream, y, rstd, at = x, None, None, 0
     summed = residual is not None or post_gain is not None or gate is not None or scale != 1.0
-    empty = torch.empty
-    stream = empty((T, H), dtype=x.dtype if residual is None else residual.dtype,
-                   device=dev) if summed else x
-    y = None if pre_gain is None else empty((T, H), dtype=x.dtype, device=dev)
-    post_rstd = None if post_gain is None else empty(T, dtype=torch.float32, device=dev)
-    pre_rstd = None if pre_gain is None else empty(T, dtype=torch.float32, device=dev)
+    if summed:
+        stream = torch.empty((T, H), dtype=x.dtype if residual is None else residual.dtype,
+                             device=dev)
+    if pre_gain is not None:
+        y = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if pre_gain is not None or post_gain is not None:
+        rstd = torch.empty((2, T), dtype=torch.float32, device=dev)
+        at = rstd.data_ptr()
     _run(dev, fo.fo_block_norm, desc, x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
-         0 if residual is None else _row_stride(residual, "residual"), _ptr(post_gain),
-         _ptr(gate), gate_stride, _ptr(pre_gain), stream.data_ptr() if summed else 0, H, _ptr(y),
-         H, _ptr(post_rstd), _ptr(pre_rstd), _stream(dev))
-    return Normed(stream, y, post_rstd, pre_rstd)
+         _stride(residual, "residual"), _ptr(post_gain), _ptr(gate), gate_stride, _ptr(pre_gain),
+         stream.data_ptr() if summed else 0, H, _ptr(y), H, at, at + 4 * T if at else 0,
+         _stream(dev))
+    return Normed(stream, y, rstd)
 
 
 def norm_backward(x, residual, normed, dstream=None, dy=None, post_gain=None, gate=None,
@@ -127,32 +153,34 @@ def norm_backward(x, residual, normed, dstream=None, dy=None, post_gain=None, ga
     """The gradients of norm's inputs and parameters, from those of its stream
     (None: zeros) and of its y (None where there was none).  x, residual and the
     parameters: the forward call's; normed: what it returned."""
-    _detached(x, residual, post_gain, gate, pre_gain, dstream, dy)
-    dev, T, H, desc, gate_stride = _norm_desc(x, residual, post_gain, gate, pre_gain, scale, 0.0)
-    _on_gpu(x, dstream, dy, normed.post_rstd, normed.pre_rstd)
+    _untracked(x, residual, post_gain, gate, pre_gain, dstream, dy)
+    dev, T, H, (desc, nbytes), gate_stride = _norm_args(x, residual, post_gain, gate, pre_gain,
+                                                        scale, 0.0)
+    rstd = normed.rstd
+    _on_gpu(x, dstream, dy, rstd)
     if (dy is None) != (pre_gain is None):
         raise ValueError("dy and pre_gain go together")
     if dy is not None:
         _matrix(dy, (T, H), x.dtype, "dy")
     if dstream is not None:
         _matrix(dstream, (T, H), x.dtype if residual is None else residual.dtype, "dstream")
-    for gain, rstd, what in ((post_gain, normed.post_rstd, "post"),
-                             (pre_gain, normed.pre_rstd, "pre")):
-        if gain is not None and (rstd is None or tuple(rstd.shape) != (T,)):
-            raise ValueError(f"normed holds no {what}_rstd of {T} tokens")
+    at = 0
+    if post_gain is not None or pre_gain is not None:
+        if rstd is None or rstd.shape != (2, T) or not rstd.is_contiguous():
+            raise ValueError(f"normed holds no norms of {T} tokens")
+        at = rstd.data_ptr()
     empty, like = torch.empty, torch.empty_like
     dx = empty((T, H), dtype=x.dtype, device=dev)
     dresidual = None if residual is None else empty((T, H), dtype=residual.dtype, device=dev)
     dpost = None if post_gain is None else like(post_gain)
     dpre = None if pre_gain is None else like(pre_gain)
     dgate = None if gate is None else empty(gate.shape, dtype=gate.dtype, device=dev)
-    ws = empty(fo.fo_block_norm_workspace(desc), dtype=torch.uint8, device=dev)
+    ws = empty(nbytes, dtype=torch.uint8, device=dev)
     _run(dev, fo.fo_block_norm_backward, desc, x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
-         0 if residual is None else _row_stride(residual, "residual"), _ptr(post_gain),
-         _ptr(gate), gate_stride, _ptr(pre_gain), _ptr(normed.post_rstd), _ptr(normed.pre_rstd),
-         _ptr(dstream), 0 if dstream is None else _row_stride(dstream, "dstream"), _ptr(dy),
-         0 if dy is None else _row_stride(dy, "dy"), dx.data_ptr(), H, _ptr(dresidual), H,
-         _ptr(dpost), _ptr(dgate), _ptr(dpre), ws.data_ptr(), _stream(dev))
+         _stride(residual, "residual"), _ptr(post_gain), _ptr(gate), gate_stride, _ptr(pre_gain),
+         at, at + 4 * T if at else 0, _ptr(dstream), _stride(dstream, "dstream"), _ptr(dy),
+         _stride(dy, "dy"), dx.data_ptr(), H, _ptr(dresidual), H, _ptr(dpost), _ptr(dgate),
+         _ptr(dpre), ws.data_ptr(), _stream(dev))
     return NormGrads(dx, dresidual, dpost, dgate, dpre)
 
 
@@ -181,7 +209,7 @@ def activate(u, act="silu", checkpoint=False):
     """h = act(gate) * up for rows u = [gate | up] (bf16 or fp32, any row stride),
     and with checkpoint what activate_backward needs of u, in 8 bits: (h, kept),
     kept None without."""
-    _detached(u)
+    _untracked(u)
     if u.dim() != 2 or u.shape[1] % 2:
         raise ValueError("u: [rows, 2 * inter] expected")
     dev, type_ = _on_gpu(u), _type(u.dtype)
@@ -203,7 +231,7 @@ def activate(u, act="silu", checkpoint=False):
 def activate_backward(dh, kept):
     """The gradient of u (in dh's type) from that of h, with the values that the
     checkpoint stands for."""
-    _detached(dh)
+    _untracked(dh)
     if tuple(dh.shape) != (kept.rows, kept.inter):
         raise ValueError(f"dh: {(kept.rows, kept.inter)} expected, not {tuple(dh.shape)}")
     dev, type_ = _on_gpu(dh, kept.codes, kept.scales), _type(dh.dtype)
@@ -230,7 +258,7 @@ def combine(rows, token_row, weights=None, out=None, out_dtype=None):
     """y[t] = sum over slots s of weights[t, s] * rows[token_row[t, s]] (-1: no
     row; no weights: ones).  rows: [table rows, hidden], bf16 or fp32, any row
     stride; token_row and weights as a Routing holds them."""
-    _detached(rows, weights)
+    _untracked(rows, weights)
     if rows.dim() != 2:
         raise ValueError("rows: [table rows, hidden] expected")
     T, k = _slots(token_row, weights)
@@ -250,7 +278,7 @@ def combine_backward(dy, rows, token_row, row_token, weights=None):
     """(drows, dweights): drows has rows' type, with zeros where a row holds no
     token; dweights (fp32) is None without weights.  token_row and row_token: of
     one Routing."""
-    _detached(dy, rows, weights)
+    _untracked(dy, rows, weights)
     if rows.dim() != 2:
         raise ValueError("rows: [table rows, hidden] expected")
     T, k = _slots(token_row, weights)

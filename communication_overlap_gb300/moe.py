@@ -51,9 +51,12 @@ def _on_gpu(first, *others):
 
 
 def _untracked(*tensors):
-    """Refuses tensors whose gradient a call would lose without a word."""
+    """Refuses tensors whose gradient a call would lose without a word (None entries
+    are skipped)."""
+    if not torch.is_grad_enabled():
+        return
     for t in tensors:
-        if t.requires_grad and torch.is_grad_enabled():
+        if t is not None and t.requires_grad:
             raise ValueError("no gradient flows through this call: detach its tensors, or call it "
                              "under torch.no_grad() (route_backward is the router's gradient)")
 
@@ -294,22 +297,23 @@ def route(logits, top_k, renormalize=True, capacity=0, scoring="softmax", bias=N
         desc = fo.make_route_desc(E, top_k, renormalize, capacity, top_groups=top_groups,
                                   group_top=group_top)
     # (seven allocations are cheaper than one and seven views of it)
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
-    ids, token_row, row_token, row_slot = new(T, top_k), new(T, top_k), new(M), new(M)
-    first, rows = new(E), new(E)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    empty, i32 = torch.empty, torch.int32
+    ids = empty((T, top_k), dtype=i32, device=dev)
+    token_row = empty((T, top_k), dtype=i32, device=dev)
+    row_token = empty(M, dtype=i32, device=dev)
+    row_slot = empty(M, dtype=i32, device=dev)
+    first, rows = empty(E, dtype=i32, device=dev), empty(E, dtype=i32, device=dev)
+    weights = empty((T, top_k), dtype=torch.float32, device=dev)
     ws = _workspace("route", dev, nbytes)
+    to = (ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(), row_slot.data_ptr(),
+          token_row.data_ptr(), first.data_ptr(), rows.data_ptr(), ws.data_ptr(),
+          _status_word(dev), _stream(dev))
     if desc is None:
         _run(dev, fo.fo_moe_route, logits.data_ptr(), type_, T, E, _row_stride(logits, "logits"),
-             top_k, renormalize, capacity, ids.data_ptr(), weights.data_ptr(),
-             row_token.data_ptr(), row_slot.data_ptr(), token_row.data_ptr(), first.data_ptr(),
-             rows.data_ptr(), ws.data_ptr(), _status_word(dev), _stream(dev))
+             top_k, renormalize, capacity, *to)
     else:
         _run(dev, fo.fo_moe_route_scored, desc, logits.data_ptr(), type_, T,
-             _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(),
-             ids.data_ptr(), weights.data_ptr(), row_token.data_ptr(), row_slot.data_ptr(),
-             token_row.data_ptr(), first.data_ptr(), rows.data_ptr(), ws.data_ptr(),
-             _status_word(dev), _stream(dev))
+             _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(), *to)
     return Routing(ids, weights, row_token, row_slot, token_row, first, rows)
 
 
