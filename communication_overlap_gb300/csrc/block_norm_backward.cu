@@ -553,6 +553,7 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
 
 // Both means of every token, and the workers' parts.
 int64_t block_norm_workspace_bytes(int64_t tokens, int64_t hidden, int64_t gates) {
+  if (hidden == 0) return 16;
   int64_t workers = column_workers(hidden, 8, kMaxSms);
   if (hidden <= 8192 && workers < whole_workers(hidden, kMaxSms))
     workers = whole_workers(hidden, kMaxSms);
