@@ -1,27 +1,36 @@
-"""An expert layer made of the operators of ``moe.py``, as a model runs it.
+"""An expert layer made of the operators of ``moe.py``, as a model runs it, and the
+block around it, with those of ``block.py``.
 
   layer = ExpertLayer.random(hidden, inter, experts, top_k)
   y = layer(x)                       # many tokens: a prompt; few: a generation step
   y, step = layer.forward(x)         # the same, and what a backward pass needs
   dlogits, dx = layer.backward(step, dweights, dup)
 
+  block = ExpertBlock.random(hidden, inter, experts, top_k, routing=dict(scoring="sigmoid"))
+  stream = block(stream)             # norm, router, experts, norm, gate, residual
+  stream, step = block.forward(stream)
+  grads = block.backward(step, dstream)
+
 Weights are kept once, in the 4-bit form.  Up to fo.FO_MOE_FEW_TOKENS tokens
 go through the one-kernel layer, which reads only the experts that are chosen.
 More go through the router, the gathering quantizer and one product per
-projection over all experts; the router's logits, the activation between the
-projections and the weighted sum of a token's rows are plain torch operations.
+projection over all experts; in ExpertLayer the router's logits, the activation
+between the projections and the weighted sum of a token's rows are plain torch
+operations, in ExpertBlock only the logits and their gradient are.
 Neither way is part of autograd: backward is called with gradients, and tensors
 that require one are refused.
 
 ``python -m communication_overlap_gb300.expert_layer`` runs a prompt, a
-gradient and some generation steps (the last ones replayed from a CUDA graph)
-and prints what they took.
+gradient, some generation steps (the last ones replayed from a CUDA graph) and
+a block's forward and backward pass, and prints what they took.
 """
 import argparse
 from dataclasses import dataclass
+from typing import Optional
 
 import torch
 
+from . import block as ops
 from . import fo, moe
 
 
@@ -102,6 +111,112 @@ class ExpertLayer:
         return dlogits, dx
 
 
+@dataclass
+class BlockStep:
+    """What a block's forward leaves for its backward: of the experts' inner values
+    the 8-bit checkpoint alone."""
+    stream: torch.Tensor
+    before: ops.Normed
+    logits: torch.Tensor
+    routing: moe.Routing
+    kept: ops.Checkpoint
+    rows: torch.Tensor
+    mixed: torch.Tensor
+    after: ops.Normed
+
+
+@dataclass
+class BlockGrads:
+    stream: torch.Tensor
+    router: torch.Tensor                    # fp32
+    pre_gain: torch.Tensor
+    post_gain: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+
+
+class ExpertBlock:
+    """A model's block with an expert layer:
+
+      n = RMS norm of the stream times pre_gain
+      z = the experts' outputs for n, weighted by the router
+      stream + scale * gate * (RMS norm of z times post_gain)
+
+    layer: an ExpertLayer (its w1_t, and here w2_t, for backward: the transpose of
+    w2, quantized along its own rows).  post_gain and gate may be None.  routing: a
+    dict of moe.route's options beyond those of the layer (scoring, bias, groups,
+    top_groups, group_top, scale).  The stream is bf16 [tokens, hidden].  The
+    experts' weights are not trained (they are in 4 bits): backward gives the
+    gradients of the stream, the router and the norms' parameters."""
+
+    def __init__(self, layer, pre_gain, post_gain=None, gate=None, scale=1.0, eps=1e-6, w2_t=None,
+                 routing=None):
+        self.layer, self.w2_t = layer, w2_t
+        self.pre_gain, self.post_gain, self.gate = pre_gain, post_gain, gate
+        self.scale, self.eps, self.routing = scale, eps, routing or {}
+
+    @classmethod
+    def random(cls, hidden, inter, experts, top_k, seed=0, device="cuda", scale=1.0, routing=None):
+        """Seeded weights as ExpertLayer.random's, gains about 1, a gate about 1/2."""
+        layer = ExpertLayer.random(hidden, inter, experts, top_k, seed, device)
+        g = torch.Generator(device=device).manual_seed(seed + 1)
+        near = lambda at: (at + 0.1 * torch.randn(hidden, generator=g, device=device)).bfloat16()
+        # (w2 once more, from the values that its 4-bit form stands for)
+        w2_t = moe.quantize(moe.dequantize(layer.w2), transpose=True)
+        return cls(layer, near(1.0), near(1.0), near(0.5), scale, w2_t=w2_t, routing=routing)
+
+    def __call__(self, stream):
+        layer = self.layer
+        if stream.shape[0] <= fo.FO_MOE_FEW_TOKENS and not self.routing:
+            n = ops.norm(stream, pre_gain=self.pre_gain, eps=self.eps)
+            return self._join(layer.few(n.y), stream).stream
+        return self._forward(stream, False)[0]
+
+    def forward(self, stream):
+        return self._forward(stream, True)
+
+    def _join(self, z, stream):
+        return ops.norm(z, stream, self.post_gain, self.gate, self.scale, eps=self.eps)
+
+    def _forward(self, stream, keep):
+        layer = self.layer
+        n = ops.norm(stream, pre_gain=self.pre_gain, eps=self.eps)
+        logits = torch.mm(n.y, layer.router.t(), out_dtype=torch.float32)
+        r = moe.route(logits, layer.top_k, layer.renormalize, **self.routing)
+        # (rows of no expert are left as they are, and nothing reads them)
+        up = self._product(moe.quantize(n.y, row_index=r.row_token), layer.w1, r)
+        h, kept = ops.activate(up, checkpoint=keep)
+        rows = self._product(moe.quantize(h), layer.w2, r)
+        z = ops.combine(rows, r.token_row, r.weights)
+        after = self._join(z, stream)
+        return after.stream, BlockStep(stream, n, logits, r, kept, rows, z, after) if keep else None
+
+    @staticmethod
+    def _product(a, w, r):
+        out = torch.empty((a.rows, w.rows), dtype=torch.bfloat16, device=a.codes.device)
+        return moe.mx_gemm(a, w, out=out, group_first=r.expert_first, group_rows=r.expert_rows)
+
+    def backward(self, step, dstream):
+        """The gradients from that of the stream after the block (bf16)."""
+        layer, r = self.layer, step.routing
+        if layer.w1_t is None or self.w2_t is None:
+            raise ValueError("backward needs w1_t and w2_t")
+        after = ops.norm_backward(step.mixed, step.stream, step.after, dstream,
+                                  post_gain=self.post_gain, gate=self.gate, scale=self.scale)
+        drows, dweights = ops.combine_backward(after.x, step.rows, r.token_row, r.row_token,
+                                               r.weights)
+        dh = self._product(moe.quantize(drows), self.w2_t, r)
+        dup = ops.activate_backward(dh, step.kept)
+        dn = ops.combine(self._product(moe.quantize(dup), layer.w1_t, r), r.token_row)
+        how = {k: v for k, v in self.routing.items() if k in ("scoring", "scale")}
+        dlogits = moe.route_backward(step.logits, r.ids, r.weights, dweights, layer.renormalize,
+                                     **how).to(torch.bfloat16)
+        dn.addmm_(dlogits, layer.router)
+        drouter = torch.mm(dlogits.t(), step.before.y, out_dtype=torch.float32)
+        before = ops.norm_backward(step.stream, None, step.before, after.residual, dn,
+                                   pre_gain=self.pre_gain)
+        return BlockGrads(before.x, drouter, before.pre_gain, after.post_gain, after.gate)
+
+
 def _timed(what, call, n=5):
     call()
     s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -137,6 +252,13 @@ def main(argv=None):
     off = ((out.float() - few).norm() / few.norm()).item()
     print(f"the prompt's first token against generation's: {off:.3f} apart (the prompt's "
           "activations are 4-bit)")
+    bias = torch.zeros(a.experts, device="cuda")
+    block = ExpertBlock.random(a.hidden, a.inter, a.experts, a.top_k,
+                               routing=dict(scoring="sigmoid", bias=bias, scale=2.5))
+    _, step = _timed(f"a block's forward pass, {a.tokens} tokens", lambda: block.forward(x))
+    dstream = torch.randn_like(x)
+    _timed("its backward pass", lambda: block.backward(step, dstream))
+    _timed("a block of 1 token", lambda: block(x[:1]))
     if moe.device_status() != fo.FO_OK:
         raise SystemExit(fo.fo_status_string(moe.device_status()))
 
