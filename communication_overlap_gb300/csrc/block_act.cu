@@ -140,34 +140,28 @@ struct ActArgs {
   int32_t pieces, chunks, per_cta;    // the grid's shape, in threads' chunks
 };
 
-// A thread's first row and first column: of eight columns where VEC, else of one.
-// It has `rows` rows, `per_cta` apart.
+// A thread's first row and first of eight columns.  It has `rows` rows, `per_cta` apart.
 struct Place {
   int64_t row;
   int col;
   bool live;      // the column exists, and the thread has a row's place
 };
-__device__ __forceinline__ Place place(const ActArgs& a, int width, int rows) {
+__device__ __forceinline__ Place place(const ActArgs& a, int rows) {
   const int piece = int(blockIdx.x % unsigned(a.pieces));
   const int64_t r0 = int64_t(blockIdx.x / unsigned(a.pieces)) * a.per_cta * rows;
   const int local = a.pieces > 1 ? 0 : int(threadIdx.x) / a.chunks;
   const int c = a.pieces > 1 ? piece * kThreads + int(threadIdx.x) : int(threadIdx.x) % a.chunks;
   Place p;
   p.row = r0 + local;
-  p.col = c * width;
+  p.col = c * 8;
   p.live = local < a.per_cta && p.col < a.padded;
   return p;
 }
 
-// Four neighbouring lanes (VEC) or a warp hold a block of 32.
-template <bool VEC>
+// The largest over the four neighbouring lanes that hold a block of 32.
 __device__ __forceinline__ uint32_t block_max(uint32_t m) {
-  if constexpr (VEC) {
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  } else {
-    return __reduce_max_sync(0xffffffffu, m);
-  }
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
 __device__ __forceinline__ void store_scales(const ActArgs& a, int64_t row, int col, uint32_t sg,
@@ -183,7 +177,7 @@ __device__ __forceinline__ void store_scales(const ActArgs& a, int64_t row, int 
 // whose loads are all under way at once.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads) act_kernel(const ActArgs a) {
-  const Place p = place(a, 8, ROWS);
+  const Place p = place(a, ROWS);
   const bool in = p.live && p.col < a.inter;
   Pack8<T> pg[ROWS], pu[ROWS];
   const T* src = static_cast<const T*>(a.u) + p.row * a.u_stride + p.col;
@@ -209,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const ActArgs a) {
     for (int i = 0; i < 8; ++i) h[i] = gated<T>(g[i], u[i], a.act);
     store8_warp(static_cast<T*>(a.h) + row * a.h_stride + p.col, live && in, h);
     if (a.codes == nullptr) continue;
-    const uint32_t mg = block_max<true>(amax_of(pg[r])), mu = block_max<true>(amax_of(pu[r]));
+    const uint32_t mg = block_max(amax_of(pg[r])), mu = block_max(amax_of(pu[r]));
     if (!live) continue;
     const uint32_t sg = step_byte(mg), su = step_byte(mu);
     int8_t* to = a.codes + row * 2 * a.padded + p.col;
@@ -219,33 +213,91 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const ActArgs a) {
   }
 }
 
-// Any rows: a column per thread, a warp to a block of 32.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a) {
-  const Place p = place(a, 1, 1);
-  const bool live = p.live && p.row < a.rows, in = live && p.col < a.inter;
-  const T* src = static_cast<const T*>(a.u) + p.row * a.u_stride + p.col;
-  float g = 0.0f, u = 0.0f;
-  if (in) {
-    g = widen(__ldcs(src));
-    u = widen(__ldcs(src + a.inter));
-    static_cast<T*>(a.h)[p.row * a.h_stride + p.col] = narrow<T>(gated<T>(g, u, a.act));
+// Rows that need not lie on 16 bytes: a warp takes kUnits times 32 E columns of a row, a
+// lane E neighbouring ones of each 32 E, so that its loads and stores are of
+// neighbouring addresses (one column per thread took 325 us for 16384 x 4095 of bf16).
+constexpr int kUnits = 8;
+
+// The largest over the lanes that hold a block of 32 columns.
+template <int E>
+__device__ __forceinline__ uint32_t few_max(uint32_t m) {
+  if constexpr (E == 1) {
+    return __reduce_max_sync(0xffffffffu, m);
+  } else {
+#pragma unroll
+    for (int o = 1; o < 32 / E; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
   }
-  if (a.codes == nullptr) return;
-  const uint32_t mg = block_max<false>(__float_as_uint(g) & 0x7fffffffu);
-  const uint32_t mu = block_max<false>(__float_as_uint(u) & 0x7fffffffu);
-  if (!live) return;
-  const uint32_t sg = step_byte(mg), su = step_byte(mu);
-  int8_t* to = a.codes + p.row * 2 * a.padded + p.col;
-  to[0] = int8_t(code_of(g, inverse_step(sg), sg));
-  to[a.padded] = int8_t(code_of(u, inverse_step(su), su));
-  store_scales(a, p.row, p.col, sg, su);
+}
+
+// A warp's row and first column.
+struct WarpPlace {
+  int64_t row;
+  int col;
+};
+template <int E>
+__device__ __forceinline__ WarpPlace warp_place(const ActArgs& a) {
+  const int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  return {item / a.pieces, int(item % a.pieces) * kUnits * 32 * E};
+}
+
+template <typename T, int E>
+__global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a) {
+  const WarpPlace p = warp_place<E>(a);
+  if (p.row >= a.rows) return;
+  const int lane = threadIdx.x & 31, first = p.col + lane * E;
+  const T* src = static_cast<const T*>(a.u) + p.row * a.u_stride + first;
+  T* dst = static_cast<T*>(a.h) + p.row * a.h_stride + first;
+  Few<T, E> pg[kUnits], pu[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    pg[i].zero();
+    pu[i].zero();
+    if (first + i * 32 * E < a.inter) {
+      pg[i].load(src + i * 32 * E);
+      pu[i].load(src + a.inter + i * 32 * E);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int col = first + i * 32 * E;
+    if (p.col + i * 32 * E >= a.padded) break;      // (the same for the warp)
+    float g[E], u[E], h[E];
+    pg[i].get(g);
+    pu[i].get(u);
+    if (col < a.inter) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = gated<T>(g[e], u[e], a.act);
+      Few<T, E>::store(dst + i * 32 * E, h);
+    }
+    if (a.codes == nullptr) continue;
+    uint32_t mg = 0, mu = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      mg = max(mg, __float_as_uint(g[e]) & 0x7fffffffu);
+      mu = max(mu, __float_as_uint(u[e]) & 0x7fffffffu);
+    }
+    const uint32_t sg = step_byte(few_max<E>(mg)), su = step_byte(few_max<E>(mu));
+    if (col >= a.padded) continue;
+    int8_t* to = a.codes + p.row * 2 * a.padded + col;
+    const float ig = inverse_step(sg), iu = inverse_step(su);
+    if constexpr (E == 1) {
+      to[0] = int8_t(code_of(g[0], ig, sg));
+      to[a.padded] = int8_t(code_of(u[0], iu, su));
+    } else {
+      const auto two = [](int x, int y) { return uint16_t((x & 255) | (y & 255) << 8); };
+      *reinterpret_cast<uint16_t*>(to) = two(code_of(g[0], ig, sg), code_of(g[E - 1], ig, sg));
+      *reinterpret_cast<uint16_t*>(to + a.padded) =
+          two(code_of(u[0], iu, su), code_of(u[E - 1], iu, su));
+    }
+    store_scales(a, p.row, col, sg, su);
+  }
 }
 
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a, const void* dh,
                                                                void* du) {
-  const Place p = place(a, 8, ROWS);
+  const Place p = place(a, ROWS);
   const bool in = p.live && p.col < a.inter;
   const int blocks = a.padded / kCheckpointBlock;
   Pack8<T> pd[ROWS];
@@ -283,38 +335,64 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a,
   }
 }
 
-template <typename T>
+template <typename T, int E>
 __global__ void __launch_bounds__(kThreads) act_backward_any_kernel(const ActArgs a,
                                                                    const void* dh, void* du) {
-  const Place p = place(a, 1, 1);
-  if (!p.live || p.row >= a.rows || p.col >= a.inter) return;
+  const WarpPlace p = warp_place<E>(a);
+  if (p.row >= a.rows) return;
+  const int lane = threadIdx.x & 31, first = p.col + lane * E;
   const int blocks = a.padded / kCheckpointBlock;
-  const int8_t* from = a.codes + p.row * 2 * a.padded + p.col;
-  const uint8_t* s = a.scales + p.row * 2 * blocks + p.col / kCheckpointBlock;
-  const float d = widen(__ldcs(static_cast<const T*>(dh) + p.row * a.h_stride + p.col));
-  const float g = float(from[0]) * step_value(__ldg(s));
-  const float u = float(from[a.padded]) * step_value(__ldg(s + blocks));
-  float og, ou;
-  gated_backward<T>(d, g, u, a.act, og, ou);
-  T* dst = static_cast<T*>(du) + p.row * a.u_stride + p.col;
-  dst[0] = narrow<T>(og);
-  dst[a.inter] = narrow<T>(ou);
+  const T* src = static_cast<const T*>(dh) + p.row * a.h_stride + first;
+  T* dst = static_cast<T*>(du) + p.row * a.u_stride + first;
+  const int8_t* codes = a.codes + p.row * 2 * a.padded + first;
+  const uint8_t* scales = a.scales + p.row * 2 * blocks;
+  Few<T, E> pd[kUnits];
+  uint32_t qg[kUnits], qu[kUnits], sg[kUnits], su[kUnits];
+  const auto load = [](const int8_t* p) {
+    return E == 1 ? uint32_t(uint8_t(*p)) : uint32_t(*reinterpret_cast<const uint16_t*>(p));
+  };
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int col = first + i * 32 * E;
+    if (col >= a.inter) continue;
+    pd[i].load(src + i * 32 * E);
+    qg[i] = load(codes + i * 32 * E);
+    qu[i] = load(codes + a.padded + i * 32 * E);
+    sg[i] = __ldg(scales + col / kCheckpointBlock);
+    su[i] = __ldg(scales + blocks + col / kCheckpointBlock);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (first + i * 32 * E >= a.inter) continue;
+    float d[E], og[E], ou[E];
+    pd[i].get(d);
+    const float vg = step_value(sg[i]), vu = step_value(su[i]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      gated_backward<T>(d[e], float(int8_t(qg[i] >> (8 * e))) * vg,
+                        float(int8_t(qu[i] >> (8 * e))) * vu, a.act, og[e], ou[e]);
+    Few<T, E>::store(dst + i * 32 * E, og);
+    Few<T, E>::store(dst + a.inter + i * 32 * E, ou);
+  }
 }
 
-bool on_16(const void* p, int64_t stride, fo_type type) {
-  const int64_t size = type == FO_TYPE_BF16 ? 2 : 4;
-  return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) & 15) == 0;
-}
-
-// The grid over rows x padded columns, a chunk of `width` columns of `rows` rows per
+// The grid over rows x padded columns, a chunk of eight columns of `rows` rows per
 // thread; false where it has too many CTAs.
-bool grid_of(ActArgs* a, int width, int rows, int64_t* grid) {
-  const int64_t chunks = a->padded / width;
+bool grid_of(ActArgs* a, int rows, int64_t* grid) {
+  const int64_t chunks = a->padded / 8;
   a->pieces = int32_t((chunks + kThreads - 1) / kThreads);
   a->chunks = int32_t(chunks < kThreads ? chunks : kThreads);
   a->per_cta = a->pieces > 1 ? 1 : kThreads / a->chunks;
   const int64_t of_cta = int64_t(a->per_cta) * rows;
   *grid = (int64_t(a->rows) + of_cta - 1) / of_cta * a->pieces;
+  return *grid < (int64_t(1) << 31);
+}
+
+// The grid of warps over rows and pieces of kUnits * 32 * E columns.
+bool grid_of_warps(ActArgs* a, int e, int64_t* grid) {
+  const int width = kUnits * 32 * e;
+  a->pieces = (a->padded + width - 1) / width;
+  *grid = (int64_t(a->rows) * a->pieces + kThreads / 32 - 1) / (kThreads / 32);
   return *grid < (int64_t(1) << 31);
 }
 
@@ -334,10 +412,14 @@ fo_status launch_gated_act(const void* u, fo_type type, int64_t rows, int64_t in
   a.u = u, a.h = h, a.u_stride = u_stride, a.h_stride = h_stride;
   a.codes = static_cast<int8_t*>(codes), a.scales = static_cast<uint8_t*>(scales);
   a.rows = int32_t(rows), a.inter = int32_t(inter), a.padded = padded_of(inter), a.act = act;
-  const bool vec = inter % 8 == 0 && on_16(u, u_stride, type) && on_16(h, h_stride, type);
+  const bool vec = inter % 8 == 0 && rows_on(u, u_stride, type, 16) &&
+                   rows_on(h, h_stride, type, 16);
+  const bool two = inter % 2 == 0 && rows_on_two(u, u_stride, type) &&
+                   rows_on_two(h, h_stride, type);
   const bool bf16 = type == FO_TYPE_BF16;
   int64_t grid = 0;
-  if (!grid_of(&a, vec ? 8 : 1, !vec ? 1 : bf16 ? kRowsOf2 : kRowsOf4, &grid))
+  if (!(vec ? grid_of(&a, bf16 ? kRowsOf2 : kRowsOf4, &grid)
+            : grid_of_warps(&a, two ? 2 : 1, &grid)))
     return FO_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned n = unsigned(grid);
@@ -345,10 +427,14 @@ fo_status launch_gated_act(const void* u, fo_type type, int64_t rows, int64_t in
     act_kernel<uint16_t, kRowsOf2><<<n, kThreads, 0, st>>>(a);
   else if (vec)
     act_kernel<float, kRowsOf4><<<n, kThreads, 0, st>>>(a);
+  else if (bf16 && two)
+    act_any_kernel<uint16_t, 2><<<n, kThreads, 0, st>>>(a);
   else if (bf16)
-    act_any_kernel<uint16_t><<<n, kThreads, 0, st>>>(a);
+    act_any_kernel<uint16_t, 1><<<n, kThreads, 0, st>>>(a);
+  else if (two)
+    act_any_kernel<float, 2><<<n, kThreads, 0, st>>>(a);
   else
-    act_any_kernel<float><<<n, kThreads, 0, st>>>(a);
+    act_any_kernel<float, 1><<<n, kThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
@@ -361,10 +447,14 @@ fo_status launch_gated_act_backward(const void* dh, fo_type type, int64_t rows, 
   a.codes = static_cast<int8_t*>(const_cast<void*>(codes));
   a.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
   a.rows = int32_t(rows), a.inter = int32_t(inter), a.padded = padded_of(inter), a.act = act;
-  const bool vec = inter % 8 == 0 && on_16(dh, dh_stride, type) && on_16(du, du_stride, type);
+  const bool vec = inter % 8 == 0 && rows_on(dh, dh_stride, type, 16) &&
+                   rows_on(du, du_stride, type, 16);
+  const bool two = inter % 2 == 0 && rows_on_two(dh, dh_stride, type) &&
+                   rows_on_two(du, du_stride, type);
   const bool bf16 = type == FO_TYPE_BF16;
   int64_t grid = 0;
-  if (!grid_of(&a, vec ? 8 : 1, !vec ? 1 : bf16 ? kRowsOf2 : kRowsOf4, &grid))
+  if (!(vec ? grid_of(&a, bf16 ? kRowsOf2 : kRowsOf4, &grid)
+            : grid_of_warps(&a, two ? 2 : 1, &grid)))
     return FO_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned n = unsigned(grid);
@@ -372,10 +462,14 @@ fo_status launch_gated_act_backward(const void* dh, fo_type type, int64_t rows, 
     act_backward_kernel<uint16_t, kRowsOf2><<<n, kThreads, 0, st>>>(a, dh, du);
   else if (vec)
     act_backward_kernel<float, kRowsOf4><<<n, kThreads, 0, st>>>(a, dh, du);
+  else if (bf16 && two)
+    act_backward_any_kernel<uint16_t, 2><<<n, kThreads, 0, st>>>(a, dh, du);
   else if (bf16)
-    act_backward_any_kernel<uint16_t><<<n, kThreads, 0, st>>>(a, dh, du);
+    act_backward_any_kernel<uint16_t, 1><<<n, kThreads, 0, st>>>(a, dh, du);
+  else if (two)
+    act_backward_any_kernel<float, 2><<<n, kThreads, 0, st>>>(a, dh, du);
   else
-    act_backward_any_kernel<float><<<n, kThreads, 0, st>>>(a, dh, du);
+    act_backward_any_kernel<float, 1><<<n, kThreads, 0, st>>>(a, dh, du);
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 

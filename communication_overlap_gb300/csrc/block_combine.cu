@@ -38,33 +38,10 @@ __device__ __forceinline__ int row_of(int32_t r, int64_t table_rows, int32_t* st
   return -1;
 }
 
-// W columns of a row, as they lie in memory: eight on 16 bytes, or one.
-template <typename T, int W>
-struct Columns {
-  Pack8<T> p;
-  __device__ __forceinline__ void load_once(const T* at) { p.load_once(at); }
-  __device__ __forceinline__ void load(const T* at) { p.load(at); }
-  __device__ __forceinline__ void get(float (&v)[8]) const { p.get(v); }
-  // by whole warps; `in`: of this lane
-  __device__ __forceinline__ static void store(T* at, bool in, const float (&v)[8]) {
-    store8_warp(at, in, v);
-  }
-};
-template <typename T>
-struct Columns<T, 1> {
-  T e;
-  __device__ __forceinline__ void load_once(const T* at) { e = __ldcs(at); }
-  __device__ __forceinline__ void load(const T* at) { e = __ldg(at); }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = widen(e); }
-  __device__ __forceinline__ static void store(T* at, bool in, const float (&v)[1]) {
-    if (in) __stcs(at, narrow<T>(v[0]));
-  }
-};
-
-// A thread takes W columns of TOKENS tokens, SLOTS of their slots at a time.  CTAs walk
-// over the items, and the next item's rows are looked up while this one's are on
+// Rows on 16 bytes: a thread takes eight columns of TOKENS tokens, SLOTS of their slots
+// at a time.  CTAs walk over the items, and the next item's rows are looked up while this one's are on
 // their way: a look-up and the rows it names are two waits in a row otherwise.
-template <typename T, typename O, int W, int SLOTS, int TOKENS>
+template <typename T, typename O, int SLOTS, int TOKENS>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
   const int local = a.pieces > 1 ? 0 : int(threadIdx.x) / a.chunks;
   const int lane_col = a.pieces > 1 ? int(threadIdx.x) : int(threadIdx.x) % a.chunks;
@@ -75,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
     return int64_t(item / a.pieces) * a.per_item + local + i * per;
   };
   const auto column = [&](int item) {
-    return (int64_t(item % a.pieces) * kThreads + lane_col) * W;
+    return (int64_t(item % a.pieces) * kThreads + lane_col) * 8;
   };
   const auto look_up = [&](int item, int s0) {
 #pragma unroll
@@ -95,14 +72,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
     const int64_t col = column(item);
     const bool in = col < a.hidden;
     const T* rows = static_cast<const T*>(a.rows) + col;
-    float acc[TOKENS][W];
+    float acc[TOKENS][8];
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) acc[i][k] = 0.0f;
+      for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
     }
     for (int s0 = 0; s0 < a.top_k; s0 += SLOTS) {
-      Columns<T, W> v[TOKENS][SLOTS];
+      Pack8<T> v[TOKENS][SLOTS];
       float by[TOKENS][SLOTS];
       bool has[TOKENS][SLOTS];
 #pragma unroll
@@ -124,20 +101,75 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
           if (has[i][j]) {
-            float f[W];
+            float f[8];
             v[i][j].get(f);
 #pragma unroll
-            for (int k = 0; k < W; ++k) acc[i][k] = fmaf(by[i][j], f[k], acc[i][k]);
+            for (int k = 0; k < 8; ++k) acc[i][k] = fmaf(by[i][j], f[k], acc[i][k]);
           }
       }
     }
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
       const int64_t t = token(item, i);
-      Columns<O, W>::store(static_cast<O*>(a.y) + t * a.y_stride + col,
-                           in && local < per && t < a.tokens, acc[i]);
+      store8_warp(static_cast<O*>(a.y) + t * a.y_stride + col,
+                  in && local < per && t < a.tokens, acc[i]);
     }
   }
+}
+
+// Any rows: a warp takes kUnits times 32 E columns of a token, a lane E neighbouring
+// ones of each 32 E (one column of two tokens per thread: 245 us for 16384 x 4095 of
+// bf16, top 1, where rows on 16 bytes take 35).
+constexpr int kUnits = 4;
+template <typename T, typename O, int E>
+__global__ void __launch_bounds__(kThreads) combine_any_kernel(const CombineArgs a) {
+  constexpr int kSlots = 4;
+  const int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = item / a.pieces;
+  if (t >= a.tokens) return;
+  const int lane = threadIdx.x & 31;
+  const int first = int(item % a.pieces) * kUnits * 32 * E + lane * E;
+  const T* rows = static_cast<const T*>(a.rows) + first;
+  float acc[kUnits][E];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[i][e] = 0.0f;
+  }
+  for (int s0 = 0; s0 < a.top_k; s0 += kSlots) {
+    int r[kSlots];
+    float w[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const bool has = s0 + j < a.top_k;
+      r[j] = has ? __ldg(a.token_row + t * a.top_k + s0 + j) : -1;
+      w[j] = has && a.weights ? __ldg(a.weights + t * a.top_k + s0 + j) : 1.0f;
+    }
+    Few<T, E> v[kSlots][kUnits];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (r[j] >= 0) r[j] = row_of(r[j], a.table_rows, a.status);
+      if (r[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        if (first + i * 32 * E < a.hidden) v[j][i].load(rows + r[j] * a.row_stride + i * 32 * E);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (r[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        float x[E];
+        v[j][i].get(x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] = fmaf(w[j], x[e], acc[i][e]);
+      }
+    }
+  }
+  O* y = static_cast<O*>(a.y) + t * a.y_stride + first;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+    if (first + i * 32 * E < a.hidden) Few<O, E>::store(y + i * 32 * E, acc[i]);
 }
 
 struct CombineBackArgs {
@@ -153,7 +185,7 @@ struct CombineBackArgs {
 
 // The rows that hold no token become zeros: a warp looks at 32 of them, far apart, as
 // they come in runs.
-template <typename T, int W>
+template <typename T, bool VEC>
 __device__ __forceinline__ void zero_empty_rows(const CombineBackArgs& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t looks = (a.f.table_rows + 31) / 32;
@@ -164,11 +196,13 @@ __device__ __forceinline__ void zero_empty_rows(const CombineBackArgs& a) {
         __ballot_sync(0xffffffffu, row < a.f.table_rows && __ldg(a.row_token + row) < 0);
     for (; todo; todo &= todo - 1) {
       T* at = static_cast<T*>(a.drows) + (i + (__ffs(todo) - 1) * looks) * a.drows_stride;
-      float zero[W];
-#pragma unroll
-      for (int k = 0; k < W; ++k) zero[k] = 0.0f;
-      for (int c = lane * W; c - lane * W < a.f.hidden; c += 32 * W)
-        Columns<T, W>::store(at + c, c < a.f.hidden, zero);
+      if constexpr (VEC) {
+        constexpr int kOf16 = 16 / int(sizeof(T));
+        for (int c = lane * kOf16; c < a.f.hidden; c += 32 * kOf16)
+          __stcs(reinterpret_cast<uint4*>(at + c), make_uint4(0, 0, 0, 0));
+      } else {
+        for (int c = lane; c < a.f.hidden; c += 32) at[c] = T(0);
+      }
     }
   }
 }
@@ -348,11 +382,11 @@ __global__ void __launch_bounds__(kThreads, 3) combine_backward_kernel(const Com
     now.advance(f, step);
   }
   OwnRing::wait<0>();
-  zero_empty_rows<T, 8>(a);
+  zero_empty_rows<T, true>(a);
 }
 
-// Any rows: a column per thread at a time, without the ring.
-template <typename T, typename O, int SLOTS>
+// Any rows: E neighbouring columns per thread and 32 E, without the ring.
+template <typename T, typename O, int SLOTS, int E>
 __global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const CombineBackArgs a) {
   __shared__ float part[2][kThreads / 32][SLOTS];
   const CombineArgs& f = a.f;
@@ -379,33 +413,39 @@ __global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const Co
       dot[j] = 0.0f;
     }
     const O* dy = static_cast<const O*>(a.dy) + now.t * a.dy_stride;
-    // CHUNKS columns' loads before their stores
-    constexpr int kChunks = 4;
-    const int stride = a.warps * 32;
-    for (int c0 = (warp % a.warps) * 32 + lane; c0 < f.hidden; c0 += kChunks * stride) {
-      O g[kChunks];
-      T v[kChunks][SLOTS];
+    // kUnits loads of a row before their stores
+    const int stride = a.warps * 32 * E;
+    for (int c0 = ((warp % a.warps) * 32 + lane) * E; c0 < f.hidden; c0 += kUnits * stride) {
+      Few<O, E> g[kUnits];
+      Few<T, E> v[kUnits][SLOTS];
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
+      for (int k = 0; k < kUnits; ++k) {
         const int c = c0 + k * stride;
         if (c >= f.hidden) continue;
-        g[k] = __ldg(dy + c);
+        g[k].load(dy + c);
         if (a.dweights == nullptr) continue;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-          if (r[j] >= 0)
-            v[k][j] = __ldcs(static_cast<const T*>(f.rows) + (r[j] * f.row_stride + c));
+          if (r[j] >= 0) v[k][j].load(static_cast<const T*>(f.rows) + (r[j] * f.row_stride + c));
       }
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
+      for (int k = 0; k < kUnits; ++k) {
         const int c = c0 + k * stride;
         if (c >= f.hidden) continue;
-        const float x = widen(g[k]);
+        float x[E];
+        g[k].get(x);
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
           if (r[j] >= 0) {
-            if (a.dweights) dot[j] = fmaf(x, widen(v[k][j]), dot[j]);
-            __stcs(static_cast<T*>(a.drows) + (r[j] * a.drows_stride + c), narrow<T>(w[j] * x));
+            float y[E];
+            if (a.dweights) {
+              v[k][j].get(y);
+#pragma unroll
+              for (int e = 0; e < E; ++e) dot[j] = fmaf(x[e], y[e], dot[j]);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = w[j] * x[e];
+            Few<T, E>::store(static_cast<T*>(a.drows) + (r[j] * a.drows_stride + c), y);
           }
       }
     }
@@ -423,13 +463,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const Co
     }
     turn ^= 1;
   }
-  zero_empty_rows<T, 1>(a);
-}
-
-// 16-byte rows of 8-element pieces.
-bool vec_rows(const void* p, int64_t stride, fo_type type) {
-  const int64_t size = type == FO_TYPE_BF16 ? 2 : 4;
-  return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) & 15) == 0;
+  zero_empty_rows<T, false>(a);
 }
 
 // How many CTAs of a kernel, with so much shared memory always, the device holds at
@@ -453,16 +487,16 @@ fo_status resident(int smem, int* ctas) {
   return count[slot] > 0 ? FO_OK : FO_ERR_CUDA;
 }
 
-template <typename T, typename O, int W, int SLOTS, int TOKENS>
+template <typename T, typename O, int SLOTS, int TOKENS>
 fo_status forward_as(CombineArgs a, cudaStream_t st) {
-  const int64_t chunks = (a.hidden + W - 1) / W;
+  const int64_t chunks = a.hidden / 8;
   a.pieces = int32_t((chunks + kThreads - 1) / kThreads);
   a.chunks = int32_t(chunks < kThreads ? chunks : kThreads);
   a.per_item = (a.pieces > 1 ? 1 : kThreads / a.chunks) * TOKENS;
   const int64_t items = (int64_t(a.tokens) + a.per_item - 1) / a.per_item * a.pieces;
   if (items >= (int64_t(1) << 30)) return FO_ERR_UNSUPPORTED;
   a.items = int32_t(items);
-  constexpr auto kernel = combine_kernel<T, O, W, SLOTS, TOKENS>;
+  constexpr auto kernel = combine_kernel<T, O, SLOTS, TOKENS>;
   int ctas = 0;
   const fo_status q = resident<kernel>(0, &ctas);
   if (q != FO_OK) return q;
@@ -470,11 +504,24 @@ fo_status forward_as(CombineArgs a, cudaStream_t st) {
   return FO_OK;
 }
 
+template <typename T, typename O, int E>
+fo_status forward_any(CombineArgs a, cudaStream_t st) {
+  a.pieces = (a.hidden + kUnits * 32 * E - 1) / (kUnits * 32 * E);
+  const int64_t grid = (int64_t(a.tokens) * a.pieces + kThreads / 32 - 1) / (kThreads / 32);
+  if (grid >= (int64_t(1) << 31)) return FO_ERR_UNSUPPORTED;
+  combine_any_kernel<T, O, E><<<unsigned(grid), kThreads, 0, st>>>(a);
+  return FO_OK;
+}
+
+// How all of a call's rows lie: on 16 bytes and eight columns, on two elements, or not.
+enum class Rows { kEight, kTwo, kOne };
+
 template <typename T, typename O>
-fo_status forward(const CombineArgs& a, bool vec, cudaStream_t st) {
-  if (!vec) return forward_as<T, O, 1, 4, 2>(a, st);
-  if (a.top_k <= 2) return forward_as<T, O, 8, 2, 2>(a, st);
-  return forward_as<T, O, 8, 4, 1>(a, st);
+fo_status forward(const CombineArgs& a, Rows rows, cudaStream_t st) {
+  if (rows == Rows::kOne) return forward_any<T, O, 1>(a, st);
+  if (rows == Rows::kTwo) return forward_any<T, O, 2>(a, st);
+  if (a.top_k <= 2) return forward_as<T, O, 2, 2>(a, st);
+  return forward_as<T, O, 4, 1>(a, st);
 }
 
 // The warps of a token: the fewest (they meet at each of its sums) with which the
@@ -521,8 +568,11 @@ fo_status backward_slots(const CombineBackArgs& a, cudaStream_t st) {
 }
 
 template <typename T, typename O>
-fo_status backward(const CombineBackArgs& a, bool vec, cudaStream_t st) {
-  if (!vec) return backward_as<combine_backward_any_kernel<T, O, 4>>(a, 0, 32, st);
+fo_status backward(const CombineBackArgs& a, Rows lie, cudaStream_t st) {
+  if (lie == Rows::kOne)
+    return backward_as<combine_backward_any_kernel<T, O, 4, 1>>(a, 0, 32, st);
+  if (lie == Rows::kTwo)
+    return backward_as<combine_backward_any_kernel<T, O, 4, 2>>(a, 0, 64, st);
   const int rounds = (a.f.top_k + 3) / 4;
   switch ((a.f.top_k + rounds - 1) / rounds) {
     case 1: return backward_slots<T, O, 1>(a, st);
@@ -545,14 +595,17 @@ fo_status launch_combine(const void* rows, fo_type type, int64_t table_rows, int
   a.token_row = token_row, a.weights = weights;
   a.tokens = int32_t(tokens), a.hidden = int32_t(hidden), a.top_k = top_k;
   a.y = y, a.y_stride = y_stride, a.status = dev_status;
-  const bool vec = hidden % 8 == 0 && vec_rows(rows, row_stride, type) &&
-                   vec_rows(y, y_stride, y_type);
+  const bool vec = hidden % 8 == 0 && rows_on(rows, row_stride, type, 16) &&
+                   rows_on(y, y_stride, y_type, 16);
+  const bool two = hidden % 2 == 0 && rows_on_two(rows, row_stride, type) &&
+                   rows_on_two(y, y_stride, y_type);
+  const Rows lie = vec ? Rows::kEight : two ? Rows::kTwo : Rows::kOne;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = type == FO_TYPE_BF16, ybf = y_type == FO_TYPE_BF16;
-  const fo_status q = bf && ybf ? forward<uint16_t, uint16_t>(a, vec, st)
-                      : bf      ? forward<uint16_t, float>(a, vec, st)
-                      : ybf     ? forward<float, uint16_t>(a, vec, st)
-                                : forward<float, float>(a, vec, st);
+  const fo_status q = bf && ybf ? forward<uint16_t, uint16_t>(a, lie, st)
+                      : bf      ? forward<uint16_t, float>(a, lie, st)
+                      : ybf     ? forward<float, uint16_t>(a, lie, st)
+                                : forward<float, float>(a, lie, st);
   return q == FO_OK ? launched() : q;
 }
 
@@ -571,15 +624,18 @@ fo_status launch_combine_backward(const void* dy, fo_type dy_type, int64_t dy_st
   f.status = dev_status;
   a.dy = dy, a.dy_stride = dy_stride, a.row_token = row_token;
   a.drows = drows, a.drows_stride = drows_stride, a.dweights = dweights;
-  const bool vec = hidden % 8 == 0 && (!dweights || vec_rows(rows, row_stride, type)) &&
-                   vec_rows(dy, dy_stride, dy_type) && vec_rows(drows, drows_stride, type);
+  const bool vec = hidden % 8 == 0 && (!dweights || rows_on(rows, row_stride, type, 16)) &&
+                   rows_on(dy, dy_stride, dy_type, 16) && rows_on(drows, drows_stride, type, 16);
+  const bool two = hidden % 2 == 0 && (!dweights || rows_on_two(rows, row_stride, type)) &&
+                   rows_on_two(dy, dy_stride, dy_type) && rows_on_two(drows, drows_stride, type);
+  const Rows lie = vec ? Rows::kEight : two ? Rows::kTwo : Rows::kOne;
   if (tokens == 0 && table_rows == 0) return FO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = type == FO_TYPE_BF16, ybf = dy_type == FO_TYPE_BF16;
-  const fo_status q = bf && ybf ? backward<uint16_t, uint16_t>(a, vec, st)
-                      : bf      ? backward<uint16_t, float>(a, vec, st)
-                      : ybf     ? backward<float, uint16_t>(a, vec, st)
-                                : backward<float, float>(a, vec, st);
+  const fo_status q = bf && ybf ? backward<uint16_t, uint16_t>(a, lie, st)
+                      : bf      ? backward<uint16_t, float>(a, lie, st)
+                      : ybf     ? backward<float, uint16_t>(a, lie, st)
+                                : backward<float, float>(a, lie, st);
   return q == FO_OK ? launched() : q;
 }
 

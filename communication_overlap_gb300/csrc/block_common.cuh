@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "block_internal.h"
 #include "device_common.cuh"
@@ -208,6 +209,54 @@ __device__ __forceinline__ void get_pairs(const OwnRing& ring, int piece, Pair (
   Pack8<T> p;
   ring.get(piece, p);
   pairs_of(p, x);
+}
+
+// E neighbouring elements of a row that need not lie on 16 bytes: two where all rows
+// start on two elements and have an even number, else one.
+template <typename T, int E>
+struct Few {
+  static_assert(E == 1 || E == 2, "one element or two");
+  using Word = typename std::conditional<sizeof(T) * E == 2, uint16_t,
+               typename std::conditional<sizeof(T) * E == 4, uint32_t, uint2>::type>::type;
+  Word w;
+  __device__ __forceinline__ void zero() {
+    if constexpr (sizeof(Word) == 8)
+      w = make_uint2(0, 0);
+    else
+      w = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) { w = __ldcs(reinterpret_cast<const Word*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+    if constexpr (sizeof(Word) == 8) {
+      v[0] = __uint_as_float(w.x);
+      v[E - 1] = __uint_as_float(w.y);
+    } else if constexpr (E == 2) {
+      v[0] = bf16lo(w);
+      v[E - 1] = bf16hi(w);
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(w);
+    } else {
+      v[0] = widen(w);
+    }
+  }
+  __device__ __forceinline__ static void store(T* p, const float (&v)[E]) {
+    if constexpr (sizeof(Word) == 8)
+      __stcs(reinterpret_cast<uint2*>(p), make_uint2(__float_as_uint(v[0]), __float_as_uint(v[E - 1])));
+    else if constexpr (E == 2)
+      __stcs(reinterpret_cast<uint32_t*>(p), pack_bf16x2(v[0], v[E - 1]));
+    else
+      __stcs(p, narrow<T>(v[0]));
+  }
+};
+
+// Whether rows start on `bytes` bytes.
+inline bool rows_on(const void* p, int64_t stride, fo_type type, int bytes) {
+  const int64_t size = type == FO_TYPE_BF16 ? 2 : 4;
+  return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) & (bytes - 1)) == 0;
+}
+// And on two elements.
+inline bool rows_on_two(const void* p, int64_t stride, fo_type type) {
+  return rows_on(p, stride, type, type == FO_TYPE_BF16 ? 4 : 8);
 }
 
 // The current device's SMs.

@@ -36,6 +36,15 @@ __device__ __forceinline__ void store_piece(T* at, const float (&v)[W]) {
     __stcs(at, narrow<T>(v[0]));
 }
 
+// E values of a gain or of a gate's row, which need not lie on 16 bytes.
+template <int E>
+__device__ __forceinline__ void load_few_param(const void* p, int64_t i, bool f32, float (&v)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    v[e] = f32 ? __ldg(static_cast<const float*>(p) + i + e)
+               : widen(__ldg(static_cast<const uint16_t*>(p) + i + e));
+}
+
 // W values of a gain or of a gate's row, from element i on (bf16 or fp32).
 template <int W>
 __device__ __forceinline__ void load_param(const void* p, int64_t i, bool f32, float (&v)[W]) {
@@ -159,6 +168,25 @@ inline RowShape row_shape(int64_t hidden, int nv, int cta_warps) {
   return s;
 }
 
+// scale gate post of E columns (factors that are not given left out).
+template <int E>
+__device__ __forceinline__ void load_few_factor(const NormArgs& a, int col, int64_t gate_row,
+                                                float (&w)[E]) {
+  float p[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] = a.scale;
+  if (a.gate != nullptr) {
+    load_few_param<E>(a.gate, gate_row + col, a.params_f32, p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] *= p[e];
+  }
+  if (a.post != nullptr) {
+    load_few_param<E>(a.post, col, a.params_f32, p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] *= p[e];
+  }
+}
+
 // scale gate post of eight columns (factors that are not given left out).
 __device__ __forceinline__ void load_factor(const NormArgs& a, int col, int64_t gate_row,
                                             float (&w)[8]) {
@@ -179,6 +207,12 @@ __device__ __forceinline__ void load_factor(const NormArgs& a, int col, int64_t 
 
 inline bool norm_on_16(const void* p, int64_t stride, int64_t size) {
   return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) & 15) == 0;
+}
+// Whether all rows of the forward call's tensors start on two elements.
+inline bool norm_rows_on_two(const NormArgs& a, fo_type type, fo_type stream_type) {
+  return a.hidden % 2 == 0 && rows_on_two(a.x, a.x_stride, type) &&
+         rows_on_two(a.residual, a.residual_stride, stream_type) &&
+         rows_on_two(a.sum, a.sum_stride, stream_type) && rows_on_two(a.y, a.y_stride, type);
 }
 inline int64_t size_of(fo_type t) { return t == FO_TYPE_BF16 ? 2 : 4; }
 

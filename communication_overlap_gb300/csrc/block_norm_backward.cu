@@ -384,6 +384,142 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
   }
 }
 
+// Rows of up to 4096 columns that need not lie on 16 bytes, as norm_few_kernel has
+// them: eight columns per thread, E neighbouring ones of each 32 E of the row's
+// threads; the next row is loaded while one is worked on.  (In two kernels, a column
+// per thread: 838 us for 16384 x 4095 of bf16.)
+template <typename A, typename S, int E>
+__global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBackArgs a,
+                                                                   const BackShape n, int warps) {
+  constexpr int U = 8 / E;
+  __shared__ __align__(16) float buf[2 * 8 * 48];           // of up to eight rows
+  for (int i = threadIdx.x; i < 2 * 8 * 48; i += blockDim.x) buf[i] = 0.0f;
+  __syncthreads();
+  int turn = 0;
+  const NormArgs& f = a.f;
+  const RowGroup g = RowGroup::of(warps);
+  const int first = g.tid * E, stride = warps * 32 * E;
+  const int64_t worker = int64_t(blockIdx.x) * (int(blockDim.x) / (warps * 32)) + g.index;
+  const int t0 = int(min(worker * n.per_worker, int64_t(f.tokens)));
+  const int t1 = min(t0 + n.per_worker, f.tokens);
+  const float inv = 1.0f / float(f.hidden);
+  Few<A, E> px[U], py[U];
+  Few<S, E> pr[U], pd[U];
+  const auto load = [&](int t) {
+    const A* x = static_cast<const A*>(f.x) + (t * f.x_stride + first);
+    const A* y = static_cast<const A*>(a.dy) + (t * a.dy_stride + first);
+    const S* r = static_cast<const S*>(f.residual) + (t * f.residual_stride + first);
+    const S* d = static_cast<const S*>(a.dsum) + (t * a.dsum_stride + first);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const bool has = t < t1 && first + i * stride < f.hidden;
+      px[i].zero(), py[i].zero(), pr[i].zero(), pd[i].zero();
+      if (has) px[i].load(x + i * stride);
+      if (has && f.pre != nullptr) py[i].load(y + i * stride);
+      if (has && f.residual != nullptr) pr[i].load(r + i * stride);
+      if (has && a.dsum != nullptr) pd[i].load(d + i * stride);
+    }
+  };
+  load(t0);
+  float w[U][E], pre[U][E], dpre[U][E], dpost[U][E], sum_g[U][E];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[i][e] = pre[i][e] = dpre[i][e] = dpost[i][e] = sum_g[i][e] = 0.0f;
+    if (f.pre != nullptr && first + i * stride < f.hidden)
+      load_few_param<E>(f.pre, first + i * stride, f.params_f32, pre[i]);
+  }
+  int gate_row = 0, gate_end = t0;
+  for (int t = t0; t < t1; ++t) {
+    if (t >= gate_end) {
+      gate_row = f.gate ? int(uint32_t(t) / uint32_t(f.gate_rows)) : 0;
+      gate_end = f.gate ? int(min(int64_t(gate_row + 1) * f.gate_rows, int64_t(t1))) : t1;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (first + i * stride < f.hidden)
+          load_few_factor<E>(f, first + i * stride, gate_row * f.gate_stride, w[i]);
+    }
+    float xn[U][E], sn[U][E], dy[U][E], d[U][E];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      px[i].get(xn[i]);
+      py[i].get(dy[i]);
+      pr[i].get(sn[i]);
+      pd[i].get(d[i]);
+    }
+    load(t + 1);
+    const float r1 = f.post ? f.post_rstd[t] : 1.0f, r2 = f.pre ? f.pre_rstd[t] : 0.0f;
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        xn[i][e] *= r1;
+        const float z = w[i][e] * xn[i][e], q = dy[i][e] * pre[i][e];
+        sn[i][e] = (sn[i][e] + z) * r2;
+        d[i][e] = fmaf(r2, q, d[i][e]);
+        sum[0] = fmaf(q, sn[i][e], sum[0]);
+        sum[1] = fmaf(z, d[i][e], sum[1]);
+        sum[2] = fmaf(z, sn[i][e], sum[2]);
+      }
+    }
+    g.sums<3>(sum, buf, turn);
+    const float k = r2 * (sum[0] * inv);
+    const float m1 = (sum[1] - k * sum[2]) * inv;
+    S* dres = static_cast<S*>(a.dresidual) + (t * a.dresidual_stride + first);
+    A* dx = static_cast<A*>(a.dx) + (t * a.dx_stride + first);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        d[i][e] = fmaf(-k, sn[i][e], d[i][e]);
+        dpre[i][e] = fmaf(dy[i][e], sn[i][e], dpre[i][e]);
+        sum_g[i][e] = fmaf(xn[i][e], d[i][e], sum_g[i][e]);
+        o[e] = w[i][e] * d[i][e];
+        if (f.post != nullptr) o[e] = r1 * fmaf(-m1, xn[i][e], o[e]);
+      }
+      if (first + i * stride >= f.hidden) continue;
+      if (a.dresidual != nullptr) Few<S, E>::store(dres + i * stride, d[i]);
+      Few<A, E>::store(dx + i * stride, o);
+    }
+    if (t + 1 < gate_end) continue;
+    // the last token with this gate here
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int col = first + i * stride;
+      if (col >= f.hidden) continue;
+      float p[E], q[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) p[e] = q[e] = 1.0f;
+      if (f.post != nullptr) load_few_param<E>(f.post, col, f.params_f32, p);
+      if (f.gate != nullptr)
+        load_few_param<E>(f.gate, gate_row * f.gate_stride + col, f.params_f32, q);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float scaled = f.scale * sum_g[i][e];
+        dpost[i][e] = fmaf(q[e], scaled, dpost[i][e]);
+        sum_g[i][e] = 0.0f;
+        if (f.gate != nullptr) {
+          const float v[1] = {p[e] * scaled};
+          store_gate<1>(a, n, t, worker, col + e, v);
+        }
+      }
+    }
+  }
+  if (t0 >= t1) return;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (first + i * stride >= f.hidden) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int64_t at = worker * f.hidden + first + i * stride + e;
+      if (f.pre != nullptr) n.pre_part[at] = dpre[i][e];
+      if (f.post != nullptr) n.post_part[at] = dpost[i][e];
+    }
+  }
+}
+
 // Any rows, first: the two means of each token, by a CTA.
 template <typename A, typename S, int W>
 __global__ void __launch_bounds__(512) norm_means_kernel(const NormBackArgs a, const BackShape n) {
@@ -507,15 +643,16 @@ fo_status launch_ring(const NormBackArgs& a, const BackShape& n, const RowShape&
 }
 
 template <typename A, typename S>
-fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec, int sms,
-                 cudaStream_t st) {
+fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec, bool two,
+                 int sms, cudaStream_t st) {
   const NormArgs& f = a.f;
   const int64_t H = f.hidden;
   const RowShape s = whole_shape(H <= 8192 ? H : 0);
   const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S));
   const int params = s.nv == 1 ? 0 : s.threads * s.nv * 64;
   const bool whole = vec && H <= 8192 && 2 * row + params <= kBlockSmem;
-  if (whole) {
+  const bool few = !vec && H <= 4096;
+  if (whole || few) {
     share_out(n, f.tokens, whole_workers(H, sms));
   } else {
     share_out(n, f.tokens, column_workers(H, vec ? 8 : 1, sms));
@@ -536,6 +673,14 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
                    : launch_ring<A, S, 1, 2, false>(a, *n, s, row, st);
     return gates ? launch_ring<A, S, 2, 2, true>(a, *n, s, row, st)
                  : launch_ring<A, S, 2, 2, false>(a, *n, s, row, st);
+  }
+  if (few) {
+    const unsigned grid = unsigned((n->workers + s.rows - 1) / s.rows);
+    if (two)
+      norm_backward_few_kernel<A, S, 2><<<grid, s.threads, 0, st>>>(a, *n, s.warps);
+    else
+      norm_backward_few_kernel<A, S, 1><<<grid, s.threads, 0, st>>>(a, *n, s.warps);
+    return FO_OK;
   }
   if (vec) {
     const int pieces = int((H + 2047) / 2048);
@@ -570,6 +715,10 @@ fo_status launch_block_norm_backward(const NormBackArgs& a, fo_type type, fo_typ
                    norm_on_16(a.dy, a.dy_stride, sa) && norm_on_16(a.dx, a.dx_stride, sa) &&
                    norm_on_16(a.dresidual, a.dresidual_stride, ss) &&
                    norm_on_16(a.dgate, f.hidden, sp);
+  const bool two = norm_rows_on_two(f, type, stream_type) &&
+                   rows_on_two(a.dsum, a.dsum_stride, stream_type) &&
+                   rows_on_two(a.dy, a.dy_stride, type) && rows_on_two(a.dx, a.dx_stride, type) &&
+                   rows_on_two(a.dresidual, a.dresidual_stride, stream_type);
   int sms = 0;
   fo_status q = sm_count(&sms);
   if (q != FO_OK) return q;
@@ -584,11 +733,11 @@ fo_status launch_block_norm_backward(const NormBackArgs& a, fo_type type, fo_typ
   // (without tokens there are no parts, and the sums are zeros)
   if (f.tokens > 0) {
     if (type == FO_TYPE_F32)
-      q = launch<float, float>(a, &n, a.workspace, vec, sms, st);
+      q = launch<float, float>(a, &n, a.workspace, vec, two, sms, st);
     else if (stream_type == FO_TYPE_F32)
-      q = launch<uint16_t, float>(a, &n, a.workspace, vec, sms, st);
+      q = launch<uint16_t, float>(a, &n, a.workspace, vec, two, sms, st);
     else
-      q = launch<uint16_t, uint16_t>(a, &n, a.workspace, vec, sms, st);
+      q = launch<uint16_t, uint16_t>(a, &n, a.workspace, vec, two, sms, st);
   }
   if (q != FO_OK) return q;
   if (cudaGetLastError() != cudaSuccess) return FO_ERR_CUDA;
