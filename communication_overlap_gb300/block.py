@@ -198,6 +198,8 @@ class Checkpoint:
 
     def values(self, dtype=torch.float32):
         """The values it stands for, [rows, 2 * inter]."""
+        if self.rows == 0 or self.inter == 0:
+            return torch.empty((self.rows, 2 * self.inter), dtype=dtype, device=self.codes.device)
         s = self.scales.view(self.rows, 2, -1, 1).to(torch.int32)
         step = torch.where(s == 0, torch.full_like(s, 1 << 22), s << 23).view(torch.float32)
         step = torch.where(s == 255, torch.full_like(step, float("nan")), step)

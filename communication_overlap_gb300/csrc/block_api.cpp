@@ -17,6 +17,11 @@ namespace {
 
 constexpr int64_t kMaxBytes = int64_t(1) << 62;
 
+// Tokens and columns that the kernels walk over with 32-bit steps.
+bool walkable(int64_t tokens, int64_t columns) {
+  return tokens <= (int64_t(1) << 31) - (int64_t(1) << 20) && columns <= int64_t(1) << 30;
+}
+
 bool act_ok(fo_activation act) { return act >= FO_ACT_NONE && act <= FO_ACT_SILU; }
 
 bool norm_desc_ok(const fo_norm_desc* d) {
@@ -81,8 +86,7 @@ fo_status fo_moe_combine(const void* rows, fo_type type, int64_t table_rows, int
   if (!aligned_type(rows, type) || !aligned_type(y, y_type) || !fo::aligned4(token_row) ||
       !fo::aligned4(weights))
     return FO_ERR_ARG;
-  if (!fits_int32(tokens) || !fits_int32(hidden) || !fits_int32(table_rows))
-    return FO_ERR_UNSUPPORTED;
+  if (!walkable(tokens, hidden) || !fits_int32(table_rows)) return FO_ERR_UNSUPPORTED;
   fo_status st;
   if (!device_ok(&st)) return st;
   return fo::launch_combine(rows, type, table_rows, hidden, row_stride, token_row, weights,
@@ -109,8 +113,7 @@ fo_status fo_moe_combine_backward(const void* dy, fo_type dy_type, int64_t dy_st
       !fo::aligned4(token_row) || !fo::aligned4(row_token) || !fo::aligned4(weights) ||
       !fo::aligned4(dweights))
     return FO_ERR_ARG;
-  if (!fits_int32(tokens) || !fits_int32(hidden) || !fits_int32(table_rows))
-    return FO_ERR_UNSUPPORTED;
+  if (!walkable(tokens, hidden) || !fits_int32(table_rows)) return FO_ERR_UNSUPPORTED;
   fo_status st;
   if (!device_ok(&st)) return st;
   return fo::launch_combine_backward(dy, dy_type, dy_stride, rows, type, table_rows, hidden,
@@ -175,7 +178,7 @@ fo_status fo_block_norm(const fo_norm_desc* d, const void* x, int64_t x_stride,
     return FO_ERR_ARG;
   if (pre_gain && (!y || y_stride < d->hidden || !aligned_type(y, fo_type(d->type))))
     return FO_ERR_ARG;
-  if (!fits_int32(d->tokens) || !fits_int32(d->hidden)) return FO_ERR_UNSUPPORTED;
+  if (!walkable(d->tokens, d->hidden)) return FO_ERR_UNSUPPORTED;
   fo_status st;
   if (!device_ok(&st)) return st;
   fo::NormArgs a = norm_args(*d, x, x_stride, residual, residual_stride, post_gain, gate,
@@ -187,7 +190,7 @@ fo_status fo_block_norm(const fo_norm_desc* d, const void* x, int64_t x_stride,
 
 fo_status fo_block_norm_workspace(const fo_norm_desc* d, int64_t* bytes) {
   if (!norm_desc_ok(d) || !bytes) return FO_ERR_ARG;
-  if (!fits_int32(d->tokens) || !fits_int32(d->hidden)) return FO_ERR_UNSUPPORTED;
+  if (!walkable(d->tokens, d->hidden)) return FO_ERR_UNSUPPORTED;
   *bytes = fo::block_norm_workspace_bytes(d->tokens, d->hidden, d->gates);
   return FO_OK;
 }
@@ -217,7 +220,7 @@ fo_status fo_block_norm_backward(const fo_norm_desc* d, const void* x, int64_t x
     if (dresidual && (dresidual_stride < d->hidden || !aligned_type(dresidual, s)))
       return FO_ERR_ARG;
   }
-  if (!fits_int32(d->tokens) || !fits_int32(d->hidden)) return FO_ERR_UNSUPPORTED;
+  if (!walkable(d->tokens, d->hidden)) return FO_ERR_UNSUPPORTED;
   fo_status st;
   if (!device_ok(&st)) return st;
   fo::NormBackArgs a{};

@@ -345,7 +345,10 @@ fo_status launch(const NormArgs& a, bool vec, bool two, cudaStream_t st) {
     const int row = s.threads * s.nv * 16 * int(sizeof(A) + sizeof(S)) / 2;
     const bool deep = 4 * row <= (s.threads <= 256 ? kBlockSmem / 2 : kBlockSmem);
     if (s.nv == 1) return launch_ring<A, S, 1, 4>(a, s, row, st);
-    return deep ? launch_ring<A, S, 2, 4>(a, s, row, st) : launch_ring<A, S, 2, 2>(a, s, row, st);
+    if constexpr (sizeof(A) == 4) {       // (of bf16 rows four always fit)
+      if (!deep) return launch_ring<A, S, 2, 2>(a, s, row, st);
+    }
+    return launch_ring<A, S, 2, 4>(a, s, row, st);
   } else if (!vec && a.hidden <= 4096) {
     int sms = 0;
     const fo_status q = sm_count(&sms);

@@ -664,13 +664,16 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   n->gate_part = n->post_part + n->workers * H;
   if (whole) {
     const bool gates = f.gate != nullptr && f.gate_rows < f.tokens;
-    // four rows under way where they fit
-    if (s.nv == 1 && 4 * row <= kBlockSmem)
+    // four rows under way where they fit, as those of bf16 do
+    if (s.nv == 1) {
+      if constexpr (sizeof(A) == 4) {
+        if (4 * row > kBlockSmem)
+          return gates ? launch_ring<A, S, 1, 2, true>(a, *n, s, row, st)
+                       : launch_ring<A, S, 1, 2, false>(a, *n, s, row, st);
+      }
       return gates ? launch_ring<A, S, 1, 4, true>(a, *n, s, row, st)
                    : launch_ring<A, S, 1, 4, false>(a, *n, s, row, st);
-    if (s.nv == 1)
-      return gates ? launch_ring<A, S, 1, 2, true>(a, *n, s, row, st)
-                   : launch_ring<A, S, 1, 2, false>(a, *n, s, row, st);
+    }
     return gates ? launch_ring<A, S, 2, 2, true>(a, *n, s, row, st)
                  : launch_ring<A, S, 2, 2, false>(a, *n, s, row, st);
   }

@@ -795,6 +795,8 @@ fo_status fo_moe_few(const fo_moe_few_desc* desc, const void* x, int64_t x_strid
  * bytes, of a multiple of 8 columns, go fastest).  Outputs do not overlap
  * inputs.  Sums, means and everything between loads and stores are fp32, each
  * output is rounded once.  No result depends on the order in which CTAs run.
+ * FO_ERR_UNSUPPORTED above 2^30 columns, or 2^31 - 2^20 tokens (rows of an
+ * activation: 2^31 - 256).
  * ---------------------------------------------------------------------- */
 
 /* The weighted sum of a token's rows of the experts' outputs:
@@ -862,9 +864,9 @@ fo_status fo_gated_act_backward(const void* dh, fo_type type, int64_t rows, int6
  *       (not written where pre_gain is NULL; of the unrounded sum).
  * residual NULL: zeros; gate NULL: ones; sum NULL: not written.
  *  x, y: type.  residual, sum: stream_type (F32 where type is F32).  gains
- *      [hidden] and gate [gates][hidden]: param_type.  gates divides tokens,
- *      and tokens / gates consecutive tokens share a row of the gate (1: one
- *      row for all; tokens: a row each); ignored where gate is NULL.
+ *      [hidden] and gate [gates][hidden]: param_type.  gates (at least 1)
+ *      divides tokens, and tokens / gates consecutive tokens share a row of
+ *      the gate (1: one row for all; tokens: a row each).
  *  post_rstd, pre_rstd: device float[tokens], written where their gain is
  *      given (the backward pass reads them). */
 typedef struct {

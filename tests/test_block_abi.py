@@ -80,9 +80,12 @@ def test_combine_refuses(bad):
 def test_combine_of_nothing_and_of_too_much():
     fo.fo_moe_combine(*{**COMBINE, "tokens": 0, "token_row": 0, "y": 0}.values())
     fo.fo_moe_combine(*{**COMBINE, "hidden": 0}.values())
-    for big in (dict(tokens=1 << 31), dict(table_rows=1 << 31),
-                dict(hidden=1 << 31, row_stride=1 << 31, y_stride=1 << 31)):
-        refused(UNSUP, fo.fo_moe_combine, *{**COMBINE, **big}.values())
+    for big in (dict(tokens=(1 << 31) - (1 << 19)), dict(table_rows=1 << 31),
+                dict(hidden=1 << 31, row_stride=1 << 31, y_stride=1 << 31, dy_stride=1 << 31,
+                     drows_stride=1 << 31)):
+        for call, args in ((fo.fo_moe_combine, COMBINE),
+                           (fo.fo_moe_combine_backward, COMBINE_BACK)):
+            refused(UNSUP, call, *{**args, **{k: v for k, v in big.items() if k in args}}.values())
 
 
 COMBINE_BACK = dict(dy=64, dy_type=0, dy_stride=16, rows=64, type=0, table_rows=8, hidden=16,
@@ -190,7 +193,9 @@ def test_norm_backward_refuses(bad):
 def test_norm_of_nothing_and_of_too_much():
     fo.fo_block_norm(*norm_args(NORM, dict(tokens=0)))
     fo.fo_block_norm(*norm_args(NORM, dict(hidden=0)))
-    refused(UNSUP, fo.fo_block_norm, *norm_args(NORM, dict(tokens=1 << 32)))
+    for tokens in (1 << 32, (1 << 31) - (1 << 19)):
+        refused(UNSUP, fo.fo_block_norm, *norm_args(NORM, dict(tokens=tokens)))
+        refused(UNSUP, fo.fo_block_norm_backward, *norm_args(NORM_BACK, dict(tokens=tokens)))
     desc = fo.make_norm_desc(**NORM_DESC)
     assert fo.fo_block_norm_workspace(desc) > 0
     refused(ARG, fo.fo_block_norm_workspace, fo.make_norm_desc(**{**NORM_DESC, "gates": 3}))

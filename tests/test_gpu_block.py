@@ -410,6 +410,14 @@ def test_nothing():
     drows, dw = block.combine_backward(z(0, 8), z(3, 8) + 1, empty, none.view(-1)[:3].contiguous(),
                                        z(0, 2))
     assert not drows.any() and dw.shape == (0, 2)
+    # rows without columns: products of nothing
+    index = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    drows, dw = block.combine_backward(z(1, 0), z(3, 0), index,
+                                       torch.tensor([0, 0, -1], dtype=torch.int32, device="cuda"),
+                                       z(1, 2) + 5)
+    assert drows.shape == (3, 0) and not dw.any() and block.combine(z(3, 0), index).shape == (1, 0)
+    assert block.activate(z(0, 64), checkpoint=True)[1].values().shape == (0, 64)
+    assert block.activate(z(4, 0), checkpoint=True)[1].values().shape == (4, 0)
 
 
 # ------------------------------------------------------------------ how they are called

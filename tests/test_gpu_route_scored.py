@@ -165,6 +165,24 @@ def test_far_logits():
     check(l, 3, True, "softmax", scale=3.0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_masked_by_the_lowest_value(scoring, dtype):
+    """Experts masked by the type's lowest number instead of -inf may be chosen where
+    nothing else is left; a bias as low decides like one."""
+    rng = np.random.default_rng(11)
+    low = torch.finfo(dtype).min
+    l = normal(rng, (40, 24), dtype)
+    l[torch.from_numpy(rng.random((40, 24)) < 0.8).cuda()] = low
+    l[3] = low
+    bias = normal(rng, (24,), F32, 0.05)
+    bias[5:9] = torch.finfo(F32).min
+    for b in (None, bias):
+        for groups, top, group_top in ((1, 1, 1), (4, 2, 1), (4, 2, 2)):
+            check(l, 6, True, scoring, b, groups, top, group_top)
+            check(l, 6, False, scoring, b, groups, top, group_top)
+
+
 @pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
 def test_barred(scoring):
     """-inf bars an expert, by its logit or its bias; tokens and groups may have
