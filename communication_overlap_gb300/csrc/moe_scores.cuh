@@ -424,6 +424,16 @@ __device__ __forceinline__ void make_keys(const ScoreArgs& a, const LaneExperts<
   c.open = own.count > 0;
 }
 
+// What a group's score may be off for the bits that its logits' keys leave out, V ulps
+// of l each: p |l| <= p |max| + p |l - max|, the latter at most 0.37 of the largest p.
+// (Of a sigmoid, whose s (1 - s) |l| is at most 0.28, the other margins hold that.)
+template <int V>
+__device__ __forceinline__ float cut_logit_margin(const ScoreArgs& a, const Choice<V>& c, float v) {
+  return a.bias || a.sigmoid || a.group_top == 1 || a.bf16
+             ? 0.0f
+             : (v * fabsf(c.top) + c.inv) * (float(V) * 0x1p-22f);
+}
+
 // Bars the experts of the groups that do not stay.
 template <int V>
 __device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choice<V>& c) {
@@ -458,7 +468,8 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choi
     // by twice as much)
     const bool logits = by_logit && a.group_top == 1;
     const float s0 = score_margin(a.sigmoid, c.inv, V), vi = order_value(in);
-    const float margin = logits ? 0.0f : 2.0f * choice_margin(s0, vi, float(4 * V));
+    const float margin =
+        logits ? 0.0f : 2.0f * choice_margin(s0, vi, float(4 * V)) + cut_logit_margin(a, c, vi);
     const bool near = in == out ? !(logits && a.bf16) : vi - order_value(out) < margin;
     if (near && !all_alike(a, at)) {
       // groups further than a margin from the last that stays are sure
@@ -470,7 +481,8 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choi
       const float least = order_value(a.group_top == 2 && k2 != 0u ? k2 : k1);
       const float low =
           least - (logits ? fabsf(least) * (float(V) * 0x1p-22f)
-                          : choice_margin(s0, least, float(4 * V)));
+                          : choice_margin(s0, least, float(4 * V)) +
+                                cut_logit_margin(a, c, least));
       const uint32_t best =
           groups_64(a, at, V, c.top, c.inv, low, unsure, a.top_groups - n_sure);
       stays = sure || (unsure && (best >> g & 1u));

@@ -139,6 +139,21 @@ def test_pairs_that_fp32_cannot_tell(top_groups):
           torch.from_numpy(bias).to(F32).cuda(), groups, top_groups, 2)
 
 
+@pytest.mark.parametrize("offset", [100.0, -1000.0])
+@pytest.mark.parametrize("n, groups", [(256, 8), (64, 4)])
+def test_groups_of_logits_far_from_zero(n, groups, offset):
+    """Two groups whose pairs differ by few steps of fp32, each of them a large part of
+    a score: softmax looks at differences, not at sizes."""
+    rng = np.random.default_rng(n)
+    T, per, step = 600, n // groups, np.spacing(np.float32(abs(offset)))
+    l = np.float32(offset - 8.0 + rng.standard_normal((T, n)))
+    for t in range(T):
+        for g in rng.choice(groups, 2, replace=False):
+            for e in rng.choice(per, 2, replace=False):
+                l[t, g * per + e] = np.float32(offset) + np.float32(step * rng.integers(0, 17))
+    check(torch.from_numpy(l).cuda(), 4, True, "softmax", None, groups, 1, 2)
+
+
 @pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups, top_groups", [(1, 1), (4, 2), (4, 4)])
 def test_ties(scoring, groups, top_groups):
