@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredA
   int32_t* total = start + E;                             // [E]
   int32_t* first = total + E;                             // [E]
   __shared__ int32_t ok_s;
+  __shared__ Slot slots_s[kScoredThreads / 32][V <= 8 ? 2 : 1][kSlots];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = int(blockDim.x) / 32;
   const bool lead = !a.alone || blockIdx.x == 0;          // this CTA writes its tokens' outputs
   const int64_t t0 = a.alone ? 0 : int64_t(blockIdx.x) * a.chunk;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredA
       for (int i = 0; i < V; ++i) x[j][i] = ahead[j][i];
     }
     if constexpr (kAhead) load(t + kTokens * warps);
-    warp_choose<V, kTokens>(a.score, own, at, x, id, w);
+    warp_choose<V, kTokens>(a.score, own, at, x, slots_s[warp], id, w);
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
       const int u = t + j * warps;
@@ -158,17 +159,24 @@ __global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredA
         uint32_t before[4] = {0, 0, 0, 0}, all[4] = {0, 0, 0, 0};     // two experts each:
         int hi_before[4] = {0, 0, 0, 0}, hi_all[4] = {0, 0, 0, 0};    // low halves, high halves
         const uint4* row = static_cast<const uint4*>(a.counts) + col;
-#pragma unroll 8
-        for (int c = i / columns; c < int(gridDim.x); c += parts) {
-          const uint4 v = __ldcg(row + c * columns);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        constexpr int kRows = 10;       // at a time: 152 CTAs' 256 experts at once
+        for (int c0 = i / columns; c0 < int(gridDim.x); c0 += kRows * parts) {
+          uint4 v[kRows];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            all[j] += u[j] & 0xffffu;
-            hi_all[j] += int(u[j] >> 16);
-            if (c < int(blockIdx.x)) {
-              before[j] += u[j] & 0xffffu;
-              hi_before[j] += int(u[j] >> 16);
+          for (int k = 0; k < kRows; ++k) {
+            const int c = c0 + k * parts;
+            v[k] = c < int(gridDim.x) ? __ldcg(row + c * columns) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            const bool earlier = c0 + k * parts < int(blockIdx.x);
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              all[j] += u[j] & 0xffffu;
+              hi_all[j] += int(u[j] >> 16);
+              before[j] += earlier ? u[j] & 0xffffu : 0u;
+              hi_before[j] += earlier ? int(u[j] >> 16) : 0;
             }
           }
         }

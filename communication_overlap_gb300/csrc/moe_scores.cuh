@@ -53,6 +53,18 @@ __device__ __forceinline__ float order_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
+// The same in 64 bits, 0 below every number; a NaN above them.
+__device__ __forceinline__ uint64_t order_key_64(double x) {
+  const int64_t b = __double_as_longlong(x + 0.0);
+  return x != x ? ~uint64_t(0) : uint64_t(b) ^ (uint64_t(b >> 63) | uint64_t(1) << 63);
+}
+__device__ __forceinline__ double order_value_64(uint64_t key) {
+  return __longlong_as_double(int64_t(key >> 63 ? key ^ uint64_t(1) << 63 : ~key));
+}
+__device__ __forceinline__ uint64_t shfl_64(uint64_t x, int from) {
+  return __shfl_sync(0xffffffffu, static_cast<unsigned long long>(x), from);
+}
+
 __device__ __forceinline__ float warp_add(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -128,75 +140,6 @@ __device__ __noinline__ bool all_alike(const ScoreArgs& a, int64_t at) {
   for (int e = threadIdx.x & 31; e < a.experts; e += 32)
     if (logit_at(a, at + e) != l0 || (a.bias && __ldg(a.bias + e) != b0)) alike = false;
   return __all_sync(0xffffffffu, alike);
-}
-
-// Of the groups whose lanes say `unsure` the `open_groups` best, in fp64: bit g of the
-// result.  Only experts that may be among a group's two largest are computed, those
-// from `low` on (at most its second, or only, fp32 choice, less a margin), and all of
-// them at once, a lane each: an exponential and a division in fp64 take a
-// microsecond.
-__device__ __noinline__ uint32_t groups_64(const ScoreArgs& a, int64_t at, int width, float top,
-                                           float inv, float low, bool unsure, int open_groups) {
-  const int lane = threadIdx.x & 31;
-  const int g = lane >> a.lane_bits, sub = lane & ((1 << a.lane_bits) - 1);
-  const float ninf = __int_as_float(0xff800000);
-  // (without a bias the largest choice is the largest logit's)
-  const bool by_logit = a.bias == nullptr && a.group_top == 1;
-  const double sum = a.sigmoid || by_logit ? 1.0 : softmax_sum_64(a, at, top);
-  double m1 = 0.0, m2 = 0.0;    // of group `lane`, the two largest so far
-  int n = 0;                    // and how many of them there are
-  bool nan = false;             // ranks the group above every number
-  int mine = -1, held = 0;      // the lane's candidate, and how many lanes have one
-  const auto take = [&]() {
-    float l = 0.0f, b = 0.0f;
-    if (mine >= 0) l = logit_at(a, at + mine), b = a.bias ? __ldg(a.bias + mine) : 0.0f;
-    const double v = mine < 0 ? 0.0 : by_logit ? double(l) : choice_64(a, l, b, top, sum);
-    for (int j = 0; j < held; ++j) {
-      const double w = __shfl_sync(0xffffffffu, v, j);
-      const int e = __shfl_sync(0xffffffffu, mine, j);
-      if (e / a.per != lane) continue;
-      if (w != w) {
-        nan = true;
-      } else if (n == 0 || w > m1) {
-        m2 = m1;
-        m1 = w;
-        n = n ? 2 : 1;
-      } else if (n == 1 || w > m2) {
-        m2 = w;
-        n = 2;
-      }
-    }
-    mine = -1, held = 0;
-  };
-  for (int i = 0; i < width; ++i) {
-    const int k = sub * width + i, e = g * a.per + k;
-    bool in = unsure && g < a.groups && k < a.per;
-    if (in) {
-      const float l = logit_at(a, at + e);
-      const float c = by_logit ? l : score_32(a, l, top, inv) + (a.bias ? __ldg(a.bias + e) : 0.0f);
-      in = l != ninf && c != ninf && !(c < low);
-    }
-    uint32_t todo = __ballot_sync(0xffffffffu, in);
-    if (held + __popc(todo) > 32) take();
-    for (; todo; todo &= todo - 1) {
-      const int c = __shfl_sync(0xffffffffu, e, __ffs(todo) - 1);
-      if (lane == held) mine = c;
-      ++held;
-    }
-  }
-  take();
-  const bool any = n > 0 || nan;
-  const double score = a.group_top == 2 && n == 2 ? m1 + m2 : m1;
-  int rank = 0;
-  for (int h = 0; h < a.groups; ++h) {
-    const double v = __shfl_sync(0xffffffffu, score, h);
-    const bool has = __shfl_sync(0xffffffffu, int(any), h) != 0;
-    const bool its = __shfl_sync(0xffffffffu, int(nan), h) != 0;
-    const bool above = its || nan ? its && (!nan || h < lane)
-                                  : v > score || (v == score && h < lane);
-    rank += has && above;
-  }
-  return __ballot_sync(0xffffffffu, any && rank < open_groups);
 }
 
 // A choice among any number of near ties: each round takes the largest fp32 value
@@ -276,15 +219,13 @@ __device__ __noinline__ int rank_again(const ScoreArgs& a, int64_t at, float top
                                        float b, int n) {
   const int lane = threadIdx.x & 31;
   const double sum = a.sigmoid || !a.bias ? 1.0 : softmax_sum_64(a, at, top);
-  double mine = a.bias ? choice_64(a, l, b, top, sum) : double(l);
-  // NaN above infinity above the rest, and all of them comparable
-  if (mine > 1e300) mine = 1e300;
-  if (mine != mine) mine = 1e301;
+  const double mine = a.bias ? choice_64(a, l, b, top, sum) : double(l);
+  const uint64_t key = order_key_64(mine);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
-    const double v = __shfl_sync(0xffffffffu, mine, j);
+    const uint64_t v = shfl_64(key, j);
     const int e = __shfl_sync(0xffffffffu, id, j);
-    rank += v > mine || (v == mine && e < id);
+    rank += v > key || (v == key && e < id);
   }
   int out = -1;
   for (int j = 0; j < n; ++j) {
@@ -380,9 +321,14 @@ struct Choice {
   uint32_t key[V];
   float top, sum, inv;      // softmax's
   bool open;                // this lane's experts may be chosen
-  int win;                  // slot `lane`: the lane that had it, and its key
-  uint32_t full;
 };
+
+// A rank's expert (-1: none was left) and its key, in shared memory.
+struct Slot {
+  uint32_t key;
+  int32_t expert;
+};
+constexpr int kSlots = 32;
 
 // The keys, sorted.
 template <int V>
@@ -434,12 +380,22 @@ __device__ __forceinline__ float cut_logit_margin(const ScoreArgs& a, const Choi
              : (v * fabsf(c.top) + c.inv) * (float(V) * 0x1p-22f);
 }
 
-// Bars the experts of the groups that do not stay.
+// Which groups stay, as far as fp32 tells.
+struct GroupCut {
+  uint32_t score;           // of this lane's group
+  uint32_t second;          // the least choice that it counts
+  uint32_t in;              // the last that stays
+  float margin;
+  bool stays;
+  bool near;                // the first that goes may have to stay instead (of every lane)
+};
+
 template <int V>
-__device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choice<V>& c) {
+__device__ __forceinline__ GroupCut cut_groups(const ScoreArgs& a, const Choice<V>& c) {
   constexpr uint32_t kMask = V - 1;
   const int lane = threadIdx.x & 31, lanes = 1 << a.lane_bits, g = lane >> a.lane_bits;
   const bool by_logit = a.bias == nullptr;
+  GroupCut r;
   // the two largest of the lane, then of the group
   uint32_t k1 = c.key[0] & ~kMask, k2 = V > 1 ? c.key[V > 1 ? 1 : 0] & ~kMask : 0u;
   if (by_logit && a.group_top == 2) {     // (scores grow with the logits)
@@ -452,61 +408,111 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs& a, int64_t at, Choi
     k2 = max(max(k2, v2), min(k1, v1));
     k1 = max(k1, v1);
   }
-  uint32_t score = k1;
-  if (a.group_top == 2 && k2 != 0u) score = order_key(order_value(k1) + order_value(k2));
+  const bool two = a.group_top == 2 && k2 != 0u;
+  r.score = two ? order_key(order_value(k1) + order_value(k2)) : k1;
+  r.second = two ? k2 : k1;
   int rank = 0;
 #pragma unroll 8
   for (int h = 0; h < a.groups; ++h) {
-    const uint32_t v = __shfl_sync(0xffffffffu, score, h << a.lane_bits);
-    rank += v > score || (v == score && h < g);
+    const uint32_t v = __shfl_sync(0xffffffffu, r.score, h << a.lane_bits);
+    rank += v > r.score || (v == r.score && h < g);
   }
-  bool stays = g < a.groups && score != 0u && rank < a.top_groups;
-  const uint32_t in = __reduce_min_sync(0xffffffffu, stays ? score : 0xffffffffu);
-  const uint32_t out = __reduce_max_sync(0xffffffffu, g < a.groups && !stays ? score : 0u);
-  if (out != 0u) {
-    // (bf16 logits are exact; of fp32 ones the keys leave bits out; sums of two are off
-    // by twice as much)
-    const bool logits = by_logit && a.group_top == 1;
-    const float s0 = score_margin(a.sigmoid, c.inv, V), vi = order_value(in);
-    const float margin =
-        logits ? 0.0f : 2.0f * choice_margin(s0, vi, float(4 * V)) + cut_logit_margin(a, c, vi);
-    const bool near = in == out ? !(logits && a.bf16) : vi - order_value(out) < margin;
-    if (near && !all_alike(a, at)) {
-      // groups further than a margin from the last that stays are sure
-      const bool unsure = g < a.groups && score != 0u &&
-                          (score == in || fabsf(order_value(score) - vi) <= margin);
-      const bool sure = stays && !unsure;
-      const int n_sure =
-          __popc(__ballot_sync(0xffffffffu, sure && (lane & (lanes - 1)) == 0));
-      const float least = order_value(a.group_top == 2 && k2 != 0u ? k2 : k1);
-      const float low =
-          least - (logits ? fabsf(least) * (float(V) * 0x1p-22f)
-                          : choice_margin(s0, least, float(4 * V)) +
-                                cut_logit_margin(a, c, least));
-      const uint32_t best =
-          groups_64(a, at, V, c.top, c.inv, low, unsure, a.top_groups - n_sure);
-      stays = sure || (unsure && (best >> g & 1u));
-    }
-  }
-  c.open = c.open && stays;
-  if (!stays) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) c.key[i] = 0u;
-  }
+  r.stays = g < a.groups && r.score != 0u && rank < a.top_groups;
+  r.in = __reduce_min_sync(0xffffffffu, r.stays ? r.score : 0xffffffffu);
+  const uint32_t out = __reduce_max_sync(0xffffffffu, g < a.groups && !r.stays ? r.score : 0u);
+  // (bf16 logits are exact; of fp32 ones the keys leave bits out; sums of two are off
+  // by twice as much)
+  const bool logits = by_logit && a.group_top == 1;
+  const float vi = order_value(r.in);
+  r.margin = logits ? 0.0f
+                    : 2.0f * choice_margin(score_margin(a.sigmoid, c.inv, V), vi, float(4 * V)) +
+                          cut_logit_margin(a, c, vi);
+  r.near = out != 0u && (r.in == out ? !(logits && a.bf16) : vi - order_value(out) < r.margin);
+  return r;
 }
 
-// The next rank: the largest head of the lanes' lists, on the lowest lane that has
-// it.  Its key without the lane's bits, 0 where none is left.
+// The groups near the cut again, in fp64: whether this lane's stays.  Only experts that
+// may be among a group's two largest are computed, all of them at once, a lane each: an
+// exponential and a division in fp64 take a microsecond.  In the sorted keys of a lane
+// they come first.
 template <int V>
-__device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int s) {
+__device__ __noinline__ bool settle_groups(const ScoreArgs& a, int64_t at, int first, Choice<V> c,
+                                           GroupCut r) {
   constexpr uint32_t kMask = V - 1;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, g = lane >> a.lane_bits;
+  // without a bias the largest choice is the largest logit's
+  const bool by_logit = a.bias == nullptr, logits = by_logit && a.group_top == 1;
+  // groups further than a margin from the last that stays are sure
+  const bool unsure = g < a.groups && r.score != 0u &&
+                      (r.score == r.in || fabsf(order_value(r.score) - order_value(r.in)) <= r.margin);
+  const bool leads = (lane & ((1 << a.lane_bits) - 1)) == 0;
+  const int open =
+      a.top_groups - __popc(__ballot_sync(0xffffffffu, r.stays && !unsure && leads));
+  const float least = order_value(r.second);
+  const float low =
+      least - (logits ? fabsf(least) * (float(V) * 0x1p-22f)
+                      : choice_margin(score_margin(a.sigmoid, c.inv, V), least, float(4 * V)) +
+                            cut_logit_margin(a, c, least));
+  const double sum = a.sigmoid || logits ? 1.0 : softmax_sum_64(a, at, c.top);
+  uint64_t m1 = 0, m2 = 0;      // of group `lane`, the two largest so far
+  int mine = -1, held = 0;      // the lane's candidate, and how many lanes have one
+  const auto take = [&]() {
+    uint64_t key = 0;
+    if (mine >= 0) {
+      const float l = logit_at(a, at + mine);
+      key = order_key_64(logits ? double(l)
+                                : choice_64(a, l, a.bias ? __ldg(a.bias + mine) : 0.0f, c.top, sum));
+    }
+    const int group = mine >= 0 ? mine / a.per : -1;
+    for (int j = 0; j < held; ++j) {
+      const uint64_t v = shfl_64(key, j);
+      const uint64_t k = __shfl_sync(0xffffffffu, group, j) == lane ? v : 0;
+      m2 = max(m2, min(m1, k));
+      m1 = max(m1, k);
+    }
+    mine = -1, held = 0;
+  };
+  for (int i = 0; i < V; ++i) {
+    const uint32_t k = c.key[i];
+    float v = order_value(k & ~kMask);
+    if (by_logit && !logits) v = score_32(a, v, c.top, c.inv);
+    const bool in = unsure && k != 0u && !(v < low);
+    uint32_t todo = __ballot_sync(0xffffffffu, in);
+    if (todo == 0u) break;      // (a lane's keys are sorted)
+    if (held + __popc(todo) > 32) take();
+    const int e = first + int(kMask - (k & kMask));
+    for (; todo; todo &= todo - 1) {
+      const int from = __shfl_sync(0xffffffffu, e, __ffs(todo) - 1);
+      if (lane == held) mine = from;
+      ++held;
+    }
+  }
+  take();
+  const uint64_t score = a.group_top == 2 && m2 != 0
+                             ? order_key_64(order_value_64(m1) + order_value_64(m2))
+                             : m1;
+  int rank = 0;
+  for (uint32_t todo = __ballot_sync(0xffffffffu, m1 != 0); todo; todo &= todo - 1) {
+    const int h = __ffs(todo) - 1;
+    const uint64_t v = shfl_64(score, h);
+    rank += v > score || (v == score && h < lane);
+  }
+  const uint32_t best = __ballot_sync(0xffffffffu, m1 != 0 && rank < open);
+  return unsure ? (best >> g & 1u) != 0 : r.stays;
+}
+
+// The next rank, to slot s: the largest head of the lanes' lists, on the lowest lane
+// that has it.  Its key without the lane's bits, 0 where none is left.
+template <int V>
+__device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int first, Slot* slot, int s) {
+  constexpr uint32_t kMask = V - 1;
+  uint32_t below;
+  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(below));
   const uint32_t head = c.key[0] & ~kMask;
   const uint32_t best = __reduce_max_sync(0xffffffffu, head);
-  const int win = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
-  const uint32_t full = __shfl_sync(0xffffffffu, c.key[0], win);
-  if (lane == s) c.win = win, c.full = full;
-  const bool mine = lane == win;
+  const uint32_t have = __ballot_sync(0xffffffffu, head == best);
+  const bool mine = head == best && (have & below) == 0u;
+  if (mine) slot[s] = {c.key[0], best ? first + int(kMask - (c.key[0] & kMask)) : -1};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const uint32_t after = i + 1 < V ? c.key[i + 1 < V ? i + 1 : i] : 0u;
@@ -521,111 +527,158 @@ __device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int s) {
 template <int V, int N>
 __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExperts<V>& own,
                                             const int64_t (&at)[N], const float (&x)[N][V],
-                                            int (&id)[N], float (&weight)[N]) {
+                                            Slot (*slots)[kSlots], int (&id)[N],
+                                            float (&weight)[N]) {
   constexpr uint32_t kMask = V - 1;
   const int lane = threadIdx.x & 31, K = a.top_k;
-  const float ninf = __int_as_float(0xff800000);
   const bool by_logit = a.bias == nullptr;
   Choice<V> c[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) make_keys<V>(a, own, x[n], c[n]);
   if (a.groups > 1) {
+    GroupCut r[N];
+    bool near = false;
 #pragma unroll
-    for (int n = 0; n < N; ++n) keep_groups<V>(a, at[n], c[n]);
+    for (int n = 0; n < N; ++n) {
+      r[n] = cut_groups<V>(a, c[n]);
+      near = near || r[n].near;
+    }
+    if (near) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (r[n].near && !all_alike(a, at[n]))
+          r[n].stays = settle_groups<V>(a, at[n], own.first, c[n], r[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      c[n].open = c[n].open && r[n].stays;
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[n].key[i] = r[n].stays ? c[n].key[i] : 0u;
+    }
   }
-#pragma unroll
-  for (int n = 0; n < N; ++n) c[n].win = 0, c[n].full = 0u;
   // the slots, and the expert that comes next for its margin (bf16 logits alone keep
   // all their bits in a key and need none)
   const bool exact = by_logit && a.bf16;
   const int rounds = exact || K == 32 ? K : K + 1;
   uint32_t last[N];
+  __syncwarp();       // (the slots of the tokens before have been read)
   for (int s = 0; s < rounds; ++s) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) last[n] = next_rank<V>(c[n], s);
+    for (int n = 0; n < N; ++n) last[n] = next_rank<V>(c[n], own.first, slots[n], s);
   }
+  __syncwarp();
+  uint32_t key[N];    // of slot `lane`
+  const auto read = [&](int n, int ranks) {
+    const Slot q = lane < ranks ? slots[n][lane] : Slot{0u, -1};
+    key[n] = q.key & ~kMask;
+    id[n] = q.expert;
+  };
   float l[N], b[N];
-  const auto expert = [&](const Choice<V>& q) {
-    return q.full == 0u ? -1
-                        : (q.win >> a.lane_bits) * a.per +
-                              (q.win & ((1 << a.lane_bits) - 1)) * V + int(kMask - (q.full & kMask));
+  const auto fetch = [&](int n) {
+    l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
+    b[n] = id[n] >= 0 && !by_logit ? __ldg(a.bias + id[n]) : 0.0f;
   };
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    id[n] = expert(c[n]);
-    l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
-    b[n] = id[n] >= 0 && !by_logit ? __ldg(a.bias + id[n]) : 0.0f;
+    read(n, rounds);
+    fetch(n);
   }
   if (!exact) {
+    const auto near = [&](int n, uint32_t hi, uint32_t lo) {
+      if (hi == 0u || lo == 0u) return false;
+      if (by_logit || hi == lo) return hi == lo;
+      const float v = order_value(hi);
+      return v - order_value(lo) < choice_margin(score_margin(a.sigmoid, c[n].inv, V), v, float(V));
+    };
+    bool unsure[N], all[N], some = false;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const auto near = [&](uint32_t hi, uint32_t lo) {
-        if (hi == 0u || lo == 0u) return false;
-        if (by_logit || hi == lo) return hi == lo;
-        const float v = order_value(hi);
-        return v - order_value(lo) < choice_margin(score_margin(a.sigmoid, c[n].inv, V), v, float(V));
-      };
-      const uint32_t mine = c[n].full & ~kMask;
-      const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+      const uint32_t next = __shfl_down_sync(0xffffffffu, key[n], 1);
       const float next_l = __shfl_down_sync(0xffffffffu, l[n], 1);
       const float next_b = __shfl_down_sync(0xffffffffu, b[n], 1);
       // (alike neighbours lie in order; but at the last slot another expert may be as
       // near behind them)
       const bool alike = lane + 1 < K && l[n] == next_l && b[n] == next_b;
-      const bool unsure = lane < K && lane < 31 && !alike && near(mine, next);
-      bool all = false;       // (no lane holds the expert after slot 31)
+      unsure[n] = lane < K && lane < 31 && !alike && near(n, key[n], next);
+      all[n] = false;       // (no lane holds the expert after slot 31)
       if (K == 32)
-        all = near(__shfl_sync(0xffffffffu, mine, 31),
-                   __reduce_max_sync(0xffffffffu, c[n].key[0] & ~kMask));
-      if ((!__any_sync(0xffffffffu, unsure) && !all) || all_alike(a, at[n])) continue;
-      // the ranks that follow, as far as they are near to the one before
-      int s = rounds;
-      bool chain = K < 32 && near(__shfl_sync(0xffffffffu, mine, K - 1), last[n]);
-      while (chain && s < 32) {
-        const uint32_t before = last[n];
-        last[n] = next_rank<V>(c[n], s++);
-        chain = near(before, last[n]);
-      }
-      if (all || chain) {
-        id[n] = choose_among_all(a, at[n], V, c[n].top, c[n].inv, c[n].open);
-      } else {
-        id[n] = expert(c[n]);
+        all[n] = near(n, __shfl_sync(0xffffffffu, key[n], 31),
+                      __reduce_max_sync(0xffffffffu, c[n].key[0] & ~kMask));
+      some = some || unsure[n] || all[n];
+    }
+    if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if ((!__any_sync(0xffffffffu, unsure[n]) && !all[n]) || all_alike(a, at[n])) continue;
+        // the ranks that follow, as far as they are near to the one before
+        int s = rounds;
+        bool chain = K < 32 && near(n, __shfl_sync(0xffffffffu, key[n], K - 1), last[n]);
+        while (chain && s < kSlots) {
+          const uint32_t before = last[n];
+          last[n] = next_rank<V>(c[n], own.first, slots[n], s++);
+          chain = near(n, before, last[n]);
+        }
+        if (all[n] || chain) {
+          id[n] = choose_among_all(a, at[n], V, c[n].top, c[n].inv, c[n].open);
+        } else {
+          __syncwarp();
+          read(n, s);
+          fetch(n);
+          const uint32_t lanes = __ballot_sync(0xffffffffu, id[n] >= 0);
+          id[n] = rank_again(a, at[n], c[n].top, id[n], l[n], b[n], __popc(lanes));
+        }
+        if (lane >= K) id[n] = -1;
         l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
-        b[n] = id[n] >= 0 && !by_logit ? __ldg(a.bias + id[n]) : 0.0f;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, id[n] >= 0);
-        id[n] = rank_again(a, at[n], c[n].top, id[n], l[n], b[n], __popc(lanes));
       }
-      if (lane >= K) id[n] = -1;
-      l[n] = id[n] >= 0 ? logit_at(a, at[n] + id[n]) : 0.0f;
     }
   }
   // the weights, in fp32, by expf and a division of 2 ulp.  Chosen scores may all be
   // far below 1: those to be renormalised share a factor that makes the largest
   // about 1.
+  float w[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < N; ++n)
     if (lane >= K) id[n] = -1;
-    float w = 0.0f;
-    if (a.renormalize) {
-      // e^(l - m) / (1 + e^l), m the largest chosen logit where that is negative; softmax
-      // over the chosen, whatever share of the whole they have (a NaN or +inf anywhere
-      // enters every score)
-      const float most =
-          order_value(__reduce_max_sync(0xffffffffu, id[n] >= 0 ? order_key(l[n]) : 0u));
-      if (a.sigmoid)
-        w = __fdividef(expf(fminf(l[n], 0.0f) - fminf(most, 0.0f)), 1.0f + expf(-fabsf(l[n])));
-      else
-        w = c[n].sum == c[n].sum ? expf(l[n] - most) : c[n].sum;
-      if (l[n] != l[n]) w = l[n];       // (fminf would drop a NaN)
-      w = id[n] >= 0 ? w : 0.0f;
-      w = __fdividef(w, warp_add(w));
-    } else if (a.sigmoid) {
-      w = __fdividef(1.0f, 1.0f + expf(-l[n]));
+  if (a.renormalize) {
+    // e^(l - m) / (1 + e^l), m the largest chosen logit where that is negative; softmax
+    // over the chosen, whatever share of the whole they have (a NaN or +inf anywhere
+    // enters every score)
+    float most[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      most[n] = order_value(__reduce_max_sync(0xffffffffu, id[n] >= 0 ? order_key(l[n]) : 0u));
+    if (a.sigmoid) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        w[n] = __fdividef(expf(fminf(l[n], 0.0f) - fminf(most[n], 0.0f)), 1.0f + expf(-fabsf(l[n])));
     } else {
-      w = __fdividef(expf(l[n] - c[n].top), c[n].sum);
+#pragma unroll
+      for (int n = 0; n < N; ++n) w[n] = c[n].sum == c[n].sum ? expf(l[n] - most[n]) : c[n].sum;
     }
-    weight[n] = id[n] >= 0 ? a.scale * w : 0.0f;
+    float sum[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (l[n] != l[n]) w[n] = l[n];       // (fminf would drop a NaN)
+      w[n] = id[n] >= 0 ? w[n] : 0.0f;
+      sum[n] = w[n];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= K) continue;                // (of lanes without a slot: zeros)
+#pragma unroll
+      for (int n = 0; n < N; ++n) sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], o);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = __fdividef(w[n], sum[n]);
+  } else if (a.sigmoid) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = __fdividef(1.0f, 1.0f + expf(-l[n]));
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = __fdividef(expf(l[n] - c[n].top), c[n].sum);
   }
+#pragma unroll
+  for (int n = 0; n < N; ++n) weight[n] = id[n] >= 0 ? a.scale * w[n] : 0.0f;
 }
 
 }  // namespace fo
