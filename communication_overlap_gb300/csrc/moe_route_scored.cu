@@ -69,7 +69,6 @@ __global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredA
   int32_t* total = start + E;                             // [E]
   int32_t* first = total + E;                             // [E]
   __shared__ int32_t ok_s;
-  __shared__ Slot slots_s[kScoredThreads / 32][V <= 8 ? 2 : 1][kSlots];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = int(blockDim.x) / 32;
   const bool lead = !a.alone || blockIdx.x == 0;          // this CTA writes its tokens' outputs
   const int64_t t0 = a.alone ? 0 : int64_t(blockIdx.x) * a.chunk;
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1) scored_kernel(const ScoredA
       for (int i = 0; i < V; ++i) x[j][i] = ahead[j][i];
     }
     if constexpr (kAhead) load(t + kTokens * warps);
-    warp_choose<V, kTokens>(a.score, own, at, x, slots_s[warp], id, w);
+    warp_choose<V, kTokens>(a.score, own, at, x, id, w);
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
       const int u = t + j * warps;

@@ -321,14 +321,9 @@ struct Choice {
   uint32_t key[V];
   float top, sum, inv;      // softmax's
   bool open;                // this lane's experts may be chosen
+  int win;                  // rank `lane`: the lane that had it, and its key
+  uint32_t full;
 };
-
-// A rank's expert (-1: none was left) and its key, in shared memory.
-struct Slot {
-  uint32_t key;
-  int32_t expert;
-};
-constexpr int kSlots = 32;
 
 // The keys, sorted.
 template <int V>
@@ -501,18 +496,19 @@ __device__ __noinline__ bool settle_groups(const ScoreArgs& a, int64_t at, int f
   return unsure ? (best >> g & 1u) != 0 : r.stays;
 }
 
-// The next rank, to slot s: the largest head of the lanes' lists, on the lowest lane
-// that has it.  Its key without the lane's bits, 0 where none is left.
+// The next rank: the largest head of the lanes' lists, on the lowest lane that has
+// it.  Its key without the lane's bits, 0 where none is left.
 template <int V>
-__device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int first, Slot* slot, int s) {
+__device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int s) {
   constexpr uint32_t kMask = V - 1;
-  uint32_t below;
-  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(below));
+  const int lane = threadIdx.x & 31;
   const uint32_t head = c.key[0] & ~kMask;
   const uint32_t best = __reduce_max_sync(0xffffffffu, head);
-  const uint32_t have = __ballot_sync(0xffffffffu, head == best);
-  const bool mine = head == best && (have & below) == 0u;
-  if (mine) slot[s] = {c.key[0], best ? first + int(kMask - (c.key[0] & kMask)) : -1};
+  const int win = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+  const uint32_t full = __shfl_sync(0xffffffffu, c.key[0], win);
+  c.win = lane == s ? win : c.win;
+  c.full = lane == s ? full : c.full;
+  const bool mine = lane == win;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const uint32_t after = i + 1 < V ? c.key[i + 1 < V ? i + 1 : i] : 0u;
@@ -527,8 +523,7 @@ __device__ __forceinline__ uint32_t next_rank(Choice<V>& c, int first, Slot* slo
 template <int V, int N>
 __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExperts<V>& own,
                                             const int64_t (&at)[N], const float (&x)[N][V],
-                                            Slot (*slots)[kSlots], int (&id)[N],
-                                            float (&weight)[N]) {
+                                            int (&id)[N], float (&weight)[N]) {
   constexpr uint32_t kMask = V - 1;
   const int lane = threadIdx.x & 31, K = a.top_k;
   const bool by_logit = a.bias == nullptr;
@@ -561,17 +556,19 @@ __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExpert
   const bool exact = by_logit && a.bf16;
   const int rounds = exact || K == 32 ? K : K + 1;
   uint32_t last[N];
-  __syncwarp();       // (the slots of the tokens before have been read)
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n].win = 0, c[n].full = 0u;
   for (int s = 0; s < rounds; ++s) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) last[n] = next_rank<V>(c[n], own.first, slots[n], s);
+    for (int n = 0; n < N; ++n) last[n] = next_rank<V>(c[n], s);
   }
-  __syncwarp();
-  uint32_t key[N];    // of slot `lane`
-  const auto read = [&](int n, int ranks) {
-    const Slot q = lane < ranks ? slots[n][lane] : Slot{0u, -1};
-    key[n] = q.key & ~kMask;
-    id[n] = q.expert;
+  uint32_t key[N];    // of rank `lane`
+  const auto read = [&](int n) {
+    key[n] = c[n].full & ~kMask;
+    id[n] = c[n].full == 0u
+                ? -1
+                : (c[n].win >> a.lane_bits) * a.per + (c[n].win & ((1 << a.lane_bits) - 1)) * V +
+                      int(kMask - (c[n].full & kMask));
   };
   float l[N], b[N];
   const auto fetch = [&](int n) {
@@ -580,7 +577,7 @@ __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExpert
   };
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    read(n, rounds);
+    read(n);
     fetch(n);
   }
   if (!exact) {
@@ -613,16 +610,15 @@ __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExpert
         // the ranks that follow, as far as they are near to the one before
         int s = rounds;
         bool chain = K < 32 && near(n, __shfl_sync(0xffffffffu, key[n], K - 1), last[n]);
-        while (chain && s < kSlots) {
+        while (chain && s < 32) {
           const uint32_t before = last[n];
-          last[n] = next_rank<V>(c[n], own.first, slots[n], s++);
+          last[n] = next_rank<V>(c[n], s++);
           chain = near(n, before, last[n]);
         }
         if (all[n] || chain) {
           id[n] = choose_among_all(a, at[n], V, c[n].top, c[n].inv, c[n].open);
         } else {
-          __syncwarp();
-          read(n, s);
+          read(n);
           fetch(n);
           const uint32_t lanes = __ballot_sync(0xffffffffu, id[n] >= 0);
           id[n] = rank_again(a, at[n], c[n].top, id[n], l[n], b[n], __popc(lanes));
