@@ -7,8 +7,9 @@
 //   softmax:               w g - p dot, and -p dot at every other expert
 // elsewhere zero.  The bias decides the choice only and has no gradient.
 //
-// A warp per token writes the row (zeros, or -p dot), then its slots.  The bytes
-// of dlogits bound it.
+// A warp per token writes the row (zeros, in 16 bytes per lane, while the slots are on
+// their way; or -p dot), then its slots.  16384 x 256 in fp32: 4.9 us within a graph
+// (5.7 with a lane's element per store), 11.4 where softmax's sum is formed again.
 #include <cuda_runtime.h>
 
 #include "moe_common.cuh"
@@ -42,26 +43,38 @@ __device__ __forceinline__ void put(const BackArgs& a, int64_t i, float v) {
     static_cast<float*>(a.dlogits)[i] = v;
 }
 
+// A row of zeros, by a warp.
+__device__ __forceinline__ void put_zeros(const BackArgs& a, int64_t at) {
+  const int lane = threadIdx.x & 31, size = a.bf16 ? 2 : 4;
+  char* p = static_cast<char*>(a.dlogits) + at * size;
+  int bytes = 0;                // that were written in wide stores
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    bytes = a.experts * size & ~15;
+    for (int i = lane * 16; i < bytes; i += 512)
+      *reinterpret_cast<int4*>(p + i) = make_int4(0, 0, 0, 0);
+  }
+  for (int e = bytes / size + lane; e < a.experts; e += 32) put(a, at + e, 0.0f);
+}
+
 __global__ void __launch_bounds__(256) scored_backward_kernel(const BackArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= a.tokens) return;
   const int E = a.experts, K = a.top_k;
+  const bool zeros = a.sigmoid || a.renormalize;      // but at the chosen
+  const int64_t to = t * a.dstride, from = t * a.stride;
   int id = -1;
   float w = 0.0f, g = 0.0f;
   if (lane < K) {
     id = a.ids[t * K + lane];
-    if (id >= 0 && id < E) {
-      w = a.weights[t * K + lane];
-      g = a.dweights[t * K + lane];
-    } else {
-      id = -1;
-    }
+    w = a.weights[t * K + lane];
+    g = a.dweights[t * K + lane];
   }
+  if (zeros) put_zeros(a, to);
+  if (id < 0 || id >= E) id = -1, w = g = 0.0f;
   float dot = w * g;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  const int64_t to = t * a.dstride, from = t * a.stride;
   float d = 0.0f;
   if (a.sigmoid) {
     // 1 - s = 1 / (1 + e^l)
@@ -70,9 +83,7 @@ __global__ void __launch_bounds__(256) scored_backward_kernel(const BackArgs a) 
   } else if (a.renormalize) {
     d = w * (g - dot / a.scale);
   }
-  if (a.sigmoid || a.renormalize) {
-    for (int e = lane; e < E; e += 32) put(a, to + e, 0.0f);
-  } else {
+  if (!zeros) {
     const float ninf = __int_as_float(0xff800000);
     float top = ninf;
     for (int e = lane; e < E; e += 32) top = fmaxf(top, logit_at(a, from + e));
