@@ -2,12 +2,12 @@
 // tables, a stable counting sort of the (token, slot) pairs by expert:
 //   row(t, s) = first[e] + |{(t', s') before (t, s): id(t', s') = e}|.
 //
-// One kernel.  CTA c owns a contiguous chunk of tokens, a warp one token at a time:
+// One kernel.  CTA c owns a contiguous chunk of tokens, a warp one or two at a time:
 //   1. choose; ids stay in shared memory; the CTA's share of the tables is emptied;
 //   2. count the chunk's pairs per expert and segment (32 pairs or a multiple);
 //   3. grid barrier, with every chunk's counts in global memory;
 //   4. the experts' ranges and this chunk's start in each, then the pairs' rows.
-// Up to a warp's worth of tokens per warp of a CTA need no barrier: then every CTA
+// Up to 16 tokens, one per warp of a CTA, need no barrier: then every CTA
 // makes the same choice, and each fills its share of the tables (of one token over
 // 128 experts these are 130 KB, more than one CTA should write).
 //
@@ -15,7 +15,7 @@
 // groups, top 8, take 32 us on the device: 18 of choosing, with about 900 warp
 // instructions a token and three quarters of the issue slots in use, up to 5 more in a
 // CTA with a token to decide in fp64, 1.5 to begin, and 6 of barrier, counts and rows.
-// One token takes 8.6, 130 KB of tables to empty among it.
+// One token takes 8.
 #include <cuda_runtime.h>
 
 #include <mutex>
