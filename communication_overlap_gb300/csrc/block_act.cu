@@ -13,8 +13,8 @@
 // size has 4 significant bits per value: three times the error on normal data.
 //
 // Both passes move each byte once and HBM bounds them: 32768 x 14336 of bf16, 3.79 GB
-// each, 572 us forward (6.6 TB/s) and 617 back (6.1), where issue slots are 43 and 55 %
-// busy.  Two rows of 14336 take 1.6 us on the device.
+// each, 572 us forward (6.6 TB/s) and 617 back (6.1), where 65 and 64 % of the
+// issue slots are in use.  Two rows of 14336 take 1.6 us on the device.
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"

@@ -13,7 +13,7 @@
 //
 // Bytes are few (a logit once); instructions bound it.  16384 tokens of 256 experts in 8
 // groups, top 8, take 32 us on the device: 18 of choosing, with about 900 warp
-// instructions a token and three quarters of the issue slots in use, up to 5 more in a
+// instructions a token and about two thirds of the issue slots in use, up to 5 more in a
 // CTA with a token to decide in fp64, 1.5 to begin, and 6 of barrier, counts and rows.
 // One token takes 8.
 #include <cuda_runtime.h>
