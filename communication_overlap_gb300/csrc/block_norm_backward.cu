@@ -577,15 +577,15 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackArgs a,
   store_parts<W>(a, n, worker, col, dpre, dpost);
 }
 
-// The parts' sums: a CTA takes 32 columns of one result, its warps every eighth
-// part, and joins them in their order.
-__global__ void __launch_bounds__(256) norm_join_kernel(const NormBackArgs a, const BackShape n,
-                                                        int columns) {
-  __shared__ float buf[8][33];
+// The parts' sums: a CTA takes 32 columns of one result, its warps every eighth part
+// (or every 32nd, of many short rows' workers), and joins them in their order.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const NormBackArgs a, const BackShape n,
+                                                         int columns) {
+  __shared__ float buf[32][33];
   const NormArgs& f = a.f;
   int64_t which = blockIdx.x / unsigned(columns);
   const int col = int(blockIdx.x % unsigned(columns)) * 32 + (threadIdx.x & 31);
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, warps = int(blockDim.x) >> 5;
   const float* from = nullptr;
   void* to = nullptr;
   int64_t lo = 0, hi = n.workers, at = 0;
@@ -603,14 +603,20 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormBackArgs a, co
   }
   float sum = 0.0f;
   if (col < f.hidden) {
-#pragma unroll 4
-    for (int64_t w = lo + warp; w < hi; w += 8) sum += __ldcs(from + w * f.hidden + col);
+    constexpr int kAtOnce = 10;       // 152 workers: two waits
+    for (int64_t w = lo + warp; w < hi; w += kAtOnce * warps) {
+      float v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        v[i] = w + i * warps < hi ? __ldcs(from + (w + i * warps) * f.hidden + col) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) sum += v[i];
+    }
   }
   buf[warp][threadIdx.x & 31] = sum;
   __syncthreads();
   if (warp != 0 || col >= f.hidden) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) sum += buf[i][threadIdx.x];
+  for (int i = 1; i < warps; ++i) sum += buf[i][threadIdx.x];
   if (f.params_f32)
     static_cast<float*>(to)[at + col] = sum;
   else
@@ -748,8 +754,10 @@ fo_status launch_block_norm_backward(const NormBackArgs& a, fo_type type, fo_typ
   }
   if (q != FO_OK) return q;
   if (cudaGetLastError() != cudaSuccess) return FO_ERR_CUDA;
+  // (16384 x 64 in bf16, 2432 workers: 37 us with eight warps, 20 with 32)
   if (results > 0)
-    norm_join_kernel<<<unsigned(results * columns), 256, 0, st>>>(a, n, int(columns));
+    norm_join_kernel<<<unsigned(results * columns), n.workers > 160 ? 1024 : 256, 0, st>>>(
+        a, n, int(columns));
   return cudaGetLastError() == cudaSuccess ? FO_OK : FO_ERR_CUDA;
 }
 
