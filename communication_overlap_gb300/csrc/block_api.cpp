@@ -123,7 +123,7 @@ fo_status fo_moe_combine_backward(const void* dy, fo_type dy_type, int64_t dy_st
 
 fo_status fo_checkpoint_sizes(int64_t rows, int64_t inter, int64_t* code_bytes,
                               int64_t* scale_bytes) {
-  if (rows < 0 || inter < 0 || inter > kMaxBytes - 31) return FO_ERR_ARG;
+  if (rows < 0 || inter < 0 || inter > kMaxBytes / 2 - 32) return FO_ERR_ARG;
   const int64_t padded = (inter + 31) / 32 * 32;
   int64_t n;
   if (__builtin_mul_overflow(rows, 2 * padded, &n) || n >= kMaxBytes) return FO_ERR_ARG;

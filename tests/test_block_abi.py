@@ -104,6 +104,14 @@ def test_combine_backward_refuses(bad):
     refused(ARG, fo.fo_moe_combine_backward, *{**COMBINE_BACK, **bad}.values())
 
 
+def test_checkpoint_sizes_that_do_not_fit():
+    for inter in ((1 << 62) - 31, (1 << 62) - 32, (1 << 61) - 31, 1 << 61):
+        for rows in (1, 2, 3):
+            refused(ARG, fo.fo_checkpoint_sizes, rows, inter)
+    n = (1 << 60) - 32
+    assert fo.fo_checkpoint_sizes(1, n) == (2 * n, n // 16)
+
+
 def test_checkpoint_sizes():
     assert fo.fo_checkpoint_sizes(3, 33) == (3 * 2 * 64, 3 * 2 * 2)
     assert fo.fo_checkpoint_sizes(0, 5) == (0, 0) and fo.fo_checkpoint_sizes(5, 0) == (0, 0)
