@@ -166,7 +166,8 @@ def norm_backward(x, residual, normed, dstream=None, dy=None, post_gain=None, ga
         _matrix(dstream, (T, H), x.dtype if residual is None else residual.dtype, "dstream")
     at = 0
     if post_gain is not None or pre_gain is not None:
-        if rstd is None or rstd.shape != (2, T) or not rstd.is_contiguous():
+        if (rstd is None or rstd.shape != (2, T) or rstd.dtype != torch.float32
+                or not rstd.is_contiguous()):
             raise ValueError(f"normed holds no norms of {T} tokens")
         at = rstd.data_ptr()
     empty, like = torch.empty, torch.empty_like
@@ -195,6 +196,18 @@ class Checkpoint:
     rows: int
     inter: int
     act: str
+
+    def __post_init__(self):
+        want = _checkpoint_sizes(self.rows, self.inter)
+        have = (self.codes.numel(), self.scales.numel())
+        if have != want or self.codes.dtype != torch.int8 or self.scales.dtype != torch.uint8:
+            raise ValueError(f"int8 codes and uint8 scales of {want} bytes expected, not {have}")
+        if not (self.codes.is_contiguous() and self.scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        if self.codes.get_device() != self.scales.get_device():
+            raise ValueError("codes and scales must be on one device")
+        if self.act not in _ACTS:
+            raise ValueError(f"act: one of {sorted(_ACTS)} expected, not {self.act!r}")
 
     def values(self, dtype=torch.float32):
         """The values it stands for, [rows, 2 * inter]."""

@@ -507,3 +507,36 @@ def test_refusals():
     for call in bad:
         with pytest.raises((ValueError, fo.FoError)):
             call()
+
+
+@pytest.mark.parametrize("H", [72, 73, 4096])
+@pytest.mark.parametrize("slots", [(0, 1), (1, 4), (2, 5), (0, 5)])
+def test_combine_a_row_named_twice(H, slots):
+    """Forward it counts twice; its gradient is that of the last slot.  A row that
+    another token's slot names as well: left out there, and the status says so."""
+    T, k = 37, 6
+    rng = np.random.default_rng(H)
+    token_row = np.arange(T * k, dtype=np.int32).reshape(T, k)
+    row_token = np.repeat(np.arange(T, dtype=np.int32), k)
+    lost = token_row[:, slots[1]].copy()
+    token_row[:, slots[1]] = token_row[:, slots[0]]
+    row_token[lost] = -1
+    rows = rng.integers(-4, 5, (T * k, H)).astype(np.float32)
+    w = rng.integers(1, 5, (T, k)).astype(np.float32)
+    dy = rng.integers(-4, 5, (T, H)).astype(np.float32)
+    put = lambda a: torch.from_numpy(a).cuda()
+    y = block.combine(put(rows), put(token_row), put(w))
+    assert np.array_equal(y.cpu().numpy(), np.einsum("tk,tkh->th", w, rows[token_row]))
+    drows, dw = block.combine_backward(put(dy), put(rows), put(token_row), put(row_token), put(w))
+    want = np.zeros_like(rows)
+    for t in range(T):
+        for s in range(k):
+            want[token_row[t, s]] = w[t, s] * dy[t]
+    assert np.array_equal(drows.cpu().numpy(), want)
+    assert np.array_equal(dw.cpu().numpy(), np.einsum("th,tkh->tk", dy, rows[token_row]))
+    assert moe.device_status() == fo.FO_OK
+    token_row[1, slots[0]] = token_row[0, 3]
+    drows, dw = block.combine_backward(put(dy), put(rows), put(token_row), put(row_token), put(w))
+    assert np.array_equal(drows.cpu().numpy()[token_row[0, 3]], want[token_row[0, 3]])
+    assert dw.cpu().numpy()[1, slots[0]] == 0
+    assert moe.device_status(clear=True) == fo.FO_ERR_ARG
