@@ -12,7 +12,7 @@
 //
 // 16384 x 4096 of bf16: 537 MB in 84 us (6.4 TB/s).  Few or short rows leave each CTA a
 // few rows only, and launch, the first row's way and the last CTA's weigh more: 4095 x
-// 2752 of bf16 into an fp32 stream 135 MB in 35 us (3.9).  One row of 4096 takes 3.3 us.
+// 2752 of bf16 into an fp32 stream 135 MB in 30 us (4.5).  One row of 4096 takes 3.3 us.
 #include <cuda_runtime.h>
 
 #include "block_norm.cuh"
@@ -43,6 +43,23 @@ __device__ __forceinline__ void stream_of(const NormArgs& a, int col, int64_t ga
   for (int i = 0; i < W; ++i) s[i] = fmaf(a.scale, v[i], r[i]);
 }
 
+// A worker's tokens: with several rows of the gate next to each other, so that it meets
+// few of them (their factors are a wait each: five sequences of 819 x 2752 33 -> 30 us),
+// else at a stride (16384 x 4096 in bf16 92 us, next to each other 98).
+struct Tokens {
+  int first, end, step;
+  __device__ __forceinline__ Tokens(const NormArgs& a, int worker, int workers) {
+    if (a.gate_stride == 0) {
+      first = worker, end = a.tokens, step = workers;
+    } else {
+      const int each = a.tokens / workers, more = a.tokens % workers;
+      first = worker * each + min(worker, more);
+      end = first + each + (worker < more ? 1 : 0);
+      step = 1;
+    }
+  }
+};
+
 // Rows of up to 8192 columns; several to a CTA where they have few warps.  CTAs walk
 // over the tokens with the parameters' product in registers and DEPTH rows under way
 // in the ring, two values per instruction.  16384 x 4096: a CTA per row, which loads
@@ -60,8 +77,8 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
   const RowGroup g = RowGroup::of(warps);
   const OwnRing ring(smem);
   const int rows = int(blockDim.x) / (warps * 32);
-  const int step = int(gridDim.x) * rows;
-  const int t0 = int(blockIdx.x) * rows + g.index;
+  const Tokens own(a, int(blockIdx.x) * rows + g.index, int(gridDim.x) * rows);
+  const int t0 = own.first;
   const float inv = 1.0f / float(a.hidden);
   int col[NV];
   bool has[NV];
@@ -72,10 +89,10 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
   }
   const A* x_at = static_cast<const A*>(a.x) + int64_t(t0) * a.x_stride;
   const S* r_at = static_cast<const S*>(a.residual) + int64_t(t0) * a.residual_stride;
-  const int64_t x_step = step * a.x_stride, r_step = step * a.residual_stride;
+  const int64_t x_step = own.step * a.x_stride, r_step = own.step * a.residual_stride;
   int fetched = t0;
   const auto fetch = [&](int stage) {
-    if (fetched < a.tokens) {
+    if (fetched < own.end) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int at = stage * kPieces + v * (kA + kS);
@@ -84,7 +101,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
       }
     }
     OwnRing::commit();
-    fetched += step;
+    fetched += own.step;
     x_at += x_step;
     r_at += r_step;
   };
@@ -103,8 +120,8 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
   int gate_row = -1, stage = 0;
   S* sum_at = static_cast<S*>(a.sum) + int64_t(t0) * a.sum_stride;
   A* y_at = static_cast<A*>(a.y) + int64_t(t0) * a.y_stride;
-  const int64_t sum_step = step * a.sum_stride, y_step = step * a.y_stride;
-  for (int t = t0; t < a.tokens; t += step) {
+  const int64_t sum_step = own.step * a.sum_stride, y_step = own.step * a.y_stride;
+  for (int t = t0; t < own.end; t += own.step) {
     const int row = a.gate_stride ? int(uint32_t(t) / uint32_t(a.gate_rows)) : 0;
     if (row != gate_row) {
 #pragma unroll
@@ -184,7 +201,8 @@ __global__ void __launch_bounds__(512, 1) norm_few_kernel(const NormArgs a, int 
   __syncthreads();
   int turn = 0;
   const RowGroup g = RowGroup::of(warps);
-  const int rows = int(blockDim.x) / (warps * 32), step = int(gridDim.x) * rows;
+  const int rows = int(blockDim.x) / (warps * 32);
+  const Tokens own(a, int(blockIdx.x) * rows + g.index, int(gridDim.x) * rows);
   const int first = g.tid * E, stride = warps * 32 * E;
   const float inv = 1.0f / float(a.hidden);
   Few<A, E> px[U];
@@ -194,15 +212,14 @@ __global__ void __launch_bounds__(512, 1) norm_few_kernel(const NormArgs a, int 
     const S* r = static_cast<const S*>(a.residual) + t * a.residual_stride + first;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool has = t < a.tokens && first + i * stride < a.hidden;
+      const bool has = t < own.end && first + i * stride < a.hidden;
       px[i].zero();
       pr[i].zero();
       if (has) px[i].load(x + i * stride);
       if (has && a.residual != nullptr) pr[i].load(r + i * stride);
     }
   };
-  const int t0 = int(blockIdx.x) * rows + g.index;
-  load(t0);
+  load(own.first);
   float w[U][E], pre[U][E];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(512, 1) norm_few_kernel(const NormArgs a, int 
       load_few_param<E>(a.pre, first + i * stride, a.params_f32, pre[i]);
   }
   int gate_row = -1;
-  for (int t = t0; t < a.tokens; t += step) {
+  for (int t = own.first; t < own.end; t += own.step) {
     const int row = a.gate_stride ? int(uint32_t(t) / uint32_t(a.gate_rows)) : 0;
     if (row != gate_row) {
 #pragma unroll
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(512, 1) norm_few_kernel(const NormArgs a, int 
       px[i].get(x[i]);
       pr[i].get(s[i]);
     }
-    load(int64_t(t) + step);
+    load(int64_t(t) + own.step);
     if (a.post != nullptr) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
