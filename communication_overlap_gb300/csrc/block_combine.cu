@@ -4,7 +4,7 @@
 //   drows[r_ts] = w_ts dy_t,  dw_ts = <dy_t, rows[r_ts]>,  drows = 0 elsewhere.
 //
 // Both move each byte once and HBM bounds them: 16384 x 4096 of bf16, top 2, 403 MB in
-// 68 us (5.9 TB/s) and back 680 MB in 105 (6.5); 5001 x 2048 of fp32, top 6, 265 MB in
+// 66 us (6.1 TB/s) and back 680 MB in 105 (6.5); 5001 x 2048 of fp32, top 6, 265 MB in
 // 42 us (6.3) and 517 MB in 84 (6.1).  Sums are fp32, in slot order; outputs are rounded
 // once.
 #include <cuda_runtime.h>
@@ -41,10 +41,13 @@ __device__ __forceinline__ int row_of(int32_t r, int64_t table_rows, int32_t* st
 }
 
 // Rows on 16 bytes: a thread takes eight columns of TOKENS tokens, SLOTS of their slots
-// at a time.  CTAs walk over the items, and the next item's rows are looked up while this one's are on
-// their way: a look-up and the rows it names are two waits in a row otherwise.
+// at a time.  CTAs walk over the items, and the next item's rows are looked up while
+// this one's are on their way: a look-up and the rows it names are two waits in a row
+// otherwise.  Of bf16 rows four CTAs fit on an SM (16384 x 4096, top 2, 66.5 us; three
+// 69); fp32 rows' registers would spill (106 -> 151).
 template <typename T, typename O, int SLOTS, int TOKENS>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1)
+    combine_kernel(const CombineArgs a) {
   const int local = a.pieces > 1 ? 0 : int(threadIdx.x) / a.chunks;
   const int lane_col = a.pieces > 1 ? int(threadIdx.x) : int(threadIdx.x) % a.chunks;
   const int per = a.per_item / TOKENS;      // from one of the thread's tokens to the next
@@ -522,7 +525,9 @@ template <typename T, typename O>
 fo_status forward(const CombineArgs& a, Rows rows, cudaStream_t st) {
   if (rows == Rows::kOne) return forward_any<T, O, 1>(a, st);
   if (rows == Rows::kTwo) return forward_any<T, O, 2>(a, st);
-  if (a.top_k <= 2) return forward_as<T, O, 2, 2>(a, st);
+  // (16384 x 4096, top 1: as half of two slots 56 us, of fp32 77; so 49 and 65)
+  if (a.top_k == 1) return forward_as<T, O, 1, 2>(a, st);
+  if (a.top_k == 2) return forward_as<T, O, 2, 2>(a, st);
   return forward_as<T, O, 4, 1>(a, st);
 }
 
