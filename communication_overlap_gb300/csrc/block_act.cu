@@ -13,8 +13,8 @@
 // size has 4 significant bits per value: three times the error on normal data.
 //
 // Both passes move each byte once and HBM bounds them: 32768 x 14336 of bf16, 3.79 GB
-// each, 572 us forward (6.6 TB/s) and 617 back (6.1), where 65 and 64 % of the
-// issue slots are in use.  Two rows of 14336 take 1.6 us on the device.
+// each, 584 us forward (6.5 TB/s) and 540 back (7.0).  Two rows of 14336 take 1.6 us on
+// the device.
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"
@@ -128,6 +128,42 @@ __device__ __forceinline__ void gated_backward(float dh, float g, float u, int a
   } else {
     dg = dh * u;
     du = dh * g;
+  }
+}
+
+// The same for eight columns whose g and u are codes; of silu two values per
+// instruction.
+__device__ __forceinline__ Pair code_pair(uint32_t flipped, int i, float step) {
+  const Pair v = Pair::of(__uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 + 2 * i)),
+                          __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7441 + 2 * i)));
+  return (v + Pair::of(-8388736.0f)) * Pair::of(step);
+}
+template <typename T>
+__device__ __forceinline__ void gated_backward(const Pack8<T>& dh, uint2 gate, uint2 up,
+                                               float gate_step, float up_step, int act,
+                                               float (&dg)[8], float (&du)[8]) {
+  if (act == FO_ACT_SILU) {
+    Pair d[4];
+    pairs_of(dh, d);
+    const uint32_t qg[2] = {gate.x ^ 0x80808080u, gate.y ^ 0x80808080u};
+    const uint32_t qu[2] = {up.x ^ 0x80808080u, up.y ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Pair g = code_pair(qg[i / 2], i & 1, gate_step), u = code_pair(qu[i / 2], i & 1, up_step);
+      float a, b;
+      g.get(a, b);
+      const Pair s = Pair::of(sigmoid<T>(a), sigmoid<T>(b)), one = Pair::of(1.0f);
+      const Pair slope = s * fma2(g, fma2(s, Pair::of(-1.0f), one), one);
+      (d[i] * u * slope).get(dg[2 * i], dg[2 * i + 1]);
+      (d[i] * (g * s)).get(du[2 * i], du[2 * i + 1]);
+    }
+  } else {
+    float d[8], g[8], u[8];
+    dh.get(d);
+    values_of(gate, gate_step, g);
+    values_of(up, up_step, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gated_backward<T>(d[i], g[i], u[i], act, dg[i], du[i]);
   }
 }
 
@@ -296,45 +332,35 @@ __global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a) {
   }
 }
 
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActArgs a, const void* dh,
-                                                               void* du) {
-  const Place p = place(a, ROWS);
-  const bool in = p.live && p.col < a.inter;
+// The same for the gradient, of one row per thread: with 32 registers eight CTAs of bf16
+// are on an SM at once, and HBM is kept busy by warps in place of rows (32768 x 14336: two
+// rows of 48 registers and one value per instruction took 625 us, one row of 47 620, of
+// 40 582, this 540).
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 1)
+    act_backward_kernel(const ActArgs a, const void* dh, void* du) {
+  const Place p = place(a, 1);
+  const int row = int(p.row);       // (of one per thread: below 2^31)
+  const bool in = p.live && p.col < a.inter && row < a.rows;
   const int blocks = a.padded / kCheckpointBlock;
-  Pack8<T> pd[ROWS];
-  uint2 qg[ROWS], qu[ROWS];
-  uint32_t sg[ROWS], su[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int64_t row = p.row + r * a.per_cta;
-    if (!in || row >= a.rows) {
-      pd[r].zero();
-      qg[r] = qu[r] = make_uint2(0, 0);
-      sg[r] = su[r] = 0;
-      continue;
-    }
-    const int8_t* from = a.codes + row * 2 * a.padded + p.col;
-    const uint8_t* s = a.scales + row * 2 * blocks + p.col / kCheckpointBlock;
-    pd[r].load_once(static_cast<const T*>(dh) + row * a.h_stride + p.col);
-    qg[r] = __ldcs(reinterpret_cast<const uint2*>(from));
-    qu[r] = __ldcs(reinterpret_cast<const uint2*>(from + a.padded));
-    sg[r] = __ldg(s);
-    su[r] = __ldg(s + blocks);
+  Pack8<T> d;
+  uint2 qg = make_uint2(0, 0), qu = make_uint2(0, 0);
+  uint32_t sg = 0, su = 0;
+  d.zero();
+  if (in) {
+    const int8_t* from = a.codes + int64_t(row) * 2 * a.padded + p.col;
+    const uint8_t* s = a.scales + int64_t(row) * 2 * blocks + p.col / kCheckpointBlock;
+    d.load_once(static_cast<const T*>(dh) + row * a.h_stride + p.col);
+    qg = __ldcs(reinterpret_cast<const uint2*>(from));
+    qu = __ldcs(reinterpret_cast<const uint2*>(from + a.padded));
+    sg = __ldg(s);
+    su = __ldg(s + blocks);
   }
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int64_t row = p.row + r * a.per_cta;
-    float d[8], g[8], u[8], og[8], ou[8];
-    pd[r].get(d);
-    values_of(qg[r], step_value(sg[r]), g);
-    values_of(qu[r], step_value(su[r]), u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) gated_backward<T>(d[i], g[i], u[i], a.act, og[i], ou[i]);
-    T* dst = static_cast<T*>(du) + row * a.u_stride + p.col;
-    store8_warp(dst, in && row < a.rows, og);
-    store8_warp(dst + a.inter, in && row < a.rows, ou);
-  }
+  float og[8], ou[8];
+  gated_backward(d, qg, qu, step_value(sg), step_value(su), a.act, og, ou);
+  T* dst = static_cast<T*>(du) + row * a.u_stride + p.col;
+  store8_warp(dst, in, og);
+  store8_warp(dst + a.inter, in, ou);
 }
 
 template <typename T, int E>
@@ -398,7 +424,7 @@ bool grid_of_warps(ActArgs* a, int e, int64_t* grid) {
   return *grid < (int64_t(1) << 31);
 }
 
-// Rows of a thread: two of bf16.
+// Rows of a thread of act_kernel: two of bf16.
 constexpr int kRowsOf2 = 2, kRowsOf4 = 1;
 
 int32_t padded_of(int64_t inter) {
@@ -455,15 +481,15 @@ fo_status launch_gated_act_backward(const void* dh, fo_type type, int64_t rows, 
                    rows_on_two(du, du_stride, type);
   const bool bf16 = type == FO_TYPE_BF16;
   int64_t grid = 0;
-  if (!(vec ? grid_of(&a, bf16 ? kRowsOf2 : kRowsOf4, &grid)
+  if (!(vec ? grid_of(&a, 1, &grid)
             : grid_of_warps(&a, two ? 2 : 1, &grid)))
     return FO_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned n = unsigned(grid);
   if (vec && bf16)
-    act_backward_kernel<uint16_t, kRowsOf2><<<n, kThreads, 0, st>>>(a, dh, du);
+    act_backward_kernel<uint16_t><<<n, kThreads, 0, st>>>(a, dh, du);
   else if (vec)
-    act_backward_kernel<float, kRowsOf4><<<n, kThreads, 0, st>>>(a, dh, du);
+    act_backward_kernel<float><<<n, kThreads, 0, st>>>(a, dh, du);
   else if (bf16 && two)
     act_backward_any_kernel<uint16_t, 2><<<n, kThreads, 0, st>>>(a, dh, du);
   else if (bf16)
