@@ -188,26 +188,31 @@ struct CombineBackArgs {
   int32_t warps;            // of a token: 1, 2, 4 or 8
 };
 
-// The rows that hold no token become zeros: a warp looks at 32 of them, far apart, as
-// they come in runs.
-template <typename T, bool VEC>
+// The rows that hold no token become zeros: a warp looks at up to 32 of them, far apart,
+// as they come in runs, and at few where there are few (256 tokens of 4096 with 1024
+// empty rows: 32 each 27 us, so 7; 5 of 4271, 60 experts of which most rows are empty,
+// 70 and 26).  Rows need not lie on 16 bytes.
+template <typename T>
 __device__ __forceinline__ void zero_empty_rows(const CombineBackArgs& a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t looks = (a.f.table_rows + 31) / 32;
-  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + warp; i < looks;
-       i += int64_t(gridDim.x) * (kThreads / 32)) {
-    const int64_t row = i + lane * looks;
+  constexpr int kOf16 = 16 / int(sizeof(T));
+  const int lane = threadIdx.x & 31;
+  const int warps = int(gridDim.x) * (kThreads / 32), rows = int(a.f.table_rows);
+  const int each = min(32, (rows - 1) / warps + 1), looks = (rows - 1) / each + 1;
+  for (int i = int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5); i < looks; i += warps) {
+    const int64_t row = i + int64_t(lane) * looks;
     uint32_t todo =
-        __ballot_sync(0xffffffffu, row < a.f.table_rows && __ldg(a.row_token + row) < 0);
+        __ballot_sync(0xffffffffu, lane < each && row < rows && __ldg(a.row_token + row) < 0);
     for (; todo; todo &= todo - 1) {
-      T* at = static_cast<T*>(a.drows) + (i + (__ffs(todo) - 1) * looks) * a.drows_stride;
-      if constexpr (VEC) {
-        constexpr int kOf16 = 16 / int(sizeof(T));
-        for (int c = lane * kOf16; c < a.f.hidden; c += 32 * kOf16)
-          __stcs(reinterpret_cast<uint4*>(at + c), make_uint4(0, 0, 0, 0));
-      } else {
-        for (int c = lane; c < a.f.hidden; c += 32) at[c] = T(0);
-      }
+      T* at = static_cast<T*>(a.drows) + (i + int64_t(__ffs(todo) - 1) * looks) * a.drows_stride;
+      // up to the first 16 bytes, in wide stores, and the rest
+      const int head = min(int((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / int(sizeof(T)),
+                           a.f.hidden);
+      const int wide = (a.f.hidden - head) / kOf16, tail = (a.f.hidden - head) % kOf16;
+      if (lane < head) at[lane] = T(0);
+      at += head;
+      for (int c = lane; c < wide; c += 32)
+        __stcs(reinterpret_cast<uint4*>(at) + c, make_uint4(0, 0, 0, 0));
+      if (lane < tail) at[wide * kOf16 + lane] = T(0);
     }
   }
 }
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 3) combine_backward_kernel(const Com
     now.advance(f, step);
   }
   OwnRing::wait<0>();
-  zero_empty_rows<T, true>(a);
+  zero_empty_rows<T>(a);
 }
 
 // Any rows: E neighbouring columns per thread and 32 E, without the ring.
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_any_kernel(const Co
     }
     turn ^= 1;
   }
-  zero_empty_rows<T, false>(a);
+  zero_empty_rows<T>(a);
 }
 
 // How many CTAs of a kernel, with so much shared memory always, the device holds at
@@ -556,7 +561,8 @@ fo_status backward_as(CombineBackArgs a, int smem, int width, cudaStream_t st) {
   a.warps = token_warps(a.f.tokens, a.f.hidden, width, ctas);
   const int64_t per = (kThreads / 32) / a.warps;
   int64_t grid = (int64_t(a.f.tokens) + per - 1) / per;
-  const int64_t looks = (a.f.table_rows + kThreads - 1) / kThreads;
+  // (two rows to look at for a warp, if that many CTAs are resident)
+  const int64_t looks = (a.f.table_rows + kThreads / 16 - 1) / (kThreads / 16);
   if (grid < looks) grid = looks;
   K<<<unsigned(grid < ctas ? grid : ctas), kThreads, smem, st>>>(a);
   return FO_OK;
