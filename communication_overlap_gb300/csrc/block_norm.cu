@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormArgs a, int warp
         const int at = stage * kPieces + v * (kA + kS);
         ring.fetch(at, x_at, col[v], a.hidden);
         if (a.residual != nullptr) ring.fetch(at + kA, r_at, col[v], a.hidden);
+        if (has[v]) prefetch_gate(a, fetched, col[v]);
       }
     }
     OwnRing::commit();

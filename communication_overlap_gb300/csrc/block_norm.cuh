@@ -62,6 +62,17 @@ __device__ __forceinline__ void load_param(const void* p, int64_t i, bool f32, f
   }
 }
 
+// A token's own row of the gate on its way to the L2, with the token's other rows, as its
+// factors are waited for (16384 x 4096 in bf16 with a gate per token 167 -> 141 us, and
+// back 266 -> 239).
+__device__ __forceinline__ void prefetch_gate(const NormArgs& a, int64_t t, int col) {
+  if (a.gate_rows != 1 || a.gate_stride == 0) return;
+  const int64_t i = t * a.gate_stride + col;
+  const void* p = a.params_f32 ? static_cast<const void*>(static_cast<const float*>(a.gate) + i)
+                               : static_cast<const uint16_t*>(a.gate) + i;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Sums over the warps of a CTA of N values per thread, the same on every thread:
 // by shuffles, then through shared memory in warp order.  Every thread of the CTA
 // calls it; buf: [2][N][32], the halves taken in turn, so that one barrier per sum

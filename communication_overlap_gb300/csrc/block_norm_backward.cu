@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
       for (int v = 0; v < NV; ++v) {
         const int at = stage * kPieces + v * kOf;
         ring.fetch(at, x_at, col[v], f.hidden);
+        if (GATES && has[v]) prefetch_gate(f, fetched, col[v]);
         if (f.pre != nullptr) ring.fetch(at + kA, dy_at, col[v], f.hidden);
         if (f.residual != nullptr) ring.fetch(at + 2 * kA, r_at, col[v], f.hidden);
         if (a.dsum != nullptr) ring.fetch(at + 2 * kA + kS, d_at, col[v], f.hidden);
