@@ -31,6 +31,7 @@ struct CombineArgs {
   int32_t per_item;
   int32_t chunks;          // threads along a token's columns
   int32_t items;
+  int32_t side_by_side;    // two neighbouring lanes' eights lie next to each other in y
 };
 
 // The row of a pair, -1 for none; a row outside the table is recorded.
@@ -116,8 +117,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1)
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
       const int64_t t = token(item, i);
-      store8_warp(static_cast<O*>(a.y) + t * a.y_stride + col,
-                  in && local < per && t < a.tokens, acc[i]);
+      const bool live = in && local < per && t < a.tokens;
+      O* to = static_cast<O*>(a.y) + t * a.y_stride + col;
+      if (sizeof(O) == 2 || a.side_by_side)
+        store8_warp(to, live, acc[i]);
+      else if (live)
+        store8(to, acc[i]);
     }
   }
 }
@@ -506,6 +511,9 @@ fo_status forward_as(CombineArgs a, cudaStream_t st) {
   const int64_t items = (int64_t(a.tokens) + a.per_item - 1) / a.per_item * a.pieces;
   if (items >= (int64_t(1) << 30)) return FO_ERR_UNSUPPORTED;
   a.items = int32_t(items);
+  // (of an odd number of eights every other token's last has the next one's first beside it,
+  // which follows in memory only where the rows are not padded)
+  a.side_by_side = a.pieces > 1 || a.chunks % 2 == 0 || a.y_stride == a.hidden;
   constexpr auto kernel = combine_kernel<T, O, SLOTS, TOKENS>;
   int ctas = 0;
   const fo_status q = resident<kernel>(0, &ctas);

@@ -114,9 +114,11 @@ __device__ __forceinline__ void pairs_of(const float (&v)[8], Pair (&x)[4]) {
   for (int i = 0; i < 4; ++i) x[i] = Pair::of(v[2 * i], v[2 * i + 1]);
 }
 
-// store8 by a whole warp whose lanes have neighbouring eights; `in`: this lane's are to
-// be stored.  Of fp32 two lanes trade halves, so that a store of theirs is 32 bytes in
-// one piece: half a sector each costs twice the traffic to L2.
+// store8 by a whole warp; `in`: this lane's eights are to be stored.  Of fp32 two lanes
+// trade halves, so that a store of theirs is 32 bytes in one piece: half a sector each
+// costs twice the traffic to L2.  So the odd lane's eights lie right behind the even
+// one's wherever either is to store: where lanes run over rows, an even number of eights
+// to a row, or rows that follow each other without a gap.
 template <typename T>
 __device__ __forceinline__ void store8_warp(T* p, bool in, const float (&v)[8]) {
   if constexpr (sizeof(T) == 2) {

@@ -540,3 +540,32 @@ def test_combine_a_row_named_twice(H, slots):
     assert np.array_equal(drows.cpu().numpy()[token_row[0, 3]], want[token_row[0, 3]])
     assert dw.cpu().numpy()[1, slots[0]] == 0
     assert moe.device_status(clear=True) == fo.FO_ERR_ARG
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("H", [8, 40, 64, 72, 136, 1000, 2040, 2056])
+@pytest.mark.parametrize("T, k", [(1, 1), (9, 1), (9, 2), (14, 3)])
+def test_combine_padded_rows(T, k, H, types):
+    """Every row of 8 columns and padding on 16 bytes, an odd number of eights to a row or an
+    even one: all of y, and nothing beside or behind it."""
+    rng = np.random.default_rng(H + T)
+    t, o = types
+    n = 3 * T * k
+    index, token_row, row_token = routing(rng, T, n, k)
+    rows, w, dy = normal(rng, (n, H), t), normal(rng, (T, k), F32), normal(rng, (T, H), o)
+    r64, w64 = host(rows), host(w)
+    want = oracle.combine(r64, index, w64)
+    bound = k * E * oracle.combine(np.abs(r64), index, np.abs(w64))
+    drows, dw = block.combine_backward(dy, rows, token_row, row_token, w)
+    for pad in (4, 8, 24, 3, 2):
+        buf = torch.full(((T + 1) * (H + pad),), 7.0, dtype=o, device="cuda")
+        out = buf[:T * (H + pad)].view(T, H + pad)
+        block.combine(strided(rows, pad), token_row, w, out=out[:, :H])
+        near(out[:, :H], want, bound, o)
+        assert (out[:, H:] == 7).all() and (buf[T * (H + pad):] == 7).all()
+        drows2, dw2 = block.combine_backward(strided(dy, pad), strided(rows, pad), token_row,
+                                             row_token, w)
+        assert torch.equal(drows2, drows)
+        mag = np.abs(host(dy)).max() * np.abs(r64).max() * H
+        near(dw2, host(dw), 2 * (H / 32 + 16) * E * mag, F32)
+    assert moe.device_status() == fo.FO_OK
