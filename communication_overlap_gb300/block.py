@@ -25,8 +25,8 @@ from typing import Optional
 import torch
 
 from . import fo
-from .moe import (_ACTS, _int32, _on_gpu, _row_stride, _run, _status_word, _stream, _type,
-                  _untracked)
+from .moe import (_ACTS, _int32, _number, _on_gpu, _row_stride, _run, _status_word, _stream,
+                  _type, _untracked)
 
 _checkpoint_sizes = functools.lru_cache(256)(fo.fo_checkpoint_sizes)
 
@@ -129,6 +129,7 @@ def norm(x, residual=None, post_gain=None, gate=None, scale=1.0, pre_gain=None, 
     tokens / rows tokens); all of one type.  Where nothing but pre_gain is
     given, the stream is x itself."""
     _untracked(x, residual, post_gain, gate, pre_gain)
+    scale, eps = _number(scale), _number(eps)
     dev, T, H, (desc, _), gate_stride = _norm_args(x, residual, post_gain, gate, pre_gain, scale,
                                                    eps)
     stream, y, rstd, at = x, None, None, 0
@@ -155,7 +156,7 @@ def norm_backward(x, residual, normed, dstream=None, dy=None, post_gain=None, ga
     parameters: the forward call's; normed: what it returned."""
     _untracked(x, residual, post_gain, gate, pre_gain, dstream, dy)
     dev, T, H, (desc, nbytes), gate_stride = _norm_args(x, residual, post_gain, gate, pre_gain,
-                                                        scale, 0.0)
+                                                        _number(scale), 0.0)
     rstd = normed.rstd
     _on_gpu(x, dstream, dy, rstd)
     if (dy is None) != (pre_gain is None):

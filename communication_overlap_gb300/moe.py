@@ -21,6 +21,7 @@ A generation step makes small calls, so the time here counts: the device is
 switched only where another is current, sizes are computed once per shape.
 """
 import functools
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -59,6 +60,16 @@ def _untracked(*tensors):
         if t is not None and t.requires_grad:
             raise ValueError("no gradient flows through this call: detach its tensors, or call it "
                              "under torch.no_grad() (route_backward is the router's gradient)")
+
+
+def _number(x):
+    """x as a float: what is kept per argument is kept by its value, not by a tensor's
+    identity.  A tensor that requires a gradient is refused."""
+    if type(x) is float:
+        return x
+    if isinstance(x, torch.Tensor):
+        _untracked(x)
+    return float(x)
 
 
 def _int32(t, n, what):
@@ -284,9 +295,12 @@ def route(logits, top_k, renormalize=True, capacity=0, scoring="softmax", bias=N
         raise ValueError("logits: [tokens, experts] expected")
     dev, type_ = _on_gpu(logits, bias), _type(logits.dtype)
     T, E = logits.shape
+    index = operator.index      # (as _number: integers, not tensors that may change)
+    top_k, capacity, groups = index(top_k), index(capacity), index(groups)
+    top_groups, group_top, scale = index(top_groups), index(group_top), _number(scale)
     M, nbytes = _route_sizes(T, E, top_k, capacity)
     desc = _route_desc(E, top_k, bool(renormalize), capacity, scoring, groups, top_groups,
-                       group_top, float(scale))
+                       group_top, scale)
     if bias is not None:
         if bias.dtype != torch.float32 or not bias.is_contiguous() or tuple(bias.shape) != (E,):
             raise ValueError(f"bias: contiguous fp32[{E}] expected")
@@ -331,7 +345,7 @@ def route_backward(logits, ids, weights, dweights, renormalize=True, scoring="so
     for t, what in ((weights, "weights"), (dweights, "dweights")):
         if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != T * k:
             raise ValueError(f"{what}: contiguous fp32[{T}, {k}] expected")
-    desc = _route_desc(E, k, bool(renormalize), 0, scoring, 1, 1, 1, float(scale))
+    desc = _route_desc(E, k, bool(renormalize), 0, scoring, 1, 1, 1, _number(scale))
     out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     if desc is None:
         _run(dev, fo.fo_moe_route_backward, logits.data_ptr(), type_, T, E,

@@ -569,3 +569,25 @@ def test_combine_padded_rows(T, k, H, types):
         mag = np.abs(host(dy)).max() * np.abs(r64).max() * H
         near(dw2, host(dw), 2 * (H / 32 + 16) * E * mag, F32)
     assert moe.device_status() == fo.FO_OK
+
+
+def test_norm_scale_of_a_tensor():
+    """A scale or an eps that is a tensor counts by what it holds at the call, and one
+    that requires a gradient is refused."""
+    x, g = torch.ones((3, 8), device="cuda"), torch.ones(8, device="cuda")
+    for device in ("cpu", "cuda"):
+        scale, eps = torch.tensor(0.5, device=device), torch.tensor(0.0, device=device)
+        for s, e in ((0.5, 0.0), (2.0, 3.0), (0.25, 15.0)):
+            scale.fill_(s)
+            eps.fill_(e)
+            n = block.norm(x, scale=scale, pre_gain=g, eps=eps)
+            assert (n.stream == s).all() and torch.equal(n.y, block.norm(x, scale=s, pre_gain=g, eps=e).y)
+            assert (block.norm_backward(x, None, n, x, x - x, scale=scale, pre_gain=g).x == s).all()
+    for how in (dict(scale=torch.tensor(1.0, requires_grad=True)),
+                dict(eps=torch.tensor(1.0, requires_grad=True))):
+        with pytest.raises(ValueError):
+            block.norm(x, pre_gain=g, **how)
+    with pytest.raises(ValueError):
+        block.norm_backward(x, None, n, x, x, pre_gain=g, scale=torch.tensor(1.0, requires_grad=True))
+    with torch.no_grad():
+        assert (block.norm(x, scale=torch.tensor(2.0, requires_grad=True)).stream == 2).all()

@@ -328,3 +328,28 @@ def test_more_tokens_than_16_bits_count():
         assert torch.equal(r.token_row[tokens, 0].long(), rows)
         assert torch.equal(r.row_token[rows].long(), tokens)
     assert int((r.row_token >= 0).sum()) == T
+
+
+def test_numbers_that_are_tensors():
+    """They count by what they hold at the call; a scale that requires a gradient is refused."""
+    rng = np.random.default_rng(12)
+    l, bias = normal(rng, (40, 16)), normal(rng, (16,), F32, 0.05)
+    one = lambda v: torch.tensor(v)
+    k, groups, top, two, cap, scale = one(1), one(1), one(1), one(1), one(0), one(1.0)
+    for v in ((2, 4, 3, 2, 0, 2.0), (3, 2, 1, 1, 8, 0.5), (5, 8, 4, 2, 128, 1.0)):
+        for t, x in zip((k, groups, top, two, cap, scale), v):
+            t.fill_(x)
+        got = moe.route(l, k, True, cap, "sigmoid", bias, groups, top, two, scale)
+        want = check(l, v[0], True, "sigmoid", bias, v[1], v[2], v[3], v[5], v[4])
+        assert all(torch.equal(p, q) for p, q in zip(vars(got).values(), vars(want).values()))
+        assert torch.equal(
+            moe.route_backward(l, got.ids, got.weights, got.weights, False, "sigmoid", scale),
+            moe.route_backward(l, got.ids, got.weights, got.weights, False, "sigmoid", v[5]))
+    plain = [moe.route(l, k.fill_(n)) for n in (2, 6)]
+    assert [r.ids.shape[1] for r in plain] == [2, 6]
+    order = l.sort(dim=1, descending=True, stable=True).indices.int()
+    assert all(torch.equal(r.ids, order[:, :r.ids.shape[1]]) for r in plain)
+    for call in (lambda s: moe.route(l, 2, scoring="sigmoid", scale=s),
+                 lambda s: moe.route_backward(l, got.ids, got.weights, got.weights, scale=s)):
+        with pytest.raises(ValueError):
+            call(torch.tensor(1.0, requires_grad=True))
