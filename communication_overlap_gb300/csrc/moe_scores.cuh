@@ -406,6 +406,14 @@ __device__ __forceinline__ GroupCut cut_groups(const ScoreArgs& a, const Choice<
   const bool two = a.group_top == 2 && k2 != 0u;
   r.score = two ? order_key(order_value(k1) + order_value(k2)) : k1;
   r.second = two ? k2 : k1;
+  // a sum of two choices of unlike signs is smaller than they are, and off by what they
+  // are off: by how much, the most of any group (one far from the cut may be off as far)
+  float apart = 0.0f;
+  if (a.bias != nullptr && a.group_top == 2) {
+    const float v1 = order_value(k1), v2 = order_value(k2);
+    if (two && v1 > 0.0f && v2 < 0.0f) apart = 2.0f * fminf(v1, -v2);
+    apart = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(apart)));
+  }
   int rank = 0;
 #pragma unroll 8
   for (int h = 0; h < a.groups; ++h) {
@@ -420,7 +428,8 @@ __device__ __forceinline__ GroupCut cut_groups(const ScoreArgs& a, const Choice<
   const bool logits = by_logit && a.group_top == 1;
   const float vi = order_value(r.in);
   r.margin = logits ? 0.0f
-                    : 2.0f * choice_margin(score_margin(a.sigmoid, c.inv, V), vi, float(4 * V)) +
+                    : 2.0f * choice_margin(score_margin(a.sigmoid, c.inv, V), fabsf(vi) + apart,
+                                               float(4 * V)) +
                           cut_logit_margin(a, c, vi);
   r.near = out != 0u && (r.in == out ? !(logits && a.bf16) : vi - order_value(out) < r.margin);
   return r;

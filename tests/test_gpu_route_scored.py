@@ -139,6 +139,32 @@ def test_pairs_that_fp32_cannot_tell(top_groups):
           torch.from_numpy(bias).to(F32).cuda(), groups, top_groups, 2)
 
 
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [1000.0, 30000.0])
+@pytest.mark.parametrize("n, groups", [(256, 8), (64, 4), (60, 6), (1024, 32)])
+def test_groups_of_choices_of_unlike_signs(n, groups, size, scoring):
+    """Two groups of pairs that cancel but for their scores, which differ by a few of the
+    steps of fp32 that the pair's own size has."""
+    rng = np.random.default_rng(n)
+    T, per, step = 300, n // groups, float(np.spacing(np.float32(size)))
+    bias = np.full(n, -size)
+    bias[::per] = size
+    l = np.float32(rng.standard_normal((T, n)) - 6.0)
+    for t in range(T):
+        g, h = rng.choice(groups, 2, replace=False) * per
+        if scoring == "sigmoid":
+            p = rng.uniform(0.3, 0.7, 3)
+            q = np.clip(p[0] + p[1] - p[2] + step * rng.uniform(-4, 4), 0.05, 0.95)
+            x, i = np.log((*p, q)) - np.log1p(-np.array((*p, q))), (g, g + 1, h, h + 1)
+        else:
+            x = rng.uniform(0.0, 1.0, 3)
+            q = max(np.exp(x[0]) + np.exp(x[1]) - np.exp(x[2]) + step * rng.uniform(-8, 8), 0.1)
+            x, i = (*x, np.log(q)), (g, g + 1, h, h + 1)
+        l[t, list(i)] = np.float32(x)
+    check(torch.from_numpy(l).cuda(), min(4, per), True, scoring,
+          torch.from_numpy(np.float32(bias)).cuda(), groups, 1, 2)
+
+
 @pytest.mark.parametrize("offset", [100.0, -1000.0])
 @pytest.mark.parametrize("n, groups", [(256, 8), (64, 4)])
 def test_groups_of_logits_far_from_zero(n, groups, offset):
