@@ -224,8 +224,9 @@ fo_status fo_block_norm_backward(const fo_norm_desc* d, const void* x, int64_t x
   fo_status st;
   if (!device_ok(&st)) return st;
   fo::NormBackArgs a{};
-  a.f = norm_args(*d, x, x_stride, residual, residual_stride, post_gain, gate, gate_stride,
-                  pre_gain, post_rstd, pre_rstd);
+  // (without the second norm no gradient takes a value of the stream)
+  a.f = norm_args(*d, x, x_stride, pre_gain ? residual : nullptr, residual_stride, post_gain, gate,
+                  gate_stride, pre_gain, post_rstd, pre_rstd);
   a.dsum = dsum, a.dsum_stride = dsum ? dsum_stride : 0;
   a.dy = pre_gain ? dy : nullptr, a.dy_stride = pre_gain ? dy_stride : 0;
   a.dx = dx, a.dx_stride = dx_stride;

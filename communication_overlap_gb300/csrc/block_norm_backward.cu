@@ -10,7 +10,9 @@
 // from one round of sums over the row: with w = q post xn,
 //   a = sum dy pre sn,  b = sum w (dsum + r2 dy pre),  c = sum w sn,
 //   mean(q D post xn) = (b - r2 (a / H) c) / H.
-// s is formed again from x and the residual, unrounded, instead of being read.
+// s is formed again from x and the residual, unrounded, instead of being read.  Without
+// pre D = dsum, and no value of s enters: an infinity or a NaN of it must not by way of
+// r2 = 0 either, so kernels that hold a row have that form by itself (PRE).
 //
 // A worker takes a contiguous range of tokens and keeps the parameters' sums of
 // its columns in registers; a last kernel adds the workers' in their order, so
@@ -87,7 +89,8 @@ struct Columns {
     py.get(dy);
     pd.get(d);
 #pragma unroll
-    for (int i = 0; i < W; ++i) sn[i] = fmaf(q[i], u[i], sn[i]) * r2;
+    for (int i = 0; i < W; ++i)
+      sn[i] = f.pre != nullptr ? fmaf(q[i], u[i], sn[i]) * r2 : 0.0f;
     if (f.pre != nullptr) {
       load_param<W>(f.pre, col, f.params_f32, p);
 #pragma unroll
@@ -180,9 +183,9 @@ __device__ __forceinline__ void store_parts(const NormBackArgs& a, const BackSha
 // scale gate post and pre lie behind it, and one instruction takes two values.  Of the
 // parameters' sums two are kept: of dy sn, and G of xn D over tokens with the same
 // gate, since dgate = scale post G and dpost = scale gate G (summed over the gates,
-// where a worker meets several: GATES).  16384 x 4096: eight columns per thread and one
-// value per instruction took 174 us.
-template <typename A, typename S, int NV, int DEPTH, bool GATES>
+// where a worker meets several: GATES).  PRE: there is a norm before the next block.
+// 16384 x 4096: eight columns per thread and one value per instruction took 174 us.
+template <typename A, typename S, int NV, int DEPTH, bool GATES, bool PRE>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArgs a,
                                                                const BackShape n, int warps) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -199,6 +202,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
   const NormArgs& f = a.f;
   const RowGroup g = RowGroup::of(warps);
   const OwnRing ring(smem);
+  // (asked at run time as well: 8192 columns 201 us, where PRE alone decides 214)
+  const auto normed = [&] { return PRE && f.pre != nullptr; };
   int col[NV];
   bool has[NV];
 #pragma unroll
@@ -224,8 +229,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
         const int at = stage * kPieces + v * kOf;
         ring.fetch(at, x_at, col[v], f.hidden);
         if (GATES && has[v]) prefetch_gate(f, fetched, col[v]);
-        if (f.pre != nullptr) ring.fetch(at + kA, dy_at, col[v], f.hidden);
-        if (f.residual != nullptr) ring.fetch(at + 2 * kA, r_at, col[v], f.hidden);
+        if (normed()) ring.fetch(at + kA, dy_at, col[v], f.hidden);
+        if (PRE && f.residual != nullptr) ring.fetch(at + 2 * kA, r_at, col[v], f.hidden);
         if (a.dsum != nullptr) ring.fetch(at + 2 * kA + kS, d_at, col[v], f.hidden);
       }
     }
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = 0.0f;
     set_w(v, p);
-    if (has[v] && f.pre != nullptr) load_param<8>(f.pre, col[v], f.params_f32, p);
+    if (has[v] && normed()) load_param<8>(f.pre, col[v], f.params_f32, p);
     if constexpr (kKeep)
       pairs_of(p, kept_pre);
     else
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
   int gate_row = 0, gate_end = t0;
   int stage = 0;
   float r1 = f.post && t0 < t1 ? f.post_rstd[t0] : 1.0f;
-  float r2 = f.pre && t0 < t1 ? f.pre_rstd[t0] : 0.0f;
+  float r2 = normed() && t0 < t1 ? f.pre_rstd[t0] : 0.0f;
   for (int t = t0; t < t1; ++t) {
     if (t >= gate_end) {
       gate_row = f.gate ? int(uint32_t(t) / uint32_t(f.gate_rows)) : 0;
@@ -300,47 +305,63 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
     for (int v = 0; v < NV; ++v) {
       const int at = stage * kPieces + v * kOf;
       ring.get(at, px[v]);
-      ring.get(at + kA, py[v]);
-      get_pairs<S>(ring, at + 2 * kA, sn[v]);
+      if constexpr (PRE) {
+        ring.get(at + kA, py[v]);
+        get_pairs<S>(ring, at + 2 * kA, sn[v]);
+      }
       get_pairs<S>(ring, at + 2 * kA + kS, d[v]);
     }
     fetch(stage);
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
     const int next = t + 1 < t1 ? t + 1 : t;
     const float next_r1 = f.post ? f.post_rstd[next] : 1.0f;
-    const float next_r2 = f.pre ? f.pre_rstd[next] : 0.0f;
+    const float next_r2 = normed() ? f.pre_rstd[next] : 0.0f;
     Pair sa = zero, sb = zero, sc = zero;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       Pair w[4], pre[4], x[4], dy[4];
       pairs_of(px[v], x);
-      pairs_of(py[v], dy);
+      if constexpr (PRE) pairs_of(py[v], dy);
       get_params(v, w, pre);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Pair z = w[i] * (x[i] * Pair::of(r1)), e = dy[i] * pre[i];
-        sn[v][i] = (sn[v][i] + z) * Pair::of(r2);
-        d[v][i] = fma2(Pair::of(r2), e, d[v][i]);
-        sa = fma2(e, sn[v][i], sa);
-        sb = fma2(z, d[v][i], sb);
-        sc = fma2(z, sn[v][i], sc);
+        const Pair z = w[i] * (x[i] * Pair::of(r1));
+        if constexpr (!PRE) {
+          sb = fma2(z, d[v][i], sb);
+        } else {
+          const Pair e = dy[i] * pre[i];
+          sn[v][i] = (sn[v][i] + z) * Pair::of(r2);
+          d[v][i] = fma2(Pair::of(r2), e, d[v][i]);
+          sa = fma2(e, sn[v][i], sa);
+          sb = fma2(z, d[v][i], sb);
+          sc = fma2(z, sn[v][i], sc);
+        }
       }
     }
-    float sum[3] = {sa.sum(), sb.sum(), sc.sum()};
-    g.sums<3>(sum, buf, turn);
-    const float k = r2 * (sum[0] * inv);
-    const float m1 = (sum[1] - k * sum[2]) * inv;
+    float k = 0.0f, m1;
+    if constexpr (PRE) {
+      float sum[3] = {sa.sum(), sb.sum(), sc.sum()};
+      g.sums<3>(sum, buf, turn);
+      k = r2 * (sum[0] * inv);
+      m1 = (sum[1] - k * sum[2]) * inv;
+    } else {
+      float sum[1] = {sb.sum()};
+      g.sums<1>(sum, buf, turn);
+      m1 = sum[0] * inv;
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       Pair w[4], pre[4], o[4], x[4], dy[4];
       pairs_of(px[v], x);
-      pairs_of(py[v], dy);
+      if constexpr (PRE) pairs_of(py[v], dy);
       get_params(v, w, pre);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Pair xn = x[i] * Pair::of(r1);
-        d[v][i] = fma2(Pair::of(-k), sn[v][i], d[v][i]);
-        dpre[v][i] = fma2(dy[i], sn[v][i], dpre[v][i]);
+        if constexpr (PRE) {
+          d[v][i] = fma2(Pair::of(-k), sn[v][i], d[v][i]);
+          dpre[v][i] = fma2(dy[i], sn[v][i], dpre[v][i]);
+        }
         sum_g[v][i] = fma2(xn, d[v][i], sum_g[v][i]);
         o[i] = w[i] * d[v][i];
         if (f.post != nullptr) o[i] = Pair::of(r1) * fma2(Pair::of(-m1), xn, o[i]);
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     if (!has[v]) continue;
-    if (f.pre != nullptr) store_pairs(n.pre_part + worker * f.hidden + col[v], dpre[v]);
+    if (normed()) store_pairs(n.pre_part + worker * f.hidden + col[v], dpre[v]);
     if (GATES && f.post != nullptr)
       store_pairs(n.post_part + worker * f.hidden + col[v], dpost[GATES ? v : 0]);
   }
@@ -393,7 +414,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormBackArg
 // them: eight columns per thread, E neighbouring ones of each 32 E of the row's
 // threads; the next row is loaded while one is worked on.  (In two kernels, a column
 // per thread: 838 us for 16384 x 4095 of bf16.)
-template <typename A, typename S, int E>
+template <typename A, typename S, int E, bool PRE>
 __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBackArgs a,
                                                                    const BackShape n, int warps) {
   constexpr int U = 8 / E;
@@ -420,8 +441,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBac
       const bool has = t < t1 && first + i * stride < f.hidden;
       px[i].zero(), py[i].zero(), pr[i].zero(), pd[i].zero();
       if (has) px[i].load(x + i * stride);
-      if (has && f.pre != nullptr) py[i].load(y + i * stride);
-      if (has && f.residual != nullptr) pr[i].load(r + i * stride);
+      if (PRE && has) py[i].load(y + i * stride);
+      if (PRE && has && f.residual != nullptr) pr[i].load(r + i * stride);
       if (has && a.dsum != nullptr) pd[i].load(d + i * stride);
     }
   };
@@ -431,7 +452,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBac
   for (int i = 0; i < U; ++i) {
 #pragma unroll
     for (int e = 0; e < E; ++e) w[i][e] = pre[i][e] = dpre[i][e] = dpost[i][e] = sum_g[i][e] = 0.0f;
-    if (f.pre != nullptr && first + i * stride < f.hidden)
+    if (PRE && first + i * stride < f.hidden)
       load_few_param<E>(f.pre, first + i * stride, f.params_f32, pre[i]);
   }
   int gate_row = 0, gate_end = t0;
@@ -453,24 +474,34 @@ __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBac
       pd[i].get(d[i]);
     }
     load(t + 1);
-    const float r1 = f.post ? f.post_rstd[t] : 1.0f, r2 = f.pre ? f.pre_rstd[t] : 0.0f;
+    const float r1 = f.post ? f.post_rstd[t] : 1.0f, r2 = PRE ? f.pre_rstd[t] : 0.0f;
     float sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < U; ++i) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         xn[i][e] *= r1;
-        const float z = w[i][e] * xn[i][e], q = dy[i][e] * pre[i][e];
-        sn[i][e] = (sn[i][e] + z) * r2;
-        d[i][e] = fmaf(r2, q, d[i][e]);
-        sum[0] = fmaf(q, sn[i][e], sum[0]);
+        const float z = w[i][e] * xn[i][e];
+        if constexpr (PRE) {
+          const float q = dy[i][e] * pre[i][e];
+          sn[i][e] = (sn[i][e] + z) * r2;
+          d[i][e] = fmaf(r2, q, d[i][e]);
+          sum[0] = fmaf(q, sn[i][e], sum[0]);
+          sum[2] = fmaf(z, sn[i][e], sum[2]);
+        }
         sum[1] = fmaf(z, d[i][e], sum[1]);
-        sum[2] = fmaf(z, sn[i][e], sum[2]);
       }
     }
-    g.sums<3>(sum, buf, turn);
-    const float k = r2 * (sum[0] * inv);
-    const float m1 = (sum[1] - k * sum[2]) * inv;
+    float k = 0.0f, m1;
+    if constexpr (PRE) {
+      g.sums<3>(sum, buf, turn);
+      k = r2 * (sum[0] * inv);
+      m1 = (sum[1] - k * sum[2]) * inv;
+    } else {
+      float only[1] = {sum[1]};
+      g.sums<1>(only, buf, turn);
+      m1 = only[0] * inv;
+    }
     S* dres = static_cast<S*>(a.dresidual) + (t * a.dresidual_stride + first);
     A* dx = static_cast<A*>(a.dx) + (t * a.dx_stride + first);
 #pragma unroll
@@ -478,8 +509,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBac
       float o[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        d[i][e] = fmaf(-k, sn[i][e], d[i][e]);
-        dpre[i][e] = fmaf(dy[i][e], sn[i][e], dpre[i][e]);
+        if constexpr (PRE) {
+          d[i][e] = fmaf(-k, sn[i][e], d[i][e]);
+          dpre[i][e] = fmaf(dy[i][e], sn[i][e], dpre[i][e]);
+        }
         sum_g[i][e] = fmaf(xn[i][e], d[i][e], sum_g[i][e]);
         o[e] = w[i][e] * d[i][e];
         if (f.post != nullptr) o[e] = r1 * fmaf(-m1, xn[i][e], o[e]);
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_few_kernel(const NormBac
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int64_t at = worker * f.hidden + first + i * stride + e;
-      if (f.pre != nullptr) n.pre_part[at] = dpre[i][e];
+      if (PRE) n.pre_part[at] = dpre[i][e];
       if (f.post != nullptr) n.post_part[at] = dpost[i][e];
     }
   }
@@ -642,15 +675,34 @@ int64_t column_workers(int64_t hidden, int width, int sms) {
   return (int64_t(sms) * 4 + pieces - 1) / pieces;
 }
 
-template <typename A, typename S, int NV, int DEPTH, bool GATES>
-fo_status launch_ring(const NormBackArgs& a, const BackShape& n, const RowShape& s, int row_bytes,
+template <typename A, typename S, int NV, int DEPTH, bool GATES, bool PRE>
+fo_status launch_kernel(const NormBackArgs& a, const BackShape& n, const RowShape& s, int row_bytes,
                       cudaStream_t st) {
-  constexpr auto kernel = norm_backward_kernel<A, S, NV, DEPTH, GATES>;
+  constexpr auto kernel = norm_backward_kernel<A, S, NV, DEPTH, GATES, PRE>;
   const fo_status q = allow_smem<kernel>();
   if (q != FO_OK) return q;
   const int smem = DEPTH * row_bytes + (NV == 1 ? 0 : s.threads * NV * 64);
   kernel<<<unsigned((n.workers + s.rows - 1) / s.rows), s.threads, smem, st>>>(a, n, s.warps);
   return FO_OK;
+}
+template <typename A, typename S, int NV, int DEPTH>
+fo_status launch_ring(const NormBackArgs& a, const BackShape& n, const RowShape& s, int row_bytes,
+                      cudaStream_t st) {
+  const bool gates = a.f.gate != nullptr && a.f.gate_rows < a.f.tokens;
+  if (a.f.pre != nullptr)
+    return gates ? launch_kernel<A, S, NV, DEPTH, true, true>(a, n, s, row_bytes, st)
+                 : launch_kernel<A, S, NV, DEPTH, false, true>(a, n, s, row_bytes, st);
+  return gates ? launch_kernel<A, S, NV, DEPTH, true, false>(a, n, s, row_bytes, st)
+               : launch_kernel<A, S, NV, DEPTH, false, false>(a, n, s, row_bytes, st);
+}
+
+template <typename A, typename S, int E>
+void launch_few(const NormBackArgs& a, const BackShape& n, const RowShape& s, cudaStream_t st) {
+  const unsigned grid = unsigned((n.workers + s.rows - 1) / s.rows);
+  if (a.f.pre != nullptr)
+    norm_backward_few_kernel<A, S, E, true><<<grid, s.threads, 0, st>>>(a, n, s.warps);
+  else
+    norm_backward_few_kernel<A, S, E, false><<<grid, s.threads, 0, st>>>(a, n, s.warps);
 }
 
 template <typename A, typename S>
@@ -674,26 +726,18 @@ fo_status launch(const NormBackArgs& a, BackShape* n, float* workspace, bool vec
   n->post_part = n->pre_part + n->workers * H;
   n->gate_part = n->post_part + n->workers * H;
   if (whole) {
-    const bool gates = f.gate != nullptr && f.gate_rows < f.tokens;
     // four rows under way where they fit, as those of bf16 do
-    if (s.nv == 1) {
-      if constexpr (sizeof(A) == 4) {
-        if (4 * row > kBlockSmem)
-          return gates ? launch_ring<A, S, 1, 2, true>(a, *n, s, row, st)
-                       : launch_ring<A, S, 1, 2, false>(a, *n, s, row, st);
-      }
-      return gates ? launch_ring<A, S, 1, 4, true>(a, *n, s, row, st)
-                   : launch_ring<A, S, 1, 4, false>(a, *n, s, row, st);
+    if (s.nv == 2) return launch_ring<A, S, 2, 2>(a, *n, s, row, st);
+    if constexpr (sizeof(A) == 4) {
+      if (4 * row > kBlockSmem) return launch_ring<A, S, 1, 2>(a, *n, s, row, st);
     }
-    return gates ? launch_ring<A, S, 2, 2, true>(a, *n, s, row, st)
-                 : launch_ring<A, S, 2, 2, false>(a, *n, s, row, st);
+    return launch_ring<A, S, 1, 4>(a, *n, s, row, st);
   }
   if (few) {
-    const unsigned grid = unsigned((n->workers + s.rows - 1) / s.rows);
     if (two)
-      norm_backward_few_kernel<A, S, 2><<<grid, s.threads, 0, st>>>(a, *n, s.warps);
+      launch_few<A, S, 2>(a, *n, s, st);
     else
-      norm_backward_few_kernel<A, S, 1><<<grid, s.threads, 0, st>>>(a, *n, s.warps);
+      launch_few<A, S, 1>(a, *n, s, st);
     return FO_OK;
   }
   if (vec) {

@@ -887,6 +887,7 @@ fo_status fo_block_norm(const fo_norm_desc* desc, const void* x, int64_t x_strid
  * where pre_gain is): dx (type), dresidual (stream_type; NULL: not written),
  * and for each parameter that is given its own in param_type, dpost and dpre
  * [hidden], dgate [gates][hidden], summed over the tokens that share it.
+ * Without pre_gain no value of the stream enters, and residual is not read.
  *  post_rstd, pre_rstd: as the forward call wrote them.
  *  workspace: device, 16-byte aligned, fo_block_norm_workspace bytes, of any
  *      content; calls that overlap in time need one each. */

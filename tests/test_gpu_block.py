@@ -591,3 +591,41 @@ def test_norm_scale_of_a_tensor():
         block.norm_backward(x, None, n, x, x, pre_gain=g, scale=torch.tensor(1.0, requires_grad=True))
     with torch.no_grad():
         assert (block.norm(x, scale=torch.tensor(2.0, requires_grad=True)).stream == 2).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("H, pad", [(264, 0), (264, 3), (264, 2), (4104, 0), (8200, 0), (9001, 0)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_gradient_does_not_see_the_stream(H, pad, types, residual):
+    """Without a norm before the next block the gradients take no value of the stream: an
+    infinity or a NaN there stays out of all of them, one of x where nothing norms it comes
+    into the gate's gradient of its own column alone."""
+    rng = np.random.default_rng(H + pad)
+    wide = (lambda t: strided(t, pad)) if pad else (lambda t: t)
+    bad = [(1, 3, float("inf")), (2, 5, float("nan")), (4, H - 1, float("-inf"))]
+    for post in ((True, False) if residual else (False,)):
+        x, res, p, gate, scale, _, eps, ds, _ = norm_case(rng, 6, H, *types, post, 3, False, residual)
+        n = block.norm(x, res, p, gate, scale, eps=eps)
+        want = block.norm_backward(x, res, n, ds, None, p, gate, scale)
+        touched = res if residual else x
+        for t, c, v in bad:
+            touched[t, c] = v
+        got = block.norm_backward(wide(x), None if res is None else wide(res), n, wide(ds), None, p,
+                                  gate, scale)
+        for name in ("x", "residual", "post_gain"):
+            a, b = getattr(got, name), getattr(want, name)
+            assert (a is None and b is None) or torch.isfinite(a).all(), name
+        # (dx and the residual's gradient go by the same steps; sums may have another order)
+        if not pad:
+            assert torch.equal(got.x, want.x)
+            assert not residual or torch.equal(got.residual, want.residual)
+        alone = torch.isfinite(got.gate)
+        assert alone.all() if residual else int((~alone).sum()) == len(bad)
+        if not pad:
+            assert torch.equal(got.gate[alone], want.gate[alone])
+        if post:        # and where x is normed, its NaN stays out of the residual's gradient
+            for t, c, v in bad:
+                x[t, c] = v
+            got = block.norm_backward(wide(x), wide(res), block.norm(x, res, p, gate, scale, eps=eps),
+                                      wide(ds), None, p, gate, scale)
+            assert torch.equal(got.residual, ds.to(res.dtype))
