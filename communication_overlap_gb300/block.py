@@ -106,7 +106,8 @@ def _norm_args(x, residual, post_gain, gate, pre_gain, scale, eps):
         param_dtype = p.dtype
     if gate is not None:
         if gate.dim() == 2 and gate.shape[1] == H:
-            gates, gate_stride = gate.shape[0], _row_stride(gate, "gate")
+            # (of no tokens, no rows are a row for each, too)
+            gates, gate_stride = gate.shape[0] or int(T == 0), _row_stride(gate, "gate")
         elif gate.shape == (H,) and gate.is_contiguous():
             gate_stride = H
         else:

@@ -629,3 +629,17 @@ def test_norm_gradient_does_not_see_the_stream(H, pad, types, residual):
             got = block.norm_backward(wide(x), wide(res), block.norm(x, res, p, gate, scale, eps=eps),
                                       wide(ds), None, p, gate, scale)
             assert torch.equal(got.residual, ds.to(res.dtype))
+
+
+@pytest.mark.parametrize("rows", [0, 1, 3])
+@pytest.mark.parametrize("H", [16, 33, 0])
+def test_norm_of_no_tokens_with_a_gate(H, rows):
+    """A gate per token has no rows either; rows that no token meets have zeros."""
+    z = lambda *s: torch.zeros(s, device="cuda")
+    n = block.norm(z(0, H), z(0, H), z(H), z(rows, H), 0.5, z(H))
+    assert n.stream.shape == n.y.shape == (0, H)
+    d = block.norm_backward(z(0, H), z(0, H), n, z(0, H), z(0, H), z(H), z(rows, H), 0.5, z(H))
+    assert d.x.shape == d.residual.shape == (0, H) and d.gate.shape == (rows, H)
+    assert not d.gate.any() and not d.post_gain.any() and not d.pre_gain.any()
+    with pytest.raises(ValueError):
+        block.norm(z(2, H), gate=z(0, H))
