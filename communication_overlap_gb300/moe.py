@@ -304,9 +304,7 @@ def route(logits, top_k, renormalize=True, capacity=0, scoring="softmax", bias=N
     if bias is not None:
         if bias.dtype != torch.float32 or not bias.is_contiguous() or tuple(bias.shape) != (E,):
             raise ValueError(f"bias: contiguous fp32[{E}] expected")
-        if desc is None:
-            desc = fo.make_route_desc(E, top_k, renormalize, capacity)
-    elif desc is None and (top_groups, group_top) != (1, 1):
+    if desc is None and (bias is not None or (top_groups, group_top) != (1, 1)):
         # (of one group there is one to choose: as the balanced router refuses others)
         desc = fo.make_route_desc(E, top_k, renormalize, capacity, top_groups=top_groups,
                                   group_top=group_top)

@@ -379,3 +379,17 @@ def test_numbers_that_are_tensors():
                  lambda s: moe.route_backward(l, got.ids, got.weights, got.weights, scale=s)):
         with pytest.raises(ValueError):
             call(torch.tensor(1.0, requires_grad=True))
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("how", [dict(top_groups=2), dict(top_groups=0), dict(group_top=3),
+                                 dict(group_top=0), dict(groups=2, top_groups=3)])
+def test_refusals_of_groups(how, biased):
+    """The same with a bias and without, of the plain router's scores as of others."""
+    l = torch.zeros((2, 8), device="cuda")
+    bias = torch.zeros(8, device="cuda") if biased else None
+    for scoring, scale in (("softmax", 1.0), ("softmax", 2.0), ("sigmoid", 1.0)):
+        with pytest.raises((ValueError, fo.FoError)):
+            moe.route(l, 2, scoring=scoring, scale=scale, bias=bias, **how)
+    r = moe.route(l, 2, bias=bias, group_top=2)
+    assert r.ids.tolist() == [[0, 1]] * 2
