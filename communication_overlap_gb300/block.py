@@ -274,8 +274,9 @@ def _slots(token_row, weights):
 def combine(rows, token_row, weights=None, out=None, out_dtype=None):
     """y[t] = sum over slots s of weights[t, s] * rows[token_row[t, s]] (-1: no
     row; no weights: ones).  rows: [table rows, hidden], bf16 or fp32, any row
-    stride; token_row and weights as a Routing holds them."""
-    _untracked(rows, weights)
+    stride; token_row and weights as a Routing holds them; out must not overlap
+    rows."""
+    _untracked(rows, weights, out)
     if rows.dim() != 2:
         raise ValueError("rows: [table rows, hidden] expected")
     T, k = _slots(token_row, weights)

@@ -32,6 +32,14 @@ def test_a_checkpoint_holds_what_its_sizes_say():
             block.Checkpoint(*bad)
 
 
+def test_a_sum_into_a_tensor_that_requires_a_gradient():
+    index = torch.zeros((2, 1), dtype=torch.int32)
+    with pytest.raises(ValueError, match="gradient"):
+        block.combine(torch.zeros((4, 8)), index, out=torch.zeros((2, 8), requires_grad=True))
+    with pytest.raises(ValueError, match="one CUDA device"), torch.no_grad():
+        block.combine(torch.zeros((4, 8)), index, out=torch.zeros((2, 8), requires_grad=True))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float64])
 def test_norms_of_another_type(dtype):
