@@ -643,3 +643,109 @@ def test_norm_of_no_tokens_with_a_gate(H, rows):
     assert not d.gate.any() and not d.post_gain.any() and not d.pre_gain.any()
     with pytest.raises(ValueError):
         block.norm(z(2, H), gate=z(0, H))
+
+
+PADS = [(4, 0), (8, 8), (1, 0), (3, 1), (2, 2), (24, 0)]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("pad, offset", PADS)
+@pytest.mark.parametrize("T, H", [(1, 72), (7, 72), (6, 136), (4, 1000), (3, 4104)])
+def test_norm_strides_of_all_types(T, H, pad, offset, types):
+    rng = np.random.default_rng(pad + H)
+    wide = lambda t: strided(t, pad, offset)
+    for post, pre in ((True, True), (False, True), (True, False)):
+        x, res, p, gate, scale, q, eps, ds, dy = norm_case(rng, T, H, *types, post, T, pre, True)
+        check_norm(wide(x), wide(res), p, wide(gate), scale, q, eps, wide(ds),
+                   None if dy is None else wide(dy))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pad, offset", PADS)
+@pytest.mark.parametrize("rows, inter", [(1, 72), (7, 72), (6, 136), (5, 33), (3, 2056)])
+def test_act_strides_of_all_types(rows, inter, pad, offset, dtype):
+    rng = np.random.default_rng(pad + inter)
+    u, dh = normal(rng, (rows, 2 * inter), dtype), normal(rng, (rows, inter), dtype)
+    for kind in ("silu", "relu"):
+        check_act(strided(u, pad, offset), strided(dh, pad, offset), kind)
+        h, kept = block.activate(u, kind, checkpoint=True)
+        wide, same = block.activate(strided(u, pad, offset), kind, checkpoint=True)
+        assert torch.equal(h, wide) and torch.equal(kept.codes, same.codes)
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("H", [8, 72, 136, 1000, 4104, 33, 4097])
+def test_norm_writes_its_rows_alone(H, types):
+    """By the library's calls, which take strides of the outputs too: nothing in the rows'
+    padding, before the first row or behind the last."""
+    rng = np.random.default_rng(H)
+    x_type, s_type = types
+    T, code = 5, {BF16: fo.FO_TYPE_BF16, F32: fo.FO_TYPE_F32}
+    x, res = normal(rng, (T, H), x_type), normal(rng, (T, H), s_type)
+    p, q = normal(rng, (H,), F32), normal(rng, (H,), F32)
+    ds, dy = normal(rng, (T, H), s_type), normal(rng, (T, H), x_type)
+    want = block.norm(x, res, p, None, 0.5, q)
+    dwant = block.norm_backward(x, res, want, ds, dy, p, None, 0.5, q)
+    desc = fo.make_norm_desc(T, H, code[x_type], code[s_type], fo.FO_TYPE_F32, 1, 0.5, 1e-6)
+    ws = torch.empty(fo.fo_block_norm_workspace(desc), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for pad in (4, 8, 24, 1, 2):
+        W = H + pad
+        bufs = {}
+
+        def out(name, dtype, rows=T, cols=H):
+            bufs[name] = torch.full(((rows + 2) * W,), 7.0, dtype=dtype, device="cuda")
+            return bufs[name].data_ptr() + W * bufs[name].element_size()
+
+        rstd = torch.empty((2, T), device="cuda")
+        at = rstd.data_ptr()
+        fo.fo_block_norm(desc, x.data_ptr(), H, res.data_ptr(), H, p.data_ptr(), 0, 0, q.data_ptr(),
+                         out("stream", s_type), W, out("y", x_type), W, at, at + 4 * T, stream)
+        dp, dq = torch.empty_like(p), torch.empty_like(q)
+        fo.fo_block_norm_backward(desc, x.data_ptr(), H, res.data_ptr(), H, p.data_ptr(), 0, 0,
+                                  q.data_ptr(), at, at + 4 * T, ds.data_ptr(), H, dy.data_ptr(), H,
+                                  out("x", x_type), W, out("residual", s_type), W, dp.data_ptr(), 0,
+                                  dq.data_ptr(), ws.data_ptr(), stream)
+        for name, w in (("stream", want.stream), ("y", want.y), ("x", dwant.x),
+                        ("residual", dwant.residual)):
+            m = bufs[name].view(T + 2, W)
+            # (other kernels, other orders of a row's sums: within the norms' bound of it)
+            off = (m[1:-1, :H].double() - w.double()).abs().amax()
+            assert off <= 2 * (half_step(w.dtype) + 256 * E) * 16 * w.double().abs().amax(), name
+            assert (m[0] == 7).all() and (m[-1] == 7).all() and (m[1:-1, H:] == 7).all(), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [8, 72, 136, 1000, 33, 2056])
+def test_act_and_combine_gradients_write_their_rows_alone(H, dtype):
+    rng = np.random.default_rng(H)
+    T, k, code = 7, 2, {BF16: fo.FO_TYPE_BF16, F32: fo.FO_TYPE_F32}[dtype]
+    n = 3 * T * k
+    _, token_row, row_token = routing(rng, T, n, k)
+    rows, w, dy = normal(rng, (n, H), dtype), normal(rng, (T, k), F32), normal(rng, (T, H), dtype)
+    drows, dw = block.combine_backward(dy, rows, token_row, row_token, w)
+    u = normal(rng, (T, 2 * H), dtype)
+    h, kept = block.activate(u, checkpoint=True)
+    du = block.activate_backward(dy, kept)
+    stream, status = torch.cuda.current_stream().cuda_stream, torch.zeros(1, dtype=torch.int32,
+                                                                          device="cuda")
+    for pad in (4, 8, 24, 1, 2):
+
+        def check(want, call):
+            R, C = want.shape
+            buf = torch.full((R + 2, C + pad), 7.0, dtype=dtype, device="cuda")
+            call(buf[1].data_ptr(), C + pad)
+            assert torch.equal(buf[1:-1, :C], want)
+            assert (buf[0] == 7).all() and (buf[-1] == 7).all() and (buf[1:-1, C:] == 7).all()
+
+        got = torch.empty_like(dw)
+        check(drows, lambda to, stride: fo.fo_moe_combine_backward(
+            dy.data_ptr(), code, H, rows.data_ptr(), code, n, H, H, token_row.data_ptr(),
+            row_token.data_ptr(), w.data_ptr(), T, k, to, stride, got.data_ptr(), status.data_ptr(),
+            stream))
+        check(h, lambda to, stride: fo.fo_gated_act(u.data_ptr(), code, T, H, 2 * H, fo.FO_ACT_SILU,
+                                                    to, stride, 0, 0, stream))
+        check(du, lambda to, stride: fo.fo_gated_act_backward(
+            dy.data_ptr(), code, T, H, H, fo.FO_ACT_SILU, kept.codes.data_ptr(),
+            kept.scales.data_ptr(), to, stride, stream))
+    assert status.item() == fo.FO_OK

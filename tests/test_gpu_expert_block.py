@@ -145,3 +145,112 @@ def test_gradient_captured():
         # (rows of no expert hold anything: the results that do not see them are equal)
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
         assert all(torch.equal(a, b) for a, b in zip(beside, want[0]))
+
+
+EXACT = [
+    (True, dict(scoring="sigmoid", scale=2.0)),
+    (False, dict(scoring="sigmoid", scale=2.0)),
+    (True, dict(scale=2.0)),
+    (False, dict(scale=2.0)),
+    (True, dict(scoring="sigmoid", scale=2.0, groups=4, top_groups=1, group_top=2)),
+    (False, dict(scoring="softmax", scale=2.0, groups=4, top_groups=1, group_top=1)),
+]
+
+
+@pytest.mark.parametrize("renormalize, routing", EXACT)
+@pytest.mark.parametrize("T", [65, 300])
+def test_block_of_values_that_4_bits_hold(T, renormalize, routing):
+    """The whole chain without a rounding to 4 bits, so that each result is off by bf16's
+    roundings alone, element by element.
+
+    The stream is -1 and 1 (1 in its first 32 columns), so are its norm and its product with
+    pre_gain; a row of w1 has one value, 16 in a column of ones for a gate (silu is the gate
+    itself there, to 2^-23) and 1 or 2 for the others; w2 is a permutation with signs for
+    each expert; both chosen experts have the logit 0, and weights of 2 / 2; the gradient of
+    the stream is 1, 1.5, 2 or 3.  So every block of 32 that is converted holds multiples by
+    a power of two of 0.5, 1, 1.5, 2, 3, 4 and 6, the values of 4 bits, and 8-bit codes
+    hold them too.  Roundings to bf16, 2^-9 each: of the product with w1_t, of its rows'
+    sum, of the logits' gradient, of their sum, and of the result: five, below 2^-6
+    of the magnitudes that were added.  The gradients of router and gate see one and two."""
+    H, I, E, k = 64, 64, 8, 2
+    rng = np.random.default_rng(T)
+    sign = lambda *shape: rng.choice([-1.0, 1.0], shape)
+    stream, pre = sign(T, H), sign(H)
+    stream[:, :32], pre[:42] = 1, 1
+    w1, w2 = np.zeros((E, 2 * I, H)), np.zeros((E, H, I))
+    for e in range(E):
+        w1[e, np.arange(I), np.arange(I) % 32] = 16
+        w1[e, I + np.arange(I), rng.integers(0, H, I)] = sign(I) * rng.choice([1, 2], I)
+        w2[e, rng.permutation(H), np.arange(I)] = sign(I) / 16
+    # two experts per pair of signs of columns 40 and 41: theirs have the logit 0
+    router = np.zeros((E, H))
+    for e in range(E):
+        router[e, 0], router[e, 40], router[e, 41] = -64, 32 * (-1) ** (e // 2), 32 * (-1) ** (e // 4)
+    gate, scale = sign(H), 0.5
+    dstream = sign(T, H) * rng.choice([1, 1.5, 2, 3], (T, H))
+    put = lambda a: torch.from_numpy(a).to(BF16).cuda()
+    kept = [(moe.quantize(put(w)), moe.quantize(put(w), transpose=True)) for w in (w1, w2)]
+    for w, (q, _) in zip((w1, w2), kept):
+        assert torch.equal(moe.dequantize(q), put(w))
+    layer = expert_layer.ExpertLayer(put(router), kept[0][0], kept[1][0], k, renormalize,
+                                     w1_t=kept[0][1])
+    block = expert_layer.ExpertBlock(layer, put(pre), None, put(gate), scale, w2_t=kept[1][1],
+                                     routing=routing)
+    out, step = block.forward(put(stream))
+    grads = block.backward(step, put(dstream))
+    # the definitions in 64 bits
+    n = stream * pre / np.sqrt(1 + block.eps)
+    logits = n @ router.T
+    ids = step.routing.ids.cpu().numpy()
+    pair = 2 * (stream[:, 41] < 0) + (stream[:, 40] < 0)
+    assert np.array_equal(np.sort(ids, 1), np.stack([2 * pair, 2 * pair + 1], 1))
+    every = np.arange(T)[:, None]
+    if routing.get("scoring") == "sigmoid":
+        s = 1 / (1 + np.exp(-logits))
+        slope = lambda ds: ds * s * (1 - s)
+    else:
+        s = np.exp(logits) / np.exp(logits).sum(1, keepdims=True)
+        slope = lambda ds: s * (ds - (s * ds).sum(1, keepdims=True))
+    chosen = s[every, ids]
+    total = chosen.sum(1, keepdims=True)
+    w = 2 * chosen / (total if renormalize else 1)
+    up = np.einsum("tsih,th->tsi", w1[ids], n)
+    g, v = up[..., :I], up[..., I:]
+    act = g / (1 + np.exp(-g))
+    rows = np.einsum("tshi,tsi->tsh", w2[ids], act * v)
+    z = (w[..., None] * rows).sum(1)
+    host = lambda t: t.double().cpu().numpy()
+
+    def near(got, want, part, size):
+        off = np.abs(host(got) - want)
+        assert (off <= part * size).all(), (off / size).max()
+
+    near(step.mixed, z, 2.0 ** -8, np.abs(z))
+    near(out, stream + scale * gate * z, 2.0 ** -8, np.abs(stream) + np.abs(scale * z))
+    values = host(step.kept.values()).reshape(-1, 2 * I)
+    held = step.routing.token_row.long().cpu().numpy()
+    assert np.array_equal(values[held], np.einsum("tsih,th->tsi", w1[ids], stream * pre))
+    dz = scale * gate * dstream
+    dw = (dz[:, None] * rows).sum(2)
+    dh = np.einsum("tshi,tsh->tsi", w2[ids], w[..., None] * dz[:, None])
+    sg = 1 / (1 + np.exp(-g))
+    dup = np.concatenate([dh * v * sg * (1 + g * (1 - sg)), dh * act], 2)
+    dn = np.einsum("tsih,tsi->tsh", w1[ids], dup)
+    ds = np.zeros((T, E))
+    ds[every, ids] = 2 * (dw / total - (dw * chosen).sum(1, keepdims=True) / total ** 2
+                          if renormalize else dw)
+    dl = slope(ds)
+    near(grads.router, dl.T @ n, 2.0 ** -8, np.abs(dl).T @ np.abs(n) + 2.0 ** -20 * np.abs(dw).max())
+    sn = stream / np.sqrt(1 + block.eps)
+    sum_n = dn.sum(1) + dl @ router
+    size = np.abs(dn).sum(1) + np.abs(dl) @ np.abs(router)
+    near(grads.pre_gain, (sum_n * sn).sum(0), 2.0 ** -6, size.sum(0))
+    near(grads.gate, (scale * z * dstream).sum(0), 2.0 ** -8, np.abs(scale * z * dstream).sum(0))
+    e = sum_n * pre
+    want = dstream + (e - sn * (e * sn).mean(1, keepdims=True)) / np.sqrt(1 + block.eps)
+    bound = np.abs(dstream) + size + size.mean(1, keepdims=True)
+    near(grads.stream, want, 2.0 ** -6, bound)
+    # a third of the experts' part would not pass, in most of the elements that have one
+    part = np.abs(dn.sum(1))
+    assert (part / 3 > 2.0 ** -6 * bound)[part > 0].mean() > 0.5
+    assert moe.device_status() == fo.FO_OK
