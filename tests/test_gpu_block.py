@@ -749,3 +749,50 @@ def test_act_and_combine_gradients_write_their_rows_alone(H, dtype):
             dy.data_ptr(), code, T, H, H, fo.FO_ACT_SILU, kept.codes.data_ptr(),
             kept.scales.data_ptr(), to, stride, stream))
     assert status.item() == fo.FO_OK
+
+
+@pytest.mark.parametrize("H, pad", [(4096, 0), (4095, 1)])
+def test_rows_past_32_bits(H, pad):
+    """Offsets above 2^32 elements: the last rows as calls on those alone have them."""
+    T, last, W = (1 << 32) // 4096 + 40, 24, H + pad
+    g = torch.Generator(device="cuda").manual_seed(H)
+
+    def draw(rows, cols=H, stride=W):
+        t = torch.empty((rows, stride), dtype=BF16, device="cuda")[:, :cols]
+        t[-last:] = torch.randn((last, cols), generator=g, device="cuda")
+        t[:-last] = 1
+        return t
+
+    x, res, ds, dy = (draw(T) for _ in range(4))
+    p, q = (torch.randn(H, generator=g, device="cuda") for _ in range(2))
+    n = block.norm(x, res, p, None, 0.5, q)
+    few = block.norm(x[-last:], res[-last:], p, None, 0.5, q)
+    assert torch.equal(n.stream[-last:], few.stream) and torch.equal(n.y[-last:], few.y)
+    d = block.norm_backward(x, res, n, ds, dy, p, None, 0.5, q)
+    want = block.norm_backward(x[-last:], res[-last:], few, ds[-last:], dy[-last:], p, None, 0.5, q)
+    assert torch.equal(d.x[-last:], want.x) and torch.equal(d.residual[-last:], want.residual)
+    del d, n, ds
+    # the same rows as a table, which two tokens name from both of its ends
+    index = torch.tensor([[T - 1, 0], [T - 2, -1]], dtype=torch.int32, device="cuda")
+    row_token = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    row_token[[T - 1, 0, T - 2]] = torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[2.0, 0.5], [4.0, 8.0]], device="cuda")
+    y = block.combine(x, index, w)
+    assert torch.equal(y[0], (2 * x[-1].float() + 0.5 * x[0].float()).to(BF16))
+    assert torch.equal(y[1], 4 * x[-2])
+    drows, dw = block.combine_backward(y, x, index, row_token, w)
+    assert torch.equal(drows[-1], 2 * y[0]) and torch.equal(drows[-2], 4 * y[1])
+    assert torch.equal(drows[0], 0.5 * y[0])
+    drows[[T - 1, T - 2, 0]] = 0
+    assert not drows.any()
+    del x, res, dy, drows
+    # and the activation
+    I = 14336 - pad
+    R = (1 << 32) // (2 * 14336) + 40
+    u, dh = draw(R, 2 * I, 2 * I), draw(R, I, I)
+    h, kept = block.activate(u, checkpoint=True)
+    few, fewer = block.activate(u[-last:], checkpoint=True)
+    assert torch.equal(h[-last:], few) and torch.equal(kept.codes[-fewer.codes.numel():], fewer.codes)
+    assert torch.equal(block.activate_backward(dh, kept)[-last:],
+                       block.activate_backward(dh[-last:], fewer))
+    assert moe.device_status() == fo.FO_OK
