@@ -406,14 +406,6 @@ __device__ __forceinline__ GroupCut cut_groups(const ScoreArgs& a, const Choice<
   const bool two = a.group_top == 2 && k2 != 0u;
   r.score = two ? order_key(order_value(k1) + order_value(k2)) : k1;
   r.second = two ? k2 : k1;
-  // a sum of two choices of unlike signs is smaller than they are, and off by what they
-  // are off: by how much, the most of any group (one far from the cut may be off as far)
-  float apart = 0.0f;
-  if (a.bias != nullptr && a.group_top == 2) {
-    const float v1 = order_value(k1), v2 = order_value(k2);
-    if (two && v1 > 0.0f && v2 < 0.0f) apart = 2.0f * fminf(v1, -v2);
-    apart = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(apart)));
-  }
   int rank = 0;
 #pragma unroll 8
   for (int h = 0; h < a.groups; ++h) {
@@ -428,10 +420,27 @@ __device__ __forceinline__ GroupCut cut_groups(const ScoreArgs& a, const Choice<
   const bool logits = by_logit && a.group_top == 1;
   const float vi = order_value(r.in);
   r.margin = logits ? 0.0f
-                    : 2.0f * choice_margin(score_margin(a.sigmoid, c.inv, V), fabsf(vi) + apart,
-                                               float(4 * V)) +
+                    : 2.0f * choice_margin(score_margin(a.sigmoid, c.inv, V), vi, float(4 * V)) +
                           cut_logit_margin(a, c, vi);
   r.near = out != 0u && (r.in == out ? !(logits && a.bf16) : vi - order_value(out) < r.margin);
+  return r;
+}
+
+// A sum of two choices of unlike signs is smaller than they are, and off by what they are
+// off: the margin counts that, the most of any group (one far from the cut may be off as
+// far).  Sums of like signs are near each other only if their choices are as large.
+template <int V>
+__device__ __noinline__ GroupCut widen_cut(const ScoreArgs& a, GroupCut r) {
+  const int g = (threadIdx.x & 31) >> a.lane_bits;
+  const float second = order_value(r.second), vi = order_value(r.in);
+  // (the larger of the two is the sum without the other; a choice alone is both)
+  const float apart =
+      g < a.groups && second < 0.0f ? 2.0f * fmaxf(fminf(order_value(r.score) - second, -second), 0.0f)
+                                    : 0.0f;
+  const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(apart)));
+  const uint32_t out = __reduce_max_sync(0xffffffffu, g < a.groups && !r.stays ? r.score : 0u);
+  r.margin += 2.0f * choice_margin(0.0f, most, float(4 * V));
+  r.near = r.near || (out != 0u && vi - order_value(out) < r.margin);
   return r;
 }
 
@@ -543,10 +552,19 @@ __device__ __forceinline__ void warp_choose(const ScoreArgs& a, const LaneExpert
     GroupCut r[N];
     bool near = false;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      r[n] = cut_groups<V>(a, c[n]);
-      near = near || r[n].near;
+    for (int n = 0; n < N; ++n) r[n] = cut_groups<V>(a, c[n]);
+    if (a.bias != nullptr && a.group_top == 2) {
+      // (a key of a negative number; 0 is none)
+      bool unlike = false;
+#pragma unroll
+      for (int n = 0; n < N; ++n) unlike = unlike || r[n].second - 1u < 0x7fffffffu;
+      if (__any_sync(0xffffffffu, unlike)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) r[n] = widen_cut<V>(a, r[n]);
+      }
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n) near = near || r[n].near;
     if (near) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
