@@ -92,16 +92,22 @@ __device__ __forceinline__ uint32_t amax_of(const Pack8<float>& p) {
   return m;
 }
 
-// 1 / (1 + e^-g).  With fp32 outputs by expf and a division.  With bf16 ones, which are rounded by
-// 2^-9, by one power of two (its argument is rounded twice and itself off by 2^-22: with
-// the reciprocal's 2^-23 off by less than (|g| + 4) 2^-22): a third of the
-// instructions, where those bind.
+// k / (1 + e^-kg), k = kScale of T: times g it is the silu of kg.  With fp32 outputs k = 1,
+// by expf and a division.  With bf16 ones, which are rounded by 2^-9, by one power of two,
+// and k = 2^8, so that the reciprocal has no number to flush while the power is one: without,
+// silu was 0 from -87.3 on.  (The power's argument is rounded twice and itself off by
+// 2^-22: with the reciprocal's 2^-23 off by less than (|kg| + 4) 2^-22.)  A third of
+// expf's instructions, where those bind.
 template <typename T>
-__device__ __forceinline__ float sigmoid(float g) {
+constexpr float kScale = sizeof(T) == 2 ? 0x1p8f : 1.0f;
+template <typename T>
+constexpr float kPart = 1.0f / kScale<T>;
+template <typename T>
+__device__ __forceinline__ float scaled_sigmoid(float g) {
   if constexpr (sizeof(T) == 2) {
     float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (-1.4426950408889634f * kScale<T>)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(e, kPart<T>, kPart<T>)));
     return s;
   } else {
     return 1.0f / (1.0f + expf(-g));
@@ -110,7 +116,10 @@ __device__ __forceinline__ float sigmoid(float g) {
 
 template <typename T>
 __device__ __forceinline__ float gated(float g, float u, int act) {
-  if (act == FO_ACT_SILU) return g * sigmoid<T>(g) * u;
+  if (act == FO_ACT_SILU) {
+    g *= kPart<T>;
+    return g * scaled_sigmoid<T>(g) * u;
+  }
   if (act == FO_ACT_RELU) return (g > 0.0f ? g : 0.0f) * u;
   return g * u;
 }
@@ -119,8 +128,9 @@ template <typename T>
 __device__ __forceinline__ void gated_backward(float dh, float g, float u, int act, float& dg,
                                                float& du) {
   if (act == FO_ACT_SILU) {
-    const float s = sigmoid<T>(g);
-    dg = dh * u * (s * fmaf(g, 1.0f - s, 1.0f));
+    g *= kPart<T>;
+    const float s = scaled_sigmoid<T>(g);
+    dg = dh * u * (s * fmaf(g, fmaf(s, -kPart<T>, 1.0f), kPart<T>));
     du = dh * (g * s);
   } else if (act == FO_ACT_RELU) {
     dg = g > 0.0f ? dh * u : 0.0f;
@@ -147,13 +157,14 @@ __device__ __forceinline__ void gated_backward(const Pack8<T>& dh, uint2 gate, u
     pairs_of(dh, d);
     const uint32_t qg[2] = {gate.x ^ 0x80808080u, gate.y ^ 0x80808080u};
     const uint32_t qu[2] = {up.x ^ 0x80808080u, up.y ^ 0x80808080u};
+    const float part_step = gate_step * kPart<T>;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const Pair g = code_pair(qg[i / 2], i & 1, gate_step), u = code_pair(qu[i / 2], i & 1, up_step);
+      const Pair g = code_pair(qg[i / 2], i & 1, part_step), u = code_pair(qu[i / 2], i & 1, up_step);
       float a, b;
       g.get(a, b);
-      const Pair s = Pair::of(sigmoid<T>(a), sigmoid<T>(b)), one = Pair::of(1.0f);
-      const Pair slope = s * fma2(g, fma2(s, Pair::of(-1.0f), one), one);
+      const Pair s = Pair::of(scaled_sigmoid<T>(a), scaled_sigmoid<T>(b));
+      const Pair slope = s * fma2(g, fma2(s, Pair::of(-kPart<T>), Pair::of(1.0f)), Pair::of(kPart<T>));
       (d[i] * u * slope).get(dg[2 * i], dg[2 * i + 1]);
       (d[i] * (g * s)).get(du[2 * i], du[2 * i + 1]);
     }

@@ -841,8 +841,9 @@ fo_status fo_checkpoint_sizes(int64_t rows, int64_t inter, int64_t* code_bytes,
                               int64_t* scale_bytes);
 
 /* h = act(g) * v for rows [g | v] of u (2 * inter columns); RELU keeps g when
- * g > 0 (else 0), SILU is g / (1 + exp(-g)).  With codes and scales (both or
- * neither NULL) u is also kept in 8 bits for the backward pass.
+ * g > 0 (else 0), SILU is g / (1 + exp(-g)) (it and its derivative may be 0 where
+ * exp(-g) passes the largest fp32 number, below -88.7).  With codes and scales
+ * (both or neither NULL) u is also kept in 8 bits for the backward pass.
  *  codes, scales: device, codes 16-byte aligned, of fo_checkpoint_sizes bytes. */
 fo_status fo_gated_act(const void* u, fo_type type, int64_t rows, int64_t inter,
                        int64_t u_stride, fo_activation act, void* h, int64_t h_stride,

@@ -796,3 +796,32 @@ def test_rows_past_32_bits(H, pad):
     assert torch.equal(block.activate_backward(dh, kept)[-last:],
                        block.activate_backward(dh[-last:], fewer))
     assert moe.device_status() == fo.FO_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [32, 33])
+def test_act_gates_where_sigmoid_ends(inter, dtype):
+    """silu of gates about -88, where 1 / (1 + e^-g) passes below the normal numbers: its
+    product with a value that is not small is no zero.  s may be zero where e^-g passes
+    fp32's largest number; else as above."""
+    g = -torch.arange(127 - 63, 127, device="cuda", dtype=F32).repeat(inter)
+    g = g[:g.numel() // inter * inter].view(-1, inter).to(dtype)      # (codes hold whole numbers)
+    last = 2.0 ** -127.9
+    rng = np.random.default_rng(inter)
+    for size in (1.0, 40.0, 2.0 ** 40, 2.0 ** 100):
+        v = torch.from_numpy(size * rng.choice([-1.0, 1.0], g.shape)).to(dtype).cuda()
+        dh = normal(rng, tuple(g.shape), dtype)
+        h, kept = block.activate(torch.cat((g, v), 1), checkpoint=True)
+        assert torch.equal(kept.values(), torch.cat((g, v), 1).float())
+        g64, v64, d64 = host(g), host(v), host(dh)
+        off = 8 if dtype == F32 else 16 + 4 * np.abs(g64)
+        want = oracle.act(g64, "silu") * v64
+        near(h, want, off * E * np.abs(want) + last * np.abs(g64 * v64), dtype)
+        assert size < 40 or bool((h[g >= -88] != 0).all())
+        du = block.activate_backward(dh, kept)
+        want = d64 * oracle.act(g64, "silu")
+        near(du[:, inter:], want, 2 * off * E * np.abs(want) + last * np.abs(g64 * d64), dtype)
+        s = 1 / (1 + np.exp(-g64))
+        size_of = np.abs(d64 * v64) * (1 + np.abs(g64))
+        near(du[:, :inter], d64 * v64 * oracle.act_slope(g64, "silu"),
+             2 * off * E * s * size_of + last * size_of, dtype)
