@@ -578,7 +578,8 @@ fo_status backward_as(CombineBackArgs a, int smem, int width, cudaStream_t st) {
 
 // The slots of a round come out even over a token's rounds (6 as 3 and 3: 5001 x 2048
 // in fp32 113 -> 89 us against 4 and 2), with two pieces of columns where few rows are
-// under way in one, and as many stages as fit three CTAs' rings on an SM.
+// under way in one, and as many stages as let three CTAs' rings fit on an SM.  (With fp32
+// dy two fit where the rows are fp32 and a round has one slot or four, or bf16 and two.)
 template <typename T, typename O, int SLOTS>
 fo_status backward_slots(const CombineBackArgs& a, cudaStream_t st) {
   constexpr int kT = sizeof(T) / 2, kO = sizeof(O) / 2;

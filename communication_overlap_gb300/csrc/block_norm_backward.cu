@@ -16,13 +16,16 @@
 //
 // A worker takes a contiguous range of tokens and keeps the parameters' sums of
 // its columns in registers; a last kernel adds the workers' in their order, so
-// results do not vary from run to run.  Rows of up to 8192 columns on 16 bytes (4096
-// in fp32) go through one kernel, which holds a row in registers between the two
-// passes; others through two, one for the means and one for the columns.
+// results do not vary from run to run.  Rows on 16 bytes of up to 8192 columns (of bf16
+// into an fp32 stream 6656, of fp32 5632: two rows and the parameters have to fit in
+// shared memory), and others of up to 4096, go through one kernel, which holds a row in
+// registers between the two passes; the rest through two, one for the means and one for
+// the columns.
 //
 // 16384 x 4096 of bf16: 805 MB in 130 us (6.2 TB/s) and 7 us for the joining kernel,
 // whose launch most of that is; 4095 x 2752 of bf16 with an fp32 stream 203 MB in 42
-// (4.8) and 7.  Rows of 8192 move 4.5 TB/s, 12288 in two kernels 2.5.
+// (4.8) and 7.  Rows of 8192 move 4.3 TB/s, 12288 in two kernels 2.4.  Without pre,
+// 16384 x 4096 of bf16, 537 MB in 92 us (5.8).
 #include <cuda_runtime.h>
 
 #include "block_norm.cuh"

@@ -6,8 +6,8 @@
 //
 // Two c may be nearer to each other than fp32 tells, and then another choice
 // than the mathematics' would follow.  So every decision looks at its margin:
-// where it is below what the values may be off, it is made again in fp64 (one
-// token in a few thousand on spread-out logits).  Without a bias c grows with l,
+// where it is below what the values may be off, it is made again in fp64 (of
+// 16384 tokens of 256 experts in 8 groups, normal logits, some 30).  Without a bias c grows with l,
 // and the logits decide.
 //
 // A lane holds V consecutive experts, 2^n lanes a group, as order-preserving keys

@@ -146,7 +146,11 @@ class ExpertBlock:
     dict of moe.route's options beyond those of the layer (scoring, bias, groups,
     top_groups, group_top, scale).  The stream is bf16 [tokens, hidden].  The
     experts' weights are not trained (they are in 4 bits): backward gives the
-    gradients of the stream, the router and the norms' parameters."""
+    gradients of the stream, the router and the norms' parameters.
+
+    Between its operators the block keeps bf16, where ExpertLayer has fp32: the
+    experts' rows of both directions (half the bytes of the largest tensors), and the
+    logits' gradient, which the two products with the router take in bf16."""
 
     def __init__(self, layer, pre_gain, post_gain=None, gate=None, scale=1.0, eps=1e-6, w2_t=None,
                  routing=None):

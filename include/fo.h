@@ -708,6 +708,9 @@ fo_status fo_moe_route_backward(const void* logits, fo_type type, int64_t tokens
  *   weight = scale * s_e, or with renormalize scale * s_e / sum over the chosen.
  * The choice is the one that 64-bit arithmetic on these formulas makes: where
  * fp32 values are too near to each other to tell, they are computed again.
+ * Without a bias c grows with l, and experts (and groups with group_top 1) go
+ * by their logits, also where 64-bit scores are equal (sigmoids of 40 and 50
+ * are both 1); sums of two scores go by the 64-bit scores.
  * Weights are computed in fp32.  A logit or a choice value of -inf bars the
  * expert; slots without one, the row tables, -1 entries, workspace, status and
  * alignment are fo_moe_route's.  A NaN choice value ranks above every number
