@@ -7,8 +7,8 @@
 // Two c may be nearer to each other than fp32 tells, and then another choice
 // than the mathematics' would follow.  So every decision looks at its margin:
 // where it is below what the values may be off, it is made again in fp64 (of
-// 16384 tokens of 256 experts in 8 groups, normal logits, some 30).  Without a bias c grows with l,
-// and the logits decide.
+// 16384 tokens of 256 experts in 8 groups, normal logits, some 30).  Without a
+// bias c grows with l, and the logits decide.
 //
 // A lane holds V consecutive experts, 2^n lanes a group, as order-preserving keys
 // whose lowest bits say which of the lane's experts it is.  So sorting a lane's

@@ -825,3 +825,16 @@ def test_act_gates_where_sigmoid_ends(inter, dtype):
         size_of = np.abs(d64 * v64) * (1 + np.abs(g64))
         near(du[:, :inter], d64 * v64 * oracle.act_slope(g64, "silu"),
              2 * off * E * s * size_of + last * size_of, dtype)
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (BF16, F32, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("H", [64, 2752, 333, 4104])
+@pytest.mark.parametrize("T, gates", [(2500, 0), (2500, None), (2500, 4), (2500, 1250), (3000, 3000),
+                                      (1217, 1)])
+def test_norm_of_many_tokens_without_the_second(T, gates, H, types):
+    if H > 2000:
+        T, gates = T // 5, 4 if gates == 4 else gates and min(gates, T // 5)
+        gates = gates if gates in (0, 1, 4, None) else T
+    rng = np.random.default_rng(T + H)
+    for post, residual in ((True, True), (False, True), (True, False)):
+        check_norm(*norm_case(rng, T, H, *types, post, gates, False, residual))
